@@ -59,6 +59,9 @@ typedef enum pkv_dtype { PKV_F32 = 0, PKV_BF16 = 1, PKV_FP8_E4M3 = 2 } pkv_dtype
 #define PKV_ERRBIT_SLOT 2     /* slot_mapping entry outside [-1, num_blocks*block_size) */
 #define PKV_ERRBIT_SEQ_LEN 4  /* seq_lens entry < 0 or > max_seq_len of the call */
 #define PKV_ERRBIT_TIMEOUT 8  /* a bounded pipeline wait expired; that CTA skipped its output */
+#define PKV_ERRBIT_POSITION 16 /* a position outside [0, max_pos) of the rotation table */
+#define PKV_ERRBIT_STEP 32     /* tables: new_tokens < 0 or past max_tokens, or a free list state that cannot be */
+#define PKV_ERRBIT_GROUP 64    /* shared prefixes: offsets not ascending within [0, num_seqs], or a length < 0 */
 
 /* Kernel design used by paged_decode_attention. */
 typedef enum pkv_algo {
@@ -293,6 +296,151 @@ pkv_status paged_decode_attention_static_ws(const void* q, pkv_dtype q_dtype, co
  * pools with head_dim 128, block size 16/32/64 and 1 <= group <= 64 (when the
  * driver provides TMA descriptors), SIMT otherwise. */
 int32_t paged_decode_algo(const pkv_pool* pool, int32_t group, pkv_algo requested);
+
+/*
+ * Decode attention of a batch whose sequences share prefixes ("How does
+ * TensorRT-LLM work?", "The paged KV cache": requests that begin with the
+ * same text point at the same blocks).  The result is that of
+ * paged_decode_attention with the same arguments, up to rounding; a prefix is
+ * read, and multiplied with its group's queries, once for the whole group.
+ *   group_offsets device int32 [num_groups + 1], ascending in [0, num_seqs]:
+ *                 sequences group_offsets[g] .. group_offsets[g + 1] - 1 share
+ *                 the first prefix_lens[g] tokens.  Groups may be empty, and
+ *                 sequences before the first or behind the last group share
+ *                 nothing.
+ *   prefix_lens   device int32 [num_groups], >= 0; need not be a multiple of
+ *                 anything (a remainder below 64 tokens is read
+ *                 per sequence).
+ *   block_tables  as for paged_decode_attention: every sequence's whole table.
+ *                 Within a group, the entries of the shared tokens name blocks
+ *                 of equal content; those of one sequence are read.
+ * A sequence shorter than its group's prefix is attended on its own.  Offsets
+ * that do not ascend set PKV_ERRBIT_GROUP and nothing is shared; a negative
+ * prefix length sets it and that group shares nothing: the results stay right.  Lengths and groups are read on the device: a captured call may be
+ * replayed with other ones, within max_seq_len and num_groups.
+ *   algo          PKV_ALGO_AUTO: the sharing design (tcgen05) where it serves
+ *                 the pool, else paged_decode_attention's choice, which reads
+ *                 every sequence's prefix (from L2, mostly) and looks at no
+ *                 group.  PKV_ALGO_TC: the sharing design or
+ *                 PKV_ERR_UNSUPPORTED.  PKV_ALGO_MMA, PKV_ALGO_SIMT: those.
+ *                 The sharing design serves BF16 pools of head_dim 128, up to
+ *                 4096 sequences and groups, up to 128 query heads per KV head.
+ *   workspace     at least paged_prefix_decode_plan's bytes, 256-byte aligned,
+ *                 zeroed before its first call; stream-ordered calls may share
+ *                 it, also with paged_decode_attention calls of as many
+ *                 sequences.
+ */
+pkv_status paged_prefix_decode_plan(const pkv_pool* pool, int32_t num_seqs, int32_t num_groups, int32_t num_q_heads,
+                                    int32_t max_seq_len, size_t* workspace_bytes_out);
+/* The design the call would run: PKV_ALGO_TC (prefixes shared), PKV_ALGO_MMA
+ * or PKV_ALGO_SIMT (each sequence on its own), or -1. */
+int32_t paged_prefix_decode_algo(const pkv_pool* pool, int32_t num_seqs, int32_t num_groups, int32_t num_q_heads,
+                                 int32_t max_seq_len, pkv_algo requested);
+pkv_status paged_prefix_decode_attention(const void* q, pkv_dtype q_dtype, const pkv_pool* pool, int32_t layer,
+                                         const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                         const int32_t* seq_lens, int32_t num_seqs, int32_t num_q_heads,
+                                         int32_t max_seq_len, const int32_t* group_offsets,
+                                         const int32_t* prefix_lens, int32_t num_groups, float scale, pkv_algo algo,
+                                         void* workspace, size_t workspace_bytes, void* out, void* stream);
+
+/*
+ * Between the QKV projection and attention, in one launch: RMS norm of every
+ * query and key head, rotary position embedding of both, and the append of K
+ * and V ("How does TensorRT-LLM work?", "Kernel fusion").  For a head's row x
+ * of D = head_dim elements:
+ *     y_i = x_i * w_i / sqrt(mean(x^2) + eps)       (with weights; else y = x)
+ *     (z_a, z_b) = (y_a c - y_b s, y_b c + y_a s)   for each rotated pair
+ * Pair j < rotary_dim / 2 is elements (j, j + rotary_dim / 2), or (2 j,
+ * 2 j + 1) when interleaved; the elements from rotary_dim on are not rotated.
+ * Its c and s are cos_sin[p][j] and cos_sin[p][rotary_dim / 2 + j] at the
+ * token's position p on the pair's axis: axis 0 has the first sections[0]
+ * pairs, axis 1 the next sections[1], axis 2 the rest (time, height, width).
+ * All in binary32 with one rounding, of the stored element.  V is stored as
+ * kv_append stores it.
+ */
+typedef struct pkv_norm_rope {
+    const float* cos_sin;   /* device [max_pos][rotary_dim], 16-byte aligned */
+    int32_t max_pos;
+    int32_t rotary_dim;     /* a multiple of 16, 16 .. head_dim */
+    int32_t interleaved;    /* 0 or 1 */
+    int32_t num_axes;       /* 1 .. 3 */
+    int32_t sections[3];    /* pairs per axis, each >= 0; the first num_axes sum to rotary_dim / 2 */
+    const void* q_weight;   /* device [head_dim], 16-byte aligned; both NULL: no norm */
+    const void* k_weight;
+    pkv_dtype weight_dtype; /* PKV_F32 or PKV_BF16 */
+    float eps;              /* > 0 when there are weights */
+} pkv_norm_rope;
+/*
+ *   q, k, v       device; token t's heads are [heads][head_dim], contiguous,
+ *                 at element t * q_stride (k_stride, v_stride): rows of one
+ *                 fused projection, or tensors of their own.  Strides are
+ *                 multiples of 8 elements (16 bytes) of in_dtype (PKV_F32 or
+ *                 PKV_BF16; an F32 pool takes F32 only), >= 0.
+ *   positions     device int32 [num_axes][num_tokens].  A position outside
+ *                 [0, max_pos) sets PKV_ERRBIT_POSITION: that token's queries
+ *                 become zero and its K and V are not stored.
+ *   slot_mapping  as kv_append; -1 stores no K and V (the queries are written).
+ *   q_out         device [num_tokens][num_q_heads][head_dim] in the dtype
+ *                 attention takes with this pool (F32 pool: F32, else BF16).
+ *                 May be q itself when that is contiguous and of that dtype;
+ *                 any other overlap with q, k or v is PKV_ERR_INVALID_ARG.
+ */
+pkv_status kv_append_norm_rope(const pkv_pool* pool, int32_t layer, const void* q, const void* k, const void* v,
+                               pkv_dtype in_dtype, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                               const int32_t* positions, const int64_t* slot_mapping, int32_t num_tokens,
+                               int32_t num_q_heads, const pkv_norm_rope* rope, void* q_out, void* stream);
+
+/*
+ * Block tables, slots and the free list of a step, on the device ("How does
+ * TensorRT-LLM work?", "The paged KV cache"; "TensorRT-LLM, in depth",
+ * "In-flight batching and the scheduler"): what the host block manager below
+ * does for a list of requests, for loops that are captured or never return to
+ * the host.  (It shares no blocks between requests; see keep_blocks.)
+ *
+ * The free list is a ring: int32 free_ring[ring_size] and free_state = {head,
+ * count}; free blocks are entries head .. head + count - 1, modulo ring_size.
+ *
+ * kv_tables_grow reserves the next new_tokens[b] positions of every request b,
+ * in order.  Request b of length L = seq_lens[b] needs d = ceil((L +
+ * new_tokens[b]) / bs) - ceil(L / bs) blocks, the next d of the ring, written
+ * to its table row behind the blocks it holds.  It is served if that row has
+ * room and the needs of the requests up to and including it do not exceed the
+ * free blocks (a request that needs none is always served); otherwise it waits:
+ * no block, no slot, its length unchanged.  For one new token each that is
+ * kv_bm_decode_slots.
+ *   new_tokens    device int32 [num_seqs], >= 0; the token rows of the step
+ *                 are those of request 0, then of request 1, ..., waiting ones
+ *                 included
+ *   slot_mapping  device int64 [max_tokens] out: block * bs + offset, -1 for
+ *                 rows of waiting requests and behind the last row
+ *   positions     device int32 [max_tokens] out: L + i (0 behind the last row)
+ *   token_seqs    device int32 [max_tokens] out: request (-1 behind the last)
+ *   token_offsets device int32 [num_seqs + 1] out: first row of each request
+ *   granted       device int32 [num_seqs] out: new_tokens[b], or 0 if it waits
+ *   seq_lens_out, free_state_out   out; may be seq_lens and free_state
+ * Flagged, and the request waits: a length < 0 or beyond its table row
+ * (PKV_ERRBIT_SEQ_LEN); new_tokens < 0 (counted as no rows) or rows past
+ * max_tokens (PKV_ERRBIT_STEP).  A table or ring entry outside the pool sets
+ * PKV_ERRBIT_BLOCK_ID, gives slot -1 and, from the ring, a table entry of -1.
+ * A free_state that cannot be (head outside the ring, count outside 0 ..
+ * ring_size) sets PKV_ERRBIT_STEP and counts as an empty list.
+ *
+ * kv_tables_release returns the blocks of every request with finished[b] != 0,
+ * in table order, behind the ring's tail, and makes its length 0 (the table row
+ * stays).  The first keep_blocks[b] blocks of its row (NULL: 0) are kept out:
+ * a prefix that others use.  If the ring cannot hold them all, or free_state
+ * cannot be, PKV_ERRBIT_STEP is set and nothing is released.
+ */
+pkv_status kv_tables_grow(const pkv_pool* pool, int32_t* block_tables, int32_t max_blocks_per_seq,
+                          const int32_t* seq_lens, const int32_t* new_tokens, int32_t num_seqs,
+                          const int32_t* free_ring, int32_t ring_size, const int32_t* free_state,
+                          int32_t max_tokens, int64_t* slot_mapping, int32_t* positions, int32_t* token_seqs,
+                          int32_t* token_offsets, int32_t* granted, int32_t* seq_lens_out, int32_t* free_state_out,
+                          void* stream);
+pkv_status kv_tables_release(const pkv_pool* pool, const int32_t* block_tables, int32_t max_blocks_per_seq,
+                             const int32_t* seq_lens, const int32_t* finished, const int32_t* keep_blocks,
+                             int32_t num_seqs, int32_t* free_ring, int32_t ring_size, const int32_t* free_state,
+                             int32_t* seq_lens_out, int32_t* free_state_out, void* stream);
 
 /*
  * Host-side block manager ("How does TensorRT-LLM work?", "The paged KV

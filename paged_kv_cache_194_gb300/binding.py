@@ -7,9 +7,10 @@ there is no fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Sequence, Tuple
 
 import torch
 
@@ -21,12 +22,15 @@ ALGOS = {"auto": 0, "simt": 1, "mma": 2, "tc": 3}
 STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported", 3: "workspace", 4: "cuda error",
           5: "device bounds", 6: "out of blocks", 7: "inconsistent"}
 ERRBIT_BLOCK_ID, ERRBIT_SLOT, ERRBIT_SEQ_LEN, ERRBIT_TIMEOUT = 1, 2, 4, 8
+ERRBIT_POSITION, ERRBIT_STEP, ERRBIT_GROUP = 16, 32, 64
 
 # Every symbol include/pkv.h declares.
 EXPORTS = ("kv_pool_create", "kv_pool_destroy", "kv_pool_tensor_bytes", "kv_bytes_per_token",
            "kv_append", "paged_decode_plan", "paged_decode_algo", "paged_decode_attention",
            "paged_multi_query_plan", "paged_multi_query_algo", "paged_multi_query_attention",
            "paged_decode_append_attention",
+           "paged_prefix_decode_plan", "paged_prefix_decode_algo", "paged_prefix_decode_attention",
+           "kv_append_norm_rope", "kv_tables_grow", "kv_tables_release",
            "paged_decode_attention_static_ws", "pkv_set_first_wait_limit_for_testing", "pkv_status_string",
            "pkv_last_cuda_error",
            "kv_block_manager_create", "kv_block_manager_destroy", "kv_bm_num_free", "kv_bm_add_sequence",
@@ -51,6 +55,13 @@ class PoolDesc(ctypes.Structure):
                 ("head_dim", ctypes.c_int32), ("kv_dtype", ctypes.c_int), ("k_scale", ctypes.c_float),
                 ("v_scale", ctypes.c_float), ("k_base", ctypes.c_void_p), ("v_base", ctypes.c_void_p),
                 ("error_word", ctypes.c_void_p)]
+
+
+class NormRopeDesc(ctypes.Structure):
+    _fields_ = [("cos_sin", ctypes.c_void_p), ("max_pos", ctypes.c_int32), ("rotary_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("num_axes", ctypes.c_int32), ("sections", ctypes.c_int32 * 3),
+                ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("weight_dtype", ctypes.c_int),
+                ("eps", ctypes.c_float)]
 
 
 _lib = None
@@ -101,6 +112,20 @@ def lib() -> ctypes.CDLL:
                                                    c.c_int32, c.c_int32, c.c_float, c.c_int32, c.c_int, P, P]
     L.paged_decode_algo.restype = c.c_int32
     L.paged_decode_algo.argtypes = [P, c.c_int32, c.c_int]
+    L.paged_prefix_decode_plan.restype = c.c_int
+    L.paged_prefix_decode_plan.argtypes = [P, c.c_int32, c.c_int32, c.c_int32, c.c_int32, c.POINTER(c.c_size_t)]
+    L.paged_prefix_decode_algo.restype = c.c_int32
+    L.paged_prefix_decode_algo.argtypes = [P, c.c_int32, c.c_int32, c.c_int32, c.c_int32, c.c_int]
+    L.paged_prefix_decode_attention.restype = c.c_int
+    L.paged_prefix_decode_attention.argtypes = [P, c.c_int, P, c.c_int32, P, c.c_int32, P, c.c_int32, c.c_int32,
+                                                c.c_int32, P, P, c.c_int32, c.c_float, c.c_int, P, c.c_size_t, P, P]
+    L.kv_append_norm_rope.restype = c.c_int
+    L.kv_append_norm_rope.argtypes = [P, c.c_int32, P, P, P, c.c_int, c.c_int64, c.c_int64, c.c_int64, P, P,
+                                      c.c_int32, c.c_int32, c.POINTER(NormRopeDesc), P, P]
+    L.kv_tables_grow.restype = c.c_int
+    L.kv_tables_grow.argtypes = [P, P, c.c_int32, P, P, c.c_int32, P, c.c_int32, P, c.c_int32, P, P, P, P, P, P, P, P]
+    L.kv_tables_release.restype = c.c_int
+    L.kv_tables_release.argtypes = [P, P, c.c_int32, P, P, P, c.c_int32, P, c.c_int32, P, P, P, P]
     L.pkv_set_first_wait_limit_for_testing.restype = None
     L.pkv_set_first_wait_limit_for_testing.argtypes = [c.c_int32, c.c_int32]
     L.pkv_status_string.restype = c.c_char_p
@@ -349,3 +374,254 @@ def paged_multi_query_attention(q: torch.Tensor, pool: KVPool, layer: int, block
         split_tokens, ALGOS[algo], ws_ptr, ws_bytes, _dev(out, "out", q.dtype), _stream_ptr(stream))
     _check(rc, "paged_multi_query_attention")
     return out
+
+
+# ------------------------------------------------------------- one decode step
+# The calls below check that every tensor lies on the pool's device and launch
+# there, whatever device is current; what they allocate belongs to the stream
+# they run on.  A decode step makes them for every layer and their kernels take
+# a few microseconds, so the checks are kept short (messages are made only when
+# one fails).
+
+def _refuse(name: str, t: torch.Tensor, dev: torch.device, dtype, shape):
+    if t.device != dev:
+        raise ValueError("%s must be on %s, the pool's device, not %s" % (name, dev, t.device))
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if shape is not None and t.shape != shape:
+        raise ValueError("%s must be of shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    raise ValueError("%s must be contiguous" % name)
+
+
+def _ptr_on(dev: torch.device, name: str, t: torch.Tensor, dtype, shape) -> int:
+    """Data pointer of a contiguous tensor of this device, dtype and shape (None: any)."""
+    if (t.device != dev or (dtype is not None and t.dtype != dtype) or (shape is not None and t.shape != shape)
+            or not t.is_contiguous()):
+        _refuse(name, t, dev, dtype, shape)
+    return t.data_ptr()
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _device_of(pool: KVPool, stream):
+    """Context in which the pool's device is current, and `stream` when given
+    (so that allocations belong to it)."""
+    dev = pool.k.device
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError("stream must be on %s, the pool's device, not %s" % (dev, stream.device))
+        return torch.cuda.stream(stream)
+    if dev.type != "cuda" or dev.index == torch.cuda.current_device():
+        return _HERE
+    return torch.cuda.device(dev)
+
+
+def _stream_of(pool: KVPool, stream) -> int:
+    return (torch.cuda.current_stream(pool.k.device) if stream is None else stream).cuda_stream
+
+
+def _table_width(block_tables: torch.Tensor, num_seqs: int) -> int:
+    if block_tables.dim() != 2 or block_tables.shape[0] != num_seqs:
+        raise ValueError("block_tables must be [num_seqs, max_blocks]")
+    return block_tables.shape[1]
+
+
+def prefix_decode_workspace(pool: KVPool, num_seqs: int, num_groups: int, num_q_heads: int,
+                            max_seq_len: int) -> Optional[torch.Tensor]:
+    """A zeroed workspace for paged_prefix_decode_attention calls of this size."""
+    ws = ctypes.c_size_t()
+    with _device_of(pool, None):
+        _check(lib().paged_prefix_decode_plan(pool.handle, num_seqs, num_groups, num_q_heads, max_seq_len,
+                                              ctypes.byref(ws)), "paged_prefix_decode_plan")
+        return torch.zeros(ws.value, dtype=torch.uint8, device=pool.k.device) if ws.value else None
+
+
+def prefix_decode_algo(pool: KVPool, num_seqs: int, num_groups: int, num_q_heads: int, max_seq_len: int,
+                       algo: str = "auto") -> str:
+    """Kernel design of such a call: "tc" shares the prefixes."""
+    r = lib().paged_prefix_decode_algo(pool.handle, num_seqs, num_groups, num_q_heads, max_seq_len, ALGOS[algo])
+    if r < 0:
+        raise PkvError(2, "no kernel design serves this request")
+    return ALGO_NAMES[r]
+
+
+def paged_prefix_decode_attention(q: torch.Tensor, pool: KVPool, layer: int, block_tables: torch.Tensor,
+                                  seq_lens: torch.Tensor, max_seq_len: int, group_offsets: torch.Tensor,
+                                  prefix_lens: torch.Tensor, scale: float, out: Optional[torch.Tensor] = None,
+                                  workspace: Optional[torch.Tensor] = None, algo: str = "auto",
+                                  stream=None) -> torch.Tensor:
+    """paged_decode_attention for a batch whose sequences group_offsets[g] ..
+    group_offsets[g + 1] - 1 share their first prefix_lens[g] tokens (int32
+    tensors [groups + 1] and [groups]): each prefix is read once per group."""
+    B, Hq, D = q.shape
+    G = prefix_lens.shape[0]
+    if D != pool.head_dim:
+        raise ValueError("q must be [num_seqs, num_q_heads, head_dim]")
+    width = _table_width(block_tables, B)
+    with _device_of(pool, stream):
+        if out is None:
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        if workspace is None:
+            workspace = prefix_decode_workspace(pool, B, G, Hq, max_seq_len)
+        dev, i32 = pool.k.device, torch.int32
+        ws = _ptr_on(dev, "workspace", workspace, None, None) if workspace is not None else None
+        rc = lib().paged_prefix_decode_attention(
+            _ptr_on(dev, "q", q, None, None), _dtype_code(q.dtype), pool.handle, layer,
+            _ptr_on(dev, "block_tables", block_tables, i32, None), width, _ptr_on(dev, "seq_lens", seq_lens, i32, (B,)),
+            B, Hq, max_seq_len, _ptr_on(dev, "group_offsets", group_offsets, i32, (G + 1,)),
+            _ptr_on(dev, "prefix_lens", prefix_lens, i32, (G,)), G, scale, ALGOS[algo], ws,
+            workspace.numel() * workspace.element_size() if workspace is not None else 0,
+            _ptr_on(dev, "out", out, q.dtype, q.shape), _stream_of(pool, stream))
+    _check(rc, "paged_prefix_decode_attention")
+    return out
+
+
+class RopeTable:
+    """Cosines and sines of rotary positions: cos_sin [max_pos, rotary_dim]
+    float32, cosines of the rotary_dim / 2 pairs, then sines.  sections: the
+    pairs that follow each position axis, in order (default: all, one axis).
+    interleaved: pairs are (2 j, 2 j + 1) instead of (j, j + rotary_dim / 2)."""
+
+    def __init__(self, cos_sin: torch.Tensor, sections: Optional[Sequence[int]] = None, interleaved: bool = False):
+        if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32 or not cos_sin.is_contiguous():
+            raise ValueError("cos_sin must be a contiguous float32 [max_pos, rotary_dim] tensor")
+        self.cos_sin = cos_sin
+        self.sections = tuple(int(s) for s in (sections if sections is not None else (cos_sin.shape[1] // 2,)))
+        self.interleaved = bool(interleaved)
+        if not 1 <= len(self.sections) <= 3 or min(self.sections) < 0 or 2 * sum(self.sections) != cos_sin.shape[1]:
+            raise ValueError("sections must be 1 to 3 counts of pairs that sum to rotary_dim / 2")
+        self._desc = NormRopeDesc(max_pos=cos_sin.shape[0], rotary_dim=cos_sin.shape[1],
+                                  interleaved=int(self.interleaved), num_axes=len(self.sections),
+                                  sections=(ctypes.c_int32 * 3)(*self.sections))
+
+    @classmethod
+    def create(cls, max_pos: int, rotary_dim: int, base: float = 10000.0, sections: Optional[Sequence[int]] = None,
+               interleaved: bool = False, device="cuda") -> "RopeTable":
+        """The usual table: pair j of position p turns by p * base^(-2 j /
+        rotary_dim), the angle taken in 64 bits (a 32-bit one is off by 0.004
+        at position 65536)."""
+        j = torch.arange(rotary_dim // 2, dtype=torch.float64)
+        a = torch.arange(max_pos, dtype=torch.float64)[:, None] * float(base) ** (-2.0 * j / rotary_dim)
+        return cls(torch.cat([a.cos(), a.sin()], 1).to(torch.float32).to(device), sections, interleaved)
+
+
+def _head_rows(dev: torch.device, name: str, x: torch.Tensor, shape, dtype) -> int:
+    """Token stride (elements) of x [T, heads, head_dim], whose heads must lie one after the other."""
+    if x.shape != shape or x.dtype != dtype:
+        raise ValueError("%s must be %s %s, got %s %s" % (name, dtype, shape, x.dtype, tuple(x.shape)))
+    if x.device != dev:
+        raise ValueError("%s must be on %s, the pool's device, not %s" % (name, dev, x.device))
+    s0, s1, s2 = x.stride()
+    if s2 != 1 or (s1 != shape[2] and shape[1] > 1):
+        raise ValueError("%s: a token's heads must be contiguous" % name)
+    return s0 if shape[0] > 1 else 0
+
+
+def kv_append_norm_rope(pool: KVPool, layer: int, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                        positions: torch.Tensor, slot_mapping: torch.Tensor, rope: RopeTable,
+                        q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+                        eps: float = 1e-6, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """RMS norm of every query and key head (with weights [head_dim]; none: no
+    norm), rotary positions for both, and kv_append of K and V, in one launch.
+    q [T, Hq, D], k and v [T, Hkv, D] may be slices of one projection's rows;
+    positions int32 [axes, T] (or [T] for one axis).  Returns the queries [T,
+    Hq, D] in the dtype attention takes; `out` may be a contiguous q itself."""
+    if q.dim() != 3:
+        raise ValueError("q must be [T, num_q_heads, head_dim]")
+    T, Hq = q.shape[0], q.shape[1]
+    D, dev, in_dtype = pool.head_dim, pool.k.device, q.dtype
+    kv_shape = (T, pool.num_kv_heads, D)
+    qs = _head_rows(dev, "q", q, (T, Hq, D), in_dtype)
+    ks = _head_rows(dev, "k", k, kv_shape, in_dtype)
+    vs = _head_rows(dev, "v", v, kv_shape, in_dtype)
+    axes = len(rope.sections)
+    dtype = torch.float32 if pool.kv_dtype == "f32" else torch.bfloat16
+    desc = NormRopeDesc.from_buffer_copy(rope._desc)
+    desc.cos_sin = _ptr_on(dev, "cos_sin", rope.cos_sin, torch.float32, None)
+    if q_weight is not None or k_weight is not None:
+        if q_weight is None or k_weight is None:
+            raise ValueError("q_weight and k_weight go together")
+        desc.q_weight = _ptr_on(dev, "q_weight", q_weight, None, (D,))
+        desc.k_weight = _ptr_on(dev, "k_weight", k_weight, q_weight.dtype, (D,))
+        desc.weight_dtype, desc.eps = _dtype_code(q_weight.dtype), eps
+    pp = _ptr_on(dev, "positions", positions, torch.int32, (T,) if axes == 1 and positions.dim() == 1 else (axes, T))
+    psl = _ptr_on(dev, "slot_mapping", slot_mapping, torch.int64, (T,))
+    with _device_of(pool, stream):
+        if out is None:
+            out = torch.empty((T, Hq, D), dtype=dtype, device=dev)
+        rc = lib().kv_append_norm_rope(pool.handle, layer, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                       _dtype_code(in_dtype), qs, ks, vs, pp, psl, T, Hq, desc,
+                                       _ptr_on(dev, "out", out, dtype, (T, Hq, D)), _stream_of(pool, stream))
+    _check(rc, "kv_append_norm_rope")
+    return out
+
+
+class StepTables(NamedTuple):
+    """What kv_tables_grow writes (beside the block tables)."""
+    slot_mapping: torch.Tensor    # int64 [max_tokens]
+    positions: torch.Tensor       # int32 [max_tokens]
+    token_seqs: torch.Tensor      # int32 [max_tokens]
+    token_offsets: torch.Tensor   # int32 [num_seqs + 1]
+    granted: torch.Tensor         # int32 [num_seqs]
+    seq_lens: torch.Tensor        # int32 [num_seqs]
+    free_state: torch.Tensor      # int32 [2]
+
+    @classmethod
+    def empty(cls, num_seqs: int, max_tokens: int, device="cuda") -> "StepTables":
+        i32 = lambda n: torch.empty(n, dtype=torch.int32, device=device)
+        return cls(torch.empty(max_tokens, dtype=torch.int64, device=device), i32(max_tokens), i32(max_tokens),
+                   i32(num_seqs + 1), i32(num_seqs), i32(num_seqs), i32(2))
+
+
+def kv_tables_grow(pool: KVPool, block_tables: torch.Tensor, seq_lens: torch.Tensor, new_tokens: torch.Tensor,
+                   free_ring: torch.Tensor, free_state: torch.Tensor, max_tokens: int,
+                   out: Optional[StepTables] = None, stream=None) -> StepTables:
+    """Reserve the next new_tokens[b] positions of every request on the device:
+    blocks from the free ring into block_tables (in place), the slot, position
+    and request of every token row, the new lengths and free state.  All int32
+    tensors but the slots.  `out` may hold seq_lens and free_state themselves."""
+    B = seq_lens.shape[0]
+    width = _table_width(block_tables, B)
+    dev, i32, T = pool.k.device, torch.int32, max_tokens
+    with _device_of(pool, stream):
+        if out is None:
+            out = StepTables.empty(B, T, device=dev)
+        slots, positions, token_seqs, token_offsets, granted, lens_out, state_out = out
+        rc = lib().kv_tables_grow(
+            pool.handle, _ptr_on(dev, "block_tables", block_tables, i32, None), width,
+            _ptr_on(dev, "seq_lens", seq_lens, i32, (B,)), _ptr_on(dev, "new_tokens", new_tokens, i32, (B,)), B,
+            _ptr_on(dev, "free_ring", free_ring, i32, None), free_ring.numel(),
+            _ptr_on(dev, "free_state", free_state, i32, (2,)), T,
+            _ptr_on(dev, "slot_mapping", slots, torch.int64, (T,)), _ptr_on(dev, "positions", positions, i32, (T,)),
+            _ptr_on(dev, "token_seqs", token_seqs, i32, (T,)),
+            _ptr_on(dev, "token_offsets", token_offsets, i32, (B + 1,)), _ptr_on(dev, "granted", granted, i32, (B,)),
+            _ptr_on(dev, "out.seq_lens", lens_out, i32, (B,)), _ptr_on(dev, "out.free_state", state_out, i32, (2,)),
+            _stream_of(pool, stream))
+    _check(rc, "kv_tables_grow")
+    return out
+
+
+def kv_tables_release(pool: KVPool, block_tables: torch.Tensor, seq_lens: torch.Tensor, finished: torch.Tensor,
+                      free_ring: torch.Tensor, free_state: torch.Tensor, keep_blocks: Optional[torch.Tensor] = None,
+                      seq_lens_out: Optional[torch.Tensor] = None, free_state_out: Optional[torch.Tensor] = None,
+                      stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Return the blocks of every request with finished[b] != 0, but for the
+    first keep_blocks[b] of its row, to the free ring (in place).  Returns the
+    new lengths and free state; the outputs may be the inputs themselves."""
+    B = seq_lens.shape[0]
+    width = _table_width(block_tables, B)
+    dev, i32 = pool.k.device, torch.int32
+    with _device_of(pool, stream):
+        seq_lens_out = torch.empty_like(seq_lens) if seq_lens_out is None else seq_lens_out
+        free_state_out = torch.empty_like(free_state) if free_state_out is None else free_state_out
+        rc = lib().kv_tables_release(
+            pool.handle, _ptr_on(dev, "block_tables", block_tables, i32, None), width,
+            _ptr_on(dev, "seq_lens", seq_lens, i32, (B,)), _ptr_on(dev, "finished", finished, i32, (B,)),
+            _ptr_on(dev, "keep_blocks", keep_blocks, i32, (B,)) if keep_blocks is not None else None, B,
+            _ptr_on(dev, "free_ring", free_ring, i32, None), free_ring.numel(),
+            _ptr_on(dev, "free_state", free_state, i32, (2,)),
+            _ptr_on(dev, "seq_lens_out", seq_lens_out, i32, (B,)),
+            _ptr_on(dev, "free_state_out", free_state_out, i32, (2,)), _stream_of(pool, stream))
+    _check(rc, "kv_tables_release")
+    return seq_lens_out, free_state_out

@@ -579,3 +579,292 @@ pkv_status paged_decode_attention(const void* q, pkv_dtype q_dtype, const pkv_po
 }
 
 }  // extern "C"
+
+// ------------------------------------------- shared prefixes, norm + rotation, tables
+namespace pkv {
+namespace {
+
+bool prefix_tc_fits(const pkv_pool* p, int num_seqs, int num_groups, int gh, int max_seq_len) {
+    if (!attention_tc_supported(p->d.kv_dtype, p->d.head_dim, p->d.block_size)) return false;
+    if (num_seqs > kPrefixMaxSeqs || num_groups > kPrefixMaxSeqs || gh > kPrefixRows) return false;
+    // tile counts are int32
+    const int64_t tiles = (static_cast<int64_t>(max_seq_len) + kTileTokens - 1) / kTileTokens;
+    return tiles * num_seqs * p->d.num_kv_heads <= INT32_MAX / 2;
+}
+
+// Workspace of the sharing design behind the decode counters (which it leaves
+// alone, so that both kinds of calls may use one workspace).
+size_t prefix_layout(const pkv_pool* p, int num_seqs, int num_groups, int num_q_heads, uint8_t* base, PrefixArgs* a) {
+    size_t at = counters_bytes(num_seqs, p->d.num_kv_heads);
+    auto take = [&](size_t bytes) {
+        uint8_t* r = base + at;
+        at += round_up(bytes, 256);
+        return r;
+    };
+    const int ctas = bal_ctas();
+    const size_t B = num_seqs, G = num_groups, gh = num_q_heads / p->d.num_kv_heads;
+    const size_t pre = B * num_q_heads + static_cast<size_t>(ctas) * kPrefixRows, own = B * num_q_heads + ctas * gh;
+    const size_t row = static_cast<size_t>(p->d.head_dim) * sizeof(float);
+    PrefixArgs x{};
+    x.ctas = ctas;
+    x.totals = reinterpret_cast<int32_t*>(take(2 * sizeof(int32_t)));
+    x.seq_len = reinterpret_cast<int32_t*>(take(B * sizeof(int32_t)));
+    x.seq_pre = reinterpret_cast<int32_t*>(take(B * sizeof(int32_t)));
+    x.seq_group = reinterpret_cast<int32_t*>(take(B * sizeof(int32_t)));
+    x.cum_s = reinterpret_cast<int32_t*>(take(B * sizeof(int32_t)));
+    x.cum_p = reinterpret_cast<int32_t*>(take(G * sizeof(int32_t)));
+    x.groups = reinterpret_cast<int4*>(take(G * sizeof(int4)));
+    x.starts = reinterpret_cast<int4*>(take(2 * static_cast<size_t>(ctas) * sizeof(int4)));
+    x.pre_o = reinterpret_cast<float*>(take(pre * row));
+    x.pre_lse = reinterpret_cast<float*>(take(pre * sizeof(float)));
+    x.own_o = reinterpret_cast<float*>(take(own * row));
+    x.own_lse = reinterpret_cast<float*>(take(own * sizeof(float)));
+    if (a) *a = x;
+    return at;
+}
+
+// PKV_ALGO_TC when the sharing design runs, else what decode attention runs.
+int prefix_design(const pkv_pool* p, int num_seqs, int num_groups, int num_q_heads, int max_seq_len, pkv_algo algo) {
+    const int gh = num_q_heads / p->d.num_kv_heads;
+    if (algo == PKV_ALGO_AUTO || algo == PKV_ALGO_TC) {
+        pkv_pool* mp = const_cast<pkv_pool*>(p);
+        if (prefix_tc_fits(p, num_seqs, num_groups, gh, max_seq_len) && ensure_tmaps(mp) && p->tmap_half == 1)
+            return PKV_ALGO_TC;
+        if (algo == PKV_ALGO_TC) return -1;
+    }
+    return design_for(p, 1, gh, 0, algo, false);
+}
+
+bool ranges_overlap(const void* a, size_t na, const void* b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
+}
+
+}  // namespace
+}  // namespace pkv
+
+extern "C" {
+
+pkv_status paged_prefix_decode_plan(const pkv_pool* p, int32_t num_seqs, int32_t num_groups, int32_t num_q_heads,
+                                    int32_t max_seq_len, size_t* ws_out) {
+    if (num_groups < 0) return PKV_ERR_INVALID_ARG;
+    size_t need = 0;
+    const pkv_status st = paged_decode_plan(p, num_seqs, num_q_heads, max_seq_len, 0, nullptr, nullptr, &need);
+    if (st != PKV_OK) return st;
+    if (prefix_tc_fits(p, num_seqs, num_groups, num_q_heads / p->d.num_kv_heads, max_seq_len)) {
+        const size_t shared = prefix_layout(p, num_seqs, num_groups, num_q_heads, nullptr, nullptr);
+        if (shared > need) need = shared;
+    }
+    if (ws_out) *ws_out = need;
+    return PKV_OK;
+}
+
+int32_t paged_prefix_decode_algo(const pkv_pool* p, int32_t num_seqs, int32_t num_groups, int32_t num_q_heads,
+                                 int32_t max_seq_len, pkv_algo algo) {
+    if (!p || num_seqs < 0 || num_groups < 0 || num_q_heads < 1 || num_q_heads % p->d.num_kv_heads != 0 ||
+        max_seq_len < 0)
+        return -1;
+    return prefix_design(p, num_seqs, num_groups, num_q_heads, max_seq_len, algo);
+}
+
+pkv_status paged_prefix_decode_attention(const void* q, pkv_dtype q_dtype, const pkv_pool* p, int32_t layer,
+                                         const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                         const int32_t* seq_lens, int32_t num_seqs, int32_t num_q_heads,
+                                         int32_t max_seq_len, const int32_t* group_offsets,
+                                         const int32_t* prefix_lens, int32_t num_groups, float scale, pkv_algo algo,
+                                         void* workspace, size_t workspace_bytes, void* out, void* stream) {
+    size_t need = 0;
+    if (!p) return PKV_ERR_INVALID_ARG;
+    pkv_status st = paged_prefix_decode_plan(p, num_seqs, num_groups, num_q_heads, max_seq_len, &need);
+    if (st != PKV_OK) return st;
+    if (num_groups > 0 && (!group_offsets || !prefix_lens || !aligned(group_offsets, 4) || !aligned(prefix_lens, 4)))
+        return PKV_ERR_INVALID_ARG;
+    const int design = prefix_design(p, num_seqs, num_groups, num_q_heads, max_seq_len, algo);
+    // every other check is decode attention's (TC there means another kernel)
+    const pkv_algo decode_algo = algo == PKV_ALGO_TC ? PKV_ALGO_AUTO : algo;
+    st = attention_call(q, q_dtype, p, layer, block_tables, max_blocks_per_seq, seq_lens, num_seqs, 1, num_q_heads,
+                        max_seq_len, scale, 0, decode_algo, workspace, workspace_bytes, out, stream, nullptr, nullptr,
+                        PKV_BF16, true);
+    // (which may lack a kernel for a number of query heads that sharing serves)
+    if (st != PKV_OK && !(design == PKV_ALGO_TC && st == PKV_ERR_UNSUPPORTED && q_dtype == PKV_BF16)) return st;
+    if (design < 0) return PKV_ERR_UNSUPPORTED;
+    if (num_seqs == 0) return PKV_OK;
+    if (!workspace || workspace_bytes < need || !aligned(workspace, 256)) return PKV_ERR_WORKSPACE;
+    if (design != PKV_ALGO_TC)
+        return attention_call(q, q_dtype, p, layer, block_tables, max_blocks_per_seq, seq_lens, num_seqs, 1,
+                              num_q_heads, max_seq_len, scale, 0, algo, workspace, workspace_bytes, out, stream,
+                              nullptr, nullptr, PKV_BF16);
+    PrefixArgs a{};
+    prefix_layout(p, num_seqs, num_groups, num_q_heads, static_cast<uint8_t*>(workspace), &a);
+    a.q = q;
+    a.out = out;
+    a.tables = block_tables;
+    a.lens = seq_lens;
+    a.group_offsets = group_offsets;
+    a.prefix_lens = prefix_lens;
+    a.err = p->d.error_word;
+    a.layer = layer;
+    a.max_blocks = max_blocks_per_seq;
+    a.max_len = max_seq_len;
+    a.num_seqs = num_seqs;
+    a.num_groups = num_groups;
+    a.num_q_heads = num_q_heads;
+    a.num_kv_heads = p->d.num_kv_heads;
+    a.block_size = p->d.block_size;
+    a.num_blocks = p->d.num_blocks;
+    a.gh = num_q_heads / p->d.num_kv_heads;
+    a.seqs_per_tile = kPrefixRows / a.gh;
+    a.qk_scale_log2 = scale * p->d.k_scale * 1.4426950408889634f;
+    a.v_scale = p->d.v_scale;
+    return cuda_status(launch_prefix_attention(a, &p->tmap_kh, &p->tmap_vh, static_cast<cudaStream_t>(stream)));
+}
+
+pkv_status kv_append_norm_rope(const pkv_pool* p, int32_t layer, const void* q, const void* k, const void* v,
+                               pkv_dtype in_dtype, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                               const int32_t* positions, const int64_t* slot_mapping, int32_t num_tokens,
+                               int32_t num_q_heads, const pkv_norm_rope* r, void* q_out, void* stream) {
+    if (!p || !r || layer < 0 || layer >= p->d.num_layers || num_tokens < 0 || num_q_heads < 1)
+        return PKV_ERR_INVALID_ARG;
+    if (in_dtype != PKV_F32 && in_dtype != PKV_BF16) return PKV_ERR_INVALID_ARG;
+    if (p->d.kv_dtype == PKV_F32 && in_dtype != PKV_F32) return PKV_ERR_UNSUPPORTED;
+    const int D = p->d.head_dim;
+    if (static_cast<int64_t>(num_q_heads) + 2LL * p->d.num_kv_heads > (1 << 20)) return PKV_ERR_UNSUPPORTED;
+    if (r->rotary_dim < 16 || r->rotary_dim > D || r->rotary_dim % 16 != 0 || r->max_pos < 1)
+        return PKV_ERR_INVALID_ARG;
+    if ((r->interleaved != 0 && r->interleaved != 1) || r->num_axes < 1 || r->num_axes > 3) return PKV_ERR_INVALID_ARG;
+    int64_t pairs = 0;
+    for (int i = 0; i < r->num_axes; ++i) {
+        if (r->sections[i] < 0) return PKV_ERR_INVALID_ARG;
+        pairs += r->sections[i];
+    }
+    if (pairs != r->rotary_dim / 2) return PKV_ERR_INVALID_ARG;
+    if ((r->q_weight == nullptr) != (r->k_weight == nullptr)) return PKV_ERR_INVALID_ARG;
+    if (r->q_weight) {
+        if (r->weight_dtype != PKV_F32 && r->weight_dtype != PKV_BF16) return PKV_ERR_INVALID_ARG;
+        if (!aligned(r->q_weight, 16) || !aligned(r->k_weight, 16)) return PKV_ERR_INVALID_ARG;
+        if (!(std::isfinite(r->eps) && r->eps > 0.f)) return PKV_ERR_INVALID_ARG;
+    }
+    for (int64_t s : {q_stride, k_stride, v_stride})
+        if (s < 0 || s % 8 != 0 || s > INT64_MAX / 8 / (num_tokens > 0 ? num_tokens : 1)) return PKV_ERR_INVALID_ARG;
+    if (num_tokens == 0) return PKV_OK;
+    if (!q || !k || !v || !q_out || !positions || !slot_mapping || !r->cos_sin) return PKV_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) || !aligned(r->cos_sin, 16) ||
+        !aligned(positions, 4) || !aligned(slot_mapping, 8))
+        return PKV_ERR_INVALID_ARG;
+    const pkv_dtype q_dtype = p->d.kv_dtype == PKV_F32 ? PKV_F32 : PKV_BF16;
+    const size_t in_bytes = dtype_bytes(in_dtype), T1 = num_tokens - 1;
+    const size_t q_row = static_cast<size_t>(num_q_heads) * D, kv_row = static_cast<size_t>(p->d.num_kv_heads) * D;
+    const size_t out_bytes = q_row * num_tokens * dtype_bytes(q_dtype);
+    const bool in_place = q_out == q && q_dtype == in_dtype && (num_tokens == 1 || q_stride == static_cast<int64_t>(q_row));
+    if (!in_place && ranges_overlap(q_out, out_bytes, q, (T1 * q_stride + q_row) * in_bytes)) return PKV_ERR_INVALID_ARG;
+    if (ranges_overlap(q_out, out_bytes, k, (T1 * k_stride + kv_row) * in_bytes) ||
+        ranges_overlap(q_out, out_bytes, v, (T1 * v_stride + kv_row) * in_bytes))
+        return PKV_ERR_INVALID_ARG;
+    NormRopeArgs a{};
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.q_out = q_out;
+    a.k_layer = static_cast<uint8_t*>(p->d.k_base) + static_cast<size_t>(layer) * p->layer_bytes;
+    a.v_layer = static_cast<uint8_t*>(p->d.v_base) + static_cast<size_t>(layer) * p->layer_bytes;
+    a.positions = positions;
+    a.slots = slot_mapping;
+    a.cos_sin = r->cos_sin;
+    a.q_weight = r->q_weight;
+    a.k_weight = r->k_weight;
+    a.weight_dtype = r->weight_dtype;
+    a.eps = r->eps;
+    a.num_tokens = num_tokens;
+    a.num_q_heads = num_q_heads;
+    a.num_kv_heads = p->d.num_kv_heads;
+    a.num_slots = static_cast<int64_t>(p->d.num_blocks) * p->d.block_size;
+    a.block_shift = p->d.block_size == 16 ? 4 : (p->d.block_size == 32 ? 5 : 6);
+    a.max_pos = r->max_pos;
+    a.rotary_dim = r->rotary_dim;
+    a.interleaved = r->interleaved;
+    a.num_axes = r->num_axes;
+    a.axis_end[0] = r->sections[0];
+    a.axis_end[1] = r->num_axes > 1 ? r->sections[0] + r->sections[1] : r->sections[0];
+    a.k_inv_scale = p->k_inv_scale;
+    a.v_inv_scale = p->v_inv_scale;
+    a.err = p->d.error_word;
+    return cuda_status(launch_norm_rope_append(p->d.kv_dtype, in_dtype, D, a, static_cast<cudaStream_t>(stream)));
+}
+
+pkv_status kv_tables_grow(const pkv_pool* p, int32_t* block_tables, int32_t max_blocks_per_seq,
+                          const int32_t* seq_lens, const int32_t* new_tokens, int32_t num_seqs,
+                          const int32_t* free_ring, int32_t ring_size, const int32_t* free_state, int32_t max_tokens,
+                          int64_t* slot_mapping, int32_t* positions, int32_t* token_seqs, int32_t* token_offsets,
+                          int32_t* granted, int32_t* seq_lens_out, int32_t* free_state_out, void* stream) {
+    if (!p || num_seqs < 0 || max_blocks_per_seq < 1 || ring_size < 1 || max_tokens < 0) return PKV_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(max_blocks_per_seq) * p->d.block_size > INT32_MAX) return PKV_ERR_UNSUPPORTED;
+    if (num_seqs > 0 && (!block_tables || !seq_lens || !new_tokens || !granted || !seq_lens_out))
+        return PKV_ERR_INVALID_ARG;
+    if (max_tokens > 0 && (!slot_mapping || !positions || !token_seqs)) return PKV_ERR_INVALID_ARG;
+    if (!free_ring || !free_state || !free_state_out || !token_offsets) return PKV_ERR_INVALID_ARG;
+    for (const void* x : {static_cast<const void*>(block_tables), static_cast<const void*>(seq_lens),
+                          static_cast<const void*>(new_tokens), static_cast<const void*>(free_ring),
+                          static_cast<const void*>(free_state), static_cast<const void*>(positions),
+                          static_cast<const void*>(token_seqs), static_cast<const void*>(token_offsets),
+                          static_cast<const void*>(granted), static_cast<const void*>(seq_lens_out),
+                          static_cast<const void*>(free_state_out)})
+        if (!aligned(x, 4)) return PKV_ERR_INVALID_ARG;
+    if (!aligned(slot_mapping, 8)) return PKV_ERR_INVALID_ARG;
+    GrowArgs a{};
+    a.lens = seq_lens;
+    a.new_tokens = new_tokens;
+    a.tables = block_tables;
+    a.ring = free_ring;
+    a.free_state = free_state;
+    a.ring_size = ring_size;
+    a.num_seqs = num_seqs;
+    a.max_blocks = max_blocks_per_seq;
+    a.block_size = p->d.block_size;
+    a.num_blocks = p->d.num_blocks;
+    a.max_tokens = max_tokens;
+    a.slots = slot_mapping;
+    a.positions = positions;
+    a.token_seqs = token_seqs;
+    a.token_offsets = token_offsets;
+    a.granted = granted;
+    a.lens_out = seq_lens_out;
+    a.free_out = free_state_out;
+    a.err = p->d.error_word;
+    return cuda_status(launch_tables_grow(a, static_cast<cudaStream_t>(stream)));
+}
+
+pkv_status kv_tables_release(const pkv_pool* p, const int32_t* block_tables, int32_t max_blocks_per_seq,
+                             const int32_t* seq_lens, const int32_t* finished, const int32_t* keep_blocks,
+                             int32_t num_seqs, int32_t* free_ring, int32_t ring_size, const int32_t* free_state,
+                             int32_t* seq_lens_out, int32_t* free_state_out, void* stream) {
+    if (!p || num_seqs < 0 || max_blocks_per_seq < 1 || ring_size < 1) return PKV_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(max_blocks_per_seq) * p->d.block_size > INT32_MAX) return PKV_ERR_UNSUPPORTED;
+    if (num_seqs > 0 && (!block_tables || !seq_lens || !finished || !seq_lens_out)) return PKV_ERR_INVALID_ARG;
+    if (!free_ring || !free_state || !free_state_out) return PKV_ERR_INVALID_ARG;
+    for (const void* x : {static_cast<const void*>(block_tables), static_cast<const void*>(seq_lens),
+                          static_cast<const void*>(finished), static_cast<const void*>(keep_blocks),
+                          static_cast<const void*>(free_ring), static_cast<const void*>(free_state),
+                          static_cast<const void*>(seq_lens_out), static_cast<const void*>(free_state_out)})
+        if (!aligned(x, 4)) return PKV_ERR_INVALID_ARG;
+    ReleaseArgs a{};
+    a.lens = seq_lens;
+    a.finished = finished;
+    a.keep_blocks = keep_blocks;
+    a.tables = block_tables;
+    a.ring = free_ring;
+    a.free_state = free_state;
+    a.ring_size = ring_size;
+    a.num_seqs = num_seqs;
+    a.max_blocks = max_blocks_per_seq;
+    a.block_size = p->d.block_size;
+    a.num_blocks = p->d.num_blocks;
+    a.lens_out = seq_lens_out;
+    a.free_out = free_state_out;
+    a.err = p->d.error_word;
+    return cuda_status(launch_tables_release(a, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -116,4 +116,90 @@ cudaError_t launch_combine(pkv_dtype q_dtype, const DecodeArgs& a, cudaStream_t 
 bool attention_tc_supported(pkv_dtype kv, int head_dim, int block_size);
 cudaError_t launch_attention_tc(const DecodeArgs& a, const void* tmap_k, const void* tmap_v, cudaStream_t stream);
 
+// ------------------------------------------------- decode over shared prefixes
+constexpr int kPrefixMaxSeqs = 4096;  // sequences (and groups) the plan kernel keeps on chip
+constexpr int kPrefixRows = 128;      // query rows of one tile
+
+struct PrefixArgs {
+    const void* q;
+    void* out;
+    const int32_t* tables;
+    const int32_t* lens;
+    const int32_t* group_offsets;  // [num_groups + 1]
+    const int32_t* prefix_lens;    // [num_groups]
+    int32_t* err;
+    int layer, max_blocks, max_len, num_seqs, num_groups, num_q_heads, num_kv_heads, block_size, num_blocks;
+    int gh;                        // query heads per KV head
+    int seqs_per_tile;             // sequences whose rows fill a 128-row tile
+    int ctas;                      // CTAs of the attention kernel
+    float qk_scale_log2, v_scale;
+    // workspace: the plan ...
+    int32_t* totals;               // {shared tiles, own tiles}
+    int32_t* seq_len;              // [B] clamped lengths
+    int32_t* seq_pre;              // [B] tokens read with the group
+    int32_t* seq_group;            // [B] group, or -1
+    int32_t* cum_s;                // [B] own tiles of the sequences before
+    int32_t* cum_p;                // [G] shared tiles of the groups before
+    int4* groups;                  // [G] {first sequence, sequences, shared tiles, table row}
+    int4* starts;                  // [2][ctas] {group or sequence, unit, tile, tiles of the range}
+    // ... and the pieces: fp32 rows of O / l and log2-sum-exp
+    float *pre_o, *pre_lse;        // [B * Hq + ctas * 128]
+    float *own_o, *own_lse;        // [B * Hq + ctas * gh]
+};
+cudaError_t launch_prefix_attention(const PrefixArgs& a, const void* tmap_k, const void* tmap_v, cudaStream_t stream);
+
+// -------------------------------------------------- norm, rotation and append
+struct NormRopeArgs {
+    const void *q, *k, *v;                      // rows of one token at t * stride elements
+    int64_t q_stride, k_stride, v_stride;
+    void* q_out;                                // [T][Hq][D]
+    uint8_t *k_layer, *v_layer;
+    const int32_t* positions;                   // [num_axes][T]
+    const int64_t* slots;                       // [T]
+    const float* cos_sin;                       // [max_pos][rotary_dim]
+    const void *q_weight, *k_weight;            // [D], both or neither
+    int weight_dtype;
+    float eps;
+    int num_tokens, num_q_heads, num_kv_heads;
+    int64_t num_slots;
+    int block_shift;                            // log2(block_size)
+    int max_pos, rotary_dim, interleaved, num_axes;
+    int axis_end[2];                            // pairs of the first, and of the first two axes
+    float k_inv_scale, v_inv_scale;
+    int tokens_per_cta;                         // set by the launcher
+    int32_t* err;
+};
+cudaError_t launch_norm_rope_append(pkv_dtype pool, pkv_dtype in, int head_dim, NormRopeArgs a, cudaStream_t stream);
+
+// ----------------------------------------------------- tables and slots of a step
+struct GrowArgs {
+    const int32_t* lens;
+    const int32_t* new_tokens;
+    int32_t* tables;                            // [B][max_blocks]
+    const int32_t* ring;                        // free blocks: entries head .. head + count - 1, wrapping
+    const int32_t* free_state;                  // {head, count}
+    int ring_size, num_seqs, max_blocks, block_size, num_blocks, max_tokens;
+    int64_t* slots;                             // [max_tokens]
+    int32_t *positions, *token_seqs;            // [max_tokens]
+    int32_t* token_offsets;                     // [B + 1]
+    int32_t *granted, *lens_out;                // [B]
+    int32_t* free_out;
+    int32_t* err;
+};
+cudaError_t launch_tables_grow(const GrowArgs& a, cudaStream_t stream);
+
+struct ReleaseArgs {
+    const int32_t* lens;
+    const int32_t* finished;
+    const int32_t* keep_blocks;                 // optional
+    const int32_t* tables;
+    int32_t* ring;
+    const int32_t* free_state;
+    int ring_size, num_seqs, max_blocks, block_size, num_blocks;
+    int32_t* lens_out;
+    int32_t* free_out;
+    int32_t* err;
+};
+cudaError_t launch_tables_release(const ReleaseArgs& a, cudaStream_t stream);
+
 }  // namespace pkv
