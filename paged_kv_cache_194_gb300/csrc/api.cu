@@ -623,6 +623,21 @@ size_t prefix_layout(const pkv_pool* p, int num_seqs, int num_groups, int num_q_
     return at;
 }
 
+// Descriptor of the queries [B][Hq][128] BF16 as {64 columns, Hq, B, 2 column
+// halves}; one box is the heads of one KV head of `seqs` sequences, so it lands
+// as rows (sequence, head) of 128 bytes.
+bool encode_q_map(CUtensorMap* map, const void* q, int num_seqs, int num_q_heads, int gh, int seqs) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    const cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(num_q_heads), static_cast<cuuint64_t>(num_seqs), 2};
+    const cuuint64_t strides[3] = {256, 256ull * num_q_heads, 128};
+    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(gh), static_cast<cuuint32_t>(seqs), 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(q), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // PKV_ALGO_TC when the sharing design runs, else what decode attention runs.
 int prefix_design(const pkv_pool* p, int num_seqs, int num_groups, int num_q_heads, int max_seq_len, pkv_algo algo) {
     const int gh = num_q_heads / p->d.num_kv_heads;
@@ -716,7 +731,12 @@ pkv_status paged_prefix_decode_attention(const void* q, pkv_dtype q_dtype, const
     a.seqs_per_tile = kPrefixRows / a.gh;
     a.qk_scale_log2 = scale * p->d.k_scale * 1.4426950408889634f;
     a.v_scale = p->d.v_scale;
-    return cuda_status(launch_prefix_attention(a, &p->tmap_kh, &p->tmap_vh, static_cast<cudaStream_t>(stream)));
+    CUtensorMap q_group, q_own;
+    if (!encode_q_map(&q_group, q, num_seqs, num_q_heads, a.gh, a.seqs_per_tile) ||
+        !encode_q_map(&q_own, q, num_seqs, num_q_heads, a.gh, 1))
+        return PKV_ERR_UNSUPPORTED;
+    return cuda_status(
+        launch_prefix_attention(a, &p->tmap_kh, &p->tmap_vh, &q_group, &q_own, static_cast<cudaStream_t>(stream)));
 }
 
 pkv_status kv_append_norm_rope(const pkv_pool* p, int32_t layer, const void* q, const void* k, const void* v,

@@ -27,16 +27,16 @@
 //    tiles by memory (gh rows), and the two CTAs of an SM overlap them.  Each
 //    unit's piece leaves O / l and its log2-sum-exp in the workspace.
 //  * prefix_merge_kernel, one warp per output row, merges the pieces.
-// The tile pipeline has 7 warps:
-//  * warps 4 and 6, TMA producers for K and for V: one box {64 columns, bs
-//    rows, 1 half} per KV block and half, 128-byte swizzled: the K-major
-//    operand layout for K and the MN-major one for V;
-//  * warp 5, one thread: S = Q K^T (M 128, N 64 tokens, K 128) into one of two
+// The tile pipeline has 11 warps:
+//  * two TMA producers, for K and for V: one box {64 columns, bs rows, 1 half}
+//    per KV block and half, 128-byte swizzled: the K-major operand layout for K
+//    and the MN-major one for V; the K producer also fetches a unit's Q rows;
+//  * one MMA thread: S = Q K^T (M 128, N 64 tokens, K 128) into one of two
 //    TMEM buffers, a tile ahead of the softmax; then O += P V (N 128, K 64);
-//  * warps 0-3: softmax of row m = TMEM lane m in base 2, P back to tensor
-//    memory as BF16 pairs (half a step of 2^-9 relative each: the sum l is
-//    taken before that rounding, in fp32), the running maximum moved only
-//    when it grows by more than 8, so that O is seldom rescaled.
+//  * eight softmax warps, two threads per row (= TMEM lane): base 2, P back to
+//    tensor memory as BF16 pairs (at most 2^-8 of each weight; the sum l is
+//    taken in fp32 before that rounding), the running maximum moved only when
+//    it grows by more than 8, so that O is seldom rescaled.
 // Every wait is bounded; a CTA whose wait expires sets PKV_ERRBIT_TIMEOUT,
 // waits for its copies and products in flight, frees its TMEM and leaves.
 #include <cuda.h>
@@ -48,7 +48,9 @@
 namespace pkv {
 namespace {
 
-constexpr int kThreads = 224;  // warps 0-3 softmax, 4 K producer, 5 MMA, 6 V producer
+constexpr int kSoftmaxWarps = 8;
+constexpr int kSoftmax = 32 * kSoftmaxWarps;
+constexpr int kThreads = kSoftmax + 96;  // softmax warps, then K producer, MMA, V producer
 constexpr int kRows = kPrefixRows;
 constexpr int kTok = 64;
 constexpr int kDim = 128;
@@ -64,10 +66,34 @@ constexpr uint32_t kOCol = kNS * kTok;
 enum Bar { kQReady, kOFree, kDone, kSFull, kPFull = kSFull + kNS, kPvDone = kPFull + kNS, kKFull = kPvDone + kNS,
            kVFull = kKFull + kNS, kNumBars = kVFull + kNS };
 constexpr int kBarOff = kKVOff + kNS * kStageBytes;
-constexpr int kSmem = kBarOff + (8 * kNumBars + 8 + 63) / 64 * 64 + kAlignSlack;
+constexpr int kExOff = kBarOff + (8 * kNumBars + 8 + 63) / 64 * 64;  // the two threads of a row meet here: maxima
+constexpr int kSumOff = kExOff + 2 * kRows * 4;                        // and sums, [2][kRows] floats each
+constexpr int kSmem = kSumOff + 2 * kRows * 4 + kAlignSlack;
 static_assert(kSmem <= 115712, "two CTAs per SM");
 
 constexpr int kPlanThreads = 1024;
+
+// 16 consecutive TMEM columns of this thread's lane.
+__device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(a),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+    asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
+}
+// Rendezvous of the two warps that share 32 rows (named barrier 1 + id), and
+// with it: does any of their threads say yes?
+__device__ __forceinline__ bool pair_any(int id, bool yes) {
+    uint32_t r;
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 64, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+        : "=r"(r)
+        : "r"(yes ? 1u : 0u), "r"(1 + id)
+        : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ void pair_sync(int id) { asm volatile("barrier.cta.sync %0, 64;\n" ::"r"(1 + id) : "memory"); }
 
 // ------------------------------------------------------------------- plan
 __device__ __forceinline__ int plan_scan(int v, int* warp_sums, int* total) {  // inclusive, over the CTA
@@ -92,14 +118,19 @@ __device__ __forceinline__ int plan_scan(int v, int* warp_sums, int* total) {  /
     return v + before;
 }
 
-// A list of T tiles is cut into min(T, ctas) ranges, none of them empty: range
-// c is [c T / n, (c + 1) T / n).
+// Cost, in tiles, that a unit has beside its tiles: its Q rows to fetch, its
+// piece to write out and the pipeline to refill.  A list is cut by cost, every
+// unit being nt + kUnitCost long; the last kUnitCost of them hold no tile.
+constexpr int kUnitCost = 2;
+
+// A list of T cost units is cut into min(T, ctas) ranges, none of them empty:
+// range c is [c T / n, (c + 1) T / n).
 __device__ __forceinline__ int num_ranges(int T, int ctas) { return T < ctas ? T : ctas; }
-__device__ __forceinline__ int range_of(int x, int T, int ctas) {  // the range that tile x is in
+__device__ __forceinline__ int range_of(int x, int T, int ctas) {  // the range that x is in
     return static_cast<int>(((x + 1LL) * num_ranges(T, ctas) - 1) / T);
 }
-// Start of range c: unit group i (cum[i] <= tile < cum[i + 1]), tile x within
-// it, tiles in the range (0 from range n on).
+// Start of range c: group or sequence i (cum[i] <= start < cum[i + 1]), place x
+// within it, length of the range (0 from range n on).
 __device__ __forceinline__ void range_start(const int* cum, int n, int total, int ctas, int c, int* i, int* x, int* left) {
     const long long T = total, ranges = num_ranges(total, ctas);
     *i = *x = *left = 0;
@@ -172,7 +203,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixA
         int v = 0;
         if (g < G) {
             const int4 u = a.groups[g];
-            v = (u.y + a.seqs_per_tile - 1) / a.seqs_per_tile * Hkv * u.z;
+            v = u.z > 0 ? (u.y + a.seqs_per_tile - 1) / a.seqs_per_tile * Hkv * (u.z + kUnitCost) : 0;
         }
         const int incl = before + plan_scan(v, sums, &total);
         if (g < G) {
@@ -185,7 +216,8 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixA
     before = 0;
     for (int base = 0; base < B; base += kPlanThreads) {
         const int b = base + tid;
-        const int v = b < B ? ((a.seq_len[b] + kTok - 1) / kTok - a.seq_pre[b] / kTok) * Hkv : 0;
+        const int nt = b < B ? (a.seq_len[b] + kTok - 1) / kTok - a.seq_pre[b] / kTok : 0;
+        const int v = nt > 0 ? (nt + kUnitCost) * Hkv : 0;
         const int incl = before + plan_scan(v, sums, &total);
         if (b < B) {
             cum_s[b] = incl - v;
@@ -202,115 +234,115 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixA
     for (int c = tid; c < a.ctas; c += kPlanThreads) {
         int i, x, left;
         range_start(cum_p, G, T1, a.ctas, c, &i, &x, &left);
-        const int nt = left > 0 ? a.groups[i].z : 1;
+        const int nt = left > 0 ? a.groups[i].z + kUnitCost : 1;
         a.starts[c] = make_int4(i, x / nt, x % nt, left);
         range_start(cum_s, B, T2, a.ctas, c, &i, &x, &left);
-        const int ns = left > 0 ? (a.seq_len[i] + kTok - 1) / kTok - a.seq_pre[i] / kTok : 1;
+        const int ns = left > 0 ? (a.seq_len[i] + kTok - 1) / kTok - a.seq_pre[i] / kTok + kUnitCost : 1;
         a.starts[a.ctas + c] = make_int4(i, x / ns, x % ns, left);
     }
 }
 
 // ------------------------------------------------------------------- walk
-// The tiles of this CTA, in order: its range of one list, then of the other.
-// CTA c has range c of the shared tiles and the c-th range from the end of the
-// own tiles, so that short lists fall to different CTAs.
-struct Walk {
-    int own = 0;             // 0: shared tiles of a group, 1: own tiles of a sequence
-    int phase = 0, left = 0;
-    int i = 0, u = 0;        // group or sequence; KV head, or row tile * KV heads + KV head
-    int t = 0, nt = 0;       // tile of the unit, its tiles
-    int row = 0, tile0 = 0;  // table row; first tile's index in the sequence
-    int end = 0;             // tokens visible to the unit's rows
-    int seq0 = 0, nseq = 0;  // sequences of the unit's row tile
-    bool first = true;       // at the first tile of a segment
+// A run of one unit's tiles.
+struct Seg {
+    int own;             // 0: shared tiles of a group, 1: own tiles of a sequence
+    int tile, n;         // first tile's index in the sequence, tiles
+    int row;             // table row
+    int end;             // tokens visible to the unit's rows
+    int seq0, nseq;      // the sequences whose queries are the rows
+    int head;
+    int range;           // of the list (see piece_row)
 
-    __device__ bool more() const { return left > 0; }
-    __device__ bool last() const { return left == 1 || t == nt - 1; }
-    __device__ int head(const PrefixArgs& a) const { return u % a.num_kv_heads; }
     __device__ int rows(const PrefixArgs& a) const { return nseq * a.gh; }
-    __device__ int range(const PrefixArgs& a) const { return own ? a.ctas - 1 - static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x); }
-    // first row of this piece in the list's partials.  Consecutive pieces
+    // First row of this piece in the list's partials.  Consecutive pieces
     // differ by a range, a unit or both, so (rows of the units before) + (range)
     // x (rows of a full unit) never collides.
     __device__ size_t piece_row(const PrefixArgs& a) const {
         const size_t before = static_cast<size_t>(a.gh) * (static_cast<size_t>(a.num_kv_heads) * seq0 +
-                                                           static_cast<size_t>(head(a)) * nseq);
-        return before + static_cast<size_t>(range(a)) * (own ? a.gh : kRows);
+                                                           static_cast<size_t>(head) * nseq);
+        return before + static_cast<size_t>(range) * (own ? a.gh : kRows);
+    }
+};
+
+// The segments of this CTA, in order: its range of one list, then of the
+// other.  CTA c has range c of the shared tiles and the c-th range from the end
+// of the own tiles, so that short lists fall to different CTAs.
+struct Walk {
+    int phase = -1, left = 0;  // cost left of the range
+    int i = 0, u = 0, t = 0;   // group or sequence; KV head, or row tile * KV heads + KV head; place in the unit
+
+    __device__ bool next(const PrefixArgs& a, Seg& s) {
+        for (;;) {
+            int own = phase ^ static_cast<int>(blockIdx.x & 1);
+            while (left == 0) {
+                if (phase == 1) return false;
+                ++phase;
+                own = phase ^ static_cast<int>(blockIdx.x & 1);
+                s.range = own ? a.ctas - 1 - static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x);
+                const int4 st = a.starts[own * a.ctas + s.range];
+                i = st.x, u = st.y, t = st.z, left = st.w;
+            }
+            s.own = own;
+            s.range = own ? a.ctas - 1 - static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x);
+            const int nt = unit(a, s);
+            const int t0 = t, cost = min(left, nt + kUnitCost - t0);
+            left -= cost;
+            t = 0;
+            if (++u == units) {
+                u = 0;
+                ++i;
+            }
+            s.n = min(cost, nt - t0);
+            s.tile += t0;
+            if (s.n > 0) return true;  // (else only the end of a unit's cost fell into the range)
+        }
     }
 
-    __device__ void load(const PrefixArgs& a) {
+  private:
+    int units = 0;
+    // The unit at (i, u), or of the next i with tiles: everything but the range of tiles.  Returns its tiles.
+    __device__ int unit(const PrefixArgs& a, Seg& s) {
+        const int own = s.own;
+        int nt;
         if (own) {
-            const int L = a.seq_len[i], P = a.seq_pre[i];
-            row = seq0 = i;
-            nseq = 1;
-            tile0 = P / kTok;
-            nt = (L + kTok - 1) / kTok - tile0;
-            end = L;
-        } else {
-            const int4 g = a.groups[i];
-            const int r = u / a.num_kv_heads;
-            row = g.w;
-            nt = g.z;
-            tile0 = 0;
-            end = nt * kTok;
-            seq0 = g.x + r * a.seqs_per_tile;
-            nseq = min(a.seqs_per_tile, g.y - r * a.seqs_per_tile);
-        }
-    }
-    __device__ void start(const PrefixArgs& a) {
-        own = phase ^ static_cast<int>(blockIdx.x & 1);
-        const int4 s = a.starts[own * a.ctas + range(a)];
-        i = s.x, u = s.y, t = s.z, left = s.w;
-        first = true;
-        if (left > 0) load(a);
-    }
-    __device__ void init(const PrefixArgs& a) {
-        start(a);
-        if (left == 0) {
-            phase = 1;
-            start(a);
-        }
-    }
-    __device__ void next(const PrefixArgs& a) {
-        --left;
-        ++t;
-        first = false;
-        if (left == 0) {
-            if (phase == 0) {
-                phase = 1;
-                start(a);
-            }
-            return;
-        }
-        if (t < nt) return;
-        t = 0;
-        first = true;
-        ++u;
-        if (own) {
-            if (u < a.num_kv_heads) return;
-            u = 0;
-            do {
+            units = a.num_kv_heads;
+            for (;;) {
+                const int L = a.seq_len[i], P = a.seq_pre[i];
+                s.tile = P / kTok;
+                s.end = L;
+                nt = (L + kTok - 1) / kTok - s.tile;
+                if (nt > 0) break;
                 ++i;
-                load(a);
-            } while (nt <= 0);
-        } else {
-            const int4 g = a.groups[i];
-            const int units = (g.y + a.seqs_per_tile - 1) / a.seqs_per_tile * a.num_kv_heads;
-            if (u < units) {
-                load(a);
-                return;
             }
-            u = 0;
-            do {
+            s.row = s.seq0 = i;
+            s.nseq = 1;
+            s.head = u;
+        } else {
+            for (;;) {
+                const int4 g = a.groups[i];
+                nt = g.z;
+                units = (g.y + a.seqs_per_tile - 1) / a.seqs_per_tile * a.num_kv_heads;
+                if (nt > 0 && units > 0) {
+                    const int r = u / a.num_kv_heads;
+                    s.row = g.w;
+                    s.head = u - r * a.num_kv_heads;
+                    s.seq0 = g.x + r * a.seqs_per_tile;
+                    s.nseq = min(a.seqs_per_tile, g.y - r * a.seqs_per_tile);
+                    break;
+                }
                 ++i;
-                load(a);
-            } while (nt <= 0 || nseq <= 0);
+            }
+            s.tile = 0;
+            s.end = nt * kTok;
         }
+        return nt;
     }
 };
 
 __global__ void __launch_bounds__(kThreads, 2)
-prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, const PrefixArgs a) {
+prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
+                 const __grid_constant__ CUtensorMap tmq_group, const __grid_constant__ CUtensorMap tmq_own,
+                 const PrefixArgs a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = su32(smem), bars = sbase + kBarOff;
@@ -321,7 +353,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kNumBars; ++i)
-            bar_init(B(i), ((i >= kPFull && i < kPFull + kNS) || i == kQReady || i == kOFree) ? 4u : 1u);
+            bar_init(B(i), ((i >= kPFull && i < kPFull + kNS) || i == kOFree) ? kSoftmaxWarps : 1u);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
@@ -342,67 +374,96 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
         if (a.err) atomicOr(a.err, PKV_ERRBIT_TIMEOUT);
     };
     Walk w;
-    w.init(a);
 
-    if (warp == 4 || warp == 6) {
-        // ------------------------------------------- producers: K (warp 4), V (warp 6)
+    if (warp == kSoftmaxWarps || warp == kSoftmaxWarps + 2) {
+        // ------------------------------------------------ producers: K, V
         // Stage s is freed by the completion that signals score buffer s: S
         // done for K, PV done for V.
-        const bool is_v = warp == 6;
+        const bool is_v = warp == kSoftmaxWarps + 2;
         const CUtensorMap* map = is_v ? &tmv : &tmk;
         const int full0 = is_v ? kVFull : kKFull, empty0 = is_v ? kPvDone : kSFull;
         const int bs = a.block_size;
         const int64_t layer_blk0 = static_cast<int64_t>(a.layer) * a.num_blocks;
-        int cache = 0, cache_base = 0, cache_row = -1;  // 32 table entries, one per lane
-        int k = 0;
-        for (; w.more() && !*abort_flag; w.next(a), ++k) {
-            const int s = k % kNS;
-            const int tok0 = (w.tile0 + w.t) * kTok, n = min(kTok, w.end - tok0), nblk = (n + bs - 1) / bs;
-            const int idx0 = tok0 / bs;
-            if (w.row != cache_row || idx0 < cache_base || idx0 + nblk > cache_base + 32) {
-                cache_row = w.row;
-                cache_base = idx0;
-                const int idx = idx0 + lane;
-                cache = idx < a.max_blocks ? __ldg(a.tables + static_cast<size_t>(w.row) * a.max_blocks + idx) : 0;
-            }
-            if (k >= kNS && !bar_wait(B(empty0 + s), ((k / kNS) - 1) & 1)) {
-                if (lane == 0) fail();
-                break;
-            }
-            const uint32_t dst0 = sbase + kKVOff + s * kStageBytes + (is_v ? 2 * kHalfBytes : 0);
-            if (lane == 0) bar_expect_tx(B(full0 + s), static_cast<uint32_t>(nblk * bs * 128 * 2));
-            __syncwarp();
-            const int kb = lane >> 1, hf = lane & 1;  // one copy instruction: lane 2 kb + hf, half hf of block kb
-            int blk = __shfl_sync(0xFFFFFFFFu, cache, (idx0 + kb - cache_base) & 31);
-            if (kb < nblk) {
-                if (static_cast<unsigned>(blk) >= static_cast<unsigned>(a.num_blocks)) {
-                    if (a.err) atomicOr(a.err, PKV_ERRBIT_BLOCK_ID);
-                    blk = 0;  // an in-bounds block; the flag marks the output invalid
+        int k = 0, segs = 0;
+        bool ok = true;
+        Seg sg, nx;
+        bool has = w.next(a, sg);
+        while (has && ok) {
+            const bool has_next = w.next(a, nx);  // (early: its loads overlap this segment)
+            int cache = 0, cache_base = INT_MIN / 2;  // 32 table entries, one per lane
+            for (int t = 0; t < sg.n && ok; ++t, ++k) {
+                const int s = k % kNS;
+                const int tok0 = (sg.tile + t) * kTok, n = min(kTok, sg.end - tok0), nblk = (n + bs - 1) / bs;
+                const int idx0 = tok0 / bs;
+                if (idx0 + nblk > cache_base + 32) {
+                    cache_base = idx0;
+                    const int idx = idx0 + lane;
+                    cache = idx < a.max_blocks ? __ldg(a.tables + static_cast<size_t>(sg.row) * a.max_blocks + idx) : 0;
                 }
-                const int y = static_cast<int>(((layer_blk0 + blk) * a.num_kv_heads + w.head(a)) * bs);
-                tma_3d(dst0 + hf * kHalfBytes + kb * bs * 128, map, 0, y, hf, B(full0 + s));
+                if (__any_sync(0xFFFFFFFFu, *abort_flag != 0) ||
+                    (k >= kNS && !bar_wait_warp(B(empty0 + s), ((k / kNS) - 1) & 1))) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t dst0 = sbase + kKVOff + s * kStageBytes + (is_v ? 2 * kHalfBytes : 0);
+                if (lane == 0) bar_expect_tx(B(full0 + s), static_cast<uint32_t>(nblk * bs * 128 * 2));
+                __syncwarp();
+                const int kb = lane >> 1, hf = lane & 1;  // one copy instruction: lane 2 kb + hf, half hf of block kb
+                int blk = __shfl_sync(0xFFFFFFFFu, cache, (idx0 + kb - cache_base) & 31);
+                if (kb < nblk) {
+                    if (static_cast<unsigned>(blk) >= static_cast<unsigned>(a.num_blocks)) {
+                        if (a.err) atomicOr(a.err, PKV_ERRBIT_BLOCK_ID);
+                        blk = 0;  // an in-bounds block; the flag marks the output invalid
+                    }
+                    const int y = static_cast<int>(((layer_blk0 + blk) * a.num_kv_heads + sg.head) * bs);
+                    tma_3d(dst0 + hf * kHalfBytes + kb * bs * 128, map, 0, y, hf, B(full0 + s));
+                }
+                if (t == 0 && !is_v) {
+                    // The segment's Q rows, once the last S of the one before has read its own.
+                    if (k > 0 && !bar_wait_warp(B(kSFull + (k - 1) % kNS), ((k - 1) / kNS) & 1)) {
+                        ++k;
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0)
+                        bar_expect_tx(B(kQReady), static_cast<uint32_t>((sg.own ? 1 : a.seqs_per_tile) * a.gh * kDim * 2));
+                    __syncwarp();
+                    if (lane < 2)
+                        tma_4d(sbase + lane * kQHalf, sg.own ? &tmq_own : &tmq_group, 0, sg.head * a.gh, sg.seq0, lane,
+                               B(kQReady));
+                    ++segs;
+                }
             }
+            sg = nx;
+            has = has_next;
         }
+        if (!ok && lane == 0) fail();
         // drain: the copies in flight land before the CTA frees anything
         if (lane == 0)
             for (int j = k - 1; j >= 0 && j >= k - kNS; --j)
                 if (!bar_wait(B(full0 + j % kNS), (j / kNS) & 1)) fail();
-    } else if (warp == 5) {
+        if (lane == 0 && segs > 0 && !bar_wait(B(kQReady), (segs - 1) & 1)) fail();
+    } else if (warp == kSoftmaxWarps + 1) {
         // ------------------------------------------------------- MMA issuer
         if (lane == 0) {
             bool ok = true;
             const uint64_t dq = sdesc(sbase, 16);
             const uint64_t dk0 = sdesc(sbase + kKVOff, 16);
             const uint64_t dv0 = sdesc(sbase + kKVOff + 2 * kHalfBytes, kHalfBytes);
-            Walk ws = w;
+            // S of tile ns: the segment it is in has `left` tiles to go
+            Seg sg, nx;
             int ns = 0, seg_s = 0, seg = 0;  // S issued; segments begun by the S and by the PV cursor
-            for (int k = 0; w.more() && ok && !*abort_flag; w.next(a), ++k) {
+            bool has = w.next(a, sg), has_next = has && w.next(a, nx);
+            int left = has ? sg.n : 0;
+            bool first_s = true;
+            uint32_t firsts = 0;  // bit k & 1: tile k begins a segment
+            for (int k = 0; (k < ns || left > 0) && ok && !*abort_flag; ++k) {
                 // S of tile k, and of k + 1 (whose scores' buffer PV k - 1, issued
-                // already, has read).  Both may block: the softmax of tile k
-                // needs nothing further to signal P k or to store the next Q.
-                while (ws.more() && ns < k + kNS) {
+                // already, has read).  Both may block: neither the softmax of tile
+                // k nor the producers need anything further from this thread.
+                while (left > 0 && ns < k + kNS) {
                     const int st = ns % kNS;
-                    if (ws.first && !bar_wait(B(kQReady), seg_s & 1)) {
+                    if (first_s && !bar_wait(B(kQReady), seg_s & 1)) {
                         ok = false;
                         break;
                     }
@@ -410,7 +471,6 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                         ok = false;
                         break;
                     }
-                    if (ws.first) ++seg_s;
                     fence_after();
                     const uint64_t dk = dk0 + static_cast<uint64_t>((st * kStageBytes) >> 4);
                     const uint32_t sb = tmem + static_cast<uint32_t>(st * kTok);
@@ -421,27 +481,36 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                                  idesc(kTok, 0), ks > 0 ? 1u : 0u);
                     }
                     mma_commit(B(kSFull + st));
-                    ws.next(a);
+                    firsts = (firsts & ~(1u << st)) | (first_s ? 1u << st : 0u);
+                    if (first_s) ++seg_s;
+                    first_s = false;
                     ++ns;
+                    if (--left == 0 && has_next) {
+                        sg = nx;
+                        left = sg.n;
+                        first_s = true;
+                        has_next = w.next(a, nx);
+                    }
                 }
                 if (!ok) break;
                 const int s = k % kNS;
+                const bool first = (firsts >> s & 1u) != 0;
                 if (!bar_wait(B(kPFull + s), (k / kNS) & 1) || !bar_wait(B(kVFull + s), (k / kNS) & 1)) {
                     ok = false;
                     break;
                 }
-                if (w.first && seg > 0 && !bar_wait(B(kOFree), (seg - 1) & 1)) {  // O has been read out
+                if (first && seg > 0 && !bar_wait(B(kOFree), (seg - 1) & 1)) {  // O has been read out
                     ok = false;
                     break;
                 }
-                if (w.first) ++seg;
+                if (first) ++seg;
                 fence_after();
                 const uint64_t dv = dv0 + static_cast<uint64_t>((s * kStageBytes) >> 4);
                 const uint32_t pb = tmem + static_cast<uint32_t>(s * kTok);
 #pragma unroll
                 for (int ks = 0; ks < kTok / 16; ++ks)
                     mma_bf16_ta(tmem + kOCol, pb + 8 * ks, dv + ((ks * 16 * 128) >> 4), idesc(kDim, 1),
-                                (!w.first || ks > 0) ? 1u : 0u);
+                                (!first || ks > 0) ? 1u : 0u);
                 mma_commit(B(kPvDone + s));
             }
             if (!ok) fail();
@@ -451,174 +520,163 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
         __syncwarp();
     } else {
         // ------------------------------------------------ softmax and epilogue
-        const int m = threadIdx.x;  // row of the tile = TMEM lane
-        const uint32_t lane_off = static_cast<uint32_t>(32 * warp) << 16;
-        const int gh = a.gh;
-        const int dseq = m / gh, dhead = m % gh;
+        // Warps w and w + 4 share TMEM lanes 32 (w % 4) .. + 31: row m has one
+        // thread for tokens 0-31 of a tile and output columns 0-63, another
+        // for the rest.
+        const int pair = warp & 3, hf = warp >> 2;
+        const int m = 32 * pair + lane;
+        const uint32_t lane_off = static_cast<uint32_t>(32 * pair) << 16;
+        // (written once more only after a later rendezvous of the pair)
+        float* ex = reinterpret_cast<float*>(smem + kExOff);
+        float* sums = reinterpret_cast<float*>(smem + kSumOff);
         const float qk = a.qk_scale_log2;
-        // Q rows of a unit -> shared memory; the rows of warps without one
-        // keep what they held (their scores are never read)
-        auto load_q = [&](const Walk& wq) {
-            const int nv = wq.rows(a);
-            if (32 * warp < nv) {
-                const bool valid = m < nv;
-                const uint4* src = reinterpret_cast<const uint4*>(
-                    static_cast<const __nv_bfloat16*>(a.q) +
-                    (static_cast<size_t>(wq.seq0 + (valid ? dseq : 0)) * a.num_q_heads +
-                     static_cast<size_t>(wq.head(a)) * gh + dhead) *
-                        kDim);
-#pragma unroll 4
-                for (int ch = 0; ch < 16; ++ch) {
-                    const uint4 v = valid ? __ldg(src + ch) : make_uint4(0u, 0u, 0u, 0u);
-                    *reinterpret_cast<uint4*>(smem + tile_off(m, ch, kQHalf)) = v;
-                }
+        // A wait that expires makes the warp `dead`: it goes on through the
+        // loop, without waiting or working, only to meet its partner.
+        bool dead = false;
+        auto wait = [&](int b, int phase) {
+            if (!dead && !bar_wait_warp(B(b), phase & 1)) {
+                dead = true;
+                if (lane == 0) fail();
             }
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) bar_arrive(B(kQReady));
         };
-        if (w.more()) load_q(w);
 
-        float m_used = -INFINITY, l = 0.f;
-        bool ok = true;
-        for (int k = 0; w.more(); w.next(a), ++k) {
-            const int s = k % kNS, tok0 = (w.tile0 + w.t) * kTok;
-            const bool busy = 32 * warp < w.rows(a);
-            const int visible = w.end - tok0;  // of this tile, the same for every row
-            if (w.first) {
-                m_used = -INFINITY;
-                l = 0.f;
-            }
-            if (!bar_wait_warp(B(kSFull + s), (k / kNS) & 1)) {
-                ok = false;
-                break;
-            }
-            fence_after();
-            const uint32_t sa = tmem + lane_off + static_cast<uint32_t>(s * kTok);
-            bool rescale = false;
-            float alpha = 1.f;
-            if (busy) {
-                uint32_t v[kTok];
-#pragma unroll
-                for (int c4 = 0; c4 < kTok / 32; ++c4) tmem_ld32_nowait(sa + 32 * c4, v + 32 * c4);
-                asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
-                const bool full = visible >= kTok;
-                float mx = -INFINITY;
-                if (full && qk > 0.f) {
-                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (int i = 0; i < kTok; i += 2)
-                        m4[(i >> 1) & 3] = max3(m4[(i >> 1) & 3], __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
-                    mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * qk;
-                } else {
-#pragma unroll
-                    for (int i = 0; i < kTok; ++i)
-                        if (i < visible) mx = fmaxf(mx, __uint_as_float(v[i]) * qk);
-                }
-                const float m_new = fmaxf(m_used, mx);
-                rescale = m_used != -INFINITY && m_new > m_used + 8.f;
-                const float base_new = m_used == -INFINITY || rescale ? m_new : m_used;
-                alpha = rescale ? ex2(m_used - m_new) : 1.f;
-                m_used = base_new;
-                const float base = m_used == -INFINITY ? 0.f : m_used;
-                uint32_t pk[kTok / 2];
-                float lt = 0.f;
-                if (full) {
-                    float l0 = 0.f, l1 = 0.f;
-#pragma unroll
-                    for (int i = 0; i < kTok / 2; ++i) {
-                        float x0, x1;
-                        fma2(x0, x1, __uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), qk, qk, -base, -base);
-                        const float p0 = ex2(x0), p1 = ex2(x1);
-                        add2(l0, l1, l0, l1, p0, p1);
-                        pk[i] = bf16x2(p0, p1);
-                    }
-                    lt = l0 + l1;
-                } else {
-#pragma unroll
-                    for (int i = 0; i < kTok / 2; ++i) {
-                        const float p0 = 2 * i < visible ? ex2(fmaf(__uint_as_float(v[2 * i]), qk, -base)) : 0.f;
-                        const float p1 = 2 * i + 1 < visible ? ex2(fmaf(__uint_as_float(v[2 * i + 1]), qk, -base)) : 0.f;
-                        lt += p0 + p1;
-                        pk[i] = bf16x2(p0, p1);
-                    }
-                }
-                l = l * alpha + lt;
-                tmem_st32(sa, pk);
-            }
-            // Every PV before S k has finished (MMAs complete in order) and PV
-            // k + 1 cannot finish before P k + 1 is signalled, so a parity wait
-            // for PV k - 1 or PV k is unambiguous.
-            if (busy && __any_sync(0xFFFFFFFFu, rescale)) {
-                if (!bar_wait_warp(B(kPvDone + (k - 1) % kNS), ((k - 1) / kNS) & 1)) {
-                    ok = false;
-                    break;
-                }
+        Seg sg, nx;
+        bool has = w.next(a, sg);
+        for (int k0 = 0; has;) {
+            const bool has_next = w.next(a, nx);  // (early: its loads overlap the first S)
+            const int nv = sg.rows(a);
+            const bool busy = 32 * pair < nv;
+            float m_used = -INFINITY, l = 0.f;
+            for (int t = 0; t < sg.n; ++t) {
+                const int k = k0 + t, s = k % kNS;
+                const int visible = sg.end - (sg.tile + t) * kTok;  // of this tile, the same for every row
+                wait(kSFull + s, k / kNS);
                 fence_after();
-#pragma unroll 1
-                for (int c4 = 0; c4 < 4; ++c4) {
-                    uint32_t o[32];
-                    const uint32_t oa = tmem + lane_off + kOCol + 32 * c4;
-                    tmem_ld32(oa, o);
+                const uint32_t sa = tmem + lane_off + static_cast<uint32_t>(s * kTok);
+                bool rescale = false;
+                float alpha = 1.f;
+                if (busy) {
+                    uint32_t v[32];
+                    tmem_ld32(sa + 32 * hf, v);
+                    const int seen = visible - 32 * hf;  // of this thread's 32 tokens
+                    float mx = -INFINITY;
+                    if (seen >= 32 && qk > 0.f) {
+                        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-                    tmem_st32(oa, o);
+                        for (int i = 0; i < 32; i += 2)
+                            m4[(i >> 1) & 3] = max3(m4[(i >> 1) & 3], __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+                        mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * qk;
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (i < seen) mx = fmaxf(mx, __uint_as_float(v[i]) * qk);
+                    }
+                    // Lazy base: it moves (and O and l are rescaled) only when
+                    // a row's maximum grew by more than 8; only then do the two
+                    // threads of a row exchange theirs.  The rendezvous also
+                    // keeps P off the scores that the partner has yet to read.
+                    if (pair_any(pair, m < nv && (mx > m_used + 8.f || m_used == -INFINITY))) {
+                        ex[hf * kRows + m] = mx;
+                        pair_sync(pair);
+                        const float m_new = fmaxf(m_used, fmaxf(mx, ex[(hf ^ 1) * kRows + m]));
+                        rescale = m < nv && m_used != -INFINITY && m_new > m_used + 8.f;
+                        alpha = rescale ? ex2(m_used - m_new) : 1.f;
+                        if (rescale || m_used == -INFINITY) m_used = m_new;
+                    }
+                    const float base = m_used == -INFINITY ? 0.f : m_used;
+                    uint32_t pk[16];
+                    float lt = 0.f;
+                    if (seen >= 32) {
+                        float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            float x0, x1;
+                            fma2(x0, x1, __uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), qk, qk, -base, -base);
+                            const float p0 = ex2(x0), p1 = ex2(x1);
+                            add2(l0, l1, l0, l1, p0, p1);
+                            pk[i] = bf16x2(p0, p1);
+                        }
+                        lt = l0 + l1;
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float p0 = 2 * i < seen ? ex2(fmaf(__uint_as_float(v[2 * i]), qk, -base)) : 0.f;
+                            const float p1 = 2 * i + 1 < seen ? ex2(fmaf(__uint_as_float(v[2 * i + 1]), qk, -base)) : 0.f;
+                            lt += p0 + p1;
+                            pk[i] = bf16x2(p0, p1);
+                        }
+                    }
+                    l = l * alpha + lt;
+                    tmem_st16(sa + 16 * hf, pk);
+                    // Every PV before S k has finished (MMAs complete in order) and
+                    // PV k + 1 cannot finish before P k + 1 is signalled, so a
+                    // parity wait for PV k - 1 or PV k is unambiguous.
+                    if (__any_sync(0xFFFFFFFFu, rescale)) {
+                        wait(kPvDone + (k + kNS - 1) % kNS, (k - 1) / kNS);
+                        fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < 2; ++c) {
+                            uint32_t o[32];
+                            const uint32_t oa = tmem + lane_off + kOCol + 64 * hf + 32 * c;
+                            tmem_ld32(oa, o);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                            tmem_st32(oa, o);
+                        }
+                    }
                 }
-            }
-            // V rows past the last token: zero (stale or unwritten rows could hold NaN)
-            if (visible < kTok) {
-                if (!bar_wait_warp(B(kVFull + s), (k / kNS) & 1)) {
-                    ok = false;
-                    break;
+                // V rows past the last token: zero (stale or unwritten rows could hold NaN)
+                if (visible < kTok) {
+                    wait(kVFull + s, k / kNS);
+                    uint8_t* vs = smem + kKVOff + s * kStageBytes + 2 * kHalfBytes;
+                    const int nz = kTok - visible;
+                    for (int e = threadIdx.x; e < 2 * nz * 8; e += kSoftmax) {  // whole 128-byte rows: any swizzle
+                        const int h2 = e / (nz * 8), rem = e % (nz * 8);
+                        *reinterpret_cast<uint4*>(vs + h2 * kHalfBytes + (visible + rem / 8) * 128 + (rem % 8) * 16) =
+                            make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    fence_async_smem();
                 }
-                uint8_t* vs = smem + kKVOff + s * kStageBytes + 2 * kHalfBytes;
-                const int nz = kTok - visible;
-                for (int e = m; e < 2 * nz * 8; e += 128) {  // whole 128-byte rows: the swizzle does not matter
-                    const int hf = e / (nz * 8), rem = e % (nz * 8);
-                    *reinterpret_cast<uint4*>(vs + hf * kHalfBytes + (visible + rem / 8) * 128 + (rem % 8) * 16) =
-                        make_uint4(0u, 0u, 0u, 0u);
-                }
-                fence_async_smem();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(B(kPFull + s));
             }
-            fence_before();
-            __syncwarp();
-            if (lane == 0) bar_arrive(B(kPFull + s));
-            if (!w.last()) continue;
-
-            // ---- the unit's piece ends: its last S is done, so the next Q may be stored
-            {
-                Walk wn = w;
-                wn.next(a);
-                if (wn.more()) load_q(wn);
+            // ---- the piece ends
+            const int kl = k0 + sg.n - 1;
+            if (busy) {
+                sums[hf * kRows + m] = l;
+                pair_sync(pair);
+                l += sums[(hf ^ 1) * kRows + m];
             }
-            if (!bar_wait_warp(B(kPvDone + s), (k / kNS) & 1)) {
-                ok = false;
-                break;
-            }
+            wait(kPvDone + kl % kNS, kl / kNS);
             fence_after();
             if (busy) {
-                const bool valid = m < w.rows(a);
+                const bool valid = m < nv;
                 const float inv = l > 0.f ? 1.f / l : 0.f;
-                const size_t prow = w.piece_row(a) + (valid ? m : 0);
-                float* po = (w.own ? a.own_o : a.pre_o) + prow * kDim;
-#pragma unroll 1
-                for (int c4 = 0; c4 < 4; ++c4) {
-                    uint32_t v[32];
-                    tmem_ld32(tmem + lane_off + kOCol + 32 * c4, v);
-                    if (!valid) continue;
-                    float4* dst = reinterpret_cast<float4*>(po + 32 * c4);
+                const size_t prow = sg.piece_row(a) + (valid ? m : 0);
+                float* po = (sg.own ? a.own_o : a.pre_o) + prow * kDim + 64 * hf;
+                uint32_t v[64];
+                tmem_ld32_nowait(tmem + lane_off + kOCol + 64 * hf, v);
+                tmem_ld32(tmem + lane_off + kOCol + 64 * hf + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
+                // O is read: the next segment's first PV may overwrite it
+                fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(B(kOFree));
+                if (valid) {
+                    float4* dst = reinterpret_cast<float4*>(po);
 #pragma unroll
-                    for (int q4 = 0; q4 < 8; ++q4)
+                    for (int q4 = 0; q4 < 16; ++q4)
                         dst[q4] = make_float4(__uint_as_float(v[4 * q4 + 0]) * inv, __uint_as_float(v[4 * q4 + 1]) * inv,
                                               __uint_as_float(v[4 * q4 + 2]) * inv, __uint_as_float(v[4 * q4 + 3]) * inv);
                 }
-                if (valid) (w.own ? a.own_lse : a.pre_lse)[prow] = l > 0.f ? m_used + log2f(l) : -INFINITY;
+                if (valid && hf == 0) (sg.own ? a.own_lse : a.pre_lse)[prow] = l > 0.f ? m_used + log2f(l) : -INFINITY;
+            } else if (lane == 0) {
+                bar_arrive(B(kOFree));
             }
-            fence_before();
-            __syncwarp();
-            if (lane == 0) bar_arrive(B(kOFree));
+            k0 += sg.n;
+            sg = nx;
+            has = has_next;
         }
-        if (!ok && lane == 0) fail();
     }
     fence_before();
     __syncthreads();
@@ -647,7 +705,7 @@ __global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const Prefi
         const int4 u = a.groups[g];
         const int r = (b - u.x) / a.seqs_per_tile, seq0 = u.x + r * a.seqs_per_tile;
         const int nseq = min(a.seqs_per_tile, u.y - r * a.seqs_per_tile);
-        const int T = a.totals[0], ps = a.cum_p[g] + (r * Hkv + h) * u.z;
+        const int T = a.totals[0], ps = a.cum_p[g] + (r * Hkv + h) * (u.z + kUnitCost);
         c0[0] = range_of(ps, T, a.ctas);
         n[0] = range_of(ps + u.z - 1, T, a.ctas) - c0[0] + 1;
         base[0] = static_cast<size_t>(a.gh) * (static_cast<size_t>(Hkv) * seq0 + static_cast<size_t>(h) * nseq) +
@@ -655,7 +713,7 @@ __global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const Prefi
     }
     const int nt = (L + kTok - 1) / kTok - P / kTok;
     if (nt > 0) {
-        const int T = a.totals[1], ps = a.cum_s[b] + h * nt;
+        const int T = a.totals[1], ps = a.cum_s[b] + h * (nt + kUnitCost);
         c0[1] = range_of(ps, T, a.ctas);
         n[1] = range_of(ps + nt - 1, T, a.ctas) - c0[1] + 1;
         base[1] = static_cast<size_t>(out_row);
@@ -699,7 +757,8 @@ __global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const Prefi
 
 }  // namespace
 
-cudaError_t launch_prefix_attention(const PrefixArgs& a, const void* tmap_k, const void* tmap_v, cudaStream_t stream) {
+cudaError_t launch_prefix_attention(const PrefixArgs& a, const void* tmap_k, const void* tmap_v, const void* tmap_q_group,
+                                    const void* tmap_q_own, cudaStream_t stream) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -717,7 +776,8 @@ cudaError_t launch_prefix_attention(const PrefixArgs& a, const void* tmap_k, con
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     e = launch_dependent(prefix_tc_kernel, dim3(a.ctas), dim3(kThreads), kSmem, stream,
-                         *static_cast<const CUtensorMap*>(tmap_k), *static_cast<const CUtensorMap*>(tmap_v), a);
+                         *static_cast<const CUtensorMap*>(tmap_k), *static_cast<const CUtensorMap*>(tmap_v),
+                         *static_cast<const CUtensorMap*>(tmap_q_group), *static_cast<const CUtensorMap*>(tmap_q_own), a);
     if (e != cudaSuccess) return e;
     const int64_t rows = static_cast<int64_t>(a.num_seqs) * a.num_q_heads;
     constexpr int per = kMergeThreads / 32;
