@@ -134,14 +134,12 @@ struct PrefixArgs {
     int ctas;                      // CTAs of the attention kernel
     float qk_scale_log2, v_scale;
     // workspace: the plan ...
-    int32_t* totals;               // {shared tiles, own tiles}
-    int32_t* seq_len;              // [B] clamped lengths
-    int32_t* seq_pre;              // [B] tokens read with the group
-    int32_t* seq_group;            // [B] group, or -1
-    int32_t* cum_s;                // [B] own tiles of the sequences before
-    int32_t* cum_p;                // [G] shared tiles of the groups before
+    int2* totals;                  // cost of the shared and of the own tiles
+    int2* seqs;                    // [B] {clamped length, tiles read with the group}
     int4* groups;                  // [G] {first sequence, sequences, shared tiles, table row}
-    int4* starts;                  // [2][ctas] {group or sequence, unit, tile, tiles of the range}
+    int4* starts;                  // [2][ctas] {group or sequence, unit, place in it, cost of the range}
+    int4* pieces;                  // [B][2] {start of head 0's unit, shared tiles, rows before / gh, row / gh},
+                                   //        {rows from head to head, start of head 0's own unit, own tiles, -}
     // ... and the pieces: fp32 rows of O / l and log2-sum-exp
     float *pre_o, *pre_lse;        // [B * Hq + ctas * 128]
     float *own_o, *own_lse;        // [B * Hq + ctas * gh]

@@ -27,12 +27,14 @@
 //    tiles by memory (gh rows), and the two CTAs of an SM overlap them.  Each
 //    unit's piece leaves O / l and its log2-sum-exp in the workspace.
 //  * prefix_merge_kernel, one warp per output row, merges the pieces.
-// The tile pipeline has 11 warps:
+// The tile pipeline has 12 warps:
 //  * two TMA producers, for K and for V: one box {64 columns, bs rows, 1 half}
 //    per KV block and half, 128-byte swizzled: the K-major operand layout for K
 //    and the MN-major one for V; the K producer also fetches a unit's Q rows;
-//  * one MMA thread: S = Q K^T (M 128, N 64 tokens, K 128) into one of two
-//    TMEM buffers, a tile ahead of the softmax; then O += P V (N 128, K 64);
+//  * two MMA threads: S = Q K^T (M 128, N 64 tokens, K 128) into one of two
+//    TMEM buffers, a tile ahead of the softmax, and O += P V (N 128, K 64).
+//    Their twelve instructions a tile set the pace of shared tiles; one thread
+//    for both spent as long between them, on barriers, as issuing them;
 //  * eight softmax warps, two threads per row (= TMEM lane): base 2, P back to
 //    tensor memory as BF16 pairs (at most 2^-8 of each weight; the sum l is
 //    taken in fp32 before that rounding), the running maximum moved only when
@@ -50,7 +52,9 @@ namespace {
 
 constexpr int kSoftmaxWarps = 8;
 constexpr int kSoftmax = 32 * kSoftmaxWarps;
-constexpr int kThreads = kSoftmax + 96;  // softmax warps, then K producer, MMA, V producer
+// softmax warps, then:
+constexpr int kWarpK = kSoftmaxWarps, kWarpS = kWarpK + 1, kWarpV = kWarpK + 2, kWarpPv = kWarpK + 3;
+constexpr int kThreads = kSoftmax + 128;
 constexpr int kRows = kPrefixRows;
 constexpr int kTok = 64;
 constexpr int kDim = 128;
@@ -147,54 +151,58 @@ __device__ __forceinline__ void range_start(const int* cum, int n, int total, in
     *x = g0 - cum[lo];
 }
 
+constexpr int plan_smem_bytes(int num_seqs, int num_groups) { return 24 * num_groups + 12 * num_seqs; }
+
+// Everything after the first loads happens in shared memory: a call's latency
+// is the chain of its loads.
 __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixArgs a) {
-    __shared__ int cum_s[kPrefixMaxSeqs + 1], cum_p[kPrefixMaxSeqs + 1];
+    extern __shared__ int4 plan_smem[];
     __shared__ int sums[32];
     __shared__ int bad;
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     const int B = a.num_seqs, Hkv = a.num_kv_heads, tid = threadIdx.x;
-    const int lane = tid & 31, warp = tid >> 5;
+    int4* group = plan_smem;                                  // [G] {first sequence, sequences, tiles, table row}
+    int* cum_p = reinterpret_cast<int*>(group + a.num_groups);  // [G]
+    int* pre = cum_p + a.num_groups;                          // [G] prefix lengths
+    int* len = pre + a.num_groups;                            // [B]
+    int* mine = len + B;                                      // [B] the group it reads with, or -1
+    int* cum_s = mine + B;                                    // [B]
     if (tid == 0) bad = 0;
     __syncthreads();
-    for (int g = tid; g < a.num_groups; g += kPlanThreads) {
-        const int o0 = a.group_offsets[g], o1 = a.group_offsets[g + 1];
-        if (o0 < 0 || o1 < o0 || o1 > B) bad = 1;
-    }
     for (int b = tid; b < B; b += kPlanThreads) {
         int L = a.lens[b];
         if (L < 0 || L > a.max_len) {
             if (a.err) atomicOr(a.err, PKV_ERRBIT_SEQ_LEN);
             L = L < 0 ? 0 : a.max_len;
         }
-        a.seq_len[b] = L;
-        a.seq_pre[b] = 0;
-        a.seq_group[b] = -1;
+        len[b] = L;
+        mine[b] = -1;
+    }
+    for (int g = tid; g < a.num_groups; g += kPlanThreads) {
+        const int o0 = a.group_offsets[g], o1 = a.group_offsets[g + 1], P = a.prefix_lens[g];
+        if (o0 < 0 || o1 < o0 || o1 > B) bad = 1;
+        if (P < 0 && a.err) atomicOr(a.err, PKV_ERRBIT_GROUP);
+        group[g] = make_int4(o0, o1 - o0, 0, INT_MAX);
+        pre[g] = P < 0 || P > a.max_len ? 0 : P - P % kTok;  // (no sequence is longer than max_len)
     }
     __syncthreads();
     const int G = bad ? 0 : a.num_groups;  // no sharing at all when the groups make no sense
     if (bad && tid == 0 && a.err) atomicOr(a.err, PKV_ERRBIT_GROUP);
-    // per group: its members are the sequences that hold all of its shared tiles
-    for (int g = warp; g < G; g += kPlanThreads / 32) {
-        const int o0 = a.group_offsets[g], o1 = a.group_offsets[g + 1];
-        int P = a.prefix_lens[g];
-        if (P < 0 && lane == 0 && a.err) atomicOr(a.err, PKV_ERRBIT_GROUP);
-        if (P < 0 || P > a.max_len) P = 0;  // (no sequence is that long)
-        P -= P % kTok;
-        int members = 0, leader = INT_MAX;
-        for (int b = o0 + lane; b < o1 && P > 0; b += 32)
-            if (a.seq_len[b] >= P) {
-                ++members;
-                leader = min(leader, b);
-            }
-        members = __reduce_add_sync(0xFFFFFFFFu, members);
-        leader = __reduce_min_sync(0xFFFFFFFFu, leader);
-        if (members < 2) P = 0;
-        for (int b = o0 + lane; b < o1 && P > 0; b += 32)
-            if (a.seq_len[b] >= P) {
-                a.seq_pre[b] = P;
-                a.seq_group[b] = g;
-            }
-        if (lane == 0) a.groups[g] = make_int4(o0, o1 - o0, P / kTok, P > 0 ? leader : 0);
+    // A group's members are the sequences that hold all of its shared tiles;
+    // below two there is nothing to share.
+    for (int b = tid; b < B && G > 0; b += kPlanThreads) {
+        int lo = 0, hi = G;  // the last group that starts at or before b (the empty ones before it start there too)
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (group[mid].x <= b) lo = mid;
+            else hi = mid;
+        }
+        const int4 u = group[lo];
+        if (b >= u.x && b < u.x + u.y && pre[lo] > 0 && len[b] >= pre[lo]) {
+            mine[b] = lo;
+            atomicAdd(&group[lo].z, 1);
+            atomicMin(&group[lo].w, b);
+        }
     }
     __syncthreads();
     int before = 0, total;
@@ -202,43 +210,62 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixA
         const int g = base + tid;
         int v = 0;
         if (g < G) {
-            const int4 u = a.groups[g];
-            v = u.z > 0 ? (u.y + a.seqs_per_tile - 1) / a.seqs_per_tile * Hkv * (u.z + kUnitCost) : 0;
+            int4 u = group[g];
+            const int nt = u.z >= 2 ? pre[g] / kTok : 0;
+            u.z = nt;
+            if (nt == 0) u.w = 0;
+            group[g] = u;
+            a.groups[g] = u;
+            v = nt > 0 ? (u.y + a.seqs_per_tile - 1) / a.seqs_per_tile * Hkv * (nt + kUnitCost) : 0;
         }
         const int incl = before + plan_scan(v, sums, &total);
-        if (g < G) {
-            cum_p[g] = incl - v;
-            a.cum_p[g] = incl - v;
-        }
+        if (g < G) cum_p[g] = incl - v;
         before += total;
     }
     const int T1 = before;
     before = 0;
     for (int base = 0; base < B; base += kPlanThreads) {
         const int b = base + tid;
-        const int nt = b < B ? (a.seq_len[b] + kTok - 1) / kTok - a.seq_pre[b] / kTok : 0;
+        int nt = 0, shared = 0, g = -1;
+        if (b < B) {
+            g = mine[b];
+            shared = g >= 0 ? group[g].z : 0;
+            nt = (len[b] + kTok - 1) / kTok - shared;
+            mine[b] = shared;  // (from here on: the tiles it shares)
+        }
         const int v = nt > 0 ? (nt + kUnitCost) * Hkv : 0;
         const int incl = before + plan_scan(v, sums, &total);
         if (b < B) {
             cum_s[b] = incl - v;
-            a.cum_s[b] = incl - v;
+            a.seqs[b] = make_int2(len[b], shared);
+            // what the merge needs to find the row's pieces
+            int4 p = make_int4(0, 0, 0, 0);
+            int stride = 0;
+            if (shared > 0) {
+                const int4 u = group[g];
+                const int r = (b - u.x) / a.seqs_per_tile, seq0 = u.x + r * a.seqs_per_tile;
+                stride = min(a.seqs_per_tile, u.y - r * a.seqs_per_tile) * a.gh;
+                p = make_int4(cum_p[g] + r * Hkv * (shared + kUnitCost), shared, Hkv * seq0, b - seq0);
+            }
+            a.pieces[2 * b] = p;
+            a.pieces[2 * b + 1] = make_int4(stride, incl - v, nt, 0);
         }
         before += total;
     }
     const int T2 = before;
-    if (tid == 0) {
-        a.totals[0] = T1;
-        a.totals[1] = T2;
-    }
+    if (tid == 0) *a.totals = make_int2(T1, T2);
     __syncthreads();
-    for (int c = tid; c < a.ctas; c += kPlanThreads) {
+    for (int c = tid; c < 2 * a.ctas; c += kPlanThreads) {
         int i, x, left;
-        range_start(cum_p, G, T1, a.ctas, c, &i, &x, &left);
-        const int nt = left > 0 ? a.groups[i].z + kUnitCost : 1;
-        a.starts[c] = make_int4(i, x / nt, x % nt, left);
-        range_start(cum_s, B, T2, a.ctas, c, &i, &x, &left);
-        const int ns = left > 0 ? (a.seq_len[i] + kTok - 1) / kTok - a.seq_pre[i] / kTok + kUnitCost : 1;
-        a.starts[a.ctas + c] = make_int4(i, x / ns, x % ns, left);
+        if (c < a.ctas) {
+            range_start(cum_p, G, T1, a.ctas, c, &i, &x, &left);
+            const int vt = left > 0 ? group[i].z + kUnitCost : 1;
+            a.starts[c] = make_int4(i, x / vt, x % vt, left);
+        } else {
+            range_start(cum_s, B, T2, a.ctas, c - a.ctas, &i, &x, &left);
+            const int vt = left > 0 ? (len[i] + kTok - 1) / kTok - mine[i] + kUnitCost : 1;
+            a.starts[c] = make_int4(i, x / vt, x % vt, left);
+        }
     }
 }
 
@@ -307,10 +334,10 @@ struct Walk {
         if (own) {
             units = a.num_kv_heads;
             for (;;) {
-                const int L = a.seq_len[i], P = a.seq_pre[i];
-                s.tile = P / kTok;
-                s.end = L;
-                nt = (L + kTok - 1) / kTok - s.tile;
+                const int2 q = a.seqs[i];
+                s.tile = q.y;
+                s.end = q.x;
+                nt = (q.x + kTok - 1) / kTok - q.y;
                 if (nt > 0) break;
                 ++i;
             }
@@ -353,7 +380,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kNumBars; ++i)
-            bar_init(B(i), ((i >= kPFull && i < kPFull + kNS) || i == kOFree) ? kSoftmaxWarps : 1u);
+            bar_init(B(i), ((i >= kPFull && i < kPFull + kNS) || i == kOFree) ? kSoftmaxWarps : (i == kDone ? 2u : 1u));
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
@@ -375,11 +402,11 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
     };
     Walk w;
 
-    if (warp == kSoftmaxWarps || warp == kSoftmaxWarps + 2) {
+    if (warp == kWarpK || warp == kWarpV) {
         // ------------------------------------------------ producers: K, V
         // Stage s is freed by the completion that signals score buffer s: S
         // done for K, PV done for V.
-        const bool is_v = warp == kSoftmaxWarps + 2;
+        const bool is_v = warp == kWarpV;
         const CUtensorMap* map = is_v ? &tmv : &tmk;
         const int full0 = is_v ? kVFull : kKFull, empty0 = is_v ? kPvDone : kSFull;
         const int bs = a.block_size;
@@ -443,78 +470,69 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
             for (int j = k - 1; j >= 0 && j >= k - kNS; --j)
                 if (!bar_wait(B(full0 + j % kNS), (j / kNS) & 1)) fail();
         if (lane == 0 && segs > 0 && !bar_wait(B(kQReady), (segs - 1) & 1)) fail();
-    } else if (warp == kSoftmaxWarps + 1) {
-        // ------------------------------------------------------- MMA issuer
+    } else if (warp == kWarpS) {
+        // ----------------------------------------------------- S = Q K^T
         if (lane == 0) {
             bool ok = true;
             const uint64_t dq = sdesc(sbase, 16);
             const uint64_t dk0 = sdesc(sbase + kKVOff, 16);
-            const uint64_t dv0 = sdesc(sbase + kKVOff + 2 * kHalfBytes, kHalfBytes);
-            // S of tile ns: the segment it is in has `left` tiles to go
-            Seg sg, nx;
-            int ns = 0, seg_s = 0, seg = 0;  // S issued; segments begun by the S and by the PV cursor
-            bool has = w.next(a, sg), has_next = has && w.next(a, nx);
-            int left = has ? sg.n : 0;
-            bool first_s = true;
-            uint32_t firsts = 0;  // bit k & 1: tile k begins a segment
-            for (int k = 0; (k < ns || left > 0) && ok && !*abort_flag; ++k) {
-                // S of tile k, and of k + 1 (whose scores' buffer PV k - 1, issued
-                // already, has read).  Both may block: neither the softmax of tile
-                // k nor the producers need anything further from this thread.
-                while (left > 0 && ns < k + kNS) {
-                    const int st = ns % kNS;
-                    if (first_s && !bar_wait(B(kQReady), seg_s & 1)) {
-                        ok = false;
-                        break;
-                    }
-                    if (!bar_wait(B(kKFull + st), (ns / kNS) & 1)) {
+            Seg sg;
+            int k = 0;
+            for (int seg = 0; ok && w.next(a, sg); ++seg) {
+                for (int t = 0; t < sg.n; ++t, ++k) {
+                    const int s = k % kNS;
+                    // this segment's Q, K k, and a score buffer whose P has been multiplied (PV k - 2)
+                    if (*abort_flag || (t == 0 && !bar_wait(B(kQReady), seg & 1)) ||
+                        !bar_wait(B(kKFull + s), (k / kNS) & 1) ||
+                        (k >= kNS && !bar_wait(B(kPvDone + s), (k / kNS - 1) & 1))) {
                         ok = false;
                         break;
                     }
                     fence_after();
-                    const uint64_t dk = dk0 + static_cast<uint64_t>((st * kStageBytes) >> 4);
-                    const uint32_t sb = tmem + static_cast<uint32_t>(st * kTok);
+                    const uint64_t dk = dk0 + static_cast<uint64_t>((s * kStageBytes) >> 4);
+                    const uint32_t sb = tmem + static_cast<uint32_t>(s * kTok);
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks) {
                         const uint32_t kin = (ks & 3) * 32;
                         mma_bf16(sb, dq + (((ks >> 2) * kQHalf + kin) >> 4), dk + (((ks >> 2) * kHalfBytes + kin) >> 4),
                                  idesc(kTok, 0), ks > 0 ? 1u : 0u);
                     }
-                    mma_commit(B(kSFull + st));
-                    firsts = (firsts & ~(1u << st)) | (first_s ? 1u << st : 0u);
-                    if (first_s) ++seg_s;
-                    first_s = false;
-                    ++ns;
-                    if (--left == 0 && has_next) {
-                        sg = nx;
-                        left = sg.n;
-                        first_s = true;
-                        has_next = w.next(a, nx);
-                    }
+                    mma_commit(B(kSFull + s));
                 }
-                if (!ok) break;
-                const int s = k % kNS;
-                const bool first = (firsts >> s & 1u) != 0;
-                if (!bar_wait(B(kPFull + s), (k / kNS) & 1) || !bar_wait(B(kVFull + s), (k / kNS) & 1)) {
-                    ok = false;
-                    break;
-                }
-                if (first && seg > 0 && !bar_wait(B(kOFree), (seg - 1) & 1)) {  // O has been read out
-                    ok = false;
-                    break;
-                }
-                if (first) ++seg;
-                fence_after();
-                const uint64_t dv = dv0 + static_cast<uint64_t>((s * kStageBytes) >> 4);
-                const uint32_t pb = tmem + static_cast<uint32_t>(s * kTok);
-#pragma unroll
-                for (int ks = 0; ks < kTok / 16; ++ks)
-                    mma_bf16_ta(tmem + kOCol, pb + 8 * ks, dv + ((ks * 16 * 128) >> 4), idesc(kDim, 1),
-                                (!first || ks > 0) ? 1u : 0u);
-                mma_commit(B(kPvDone + s));
             }
             if (!ok) fail();
-            mma_commit(B(kDone));  // completes once every MMA issued above has finished
+            mma_commit(B(kDone));  // completes once every MMA this thread issued has finished
+            if (!bar_wait(B(kDone), 0)) fail();
+        }
+        __syncwarp();
+    } else if (warp == kWarpPv) {
+        // ------------------------------------------------------- O += P V
+        if (lane == 0) {
+            bool ok = true;
+            const uint64_t dv0 = sdesc(sbase + kKVOff + 2 * kHalfBytes, kHalfBytes);
+            Seg sg;
+            int k = 0;
+            for (int seg = 0; ok && w.next(a, sg); ++seg) {
+                for (int t = 0; t < sg.n; ++t, ++k) {
+                    const int s = k % kNS;
+                    // V k, P k, and for a new segment an O that has been read out
+                    if (*abort_flag || !bar_wait(B(kVFull + s), (k / kNS) & 1) || !bar_wait(B(kPFull + s), (k / kNS) & 1) ||
+                        (t == 0 && seg > 0 && !bar_wait(B(kOFree), (seg - 1) & 1))) {
+                        ok = false;
+                        break;
+                    }
+                    fence_after();
+                    const uint64_t dv = dv0 + static_cast<uint64_t>((s * kStageBytes) >> 4);
+                    const uint32_t pb = tmem + static_cast<uint32_t>(s * kTok);
+#pragma unroll
+                    for (int ks = 0; ks < kTok / 16; ++ks)
+                        mma_bf16_ta(tmem + kOCol, pb + 8 * ks, dv + ((ks * 16 * 128) >> 4), idesc(kDim, 1),
+                                    (t > 0 || ks > 0) ? 1u : 0u);
+                    mma_commit(B(kPvDone + s));
+                }
+            }
+            if (!ok) fail();
+            mma_commit(B(kDone));
             if (!bar_wait(B(kDone), 0)) fail();
         }
         __syncwarp();
@@ -608,9 +626,9 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                     }
                     l = l * alpha + lt;
                     tmem_st16(sa + 16 * hf, pk);
-                    // Every PV before S k has finished (MMAs complete in order) and
-                    // PV k + 1 cannot finish before P k + 1 is signalled, so a
-                    // parity wait for PV k - 1 or PV k is unambiguous.
+                    // S k was issued after PV k - 2 had finished, and PV k + 1 cannot
+                    // finish before P k + 1 is signalled, so a parity wait for PV
+                    // k - 1, or for PV k at the end, is unambiguous.
                     if (__any_sync(0xFFFFFFFFu, rescale)) {
                         wait(kPvDone + (k + kNS - 1) % kNS, (k - 1) / kNS);
                         fence_after();
@@ -688,64 +706,72 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
 // ------------------------------------------------------------------ merge
 constexpr int kMergeThreads = 256;
 
-// One warp per output row; lane d holds columns 4 d .. 4 d + 3.
+constexpr int kMergeAhead = 8;  // pieces whose rows are loaded before their weights are known
+
+// One warp per output row; lane d holds columns 4 d .. 4 d + 3.  A row has one
+// piece per range that its two units touch.  Three dependent rounds of loads:
+// the plan, the log-sum-exps beside the first rows, the other rows.
 __global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const PrefixArgs a) {
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     const int lane = threadIdx.x & 31;
     const int64_t out_row = blockIdx.x * static_cast<int64_t>(kMergeThreads / 32) + (threadIdx.x >> 5);
     if (out_row >= static_cast<int64_t>(a.num_seqs) * a.num_q_heads) return;
     const int b = static_cast<int>(out_row / a.num_q_heads), hq = static_cast<int>(out_row % a.num_q_heads);
-    const int h = hq / a.gh, Hkv = a.num_kv_heads;
-    const int L = a.seq_len[b], P = a.seq_pre[b], g = a.seq_group[b];
-
-    // the two lists' pieces of this row: ranges c0 .. c0 + n - 1, rows base + c * step
-    int c0[2] = {0, 0}, n[2] = {0, 0};
-    size_t base[2] = {0, 0};
-    if (g >= 0) {
-        const int4 u = a.groups[g];
-        const int r = (b - u.x) / a.seqs_per_tile, seq0 = u.x + r * a.seqs_per_tile;
-        const int nseq = min(a.seqs_per_tile, u.y - r * a.seqs_per_tile);
-        const int T = a.totals[0], ps = a.cum_p[g] + (r * Hkv + h) * (u.z + kUnitCost);
-        c0[0] = range_of(ps, T, a.ctas);
-        n[0] = range_of(ps + u.z - 1, T, a.ctas) - c0[0] + 1;
-        base[0] = static_cast<size_t>(a.gh) * (static_cast<size_t>(Hkv) * seq0 + static_cast<size_t>(h) * nseq) +
-                  (b - seq0) * a.gh + hq % a.gh;
+    const int h = hq / a.gh;
+    const int4 p = a.pieces[2 * b], q = a.pieces[2 * b + 1];
+    const int2 totals = *a.totals;
+    // pieces 0 .. n0 - 1: rows pre0 + j * kRows; then n1 more: rows own0 + j * gh
+    int n0 = 0, n1 = 0;
+    size_t pre0 = 0, own0 = 0;
+    if (p.y > 0) {
+        const int ps = p.x + h * (p.y + kUnitCost), c0 = range_of(ps, totals.x, a.ctas);
+        n0 = range_of(ps + p.y - 1, totals.x, a.ctas) - c0 + 1;
+        pre0 = static_cast<size_t>(a.gh) * (p.z + p.w) + static_cast<size_t>(h) * q.x + hq % a.gh +
+               static_cast<size_t>(c0) * kRows;
     }
-    const int nt = (L + kTok - 1) / kTok - P / kTok;
-    if (nt > 0) {
-        const int T = a.totals[1], ps = a.cum_s[b] + h * (nt + kUnitCost);
-        c0[1] = range_of(ps, T, a.ctas);
-        n[1] = range_of(ps + nt - 1, T, a.ctas) - c0[1] + 1;
-        base[1] = static_cast<size_t>(out_row);
+    if (q.z > 0) {
+        const int ps = q.y + h * (q.z + kUnitCost), c0 = range_of(ps, totals.y, a.ctas);
+        n1 = range_of(ps + q.z - 1, totals.y, a.ctas) - c0 + 1;
+        own0 = static_cast<size_t>(out_row) + static_cast<size_t>(c0) * a.gh;
     }
-    const int pieces = n[0] + n[1];
+    const int pieces = n0 + n1;
     auto row_of = [&](int j) {
-        return j < n[0] ? base[0] + static_cast<size_t>(c0[0] + j) * kRows
-                        : base[1] + static_cast<size_t>(c0[1] + j - n[0]) * a.gh;
+        return j < n0 ? pre0 + static_cast<size_t>(j) * kRows : own0 + static_cast<size_t>(j - n0) * a.gh;
     };
-    auto lse_of = [&](int j) { return j < n[0] ? a.pre_lse[row_of(j)] : a.own_lse[row_of(j)]; };
-    float M = -INFINITY;
-    for (int j = lane; j < pieces; j += 32) M = fmaxf(M, lse_of(j));
+    auto lse_of = [&](int j) { return (j < n0 ? a.pre_lse : a.own_lse)[row_of(j)]; };
+    auto o_of = [&](int j) {
+        return reinterpret_cast<const float4*>((j < n0 ? a.pre_o : a.own_o) + row_of(j) * kDim)[lane];
+    };
+    float4 v[kMergeAhead];
+#pragma unroll
+    for (int j = 0; j < kMergeAhead; ++j) v[j] = j < pieces ? o_of(j) : make_float4(0.f, 0.f, 0.f, 0.f);
+    const float first = lane < pieces ? lse_of(lane) : -INFINITY;
+    float M = first;
+    for (int j = 32 + lane; j < pieces; j += 32) M = fmaxf(M, lse_of(j));
     M = warp_max(M);
     float z = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](float w, const float4& o) {
+        acc.x = fmaf(w, o.x, acc.x);
+        acc.y = fmaf(w, o.y, acc.y);
+        acc.z = fmaf(w, o.z, acc.z);
+        acc.w = fmaf(w, o.w, acc.w);
+    };
     for (int j0 = 0; j0 < pieces; j0 += 32) {
-        float wt = 0.f;
-        if (j0 + lane < pieces) {
-            const float s = lse_of(j0 + lane);
-            wt = s == -INFINITY ? 0.f : exp2f(s - M);
-        }
+        const float s = j0 == 0 ? first : (j0 + lane < pieces ? lse_of(j0 + lane) : -INFINITY);
+        const float wt = s == -INFINITY ? 0.f : exp2f(s - M);
         z += warp_sum(wt);
+        int j = 0;
+        if (j0 == 0) {
+#pragma unroll
+            for (; j < kMergeAhead; ++j) add(__shfl_sync(0xFFFFFFFFu, wt, j), v[j]);
+        }
         const int last = min(32, pieces - j0);
-#pragma unroll 4
-        for (int j = 0; j < last; ++j) {
-            const float wj = __shfl_sync(0xFFFFFFFFu, wt, j);
-            const float* o = (j0 + j < n[0] ? a.pre_o : a.own_o) + row_of(j0 + j) * kDim;
-            const float4 v = reinterpret_cast<const float4*>(o)[lane];
-            acc.x = fmaf(wj, v.x, acc.x);
-            acc.y = fmaf(wj, v.y, acc.y);
-            acc.z = fmaf(wj, v.z, acc.z);
-            acc.w = fmaf(wj, v.w, acc.w);
+        for (; j < last; j += kMergeAhead) {
+#pragma unroll
+            for (int e = 0; e < kMergeAhead; ++e) v[e] = j + e < last ? o_of(j0 + j + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int e = 0; e < kMergeAhead; ++e) add(__shfl_sync(0xFFFFFFFFu, wt, (j + e) & 31), v[e]);
         }
     }
     const float inv = z > 0.f ? a.v_scale / z : 0.f;  // no token: a zero row
@@ -769,10 +795,13 @@ cudaError_t launch_prefix_attention(const PrefixArgs& a, const void* tmap_k, con
         if (e == cudaSuccess)
             e = cudaFuncSetAttribute(prefix_tc_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
                                      cudaSharedmemCarveoutMaxShared);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(prefix_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     plan_smem_bytes(kPrefixMaxSeqs, kPrefixMaxSeqs));
         if (e != cudaSuccess) return e;
         configured |= 1ull << dev;
     }
-    prefix_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a);
+    prefix_plan_kernel<<<1, kPlanThreads, plan_smem_bytes(a.num_seqs, a.num_groups), stream>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     e = launch_dependent(prefix_tc_kernel, dim3(a.ctas), dim3(kThreads), kSmem, stream,
