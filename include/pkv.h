@@ -324,7 +324,7 @@ int32_t paged_decode_algo(const pkv_pool* pool, int32_t group, pkv_algo requeste
  *                 group.  PKV_ALGO_TC: the sharing design or
  *                 PKV_ERR_UNSUPPORTED.  PKV_ALGO_MMA, PKV_ALGO_SIMT: those.
  *                 The sharing design serves BF16 pools of head_dim 128, up to
- *                 4096 sequences and groups, up to 128 query heads per KV head.
+ *                 4096 sequences, 512 groups and 128 query heads per KV head.
  *   workspace     at least paged_prefix_decode_plan's bytes, 256-byte aligned,
  *                 zeroed before its first call; stream-ordered calls may share
  *                 it, also with paged_decode_attention calls of as many

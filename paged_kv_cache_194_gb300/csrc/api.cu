@@ -586,10 +586,10 @@ namespace {
 
 bool prefix_tc_fits(const pkv_pool* p, int num_seqs, int num_groups, int gh, int max_seq_len) {
     if (!attention_tc_supported(p->d.kv_dtype, p->d.head_dim, p->d.block_size)) return false;
-    if (num_seqs > kPrefixMaxSeqs || num_groups > kPrefixMaxSeqs || gh > kPrefixRows) return false;
+    if (num_seqs > kPrefixMaxSeqs || num_groups > kPrefixMaxGroups || gh > kPrefixRows) return false;
     // tile counts are int32
     const int64_t tiles = (static_cast<int64_t>(max_seq_len) + kTileTokens - 1) / kTileTokens;
-    return (tiles + 8) * num_seqs * p->d.num_kv_heads <= INT32_MAX / 2;
+    return (tiles + 8) * num_seqs * p->d.num_kv_heads <= INT32_MAX / 4;
 }
 
 // Workspace of the sharing design behind the decode counters (which it leaves
@@ -607,11 +607,10 @@ size_t prefix_layout(const pkv_pool* p, int num_seqs, int num_groups, int num_q_
     const size_t row = static_cast<size_t>(p->d.head_dim) * sizeof(float);
     PrefixArgs x{};
     x.ctas = ctas;
-    x.totals = reinterpret_cast<int2*>(take(sizeof(int2)));
+    x.totals = reinterpret_cast<int32_t*>(take(sizeof(int32_t)));
     x.seqs = reinterpret_cast<int2*>(take(B * sizeof(int2)));
     x.pieces = reinterpret_cast<int4*>(take(2 * B * sizeof(int4)));
     x.groups = reinterpret_cast<int4*>(take(G * sizeof(int4)));
-    x.starts = reinterpret_cast<int4*>(take(2 * static_cast<size_t>(ctas) * sizeof(int4)));
     x.pre_o = reinterpret_cast<float*>(take(pre * row));
     x.pre_lse = reinterpret_cast<float*>(take(pre * sizeof(float)));
     x.own_o = reinterpret_cast<float*>(take(own * row));

@@ -117,7 +117,8 @@ bool attention_tc_supported(pkv_dtype kv, int head_dim, int block_size);
 cudaError_t launch_attention_tc(const DecodeArgs& a, const void* tmap_k, const void* tmap_v, cudaStream_t stream);
 
 // ------------------------------------------------- decode over shared prefixes
-constexpr int kPrefixMaxSeqs = 4096;  // sequences (and groups) the plan kernel keeps on chip
+constexpr int kPrefixMaxSeqs = 4096;   // sequences and groups that a CTA plans in its shared memory
+constexpr int kPrefixMaxGroups = 512;
 constexpr int kPrefixRows = 128;      // query rows of one tile
 
 struct PrefixArgs {
@@ -134,10 +135,9 @@ struct PrefixArgs {
     int ctas;                      // CTAs of the attention kernel
     float qk_scale_log2, v_scale;
     // workspace: the plan ...
-    int2* totals;                  // cost of the shared and of the own tiles
+    int32_t* totals;               // cost of the whole list
     int2* seqs;                    // [B] {clamped length, tiles read with the group}
     int4* groups;                  // [G] {first sequence, sequences, shared tiles, table row}
-    int4* starts;                  // [2][ctas] {group or sequence, unit, place in it, cost of the range}
     int4* pieces;                  // [B][2] {start of head 0's unit, shared tiles, rows before / gh, row / gh},
                                    //        {rows from head to head, start of head 0's own unit, own tiles, -}
     // ... and the pieces: fp32 rows of O / l and log2-sum-exp

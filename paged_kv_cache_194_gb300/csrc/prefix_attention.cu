@@ -14,18 +14,13 @@
 // read once instead of n times.  With 64 sequences over a 32768-token prefix
 // that is 0.27 GB instead of 8.7 GB, and 35 GFLOP that the tensor cores take.
 //
-// Three launches.
-//  * prefix_plan_kernel, one CTA: per group the shared tiles (64 tokens; a
-//    remainder of the prefix counts as own tokens), prefix sums of the tiles
-//    over groups and over sequences, and for every CTA of the next kernel its
-//    range of each list.
-//  * prefix_tc_kernel, 2 persistent CTAs per SM.  The units are the 128-row
-//    query tiles of a (group, KV head), over the group's shared tiles, and
-//    the (sequence, KV head) pairs, over the sequence's own tiles.  Every CTA
-//    takes an equal share of both lists, odd CTAs the own tiles first: shared
-//    tiles are bound by the tensor cores and the softmax (128 rows), own
-//    tiles by memory (gh rows), and the two CTAs of an SM overlap them.  Each
-//    unit's piece leaves O / l and its log2-sum-exp in the workspace.
+// Two launches.
+//  * prefix_tc_kernel, 2 persistent CTAs per SM.  Its units are the 128-row
+//    query tiles of a (group, KV head), over the group's shared tiles (64
+//    tokens; a remainder of the prefix counts as own tokens), then the
+//    (sequence, KV head) pairs, over the sequence's own tiles.  Every CTA plans
+//    the call and takes an equal share of that list; each unit's piece leaves
+//    O / l and its log2-sum-exp in the workspace.
 //  * prefix_merge_kernel, one warp per output row, merges the pieces.
 // The tile pipeline has 12 warps:
 //  * two TMA producers, for K and for V: one box {64 columns, bs rows, 1 half}
@@ -64,6 +59,7 @@ constexpr int kHalfBytes = kTok * 128;        // one 64-column half of a K or V 
 constexpr int kKVOff = 2 * kQHalf;
 constexpr int kStageBytes = 4 * kHalfBytes;   // K + V
 constexpr int kAlignSlack = 1024;
+static_assert(12 * kPrefixMaxSeqs + 24 * kPrefixMaxGroups <= kNS * kStageBytes, "the plan fits into the ring");
 constexpr uint32_t kTmemCols = 256;
 constexpr uint32_t kOCol = kNS * kTok;
 
@@ -74,8 +70,6 @@ constexpr int kExOff = kBarOff + (8 * kNumBars + 8 + 63) / 64 * 64;  // the two 
 constexpr int kSumOff = kExOff + 2 * kRows * 4;                        // and sums, [2][kRows] floats each
 constexpr int kSmem = kSumOff + 2 * kRows * 4 + kAlignSlack;
 static_assert(kSmem <= 115712, "two CTAs per SM");
-
-constexpr int kPlanThreads = 1024;
 
 // 16 consecutive TMEM columns of this thread's lane.
 __device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t (&v)[16]) {
@@ -100,7 +94,29 @@ __device__ __forceinline__ bool pair_any(int id, bool yes) {
 __device__ __forceinline__ void pair_sync(int id) { asm volatile("barrier.cta.sync %0, 64;\n" ::"r"(1 + id) : "memory"); }
 
 // ------------------------------------------------------------------- plan
-__device__ __forceinline__ int plan_scan(int v, int* warp_sums, int* total) {  // inclusive, over the CTA
+// Cost, in tiles, that a unit has beside its tiles: its Q rows to fetch, its
+// piece to write out and the pipeline to refill.  The list is cut by cost,
+// every unit being nt + kUnitCost long; the last kUnitCost of them hold no tile.
+constexpr int kUnitCost = 2;
+
+// A list of cost T is cut into min(T, ctas) ranges, none of them empty: range
+// r is [r T / n, (r + 1) T / n).
+__device__ __forceinline__ int num_ranges(int T, int ctas) { return T < ctas ? T : ctas; }
+__device__ __forceinline__ int range_of(int x, int T, int ctas) {  // the range that x is in
+    return static_cast<int>(((x + 1LL) * num_ranges(T, ctas) - 1) / T);
+}
+// The range of this CTA.  The list begins with the shared tiles, which the
+// tensor cores and the softmax bound, and ends with the own ones, which memory
+// does: the two CTAs of an SM (c and c + ctas / 2, as blocks are handed out)
+// get one of each, as far as there are.
+__device__ __forceinline__ int my_range(int ctas) {
+    const int c = static_cast<int>(blockIdx.x), half = ctas / 2;
+    return c < half ? c : ctas - 1 - (c - half);
+}
+
+// Inclusive sum over the CTA; *total gets the sum of all.
+__device__ __forceinline__ int plan_scan(int v, int* warp_sums, int* total) {
+    constexpr int kWarps = kThreads / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -109,88 +125,71 @@ __device__ __forceinline__ int plan_scan(int v, int* warp_sums, int* total) {  /
     }
     if (lane == 31) warp_sums[warp] = v;
     __syncthreads();
-    const int mine = warp_sums[lane];
-    int s = mine;
+    int before = 0, sum = 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xFFFFFFFFu, s, o);
-        if (lane >= o) s += x;
+    for (int w = 0; w < kWarps; ++w) {
+        const int x = warp_sums[w];
+        if (w < warp) before += x;
+        sum += x;
     }
-    *total = __shfl_sync(0xFFFFFFFFu, s, 31);
-    const int before = __shfl_sync(0xFFFFFFFFu, s - mine, warp);
-    __syncthreads();
+    *total = sum;
+    __syncthreads();  // warp_sums may be written again
     return v + before;
 }
 
-// Cost, in tiles, that a unit has beside its tiles: its Q rows to fetch, its
-// piece to write out and the pipeline to refill.  A list is cut by cost, every
-// unit being nt + kUnitCost long; the last kUnitCost of them hold no tile.
-constexpr int kUnitCost = 2;
-
-// A list of T cost units is cut into min(T, ctas) ranges, none of them empty:
-// range c is [c T / n, (c + 1) T / n).
-__device__ __forceinline__ int num_ranges(int T, int ctas) { return T < ctas ? T : ctas; }
-__device__ __forceinline__ int range_of(int x, int T, int ctas) {  // the range that x is in
-    return static_cast<int>(((x + 1LL) * num_ranges(T, ctas) - 1) / T);
-}
-// Start of range c: group or sequence i (cum[i] <= start < cum[i + 1]), place x
-// within it, length of the range (0 from range n on).
-__device__ __forceinline__ void range_start(const int* cum, int n, int total, int ctas, int c, int* i, int* x, int* left) {
-    const long long T = total, ranges = num_ranges(total, ctas);
-    *i = *x = *left = 0;
-    if (c >= ranges) return;
-    const int g0 = static_cast<int>(c * T / ranges), g1 = static_cast<int>((c + 1) * T / ranges);
-    *left = g1 - g0;
+__device__ __forceinline__ int last_at_or_before(const int* cum, int n, int x) {  // cum[0] <= x; empty entries skipped
     int lo = 0, hi = n;
-    while (hi - lo > 1) {  // the last i with cum[i] <= g0 (the empty ones before it share its start)
+    while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (cum[mid] <= g0) lo = mid;
+        if (cum[mid] <= x) lo = mid;
         else hi = mid;
     }
-    *i = lo;
-    *x = g0 - cum[lo];
+    return lo;
 }
 
-constexpr int plan_smem_bytes(int num_seqs, int num_groups) { return 24 * num_groups + 12 * num_seqs; }
+struct Start {
+    int own, i, u, t, left;  // of this CTA's range: list half, group or sequence, unit, place in the unit, cost
+};
 
-// Everything after the first loads happens in shared memory: a call's latency
-// is the chain of its loads.
-__global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixArgs a) {
-    extern __shared__ int4 plan_smem[];
-    __shared__ int sums[32];
+// Every CTA plans the whole call in its own shared memory (the ring's, before
+// the first copy): a launch less, and the latency is one round of loads plus
+// the sums.  It writes the units it will walk over to the workspace, and CTA 0
+// what the merge needs.
+__device__ void make_plan(const PrefixArgs& a, uint8_t* scratch, Start* start) {
+    __shared__ int sums[kThreads / 32];
     __shared__ int bad;
-    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     const int B = a.num_seqs, Hkv = a.num_kv_heads, tid = threadIdx.x;
-    int4* group = plan_smem;                                  // [G] {first sequence, sequences, tiles, table row}
+    const bool report = blockIdx.x == 0;
+    int4* group = reinterpret_cast<int4*>(scratch);             // [G] {first sequence, sequences, tiles, table row}
     int* cum_p = reinterpret_cast<int*>(group + a.num_groups);  // [G]
-    int* pre = cum_p + a.num_groups;                          // [G] prefix lengths
-    int* len = pre + a.num_groups;                            // [B]
-    int* mine = len + B;                                      // [B] the group it reads with, or -1
-    int* cum_s = mine + B;                                    // [B]
+    int* pre = cum_p + a.num_groups;                            // [G] prefix lengths
+    int* len = pre + a.num_groups;                              // [B]
+    int* mine = len + B;                                        // [B] the group it reads with, or -1
+    int* cum_s = mine + B;                                      // [B]
     if (tid == 0) bad = 0;
     __syncthreads();
-    for (int b = tid; b < B; b += kPlanThreads) {
+    for (int b = tid; b < B; b += kThreads) {
         int L = a.lens[b];
         if (L < 0 || L > a.max_len) {
-            if (a.err) atomicOr(a.err, PKV_ERRBIT_SEQ_LEN);
+            if (report && a.err) atomicOr(a.err, PKV_ERRBIT_SEQ_LEN);
             L = L < 0 ? 0 : a.max_len;
         }
         len[b] = L;
         mine[b] = -1;
     }
-    for (int g = tid; g < a.num_groups; g += kPlanThreads) {
+    for (int g = tid; g < a.num_groups; g += kThreads) {
         const int o0 = a.group_offsets[g], o1 = a.group_offsets[g + 1], P = a.prefix_lens[g];
         if (o0 < 0 || o1 < o0 || o1 > B) bad = 1;
-        if (P < 0 && a.err) atomicOr(a.err, PKV_ERRBIT_GROUP);
+        if (P < 0 && report && a.err) atomicOr(a.err, PKV_ERRBIT_GROUP);
         group[g] = make_int4(o0, o1 - o0, 0, INT_MAX);
         pre[g] = P < 0 || P > a.max_len ? 0 : P - P % kTok;  // (no sequence is longer than max_len)
     }
     __syncthreads();
     const int G = bad ? 0 : a.num_groups;  // no sharing at all when the groups make no sense
-    if (bad && tid == 0 && a.err) atomicOr(a.err, PKV_ERRBIT_GROUP);
+    if (bad && tid == 0 && report && a.err) atomicOr(a.err, PKV_ERRBIT_GROUP);
     // A group's members are the sequences that hold all of its shared tiles;
     // below two there is nothing to share.
-    for (int b = tid; b < B && G > 0; b += kPlanThreads) {
+    for (int b = tid; b < B && G > 0; b += kThreads) {
         int lo = 0, hi = G;  // the last group that starts at or before b (the empty ones before it start there too)
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
@@ -205,26 +204,23 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixA
         }
     }
     __syncthreads();
-    int before = 0, total;
-    for (int base = 0; base < G; base += kPlanThreads) {
+    int T = 0, total;
+    for (int base = 0; base < G; base += kThreads) {
         const int g = base + tid;
         int v = 0;
         if (g < G) {
             int4 u = group[g];
-            const int nt = u.z >= 2 ? pre[g] / kTok : 0;
-            u.z = nt;
-            if (nt == 0) u.w = 0;
+            u.z = u.z >= 2 ? pre[g] / kTok : 0;
+            if (u.z == 0) u.w = 0;
             group[g] = u;
-            a.groups[g] = u;
-            v = nt > 0 ? (u.y + a.seqs_per_tile - 1) / a.seqs_per_tile * Hkv * (nt + kUnitCost) : 0;
+            v = u.z > 0 ? (u.y + a.seqs_per_tile - 1) / a.seqs_per_tile * Hkv * (u.z + kUnitCost) : 0;
         }
-        const int incl = before + plan_scan(v, sums, &total);
+        const int incl = T + plan_scan(v, sums, &total);
         if (g < G) cum_p[g] = incl - v;
-        before += total;
+        T += total;
     }
-    const int T1 = before;
-    before = 0;
-    for (int base = 0; base < B; base += kPlanThreads) {
+    const int T1 = T;  // cost of the shared tiles
+    for (int base = 0; base < B; base += kThreads) {
         const int b = base + tid;
         int nt = 0, shared = 0, g = -1;
         if (b < B) {
@@ -234,39 +230,48 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixA
             mine[b] = shared;  // (from here on: the tiles it shares)
         }
         const int v = nt > 0 ? (nt + kUnitCost) * Hkv : 0;
-        const int incl = before + plan_scan(v, sums, &total);
+        const int incl = T + plan_scan(v, sums, &total);
         if (b < B) {
             cum_s[b] = incl - v;
-            a.seqs[b] = make_int2(len[b], shared);
-            // what the merge needs to find the row's pieces
-            int4 p = make_int4(0, 0, 0, 0);
-            int stride = 0;
-            if (shared > 0) {
-                const int4 u = group[g];
-                const int r = (b - u.x) / a.seqs_per_tile, seq0 = u.x + r * a.seqs_per_tile;
-                stride = min(a.seqs_per_tile, u.y - r * a.seqs_per_tile) * a.gh;
-                p = make_int4(cum_p[g] + r * Hkv * (shared + kUnitCost), shared, Hkv * seq0, b - seq0);
+            if (report) {  // where the merge finds the pieces of this sequence's rows
+                int4 p = make_int4(0, 0, 0, 0);
+                int stride = 0;
+                if (shared > 0) {
+                    const int4 u = group[g];
+                    const int r = (b - u.x) / a.seqs_per_tile, seq0 = u.x + r * a.seqs_per_tile;
+                    stride = min(a.seqs_per_tile, u.y - r * a.seqs_per_tile) * a.gh;
+                    p = make_int4(cum_p[g] + r * Hkv * (shared + kUnitCost), shared, Hkv * seq0, b - seq0);
+                }
+                a.pieces[2 * b] = p;
+                a.pieces[2 * b + 1] = make_int4(stride, incl - v, nt, 0);
             }
-            a.pieces[2 * b] = p;
-            a.pieces[2 * b + 1] = make_int4(stride, incl - v, nt, 0);
         }
-        before += total;
+        T += total;
     }
-    const int T2 = before;
-    if (tid == 0) *a.totals = make_int2(T1, T2);
+    if (report && tid == 0) *a.totals = T;
     __syncthreads();
-    for (int c = tid; c < 2 * a.ctas; c += kPlanThreads) {
-        int i, x, left;
-        if (c < a.ctas) {
-            range_start(cum_p, G, T1, a.ctas, c, &i, &x, &left);
-            const int vt = left > 0 ? group[i].z + kUnitCost : 1;
-            a.starts[c] = make_int4(i, x / vt, x % vt, left);
-        } else {
-            range_start(cum_s, B, T2, a.ctas, c - a.ctas, &i, &x, &left);
-            const int vt = left > 0 ? (len[i] + kTok - 1) / kTok - mine[i] + kUnitCost : 1;
-            a.starts[c] = make_int4(i, x / vt, x % vt, left);
-        }
+    const int ranges = num_ranges(T, a.ctas), r = my_range(a.ctas);
+    Start st{0, 0, 0, 0, 0};
+    if (r < ranges) {
+        const int g0 = static_cast<int>(static_cast<long long>(r) * T / ranges);
+        const int g1 = static_cast<int>((r + 1LL) * T / ranges);
+        st.left = g1 - g0;
+        st.own = g0 >= T1;
+        st.i = st.own ? last_at_or_before(cum_s, B, g0) : last_at_or_before(cum_p, G, g0);
+        const int x = g0 - (st.own ? cum_s[st.i] : cum_p[st.i]);
+        const int vt = (st.own ? (len[st.i] + kTok - 1) / kTok - mine[st.i] : group[st.i].z) + kUnitCost;
+        st.u = x / vt;
+        st.t = x % vt;
+        for (int b = tid; b < B; b += kThreads)
+            if (cum_s[b] < g1 && (b + 1 < B ? cum_s[b + 1] : T) > g0) a.seqs[b] = make_int2(len[b], mine[b]);
+        for (int g = tid; g < G; g += kThreads)
+            if (cum_p[g] < g1 && (g + 1 < G ? cum_p[g + 1] : T1) > g0) a.groups[g] = group[g];
     }
+    // the units' data, for every thread of this CTA; and no generic access to
+    // the ring behind the copies that follow
+    fence_async_smem();
+    __syncthreads();
+    *start = st;
 }
 
 // ------------------------------------------------------------------- walk
@@ -291,78 +296,67 @@ struct Seg {
     }
 };
 
-// The segments of this CTA, in order: its range of one list, then of the
-// other.  CTA c has range c of the shared tiles and the c-th range from the end
-// of the own tiles, so that short lists fall to different CTAs.
+// The segments of this CTA's range, in order.
 struct Walk {
-    int phase = -1, left = 0;  // cost left of the range
-    int i = 0, u = 0, t = 0;   // group or sequence; KV head, or row tile * KV heads + KV head; place in the unit
+    Start at;
+    int range;
 
     __device__ bool next(const PrefixArgs& a, Seg& s) {
-        for (;;) {
-            int own = phase ^ static_cast<int>(blockIdx.x & 1);
-            while (left == 0) {
-                if (phase == 1) return false;
-                ++phase;
-                own = phase ^ static_cast<int>(blockIdx.x & 1);
-                s.range = own ? a.ctas - 1 - static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x);
-                const int4 st = a.starts[own * a.ctas + s.range];
-                i = st.x, u = st.y, t = st.z, left = st.w;
-            }
-            s.own = own;
-            s.range = own ? a.ctas - 1 - static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x);
+        while (at.left > 0) {
             const int nt = unit(a, s);
-            const int t0 = t, cost = min(left, nt + kUnitCost - t0);
-            left -= cost;
-            t = 0;
-            if (++u == units) {
-                u = 0;
-                ++i;
+            const int t0 = at.t, cost = min(at.left, nt + kUnitCost - t0);
+            at.left -= cost;
+            at.t = 0;
+            if (++at.u == units) {
+                at.u = 0;
+                ++at.i;
             }
             s.n = min(cost, nt - t0);
             s.tile += t0;
+            s.range = range;
             if (s.n > 0) return true;  // (else only the end of a unit's cost fell into the range)
         }
+        return false;
     }
 
   private:
     int units = 0;
     // The unit at (i, u), or of the next i with tiles: everything but the range of tiles.  Returns its tiles.
     __device__ int unit(const PrefixArgs& a, Seg& s) {
-        const int own = s.own;
-        int nt;
-        if (own) {
-            units = a.num_kv_heads;
-            for (;;) {
-                const int2 q = a.seqs[i];
-                s.tile = q.y;
-                s.end = q.x;
-                nt = (q.x + kTok - 1) / kTok - q.y;
-                if (nt > 0) break;
-                ++i;
+        while (!at.own) {
+            if (at.i == a.num_groups) {  // on to the own tiles
+                at.own = 1;
+                at.i = 0;
+                break;
             }
-            s.row = s.seq0 = i;
-            s.nseq = 1;
-            s.head = u;
-        } else {
-            for (;;) {
-                const int4 g = a.groups[i];
-                nt = g.z;
+            const int4 g = a.groups[at.i];
+            if (g.z > 0) {
+                const int r = at.u / a.num_kv_heads;
                 units = (g.y + a.seqs_per_tile - 1) / a.seqs_per_tile * a.num_kv_heads;
-                if (nt > 0 && units > 0) {
-                    const int r = u / a.num_kv_heads;
-                    s.row = g.w;
-                    s.head = u - r * a.num_kv_heads;
-                    s.seq0 = g.x + r * a.seqs_per_tile;
-                    s.nseq = min(a.seqs_per_tile, g.y - r * a.seqs_per_tile);
-                    break;
-                }
-                ++i;
+                s.own = 0;
+                s.row = g.w;
+                s.head = at.u - r * a.num_kv_heads;
+                s.seq0 = g.x + r * a.seqs_per_tile;
+                s.nseq = min(a.seqs_per_tile, g.y - r * a.seqs_per_tile);
+                s.tile = 0;
+                s.end = g.z * kTok;
+                return g.z;
             }
-            s.tile = 0;
-            s.end = nt * kTok;
+            ++at.i;
         }
-        return nt;
+        for (;; ++at.i) {
+            const int2 q = a.seqs[at.i];
+            const int nt = (q.x + kTok - 1) / kTok - q.y;
+            if (nt <= 0) continue;
+            units = a.num_kv_heads;
+            s.own = 1;
+            s.row = s.seq0 = at.i;
+            s.nseq = 1;
+            s.head = at.u;
+            s.tile = q.y;
+            s.end = q.x;
+            return nt;
+        }
     }
 };
 
@@ -394,13 +388,14 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
     __syncthreads();
     fence_after();
     const uint32_t tmem = *tmem_slot;
-    asm volatile("griddepcontrol.wait;\n" ::: "memory");  // the plan, and everything before it
-    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     auto fail = [&]() {
         *abort_flag = 1;
         if (a.err) atomicOr(a.err, PKV_ERRBIT_TIMEOUT);
     };
     Walk w;
+    w.range = my_range(a.ctas);
+    make_plan(a, smem + kKVOff, &w.at);
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
 
     if (warp == kWarpK || warp == kWarpV) {
         // ------------------------------------------------ producers: K, V
@@ -719,19 +714,19 @@ __global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const Prefi
     const int b = static_cast<int>(out_row / a.num_q_heads), hq = static_cast<int>(out_row % a.num_q_heads);
     const int h = hq / a.gh;
     const int4 p = a.pieces[2 * b], q = a.pieces[2 * b + 1];
-    const int2 totals = *a.totals;
+    const int T = *a.totals;
     // pieces 0 .. n0 - 1: rows pre0 + j * kRows; then n1 more: rows own0 + j * gh
     int n0 = 0, n1 = 0;
     size_t pre0 = 0, own0 = 0;
     if (p.y > 0) {
-        const int ps = p.x + h * (p.y + kUnitCost), c0 = range_of(ps, totals.x, a.ctas);
-        n0 = range_of(ps + p.y - 1, totals.x, a.ctas) - c0 + 1;
+        const int ps = p.x + h * (p.y + kUnitCost), c0 = range_of(ps, T, a.ctas);
+        n0 = range_of(ps + p.y - 1, T, a.ctas) - c0 + 1;
         pre0 = static_cast<size_t>(a.gh) * (p.z + p.w) + static_cast<size_t>(h) * q.x + hq % a.gh +
                static_cast<size_t>(c0) * kRows;
     }
     if (q.z > 0) {
-        const int ps = q.y + h * (q.z + kUnitCost), c0 = range_of(ps, totals.y, a.ctas);
-        n1 = range_of(ps + q.z - 1, totals.y, a.ctas) - c0 + 1;
+        const int ps = q.y + h * (q.z + kUnitCost), c0 = range_of(ps, T, a.ctas);
+        n1 = range_of(ps + q.z - 1, T, a.ctas) - c0 + 1;
         own0 = static_cast<size_t>(out_row) + static_cast<size_t>(c0) * a.gh;
     }
     const int pieces = n0 + n1;
@@ -795,18 +790,13 @@ cudaError_t launch_prefix_attention(const PrefixArgs& a, const void* tmap_k, con
         if (e == cudaSuccess)
             e = cudaFuncSetAttribute(prefix_tc_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
                                      cudaSharedmemCarveoutMaxShared);
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(prefix_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     plan_smem_bytes(kPrefixMaxSeqs, kPrefixMaxSeqs));
         if (e != cudaSuccess) return e;
         configured |= 1ull << dev;
     }
-    prefix_plan_kernel<<<1, kPlanThreads, plan_smem_bytes(a.num_seqs, a.num_groups), stream>>>(a);
+    prefix_tc_kernel<<<a.ctas, kThreads, kSmem, stream>>>(
+        *static_cast<const CUtensorMap*>(tmap_k), *static_cast<const CUtensorMap*>(tmap_v),
+        *static_cast<const CUtensorMap*>(tmap_q_group), *static_cast<const CUtensorMap*>(tmap_q_own), a);
     e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    e = launch_dependent(prefix_tc_kernel, dim3(a.ctas), dim3(kThreads), kSmem, stream,
-                         *static_cast<const CUtensorMap*>(tmap_k), *static_cast<const CUtensorMap*>(tmap_v),
-                         *static_cast<const CUtensorMap*>(tmap_q_group), *static_cast<const CUtensorMap*>(tmap_q_own), a);
     if (e != cudaSuccess) return e;
     const int64_t rows = static_cast<int64_t>(a.num_seqs) * a.num_q_heads;
     constexpr int per = kMergeThreads / 32;

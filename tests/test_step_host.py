@@ -57,7 +57,7 @@ def test_prefix_attention_refusals(pool):
     assert call(h=pool(kv_dtype=0), dt=0, algo=3) == 2
     assert call(h=pool(head_dim=64), algo=3) == 2
     assert pk.lib().paged_prefix_decode_algo(h, 4097, 1, 8, 64, 3) == -1
-    assert pk.lib().paged_prefix_decode_algo(h, 2, 4097, 8, 64, 3) == -1
+    assert pk.lib().paged_prefix_decode_algo(h, 2, 513, 8, 64, 3) == -1
     assert pk.lib().paged_prefix_decode_algo(h, 2, 1, 2 * 129, 64, 3) == -1
     assert pk.lib().paged_prefix_decode_algo(h, 4096, 1, 8, 2 ** 31 - 1, 3) == -1
     assert pk.lib().paged_prefix_decode_algo(None, 2, 1, 8, 64, 0) == -1
