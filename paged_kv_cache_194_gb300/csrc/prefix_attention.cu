@@ -68,7 +68,11 @@ enum Bar { kQReady, kOFree, kDone, kSFull, kPFull = kSFull + kNS, kPvDone = kPFu
 constexpr int kBarOff = kKVOff + kNS * kStageBytes;
 constexpr int kExOff = kBarOff + (8 * kNumBars + 8 + 63) / 64 * 64;  // the two threads of a row meet here: maxima
 constexpr int kSumOff = kExOff + 2 * kRows * 4;                        // and sums, [2][kRows] floats each
-constexpr int kSmem = kSumOff + 2 * kRows * 4 + kAlignSlack;
+// The units of this CTA's range, as far as they fit (else the workspace's copy).
+constexpr int kSeqCache = 1024, kGroupCache = 128;
+constexpr int kGroupOff = kSumOff + 2 * kRows * 4;
+constexpr int kSeqOff = kGroupOff + 16 * kGroupCache;
+constexpr int kSmem = kSeqOff + 8 * kSeqCache + kAlignSlack;
 static_assert(kSmem <= 115712, "two CTAs per SM");
 
 // 16 consecutive TMEM columns of this thread's lane.
@@ -79,6 +83,19 @@ __device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t (&v)[16]) {
         "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
     asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
+}
+// 64 TMEM columns of 16 lanes: thread 4 r + c gets columns 8 j + 2 c, + 1 of
+// lane r in v[4 j], v[4 j + 1] and of lane r + 8 in v[4 j + 2], v[4 j + 3].
+__device__ __forceinline__ void tmem_ld_16x64(uint32_t a, uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+          "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+          "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(a));
+    asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
 }
 // Rendezvous of the two warps that share 32 rows (named barrier 1 + id), and
 // with it: does any of their threads say yes?
@@ -149,13 +166,14 @@ __device__ __forceinline__ int last_at_or_before(const int* cum, int n, int x) {
 
 struct Start {
     int own, i, u, t, left;  // of this CTA's range: list half, group or sequence, unit, place in the unit, cost
+    int seq0, group0;        // the caches' first entries
 };
 
 // Every CTA plans the whole call in its own shared memory (the ring's, before
 // the first copy): a launch less, and the latency is one round of loads plus
-// the sums.  It writes the units it will walk over to the workspace, and CTA 0
-// what the merge needs.
-__device__ void make_plan(const PrefixArgs& a, uint8_t* scratch, Start* start) {
+// the sums.  It keeps the units it will walk over (those that its caches cannot
+// hold in the workspace), and CTA 0 writes what the merge needs.
+__device__ void make_plan(const PrefixArgs& a, uint8_t* scratch, int2* seq_cache, int4* group_cache, Start* start) {
     __shared__ int sums[kThreads / 32];
     __shared__ int bad;
     const int B = a.num_seqs, Hkv = a.num_kv_heads, tid = threadIdx.x;
@@ -166,10 +184,18 @@ __device__ void make_plan(const PrefixArgs& a, uint8_t* scratch, Start* start) {
     int* len = pre + a.num_groups;                              // [B]
     int* mine = len + B;                                        // [B] the group it reads with, or -1
     int* cum_s = mine + B;                                      // [B]
+    // the first rounds' loads, all under way at once
+    const int L0 = tid < B ? a.lens[tid] : 0;
+    int first0 = 0, end0 = 0, pre0 = 0;
+    if (tid < a.num_groups) {
+        first0 = a.group_offsets[tid];
+        end0 = a.group_offsets[tid + 1];
+        pre0 = a.prefix_lens[tid];
+    }
     if (tid == 0) bad = 0;
     __syncthreads();
     for (int b = tid; b < B; b += kThreads) {
-        int L = a.lens[b];
+        int L = b == tid ? L0 : a.lens[b];
         if (L < 0 || L > a.max_len) {
             if (report && a.err) atomicOr(a.err, PKV_ERRBIT_SEQ_LEN);
             L = L < 0 ? 0 : a.max_len;
@@ -178,7 +204,9 @@ __device__ void make_plan(const PrefixArgs& a, uint8_t* scratch, Start* start) {
         mine[b] = -1;
     }
     for (int g = tid; g < a.num_groups; g += kThreads) {
-        const int o0 = a.group_offsets[g], o1 = a.group_offsets[g + 1], P = a.prefix_lens[g];
+        const bool r0 = g == tid;
+        const int o0 = r0 ? first0 : a.group_offsets[g], o1 = r0 ? end0 : a.group_offsets[g + 1];
+        const int P = r0 ? pre0 : a.prefix_lens[g];
         if (o0 < 0 || o1 < o0 || o1 > B) bad = 1;
         if (P < 0 && report && a.err) atomicOr(a.err, PKV_ERRBIT_GROUP);
         group[g] = make_int4(o0, o1 - o0, 0, INT_MAX);
@@ -251,7 +279,7 @@ __device__ void make_plan(const PrefixArgs& a, uint8_t* scratch, Start* start) {
     if (report && tid == 0) *a.totals = T;
     __syncthreads();
     const int ranges = num_ranges(T, a.ctas), r = my_range(a.ctas);
-    Start st{0, 0, 0, 0, 0};
+    Start st{0, 0, 0, 0, 0, 0, 0};
     if (r < ranges) {
         const int g0 = static_cast<int>(static_cast<long long>(r) * T / ranges);
         const int g1 = static_cast<int>((r + 1LL) * T / ranges);
@@ -262,10 +290,19 @@ __device__ void make_plan(const PrefixArgs& a, uint8_t* scratch, Start* start) {
         const int vt = (st.own ? (len[st.i] + kTok - 1) / kTok - mine[st.i] : group[st.i].z) + kUnitCost;
         st.u = x / vt;
         st.t = x % vt;
-        for (int b = tid; b < B; b += kThreads)
-            if (cum_s[b] < g1 && (b + 1 < B ? cum_s[b + 1] : T) > g0) a.seqs[b] = make_int2(len[b], mine[b]);
-        for (int g = tid; g < G; g += kThreads)
-            if (cum_p[g] < g1 && (g + 1 < G ? cum_p[g + 1] : T1) > g0) a.groups[g] = group[g];
+        st.seq0 = st.own ? st.i : 0;
+        st.group0 = st.own ? 0 : st.i;
+        for (int b = st.seq0 + tid; b < B; b += kThreads)
+            if (cum_s[b] < g1 && (b + 1 < B ? cum_s[b + 1] : T) > g0) {
+                const int2 q = make_int2(len[b], mine[b]);
+                if (b - st.seq0 < kSeqCache) seq_cache[b - st.seq0] = q;
+                else a.seqs[b] = q;
+            }
+        for (int g = st.group0 + tid; g < G; g += kThreads)
+            if (cum_p[g] < g1 && (g + 1 < G ? cum_p[g + 1] : T1) > g0) {
+                if (g - st.group0 < kGroupCache) group_cache[g - st.group0] = group[g];
+                else a.groups[g] = group[g];
+            }
     }
     // the units' data, for every thread of this CTA; and no generic access to
     // the ring behind the copies that follow
@@ -300,6 +337,8 @@ struct Seg {
 struct Walk {
     Start at;
     int range;
+    const int2* seq_cache;
+    const int4* group_cache;
 
     __device__ bool next(const PrefixArgs& a, Seg& s) {
         while (at.left > 0) {
@@ -329,7 +368,7 @@ struct Walk {
                 at.i = 0;
                 break;
             }
-            const int4 g = a.groups[at.i];
+            const int4 g = at.i - at.group0 < kGroupCache ? group_cache[at.i - at.group0] : a.groups[at.i];
             if (g.z > 0) {
                 const int r = at.u / a.num_kv_heads;
                 units = (g.y + a.seqs_per_tile - 1) / a.seqs_per_tile * a.num_kv_heads;
@@ -345,7 +384,7 @@ struct Walk {
             ++at.i;
         }
         for (;; ++at.i) {
-            const int2 q = a.seqs[at.i];
+            const int2 q = at.i - at.seq0 < kSeqCache ? seq_cache[at.i - at.seq0] : a.seqs[at.i];
             const int nt = (q.x + kTok - 1) / kTok - q.y;
             if (nt <= 0) continue;
             units = a.num_kv_heads;
@@ -394,7 +433,9 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
     };
     Walk w;
     w.range = my_range(a.ctas);
-    make_plan(a, smem + kKVOff, &w.at);
+    w.seq_cache = reinterpret_cast<const int2*>(smem + kSeqOff);
+    w.group_cache = reinterpret_cast<const int4*>(smem + kGroupOff);
+    make_plan(a, smem + kKVOff, reinterpret_cast<int2*>(smem + kSeqOff), reinterpret_cast<int4*>(smem + kGroupOff), &w.at);
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
 
     if (warp == kWarpK || warp == kWarpV) {
@@ -573,7 +614,12 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                     tmem_ld32(sa + 32 * hf, v);
                     const int seen = visible - 32 * hf;  // of this thread's 32 tokens
                     float mx = -INFINITY;
-                    if (seen >= 32 && qk > 0.f) {
+                    if (qk > 0.f) {
+                        if (seen < 32) {  // what lies behind the last token: no weight, on the path below
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (i >= seen) v[i] = 0xFF800000u;
+                        }
                         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                         for (int i = 0; i < 32; i += 2)
@@ -599,7 +645,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                     const float base = m_used == -INFINITY ? 0.f : m_used;
                     uint32_t pk[16];
                     float lt = 0.f;
-                    if (seen >= 32) {
+                    if (seen >= 32 || qk > 0.f) {
                         float l0 = 0.f, l1 = 0.f;
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
@@ -664,25 +710,34 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
             wait(kPvDone + kl % kNS, kl / kNS);
             fence_after();
             if (busy) {
-                const bool valid = m < nv;
                 const float inv = l > 0.f ? 1.f / l : 0.f;
-                const size_t prow = sg.piece_row(a) + (valid ? m : 0);
-                float* po = (sg.own ? a.own_o : a.pre_o) + prow * kDim + 64 * hf;
-                uint32_t v[64];
-                tmem_ld32_nowait(tmem + lane_off + kOCol + 64 * hf, v);
-                tmem_ld32(tmem + lane_off + kOCol + 64 * hf + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
-                // O is read: the next segment's first PV may overwrite it
-                fence_before();
-                __syncwarp();
-                if (lane == 0) bar_arrive(B(kOFree));
-                if (valid) {
-                    float4* dst = reinterpret_cast<float4*>(po);
+                const size_t row0 = sg.piece_row(a) + 32 * pair;
+                float* po = (sg.own ? a.own_o : a.pre_o) + row0 * kDim + 64 * hf + 2 * (lane & 3);
+                // Rows in quarters of the warp: eight rows by 32 bytes a store,
+                // whole sectors (a row per thread wrote half ones, 32 lines a store).
 #pragma unroll
-                    for (int q4 = 0; q4 < 16; ++q4)
-                        dst[q4] = make_float4(__uint_as_float(v[4 * q4 + 0]) * inv, __uint_as_float(v[4 * q4 + 1]) * inv,
-                                              __uint_as_float(v[4 * q4 + 2]) * inv, __uint_as_float(v[4 * q4 + 3]) * inv);
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t v[32];
+                    tmem_ld_16x64(tmem + lane_off + (static_cast<uint32_t>(16 * c) << 16) + kOCol + 64 * hf, v);
+                    if (c == 1) {  // O is read: the next segment's first PV may overwrite it
+                        fence_before();
+                        __syncwarp();
+                        if (lane == 0) bar_arrive(B(kOFree));
+                    }
+#pragma unroll
+                    for (int up = 0; up < 2; ++up) {
+                        const int r = 16 * c + 8 * up + (lane >> 2);
+                        const float f = __shfl_sync(0xFFFFFFFFu, inv, r);
+                        if (32 * pair + r < nv) {
+                            float* dst = po + r * kDim;
+#pragma unroll
+                            for (int q = 0; q < 8; ++q)
+                                *reinterpret_cast<float2*>(dst + 8 * q) =
+                                    make_float2(__uint_as_float(v[4 * q + 2 * up]) * f, __uint_as_float(v[4 * q + 2 * up + 1]) * f);
+                        }
+                    }
                 }
-                if (valid && hf == 0) (sg.own ? a.own_lse : a.pre_lse)[prow] = l > 0.f ? m_used + log2f(l) : -INFINITY;
+                if (m < nv && hf == 0) (sg.own ? a.own_lse : a.pre_lse)[row0 + lane] = l > 0.f ? m_used + log2f(l) : -INFINITY;
             } else if (lane == 0) {
                 bar_arrive(B(kOFree));
             }
