@@ -165,10 +165,10 @@ struct NormRopeArgs {
     int max_pos, rotary_dim, interleaved, num_axes;
     int axis_end[2];                            // pairs of the first, and of the first two axes
     float k_inv_scale, v_inv_scale;
-    int tokens_per_cta;                         // set by the launcher
     int32_t* err;
 };
-cudaError_t launch_norm_rope_append(pkv_dtype pool, pkv_dtype in, int head_dim, NormRopeArgs a, cudaStream_t stream);
+cudaError_t launch_norm_rope_append(pkv_dtype pool, pkv_dtype in, int head_dim, const NormRopeArgs& a,
+                                    cudaStream_t stream);
 
 // ----------------------------------------------------- tables and slots of a step
 struct GrowArgs {
