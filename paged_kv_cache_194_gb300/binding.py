@@ -395,13 +395,18 @@ def _refuse(name: str, t: torch.Tensor, dev: torch.device, dtype, shape):
 
 def _ptr_on(dev: torch.device, name: str, t: torch.Tensor, dtype, shape) -> int:
     """Data pointer of a contiguous tensor of this device, dtype and shape (None: any)."""
-    if (t.device != dev or (dtype is not None and t.dtype != dtype) or (shape is not None and t.shape != shape)
-            or not t.is_contiguous()):
-        _refuse(name, t, dev, dtype, shape)
-    return t.data_ptr()
+    if (t.is_contiguous() and t.device == dev and (dtype is None or t.dtype is dtype)
+            and (shape is None or t.shape == shape)):
+        return t.data_ptr()
+    _refuse(name, t, dev, dtype, shape)
 
 
 _HERE = contextlib.nullcontext()
+# The current device, and (device index) -> handle of its current stream, without
+# the objects and checks of the public calls, which take longer than some of the
+# kernels below.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
 def _device_of(pool: KVPool, stream):
@@ -412,13 +417,13 @@ def _device_of(pool: KVPool, stream):
         if stream.device != dev:
             raise ValueError("stream must be on %s, the pool's device, not %s" % (dev, stream.device))
         return torch.cuda.stream(stream)
-    if dev.type != "cuda" or dev.index == torch.cuda.current_device():
+    if dev.type != "cuda" or dev.index == _current_device():
         return _HERE
     return torch.cuda.device(dev)
 
 
 def _stream_of(pool: KVPool, stream) -> int:
-    return (torch.cuda.current_stream(pool.k.device) if stream is None else stream).cuda_stream
+    return _raw_stream(pool.k.device.index) if stream is None else stream.cuda_stream
 
 
 def _table_width(block_tables: torch.Tensor, num_seqs: int) -> int:

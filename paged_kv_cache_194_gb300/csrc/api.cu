@@ -646,6 +646,8 @@ int prefix_design(const pkv_pool* p, int num_seqs, int num_groups, int num_q_hea
     return design_for(p, 1, gh, 0, algo, false);
 }
 
+int block_shift(const pkv_pool* p) { return p->d.block_size == 16 ? 4 : (p->d.block_size == 32 ? 5 : 6); }
+
 bool ranges_overlap(const void* a, size_t na, const void* b, size_t nb) {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
     return x < y + nb && y < x + na;
@@ -797,7 +799,7 @@ pkv_status kv_append_norm_rope(const pkv_pool* p, int32_t layer, const void* q, 
     a.num_q_heads = num_q_heads;
     a.num_kv_heads = p->d.num_kv_heads;
     a.num_slots = static_cast<int64_t>(p->d.num_blocks) * p->d.block_size;
-    a.block_shift = p->d.block_size == 16 ? 4 : (p->d.block_size == 32 ? 5 : 6);
+    a.block_shift = block_shift(p);
     a.max_pos = r->max_pos;
     a.rotary_dim = r->rotary_dim;
     a.interleaved = r->interleaved;
@@ -838,7 +840,7 @@ pkv_status kv_tables_grow(const pkv_pool* p, int32_t* block_tables, int32_t max_
     a.ring_size = ring_size;
     a.num_seqs = num_seqs;
     a.max_blocks = max_blocks_per_seq;
-    a.block_size = p->d.block_size;
+    a.block_shift = block_shift(p);
     a.num_blocks = p->d.num_blocks;
     a.max_tokens = max_tokens;
     a.slots = slot_mapping;
@@ -875,7 +877,7 @@ pkv_status kv_tables_release(const pkv_pool* p, const int32_t* block_tables, int
     a.ring_size = ring_size;
     a.num_seqs = num_seqs;
     a.max_blocks = max_blocks_per_seq;
-    a.block_size = p->d.block_size;
+    a.block_shift = block_shift(p);
     a.num_blocks = p->d.num_blocks;
     a.lens_out = seq_lens_out;
     a.free_out = free_state_out;

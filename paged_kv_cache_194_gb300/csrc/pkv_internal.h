@@ -177,7 +177,7 @@ struct GrowArgs {
     int32_t* tables;                            // [B][max_blocks]
     const int32_t* ring;                        // free blocks: entries head .. head + count - 1, wrapping
     const int32_t* free_state;                  // {head, count}
-    int ring_size, num_seqs, max_blocks, block_size, num_blocks, max_tokens;
+    int ring_size, num_seqs, max_blocks, block_shift, num_blocks, max_tokens;  // block_shift: log2(block_size)
     int64_t* slots;                             // [max_tokens]
     int32_t *positions, *token_seqs;            // [max_tokens]
     int32_t* token_offsets;                     // [B + 1]
@@ -194,7 +194,7 @@ struct ReleaseArgs {
     const int32_t* tables;
     int32_t* ring;
     const int32_t* free_state;
-    int ring_size, num_seqs, max_blocks, block_size, num_blocks;
+    int ring_size, num_seqs, max_blocks, block_shift, num_blocks;
     int32_t* lens_out;
     int32_t* free_out;
     int32_t* err;

@@ -20,7 +20,8 @@
 // that scans 1024 requests a round (registers and shuffles, two barriers per
 // sum), writes tables and, for up to kInlineTokens token rows, the slots too;
 // a second kernel, launched to start as the first ends, fills longer slot
-// maps, one thread per token row.
+// maps, one thread per token row.  (Block sizes are powers of two; with runtime
+// divisions instead of shifts the scan took four times as long.)
 #include "device_common.cuh"
 
 namespace pkv {
@@ -56,7 +57,8 @@ __device__ __forceinline__ long long block_scan(long long v, long long* warp_sum
     return v + before;
 }
 
-__device__ __forceinline__ long long div_up(long long a, int b) { return (a + b - 1) / b; }
+// Block sizes are powers of two: blocks that `a` tokens occupy.
+__device__ __forceinline__ long long blocks_of(long long a, int shift) { return (a + (1LL << shift) - 1) >> shift; }
 __device__ __forceinline__ int sat_pos(long long p) { return p > INT32_MAX ? INT32_MAX : static_cast<int>(p); }
 
 struct FreeRing {
@@ -85,7 +87,7 @@ __device__ __forceinline__ int checked_block(int blk, int num_blocks, int32_t* e
 
 __device__ __forceinline__ void grow_entry(const GrowArgs& a, const FreeRing& f, const Job& j, int i) {
     const int blk = checked_block(f.ring[f.index(j.first + static_cast<long long>(i))], a.num_blocks, a.err);
-    a.tables[static_cast<size_t>(j.b) * a.max_blocks + div_up(j.L, a.block_size) + i] = blk;
+    a.tables[static_cast<size_t>(j.b) * a.max_blocks + blocks_of(j.L, a.block_shift) + i] = blk;
 }
 
 __device__ __forceinline__ void grow_row(const GrowArgs& a, const FreeRing& f, const Job& j, int i) {
@@ -94,12 +96,12 @@ __device__ __forceinline__ void grow_row(const GrowArgs& a, const FreeRing& f, c
     const long long p = static_cast<long long>(j.L > 0 ? j.L : 0) + i;
     long long slot = -1;
     if (j.served) {
-        const int held = static_cast<int>(div_up(j.L, a.block_size)), col = static_cast<int>(p / a.block_size);
+        const int held = static_cast<int>(blocks_of(j.L, a.block_shift)), col = static_cast<int>(p >> a.block_shift);
         // the last block held may have room; the others come from the free list
         const int blk = col < held ? a.tables[static_cast<size_t>(j.b) * a.max_blocks + col]
                                    : f.ring[f.index(j.first + static_cast<long long>(col - held))];
         if (checked_block(blk, a.num_blocks, a.err) >= 0)
-            slot = static_cast<long long>(blk) * a.block_size + p % a.block_size;
+            slot = (static_cast<long long>(blk) << a.block_shift) + (p & ((1LL << a.block_shift) - 1));
     }
     a.slots[row] = slot;
     a.positions[row] = sat_pos(p);
@@ -112,7 +114,8 @@ __device__ __forceinline__ void grow_row(const GrowArgs& a, const FreeRing& f, c
 __global__ void __launch_bounds__(kThreads, 1) grow_kernel(const GrowArgs a, const int fill_rows) {
     __shared__ long long sums[kWarps];
     __shared__ Job jobs[kThreads];
-    __shared__ int num_jobs, taken;
+    __shared__ int num_jobs, num_wide, taken;
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     FreeRing f{a.ring, a.ring_size, a.free_state[0]};
     int count = a.free_state[1];
     const bool bad_state = f.head < 0 || f.head >= f.cap || count < 0 || count > f.cap;
@@ -123,12 +126,12 @@ __global__ void __launch_bounds__(kThreads, 1) grow_kernel(const GrowArgs a, con
     if (bad_state) count = 0;
     const int head0 = f.head, count0 = a.free_state[1];
     if (bad_state) f.head = 0;
-    const long long room = static_cast<long long>(a.max_blocks) * a.block_size;
+    const long long room = static_cast<long long>(a.max_blocks) << a.block_shift;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
 
     long long rows_before = 0, need_before = 0;
     for (int base = 0; base < a.num_seqs; base += blockDim.x) {
-        if (threadIdx.x == 0) num_jobs = 0;
+        if (threadIdx.x == 0) num_jobs = num_wide = 0;
         const int b = base + threadIdx.x;
         const bool in = b < a.num_seqs;
         const int L = in ? a.lens[b] : 0, n = in ? a.new_tokens[b] : 0;
@@ -141,7 +144,8 @@ __global__ void __launch_bounds__(kThreads, 1) grow_kernel(const GrowArgs a, con
         // Requests past max_tokens still count in the sum of needs: all
         // later ones with new tokens are past it too, so it changes nothing.
         const bool fits = in && len_ok && n >= 0 && static_cast<long long>(L) + n <= room;
-        const long long need = fits ? div_up(static_cast<long long>(L) + n, a.block_size) - div_up(L, a.block_size) : 0;
+        const long long need =
+            fits ? blocks_of(static_cast<long long>(L) + n, a.block_shift) - blocks_of(L, a.block_shift) : 0;
         const long long incl = need_before + block_scan(need, sums, &total);
         need_before += total;
         if (in && a.err && (!len_ok || !rows_ok)) atomicOr(a.err, (len_ok ? 0 : PKV_ERRBIT_SEQ_LEN) | (rows_ok ? 0 : PKV_ERRBIT_STEP));
@@ -158,16 +162,14 @@ __global__ void __launch_bounds__(kThreads, 1) grow_kernel(const GrowArgs a, con
                 if (fill_rows)
                     for (int i = 0; i < j.n; ++i) grow_row(a, f, j, i);
             } else {
-                jobs[atomicAdd(&num_jobs, 1)] = j;
+                // narrow ones from the front of the list, wide ones from its end
+                const bool wide = j.need > kThreads || (fill_rows && j.n > kThreads);
+                jobs[wide ? kThreads - 1 - atomicAdd(&num_wide, 1) : atomicAdd(&num_jobs, 1)] = j;
             }
         }
         __syncthreads();
         // one warp per remaining request; very long ones by the whole CTA
-        for (int i = 0; i < num_jobs; ++i) {
-            const Job& j = jobs[i];
-            const bool wide = j.need > kThreads || (fill_rows && j.n > kThreads);
-            if (!wide && i % warps != warp) continue;
-            const int k0 = wide ? static_cast<int>(threadIdx.x) : lane, step = wide ? static_cast<int>(blockDim.x) : 32;
+        auto serve = [&](const Job& j, int k0, int step) {
 #pragma unroll 4
             for (int k = k0; k < j.need; k += step) grow_entry(a, f, j, k);
             if (fill_rows) {
@@ -175,7 +177,9 @@ __global__ void __launch_bounds__(kThreads, 1) grow_kernel(const GrowArgs a, con
 #pragma unroll 4
                 for (int k = k0; k < last; k += step) grow_row(a, f, j, k);
             }
-        }
+        };
+        for (int i = warp; i < num_jobs; i += warps) serve(jobs[i], lane, 32);
+        for (int i = 0; i < num_wide; ++i) serve(jobs[kThreads - 1 - i], threadIdx.x, blockDim.x);
         __syncthreads();
     }
     const int end = static_cast<int>(rows_before < a.max_tokens ? rows_before : a.max_tokens);
@@ -192,165 +196,180 @@ __global__ void __launch_bounds__(kThreads, 1) grow_kernel(const GrowArgs a, con
         }
 }
 
-// Slots of long steps: one thread per token row finds its request by binary
-// search over the row offsets (L1-resident, and the same path for the rows of
-// a warp) and its block in the table.
+// Slots of long steps, one thread per token row.  A warp's 32 rows mostly
+// belong to one request: the warp finds the first row's by a 32-way search over
+// the row offsets (two rounds of loads for a thousand requests), and only rows
+// behind that request's last search on.
 __global__ void __launch_bounds__(kFillThreads) fill_kernel(const GrowArgs a) {
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
-    const long long row = blockIdx.x * static_cast<long long>(kFillThreads) + threadIdx.x;
-    if (row >= a.max_tokens) return;
+    const int lane = threadIdx.x & 31;
+    const long long row = blockIdx.x * static_cast<long long>(kFillThreads) + threadIdx.x, row0 = row - lane;
+    if (row0 >= a.max_tokens) return;  // (the whole warp)
+    const int end = a.token_offsets[a.num_seqs];
     long long slot = -1;
     int pos = 0, seq = -1;
-    if (row < a.token_offsets[a.num_seqs]) {
-        int lo = 0, hi = a.num_seqs;  // the last request whose first row is <= row
+    if (row0 < end) {
+        int lo = 0, hi = a.num_seqs;  // the last request whose first row is <= row0
         while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (a.token_offsets[mid] <= row) lo = mid;
-            else hi = mid;
+            const int step = (hi - lo + 31) >> 5, at = lo + lane * step;
+            const unsigned below = __ballot_sync(0xFFFFFFFFu, at < hi && a.token_offsets[at] <= row0);
+            lo += (31 - __clz(below)) * step;  // (lane 0 always is)
+            hi = min(hi, lo + step);
         }
-        seq = lo;
-        const int n = a.granted[seq];
-        const int L = a.lens_out[seq] - n;  // the length before the step
-        const long long p = static_cast<long long>(L > 0 ? L : 0) + (row - a.token_offsets[seq]);
-        pos = sat_pos(p);
-        if (n > 0) {
-            const int blk = checked_block(a.tables[static_cast<size_t>(seq) * a.max_blocks + p / a.block_size],
-                                          a.num_blocks, a.err);
-            if (blk >= 0) slot = static_cast<long long>(blk) * a.block_size + p % a.block_size;
+        if (row < end) {
+            if (a.token_offsets[lo + 1] <= row)
+                for (hi = a.num_seqs; hi - lo > 1;) {
+                    const int mid = (lo + hi) >> 1;
+                    if (a.token_offsets[mid] <= row) lo = mid;
+                    else hi = mid;
+                }
+            seq = lo;
+            const int n = a.granted[seq];
+            const int L = a.lens_out[seq] - n;  // the length before the step
+            const long long p = static_cast<long long>(L > 0 ? L : 0) + (row - a.token_offsets[seq]);
+            pos = sat_pos(p);
+            if (n > 0) {
+                const int blk = checked_block(
+                    a.tables[static_cast<size_t>(seq) * a.max_blocks + (p >> a.block_shift)], a.num_blocks, a.err);
+                if (blk >= 0) slot = (static_cast<long long>(blk) << a.block_shift) + (p & ((1LL << a.block_shift) - 1));
+            }
         }
     }
+    if (row >= a.max_tokens) return;
     a.slots[row] = slot;
     a.positions[row] = pos;
     a.token_seqs[row] = seq;
 }
 
 // ---------------------------------------------------------------- release
-constexpr int kReleasePerCta = kWarps;     // requests of one CTA of the large form: one per warp
+constexpr int kReleasePerCta = kWarps;        // requests of one CTA of the large form: one per warp
 constexpr long long kSmallEntries = 1 << 18;  // table entries up to which one CTA does it all
 
-// Blocks request b gives back: entries [first, first + count) of its row.
-__device__ __forceinline__ void released(const ReleaseArgs& a, int b, bool report, int* first, int* count) {
-    *first = *count = 0;
-    if (a.finished[b] == 0) return;
-    const int L = a.lens[b];
-    if (L < 0 || L > static_cast<long long>(a.max_blocks) * a.block_size) {
+// Blocks request b gives back: entries [*first, *first + *count) of its row.
+// *len: its length; *gone: whether it is released (if the ring has room).
+struct Given {
+    int len, first, count;
+    bool gone;
+};
+__device__ __forceinline__ Given given(const ReleaseArgs& a, int b, bool report) {
+    // (unconditional loads: one round to L2)
+    const int done = a.finished[b], L = a.lens[b], keep0 = a.keep_blocks ? a.keep_blocks[b] : 0;
+    Given g{L, 0, 0, false};
+    if (done == 0) return g;
+    if (L < 0 || L > static_cast<long long>(a.max_blocks) << a.block_shift) {
         if (report && a.err) atomicOr(a.err, PKV_ERRBIT_SEQ_LEN);
-        return;
+        return g;
     }
-    const int held = static_cast<int>(div_up(L, a.block_size));
-    int keep = a.keep_blocks ? a.keep_blocks[b] : 0;
-    keep = keep < 0 ? 0 : (keep > held ? held : keep);
-    *first = keep;
-    *count = held - keep;
+    const int held = static_cast<int>(blocks_of(L, a.block_shift));
+    g.first = keep0 < 0 ? 0 : (keep0 > held ? held : keep0);
+    g.count = held - g.first;
+    g.gone = true;
+    return g;
 }
 
-__device__ __forceinline__ void release_copy(const ReleaseArgs& a, const FreeRing& f, long long tail, int b, int first,
-                                             int count, int k0, int step) {
+// Entries k0, k0 + step, .. of what request b gives back, behind the ring's
+// `tail` entries.
+__device__ __forceinline__ void release_copy(const ReleaseArgs& a, int head, long long tail, int b, int first, int count,
+                                             int k0, int step) {
     const int32_t* src = a.tables + static_cast<size_t>(b) * a.max_blocks + first;
 #pragma unroll 4
     for (int k = k0; k < count; k += step) {
-        long long at = f.head + tail + k;  // < 2 * cap + cap
-        if (at >= f.cap) at -= f.cap;
-        if (at >= f.cap) at -= f.cap;
+        long long at = head + tail + k;  // < 2 * ring_size
+        if (at >= a.ring_size) at -= a.ring_size;
         a.ring[at] = checked_block(src[k], a.num_blocks, a.err);
     }
 }
 
-__device__ __forceinline__ bool ring_ok(const ReleaseArgs& a, int head, int count) {
-    return head >= 0 && head < a.ring_size && count >= 0 && count <= a.ring_size;
+__device__ __forceinline__ bool ring_ok(const ReleaseArgs& a, int head, int count, long long total) {
+    return head >= 0 && head < a.ring_size && count >= 0 && count + total <= a.ring_size;
+}
+__device__ __forceinline__ void put_state(const ReleaseArgs& a, int head, int count, long long total, bool ok) {
+    a.free_out[0] = head;
+    a.free_out[1] = ok ? static_cast<int>(count + total) : count;
+    if (!ok && a.err) atomicOr(a.err, PKV_ERRBIT_STEP);
 }
 
-// Lengths and the free list's state after the release (one CTA).
-__device__ __forceinline__ void release_commit(const ReleaseArgs& a, int head, int count, long long total, bool ok) {
-    for (int b = threadIdx.x; b < a.num_seqs; b += blockDim.x) {
-        const int L = a.lens[b];
-        const bool gone = ok && a.finished[b] != 0 && L >= 0 && L <= static_cast<long long>(a.max_blocks) * a.block_size;
-        a.lens_out[b] = gone ? 0 : L;
-    }
-    if (threadIdx.x == 0) {
-        a.free_out[0] = head;
-        a.free_out[1] = ok ? static_cast<int>(count + total) : count;
-        if (!ok && a.err) atomicOr(a.err, PKV_ERRBIT_STEP);
-    }
+// Up to kThreads requests in one CTA: a thread each, then the blocks of those
+// that have any by a warp each.  The outputs may be the inputs.
+__global__ void __launch_bounds__(kThreads, 1) release_small_kernel(const ReleaseArgs a) {
+    __shared__ long long sums[kWarps];
+    struct Run {
+        int b, first, count, tail;
+    };
+    __shared__ Run runs[kThreads];
+    __shared__ int num_runs;
+    const int head = a.free_state[0], count = a.free_state[1], b = threadIdx.x;
+    Given g{0, 0, 0, false};
+    if (b < a.num_seqs) g = given(a, b, true);
+    if (b == 0) num_runs = 0;
+    long long total;
+    const long long incl = block_scan(g.count, sums, &total);
+    const bool ok = ring_ok(a, head, count, total);
+    if (ok && g.count > 0) runs[atomicAdd(&num_runs, 1)] = Run{b, g.first, g.count, static_cast<int>(count + incl - g.count)};
+    if (b < a.num_seqs) a.lens_out[b] = ok && g.gone ? 0 : g.len;
+    if (b == 0) put_state(a, head, count, total, ok);
+    __syncthreads();
+    for (int i = b >> 5; i < num_runs; i += static_cast<int>(blockDim.x >> 5))
+        release_copy(a, head, runs[i].tail, runs[i].b, runs[i].first, runs[i].count, b & 31, 32);
 }
 
-// One pass over the batch: the blocks released by requests before `upto`
+// One pass over the batch: the blocks given back by requests before `upto`
 // (*before) and by all of them (*total), for every thread of the CTA.
 __device__ __forceinline__ void release_sums(const ReleaseArgs& a, int upto, long long* sums, long long* before,
                                              long long* total) {
     long long s0 = 0, s1 = 0;
+#pragma unroll 4
     for (int b = threadIdx.x; b < a.num_seqs; b += blockDim.x) {
-        int first, count;
-        released(a, b, false, &first, &count);
-        s1 += count;
-        if (b < upto) s0 += count;
+        const int n = given(a, b, false).count;
+        s1 += n;
+        if (b < upto) s0 += n;
     }
     block_scan(s0, sums, before);
     block_scan(s1, sums, total);
 }
 
-__global__ void __launch_bounds__(kThreads) release_small_kernel(const ReleaseArgs a) {
+// Larger batches: every CTA sums the whole batch (some tens of KB from L2) and
+// moves the blocks of its own 32 requests, a warp each.  Outputs apart from the
+// inputs are written here (commit); others by a second kernel, once every CTA
+// has read them.
+__global__ void __launch_bounds__(kThreads, 1) release_copy_kernel(const ReleaseArgs a, const int commit) {
     __shared__ long long sums[kWarps];
-    __shared__ long long tails[kThreads];
-    const int head = a.free_state[0], count = a.free_state[1];
-    long long zero, total;
-    release_sums(a, 0, sums, &zero, &total);
-    const bool ok = ring_ok(a, head, count) && count + total <= a.ring_size;
-    const FreeRing f{a.ring, a.ring_size, head};
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    long long tail = count;
-    for (int base = 0; base < a.num_seqs && ok; base += kThreads) {
-        const int b = base + threadIdx.x;
-        int first = 0, n = 0;
-        if (b < a.num_seqs) released(a, b, true, &first, &n);
-        long long sum;
-        const long long incl = block_scan(n, sums, &sum);
-        tails[threadIdx.x] = n > 0 ? tail + incl - n : -1;
-        tail += sum;
-        __syncthreads();
-        const int last = a.num_seqs - base < kThreads ? a.num_seqs - base : kThreads;
-        for (int i = warp; i < last; i += kWarps) {
-            if (tails[i] < 0) continue;
-            released(a, base + i, false, &first, &n);
-            release_copy(a, f, tails[i], base + i, first, n, lane, 32);
-        }
-        __syncthreads();
-    }
-    release_commit(a, head, count, total, ok);
-}
-
-// Large batches: every CTA sums the whole batch (some tens of KB from L2) and
-// moves the blocks of its own 32 requests; the commit follows as a second
-// kernel, so that the state may be updated in place.
-__global__ void __launch_bounds__(kThreads) release_copy_kernel(const ReleaseArgs a) {
-    __shared__ long long sums[kWarps];
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     const int head = a.free_state[0], count = a.free_state[1];
     const int b0 = blockIdx.x * kReleasePerCta, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    Given g{0, 0, 0, false};
+    if (b0 + lane < a.num_seqs) g = given(a, b0 + lane, warp == 0);
     long long before, total;
     release_sums(a, b0, sums, &before, &total);
-    if (!ring_ok(a, head, count) || count + total > a.ring_size) return;
-    const FreeRing f{a.ring, a.ring_size, head};
-    int first = 0, n = 0;
-    if (b0 + lane < a.num_seqs) released(a, b0 + lane, warp == 0, &first, &n);
-    long long incl = n;
+    const bool ok = ring_ok(a, head, count, total);
+    if (commit) {
+        if (warp == 0 && b0 + lane < a.num_seqs) a.lens_out[b0 + lane] = ok && g.gone ? 0 : g.len;
+        if (b0 == 0 && threadIdx.x == 0) put_state(a, head, count, total, ok);
+    }
+    if (!ok) return;
+    long long incl = g.count;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const long long x = __shfl_up_sync(0xFFFFFFFFu, incl, o);
         if (lane >= o) incl += x;
     }
-    const long long tail = count + before + __shfl_sync(0xFFFFFFFFu, incl - n, warp);
-    first = __shfl_sync(0xFFFFFFFFu, first, warp);
-    n = __shfl_sync(0xFFFFFFFFu, n, warp);
-    if (b0 + warp < a.num_seqs) release_copy(a, f, tail, b0 + warp, first, n, lane, 32);
+    const long long tail = count + before + __shfl_sync(0xFFFFFFFFu, incl - g.count, warp);
+    const int first = __shfl_sync(0xFFFFFFFFu, g.first, warp), n = __shfl_sync(0xFFFFFFFFu, g.count, warp);
+    if (b0 + warp < a.num_seqs) release_copy(a, head, tail, b0 + warp, first, n, lane, 32);
 }
 
-__global__ void __launch_bounds__(kThreads) release_commit_kernel(const ReleaseArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) release_commit_kernel(const ReleaseArgs a) {
     __shared__ long long sums[kWarps];
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     const int head = a.free_state[0], count = a.free_state[1];
     long long zero, total;
     release_sums(a, 0, sums, &zero, &total);
-    release_commit(a, head, count, total, ring_ok(a, head, count) && count + total <= a.ring_size);
+    const bool ok = ring_ok(a, head, count, total);
+    for (int b = threadIdx.x; b < a.num_seqs; b += blockDim.x) {
+        const Given g = given(a, b, false);
+        a.lens_out[b] = ok && g.gone ? 0 : g.len;
+    }
+    if (threadIdx.x == 0) put_state(a, head, count, total, ok);
 }
 
 }  // namespace
@@ -366,13 +385,16 @@ cudaError_t launch_tables_grow(const GrowArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_tables_release(const ReleaseArgs& a, cudaStream_t stream) {
-    if (static_cast<long long>(a.num_seqs) * a.max_blocks <= kSmallEntries) {
-        release_small_kernel<<<1, kThreads, 0, stream>>>(a);
+    if (a.num_seqs <= kThreads && static_cast<long long>(a.num_seqs) * a.max_blocks <= kSmallEntries) {
+        release_small_kernel<<<1, kThreads, 0, stream>>>(a);  // (all 32 warps: they share out the blocks)
         return cudaGetLastError();
     }
-    release_copy_kernel<<<(a.num_seqs + kReleasePerCta - 1) / kReleasePerCta, kThreads, 0, stream>>>(a);
+    // (arrays that overlap otherwise than by being the same are not for this call)
+    const bool apart = a.lens_out != a.lens && a.free_out != a.free_state && a.lens_out != a.finished &&
+                       a.lens_out != a.keep_blocks;
+    release_copy_kernel<<<(a.num_seqs + kReleasePerCta - 1) / kReleasePerCta, kThreads, 0, stream>>>(a, apart ? 1 : 0);
     const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || apart) return e;
     return launch_dependent(release_commit_kernel, dim3(1), dim3(kThreads), 0, stream, a);
 }
 
