@@ -323,7 +323,7 @@ int32_t paged_decode_algo(const pkv_pool* pool, int32_t group, pkv_algo requeste
  *                 every sequence's prefix (from L2, mostly) and looks at no
  *                 group.  PKV_ALGO_TC: the sharing design or
  *                 PKV_ERR_UNSUPPORTED.  PKV_ALGO_MMA, PKV_ALGO_SIMT: those.
- *                 The sharing design serves BF16 pools of head_dim 128, up to
+ *                 The sharing design serves BF16 and FP8 pools of head_dim 128, up to
  *                 4096 sequences, 512 groups and 128 query heads per KV head.
  *   workspace     at least paged_prefix_decode_plan's bytes, 256-byte aligned,
  *                 zeroed before its first call; stream-ordered calls may share

@@ -585,7 +585,7 @@ namespace pkv {
 namespace {
 
 bool prefix_tc_fits(const pkv_pool* p, int num_seqs, int num_groups, int gh, int max_seq_len) {
-    if (!attention_tc_supported(p->d.kv_dtype, p->d.head_dim, p->d.block_size)) return false;
+    if ((p->d.kv_dtype != PKV_BF16 && p->d.kv_dtype != PKV_FP8_E4M3) || p->d.head_dim != 128) return false;
     if (num_seqs > kPrefixMaxSeqs || num_groups > kPrefixMaxGroups || gh > kPrefixRows) return false;
     // tile counts are int32
     const int64_t tiles = (static_cast<int64_t>(max_seq_len) + kTileTokens - 1) / kTileTokens;
@@ -639,7 +639,8 @@ int prefix_design(const pkv_pool* p, int num_seqs, int num_groups, int num_q_hea
     const int gh = num_q_heads / p->d.num_kv_heads;
     if (algo == PKV_ALGO_AUTO || algo == PKV_ALGO_TC) {
         pkv_pool* mp = const_cast<pkv_pool*>(p);
-        if (prefix_tc_fits(p, num_seqs, num_groups, gh, max_seq_len) && ensure_tmaps(mp) && p->tmap_half == 1)
+        if (prefix_tc_fits(p, num_seqs, num_groups, gh, max_seq_len) && ensure_tmaps(mp) &&
+            (p->d.kv_dtype == PKV_FP8_E4M3 || p->tmap_half == 1))
             return PKV_ALGO_TC;
         if (algo == PKV_ALGO_TC) return -1;
     }
@@ -733,8 +734,10 @@ pkv_status paged_prefix_decode_attention(const void* q, pkv_dtype q_dtype, const
     if (!encode_q_map(&q_group, q, num_seqs, num_q_heads, a.gh, a.seqs_per_tile) ||
         !encode_q_map(&q_own, q, num_seqs, num_q_heads, a.gh, 1))
         return PKV_ERR_UNSUPPORTED;
-    return cuda_status(
-        launch_prefix_attention(a, &p->tmap_kh, &p->tmap_vh, &q_group, &q_own, static_cast<cudaStream_t>(stream)));
+    const bool fp8 = p->d.kv_dtype == PKV_FP8_E4M3;
+    return cuda_status(launch_prefix_attention(p->d.kv_dtype, a, fp8 ? &p->tmap_k : &p->tmap_kh,
+                                               fp8 ? &p->tmap_v : &p->tmap_vh, &q_group, &q_own,
+                                               static_cast<cudaStream_t>(stream)));
 }
 
 pkv_status kv_append_norm_rope(const pkv_pool* p, int32_t layer, const void* q, const void* k, const void* v,

@@ -144,8 +144,8 @@ struct PrefixArgs {
     float *pre_o, *pre_lse;        // [B * Hq + ctas * 128]
     float *own_o, *own_lse;        // [B * Hq + ctas * gh]
 };
-cudaError_t launch_prefix_attention(const PrefixArgs& a, const void* tmap_k, const void* tmap_v, const void* tmap_q_group,
-                                    const void* tmap_q_own, cudaStream_t stream);
+cudaError_t launch_prefix_attention(pkv_dtype kv, const PrefixArgs& a, const void* tmap_k, const void* tmap_v,
+                                    const void* tmap_q_group, const void* tmap_q_own, cudaStream_t stream);
 
 // -------------------------------------------------- norm, rotation and append
 struct NormRopeArgs {

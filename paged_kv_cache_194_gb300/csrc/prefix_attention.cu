@@ -2,7 +2,7 @@
 // read and multiplied once for its whole group ("How does TensorRT-LLM
 // work?", "The paged KV cache": requests that begin with the same text point
 // at the same blocks; "TensorRT-LLM, in depth", "The paged KV cache and block
-// reuse").  BF16 pools, head_dim 128.
+// reuse").  BF16 and FP8 pools, head_dim 128.
 //
 // For sequence b of a group with P shared tokens the softmax splits at P:
 //     out = (2^(s1 - M) o1 + 2^(s2 - M) o2) / (2^(s1 - M) + 2^(s2 - M)),
@@ -34,6 +34,9 @@
 //    tensor memory as BF16 pairs (at most 2^-8 of each weight; the sum l is
 //    taken in fp32 before that rounding), the running maximum moved only when
 //    it grows by more than 8, so that O is seldom rescaled.
+// FP8 pools: raw tiles are half the bytes; the softmax warps turn them into FP16
+// operands (exact, the hardware's conversion) in shared memory, K k + 1 before
+// the softmax of tile k and V k behind it, and P is FP16 (2^-11 of each weight).
 // Every wait is bounded; a CTA whose wait expires sets PKV_ERRBIT_TIMEOUT,
 // waits for its copies and products in flight, frees its TMEM and leaves.
 #include <cuda.h>
@@ -58,19 +61,27 @@ constexpr int kQHalf = kRows * 128;           // one 64-column half of the Q til
 constexpr int kHalfBytes = kTok * 128;        // one 64-column half of a K or V tile
 constexpr int kKVOff = 2 * kQHalf;
 constexpr int kStageBytes = 4 * kHalfBytes;   // K + V
+// FP8 pools: the K and the V operand (FP16), one of each, then kNS stages of
+// raw K and kNS of raw V ([64 rows][128 bytes], 128-byte swizzled)
+constexpr int kRawBytes = kTok * kDim;
+constexpr int kRawOff = kKVOff + kStageBytes;
+static_assert(kRawOff + 2 * kNS * kRawBytes == kKVOff + kNS * kStageBytes, "the same ring");
 constexpr int kAlignSlack = 1024;
 static_assert(12 * kPrefixMaxSeqs + 24 * kPrefixMaxGroups <= kNS * kStageBytes, "the plan fits into the ring");
 constexpr uint32_t kTmemCols = 256;
 constexpr uint32_t kOCol = kNS * kTok;
 
 enum Bar { kQReady, kOFree, kDone, kSFull, kPFull = kSFull + kNS, kPvDone = kPFull + kNS, kKFull = kPvDone + kNS,
-           kVFull = kKFull + kNS, kNumBars = kVFull + kNS };
+           kVFull = kKFull + kNS,
+           // FP8 pools: K and Q operands converted, raw stages free
+           kKOp = kVFull + kNS, kQOp, kKEmpty, kVEmpty = kKEmpty + kNS, kNumBars = kVEmpty + kNS };
 constexpr int kBarOff = kKVOff + kNS * kStageBytes;
 constexpr int kExOff = kBarOff + (8 * kNumBars + 8 + 63) / 64 * 64;  // the two threads of a row meet here: maxima
 constexpr int kSumOff = kExOff + 2 * kRows * 4;                        // and sums, [2][kRows] floats each
 // The units of this CTA's range, as far as they fit (else the workspace's copy).
 constexpr int kSeqCache = 1024, kGroupCache = 128;
-constexpr int kGroupOff = kSumOff + 2 * kRows * 4;
+constexpr int kQMaxOff = kSumOff + 2 * kRows * 4;  // and, FP8 pools, the largest |q|, [2][kRows] ints
+constexpr int kGroupOff = kQMaxOff + 2 * kRows * 4;
 constexpr int kSeqOff = kGroupOff + 16 * kGroupCache;
 constexpr int kSmem = kSeqOff + 8 * kSeqCache + kAlignSlack;
 static_assert(kSmem <= 115712, "two CTAs per SM");
@@ -97,6 +108,38 @@ __device__ __forceinline__ void tmem_ld_16x64(uint32_t a, uint32_t (&v)[32]) {
         : "r"(a));
     asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
 }
+// Instruction descriptor: FP16 x FP16 -> F32, otherwise as idesc().
+constexpr uint32_t idesc_f16(int n, int b_mn) { return idesc(n, b_mn) & ~((1u << 7) | (1u << 10)); }
+
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+// Two E4M3 values -> two FP16 ones (exact: 4 bits of significand, exponents
+// from 2^-9 to 2^8; NaN stays NaN).
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two & 0xFFFFu), __NV_E4M3);
+    return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
+}
+// One raw tile of 64 rows by 128 E4M3 -> an FP16 operand tile, by kSoftmax
+// threads; rows from `rows` on become zero.  Lanes that share a row write their
+// two chunks in an order that keeps the two column halves off each other's banks.
+__device__ __forceinline__ void convert_tile(const uint8_t* raw, uint8_t* op, int rows) {
+#pragma unroll
+    for (int i = 0; i < kTok * 8 / kSoftmax; ++i) {
+        const int e = static_cast<int>(threadIdx.x) + i * kSoftmax, r = e >> 3, c = e & 7;
+        uint4 v = *reinterpret_cast<const uint4*>(raw + r * 128 + ((c ^ (r & 7)) << 4));
+        if (r >= rows) v = make_uint4(0u, 0u, 0u, 0u);
+        const uint4 lo = make_uint4(e4m3x2_to_f16x2(v.x), e4m3x2_to_f16x2(v.x >> 16), e4m3x2_to_f16x2(v.y),
+                                    e4m3x2_to_f16x2(v.y >> 16));
+        const uint4 hi = make_uint4(e4m3x2_to_f16x2(v.z), e4m3x2_to_f16x2(v.z >> 16), e4m3x2_to_f16x2(v.w),
+                                    e4m3x2_to_f16x2(v.w >> 16));
+        const int ch = 2 * c, up = c >> 2;
+        *reinterpret_cast<uint4*>(op + tile_off(r, ch + up, kHalfBytes)) = up ? hi : lo;
+        *reinterpret_cast<uint4*>(op + tile_off(r, ch + 1 - up, kHalfBytes)) = up ? lo : hi;
+    }
+}
+
 // Rendezvous of the two warps that share 32 rows (named barrier 1 + id), and
 // with it: does any of their threads say yes?
 __device__ __forceinline__ bool pair_any(int id, bool yes) {
@@ -399,6 +442,7 @@ struct Walk {
     }
 };
 
+template <bool kFp8>
 __global__ void __launch_bounds__(kThreads, 2)
 prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                  const __grid_constant__ CUtensorMap tmq_group, const __grid_constant__ CUtensorMap tmq_own,
@@ -413,7 +457,8 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kNumBars; ++i)
-            bar_init(B(i), ((i >= kPFull && i < kPFull + kNS) || i == kOFree) ? kSoftmaxWarps : (i == kDone ? 2u : 1u));
+            bar_init(B(i), ((i >= kPFull && i < kPFull + kNS) || i == kOFree || i >= kKOp) ? kSoftmaxWarps
+                                                                                           : (i == kDone ? 2u : 1u));
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
@@ -441,10 +486,10 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
     if (warp == kWarpK || warp == kWarpV) {
         // ------------------------------------------------ producers: K, V
         // Stage s is freed by the completion that signals score buffer s: S
-        // done for K, PV done for V.
+        // done for K, PV done for V; a raw FP8 one once it has been converted.
         const bool is_v = warp == kWarpV;
         const CUtensorMap* map = is_v ? &tmv : &tmk;
-        const int full0 = is_v ? kVFull : kKFull, empty0 = is_v ? kPvDone : kSFull;
+        const int full0 = is_v ? kVFull : kKFull, empty0 = kFp8 ? (is_v ? kVEmpty : kKEmpty) : (is_v ? kPvDone : kSFull);
         const int bs = a.block_size;
         const int64_t layer_blk0 = static_cast<int64_t>(a.layer) * a.num_blocks;
         int k = 0, segs = 0;
@@ -468,10 +513,12 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                     ok = false;
                     break;
                 }
-                const uint32_t dst0 = sbase + kKVOff + s * kStageBytes + (is_v ? 2 * kHalfBytes : 0);
-                if (lane == 0) bar_expect_tx(B(full0 + s), static_cast<uint32_t>(nblk * bs * 128 * 2));
+                const uint32_t dst0 = kFp8 ? sbase + kRawOff + (s + (is_v ? kNS : 0)) * kRawBytes
+                                           : sbase + kKVOff + s * kStageBytes + (is_v ? 2 * kHalfBytes : 0);
+                if (lane == 0) bar_expect_tx(B(full0 + s), static_cast<uint32_t>(nblk * bs * kDim * (kFp8 ? 1 : 2)));
                 __syncwarp();
-                const int kb = lane >> 1, hf = lane & 1;  // one copy instruction: lane 2 kb + hf, half hf of block kb
+                // one copy instruction: lane 2 kb + hf, half hf of block kb (FP8: lane kb, block kb)
+                const int kb = kFp8 ? lane : lane >> 1, hf = kFp8 ? 0 : lane & 1;
                 int blk = __shfl_sync(0xFFFFFFFFu, cache, (idx0 + kb - cache_base) & 31);
                 if (kb < nblk) {
                     if (static_cast<unsigned>(blk) >= static_cast<unsigned>(a.num_blocks)) {
@@ -479,7 +526,8 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                         blk = 0;  // an in-bounds block; the flag marks the output invalid
                     }
                     const int y = static_cast<int>(((layer_blk0 + blk) * a.num_kv_heads + sg.head) * bs);
-                    tma_3d(dst0 + hf * kHalfBytes + kb * bs * 128, map, 0, y, hf, B(full0 + s));
+                    if constexpr (kFp8) tma_2d(dst0 + kb * bs * 128, map, 0, y, B(full0 + s));
+                    else tma_3d(dst0 + hf * kHalfBytes + kb * bs * 128, map, 0, y, hf, B(full0 + s));
                 }
                 if (t == 0 && !is_v) {
                     // The segment's Q rows, once the last S of the one before has read its own.
@@ -518,20 +566,20 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                 for (int t = 0; t < sg.n; ++t, ++k) {
                     const int s = k % kNS;
                     // this segment's Q, K k, and a score buffer whose P has been multiplied (PV k - 2)
-                    if (*abort_flag || (t == 0 && !bar_wait(B(kQReady), seg & 1)) ||
-                        !bar_wait(B(kKFull + s), (k / kNS) & 1) ||
+                    if (*abort_flag || (t == 0 && !bar_wait(B(kFp8 ? kQOp : kQReady), seg & 1)) ||
+                        !(kFp8 ? bar_wait(B(kKOp), k & 1) : bar_wait(B(kKFull + s), (k / kNS) & 1)) ||
                         (k >= kNS && !bar_wait(B(kPvDone + s), (k / kNS - 1) & 1))) {
                         ok = false;
                         break;
                     }
                     fence_after();
-                    const uint64_t dk = dk0 + static_cast<uint64_t>((s * kStageBytes) >> 4);
+                    const uint64_t dk = dk0 + (kFp8 ? 0 : static_cast<uint64_t>((s * kStageBytes) >> 4));
                     const uint32_t sb = tmem + static_cast<uint32_t>(s * kTok);
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks) {
                         const uint32_t kin = (ks & 3) * 32;
                         mma_bf16(sb, dq + (((ks >> 2) * kQHalf + kin) >> 4), dk + (((ks >> 2) * kHalfBytes + kin) >> 4),
-                                 idesc(kTok, 0), ks > 0 ? 1u : 0u);
+                                 kFp8 ? idesc_f16(kTok, 0) : idesc(kTok, 0), ks > 0 ? 1u : 0u);
                     }
                     mma_commit(B(kSFull + s));
                 }
@@ -551,18 +599,19 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
             for (int seg = 0; ok && w.next(a, sg); ++seg) {
                 for (int t = 0; t < sg.n; ++t, ++k) {
                     const int s = k % kNS;
-                    // V k, P k, and for a new segment an O that has been read out
-                    if (*abort_flag || !bar_wait(B(kVFull + s), (k / kNS) & 1) || !bar_wait(B(kPFull + s), (k / kNS) & 1) ||
+                    // V k (FP8: converted before P k), P k, and for a new segment an O that has been read out
+                    if (*abort_flag || (!kFp8 && !bar_wait(B(kVFull + s), (k / kNS) & 1)) ||
+                        !bar_wait(B(kPFull + s), (k / kNS) & 1) ||
                         (t == 0 && seg > 0 && !bar_wait(B(kOFree), (seg - 1) & 1))) {
                         ok = false;
                         break;
                     }
                     fence_after();
-                    const uint64_t dv = dv0 + static_cast<uint64_t>((s * kStageBytes) >> 4);
+                    const uint64_t dv = dv0 + (kFp8 ? 0 : static_cast<uint64_t>((s * kStageBytes) >> 4));
                     const uint32_t pb = tmem + static_cast<uint32_t>(s * kTok);
 #pragma unroll
                     for (int ks = 0; ks < kTok / 16; ++ks)
-                        mma_bf16_ta(tmem + kOCol, pb + 8 * ks, dv + ((ks * 16 * 128) >> 4), idesc(kDim, 1),
+                        mma_bf16_ta(tmem + kOCol, pb + 8 * ks, dv + ((ks * 16 * 128) >> 4), kFp8 ? idesc_f16(kDim, 1) : idesc(kDim, 1),
                                     (t > 0 || ks > 0) ? 1u : 0u);
                     mma_commit(B(kPvDone + s));
                 }
@@ -583,7 +632,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
         // (written once more only after a later rendezvous of the pair)
         float* ex = reinterpret_cast<float*>(smem + kExOff);
         float* sums = reinterpret_cast<float*>(smem + kSumOff);
-        const float qk = a.qk_scale_log2;
+        float qk = a.qk_scale_log2;  // FP8 pools: of this row, see convert_q
         // A wait that expires makes the warp `dead`: it goes on through the
         // loop, without waiting or working, only to meet its partner.
         bool dead = false;
@@ -594,9 +643,63 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
             }
         };
 
+        // FP8 pools: K, V and Q reach the tensor cores as FP16.  E4M3 fits
+        // exactly; a query row is scaled by the power of two that brings its
+        // largest element to [2^14, 2^15), which leaves 8 bits of every element
+        // down to 2^-28 of that, and goes back into the row's score scale.
+        int* qmax = reinterpret_cast<int*>(smem + kQMaxOff);
+        auto convert_q = [&](int seg, const Seg& s) {
+            wait(kQReady, seg);
+            if (32 * pair < s.rows(a)) {
+                uint4 v[8];
+                int top = 0;
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    v[c] = *reinterpret_cast<const uint4*>(smem + tile_off(m, 8 * hf + c, kQHalf));
+                    const uint32_t u[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        top = max(top, max(static_cast<int>(u[i] & 0x7FFFu), static_cast<int>((u[i] >> 16) & 0x7FFFu)));
+                }
+                qmax[hf * kRows + m] = top;
+                pair_sync(pair);
+                const int ex = max(top, qmax[(hf ^ 1) * kRows + m]) >> 7;  // exponent field: 0 zero or subnormal, 255 inf, NaN
+                const int shift = ex == 0 || ex == 255 ? 0 : min(141 - ex, 126);
+                const float up = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
+                qk = a.qk_scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    uint32_t u[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) u[i] = f16x2(bf16_lo(u[i]) * up, bf16_hi(u[i]) * up);
+                    *reinterpret_cast<uint4*>(smem + tile_off(m, 8 * hf + c, kQHalf)) = make_uint4(u[0], u[1], u[2], u[3]);
+                }
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) bar_arrive(B(kQOp));
+        };
+        // K of tile k: its raw stage has landed, and S k - 1 has read the operand.
+        auto convert_k = [&](int k) {
+            const int s = k % kNS;
+            wait(kKFull + s, k / kNS);
+            convert_tile(smem + kRawOff + s * kRawBytes, smem + kKVOff, kTok);
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                bar_arrive(B(kKEmpty + s));
+                bar_arrive(B(kKOp));
+            }
+        };
+
         Seg sg, nx;
         bool has = w.next(a, sg);
-        for (int k0 = 0; has;) {
+        if (kFp8 && has) {
+            convert_k(0);
+            convert_q(0, sg);
+        }
+        int seg = 0;
+        for (int k0 = 0; has; ++seg) {
             const bool has_next = w.next(a, nx);  // (early: its loads overlap the first S)
             const int nv = sg.rows(a);
             const bool busy = 32 * pair < nv;
@@ -606,6 +709,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                 const int visible = sg.end - (sg.tile + t) * kTok;  // of this tile, the same for every row
                 wait(kSFull + s, k / kNS);
                 fence_after();
+                if (kFp8 && (t + 1 < sg.n || has_next)) convert_k(k + 1);  // (so that S k + 1 runs beside this softmax)
                 const uint32_t sa = tmem + lane_off + static_cast<uint32_t>(s * kTok);
                 bool rescale = false;
                 float alpha = 1.f;
@@ -653,7 +757,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                             fma2(x0, x1, __uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), qk, qk, -base, -base);
                             const float p0 = ex2(x0), p1 = ex2(x1);
                             add2(l0, l1, l0, l1, p0, p1);
-                            pk[i] = bf16x2(p0, p1);
+                            pk[i] = kFp8 ? f16x2(p0, p1) : bf16x2(p0, p1);
                         }
                         lt = l0 + l1;
                     } else {
@@ -662,7 +766,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                             const float p0 = 2 * i < seen ? ex2(fmaf(__uint_as_float(v[2 * i]), qk, -base)) : 0.f;
                             const float p1 = 2 * i + 1 < seen ? ex2(fmaf(__uint_as_float(v[2 * i + 1]), qk, -base)) : 0.f;
                             lt += p0 + p1;
-                            pk[i] = bf16x2(p0, p1);
+                            pk[i] = kFp8 ? f16x2(p0, p1) : bf16x2(p0, p1);
                         }
                     }
                     l = l * alpha + lt;
@@ -684,8 +788,15 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                         }
                     }
                 }
-                // V rows past the last token: zero (stale or unwritten rows could hold NaN)
-                if (visible < kTok) {
+                if constexpr (kFp8) {
+                    // V k, once PV k - 1 has read the operand before it (rows past the last token: zero)
+                    wait(kVFull + s, k / kNS);
+                    if (k > 0) wait(kPvDone + (k + kNS - 1) % kNS, (k - 1) / kNS);
+                    convert_tile(smem + kRawOff + (kNS + s) * kRawBytes, smem + kKVOff + 2 * kHalfBytes, visible);
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(B(kVEmpty + s));
+                } else if (visible < kTok) {  // V rows past the last token: zero (stale or unwritten rows could hold NaN)
                     wait(kVFull + s, k / kNS);
                     uint8_t* vs = smem + kKVOff + s * kStageBytes + 2 * kHalfBytes;
                     const int nz = kTok - visible;
@@ -702,6 +813,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
             }
             // ---- the piece ends
             const int kl = k0 + sg.n - 1;
+            if (kFp8 && has_next) convert_q(seg + 1, nx);  // (sets qk, which this piece is done with)
             if (busy) {
                 sums[hf * kRows + m] = l;
                 pair_sync(pair);
@@ -833,25 +945,34 @@ __global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const Prefi
 
 }  // namespace
 
-cudaError_t launch_prefix_attention(const PrefixArgs& a, const void* tmap_k, const void* tmap_v, const void* tmap_q_group,
-                                    const void* tmap_q_own, cudaStream_t stream) {
+namespace {
+template <bool kFp8>
+cudaError_t launch_tc(const PrefixArgs& a, const void* tmap_k, const void* tmap_v, const void* tmap_q_group,
+                      const void* tmap_q_own, cudaStream_t stream) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     static uint64_t configured = 0;
     if (dev < 0 || dev >= 64) return cudaErrorNotSupported;
     if (!(configured >> dev & 1)) {
-        e = cudaFuncSetAttribute(prefix_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        e = cudaFuncSetAttribute(prefix_tc_kernel<kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(prefix_tc_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+            e = cudaFuncSetAttribute(prefix_tc_kernel<kFp8>, cudaFuncAttributePreferredSharedMemoryCarveout,
                                      cudaSharedmemCarveoutMaxShared);
         if (e != cudaSuccess) return e;
         configured |= 1ull << dev;
     }
-    prefix_tc_kernel<<<a.ctas, kThreads, kSmem, stream>>>(
+    prefix_tc_kernel<kFp8><<<a.ctas, kThreads, kSmem, stream>>>(
         *static_cast<const CUtensorMap*>(tmap_k), *static_cast<const CUtensorMap*>(tmap_v),
         *static_cast<const CUtensorMap*>(tmap_q_group), *static_cast<const CUtensorMap*>(tmap_q_own), a);
-    e = cudaGetLastError();
+    return cudaGetLastError();
+}
+}  // namespace
+
+cudaError_t launch_prefix_attention(pkv_dtype kv, const PrefixArgs& a, const void* tmap_k, const void* tmap_v,
+                                    const void* tmap_q_group, const void* tmap_q_own, cudaStream_t stream) {
+    const cudaError_t e = kv == PKV_FP8_E4M3 ? launch_tc<true>(a, tmap_k, tmap_v, tmap_q_group, tmap_q_own, stream)
+                                             : launch_tc<false>(a, tmap_k, tmap_v, tmap_q_group, tmap_q_own, stream);
     if (e != cudaSuccess) return e;
     const int64_t rows = static_cast<int64_t>(a.num_seqs) * a.num_q_heads;
     constexpr int per = kMergeThreads / 32;

@@ -92,13 +92,14 @@ def release(tables, lens, finished, keep, ring, free_state, bs):
     return out, [head, count]
 
 
-def attention_bound(out, mass, dtype=torch.bfloat16):
-    """|error| of the tensor-core design: every weight is rounded to BF16 (half
-    a step of its own size: at most that share of `mass`), the output rounded
-    once; scores, sums and 2^x in fp32 add up to well under 2^-13 of `mass`
-    (128-term dot products of values near 4: 128 x 2^-24 x 16 in the exponent)."""
-    h = HALF[dtype]
-    return h * mass + h * (out.abs() + h * mass) + 2.0 ** -13 * mass
+def attention_bound(out, mass, kv="bf16"):
+    """|error| of the tensor-core design: every weight is rounded to BF16, with
+    FP8 pools to FP16 (half a step of its own size: at most that share of
+    `mass`), the output rounded once to BF16; scores, sums and 2^x in fp32 add up
+    to well under 2^-13 of `mass` (128-term dot products of values near 4: 128 x
+    2^-24 x 16 in the exponent)."""
+    weight, h = (2.0 ** -11 if kv == "fp8" else 2.0 ** -8), HALF[torch.bfloat16]
+    return weight * mass + h * (out.abs() + weight * mass) + 2.0 ** -13 * mass
 
 
 def scale_for(d):

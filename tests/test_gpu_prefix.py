@@ -80,7 +80,7 @@ class Batch:
         want, mass = self.reference()
         err = (out.cpu().double() - want).abs()
         if design == "tc":
-            bound = ref.attention_bound(want, mass)
+            bound = ref.attention_bound(want, mass, self.kv)
         else:  # the designs of decode attention, within its own tolerance
             bound = TOL[self.kv] * (1.0 + want.abs())
         bad = ~(err <= bound)
@@ -163,14 +163,27 @@ def test_prefix_growing_scores_rescale(kv):
     want, mass = bt.reference()
     if bt.design() == "tc":
         # scores six times as wide: 6 x the exponent's error
-        bound = ref.attention_bound(want, mass) + 5 * 2.0 ** -13 * mass
+        bound = ref.attention_bound(want, mass, kv) + 5 * 2.0 ** -13 * mass
         assert ((out.cpu().double() - want).abs() <= bound).all()
     else:
         assert ((out.cpu().double() - want).abs() <= 6 * TOL[kv] * (1 + want.abs())).all()
 
 
-def test_prefix_negative_and_zero_scale():
-    bt = Batch((300, 333, 290), [(0, 3, 256)], seed=2)
+@pytest.mark.parametrize("size", [2.0 ** -100, 1e-6, 1.0, 1e6, 2.0 ** 100])
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_prefix_query_magnitudes(kv, size):
+    """Queries of any size (the scale takes it back): FP8 pools scale each row into FP16's range."""
+    bt = Batch((300, 333, 290, 70), [(0, 3, 256)], seed=14, kv=kv)
+    rows = torch.tensor([1.0, 0.5, 3.0, 0.01]).view(4, 1, 1)  # (other sizes from row to row)
+    bt.q = (bt.q.float() * rows * size).to(torch.bfloat16)
+    bt.q[1, 2] = 0
+    bt.scale = bt.scale / size
+    bt.check(bt.run(), "tc")
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_prefix_negative_and_zero_scale(kv):
+    bt = Batch((300, 333, 290), [(0, 3, 256)], seed=2, kv=kv)
     for scale in (-0.07, 0.0):
         bt.scale = scale
         bt.check(bt.run(), bt.design())
@@ -192,18 +205,34 @@ def test_prefix_agrees_with_decode_attention(shape):
             bt.scale, algo=algo))
 
 
-def test_prefix_bad_groups_still_give_right_results():
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_prefix_bad_groups_still_give_right_results(kv):
     lens = (300, 310, 320, 330)
     for offsets, prefix, bit in (([0, 3, 1, 4], [256, 256, 256], pk.ERRBIT_GROUP), ([-1, 4], [256], pk.ERRBIT_GROUP),
                                  ([0, 9], [256], pk.ERRBIT_GROUP), ([0, 4], [-5], pk.ERRBIT_GROUP),
                                  ([0, 4], [10 ** 6], 0)):  # longer than every member: shares nothing
-        bt = Batch(lens, [(0, 4, 256)], seed=4, offsets=offsets, prefix=prefix)
+        bt = Batch(lens, [(0, 4, 256)], seed=4, kv=kv, offsets=offsets, prefix=prefix)
         bt.check(bt.run(algo="tc"), "tc")
         assert bt.pool.errors() == bit, (offsets, prefix)
 
 
-def test_prefix_reports_bad_lengths_and_blocks():
-    bt = Batch((300, 310, 320), [(0, 3, 256)], seed=4)
+def test_prefix_fp8_nan_codes_stay_nan():
+    """A NaN code in a value a sequence attends to makes its output NaN there,
+    and touches no other sequence or column."""
+    bt = Batch((300, 310, 320), [(0, 3, 256)], seed=4, kv="fp8")
+    good = bt.run()
+    blk = int(bt.tables[1, 18])  # an own block of sequence 1
+    bt.pool.v[1, blk, 0, 3, 7] = 0x7F
+    out = bt.run()
+    assert out[1, :4, 7].isnan().all()
+    keep = torch.ones_like(out, dtype=torch.bool)
+    keep[1, :4, 7] = False
+    assert torch.equal(out[keep], good[keep])
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_prefix_reports_bad_lengths_and_blocks(kv):
+    bt = Batch((300, 310, 320), [(0, 3, 256)], seed=4, kv=kv)
     good = bt.run()
     lens = bt.lens
     bt.lens = (300, 310, -2)
@@ -220,9 +249,10 @@ def test_prefix_reports_bad_lengths_and_blocks():
     assert torch.equal(out[0], good[0]) and torch.equal(out[2], good[2])
 
 
-def test_prefix_repeats_exactly_and_leaves_other_rows():
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_prefix_repeats_exactly_and_leaves_other_rows(kv):
     lens, groups = SHAPES["many"]
-    bt = Batch(lens, groups, seed=8)
+    bt = Batch(lens, groups, seed=8, kv=kv)
     B = len(lens)
     big = torch.full((B + 5,) + bt.q.shape[1:], 3.0, dtype=bt.q.dtype, device="cuda")
     ws = pk.prefix_decode_workspace(bt.pool, B, 1, bt.q.shape[1], bt.max_len)
@@ -245,9 +275,10 @@ def test_prefix_shares_a_workspace_with_decode_attention():
         assert torch.equal(b.run(algo="mma", workspace=ws), want_b)
 
 
-def test_prefix_captured_call_follows_lengths_and_groups():
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_prefix_captured_call_follows_lengths_and_groups(kv):
     """One captured call replayed over other lengths, groups and queries."""
-    bt = Batch((900, 800, 850, 700, 720), [(0, 3, 768), (3, 5, 640)], seed=6)
+    bt = Batch((900, 800, 850, 700, 720), [(0, 3, 768), (3, 5, 640)], seed=6, kv=kv)
     dev = dict(q=bt.q.cuda(), t=bt.tables.cuda(), n=torch.tensor(bt.lens, dtype=torch.int32).cuda(),
                o=bt.offsets.cuda(), p=bt.prefix.cuda())
     ws = pk.prefix_decode_workspace(bt.pool, 5, 2, 8, bt.max_len)
@@ -294,9 +325,10 @@ def test_prefix_two_streams_at_once():
         assert torch.equal(x, want[0]) and torch.equal(y, want[1])
 
 
-def test_prefix_more_sequences_than_ctas():
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_prefix_more_sequences_than_ctas(kv):
     """Many short sequences: a CTA walks over many units, some empty."""
     lens = tuple(itertools.islice(itertools.cycle((64, 70, 0, 65, 130, 64, 1)), 700))
-    bt = Batch(lens, [(0, 350, 64), (350, 700, 64)], 4, 2, seed=12, bs=64)
+    bt = Batch(lens, [(0, 350, 64), (350, 700, 64)], 4, 2, seed=12, bs=64, kv=kv)
     bt.check(bt.run(), "tc")
     assert bt.pool.errors() == 0
