@@ -34,9 +34,13 @@
 //    tensor memory as BF16 pairs (at most 2^-8 of each weight; the sum l is
 //    taken in fp32 before that rounding), the running maximum moved only when
 //    it grows by more than 8, so that O is seldom rescaled.
-// FP8 pools: raw tiles are half the bytes; the softmax warps turn them into FP16
-// operands (exact, the hardware's conversion) in shared memory, K k + 1 before
-// the softmax of tile k and V k behind it, and P is FP16 (2^-11 of each weight).
+// FP8 pools: the tensor cores multiply K and V as stored (kind f8f6f4, E4M3
+// operands), half the bytes in the ring; Q and P enter as the sum of two E4M3
+// terms, so S is two passes over K's 128 columns, 32 a step, and PV two over the
+// 64 tokens: as many instructions as for BF16.  (Tiles converted to FP16 in
+// shared memory first, by the softmax warps or by four more, took 2.3 us a tile
+// where this takes 1: the extra 56 KB a tile through shared memory and the
+// waits between the steps.)
 // Every wait is bounded; a CTA whose wait expires sets PKV_ERRBIT_TIMEOUT,
 // waits for its copies and products in flight, frees its TMEM and leaves.
 #include <cuda.h>
@@ -61,11 +65,7 @@ constexpr int kQHalf = kRows * 128;           // one 64-column half of the Q til
 constexpr int kHalfBytes = kTok * 128;        // one 64-column half of a K or V tile
 constexpr int kKVOff = 2 * kQHalf;
 constexpr int kStageBytes = 4 * kHalfBytes;   // K + V
-// FP8 pools: the K and the V operand (FP16), one of each, then kNS stages of
-// raw K and kNS of raw V ([64 rows][128 bytes], 128-byte swizzled)
-constexpr int kRawBytes = kTok * kDim;
-constexpr int kRawOff = kKVOff + kStageBytes;
-static_assert(kRawOff + 2 * kNS * kRawBytes == kKVOff + kNS * kStageBytes, "the same ring");
+constexpr int kRawBytes = kTok * kDim;        // FP8 pools: a K or V tile, [64 rows][128 bytes]
 constexpr int kAlignSlack = 1024;
 static_assert(12 * kPrefixMaxSeqs + 24 * kPrefixMaxGroups <= kNS * kStageBytes, "the plan fits into the ring");
 constexpr uint32_t kTmemCols = 256;
@@ -73,8 +73,8 @@ constexpr uint32_t kOCol = kNS * kTok;
 
 enum Bar { kQReady, kOFree, kDone, kSFull, kPFull = kSFull + kNS, kPvDone = kPFull + kNS, kKFull = kPvDone + kNS,
            kVFull = kKFull + kNS,
-           // FP8 pools: K and Q operands converted, raw stages free
-           kKOp = kVFull + kNS, kQOp, kKEmpty, kVEmpty = kKEmpty + kNS, kNumBars = kVEmpty + kNS };
+           kQOp = kVFull + kNS,  // FP8 pools: Q split into E4M3 terms
+           kNumBars };
 constexpr int kBarOff = kKVOff + kNS * kStageBytes;
 constexpr int kExOff = kBarOff + (8 * kNumBars + 8 + 63) / 64 * 64;  // the two threads of a row meet here: maxima
 constexpr int kSumOff = kExOff + 2 * kRows * 4;                        // and sums, [2][kRows] floats each
@@ -108,37 +108,46 @@ __device__ __forceinline__ void tmem_ld_16x64(uint32_t a, uint32_t (&v)[32]) {
         : "r"(a));
     asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
 }
-// Instruction descriptor: FP16 x FP16 -> F32, otherwise as idesc().
-constexpr uint32_t idesc_f16(int n, int b_mn) { return idesc(n, b_mn) & ~((1u << 7) | (1u << 10)); }
-
-__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
-    const __half2 v = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
+// Instruction descriptor: E4M3 x E4M3 -> F32, otherwise as idesc().
+constexpr uint32_t idesc_f8(int n, int b_mn) { return idesc(n, b_mn) & ~((1u << 7) | (1u << 10)); }
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(id), "r"(acc)
+        : "memory");
 }
-// Two E4M3 values -> two FP16 ones (exact: 4 bits of significand, exponents
-// from 2^-9 to 2^8; NaN stays NaN).
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two & 0xFFFFu), __NV_E4M3);
-    return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
+__device__ __forceinline__ void mma_f8_ta(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t id, uint32_t acc) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "r"(a_tmem), "l"(b), "r"(id), "r"(acc)
+        : "memory");
 }
-// One raw tile of 64 rows by 128 E4M3 -> an FP16 operand tile, by kSoftmax
-// threads; rows from `rows` on become zero.  Lanes that share a row write their
-// two chunks in an order that keeps the two column halves off each other's banks.
-__device__ __forceinline__ void convert_tile(const uint8_t* raw, uint8_t* op, int rows) {
-#pragma unroll
-    for (int i = 0; i < kTok * 8 / kSoftmax; ++i) {
-        const int e = static_cast<int>(threadIdx.x) + i * kSoftmax, r = e >> 3, c = e & 7;
-        uint4 v = *reinterpret_cast<const uint4*>(raw + r * 128 + ((c ^ (r & 7)) << 4));
-        if (r >= rows) v = make_uint4(0u, 0u, 0u, 0u);
-        const uint4 lo = make_uint4(e4m3x2_to_f16x2(v.x), e4m3x2_to_f16x2(v.x >> 16), e4m3x2_to_f16x2(v.y),
-                                    e4m3x2_to_f16x2(v.y >> 16));
-        const uint4 hi = make_uint4(e4m3x2_to_f16x2(v.z), e4m3x2_to_f16x2(v.z >> 16), e4m3x2_to_f16x2(v.w),
-                                    e4m3x2_to_f16x2(v.w >> 16));
-        const int ch = 2 * c, up = c >> 2;
-        *reinterpret_cast<uint4*>(op + tile_off(r, ch + up, kHalfBytes)) = up ? hi : lo;
-        *reinterpret_cast<uint4*>(op + tile_off(r, ch + 1 - up, kHalfBytes)) = up ? lo : hi;
-    }
+__device__ __forceinline__ void tmem_st8(uint32_t a, const uint32_t (&v)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(a), "r"(v[0]), "r"(v[1]),
+                 "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
 }
+// Four values up to 448 as the sum of two E4M3 terms: hi = rn(x), lo = rn(x -
+// hi), x rounded to FP16 first.  Exact for 8-bit significands whose last bit is
+// at least 2^-9; else off by at most 2^-8 of x (two halved steps of 2^-4, and
+// 2^-11 for FP16), or 2^-10 where lo is subnormal.
+__device__ __forceinline__ void split4(float x0, float x1, float x2, float x3, uint32_t& hi, uint32_t& lo) {
+    asm("{\n .reg .b16 a, b, c, d;\n .reg .b32 p, q, r, s;\n"
+        " cvt.rn.satfinite.e4m3x2.f32 a, %3, %2;\n cvt.rn.satfinite.e4m3x2.f32 b, %5, %4;\n"
+        " cvt.rn.f16x2.e4m3x2 p, a;\n cvt.rn.f16x2.e4m3x2 q, b;\n"
+        " cvt.rn.f16x2.f32 r, %3, %2;\n cvt.rn.f16x2.f32 s, %5, %4;\n"
+        " sub.rn.f16x2 r, r, p;\n sub.rn.f16x2 s, s, q;\n"
+        " cvt.rn.satfinite.e4m3x2.f16x2 c, r;\n cvt.rn.satfinite.e4m3x2.f16x2 d, s;\n"
+        " mov.b32 %0, {a, b};\n mov.b32 %1, {c, d};\n}\n"
+        : "=r"(hi), "=r"(lo)
+        : "f"(x0), "f"(x1), "f"(x2), "f"(x3));
+}
+// Slack of the running maximum (log2), and the power of two that E4M3 weights
+// are scaled by: 2^(7 + 1) stays below 448.
+template <bool kFp8>
+constexpr float slack_of() { return kFp8 ? 1.f : 8.f; }
+template <bool kFp8>
+constexpr float weight_shift_of() { return kFp8 ? 7.f : 0.f; }
 
 // Rendezvous of the two warps that share 32 rows (named barrier 1 + id), and
 // with it: does any of their threads say yes?
@@ -457,7 +466,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kNumBars; ++i)
-            bar_init(B(i), ((i >= kPFull && i < kPFull + kNS) || i == kOFree || i >= kKOp) ? kSoftmaxWarps
+            bar_init(B(i), ((i >= kPFull && i < kPFull + kNS) || i == kOFree || i == kQOp) ? kSoftmaxWarps
                                                                                            : (i == kDone ? 2u : 1u));
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
@@ -486,10 +495,10 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
     if (warp == kWarpK || warp == kWarpV) {
         // ------------------------------------------------ producers: K, V
         // Stage s is freed by the completion that signals score buffer s: S
-        // done for K, PV done for V; a raw FP8 one once it has been converted.
+        // done for K, PV done for V.
         const bool is_v = warp == kWarpV;
         const CUtensorMap* map = is_v ? &tmv : &tmk;
-        const int full0 = is_v ? kVFull : kKFull, empty0 = kFp8 ? (is_v ? kVEmpty : kKEmpty) : (is_v ? kPvDone : kSFull);
+        const int full0 = is_v ? kVFull : kKFull, empty0 = is_v ? kPvDone : kSFull;
         const int bs = a.block_size;
         const int64_t layer_blk0 = static_cast<int64_t>(a.layer) * a.num_blocks;
         int k = 0, segs = 0;
@@ -513,7 +522,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                     ok = false;
                     break;
                 }
-                const uint32_t dst0 = kFp8 ? sbase + kRawOff + (s + (is_v ? kNS : 0)) * kRawBytes
+                const uint32_t dst0 = kFp8 ? sbase + kKVOff + (2 * s + (is_v ? 1 : 0)) * kRawBytes
                                            : sbase + kKVOff + s * kStageBytes + (is_v ? 2 * kHalfBytes : 0);
                 if (lane == 0) bar_expect_tx(B(full0 + s), static_cast<uint32_t>(nblk * bs * kDim * (kFp8 ? 1 : 2)));
                 __syncwarp();
@@ -567,19 +576,21 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                     const int s = k % kNS;
                     // this segment's Q, K k, and a score buffer whose P has been multiplied (PV k - 2)
                     if (*abort_flag || (t == 0 && !bar_wait(B(kFp8 ? kQOp : kQReady), seg & 1)) ||
-                        !(kFp8 ? bar_wait(B(kKOp), k & 1) : bar_wait(B(kKFull + s), (k / kNS) & 1)) ||
+                        !bar_wait(B(kKFull + s), (k / kNS) & 1) ||
                         (k >= kNS && !bar_wait(B(kPvDone + s), (k / kNS - 1) & 1))) {
                         ok = false;
                         break;
                     }
                     fence_after();
-                    const uint64_t dk = dk0 + (kFp8 ? 0 : static_cast<uint64_t>((s * kStageBytes) >> 4));
+                    const uint64_t dk = dk0 + static_cast<uint64_t>((s * (kFp8 ? 2 * kRawBytes : kStageBytes)) >> 4);
                     const uint32_t sb = tmem + static_cast<uint32_t>(s * kTok);
 #pragma unroll
-                    for (int ks = 0; ks < 8; ++ks) {
+                    for (int ks = 0; ks < 8; ++ks) {  // 16 columns a step; FP8: 32, first of Q's high terms, then of the low ones
                         const uint32_t kin = (ks & 3) * 32;
-                        mma_bf16(sb, dq + (((ks >> 2) * kQHalf + kin) >> 4), dk + (((ks >> 2) * kHalfBytes + kin) >> 4),
-                                 kFp8 ? idesc_f16(kTok, 0) : idesc(kTok, 0), ks > 0 ? 1u : 0u);
+                        if constexpr (kFp8)
+                            mma_f8(sb, dq + (((ks >> 2) * kQHalf + kin) >> 4), dk + (kin >> 4), idesc_f8(kTok, 0), ks > 0 ? 1u : 0u);
+                        else mma_bf16(sb, dq + (((ks >> 2) * kQHalf + kin) >> 4), dk + (((ks >> 2) * kHalfBytes + kin) >> 4),
+                                 idesc(kTok, 0), ks > 0 ? 1u : 0u);
                     }
                     mma_commit(B(kSFull + s));
                 }
@@ -593,26 +604,28 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
         // ------------------------------------------------------- O += P V
         if (lane == 0) {
             bool ok = true;
-            const uint64_t dv0 = sdesc(sbase + kKVOff + 2 * kHalfBytes, kHalfBytes);
+            const uint64_t dv0 = sdesc(sbase + kKVOff + (kFp8 ? kRawBytes : 2 * kHalfBytes), kHalfBytes);
             Seg sg;
             int k = 0;
             for (int seg = 0; ok && w.next(a, sg); ++seg) {
                 for (int t = 0; t < sg.n; ++t, ++k) {
                     const int s = k % kNS;
-                    // V k (FP8: converted before P k), P k, and for a new segment an O that has been read out
-                    if (*abort_flag || (!kFp8 && !bar_wait(B(kVFull + s), (k / kNS) & 1)) ||
+                    // V k, P k, and for a new segment an O that has been read out
+                    if (*abort_flag || !bar_wait(B(kVFull + s), (k / kNS) & 1) ||
                         !bar_wait(B(kPFull + s), (k / kNS) & 1) ||
                         (t == 0 && seg > 0 && !bar_wait(B(kOFree), (seg - 1) & 1))) {
                         ok = false;
                         break;
                     }
                     fence_after();
-                    const uint64_t dv = dv0 + (kFp8 ? 0 : static_cast<uint64_t>((s * kStageBytes) >> 4));
+                    const uint64_t dv = dv0 + static_cast<uint64_t>((s * (kFp8 ? 2 * kRawBytes : kStageBytes)) >> 4);
                     const uint32_t pb = tmem + static_cast<uint32_t>(s * kTok);
 #pragma unroll
-                    for (int ks = 0; ks < kTok / 16; ++ks)
-                        mma_bf16_ta(tmem + kOCol, pb + 8 * ks, dv + ((ks * 16 * 128) >> 4), kFp8 ? idesc_f16(kDim, 1) : idesc(kDim, 1),
-                                    (t > 0 || ks > 0) ? 1u : 0u);
+                    for (int ks = 0; ks < kTok / 16; ++ks) {  // 16 tokens a step; FP8: 32, of P's high, then of its low terms
+                        const uint32_t acc = t > 0 || ks > 0 ? 1u : 0u;
+                        if constexpr (kFp8) mma_f8_ta(tmem + kOCol, pb + 8 * ks, dv + (((ks & 1) * 32 * 128) >> 4), idesc_f8(kDim, 1), acc);
+                        else mma_bf16_ta(tmem + kOCol, pb + 8 * ks, dv + ((ks * 16 * 128) >> 4), idesc(kDim, 1), acc);
+                    }
                     mma_commit(B(kPvDone + s));
                 }
             }
@@ -643,10 +656,12 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
             }
         };
 
-        // FP8 pools: K, V and Q reach the tensor cores as FP16.  E4M3 fits
-        // exactly; a query row is scaled by the power of two that brings its
-        // largest element to [2^14, 2^15), which leaves 8 bits of every element
-        // down to 2^-28 of that, and goes back into the row's score scale.
+        // FP8 pools: the tensor cores take K and V as stored, and one type for
+        // both operands.  A query row is scaled by the power of two that brings
+        // its largest element to [2^7, 2^8) and split into two E4M3 terms: a BF16
+        // significand has 8 bits, hi takes 4 and lo the rest, so the sum is exact
+        // for elements down to 2^-10 of the largest (below, off by 2^-18 of it).
+        // The scale goes back into the row's score scale.
         int* qmax = reinterpret_cast<int*>(smem + kQMaxOff);
         auto convert_q = [&](int seg, const Seg& s) {
             wait(kQReady, seg);
@@ -662,42 +677,36 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                         top = max(top, max(static_cast<int>(u[i] & 0x7FFFu), static_cast<int>((u[i] >> 16) & 0x7FFFu)));
                 }
                 qmax[hf * kRows + m] = top;
-                pair_sync(pair);
+                pair_sync(pair);  // (and both threads of the row have read it)
                 const int ex = max(top, qmax[(hf ^ 1) * kRows + m]) >> 7;  // exponent field: 0 zero or subnormal, 255 inf, NaN
-                const int shift = ex == 0 || ex == 255 ? 0 : min(141 - ex, 126);
+                const int shift = ex == 0 || ex == 255 ? 0 : min(134 - ex, 126);
                 const float up = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
-                qk = a.qk_scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
+                // (an infinite or NaN query, which E4M3 would clamp, makes the whole row NaN)
+                qk = ex == 255 ? __uint_as_float(0x7FC00000u)
+                               : a.qk_scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
+                // columns 64 hf .. 64 hf + 63: four 16-byte chunks of the high tile, four of the low one
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    uint32_t u[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+                for (int c = 0; c < 4; ++c) {
+                    const uint32_t u[8] = {v[2 * c].x,     v[2 * c].y,     v[2 * c].z,     v[2 * c].w,
+                                           v[2 * c + 1].x, v[2 * c + 1].y, v[2 * c + 1].z, v[2 * c + 1].w};
+                    uint32_t hi[4], lo[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) u[i] = f16x2(bf16_lo(u[i]) * up, bf16_hi(u[i]) * up);
-                    *reinterpret_cast<uint4*>(smem + tile_off(m, 8 * hf + c, kQHalf)) = make_uint4(u[0], u[1], u[2], u[3]);
+                    for (int i = 0; i < 4; ++i)
+                        split4(bf16_lo(u[2 * i]) * up, bf16_hi(u[2 * i]) * up, bf16_lo(u[2 * i + 1]) * up,
+                               bf16_hi(u[2 * i + 1]) * up, hi[i], lo[i]);
+                    const uint32_t at = tile_off(m, 4 * hf + c, 0);
+                    *reinterpret_cast<uint4*>(smem + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4*>(smem + kQHalf + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
             }
             fence_async_smem();
             __syncwarp();
             if (lane == 0) bar_arrive(B(kQOp));
         };
-        // K of tile k: its raw stage has landed, and S k - 1 has read the operand.
-        auto convert_k = [&](int k) {
-            const int s = k % kNS;
-            wait(kKFull + s, k / kNS);
-            convert_tile(smem + kRawOff + s * kRawBytes, smem + kKVOff, kTok);
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                bar_arrive(B(kKEmpty + s));
-                bar_arrive(B(kKOp));
-            }
-        };
 
         Seg sg, nx;
         bool has = w.next(a, sg);
-        if (kFp8 && has) {
-            convert_k(0);
-            convert_q(0, sg);
-        }
+        if (kFp8 && has) convert_q(0, sg);
         int seg = 0;
         for (int k0 = 0; has; ++seg) {
             const bool has_next = w.next(a, nx);  // (early: its loads overlap the first S)
@@ -709,7 +718,6 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                 const int visible = sg.end - (sg.tile + t) * kTok;  // of this tile, the same for every row
                 wait(kSFull + s, k / kNS);
                 fence_after();
-                if (kFp8 && (t + 1 < sg.n || has_next)) convert_k(k + 1);  // (so that S k + 1 runs beside this softmax)
                 const uint32_t sa = tmem + lane_off + static_cast<uint32_t>(s * kTok);
                 bool rescale = false;
                 float alpha = 1.f;
@@ -735,18 +743,18 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                             if (i < seen) mx = fmaxf(mx, __uint_as_float(v[i]) * qk);
                     }
                     // Lazy base: it moves (and O and l are rescaled) only when
-                    // a row's maximum grew by more than 8; only then do the two
+                    // a row's maximum grew by more than the slack; only then do the two
                     // threads of a row exchange theirs.  The rendezvous also
                     // keeps P off the scores that the partner has yet to read.
-                    if (pair_any(pair, m < nv && (mx > m_used + 8.f || m_used == -INFINITY))) {
+                    if (pair_any(pair, m < nv && (mx > m_used + slack_of<kFp8>() || m_used == -INFINITY))) {
                         ex[hf * kRows + m] = mx;
                         pair_sync(pair);
                         const float m_new = fmaxf(m_used, fmaxf(mx, ex[(hf ^ 1) * kRows + m]));
-                        rescale = m < nv && m_used != -INFINITY && m_new > m_used + 8.f;
+                        rescale = m < nv && m_used != -INFINITY && m_new > m_used + slack_of<kFp8>();
                         alpha = rescale ? ex2(m_used - m_new) : 1.f;
                         if (rescale || m_used == -INFINITY) m_used = m_new;
                     }
-                    const float base = m_used == -INFINITY ? 0.f : m_used;
+                    const float base = m_used == -INFINITY ? 0.f : m_used - weight_shift_of<kFp8>();
                     uint32_t pk[16];
                     float lt = 0.f;
                     if (seen >= 32 || qk > 0.f) {
@@ -757,7 +765,8 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                             fma2(x0, x1, __uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), qk, qk, -base, -base);
                             const float p0 = ex2(x0), p1 = ex2(x1);
                             add2(l0, l1, l0, l1, p0, p1);
-                            pk[i] = kFp8 ? f16x2(p0, p1) : bf16x2(p0, p1);
+                            if constexpr (kFp8) v[2 * i] = __float_as_uint(p0), v[2 * i + 1] = __float_as_uint(p1);
+                            else pk[i] = bf16x2(p0, p1);
                         }
                         lt = l0 + l1;
                     } else {
@@ -766,11 +775,23 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                             const float p0 = 2 * i < seen ? ex2(fmaf(__uint_as_float(v[2 * i]), qk, -base)) : 0.f;
                             const float p1 = 2 * i + 1 < seen ? ex2(fmaf(__uint_as_float(v[2 * i + 1]), qk, -base)) : 0.f;
                             lt += p0 + p1;
-                            pk[i] = kFp8 ? f16x2(p0, p1) : bf16x2(p0, p1);
+                            if constexpr (kFp8) v[2 * i] = __float_as_uint(p0), v[2 * i + 1] = __float_as_uint(p1);
+                            else pk[i] = bf16x2(p0, p1);
                         }
                     }
                     l = l * alpha + lt;
-                    tmem_st16(sa + 16 * hf, pk);
+                    if constexpr (kFp8) {  // columns 0-15 of the buffer: high terms of tokens 0-63; 16-31: low terms
+                        uint32_t hi[8], lo[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            split4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]), __uint_as_float(v[4 * i + 2]),
+                                   __uint_as_float(v[4 * i + 3]), hi[i], lo[i]);
+                        tmem_st8(sa + 8 * hf, hi);
+                        tmem_st8(sa + 16 + 8 * hf, lo);
+                        asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
+                    } else {
+                        tmem_st16(sa + 16 * hf, pk);
+                    }
                     // S k was issued after PV k - 2 had finished, and PV k + 1 cannot
                     // finish before P k + 1 is signalled, so a parity wait for PV
                     // k - 1, or for PV k at the end, is unambiguous.
@@ -788,19 +809,12 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                         }
                     }
                 }
-                if constexpr (kFp8) {
-                    // V k, once PV k - 1 has read the operand before it (rows past the last token: zero)
+                if (visible < kTok) {  // V rows past the last token: zero (stale or unwritten rows could hold NaN)
                     wait(kVFull + s, k / kNS);
-                    if (k > 0) wait(kPvDone + (k + kNS - 1) % kNS, (k - 1) / kNS);
-                    convert_tile(smem + kRawOff + (kNS + s) * kRawBytes, smem + kKVOff + 2 * kHalfBytes, visible);
-                    fence_async_smem();
-                    __syncwarp();
-                    if (lane == 0) bar_arrive(B(kVEmpty + s));
-                } else if (visible < kTok) {  // V rows past the last token: zero (stale or unwritten rows could hold NaN)
-                    wait(kVFull + s, k / kNS);
-                    uint8_t* vs = smem + kKVOff + s * kStageBytes + 2 * kHalfBytes;
+                    uint8_t* vs = smem + kKVOff + (kFp8 ? (2 * s + 1) * kRawBytes : s * kStageBytes + 2 * kHalfBytes);
+                    constexpr int kHalves = kFp8 ? 1 : 2;
                     const int nz = kTok - visible;
-                    for (int e = threadIdx.x; e < 2 * nz * 8; e += kSoftmax) {  // whole 128-byte rows: any swizzle
+                    for (int e = threadIdx.x; e < kHalves * nz * 8; e += kSoftmax) {  // whole 128-byte rows: any swizzle
                         const int h2 = e / (nz * 8), rem = e % (nz * 8);
                         *reinterpret_cast<uint4*>(vs + h2 * kHalfBytes + (visible + rem / 8) * 128 + (rem % 8) * 16) =
                             make_uint4(0u, 0u, 0u, 0u);
@@ -849,7 +863,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                         }
                     }
                 }
-                if (m < nv && hf == 0) (sg.own ? a.own_lse : a.pre_lse)[row0 + lane] = l > 0.f ? m_used + log2f(l) : -INFINITY;
+                if (m < nv && hf == 0) (sg.own ? a.own_lse : a.pre_lse)[row0 + lane] = l > 0.f ? m_used - weight_shift_of<kFp8>() + log2f(l) : -INFINITY;
             } else if (lane == 0) {
                 bar_arrive(B(kOFree));
             }

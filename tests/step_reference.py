@@ -8,13 +8,15 @@ HALF = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8}  # half a step, re
 
 
 def attention(q, k_pool, v_pool, tables, lens, scale, k_scale=1.0, v_scale=1.0):
-    """(out, mass): softmax(scale q K^T) V per sequence in 64 bits, and the
-    same weights over |V| (what a relative error of each weight can move)."""
+    """(out, mass, floor): softmax(scale q K^T) V per sequence in 64 bits, the
+    same weights over |V| (what a relative error of each weight can move), and
+    the largest weight times the sum of |V|."""
     B, Hq, D = q.shape
     k_pool, v_pool = k_pool.double(), v_pool.double()
     _, Hk, bs, _ = k_pool.shape
     out = torch.zeros(B, Hq, D, dtype=torch.float64)
     mass = torch.zeros(B, Hq, D, dtype=torch.float64)
+    floor = torch.zeros(B, Hq, D, dtype=torch.float64)
     for b, L in enumerate(lens):
         if L == 0:
             continue
@@ -25,8 +27,8 @@ def attention(q, k_pool, v_pool, tables, lens, scale, k_scale=1.0, v_scale=1.0):
             k = k_pool[blk, g, off] * k_scale
             v = v_pool[blk, g, off] * v_scale
             w = torch.softmax(k @ q[b, h].double() * scale, 0)
-            out[b, h], mass[b, h] = w @ v, w @ v.abs()
-    return out, mass
+            out[b, h], mass[b, h], floor[b, h] = w @ v, w @ v.abs(), w.max() * v.abs().sum(0)
+    return out, mass, floor
 
 
 def norm_rope(x, weight, eps, cos_sin, positions, sections, interleaved):
@@ -92,14 +94,21 @@ def release(tables, lens, finished, keep, ring, free_state, bs):
     return out, [head, count]
 
 
-def attention_bound(out, mass, kv="bf16"):
-    """|error| of the tensor-core design: every weight is rounded to BF16, with
-    FP8 pools to FP16 (half a step of its own size: at most that share of
-    `mass`), the output rounded once to BF16; scores, sums and 2^x in fp32 add up
-    to well under 2^-13 of `mass` (128-term dot products of values near 4: 128 x
-    2^-24 x 16 in the exponent)."""
-    weight, h = (2.0 ** -11 if kv == "fp8" else 2.0 ** -8), HALF[torch.bfloat16]
-    return weight * mass + h * (out.abs() + weight * mass) + 2.0 ** -13 * mass
+def attention_bound(out, mass, kv="bf16", floor=0.0):
+    """|error| of the tensor-core design.  Every weight is rounded to BF16 (half
+    a step: at most 2^-8 of it), with FP8 pools to two E4M3 terms (2^-4 of the
+    weight, then 2^-4 of the rest: 2^-8 again, and 2^-11 for the FP16 between; at
+    least 2^-17 of the row's largest weight, where the low term is subnormal:
+    `floor` is that weight times the sum of |V|).  The output is rounded once to
+    BF16.  Scores, sums and 2^x in fp32, and FP8's query split (exact but for
+    elements below 2^-10 of a row's largest, which are off by 2^-18 of it), add
+    up to well under 2^-13 of `mass` (128-term dot products of values near 4:
+    128 x 2^-24 x 16 in the exponent; the split: 2^-18 x 3 x 128 x 0.09)."""
+    h = HALF[torch.bfloat16]
+    weight = h * mass
+    if kv == "fp8":
+        weight = weight + 2.0 ** -11 * mass + 2.0 ** -17 * floor
+    return weight + h * (out.abs() + weight) + 2.0 ** -13 * mass
 
 
 def scale_for(d):

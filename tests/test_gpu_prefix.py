@@ -77,10 +77,10 @@ class Batch:
         return ref.attention(self.q, self.k, self.v, self.tables, self.lens, self.scale, self.k_scale, self.v_scale)
 
     def check(self, out, design):
-        want, mass = self.reference()
+        want, mass, floor = self.reference()
         err = (out.cpu().double() - want).abs()
         if design == "tc":
-            bound = ref.attention_bound(want, mass, self.kv)
+            bound = ref.attention_bound(want, mass, self.kv, floor)
         else:  # the designs of decode attention, within its own tolerance
             bound = TOL[self.kv] * (1.0 + want.abs())
         bad = ~(err <= bound)
@@ -160,10 +160,10 @@ def test_prefix_growing_scores_rescale(kv):
     with torch.no_grad():
         bt.q = (bt.q.float() * 6).to(bt.q.dtype)
     out = bt.run()
-    want, mass = bt.reference()
+    want, mass, floor = bt.reference()
     if bt.design() == "tc":
         # scores six times as wide: 6 x the exponent's error
-        bound = ref.attention_bound(want, mass, kv) + 5 * 2.0 ** -13 * mass
+        bound = ref.attention_bound(want, mass, kv, floor) + 5 * 2.0 ** -13 * mass
         assert ((out.cpu().double() - want).abs() <= bound).all()
     else:
         assert ((out.cpu().double() - want).abs() <= 6 * TOL[kv] * (1 + want.abs())).all()
@@ -196,7 +196,7 @@ def test_prefix_agrees_with_decode_attention(shape):
     out = bt.run()
     dec = pk.paged_decode_attention(bt.q.cuda(), bt.pool, 1, bt.tables.cuda(),
                                     torch.tensor(lens, dtype=torch.int32).cuda(), bt.max_len, bt.scale)
-    want, mass = bt.reference()
+    want, mass, floor = bt.reference()
     # both within their own bounds of the same value
     assert ((out.double() - dec.double()).abs().cpu() <= ref.attention_bound(want, mass) + TOL["bf16"] * (1 + want.abs())).all()
     for algo in ("mma", "simt"):
@@ -227,6 +227,19 @@ def test_prefix_fp8_nan_codes_stay_nan():
     assert out[1, :4, 7].isnan().all()
     keep = torch.ones_like(out, dtype=torch.bool)
     keep[1, :4, 7] = False
+    assert torch.equal(out[keep], good[keep])
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_prefix_infinite_queries_stay_in_their_row(kv, bad):
+    bt = Batch((300, 310, 320), [(0, 3, 256)], seed=4, kv=kv)
+    good = bt.run()
+    bt.q[1, 2, 5] = bad
+    out = bt.run()
+    assert out[1, 2].isnan().all()
+    keep = torch.ones_like(out, dtype=torch.bool)
+    keep[1, 2] = False
     assert torch.equal(out[keep], good[keep])
 
 

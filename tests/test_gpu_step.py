@@ -450,9 +450,9 @@ def test_decode_loop_of_the_step_operators(captured, kv):
         want_lens = [prompt + i + 1 if i < 12 or b != 2 else i - 11 for b in range(B)]
         assert lens == want_lens and pool.errors() == 0
         raw = (lambda x: x.view(torch.float8_e4m3fn)) if kv == "fp8" else (lambda x: x)
-        want, mass = ref.attention(q_rot.cpu(), raw(pool.k[0].cpu()), raw(pool.v[0].cpu()), tables.cpu(), lens, scale,
+        want, mass, floor = ref.attention(q_rot.cpu(), raw(pool.k[0].cpu()), raw(pool.v[0].cpu()), tables.cpu(), lens, scale,
                                    pool.k_scale, pool.v_scale)
-        bound = ref.attention_bound(want, mass) if kv == "bf16" else 2e-2 * (1 + want.abs())
+        bound = ref.attention_bound(want, mass, kv, floor)
         ok = (attn.cpu().double() - want).abs() <= bound
         assert bool(ok.all()), i
         if i == 11:  # request 2 finishes (its prompt's blocks stay) and a new one starts from nothing
