@@ -25,9 +25,9 @@
 // The tile pipeline has 12 warps:
 //  * two TMA producers, for K and for V: one box {64 columns, bs rows, 1 half}
 //    per KV block and half, 128-byte swizzled: the K-major operand layout for K
-//    and the MN-major one for V; the K producer also fetches a unit's Q rows;
-//  * two MMA threads: S = Q K^T (M 128, N 64 tokens, K 128) into one of two
-//    TMEM buffers, a tile ahead of the softmax, and O += P V (N 128, K 64).
+//    and the MN-major one for V;
+//  * two MMA threads: S = Q K^T (M 128, N 64 tokens, K 128), a tile ahead of the
+//    softmax (and the copies of Q), and O += P V (N 128, K 64).
 //    Their twelve instructions a tile set the pace of shared tiles; one thread
 //    for both spent as long between them, on barriers, as issuing them;
 //  * eight softmax warps, two threads per row (= TMEM lane): base 2, P back to
@@ -60,21 +60,31 @@ constexpr int kThreads = kSoftmax + 128;
 constexpr int kRows = kPrefixRows;
 constexpr int kTok = 64;
 constexpr int kDim = 128;
-constexpr int kNS = 2;                        // stages of each ring, and score buffers
+constexpr int kNS = 2;                        // P buffers, and stages of the BF16 rings
+constexpr int kMaxStages = 4;
+template <bool kFp8>
+constexpr int stages_of() { return kFp8 ? kMaxStages : kNS; }  // of the K ring, and of the V ring: 64 KB both ways
 constexpr int kQHalf = kRows * 128;           // one 64-column half of the Q tile
 constexpr int kHalfBytes = kTok * 128;        // one 64-column half of a K or V tile
 constexpr int kKVOff = 2 * kQHalf;
 constexpr int kStageBytes = 4 * kHalfBytes;   // K + V
 constexpr int kRawBytes = kTok * kDim;        // FP8 pools: a K or V tile, [64 rows][128 bytes]
+static_assert(kNS * kStageBytes == kMaxStages * 2 * kRawBytes, "one ring size");
 constexpr int kAlignSlack = 1024;
 static_assert(12 * kPrefixMaxSeqs + 24 * kPrefixMaxGroups <= kNS * kStageBytes, "the plan fits into the ring");
+// Tensor memory: the scores of one tile, two P buffers, O.  The softmax takes the
+// scores to registers at once, so S k + 1 need not wait for anything behind that
+// (with P written over its scores in one of two score buffers, S k + 1 waited
+// for PV k - 1, and a tile took 1.2 us instead of SEE).
 constexpr uint32_t kTmemCols = 256;
-constexpr uint32_t kOCol = kNS * kTok;
+constexpr uint32_t kPCol = kTok, kPCols = kTok / 2;
+constexpr uint32_t kOCol = kPCol + kNS * kPCols;
+static_assert(kOCol + kDim == kTmemCols, "tensor memory");
 
-enum Bar { kQReady, kOFree, kDone, kSFull, kPFull = kSFull + kNS, kPvDone = kPFull + kNS, kKFull = kPvDone + kNS,
-           kVFull = kKFull + kNS,
-           kQOp = kVFull + kNS,  // FP8 pools: Q split into E4M3 terms
-           kNumBars };
+enum Bar { kQReady, kQFree, kOFree, kSRead, kDone, kSFull, kPFull = kSFull + kNS, kPvDone = kPFull + kNS, kKFull = kPvDone + kNS,
+           kVFull = kKFull + kMaxStages,
+           // FP8 pools: Q split into E4M3 terms, stages free (BF16 ones are by S done and PV done)
+           kQOp = kVFull + kMaxStages, kKEmpty, kVEmpty = kKEmpty + kMaxStages, kNumBars = kVEmpty + kMaxStages };
 constexpr int kBarOff = kKVOff + kNS * kStageBytes;
 constexpr int kExOff = kBarOff + (8 * kNumBars + 8 + 63) / 64 * 64;  // the two threads of a row meet here: maxima
 constexpr int kSumOff = kExOff + 2 * kRows * 4;                        // and sums, [2][kRows] floats each
@@ -143,11 +153,11 @@ __device__ __forceinline__ void split4(float x0, float x1, float x2, float x3, u
         : "f"(x0), "f"(x1), "f"(x2), "f"(x3));
 }
 // Slack of the running maximum (log2), and the power of two that E4M3 weights
-// are scaled by: 2^(7 + 1) stays below 448.
+// are scaled by: 2^(5 + 3) stays below 448.
 template <bool kFp8>
-constexpr float slack_of() { return kFp8 ? 1.f : 8.f; }
+constexpr float slack_of() { return kFp8 ? 3.f : 8.f; }
 template <bool kFp8>
-constexpr float weight_shift_of() { return kFp8 ? 7.f : 0.f; }
+constexpr float weight_shift_of() { return kFp8 ? 5.f : 0.f; }
 
 // Rendezvous of the two warps that share 32 rows (named barrier 1 + id), and
 // with it: does any of their threads say yes?
@@ -466,7 +476,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kNumBars; ++i)
-            bar_init(B(i), ((i >= kPFull && i < kPFull + kNS) || i == kOFree || i == kQOp) ? kSoftmaxWarps
+            bar_init(B(i), ((i >= kPFull && i < kPFull + kNS) || i == kOFree || i == kSRead || i == kQOp) ? kSoftmaxWarps
                                                                                            : (i == kDone ? 2u : 1u));
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
@@ -494,14 +504,18 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
 
     if (warp == kWarpK || warp == kWarpV) {
         // ------------------------------------------------ producers: K, V
-        // Stage s is freed by the completion that signals score buffer s: S
-        // done for K, PV done for V.
+        // A stage is freed by the completion of the products that read it: S
+        // done for K, PV done for V, where there are as many stages as P buffers
+        // (a commit less for the MMA threads, who set the pace), else by a barrier
+        // of its own.
+        constexpr int kSt = stages_of<kFp8>();
         const bool is_v = warp == kWarpV;
         const CUtensorMap* map = is_v ? &tmv : &tmk;
-        const int full0 = is_v ? kVFull : kKFull, empty0 = is_v ? kPvDone : kSFull;
+        const int full0 = is_v ? kVFull : kKFull;
+        const int empty0 = kSt == kNS ? (is_v ? kPvDone : kSFull) : (is_v ? kVEmpty : kKEmpty);
         const int bs = a.block_size;
         const int64_t layer_blk0 = static_cast<int64_t>(a.layer) * a.num_blocks;
-        int k = 0, segs = 0;
+        int k = 0;
         bool ok = true;
         Seg sg, nx;
         bool has = w.next(a, sg);
@@ -509,7 +523,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
             const bool has_next = w.next(a, nx);  // (early: its loads overlap this segment)
             int cache = 0, cache_base = INT_MIN / 2;  // 32 table entries, one per lane
             for (int t = 0; t < sg.n && ok; ++t, ++k) {
-                const int s = k % kNS;
+                const int s = k % kSt;
                 const int tok0 = (sg.tile + t) * kTok, n = min(kTok, sg.end - tok0), nblk = (n + bs - 1) / bs;
                 const int idx0 = tok0 / bs;
                 if (idx0 + nblk > cache_base + 32) {
@@ -518,7 +532,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                     cache = idx < a.max_blocks ? __ldg(a.tables + static_cast<size_t>(sg.row) * a.max_blocks + idx) : 0;
                 }
                 if (__any_sync(0xFFFFFFFFu, *abort_flag != 0) ||
-                    (k >= kNS && !bar_wait_warp(B(empty0 + s), ((k / kNS) - 1) & 1))) {
+                    (k >= kSt && !bar_wait_warp(B(empty0 + s), ((k / kSt) - 1) & 1))) {
                     ok = false;
                     break;
                 }
@@ -538,21 +552,6 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                     if constexpr (kFp8) tma_2d(dst0 + kb * bs * 128, map, 0, y, B(full0 + s));
                     else tma_3d(dst0 + hf * kHalfBytes + kb * bs * 128, map, 0, y, hf, B(full0 + s));
                 }
-                if (t == 0 && !is_v) {
-                    // The segment's Q rows, once the last S of the one before has read its own.
-                    if (k > 0 && !bar_wait_warp(B(kSFull + (k - 1) % kNS), ((k - 1) / kNS) & 1)) {
-                        ++k;
-                        ok = false;
-                        break;
-                    }
-                    if (lane == 0)
-                        bar_expect_tx(B(kQReady), static_cast<uint32_t>((sg.own ? 1 : a.seqs_per_tile) * a.gh * kDim * 2));
-                    __syncwarp();
-                    if (lane < 2)
-                        tma_4d(sbase + lane * kQHalf, sg.own ? &tmq_own : &tmq_group, 0, sg.head * a.gh, sg.seq0, lane,
-                               B(kQReady));
-                    ++segs;
-                }
             }
             sg = nx;
             has = has_next;
@@ -560,30 +559,38 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
         if (!ok && lane == 0) fail();
         // drain: the copies in flight land before the CTA frees anything
         if (lane == 0)
-            for (int j = k - 1; j >= 0 && j >= k - kNS; --j)
-                if (!bar_wait(B(full0 + j % kNS), (j / kNS) & 1)) fail();
-        if (lane == 0 && segs > 0 && !bar_wait(B(kQReady), (segs - 1) & 1)) fail();
+            for (int j = k - 1; j >= 0 && j >= k - kSt; --j)
+                if (!bar_wait(B(full0 + j % kSt), (j / kSt) & 1)) fail();
     } else if (warp == kWarpS) {
         // ----------------------------------------------------- S = Q K^T
         if (lane == 0) {
             bool ok = true;
             const uint64_t dq = sdesc(sbase, 16);
             const uint64_t dk0 = sdesc(sbase + kKVOff, 16);
+            constexpr int kSt = stages_of<kFp8>();
             Seg sg;
-            int k = 0;
-            for (int seg = 0; ok && w.next(a, sg); ++seg) {
+            int k = 0, seg = 0;
+            for (; ok && w.next(a, sg); ++seg) {
+                // This segment's Q rows, once the last S of the one before has read its own.
+                if (seg > 0 && !bar_wait(B(kQFree), (seg - 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+                bar_expect_tx(B(kQReady), static_cast<uint32_t>((sg.own ? 1 : a.seqs_per_tile) * a.gh * kDim * 2));
+                for (int h2 = 0; h2 < 2; ++h2)
+                    tma_4d(sbase + h2 * kQHalf, sg.own ? &tmq_own : &tmq_group, 0, sg.head * a.gh, sg.seq0, h2, B(kQReady));
                 for (int t = 0; t < sg.n; ++t, ++k) {
-                    const int s = k % kNS;
-                    // this segment's Q, K k, and a score buffer whose P has been multiplied (PV k - 2)
+                    const int s = k % kNS, st = k % kSt;
+                    // Q (FP8: split), K k, and S k - 1 taken to registers
                     if (*abort_flag || (t == 0 && !bar_wait(B(kFp8 ? kQOp : kQReady), seg & 1)) ||
-                        !bar_wait(B(kKFull + s), (k / kNS) & 1) ||
-                        (k >= kNS && !bar_wait(B(kPvDone + s), (k / kNS - 1) & 1))) {
+                        !bar_wait(B(kKFull + st), (k / kSt) & 1) ||
+                        (k > 0 && !bar_wait(B(kSRead), (k - 1) & 1))) {
                         ok = false;
                         break;
                     }
                     fence_after();
-                    const uint64_t dk = dk0 + static_cast<uint64_t>((s * (kFp8 ? 2 * kRawBytes : kStageBytes)) >> 4);
-                    const uint32_t sb = tmem + static_cast<uint32_t>(s * kTok);
+                    const uint64_t dk = dk0 + static_cast<uint64_t>((st * (kFp8 ? 2 * kRawBytes : kStageBytes)) >> 4);
+                    const uint32_t sb = tmem;
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks) {  // 16 columns a step; FP8: 32, first of Q's high terms, then of the low ones
                         const uint32_t kin = (ks & 3) * 32;
@@ -593,9 +600,14 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                                  idesc(kTok, 0), ks > 0 ? 1u : 0u);
                     }
                     mma_commit(B(kSFull + s));
+                    if constexpr (kSt != kNS) mma_commit(B(kKEmpty + st));
+                    if (t == sg.n - 1) mma_commit(B(kQFree));
                 }
             }
-            if (!ok) fail();
+            if (!ok) {
+                fail();
+                if (seg > 0) bar_wait(B(kQReady), (seg - 1) & 1);  // (no copy of Q may land after the CTA has gone)
+            }
             mma_commit(B(kDone));  // completes once every MMA this thread issued has finished
             if (!bar_wait(B(kDone), 0)) fail();
         }
@@ -605,21 +617,22 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
         if (lane == 0) {
             bool ok = true;
             const uint64_t dv0 = sdesc(sbase + kKVOff + (kFp8 ? kRawBytes : 2 * kHalfBytes), kHalfBytes);
+            constexpr int kSt = stages_of<kFp8>();
             Seg sg;
             int k = 0;
             for (int seg = 0; ok && w.next(a, sg); ++seg) {
                 for (int t = 0; t < sg.n; ++t, ++k) {
-                    const int s = k % kNS;
+                    const int s = k % kNS, st = k % kSt;
                     // V k, P k, and for a new segment an O that has been read out
-                    if (*abort_flag || !bar_wait(B(kVFull + s), (k / kNS) & 1) ||
+                    if (*abort_flag || !bar_wait(B(kVFull + st), (k / kSt) & 1) ||
                         !bar_wait(B(kPFull + s), (k / kNS) & 1) ||
                         (t == 0 && seg > 0 && !bar_wait(B(kOFree), (seg - 1) & 1))) {
                         ok = false;
                         break;
                     }
                     fence_after();
-                    const uint64_t dv = dv0 + static_cast<uint64_t>((s * (kFp8 ? 2 * kRawBytes : kStageBytes)) >> 4);
-                    const uint32_t pb = tmem + static_cast<uint32_t>(s * kTok);
+                    const uint64_t dv = dv0 + static_cast<uint64_t>((st * (kFp8 ? 2 * kRawBytes : kStageBytes)) >> 4);
+                    const uint32_t pb = tmem + kPCol + static_cast<uint32_t>(s) * kPCols;
 #pragma unroll
                     for (int ks = 0; ks < kTok / 16; ++ks) {  // 16 tokens a step; FP8: 32, of P's high, then of its low terms
                         const uint32_t acc = t > 0 || ks > 0 ? 1u : 0u;
@@ -627,6 +640,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                         else mma_bf16_ta(tmem + kOCol, pb + 8 * ks, dv + ((ks * 16 * 128) >> 4), idesc(kDim, 1), acc);
                     }
                     mma_commit(B(kPvDone + s));
+                    if constexpr (kSt != kNS) mma_commit(B(kVEmpty + st));
                 }
             }
             if (!ok) fail();
@@ -716,14 +730,19 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
             for (int t = 0; t < sg.n; ++t) {
                 const int k = k0 + t, s = k % kNS;
                 const int visible = sg.end - (sg.tile + t) * kTok;  // of this tile, the same for every row
-                wait(kSFull + s, k / kNS);
+                // S k, and (odd lanes) the P buffer that PV k - 2 has read
+                const bool odd = (lane & 1) != 0 && k >= kNS;
+                wait(odd ? kPvDone + s : kSFull + s, odd ? k / kNS - 1 : k / kNS);
                 fence_after();
-                const uint32_t sa = tmem + lane_off + static_cast<uint32_t>(s * kTok);
+                const uint32_t sa = tmem + lane_off, pa = sa + kPCol + static_cast<uint32_t>(s) * kPCols;
                 bool rescale = false;
                 float alpha = 1.f;
                 if (busy) {
                     uint32_t v[32];
                     tmem_ld32(sa + 32 * hf, v);
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(B(kSRead));
                     const int seen = visible - 32 * hf;  // of this thread's 32 tokens
                     float mx = -INFINITY;
                     if (qk > 0.f) {
@@ -744,8 +763,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                     }
                     // Lazy base: it moves (and O and l are rescaled) only when
                     // a row's maximum grew by more than the slack; only then do the two
-                    // threads of a row exchange theirs.  The rendezvous also
-                    // keeps P off the scores that the partner has yet to read.
+                    // threads of a row exchange theirs.
                     if (pair_any(pair, m < nv && (mx > m_used + slack_of<kFp8>() || m_used == -INFINITY))) {
                         ex[hf * kRows + m] = mx;
                         pair_sync(pair);
@@ -786,13 +804,13 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                         for (int i = 0; i < 8; ++i)
                             split4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]), __uint_as_float(v[4 * i + 2]),
                                    __uint_as_float(v[4 * i + 3]), hi[i], lo[i]);
-                        tmem_st8(sa + 8 * hf, hi);
-                        tmem_st8(sa + 16 + 8 * hf, lo);
+                        tmem_st8(pa + 8 * hf, hi);
+                        tmem_st8(pa + 16 + 8 * hf, lo);
                         asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
                     } else {
-                        tmem_st16(sa + 16 * hf, pk);
+                        tmem_st16(pa + 16 * hf, pk);
                     }
-                    // S k was issued after PV k - 2 had finished, and PV k + 1 cannot
+                    // This warp has waited for PV k - 2 and k - 3, and PV k + 1 cannot
                     // finish before P k + 1 is signalled, so a parity wait for PV
                     // k - 1, or for PV k at the end, is unambiguous.
                     if (__any_sync(0xFFFFFFFFu, rescale)) {
@@ -808,10 +826,14 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                             tmem_st32(oa, o);
                         }
                     }
+                } else if (lane == 0) {
+                    bar_arrive(B(kSRead));
                 }
                 if (visible < kTok) {  // V rows past the last token: zero (stale or unwritten rows could hold NaN)
-                    wait(kVFull + s, k / kNS);
-                    uint8_t* vs = smem + kKVOff + (kFp8 ? (2 * s + 1) * kRawBytes : s * kStageBytes + 2 * kHalfBytes);
+                    constexpr int kSt = stages_of<kFp8>();
+                    const int st = k % kSt;
+                    wait(kVFull + st, k / kSt);
+                    uint8_t* vs = smem + kKVOff + (kFp8 ? (2 * st + 1) * kRawBytes : st * kStageBytes + 2 * kHalfBytes);
                     constexpr int kHalves = kFp8 ? 1 : 2;
                     const int nz = kTok - visible;
                     for (int e = threadIdx.x; e < kHalves * nz * 8; e += kSoftmax) {  // whole 128-byte rows: any swizzle

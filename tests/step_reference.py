@@ -98,7 +98,7 @@ def attention_bound(out, mass, kv="bf16", floor=0.0):
     """|error| of the tensor-core design.  Every weight is rounded to BF16 (half
     a step: at most 2^-8 of it), with FP8 pools to two E4M3 terms (2^-4 of the
     weight, then 2^-4 of the rest: 2^-8 again, and 2^-11 for the FP16 between; at
-    least 2^-17 of the row's largest weight, where the low term is subnormal:
+    least 2^-15 of the row's largest weight, where the low term is subnormal:
     `floor` is that weight times the sum of |V|).  The output is rounded once to
     BF16.  Scores, sums and 2^x in fp32, and FP8's query split (exact but for
     elements below 2^-10 of a row's largest, which are off by 2^-18 of it), add
@@ -107,7 +107,7 @@ def attention_bound(out, mass, kv="bf16", floor=0.0):
     h = HALF[torch.bfloat16]
     weight = h * mass
     if kv == "fp8":
-        weight = weight + 2.0 ** -11 * mass + 2.0 ** -17 * floor
+        weight = weight + 2.0 ** -11 * mass + 2.0 ** -15 * floor
     return weight + h * (out.abs() + weight) + 2.0 ** -13 * mass
 
 

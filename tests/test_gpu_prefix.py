@@ -345,3 +345,15 @@ def test_prefix_more_sequences_than_ctas(kv):
     bt = Batch(lens, [(0, 350, 64), (350, 700, 64)], 4, 2, seed=12, bs=64, kv=kv)
     bt.check(bt.run(), "tc")
     assert bt.pool.errors() == 0
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_prefix_many_segments_of_many_tiles(kv):
+    """Every CTA walks over several units of several tiles: the copies of K, V
+    and the next unit's Q run ahead across their borders."""
+    lens = tuple(600 + 37 * (i % 11) for i in range(56))
+    bt = Batch(lens, [(0, 30, 320), (30, 56, 448)], 16, 8, bs=64, seed=40, kv=kv)
+    bt.check(bt.run(), "tc")
+    bt.prefix.zero_()  # nothing shared: own units only
+    bt.check(bt.run(), "tc")
+    assert bt.pool.errors() == 0
