@@ -423,6 +423,8 @@ def _device_of(pool: KVPool, stream):
 
 
 def _stream_of(pool: KVPool, stream) -> int:
+    if pool.k.device.type != "cuda":
+        raise ValueError("the pool is not on a GPU")
     return _raw_stream(pool.k.device.index) if stream is None else stream.cuda_stream
 
 

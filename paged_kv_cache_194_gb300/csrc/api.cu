@@ -587,6 +587,7 @@ namespace {
 bool prefix_tc_fits(const pkv_pool* p, int num_seqs, int num_groups, int gh, int max_seq_len) {
     if ((p->d.kv_dtype != PKV_BF16 && p->d.kv_dtype != PKV_FP8_E4M3) || p->d.head_dim != 128) return false;
     if (num_seqs > kPrefixMaxSeqs || num_groups > kPrefixMaxGroups || gh > kPrefixRows) return false;
+    if (static_cast<int64_t>(num_seqs) * p->d.num_kv_heads * gh > INT32_MAX / 2) return false;  // rows are int32
     // tile counts are int32
     const int64_t tiles = (static_cast<int64_t>(max_seq_len) + kTileTokens - 1) / kTileTokens;
     return (tiles + 8) * num_seqs * p->d.num_kv_heads <= INT32_MAX / 4;
