@@ -7,8 +7,8 @@ there is no fallback.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import importlib.util
 import os
 from typing import NamedTuple, Optional, Sequence, Tuple
 
@@ -199,6 +199,9 @@ class KVPool:
         h = ctypes.c_void_p()
         _check(lib().kv_pool_create(ctypes.byref(self._desc), ctypes.byref(h)), "kv_pool_create")
         self.handle = h
+        # for the native calls
+        self.address = h.value
+        self.device_index = self.k.device.index if self.k.is_cuda else -1
 
     @property
     def tensor_bytes(self) -> int:
@@ -214,7 +217,7 @@ class KVPool:
     def close(self):
         if getattr(self, "handle", None) is not None and self.handle.value:
             lib().kv_pool_destroy(self.handle)
-            self.handle = None
+            self.handle = self.address = None
 
     def __del__(self):
         try:
@@ -379,29 +382,27 @@ def paged_multi_query_attention(q: torch.Tensor, pool: KVPool, layer: int, block
 # ------------------------------------------------------------- one decode step
 # The calls below check that every tensor lies on the pool's device and launch
 # there, whatever device is current; what they allocate belongs to the stream
-# they run on.  A decode step makes them for every layer and their kernels take
-# a few microseconds, so the checks are kept short (messages are made only when
-# one fails).
+# they run on.  Their argument checks are native (csrc_python/step_calls.cpp).
 
-def _refuse(name: str, t: torch.Tensor, dev: torch.device, dtype, shape):
-    if t.device != dev:
-        raise ValueError("%s must be on %s, the pool's device, not %s" % (name, dev, t.device))
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if shape is not None and t.shape != shape:
-        raise ValueError("%s must be of shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    raise ValueError("%s must be contiguous" % name)
+_step_module = None
 
 
-def _ptr_on(dev: torch.device, name: str, t: torch.Tensor, dtype, shape) -> int:
-    """Data pointer of a contiguous tensor of this device, dtype and shape (None: any)."""
-    if (t.is_contiguous() and t.device == dev and (dtype is None or t.dtype is dtype)
-            and (shape is None or t.shape == shape)):
-        return t.data_ptr()
-    _refuse(name, t, dev, dtype, shape)
+def _step():
+    """Load _pkvstep.so (raises if it is missing)."""
+    global _step_module
+    if _step_module is None:
+        lib()
+        path = os.path.join(HERE, "_pkvstep.so")
+        if not os.path.exists(path):
+            raise RuntimeError("_pkvstep.so is not built (run __graft_entry__.build() or "
+                               "python -m paged_kv_cache_194_gb300.build); no fallback exists")
+        spec = importlib.util.spec_from_file_location(__package__ + "._pkvstep", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _step_module = module
+    return _step_module
 
 
-_HERE = contextlib.nullcontext()
 # The current device, and (device index) -> handle of its current stream, without
 # the objects and checks of the public calls, which take longer than some of the
 # kernels below.
@@ -409,39 +410,35 @@ _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.curre
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
-def _device_of(pool: KVPool, stream):
+def _here(pool: KVPool, stream) -> bool:
+    """Whether a call needs no other device or stream than the current ones."""
+    return stream is None and (pool.device_index < 0 or pool.device_index == _current_device())
+
+
+def _on(pool: KVPool, stream):
     """Context in which the pool's device is current, and `stream` when given
     (so that allocations belong to it)."""
-    dev = pool.k.device
     if stream is not None:
-        if stream.device != dev:
-            raise ValueError("stream must be on %s, the pool's device, not %s" % (dev, stream.device))
+        if stream.device != pool.k.device:
+            raise ValueError("stream must be on %s, the pool's device, not %s" % (pool.k.device, stream.device))
         return torch.cuda.stream(stream)
-    if dev.type != "cuda" or dev.index == _current_device():
-        return _HERE
-    return torch.cuda.device(dev)
+    return torch.cuda.device(pool.k.device)
 
 
-def _stream_of(pool: KVPool, stream) -> int:
-    if pool.k.device.type != "cuda":
-        raise ValueError("the pool is not on a GPU")
-    return _raw_stream(pool.k.device.index) if stream is None else stream.cuda_stream
-
-
-def _table_width(block_tables: torch.Tensor, num_seqs: int) -> int:
-    if block_tables.dim() != 2 or block_tables.shape[0] != num_seqs:
-        raise ValueError("block_tables must be [num_seqs, max_blocks]")
-    return block_tables.shape[1]
+def _stream_handle(pool: KVPool) -> int:
+    return _raw_stream(pool.device_index) if pool.device_index >= 0 else 0
 
 
 def prefix_decode_workspace(pool: KVPool, num_seqs: int, num_groups: int, num_q_heads: int,
                             max_seq_len: int) -> Optional[torch.Tensor]:
     """A zeroed workspace for paged_prefix_decode_attention calls of this size."""
+    if not _here(pool, None):
+        with _on(pool, None):
+            return prefix_decode_workspace(pool, num_seqs, num_groups, num_q_heads, max_seq_len)
     ws = ctypes.c_size_t()
-    with _device_of(pool, None):
-        _check(lib().paged_prefix_decode_plan(pool.handle, num_seqs, num_groups, num_q_heads, max_seq_len,
-                                              ctypes.byref(ws)), "paged_prefix_decode_plan")
-        return torch.zeros(ws.value, dtype=torch.uint8, device=pool.k.device) if ws.value else None
+    _check(lib().paged_prefix_decode_plan(pool.handle, num_seqs, num_groups, num_q_heads, max_seq_len,
+                                          ctypes.byref(ws)), "paged_prefix_decode_plan")
+    return torch.zeros(ws.value, dtype=torch.uint8, device=pool.k.device) if ws.value else None
 
 
 def prefix_decode_algo(pool: KVPool, num_seqs: int, num_groups: int, num_q_heads: int, max_seq_len: int,
@@ -461,26 +458,19 @@ def paged_prefix_decode_attention(q: torch.Tensor, pool: KVPool, layer: int, blo
     """paged_decode_attention for a batch whose sequences group_offsets[g] ..
     group_offsets[g + 1] - 1 share their first prefix_lens[g] tokens (int32
     tensors [groups + 1] and [groups]): each prefix is read once per group."""
-    B, Hq, D = q.shape
-    G = prefix_lens.shape[0]
-    if D != pool.head_dim:
-        raise ValueError("q must be [num_seqs, num_q_heads, head_dim]")
-    width = _table_width(block_tables, B)
-    with _device_of(pool, stream):
-        if out is None:
-            out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        if workspace is None:
-            workspace = prefix_decode_workspace(pool, B, G, Hq, max_seq_len)
-        dev, i32 = pool.k.device, torch.int32
-        ws = _ptr_on(dev, "workspace", workspace, None, None) if workspace is not None else None
-        rc = lib().paged_prefix_decode_attention(
-            _ptr_on(dev, "q", q, None, None), _dtype_code(q.dtype), pool.handle, layer,
-            _ptr_on(dev, "block_tables", block_tables, i32, None), width, _ptr_on(dev, "seq_lens", seq_lens, i32, (B,)),
-            B, Hq, max_seq_len, _ptr_on(dev, "group_offsets", group_offsets, i32, (G + 1,)),
-            _ptr_on(dev, "prefix_lens", prefix_lens, i32, (G,)), G, scale, ALGOS[algo], ws,
-            workspace.numel() * workspace.element_size() if workspace is not None else 0,
-            _ptr_on(dev, "out", out, q.dtype, q.shape), _stream_of(pool, stream))
-    _check(rc, "paged_prefix_decode_attention")
+    if not _here(pool, stream):
+        with _on(pool, stream):
+            return paged_prefix_decode_attention(q, pool, layer, block_tables, seq_lens, max_seq_len, group_offsets,
+                                                 prefix_lens, scale, out, workspace, algo)
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if workspace is None and q.dim() == 3:
+        workspace = prefix_decode_workspace(pool, q.shape[0], prefix_lens.numel(), q.shape[1], max_seq_len)
+    rc = _step().prefix_attention(pool.address, pool.device_index, pool.head_dim, layer, q, block_tables, seq_lens,
+                                  max_seq_len, group_offsets, prefix_lens, scale, ALGOS[algo], workspace, out,
+                                  _stream_handle(pool))
+    if rc:
+        raise PkvError(rc, "paged_prefix_decode_attention")
     return out
 
 
@@ -498,9 +488,9 @@ class RopeTable:
         self.interleaved = bool(interleaved)
         if not 1 <= len(self.sections) <= 3 or min(self.sections) < 0 or 2 * sum(self.sections) != cos_sin.shape[1]:
             raise ValueError("sections must be 1 to 3 counts of pairs that sum to rotary_dim / 2")
-        self._desc = NormRopeDesc(max_pos=cos_sin.shape[0], rotary_dim=cos_sin.shape[1],
-                                  interleaved=int(self.interleaved), num_axes=len(self.sections),
-                                  sections=(ctypes.c_int32 * 3)(*self.sections))
+        # as the native call takes them: number of axes, 20 bits per section
+        self._axes = len(self.sections)
+        self._packed = sum(n << (20 * i) for i, n in enumerate(self.sections))
 
     @classmethod
     def create(cls, max_pos: int, rotary_dim: int, base: float = 10000.0, sections: Optional[Sequence[int]] = None,
@@ -513,18 +503,6 @@ class RopeTable:
         return cls(torch.cat([a.cos(), a.sin()], 1).to(torch.float32).to(device), sections, interleaved)
 
 
-def _head_rows(dev: torch.device, name: str, x: torch.Tensor, shape, dtype) -> int:
-    """Token stride (elements) of x [T, heads, head_dim], whose heads must lie one after the other."""
-    if x.shape != shape or x.dtype != dtype:
-        raise ValueError("%s must be %s %s, got %s %s" % (name, dtype, shape, x.dtype, tuple(x.shape)))
-    if x.device != dev:
-        raise ValueError("%s must be on %s, the pool's device, not %s" % (name, dev, x.device))
-    s0, s1, s2 = x.stride()
-    if s2 != 1 or (s1 != shape[2] and shape[1] > 1):
-        raise ValueError("%s: a token's heads must be contiguous" % name)
-    return s0 if shape[0] > 1 else 0
-
-
 def kv_append_norm_rope(pool: KVPool, layer: int, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                         positions: torch.Tensor, slot_mapping: torch.Tensor, rope: RopeTable,
                         q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
@@ -534,33 +512,16 @@ def kv_append_norm_rope(pool: KVPool, layer: int, q: torch.Tensor, k: torch.Tens
     q [T, Hq, D], k and v [T, Hkv, D] may be slices of one projection's rows;
     positions int32 [axes, T] (or [T] for one axis).  Returns the queries [T,
     Hq, D] in the dtype attention takes; `out` may be a contiguous q itself."""
-    if q.dim() != 3:
-        raise ValueError("q must be [T, num_q_heads, head_dim]")
-    T, Hq = q.shape[0], q.shape[1]
-    D, dev, in_dtype = pool.head_dim, pool.k.device, q.dtype
-    kv_shape = (T, pool.num_kv_heads, D)
-    qs = _head_rows(dev, "q", q, (T, Hq, D), in_dtype)
-    ks = _head_rows(dev, "k", k, kv_shape, in_dtype)
-    vs = _head_rows(dev, "v", v, kv_shape, in_dtype)
-    axes = len(rope.sections)
-    dtype = torch.float32 if pool.kv_dtype == "f32" else torch.bfloat16
-    desc = NormRopeDesc.from_buffer_copy(rope._desc)
-    desc.cos_sin = _ptr_on(dev, "cos_sin", rope.cos_sin, torch.float32, None)
-    if q_weight is not None or k_weight is not None:
-        if q_weight is None or k_weight is None:
-            raise ValueError("q_weight and k_weight go together")
-        desc.q_weight = _ptr_on(dev, "q_weight", q_weight, None, (D,))
-        desc.k_weight = _ptr_on(dev, "k_weight", k_weight, q_weight.dtype, (D,))
-        desc.weight_dtype, desc.eps = _dtype_code(q_weight.dtype), eps
-    pp = _ptr_on(dev, "positions", positions, torch.int32, (T,) if axes == 1 and positions.dim() == 1 else (axes, T))
-    psl = _ptr_on(dev, "slot_mapping", slot_mapping, torch.int64, (T,))
-    with _device_of(pool, stream):
-        if out is None:
-            out = torch.empty((T, Hq, D), dtype=dtype, device=dev)
-        rc = lib().kv_append_norm_rope(pool.handle, layer, q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                                       _dtype_code(in_dtype), qs, ks, vs, pp, psl, T, Hq, desc,
-                                       _ptr_on(dev, "out", out, dtype, (T, Hq, D)), _stream_of(pool, stream))
-    _check(rc, "kv_append_norm_rope")
+    if not _here(pool, stream):
+        with _on(pool, stream):
+            return kv_append_norm_rope(pool, layer, q, k, v, positions, slot_mapping, rope, q_weight, k_weight, eps, out)
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.float32 if pool.kv_dtype == "f32" else torch.bfloat16, device=q.device)
+    rc = _step().norm_rope(pool.address, pool.device_index, pool.num_kv_heads, pool.head_dim, pool.kv_dtype == "f32",
+                           layer, q, k, v, positions, slot_mapping, rope.cos_sin, rope._axes, rope._packed,
+                           rope.interleaved, q_weight, k_weight, eps, out, _stream_handle(pool))
+    if rc:
+        raise PkvError(rc, "kv_append_norm_rope")
     return out
 
 
@@ -588,24 +549,15 @@ def kv_tables_grow(pool: KVPool, block_tables: torch.Tensor, seq_lens: torch.Ten
     blocks from the free ring into block_tables (in place), the slot, position
     and request of every token row, the new lengths and free state.  All int32
     tensors but the slots.  `out` may hold seq_lens and free_state themselves."""
-    B = seq_lens.shape[0]
-    width = _table_width(block_tables, B)
-    dev, i32, T = pool.k.device, torch.int32, max_tokens
-    with _device_of(pool, stream):
-        if out is None:
-            out = StepTables.empty(B, T, device=dev)
-        slots, positions, token_seqs, token_offsets, granted, lens_out, state_out = out
-        rc = lib().kv_tables_grow(
-            pool.handle, _ptr_on(dev, "block_tables", block_tables, i32, None), width,
-            _ptr_on(dev, "seq_lens", seq_lens, i32, (B,)), _ptr_on(dev, "new_tokens", new_tokens, i32, (B,)), B,
-            _ptr_on(dev, "free_ring", free_ring, i32, None), free_ring.numel(),
-            _ptr_on(dev, "free_state", free_state, i32, (2,)), T,
-            _ptr_on(dev, "slot_mapping", slots, torch.int64, (T,)), _ptr_on(dev, "positions", positions, i32, (T,)),
-            _ptr_on(dev, "token_seqs", token_seqs, i32, (T,)),
-            _ptr_on(dev, "token_offsets", token_offsets, i32, (B + 1,)), _ptr_on(dev, "granted", granted, i32, (B,)),
-            _ptr_on(dev, "out.seq_lens", lens_out, i32, (B,)), _ptr_on(dev, "out.free_state", state_out, i32, (2,)),
-            _stream_of(pool, stream))
-    _check(rc, "kv_tables_grow")
+    if not _here(pool, stream):
+        with _on(pool, stream):
+            return kv_tables_grow(pool, block_tables, seq_lens, new_tokens, free_ring, free_state, max_tokens, out)
+    if out is None:
+        out = StepTables.empty(seq_lens.numel(), max_tokens, device=pool.k.device)
+    rc = _step().tables_grow(pool.address, pool.device_index, block_tables, seq_lens, new_tokens, free_ring, free_state,
+                             max_tokens, *out, _stream_handle(pool))
+    if rc:
+        raise PkvError(rc, "kv_tables_grow")
     return out
 
 
@@ -616,19 +568,14 @@ def kv_tables_release(pool: KVPool, block_tables: torch.Tensor, seq_lens: torch.
     """Return the blocks of every request with finished[b] != 0, but for the
     first keep_blocks[b] of its row, to the free ring (in place).  Returns the
     new lengths and free state; the outputs may be the inputs themselves."""
-    B = seq_lens.shape[0]
-    width = _table_width(block_tables, B)
-    dev, i32 = pool.k.device, torch.int32
-    with _device_of(pool, stream):
-        seq_lens_out = torch.empty_like(seq_lens) if seq_lens_out is None else seq_lens_out
-        free_state_out = torch.empty_like(free_state) if free_state_out is None else free_state_out
-        rc = lib().kv_tables_release(
-            pool.handle, _ptr_on(dev, "block_tables", block_tables, i32, None), width,
-            _ptr_on(dev, "seq_lens", seq_lens, i32, (B,)), _ptr_on(dev, "finished", finished, i32, (B,)),
-            _ptr_on(dev, "keep_blocks", keep_blocks, i32, (B,)) if keep_blocks is not None else None, B,
-            _ptr_on(dev, "free_ring", free_ring, i32, None), free_ring.numel(),
-            _ptr_on(dev, "free_state", free_state, i32, (2,)),
-            _ptr_on(dev, "seq_lens_out", seq_lens_out, i32, (B,)),
-            _ptr_on(dev, "free_state_out", free_state_out, i32, (2,)), _stream_of(pool, stream))
-    _check(rc, "kv_tables_release")
+    if not _here(pool, stream):
+        with _on(pool, stream):
+            return kv_tables_release(pool, block_tables, seq_lens, finished, free_ring, free_state, keep_blocks,
+                                     seq_lens_out, free_state_out)
+    seq_lens_out = torch.empty_like(seq_lens) if seq_lens_out is None else seq_lens_out
+    free_state_out = torch.empty_like(free_state) if free_state_out is None else free_state_out
+    rc = _step().tables_release(pool.address, pool.device_index, block_tables, seq_lens, finished, keep_blocks, free_ring,
+                                free_state, seq_lens_out, free_state_out, _stream_handle(pool))
+    if rc:
+        raise PkvError(rc, "kv_tables_release")
     return seq_lens_out, free_state_out
