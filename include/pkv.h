@@ -316,8 +316,9 @@ int32_t paged_decode_algo(const pkv_pool* pool, int32_t group, pkv_algo requeste
  *                 of equal content; those of one sequence are read.
  * A sequence shorter than its group's prefix is attended on its own.  Offsets
  * that do not ascend set PKV_ERRBIT_GROUP and nothing is shared; a negative
- * prefix length sets it and that group shares nothing: the results stay right.  Lengths and groups are read on the device: a captured call may be
- * replayed with other ones, within max_seq_len and num_groups.
+ * prefix length sets it and that group shares nothing: the results stay right.
+ * Lengths and groups are read on the device: a captured call may be replayed
+ * with other ones, within max_seq_len and num_groups.
  *   algo          PKV_ALGO_AUTO: the sharing design (tcgen05) where it serves
  *                 the pool, else paged_decode_attention's choice, which reads
  *                 every sequence's prefix (from L2, mostly) and looks at no
@@ -368,7 +369,7 @@ typedef struct pkv_norm_rope {
     const void* q_weight;   /* device [head_dim], 16-byte aligned; both NULL: no norm */
     const void* k_weight;
     pkv_dtype weight_dtype; /* PKV_F32 or PKV_BF16 */
-    float eps;              /* > 0 when there are weights */
+    float eps;              /* > 0 and normal when there are weights */
 } pkv_norm_rope;
 /*
  *   q, k, v       device; token t's heads are [heads][head_dim], contiguous,

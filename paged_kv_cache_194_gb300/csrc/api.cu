@@ -764,7 +764,8 @@ pkv_status kv_append_norm_rope(const pkv_pool* p, int32_t layer, const void* q, 
     if (r->q_weight) {
         if (r->weight_dtype != PKV_F32 && r->weight_dtype != PKV_BF16) return PKV_ERR_INVALID_ARG;
         if (!aligned(r->q_weight, 16) || !aligned(r->k_weight, 16)) return PKV_ERR_INVALID_ARG;
-        if (!(std::isfinite(r->eps) && r->eps > 0.f)) return PKV_ERR_INVALID_ARG;
+        // (a subnormal eps would count as zero, and a row of zeros become NaN)
+        if (!(std::isnormal(r->eps) && r->eps > 0.f)) return PKV_ERR_INVALID_ARG;
     }
     for (int64_t s : {q_stride, k_stride, v_stride})
         if (s < 0 || s % 8 != 0 || s > INT64_MAX / 8 / (num_tokens > 0 ? num_tokens : 1)) return PKV_ERR_INVALID_ARG;

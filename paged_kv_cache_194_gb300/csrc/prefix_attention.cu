@@ -45,6 +45,7 @@
 // waits for its copies and products in flight, frees its TMEM and leaves.
 #include <cuda.h>
 
+#include <atomic>
 #include <climits>
 
 #include "tc_common.cuh"
@@ -1019,15 +1020,15 @@ cudaError_t launch_tc(const PrefixArgs& a, const void* tmap_k, const void* tmap_
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    static uint64_t configured = 0;
+    static std::atomic<uint64_t> configured{0};  // a bit per device; setting the attributes twice does no harm
     if (dev < 0 || dev >= 64) return cudaErrorNotSupported;
-    if (!(configured >> dev & 1)) {
+    if (!(configured.load() >> dev & 1)) {
         e = cudaFuncSetAttribute(prefix_tc_kernel<kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         if (e == cudaSuccess)
             e = cudaFuncSetAttribute(prefix_tc_kernel<kFp8>, cudaFuncAttributePreferredSharedMemoryCarveout,
                                      cudaSharedmemCarveoutMaxShared);
         if (e != cudaSuccess) return e;
-        configured |= 1ull << dev;
+        configured.fetch_or(1ull << dev);
     }
     prefix_tc_kernel<kFp8><<<a.ctas, kThreads, kSmem, stream>>>(
         *static_cast<const CUtensorMap*>(tmap_k), *static_cast<const CUtensorMap*>(tmap_v),

@@ -2,8 +2,8 @@
 // tensors, then the C ABI.  A decode step makes these calls once or more per
 // layer and their kernels take a few microseconds: a call costs the host 3 us
 // here (5 for prefix attention's three kernels), where the same checks through
-// Python attributes made it 9 to 12.  Argument checks and marshalling only, as in binding.py: the
-// rules are its rules, what fails raises ValueError.
+// Python attributes made it 9 to 12.  Argument checks and marshalling only: what
+// fails raises ValueError.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 

@@ -114,6 +114,7 @@ def test_norm_rope_refusals(pool):
                 dict(num_axes=4), dict(sections=(63, 0, 0)), dict(num_axes=2, sections=(65, -1, 0)),
                 dict(cos_sin=None), dict(cos_sin=FAKE + 4), dict(q_weight=FAKE), dict(k_weight=FAKE),
                 dict(q_weight=FAKE, k_weight=FAKE, weight_dtype=2), dict(q_weight=FAKE, k_weight=FAKE, eps=0.0),
+                dict(q_weight=FAKE, k_weight=FAKE, eps=1e-40), dict(q_weight=FAKE, k_weight=FAKE, eps=-1e-6),
                 dict(q_weight=FAKE, k_weight=FAKE, eps=float("inf")), dict(q_weight=FAKE + 4, k_weight=FAKE)):
         assert call(rope=_rope(**bad)) == 1, bad
     # overlap of the output with an input, but for q itself laid out alike
@@ -185,6 +186,22 @@ def test_binding_checks_shapes_types_and_devices():
             pk.paged_prefix_decode_attention(**{**dict(q=qa, pool=pool, layer=0, block_tables=t, seq_lens=n,
                                                        max_seq_len=64, group_offsets=z(2), prefix_lens=z(1), scale=1.0),
                                                 **bad})
+
+    # every call reaches its last check with right arguments, and stops there: no GPU
+    for f, k in ((pk.kv_tables_grow, dict(block_tables=t, seq_lens=n, new_tokens=n, free_ring=z(8), free_state=z(2),
+                                          max_tokens=5, out=pk.StepTables.empty(3, 5, device="cpu"))),
+                 (pk.kv_tables_release, dict(block_tables=t, seq_lens=n, finished=n, free_ring=z(8), free_state=z(2),
+                                             keep_blocks=n)),
+                 (pk.paged_prefix_decode_attention, dict(q=qa, layer=0, block_tables=t, seq_lens=n, max_seq_len=64,
+                                                         group_offsets=z(2), prefix_lens=z(1), scale=1.0))):
+        with pytest.raises(ValueError, match="not on a GPU"):
+            f(pool=pool, **k)
+        # wrong kinds of arguments, and integers past 32 bits
+        for name, bad in (("seq_lens", [1, 2, 3]), ("block_tables", None), ("free_state", 7), ("layer", 2 ** 40),
+                          ("max_seq_len", "64"), ("scale", None), ("max_tokens", 2 ** 31)):
+            if name in k:
+                with pytest.raises((TypeError, ValueError, AttributeError, pk.PkvError, ctypes.ArgumentError)):
+                    f(pool=pool, **{**k, name: bad})
 
 
 def test_rope_table_angles_are_64_bit():
