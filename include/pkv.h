@@ -424,7 +424,8 @@ pkv_status kv_append_norm_rope(const pkv_pool* pool, int32_t layer, const void* 
  * max_tokens (PKV_ERRBIT_STEP).  A table or ring entry outside the pool sets
  * PKV_ERRBIT_BLOCK_ID, gives slot -1 and, from the ring, a table entry of -1.
  * A free_state that cannot be (head outside the ring, count outside 0 ..
- * ring_size) sets PKV_ERRBIT_STEP and counts as an empty list.
+ * ring_size) sets PKV_ERRBIT_STEP and counts as an empty list.  ring_size or
+ * max_tokens above 2^30 is PKV_ERR_UNSUPPORTED.
  *
  * kv_tables_release returns the blocks of every request with finished[b] != 0,
  * in table order, behind the ring's tail, and makes its length 0 (the table row

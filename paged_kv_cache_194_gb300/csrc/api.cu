@@ -648,6 +648,8 @@ int prefix_design(const pkv_pool* p, int num_seqs, int num_groups, int num_q_hea
     return design_for(p, 1, gh, 0, algo, false);
 }
 
+constexpr int32_t kMaxListed = 1 << 30;  // token rows and free blocks: their sums and places are int32
+
 int block_shift(const pkv_pool* p) { return p->d.block_size == 16 ? 4 : (p->d.block_size == 32 ? 5 : 6); }
 
 bool ranges_overlap(const void* a, size_t na, const void* b, size_t nb) {
@@ -824,6 +826,7 @@ pkv_status kv_tables_grow(const pkv_pool* p, int32_t* block_tables, int32_t max_
                           int32_t* granted, int32_t* seq_lens_out, int32_t* free_state_out, void* stream) {
     if (!p || num_seqs < 0 || max_blocks_per_seq < 1 || ring_size < 1 || max_tokens < 0) return PKV_ERR_INVALID_ARG;
     if (static_cast<int64_t>(max_blocks_per_seq) * p->d.block_size > INT32_MAX) return PKV_ERR_UNSUPPORTED;
+    if (ring_size > pkv::kMaxListed || max_tokens > pkv::kMaxListed) return PKV_ERR_UNSUPPORTED;
     if (num_seqs > 0 && (!block_tables || !seq_lens || !new_tokens || !granted || !seq_lens_out))
         return PKV_ERR_INVALID_ARG;
     if (max_tokens > 0 && (!slot_mapping || !positions || !token_seqs)) return PKV_ERR_INVALID_ARG;
@@ -864,7 +867,8 @@ pkv_status kv_tables_release(const pkv_pool* p, const int32_t* block_tables, int
                              int32_t num_seqs, int32_t* free_ring, int32_t ring_size, const int32_t* free_state,
                              int32_t* seq_lens_out, int32_t* free_state_out, void* stream) {
     if (!p || num_seqs < 0 || max_blocks_per_seq < 1 || ring_size < 1) return PKV_ERR_INVALID_ARG;
-    if (static_cast<int64_t>(max_blocks_per_seq) * p->d.block_size > INT32_MAX) return PKV_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(max_blocks_per_seq) * p->d.block_size > INT32_MAX || ring_size > pkv::kMaxListed)
+        return PKV_ERR_UNSUPPORTED;
     if (num_seqs > 0 && (!block_tables || !seq_lens || !finished || !seq_lens_out)) return PKV_ERR_INVALID_ARG;
     if (!free_ring || !free_state || !free_state_out) return PKV_ERR_INVALID_ARG;
     for (const void* x : {static_cast<const void*>(block_tables), static_cast<const void*>(seq_lens),

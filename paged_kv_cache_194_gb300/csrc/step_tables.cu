@@ -16,12 +16,17 @@
 // tail.
 //
 // A batch is at most some thousand lengths, so nothing here is bound by bytes:
-// a call costs its launch and a few dependent rounds to L2.  Hence one CTA
-// that scans 1024 requests a round (registers and shuffles, two barriers per
-// sum), writes tables and, for up to kInlineTokens token rows, the slots too;
-// a second kernel, launched to start as the first ends, fills longer slot
-// maps, one thread per token row.  (Block sizes are powers of two; with runtime
-// divisions instead of shifts the scan took four times as long.)
+// a call costs its launch, a few dependent rounds to L2, and the instructions
+// that one SM issues.  Hence one CTA that scans 1024 requests a round (both
+// sums at once, in 32 bits that saturate, one barrier), writes tables and, for
+// up to kInlineTokens token rows, the slots too; a second kernel, launched to
+// start as the first ends, fills longer slot maps, one thread per token row.
+// (Block sizes are powers of two; with runtime divisions instead of shifts the
+// scan took four times as long.)  256 requests of one token each: 3.3 us, of
+// which an empty launch is 2; 1024 requests, 128 of them prompts of up to 2048
+// tokens, 8 thousand blocks and 131 thousand rows: 11.5 us, six of them in the
+// one CTA.  Releases of a quarter of 256 requests: 4.9 us; of 4096 requests'
+// half a million blocks: 6.6 us.
 #include "device_common.cuh"
 
 namespace pkv {
@@ -31,30 +36,47 @@ constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kInlineTokens = 8192;  // token rows the scanning CTA fills itself
 constexpr int kDirect = 2;           // rows or blocks of a request that its own thread writes
+constexpr int kAhead = 8;            // blocks that a thread fetches at once
 constexpr int kFillThreads = 256;
 
-// Inclusive sum over the CTA's threads; *total gets the sum of all of them.
-__device__ __forceinline__ long long block_scan(long long v, long long* warp_sums, long long* total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// Sums end at kMost, which stands for "too many" (limits are at most 2^30): half
+// the instructions of 64-bit sums, and one SM issues them all.
+constexpr int kMost = INT32_MAX;
+__device__ __forceinline__ int sat(long long x) { return static_cast<int>(x < kMost ? x : kMost); }
+__device__ __forceinline__ int sat_add(int a, int b) {  // of values 0 .. kMost
+    return static_cast<int>(min(static_cast<unsigned>(a) + static_cast<unsigned>(b), static_cast<unsigned>(kMost)));
+}
+// Exclusive sums of N values over the CTA's threads; total[] gets the sums of
+// all of them.  (The caller has a barrier before `sums` is written again.)
+template <int N>
+__device__ __forceinline__ void block_scan(int (&v)[N], int (*sums)[kWarps], int (&total)[N]) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long x = __shfl_up_sync(0xFFFFFFFFu, v, o);
-        if (lane >= o) v += x;
+    for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const int x = __shfl_up_sync(0xFFFFFFFFu, v[e], o);
+            if (lane >= o) v[e] = sat_add(v[e], x);
+        }
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        if (lane == 31) sums[e][warp] = v[e];
+        v[e] = __shfl_up_sync(0xFFFFFFFFu, v[e], 1);
+        if (lane == 0) v[e] = 0;
     }
-    if (lane == 31) warp_sums[warp] = v;
     __syncthreads();
-    const int nw = blockDim.x >> 5;
-    const long long mine = lane < nw ? warp_sums[lane] : 0;
-    long long s = mine;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long x = __shfl_up_sync(0xFFFFFFFFu, s, o);
-        if (lane >= o) s += x;
+    for (int e = 0; e < N; ++e) {
+        int s = lane < nw ? sums[e][lane] : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xFFFFFFFFu, s, o);
+            if (lane >= o) s = sat_add(s, x);
+        }
+        total[e] = __shfl_sync(0xFFFFFFFFu, s, nw - 1);
+        const int before = __shfl_sync(0xFFFFFFFFu, s, max(warp - 1, 0));
+        if (warp > 0) v[e] = sat_add(v[e], before);
     }
-    *total = __shfl_sync(0xFFFFFFFFu, s, nw - 1);
-    const long long before = __shfl_sync(0xFFFFFFFFu, s - mine, warp);
-    __syncthreads();  // warp_sums may be written again
-    return v + before;
 }
 
 // Block sizes are powers of two: blocks that `a` tokens occupy.
@@ -64,19 +86,29 @@ __device__ __forceinline__ int sat_pos(long long p) { return p > INT32_MAX ? INT
 struct FreeRing {
     const int32_t* ring;
     int cap, head;
-    __device__ __forceinline__ int index(long long i) const {  // i <= cap, head < cap
-        const long long x = head + i;
-        return static_cast<int>(x >= cap ? x - cap : x);
+    __device__ __forceinline__ unsigned index(int i) const {  // i <= cap, head < cap
+        const unsigned x = static_cast<unsigned>(head) + static_cast<unsigned>(i), c = static_cast<unsigned>(cap);
+        return x >= c ? x - c : x;
     }
 };
 
-// A request whose rows or blocks are too many for its own thread.
+// A request of a round of the scan.
 struct Job {
-    int b, L, n, off;
+    int b, L;
     int first;   // its first entry of the free list, counted from the head
-    int need;    // blocks it is given
     int served;
 };
+// The last of n ascending starts that is <= x (starts[0] is): with starts that
+// are exclusive sums of counts, the item that holds place x.  (Sixty
+// instructions; all threads of one SM share its issue slots, so that those who
+// take consecutive places search only where one has left its item.)
+__device__ __forceinline__ int holder(const int* starts, int n, int x) {
+    int lo = 0;
+#pragma unroll
+    for (int step = kThreads / 2; step > 0; step >>= 1)
+        if (lo + step < n && starts[lo + step] <= x) lo += step;
+    return lo;
+}
 
 // Block id read from a table or the free list: -1 (flagged) outside the pool.
 __device__ __forceinline__ int checked_block(int blk, int num_blocks, int32_t* err) {
@@ -85,21 +117,19 @@ __device__ __forceinline__ int checked_block(int blk, int num_blocks, int32_t* e
     return -1;
 }
 
-__device__ __forceinline__ void grow_entry(const GrowArgs& a, const FreeRing& f, const Job& j, int i) {
-    const int blk = checked_block(f.ring[f.index(j.first + static_cast<long long>(i))], a.num_blocks, a.err);
-    a.tables[static_cast<size_t>(j.b) * a.max_blocks + blocks_of(j.L, a.block_shift) + i] = blk;
+// Entry `i` of the free list, counted from the head, to place `at` of the tables.
+__device__ __forceinline__ void grow_entry(const GrowArgs& a, const FreeRing& f, long long at, int i) {
+    a.tables[at] = checked_block(__ldg(f.ring + f.index(i)), a.num_blocks, a.err);
 }
 
-__device__ __forceinline__ void grow_row(const GrowArgs& a, const FreeRing& f, const Job& j, int i) {
-    const long long row = static_cast<long long>(j.off) + i;
-    if (row >= a.max_tokens) return;
+__device__ __forceinline__ void grow_row(const GrowArgs& a, const FreeRing& f, const Job& j, int row, int i) {
     const long long p = static_cast<long long>(j.L > 0 ? j.L : 0) + i;
     long long slot = -1;
     if (j.served) {
         const int held = static_cast<int>(blocks_of(j.L, a.block_shift)), col = static_cast<int>(p >> a.block_shift);
         // the last block held may have room; the others come from the free list
         const int blk = col < held ? a.tables[static_cast<size_t>(j.b) * a.max_blocks + col]
-                                   : f.ring[f.index(j.first + static_cast<long long>(col - held))];
+                                   : f.ring[f.index(j.first + (col - held))];
         if (checked_block(blk, a.num_blocks, a.err) >= 0)
             slot = (static_cast<long long>(blk) << a.block_shift) + (p & ((1LL << a.block_shift) - 1));
     }
@@ -112,9 +142,13 @@ __device__ __forceinline__ void grow_row(const GrowArgs& a, const FreeRing& f, c
 // are read by the thread that writes them, and the free list's state by every
 // thread before the first barrier.
 __global__ void __launch_bounds__(kThreads, 1) grow_kernel(const GrowArgs a, const int fill_rows) {
-    __shared__ long long sums[kWarps];
+    __shared__ int sums[2][kWarps];
     __shared__ Job jobs[kThreads];
-    __shared__ int num_jobs, num_wide, taken;
+    // of the round's requests: first block and first row of each, counted from
+    // the round's first; place of its blocks in the tables, less the former
+    __shared__ int entry_start[kThreads], row_start[kThreads];
+    __shared__ long long entry_at[kThreads];
+    __shared__ int taken;
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     FreeRing f{a.ring, a.ring_size, a.free_state[0]};
     int count = a.free_state[1];
@@ -127,62 +161,78 @@ __global__ void __launch_bounds__(kThreads, 1) grow_kernel(const GrowArgs a, con
     const int head0 = f.head, count0 = a.free_state[1];
     if (bad_state) f.head = 0;
     const long long room = static_cast<long long>(a.max_blocks) << a.block_shift;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const int lane = threadIdx.x & 31;
 
-    long long rows_before = 0, need_before = 0;
+    int rows_before = 0, need_before = 0;
     for (int base = 0; base < a.num_seqs; base += blockDim.x) {
-        if (threadIdx.x == 0) num_jobs = num_wide = 0;
-        const int b = base + threadIdx.x;
+        const int b = base + threadIdx.x, round = min(a.num_seqs - base, static_cast<int>(blockDim.x));
         const bool in = b < a.num_seqs;
         const int L = in ? a.lens[b] : 0, n = in ? a.new_tokens[b] : 0;
-        const long long rows = n > 0 ? n : 0;
-        long long total;
-        const long long off = rows_before + block_scan(rows, sums, &total) - rows;
-        rows_before += total;
+        const int rows = n > 0 ? n : 0;
         const bool len_ok = L >= 0 && L <= room;
-        const bool rows_ok = n >= 0 && (n == 0 || off + n <= a.max_tokens);
         // Requests past max_tokens still count in the sum of needs: all
         // later ones with new tokens are past it too, so it changes nothing.
         const bool fits = in && len_ok && n >= 0 && static_cast<long long>(L) + n <= room;
-        const long long need =
-            fits ? blocks_of(static_cast<long long>(L) + n, a.block_shift) - blocks_of(L, a.block_shift) : 0;
-        const long long incl = need_before + block_scan(need, sums, &total);
-        need_before += total;
+        const int held = static_cast<int>(blocks_of(len_ok ? L : 0, a.block_shift));
+        const int need = fits ? static_cast<int>(blocks_of(static_cast<long long>(L) + n, a.block_shift)) - held : 0;
+        int before[2] = {rows, need}, total[2];
+        block_scan(before, sums, total);
+        const int off = sat_add(rows_before, before[0]), first = sat_add(need_before, before[1]);
+        const bool rows_ok = n >= 0 && (n == 0 || sat_add(off, n) <= a.max_tokens);
         if (in && a.err && (!len_ok || !rows_ok)) atomicOr(a.err, (len_ok ? 0 : PKV_ERRBIT_SEQ_LEN) | (rows_ok ? 0 : PKV_ERRBIT_STEP));
-        const bool served = fits && rows_ok && (need == 0 || incl <= count);
+        // (served requests that need blocks come before all others that do)
+        const bool served = fits && rows_ok && (need == 0 || sat_add(first, need) <= count);
+        const int off_in = min(off, a.max_tokens), off0 = min(rows_before, a.max_tokens);
+        const Job j{b, L, served ? first : 0, served ? 1 : 0};
+        const long long at = static_cast<long long>(b) * a.max_blocks + held;
+        jobs[threadIdx.x] = j;
+        entry_start[threadIdx.x] = before[1];
+        entry_at[threadIdx.x] = at - before[1];
+        row_start[threadIdx.x] = off_in - off0;
         if (in) {
-            a.token_offsets[b] = static_cast<int>(off < a.max_tokens ? off : a.max_tokens);
+            a.token_offsets[b] = off_in;
             a.granted[b] = served ? n : 0;
             a.lens_out[b] = served ? L + n : L;
-            if (served && need > 0) atomicMax(&taken, static_cast<int>(incl));
-            Job j{b, L, static_cast<int>(rows), static_cast<int>(off < a.max_tokens ? off : a.max_tokens),
-                  served ? static_cast<int>(incl - need) : 0, served ? static_cast<int>(need) : 0, served ? 1 : 0};
-            if (j.need <= kDirect && (!fill_rows || j.n <= kDirect)) {
-                for (int i = 0; i < j.need; ++i) grow_entry(a, f, j, i);
-                if (fill_rows)
-                    for (int i = 0; i < j.n; ++i) grow_row(a, f, j, i);
-            } else {
-                // narrow ones from the front of the list, wide ones from its end
-                const bool wide = j.need > kThreads || (fill_rows && j.n > kThreads);
-                jobs[wide ? kThreads - 1 - atomicAdd(&num_wide, 1) : atomicAdd(&num_jobs, 1)] = j;
+            if (served && need > 0) atomicMax(&taken, first + need);
+        }
+        // A few blocks and rows each, by the request's own thread; else shared
+        // out over all threads, each finding the request that its entry is of.
+        if (!__syncthreads_or((served && need > kDirect) || (fill_rows && rows > kDirect))) {
+            if (served)
+                for (int i = 0; i < need; ++i) grow_entry(a, f, at + i, first + i);
+            if (in && fill_rows)
+                for (int i = 0; i < rows && off_in + i < a.max_tokens; ++i) grow_row(a, f, j, off_in + i, i);
+        } else {
+            const int entries = taken - min(need_before, taken);
+            const int stride = (entries + static_cast<int>(blockDim.x) - 1) / static_cast<int>(blockDim.x) * 32;  // of a warp
+            const int e0 = (threadIdx.x >> 5) * stride + lane, last = min(entries, e0 - lane + stride);
+            int i = -1;
+            for (int e = e0; e < last; e += 32 * kAhead) {  // kAhead loads under way at once
+                int blk[kAhead];
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) blk[u] = e + 32 * u < last ? __ldg(f.ring + f.index(need_before + e + 32 * u)) : 0;
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    const int x = e + 32 * u;
+                    if (x >= last) break;
+                    if (i < 0 || (i + 1 < round && entry_start[i + 1] <= x)) i = holder(entry_start, round, x);
+                    a.tables[entry_at[i] + x] = checked_block(blk[u], a.num_blocks, a.err);
+                }
+            }
+            if (fill_rows) {
+                const int num_rows = min(sat_add(rows_before, total[0]), a.max_tokens) - off0;
+                const int stride = (num_rows + static_cast<int>(blockDim.x) - 1) / static_cast<int>(blockDim.x) * 32;
+                for (int r = (threadIdx.x >> 5) * stride + lane, last = min(num_rows, r - lane + stride), i = -1; r < last; r += 32) {
+                    if (i < 0 || (i + 1 < round && row_start[i + 1] <= r)) i = holder(row_start, round, r);
+                    grow_row(a, f, jobs[i], off0 + r, r - row_start[i]);
+                }
             }
         }
-        __syncthreads();
-        // one warp per remaining request; very long ones by the whole CTA
-        auto serve = [&](const Job& j, int k0, int step) {
-#pragma unroll 4
-            for (int k = k0; k < j.need; k += step) grow_entry(a, f, j, k);
-            if (fill_rows) {
-                const int last = j.n < a.max_tokens - j.off ? j.n : a.max_tokens - j.off;
-#pragma unroll 4
-                for (int k = k0; k < last; k += step) grow_row(a, f, j, k);
-            }
-        };
-        for (int i = warp; i < num_jobs; i += warps) serve(jobs[i], lane, 32);
-        for (int i = 0; i < num_wide; ++i) serve(jobs[kThreads - 1 - i], threadIdx.x, blockDim.x);
+        rows_before = sat_add(rows_before, total[0]);
+        need_before = sat_add(need_before, total[1]);
         __syncthreads();
     }
-    const int end = static_cast<int>(rows_before < a.max_tokens ? rows_before : a.max_tokens);
+    const int end = min(rows_before, a.max_tokens);
     if (threadIdx.x == 0) {
         a.token_offsets[a.num_seqs] = end;
         a.free_out[0] = bad_state ? head0 : f.index(taken);
@@ -208,31 +258,32 @@ __global__ void __launch_bounds__(kFillThreads) fill_kernel(const GrowArgs a) {
     const int end = a.token_offsets[a.num_seqs];
     long long slot = -1;
     int pos = 0, seq = -1;
-    if (row0 < end) {
-        int lo = 0, hi = a.num_seqs;  // the last request whose first row is <= row0
-        while (hi - lo > 1) {
-            const int step = (hi - lo + 31) >> 5, at = lo + lane * step;
-            const unsigned below = __ballot_sync(0xFFFFFFFFu, at < hi && a.token_offsets[at] <= row0);
-            lo += (31 - __clz(below)) * step;  // (lane 0 always is)
-            hi = min(hi, lo + step);
-        }
-        if (row < end) {
-            if (a.token_offsets[lo + 1] <= row)
-                for (hi = a.num_seqs; hi - lo > 1;) {
-                    const int mid = (lo + hi) >> 1;
-                    if (a.token_offsets[mid] <= row) lo = mid;
-                    else hi = mid;
-                }
-            seq = lo;
-            const int n = a.granted[seq];
-            const int L = a.lens_out[seq] - n;  // the length before the step
-            const long long p = static_cast<long long>(L > 0 ? L : 0) + (row - a.token_offsets[seq]);
-            pos = sat_pos(p);
-            if (n > 0) {
-                const int blk = checked_block(
-                    a.tables[static_cast<size_t>(seq) * a.max_blocks + (p >> a.block_shift)], a.num_blocks, a.err);
-                if (blk >= 0) slot = (static_cast<long long>(blk) << a.block_shift) + (p & ((1LL << a.block_shift) - 1));
+    int lo = 0, hi = a.num_seqs;  // the last request whose first row is <= row0 (the loads do not wait for `end`)
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) >> 5, at = lo + lane * step;
+        const unsigned below = __ballot_sync(0xFFFFFFFFu, at < hi && a.token_offsets[at] <= row0);
+        lo += (31 - __clz(below)) * step;  // (lane 0 always is)
+        hi = min(hi, lo + step);
+    }
+    if (row < end) {
+        // (what a row needs of its request, in one round: mostly it is the first row's)
+        int n = a.granted[lo], len = a.lens_out[lo], first = a.token_offsets[lo];
+        if (a.token_offsets[lo + 1] <= row) {
+            for (hi = a.num_seqs; hi - lo > 1;) {
+                const int mid = (lo + hi) >> 1;
+                if (a.token_offsets[mid] <= row) lo = mid;
+                else hi = mid;
             }
+            n = a.granted[lo], len = a.lens_out[lo], first = a.token_offsets[lo];
+        }
+        seq = lo;
+        const int L = len - n;  // the length before the step
+        const long long p = static_cast<long long>(L > 0 ? L : 0) + (row - first);
+        pos = sat_pos(p);
+        if (n > 0) {
+            const int blk = checked_block(
+                a.tables[static_cast<size_t>(seq) * a.max_blocks + (p >> a.block_shift)], a.num_blocks, a.err);
+            if (blk >= 0) slot = (static_cast<long long>(blk) << a.block_shift) + (p & ((1LL << a.block_shift) - 1));
         }
     }
     if (row >= a.max_tokens) return;
@@ -269,30 +320,30 @@ __device__ __forceinline__ Given given(const ReleaseArgs& a, int b, bool report)
 
 // Entries k0, k0 + step, .. of what request b gives back, behind the ring's
 // `tail` entries.
-__device__ __forceinline__ void release_copy(const ReleaseArgs& a, int head, long long tail, int b, int first, int count,
+__device__ __forceinline__ void release_copy(const ReleaseArgs& a, int head, int tail, int b, int first, int count,
                                              int k0, int step) {
     const int32_t* src = a.tables + static_cast<size_t>(b) * a.max_blocks + first;
 #pragma unroll 4
     for (int k = k0; k < count; k += step) {
-        long long at = head + tail + k;  // < 2 * ring_size
-        if (at >= a.ring_size) at -= a.ring_size;
+        unsigned at = static_cast<unsigned>(head) + static_cast<unsigned>(tail + k);  // < 2 * ring_size
+        if (at >= static_cast<unsigned>(a.ring_size)) at -= static_cast<unsigned>(a.ring_size);
         a.ring[at] = checked_block(src[k], a.num_blocks, a.err);
     }
 }
 
-__device__ __forceinline__ bool ring_ok(const ReleaseArgs& a, int head, int count, long long total) {
-    return head >= 0 && head < a.ring_size && count >= 0 && count + total <= a.ring_size;
+__device__ __forceinline__ bool ring_ok(const ReleaseArgs& a, int head, int count, int total) {
+    return head >= 0 && head < a.ring_size && count >= 0 && static_cast<long long>(count) + total <= a.ring_size;
 }
-__device__ __forceinline__ void put_state(const ReleaseArgs& a, int head, int count, long long total, bool ok) {
+__device__ __forceinline__ void put_state(const ReleaseArgs& a, int head, int count, int total, bool ok) {
     a.free_out[0] = head;
-    a.free_out[1] = ok ? static_cast<int>(count + total) : count;
+    a.free_out[1] = ok ? count + total : count;
     if (!ok && a.err) atomicOr(a.err, PKV_ERRBIT_STEP);
 }
 
 // Up to kThreads requests in one CTA: a thread each, then the blocks of those
 // that have any by a warp each.  The outputs may be the inputs.
 __global__ void __launch_bounds__(kThreads, 1) release_small_kernel(const ReleaseArgs a) {
-    __shared__ long long sums[kWarps];
+    __shared__ int sums[1][kWarps];
     struct Run {
         int b, first, count, tail;
     };
@@ -302,12 +353,12 @@ __global__ void __launch_bounds__(kThreads, 1) release_small_kernel(const Releas
     Given g{0, 0, 0, false};
     if (b < a.num_seqs) g = given(a, b, true);
     if (b == 0) num_runs = 0;
-    long long total;
-    const long long incl = block_scan(g.count, sums, &total);
-    const bool ok = ring_ok(a, head, count, total);
-    if (ok && g.count > 0) runs[atomicAdd(&num_runs, 1)] = Run{b, g.first, g.count, static_cast<int>(count + incl - g.count)};
+    int before[1] = {g.count}, total[1];
+    block_scan(before, sums, total);
+    const bool ok = ring_ok(a, head, count, total[0]);
+    if (ok && g.count > 0) runs[atomicAdd(&num_runs, 1)] = Run{b, g.first, g.count, count + before[0]};
     if (b < a.num_seqs) a.lens_out[b] = ok && g.gone ? 0 : g.len;
-    if (b == 0) put_state(a, head, count, total, ok);
+    if (b == 0) put_state(a, head, count, total[0], ok);
     __syncthreads();
     for (int i = b >> 5; i < num_runs; i += static_cast<int>(blockDim.x >> 5))
         release_copy(a, head, runs[i].tail, runs[i].b, runs[i].first, runs[i].count, b & 31, 32);
@@ -315,17 +366,19 @@ __global__ void __launch_bounds__(kThreads, 1) release_small_kernel(const Releas
 
 // One pass over the batch: the blocks given back by requests before `upto`
 // (*before) and by all of them (*total), for every thread of the CTA.
-__device__ __forceinline__ void release_sums(const ReleaseArgs& a, int upto, long long* sums, long long* before,
-                                             long long* total) {
-    long long s0 = 0, s1 = 0;
+__device__ __forceinline__ void release_sums(const ReleaseArgs& a, int upto, int (*sums)[kWarps], int* before,
+                                             int* total) {
+    long long s[2] = {0, 0};
 #pragma unroll 4
     for (int b = threadIdx.x; b < a.num_seqs; b += blockDim.x) {
         const int n = given(a, b, false).count;
-        s1 += n;
-        if (b < upto) s0 += n;
+        s[1] += n;
+        if (b < upto) s[0] += n;
     }
-    block_scan(s0, sums, before);
-    block_scan(s1, sums, total);
+    int part[2] = {sat(s[0]), sat(s[1])}, all[2];
+    block_scan(part, sums, all);
+    *before = all[0];
+    *total = all[1];
 }
 
 // Larger batches: every CTA sums the whole batch (some tens of KB from L2) and
@@ -333,13 +386,13 @@ __device__ __forceinline__ void release_sums(const ReleaseArgs& a, int upto, lon
 // inputs are written here (commit); others by a second kernel, once every CTA
 // has read them.
 __global__ void __launch_bounds__(kThreads, 1) release_copy_kernel(const ReleaseArgs a, const int commit) {
-    __shared__ long long sums[kWarps];
+    __shared__ int sums[2][kWarps];
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     const int head = a.free_state[0], count = a.free_state[1];
     const int b0 = blockIdx.x * kReleasePerCta, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     Given g{0, 0, 0, false};
     if (b0 + lane < a.num_seqs) g = given(a, b0 + lane, warp == 0);
-    long long before, total;
+    int before, total;
     release_sums(a, b0, sums, &before, &total);
     const bool ok = ring_ok(a, head, count, total);
     if (commit) {
@@ -347,22 +400,22 @@ __global__ void __launch_bounds__(kThreads, 1) release_copy_kernel(const Release
         if (b0 == 0 && threadIdx.x == 0) put_state(a, head, count, total, ok);
     }
     if (!ok) return;
-    long long incl = g.count;
+    int incl = g.count;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long x = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+        const int x = __shfl_up_sync(0xFFFFFFFFu, incl, o);
         if (lane >= o) incl += x;
     }
-    const long long tail = count + before + __shfl_sync(0xFFFFFFFFu, incl - g.count, warp);
+    const int tail = count + before + __shfl_sync(0xFFFFFFFFu, incl - g.count, warp);
     const int first = __shfl_sync(0xFFFFFFFFu, g.first, warp), n = __shfl_sync(0xFFFFFFFFu, g.count, warp);
     if (b0 + warp < a.num_seqs) release_copy(a, head, tail, b0 + warp, first, n, lane, 32);
 }
 
 __global__ void __launch_bounds__(kThreads, 1) release_commit_kernel(const ReleaseArgs a) {
-    __shared__ long long sums[kWarps];
+    __shared__ int sums[2][kWarps];
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     const int head = a.free_state[0], count = a.free_state[1];
-    long long zero, total;
+    int zero, total;
     release_sums(a, 0, sums, &zero, &total);
     const bool ok = ring_ok(a, head, count, total);
     for (int b = threadIdx.x; b < a.num_seqs; b += blockDim.x) {

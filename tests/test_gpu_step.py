@@ -189,11 +189,13 @@ def _pool(num_blocks, bs):
     return pk.KVPool(1, num_blocks, bs, 1, 64, "fp8")
 
 
-def _grow_inputs(B, bs, len_hi, new_hi, share, seed, width=None, slack=0):
-    """Random lengths and tables; the ring holds `share` of the blocks asked for."""
+def _grow_inputs(B, bs, len_hi, new_hi, share, seed, width=None, slack=0, every=1):
+    """Random lengths and tables; the ring holds `share` of the blocks asked
+    for.  every: only each so manieth request has more than one new token."""
     r = np.random.default_rng(seed)
     lens = r.integers(0, len_hi + 1, B)
     new = r.integers(0, new_hi + 1, B)
+    new = np.where(np.arange(B) % every == every - 1, new, np.minimum(new, 1))
     held, need = -(-lens // bs), -(-(lens + new) // bs) - -(-lens // bs)
     width = width or int(max(1, (held + need).max(initial=1)))
     total = int(held.sum() + need.sum()) + 5
@@ -245,6 +247,35 @@ def test_grow_long_slot_maps():
     _check_grow(100, 16, 500, 400, 0.9, seed=1)
     _check_grow(3, 64, 10, 30000, 1.0, seed=2, extra_rows=1000)
     _check_grow(1500, 16, 50, 40, 0.5, seed=3, in_place=True)
+
+
+@pytest.mark.parametrize("B,every,new_hi,len_hi", [(1024, 97, 600, 100), (1024, 1024, 3000, 16), (2200, 31, 200, 300),
+                                                   (700, 350, 2500, 0), (256, 5, 40, 64)])
+@pytest.mark.parametrize("share", [1.0, 0.5])
+def test_grow_few_long_requests_among_short_ones(B, every, new_hi, len_hi, share):
+    _check_grow(B, 16, len_hi, new_hi, share, seed=B, every=every)
+    _check_grow(B, 64, len_hi, new_hi, share, seed=B + 1, every=every, in_place=True)
+
+
+@pytest.mark.parametrize("big", [2 ** 31 - 1, 2 ** 31 - 2, 2 ** 30])
+def test_grow_sums_past_32_bits(big):
+    """New tokens whose sum passes 2^31: those requests wait, ones before them do not."""
+    pool = _pool(64, 16)
+    B = 1100
+    lens, new = [5] * B, [0] * B
+    new[0], new[7], new[1050] = 20, 1, 1
+    for b in (40, 41, 42, 1060, 1099):
+        new[b] = big
+    ring, T = list(range(10)), 30
+    tables = [[20 + b % 40, -1, -1] for b in range(B)]
+    # (the walk goes row by row: 40 tokens pass max_tokens as well)
+    want = ref.grow([list(x) for x in tables], lens, [min(n, 40) for n in new], ring, [3, 5], 16, T)
+    t = dev(tables)
+    got = pk.kv_tables_grow(pool, t, dev(lens), dev(new), dev(ring), dev([3, 5]), T)
+    for name, x, y in zip(got._fields, got, want):
+        assert x.tolist() == y, name
+    assert got.granted.tolist()[:8] == [20, 0, 0, 0, 0, 0, 0, 1] and sum(got.granted.tolist()) == 21
+    assert t[0].tolist() == [20, 3, -1] and pool.errors() == pk.ERRBIT_STEP
 
 
 @pytest.mark.parametrize("B,new_hi", [(200, 1), (1100, 2), (30, 100)])

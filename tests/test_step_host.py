@@ -141,10 +141,11 @@ def test_tables_refusals(pool):
                      (release, ("t", "lens", "done", "ring", "st", "lo", "so"))):
         assert f(h=None) == 1 and f(mb=0) == 1 and f(size=0) == 1 and f(B=-1) == 1
         assert f(mb=2 ** 31 // 16) == 2  # positions past 2^31 - 1
+        assert f(size=2 ** 30 + 1) == 2
         for n in names:
             assert f(**{n: None}) == 1, n
             assert f(**{n: FAKE + (4 if n == "slots" else 2)}) == 1, n
-    assert grow(T=-1) == 1 and release(keep=FAKE + 2) == 1
+    assert grow(T=-1) == 1 and release(keep=FAKE + 2) == 1 and grow(T=2 ** 30 + 1) == 2
 
 
 def test_binding_checks_shapes_types_and_devices():
