@@ -204,185 +204,226 @@ __device__ __forceinline__ int my_range(int ctas) {
     return c < half ? c : ctas - 1 - (c - half);
 }
 
-// Inclusive sum over the CTA; *total gets the sum of all.
-__device__ __forceinline__ int plan_scan(int v, int* warp_sums, int* total) {
-    constexpr int kWarps = kThreads / 32;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xFFFFFFFFu, v, o);
-        if (lane >= o) v += x;
-    }
-    if (lane == 31) warp_sums[warp] = v;
-    __syncthreads();
-    int before = 0, sum = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        const int x = warp_sums[w];
-        if (w < warp) before += x;
-        sum += x;
-    }
-    *total = sum;
-    __syncthreads();  // warp_sums may be written again
-    return v + before;
-}
+// The plan runs once per CTA, so its time is that of fetching its instructions
+// (7 thousand cycles where the loops were unrolled): short code, rolled loops,
+// and sequences and groups side by side, each by warps of their own.
+constexpr int kSeqThreads = 256, kGroupThreads = kThreads - kSeqThreads;
 
-__device__ __forceinline__ int last_at_or_before(const int* cum, int n, int x) {  // cum[0] <= x; empty entries skipped
-    int lo = 0, hi = n;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (cum[mid] <= x) lo = mid;
-        else hi = mid;
+// Exclusive sum of v over this thread's kind, sequences or groups; the totals of both.
+__device__ __forceinline__ int plan_scan(int v, int* sums, int* seqs, int* groups) {
+    constexpr int kWarps = kThreads / 32, kSeqWarps = kSeqThreads / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int x = v;
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+        if (lane >= o) x += y;
     }
-    return lo;
+    if (lane == 31) sums[warp] = x;
+    __syncthreads();
+    const int all = lane < kWarps ? sums[lane] : 0;
+    const bool of_seq = lane < kSeqWarps;
+    *seqs = __reduce_add_sync(0xFFFFFFFFu, of_seq ? all : 0);
+    *groups = __reduce_add_sync(0xFFFFFFFFu, of_seq ? 0 : all);
+    return x - v + __reduce_add_sync(0xFFFFFFFFu, lane < warp && of_seq == (warp < kSeqWarps) ? all : 0);
 }
 
 struct Start {
     int own, i, u, t, left;  // of this CTA's range: list half, group or sequence, unit, place in the unit, cost
-    int seq0, group0;        // the caches' first entries
+    int seq0;                // the sequence cache's first entry
+    int groups_cached;       // the group cache holds them all (else the workspace does)
     int pos, T;              // start of the range in the list, cost of the list
 };
+
+__device__ __forceinline__ int row_tiles(const PrefixArgs& a, int seqs) {
+    return (seqs + a.seqs_per_tile - 1) / a.seqs_per_tile;
+}
+
+// What a thread fetches of the call's lengths or groups before anything else.
+struct Early {
+    int x, y, z;  // a length; or a group's first and last + 1 sequence and its prefix
+};
+__device__ __forceinline__ Early fetch_early(const PrefixArgs& a) {
+    const int b = threadIdx.x, g = b - kSeqThreads;
+    Early e{0, 0, 0};
+    if (b < kSeqThreads) {
+        if (b < a.num_seqs) e.x = a.lens[b];
+    } else if (g < a.num_groups) {
+        e.x = a.group_offsets[g];
+        e.y = a.group_offsets[g + 1];
+        e.z = a.prefix_lens[g];
+    }
+    return e;
+}
 
 // Every CTA plans the whole call in its own shared memory (the ring's, before
 // the first copy): a launch less, and the latency is one round of loads plus
 // the sums.  It keeps the units it will walk over (those that its caches cannot
-// hold in the workspace), and CTA 0 writes what the merge needs.
-__device__ void make_plan(const PrefixArgs& a, uint8_t* scratch, int2* seq_cache, int4* group_cache, Start* start) {
-    __shared__ int sums[kThreads / 32];
-    __shared__ int bad;
-    const int B = a.num_seqs, Hkv = a.num_kv_heads, tid = threadIdx.x;
+// hold in the workspace); what the merge needs the CTAs write together.
+__device__ void make_plan(const PrefixArgs& a, const Early& early, uint8_t* scratch, int2* seq_cache,
+                          int4* group_cache, Start* start) {
+    __shared__ int sums[2][kThreads / 32];
+    __shared__ Start found_smem;
+    Start* found = &found_smem;
+    const int B = a.num_seqs, Hkv = a.num_kv_heads, tid = threadIdx.x, lane = tid & 31;
+    const bool of_seq = tid < kSeqThreads;
+    const int id = of_seq ? tid : tid - kSeqThreads;
     const bool report = blockIdx.x == 0;
-    int4* group = reinterpret_cast<int4*>(scratch);             // [G] {first sequence, sequences, tiles, table row}
-    int* cum_p = reinterpret_cast<int*>(group + a.num_groups);  // [G]
+    int4* group = reinterpret_cast<int4*>(scratch);             // [G] {first sequence, sequences, members, table row}
+    int* cum_p = reinterpret_cast<int*>(group + a.num_groups);  // [G] cost of the shared units before
     int* pre = cum_p + a.num_groups;                            // [G] prefix lengths
     int* len = pre + a.num_groups;                              // [B]
     int* mine = len + B;                                        // [B] the group it reads with, or -1
-    int* cum_s = mine + B;                                      // [B]
-    // the first rounds' loads, all under way at once
-    const int L0 = tid < B ? a.lens[tid] : 0;
-    int first0 = 0, end0 = 0, pre0 = 0;
-    if (tid < a.num_groups) {
-        first0 = a.group_offsets[tid];
-        end0 = a.group_offsets[tid + 1];
-        pre0 = a.prefix_lens[tid];
-    }
-    if (tid == 0) bad = 0;
-    __syncthreads();
-    for (int b = tid; b < B; b += kThreads) {
-        int L = b == tid ? L0 : a.lens[b];
-        if (L < 0 || L > a.max_len) {
-            if (report && a.err) atomicOr(a.err, PKV_ERRBIT_SEQ_LEN);
-            L = L < 0 ? 0 : a.max_len;
+    int* cum_s = mine + B;                                      // [B] cost of the own units before, from the first own one
+    bool bad = false;
+    if (of_seq) {
+#pragma unroll 1
+        for (int b = id; b < B; b += kSeqThreads) {
+            int L = b == id ? early.x : a.lens[b];
+            if (L < 0 || L > a.max_len) {
+                if (report && a.err) atomicOr(a.err, PKV_ERRBIT_SEQ_LEN);
+                L = L < 0 ? 0 : a.max_len;
+            }
+            len[b] = L;
         }
-        len[b] = L;
-        mine[b] = -1;
+    } else {
+#pragma unroll 1
+        for (int g = id; g < a.num_groups; g += kGroupThreads) {
+            Early e = early;
+            if (g != id) e = Early{a.group_offsets[g], a.group_offsets[g + 1], a.prefix_lens[g]};
+            if (e.x < 0 || e.y < e.x || e.y > B) bad = true;
+            if (e.z < 0 && report && a.err) atomicOr(a.err, PKV_ERRBIT_GROUP);
+            group[g] = make_int4(e.x, e.y - e.x, 0, INT_MAX);
+            pre[g] = e.z < 0 || e.z > a.max_len ? 0 : e.z - e.z % kTok;  // (no sequence is longer than max_len)
+        }
     }
-    for (int g = tid; g < a.num_groups; g += kThreads) {
-        const bool r0 = g == tid;
-        const int o0 = r0 ? first0 : a.group_offsets[g], o1 = r0 ? end0 : a.group_offsets[g + 1];
-        const int P = r0 ? pre0 : a.prefix_lens[g];
-        if (o0 < 0 || o1 < o0 || o1 > B) bad = 1;
-        if (P < 0 && report && a.err) atomicOr(a.err, PKV_ERRBIT_GROUP);
-        group[g] = make_int4(o0, o1 - o0, 0, INT_MAX);
-        pre[g] = P < 0 || P > a.max_len ? 0 : P - P % kTok;  // (no sequence is longer than max_len)
-    }
-    __syncthreads();
+    bad = __syncthreads_or(bad);
     const int G = bad ? 0 : a.num_groups;  // no sharing at all when the groups make no sense
     if (bad && tid == 0 && report && a.err) atomicOr(a.err, PKV_ERRBIT_GROUP);
     // A group's members are the sequences that hold all of its shared tiles;
     // below two there is nothing to share.
-    for (int b = tid; b < B && G > 0; b += kThreads) {
+#pragma unroll 1
+    for (int base = 0; of_seq && base < B; base += kSeqThreads) {
+        const int b = base + id;
         int lo = 0, hi = G;  // the last group that starts at or before b (the empty ones before it start there too)
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (group[mid].x <= b) lo = mid;
-            else hi = mid;
+        bool member = false;
+        if (b < B && G > 0) {
+#pragma unroll 1
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (group[mid].x <= b) lo = mid;
+                else hi = mid;
+            }
+            const int first = group[lo].x, n = group[lo].y;
+            member = b >= first && b < first + n && pre[lo] > 0 && len[b] >= pre[lo];
         }
-        const int4 u = group[lo];
-        if (b >= u.x && b < u.x + u.y && pre[lo] > 0 && len[b] >= pre[lo]) {
-            mine[b] = lo;
-            atomicAdd(&group[lo].z, 1);
-            atomicMin(&group[lo].w, b);
-        }
-    }
-    __syncthreads();
-    int T = 0, total;
-    for (int base = 0; base < G; base += kThreads) {
-        const int g = base + tid;
-        int v = 0;
-        if (g < G) {
-            int4 u = group[g];
-            u.z = u.z >= 2 ? pre[g] / kTok : 0;
-            if (u.z == 0) u.w = 0;
-            group[g] = u;
-            v = u.z > 0 ? (u.y + a.seqs_per_tile - 1) / a.seqs_per_tile * Hkv * (u.z + kUnitCost) : 0;
-        }
-        const int incl = T + plan_scan(v, sums, &total);
-        if (g < G) cum_p[g] = incl - v;
-        T += total;
-    }
-    const int T1 = T;  // cost of the shared tiles
-    for (int base = 0; base < B; base += kThreads) {
-        const int b = base + tid;
-        int nt = 0, shared = 0, g = -1;
-        if (b < B) {
-            g = mine[b];
-            shared = g >= 0 ? group[g].z : 0;
-            nt = (len[b] + kTok - 1) / kTok - shared;
-            mine[b] = shared;  // (from here on: the tiles it shares)
-        }
-        const int v = nt > 0 ? (nt + kUnitCost) * Hkv : 0;
-        const int incl = T + plan_scan(v, sums, &total);
-        if (b < B) {
-            cum_s[b] = incl - v;
-            if (report) {  // where the merge finds the pieces of this sequence's rows
-                int4 p = make_int4(0, 0, 0, 0);
-                int stride = 0;
-                if (shared > 0) {
-                    const int4 u = group[g];
-                    const int r = (b - u.x) / a.seqs_per_tile, seq0 = u.x + r * a.seqs_per_tile;
-                    stride = min(a.seqs_per_tile, u.y - r * a.seqs_per_tile) * a.gh;
-                    p = make_int4(cum_p[g] + r * Hkv * (shared + kUnitCost), shared, Hkv * seq0, b - seq0);
-                }
-                a.pieces[2 * b] = p;
-                a.pieces[2 * b + 1] = make_int4(stride, incl - v, nt, 0);
+        if (b < B) mine[b] = member ? lo : -1;
+        const unsigned m = __ballot_sync(0xFFFFFFFFu, member);
+        if (m != 0) {  // counted once per warp where they are of one group
+            const int lead = __ffs(m) - 1, g = __shfl_sync(0xFFFFFFFFu, lo, lead);
+            const bool one = __all_sync(0xFFFFFFFFu, !member || lo == g);
+            if (member && (!one || lane == lead)) {
+                atomicAdd(&group[lo].z, one ? __popc(m) : 1);
+                atomicMin(&group[lo].w, b);
             }
         }
-        T += total;
     }
-    if (report && tid == 0) *a.totals = T;
     __syncthreads();
+    auto shared_of = [&](int g) { return g >= 0 && group[g].z >= 2 ? pre[g] / kTok : 0; };  // tiles
+    auto own_of = [&](int b) { return (len[b] + kTok - 1) / kTok - shared_of(mine[b]); };
+    int T1 = 0, T2 = 0;  // cost of the shared tiles, and of the own ones
+#pragma unroll 1
+    for (int round = 0; round * kSeqThreads < B || round * kGroupThreads < G; ++round) {
+        const int x = round * (of_seq ? kSeqThreads : kGroupThreads) + id;
+        int v = 0, seqs, groups;
+        if (of_seq) {
+            const int nt = x < B ? own_of(x) : 0;
+            v = nt > 0 ? (nt + kUnitCost) * Hkv : 0;
+        } else if (x < G) {
+            const int tiles = shared_of(x);
+            v = tiles > 0 ? row_tiles(a, group[x].y) * Hkv * (tiles + kUnitCost) : 0;
+        }
+        v = plan_scan(v, sums[round & 1], &seqs, &groups);
+        if (x < (of_seq ? B : G)) (of_seq ? cum_s : cum_p)[x] = (of_seq ? T2 : T1) + v;
+        T1 += groups;
+        T2 += seqs;
+    }
+    __syncthreads();
+    const int T = T1 + T2;
     const Cut cut(T, a.ctas);
     const int r = my_range(a.ctas);
     Start st{0, 0, 0, 0, 0, 0, 0, 0, T};
+    int x0 = 0, x1 = 0;  // this CTA's range, counted from the first own unit
     if (r < cut.n) {
-        const int g0 = cut.start(r), g1 = cut.start(r + 1);
-        st.left = g1 - g0;
-        st.pos = g0;
-        st.own = g0 >= T1;
-        st.i = st.own ? last_at_or_before(cum_s, B, g0) : last_at_or_before(cum_p, G, g0);
-        const int x = g0 - (st.own ? cum_s[st.i] : cum_p[st.i]);
-        const int vt = (st.own ? (len[st.i] + kTok - 1) / kTok - mine[st.i] : group[st.i].z) + kUnitCost;
-        st.u = x / vt;
-        st.t = x % vt;
-        st.seq0 = st.own ? st.i : 0;
-        st.group0 = st.own ? 0 : st.i;
+        st.pos = cut.start(r);
+        st.left = cut.start(r + 1) - st.pos;
+        st.own = st.pos >= T1;
+        x0 = st.pos - T1;
+        x1 = x0 + st.left;
+    }
+    // The thread whose sequence or group the range begins in says where (a
+    // search would be a chain of ten loads).  Of batches that the cache cannot
+    // hold it keeps the part from there on.
+    auto begin = [&](int i, int x, int tiles) {
+        const int vt = tiles + kUnitCost;
+        found->i = i;
+        found->u = x / vt;
+        found->t = x - found->u * vt;
+    };
+    auto own_end = [&](int b) { return b + 1 < B ? cum_s[b + 1] : T2; };
+    if (of_seq) {
+#pragma unroll 1
+        for (int b = id; b < B; b += kSeqThreads) {
+            const int lo = cum_s[b], hi = own_end(b);
+            if (lo <= x0 && x0 < hi) begin(b, x0 - lo, own_of(b));
+            if (lo < x1 && hi > x0 && B <= kSeqCache) seq_cache[b] = make_int2(len[b], shared_of(mine[b]));
+        }
+    } else {
+#pragma unroll 1
+        for (int g = id; g < G; g += kGroupThreads) {
+            const int lo = cum_p[g] - T1, hi = (g + 1 < G ? cum_p[g + 1] : T1) - T1;
+            if (lo <= x0 && x0 < hi) begin(g, x0 - lo, shared_of(g));
+            if (lo < x1 && hi > x0) {
+                const int tiles = shared_of(g);
+                (G <= kGroupCache ? group_cache : a.groups)[g] =
+                    make_int4(group[g].x, group[g].y, tiles, tiles > 0 ? group[g].w : 0);
+            }
+        }
+        // where the merge finds the pieces of a sequence's rows: a few by every CTA
+#pragma unroll 1
+        for (int b = static_cast<int>(blockIdx.x + gridDim.x * id); b < B; b += static_cast<int>(gridDim.x * kGroupThreads)) {
+            const int g = mine[b], shared = shared_of(g);
+            int4 p = make_int4(0, 0, 0, 0);
+            int stride = 0;
+            if (shared > 0) {
+                const int r = (b - group[g].x) / a.seqs_per_tile, seq0 = group[g].x + r * a.seqs_per_tile;
+                stride = min(a.seqs_per_tile, group[g].y - r * a.seqs_per_tile) * a.gh;
+                p = make_int4(cum_p[g] + r * Hkv * (shared + kUnitCost), shared, Hkv * seq0, b - seq0);
+            }
+            a.pieces[2 * b] = p;
+            a.pieces[2 * b + 1] = make_int4(stride, T1 + cum_s[b], own_of(b), 0);
+        }
+        if (report && id == 0) *a.totals = T;
+    }
+    st.groups_cached = G <= kGroupCache;
+    if (B > kSeqCache) {
+        __syncthreads();
+        st.seq0 = st.own ? found->i : 0;
+#pragma unroll 1
         for (int b = st.seq0 + tid; b < B; b += kThreads)
-            if (cum_s[b] < g1 && (b + 1 < B ? cum_s[b + 1] : T) > g0) {
-                const int2 q = make_int2(len[b], mine[b]);
+            if (cum_s[b] < x1 && own_end(b) > x0) {
+                const int2 q = make_int2(len[b], shared_of(mine[b]));
                 if (b - st.seq0 < kSeqCache) seq_cache[b - st.seq0] = q;
                 else a.seqs[b] = q;
-            }
-        for (int g = st.group0 + tid; g < G; g += kThreads)
-            if (cum_p[g] < g1 && (g + 1 < G ? cum_p[g + 1] : T1) > g0) {
-                if (g - st.group0 < kGroupCache) group_cache[g - st.group0] = group[g];
-                else a.groups[g] = group[g];
             }
     }
     // the units' data, for every thread of this CTA; and no generic access to
     // the ring behind the copies that follow
     fence_async_smem();
     __syncthreads();
+    st.i = found->i;
+    st.u = found->u;
+    st.t = found->t;
     *start = st;
 }
 
@@ -459,10 +500,10 @@ struct Walk {
                 at.i = 0;
                 break;
             }
-            const int4 g = at.i - at.group0 < kGroupCache ? group_cache[at.i - at.group0] : a.groups[at.i];
+            const int4 g = at.groups_cached ? group_cache[at.i] : a.groups[at.i];
             if (g.z > 0) {
                 const int r = at.u / a.num_kv_heads;
-                units = (g.y + a.seqs_per_tile - 1) / a.seqs_per_tile * a.num_kv_heads;
+                units = row_tiles(a, g.y) * a.num_kv_heads;
                 s.own = 0;
                 s.row = g.w;
                 s.head = at.u - r * a.num_kv_heads;
@@ -505,33 +546,39 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kBarOff + 8 * kNumBars + 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < kNumBars; ++i)
+    const Early early = fetch_early(a);  // (under way while the CTA sets itself up)
+    // Setting up is shared out to warps that the plan's first part hardly needs
+    // (kWarpK and behind); its barriers cover what they write.
+    if (warp == kWarpS) {
+        for (int i = lane; i < kNumBars; i += 32)
             bar_init(B(i), ((i >= kPFull && i < kPFull + kNS) || i == kOFree || i == kSRead || i == kQOp) ? kSoftmaxWarps
                                                                                            : (i == kDone ? 2u : 1u));
-        *abort_flag = 0;
+        if (lane == 0) *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
-    if (warp == 0) {
+    if (warp >= kWarpK && lane == 0) {  // (the descriptors are fetched while the plan is made)
+        const CUtensorMap* map = warp == kWarpK ? &tmk : (warp == kWarpV ? &tmv : (warp == kWarpS ? &tmq_own : &tmq_group));
+        asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+    }
+    if (warp == kWarpPv) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(su32(tmem_slot)),
                      "r"(kTmemCols)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
+        fence_before();
     }
-    fence_before();
-    __syncthreads();
-    fence_after();
-    const uint32_t tmem = *tmem_slot;
-    auto fail = [&]() {
-        *abort_flag = 1;
-        if (a.err) atomicOr(a.err, PKV_ERRBIT_TIMEOUT);
-    };
     Walk w;
     w.range = my_range(a.ctas);
     w.seq_cache = reinterpret_cast<const int2*>(smem + kSeqOff);
     w.group_cache = reinterpret_cast<const int4*>(smem + kGroupOff);
-    make_plan(a, smem + kKVOff, reinterpret_cast<int2*>(smem + kSeqOff), reinterpret_cast<int4*>(smem + kGroupOff), &w.at);
+    make_plan(a, early, smem + kKVOff, reinterpret_cast<int2*>(smem + kSeqOff), reinterpret_cast<int4*>(smem + kGroupOff), &w.at);
+    fence_after();
+    const uint32_t tmem = *tmem_slot;
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    auto fail = [&]() {
+        *abort_flag = 1;
+        if (a.err) atomicOr(a.err, PKV_ERRBIT_TIMEOUT);
+    };
 
     if (warp == kWarpK || warp == kWarpV) {
         // ------------------------------------------------ producers: K, V
@@ -898,7 +945,8 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     uint32_t v[32];
-                    tmem_ld_16x64(tmem + lane_off + (static_cast<uint32_t>(16 * c) << 16) + kOCol + 64 * hf, v);
+                    if (32 * pair + 16 * c < nv)
+                        tmem_ld_16x64(tmem + lane_off + (static_cast<uint32_t>(16 * c) << 16) + kOCol + 64 * hf, v);
                     if (c == 1) {  // O is read: the next segment's first PV may overwrite it
                         fence_before();
                         __syncwarp();
@@ -906,6 +954,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                     }
 #pragma unroll
                     for (int up = 0; up < 2; ++up) {
+                        if (32 * pair + 16 * c + 8 * up >= nv) break;  // (own units have a few rows only)
                         const int r = 16 * c + 8 * up + (lane >> 2);
                         const float f = __shfl_sync(0xFFFFFFFFu, inv, r);
                         if (32 * pair + r < nv) {
