@@ -133,6 +133,7 @@ struct PrefixArgs {
     int gh;                        // query heads per KV head
     int seqs_per_tile;             // sequences whose rows fill a 128-row tile
     int ctas;                      // CTAs of the attention kernel
+    int unit_cost;                 // cost of a unit beside its tiles, in tiles (set by the launch)
     float qk_scale_log2, v_scale;
     // workspace: the plan ...
     int32_t* totals;               // cost of the whole list

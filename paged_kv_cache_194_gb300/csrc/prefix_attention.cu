@@ -174,10 +174,15 @@ __device__ __forceinline__ bool pair_any(int id, bool yes) {
 __device__ __forceinline__ void pair_sync(int id) { asm volatile("barrier.cta.sync %0, 64;\n" ::"r"(1 + id) : "memory"); }
 
 // ------------------------------------------------------------------- plan
-// Cost, in tiles, that a unit has beside its tiles: its Q rows to fetch, its
-// piece to write out and the pipeline to refill.  The list is cut by cost,
-// every unit being nt + kUnitCost long; the last kUnitCost of them hold no tile.
-constexpr int kUnitCost = 2;
+// A unit costs more than its tiles: its Q rows to fetch (and, FP8 pools, to
+// split), its piece to write out, the pipeline to refill.  The list is cut by
+// cost, every unit being nt + unit_cost long; the last unit_cost places of it
+// hold no tile.  Two tiles' worth for BF16 (64 sequences over 32768 shared
+// tokens: 69, 64, 65 us with 1, 2, 3), five for FP8, where the tiles of
+// full row tiles also take longer than own ones (64 sequences, 2048 shared
+// tokens, own ones up to 2048: 77, 73, 69, 67.5, 68 us with 1 to 5; eight
+// groups over 1024 to 8192 tokens: 74, 67, 65, 64, 61.5).
+int unit_cost_of(pkv_dtype kv) { return kv == PKV_FP8_E4M3 ? 5 : 2; }
 
 // A list of cost T is cut into n = min(T, ctas) ranges, none of them empty, the
 // first T % n one longer than the others.
@@ -338,10 +343,10 @@ __device__ void make_plan(const PrefixArgs& a, const Early& early, uint8_t* scra
         int v = 0, seqs, groups;
         if (of_seq) {
             const int nt = x < B ? own_of(x) : 0;
-            v = nt > 0 ? (nt + kUnitCost) * Hkv : 0;
+            v = nt > 0 ? (nt + a.unit_cost) * Hkv : 0;
         } else if (x < G) {
             const int tiles = shared_of(x);
-            v = tiles > 0 ? row_tiles(a, group[x].y) * Hkv * (tiles + kUnitCost) : 0;
+            v = tiles > 0 ? row_tiles(a, group[x].y) * Hkv * (tiles + a.unit_cost) : 0;
         }
         v = plan_scan(v, sums[round & 1], &seqs, &groups);
         if (x < (of_seq ? B : G)) (of_seq ? cum_s : cum_p)[x] = (of_seq ? T2 : T1) + v;
@@ -365,7 +370,7 @@ __device__ void make_plan(const PrefixArgs& a, const Early& early, uint8_t* scra
     // search would be a chain of ten loads).  Of batches that the cache cannot
     // hold it keeps the part from there on.
     auto begin = [&](int i, int x, int tiles) {
-        const int vt = tiles + kUnitCost;
+        const int vt = tiles + a.unit_cost;
         found->i = i;
         found->u = x / vt;
         found->t = x - found->u * vt;
@@ -398,7 +403,7 @@ __device__ void make_plan(const PrefixArgs& a, const Early& early, uint8_t* scra
             if (shared > 0) {
                 const int r = (b - group[g].x) / a.seqs_per_tile, seq0 = group[g].x + r * a.seqs_per_tile;
                 stride = min(a.seqs_per_tile, group[g].y - r * a.seqs_per_tile) * a.gh;
-                p = make_int4(cum_p[g] + r * Hkv * (shared + kUnitCost), shared, Hkv * seq0, b - seq0);
+                p = make_int4(cum_p[g] + r * Hkv * (shared + a.unit_cost), shared, Hkv * seq0, b - seq0);
             }
             a.pieces[2 * b] = p;
             a.pieces[2 * b + 1] = make_int4(stride, T1 + cum_s[b], own_of(b), 0);
@@ -460,7 +465,7 @@ struct Walk {
     __device__ bool next(const PrefixArgs& a, Seg& s) {
         while (at.left > 0) {
             const int nt = unit(a, s);
-            const int t0 = at.t, cost = min(at.left, nt + kUnitCost - t0);
+            const int t0 = at.t, cost = min(at.left, nt + a.unit_cost - t0);
             at.left -= cost;
             at.t = 0;
             if (++at.u == units) {
@@ -511,7 +516,7 @@ struct Walk {
                 s.nseq = min(a.seqs_per_tile, g.y - r * a.seqs_per_tile);
                 s.tile = 0;
                 s.end = g.z * kTok;
-                ahead = r * a.num_kv_heads * (g.z + kUnitCost);
+                ahead = r * a.num_kv_heads * (g.z + a.unit_cost);
                 return g.z;
             }
             ++at.i;
@@ -1003,13 +1008,13 @@ __global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const Prefi
     int n0 = 0, n1 = 0;
     size_t pre0 = 0, own0 = 0;
     if (p.y > 0) {
-        const int ps = p.x + h * (p.y + kUnitCost), c0 = cut.of(ps);
+        const int ps = p.x + h * (p.y + a.unit_cost), c0 = cut.of(ps);
         n0 = cut.of(ps + p.y - 1) - c0 + 1;
         pre0 = static_cast<size_t>(a.gh) * (p.z + p.w) + static_cast<size_t>(h) * q.x + hq % a.gh +
                static_cast<size_t>(c0) * kRows;
     }
     if (q.z > 0) {
-        const int ps = q.y + h * (q.z + kUnitCost), c0 = cut.of(ps);
+        const int ps = q.y + h * (q.z + a.unit_cost), c0 = cut.of(ps);
         n1 = cut.of(ps + q.z - 1) - c0 + 1;
         own0 = static_cast<size_t>(out_row) + static_cast<size_t>(c0) * a.gh;
     }
@@ -1086,8 +1091,10 @@ cudaError_t launch_tc(const PrefixArgs& a, const void* tmap_k, const void* tmap_
 }
 }  // namespace
 
-cudaError_t launch_prefix_attention(pkv_dtype kv, const PrefixArgs& a, const void* tmap_k, const void* tmap_v,
+cudaError_t launch_prefix_attention(pkv_dtype kv, const PrefixArgs& args, const void* tmap_k, const void* tmap_v,
                                     const void* tmap_q_group, const void* tmap_q_own, cudaStream_t stream) {
+    PrefixArgs a = args;
+    a.unit_cost = unit_cost_of(kv);
     const cudaError_t e = kv == PKV_FP8_E4M3 ? launch_tc<true>(a, tmap_k, tmap_v, tmap_q_group, tmap_q_own, stream)
                                              : launch_tc<false>(a, tmap_k, tmap_v, tmap_q_group, tmap_q_own, stream);
     if (e != cudaSuccess) return e;
