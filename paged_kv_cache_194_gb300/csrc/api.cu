@@ -352,12 +352,10 @@ int32_t paged_decode_algo(const pkv_pool* p, int32_t G, pkv_algo algo) {
     if (!p || G < 1) return -1;
     pkv_pool* mp = const_cast<pkv_pool*>(p);
     const bool mma_ok = decode_mma_supported(p->d.kv_dtype, p->d.head_dim, G, p->d.block_size);
-    const bool simt_ok = decode_simt_supported(p->d.kv_dtype, p->d.head_dim, G);
     if (algo == PKV_ALGO_MMA) return (mma_ok && ensure_tmaps(mp)) ? PKV_ALGO_MMA : -1;
-    if (algo == PKV_ALGO_SIMT) return simt_ok ? PKV_ALGO_SIMT : -1;
+    if (algo == PKV_ALGO_SIMT) return PKV_ALGO_SIMT;  // (any number of heads, in parts if need be)
     if (algo != PKV_ALGO_AUTO) return -1;
-    if (mma_ok && ensure_tmaps(mp)) return PKV_ALGO_MMA;
-    return simt_ok ? PKV_ALGO_SIMT : -1;
+    return mma_ok && ensure_tmaps(mp) ? PKV_ALGO_MMA : PKV_ALGO_SIMT;
 }
 
 }  // extern "C"
@@ -373,7 +371,9 @@ int design_for(const pkv_pool* p, int C, int gh, int split_tokens, pkv_algo algo
     const bool tc_fits = attention_tc_supported(p->d.kv_dtype, p->d.head_dim, p->d.block_size) && !fused &&
                          split_tokens == 0 && static_cast<int64_t>(C) * gh <= (1 << 24);
     const bool mma_fits = decode_mma_supported(p->d.kv_dtype, p->d.head_dim, mma_chunk(gh, C) * gh, p->d.block_size);
-    const bool simt_fits = decode_simt_supported(p->d.kv_dtype, p->d.head_dim, simt_chunk(p, gh, C) * gh);
+    const int cs = simt_chunk(p, gh, C);
+    // (a single query's heads may run in parts, so that any number of them fits)
+    const bool simt_fits = cs == 1 || decode_simt_supported(p->d.kv_dtype, p->d.head_dim, cs * gh);
     int d = -1;
     if (algo == PKV_ALGO_TC) {
         d = tc_fits && ensure_tmaps(mp) && p->tmap_half == 1 ? PKV_ALGO_TC : -1;

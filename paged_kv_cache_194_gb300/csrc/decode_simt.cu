@@ -19,6 +19,7 @@
 //   PV   thread (token group, chunk) accumulates G x chunk outputs over its
 //        rows; groups are merged through shared memory once per split.
 // Scores are kept in the log2 domain (q is pre-scaled by scale*log2(e)).
+// Numbers of query heads without a G of their own run in parts (by_heads).
 #include <cfloat>
 #include <type_traits>
 
@@ -87,17 +88,19 @@ decode_simt_kernel(const DecodeArgs a) {
     const int t_end = min(L, t_begin + a.split_tokens);
     const bool direct = a.num_splits == 1;
 
-    // The G rows served here are C queries x gh heads: row g is query
+    // The rows served here are C queries x gh heads: row g is query
     // q_first + g / gh of the sequence (position L - C + g / gh of the
-    // visible length L, attending causally) and head h*gh + g % gh.
-    const int Cq = a.num_queries, gh = G / Cq;
+    // visible length L, attending causally) and head h*gh + g % gh.  A single
+    // query may have fewer rows than G (the others are zero and not written), or
+    // only some of the heads, from head_first on.
+    const int Cq = a.num_queries, gh = a.head_count > 0 ? a.head_count : G / Cq, rows = Cq * gh;
+    const int head0 = a.head_count > 0 ? h * (a.num_q_heads / a.num_kv_heads) + a.head_first : h * gh;
     auto qrow = [&](int g) -> size_t {
-        return (static_cast<size_t>(b) * a.q_total + a.q_first + g / gh) * a.num_q_heads + static_cast<size_t>(h) * gh +
-               g % gh;
+        return (static_cast<size_t>(b) * a.q_total + a.q_first + g / gh) * a.num_q_heads + head0 + g % gh;
     };
     if (t_begin >= t_end) {
         if (direct) {  // empty sequence: zero output rows
-            for (int i = tid; i < G * D; i += kThreads) static_cast<QT*>(a.out)[qrow(i / D) * D + i % D] = to_out<QT>(0.f);
+            for (int i = tid; i < rows * D; i += kThreads) static_cast<QT*>(a.out)[qrow(i / D) * D + i % D] = to_out<QT>(0.f);
         }
         return;
     }
@@ -110,7 +113,8 @@ decode_simt_kernel(const DecodeArgs a) {
 #pragma unroll
         for (int g = 0; g < G; ++g)
 #pragma unroll
-            for (int e = 0; e < E; ++e) qf[g][e] = load_q<QT>(qb + qrow(g) * D + qc * E + e) * a.qk_scale_log2;
+            for (int e = 0; e < E; ++e)
+                qf[g][e] = g < rows ? load_q<QT>(qb + qrow(g) * D + qc * E + e) * a.qk_scale_log2 : 0.f;
     }
 
     float m_run[kHeadsPerWarp], l_run[kHeadsPerWarp];
@@ -263,7 +267,7 @@ decode_simt_kernel(const DecodeArgs a) {
         for (int e = 0; e < E; ++e) red[(ptg * G + g) * D + pc * E + e] = acc[g][e];
     __syncthreads();
 
-    for (int i = tid; i < G * D; i += kThreads) {
+    for (int i = tid; i < rows * D; i += kThreads) {
         const int g = i / D, d = i % D;
         float sum = 0.f;
 #pragma unroll
@@ -273,7 +277,7 @@ decode_simt_kernel(const DecodeArgs a) {
         if (direct) {
             static_cast<QT*>(a.out)[qrow(g) * D + d] = to_out<QT>(o);
         } else {  // partial rows of this launch: (b, query g / gh, head)
-            const size_t row = (static_cast<size_t>(b) * Cq + g / gh) * a.num_q_heads + static_cast<size_t>(h) * gh + g % gh;
+            const size_t row = (static_cast<size_t>(b) * Cq + g / gh) * a.num_q_heads + head0 + g % gh;
             a.o_part[(row * a.num_splits + split) * D + d] = o;
             if (d == 0) a.lse_part[row * a.num_splits + split] = l > 0.f ? sM[g] + log2f(l) : -INFINITY;
         }
@@ -346,22 +350,13 @@ cudaError_t launch_one(const DecodeArgs& a, cudaStream_t stream) {
 }
 
 template <int DT, int D>
-cudaError_t by_group(const DecodeArgs& a, cudaStream_t stream) {
-    switch (a.num_queries * (a.num_q_heads / a.num_kv_heads)) {
+cudaError_t by_group(const DecodeArgs& a, int rows, cudaStream_t stream) {
+    switch (rows) {
         case 1: return launch_one<DT, D, 1>(a, stream);
         case 2: return launch_one<DT, D, 2>(a, stream);
         case 4: return launch_one<DT, D, 4>(a, stream);
         case 8: return launch_one<DT, D, 8>(a, stream);
         case 16: return launch_one<DT, D, 16>(a, stream);
-        default: return cudaErrorNotSupported;
-    }
-}
-
-template <int DT>
-cudaError_t by_dim(const DecodeArgs& a, cudaStream_t stream) {
-    switch (a.head_dim) {
-        case 64: return by_group<DT, 64>(a, stream);
-        case 128: return by_group<DT, 128>(a, stream);
         default: return cudaErrorNotSupported;
     }
 }
@@ -383,6 +378,37 @@ bool ok_dim(int d, int g) {
     if (d == 64) return ok_group<DT, 64>(g);
     if (d == 128) return ok_group<DT, 128>(g);
     return false;
+}
+
+// Rows that have a template of their own run as one launch.  Else, for a single
+// query: the heads of a KV head in parts of the largest template, the last part
+// in the smallest that holds it.
+template <int DT, int D>
+cudaError_t by_heads(const DecodeArgs& a, cudaStream_t stream) {
+    const int gh = a.num_q_heads / a.num_kv_heads;
+    if (ok_group<DT, D>(a.num_queries * gh)) return by_group<DT, D>(a, a.num_queries * gh, stream);
+    if (a.num_queries != 1) return cudaErrorNotSupported;
+    int most = kSimtMaxRows;
+    while (!ok_group<DT, D>(most)) most /= 2;
+    for (int h = 0; h < gh; h += most) {
+        DecodeArgs part = a;
+        part.head_first = h;
+        part.head_count = gh - h < most ? gh - h : most;
+        int rows = 1;
+        while (rows < part.head_count) rows *= 2;
+        const cudaError_t e = by_group<DT, D>(part, rows, stream);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+template <int DT>
+cudaError_t by_dim(const DecodeArgs& a, cudaStream_t stream) {
+    switch (a.head_dim) {
+        case 64: return by_heads<DT, 64>(a, stream);
+        case 128: return by_heads<DT, 128>(a, stream);
+        default: return cudaErrorNotSupported;
+    }
 }
 
 }  // namespace

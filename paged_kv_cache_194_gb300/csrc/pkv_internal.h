@@ -78,6 +78,7 @@ struct DecodeArgs {
     // Decode: q_total = num_queries = 1, q_first = len_trim = 0.
     int num_queries;
     int q_total, q_first, len_trim;
+    int head_first, head_count;  // SIMT design, one query: these heads of every KV head's (head_count 0: all)
     int heads_per_cta;        // tensor-core design: 1, or 2 (adjacent KV heads share a CTA; decode, 16-token blocks)
     // Fused append (tensor-core decode): the newest token of sequence b
     // (position seq_lens[b] - 1) has rows new_k / new_v [B][Hkv][D] of dtype

@@ -136,6 +136,30 @@ def test_prefix_heads_and_blocks(q_heads, kv_heads, bs, kv):
     assert bt.pool.errors() == 0
 
 
+@pytest.mark.parametrize("q_heads,kv_heads", [(12, 4), (5, 1), (16, 2), (7, 1), (34, 2), (130, 1)])
+@pytest.mark.parametrize("kv,dim", [("f32", 64), ("f32", 128), ("bf16", 64), ("fp8", 64), ("bf16", 128), ("fp8", 128)])
+def test_prefix_and_decode_any_number_of_heads(q_heads, kv_heads, kv, dim):
+    """Numbers of query heads per KV head without a launch of their own: for
+    every pool, with one split and with several, for one query and for three."""
+    bt = Batch((400, 65, 0, 700, 1), [(0, 2, 64), (3, 5, 640)], q_heads, kv_heads, dim, kv=kv, seed=q_heads)
+    bt.check(bt.run(), bt.design())
+    lens = torch.tensor(bt.lens, dtype=torch.int32).cuda()
+    args = (bt.pool, 1, bt.tables.cuda())
+    for split in (0, 1024, 128):
+        bt.check(pk.paged_decode_attention(bt.q.cuda(), *args, lens, bt.max_len, bt.scale, split_tokens=split), "decode")
+    bt.check(pk.paged_decode_attention(bt.q.cuda(), *args, lens, bt.max_len, bt.scale, algo="simt"), "decode")
+    # three queries: each as a decode call over the tokens that it sees
+    q = torch.stack([bt.q.flip(0), bt.q.flip(1), bt.q], 1).contiguous().cuda()
+    out = pk.paged_multi_query_attention(q, *args, lens, bt.max_len, bt.scale, algo="simt")
+    for c in range(3):
+        one = pk.paged_decode_attention(q[:, c].contiguous(), *args, (lens - 2 + c).clamp(min=0), bt.max_len, bt.scale,
+                                        algo="simt")
+        for b, n in enumerate(bt.lens):
+            if n - 2 + c > 0:
+                assert ((out[b, c] - one[b]).abs() <= TOL[kv] * (1 + one[b].abs())).all()
+    assert bt.pool.errors() == 0
+
+
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
 def test_prefix_many_groups(kv):
     groups = [(0, 9, 320), (9, 9, 64), (9, 12, 1024), (12, 13, 128), (13, 50, 64), (50, 52, 100)]
