@@ -7,6 +7,7 @@
 #include <cstring>
 
 #include "pkv_internal.h"
+#include "step_internal.h"
 
 namespace pkv {
 

@@ -62,7 +62,7 @@ constexpr size_t simt_smem_bytes() {
 
 template <int DT, int D, int G, typename QT>
 __global__ void __launch_bounds__(kThreads)
-decode_simt_kernel(const DecodeArgs a) {
+decode_simt_kernel(const DecodeArgs a, const int head_first, const int head_count) {
     using S = SimtShape<DT, D>;
     using T = KvTraits<DT>;
     constexpr int E = S::E, CPR = S::CPR, LPT = S::LPT, TPP = S::TPP, NTG = S::NTG;
@@ -91,10 +91,10 @@ decode_simt_kernel(const DecodeArgs a) {
     // The rows served here are C queries x gh heads: row g is query
     // q_first + g / gh of the sequence (position L - C + g / gh of the
     // visible length L, attending causally) and head h*gh + g % gh.  A single
-    // query may have fewer rows than G (the others are zero and not written), or
-    // only some of the heads, from head_first on.
-    const int Cq = a.num_queries, gh = a.head_count > 0 ? a.head_count : G / Cq, rows = Cq * gh;
-    const int head0 = a.head_count > 0 ? h * (a.num_q_heads / a.num_kv_heads) + a.head_first : h * gh;
+    // query may have head_count heads from head_first on (0: all), fewer than G:
+    // the other rows are zero and not written.
+    const int Cq = a.num_queries, gh = head_count > 0 ? head_count : G / Cq, rows = Cq * gh;
+    const int head0 = head_count > 0 ? h * (a.num_q_heads / a.num_kv_heads) + head_first : h * gh;
     auto qrow = [&](int g) -> size_t {
         return (static_cast<size_t>(b) * a.q_total + a.q_first + g / gh) * a.num_q_heads + head0 + g % gh;
     };
@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(128) combine_kernel(const DecodeArgs a) {
 }
 
 template <int DT, int D, int G>
-cudaError_t launch_one(const DecodeArgs& a, cudaStream_t stream) {
+cudaError_t launch_one(const DecodeArgs& a, int head_first, int head_count, cudaStream_t stream) {
     if constexpr (!simt_ok<DT, D, G>()) {
         return cudaErrorNotSupported;
     } else {
@@ -344,19 +344,19 @@ cudaError_t launch_one(const DecodeArgs& a, cudaStream_t stream) {
             configured_mask |= 1 << dev;
         }
         dim3 grid(a.num_splits, a.num_kv_heads, a.num_seqs);
-        kern<<<grid, kThreads, smem, stream>>>(a);
+        kern<<<grid, kThreads, smem, stream>>>(a, head_first, head_count);
         return cudaGetLastError();
     }
 }
 
 template <int DT, int D>
-cudaError_t by_group(const DecodeArgs& a, int rows, cudaStream_t stream) {
+cudaError_t by_group(const DecodeArgs& a, int rows, int head_first, int head_count, cudaStream_t stream) {
     switch (rows) {
-        case 1: return launch_one<DT, D, 1>(a, stream);
-        case 2: return launch_one<DT, D, 2>(a, stream);
-        case 4: return launch_one<DT, D, 4>(a, stream);
-        case 8: return launch_one<DT, D, 8>(a, stream);
-        case 16: return launch_one<DT, D, 16>(a, stream);
+        case 1: return launch_one<DT, D, 1>(a, head_first, head_count, stream);
+        case 2: return launch_one<DT, D, 2>(a, head_first, head_count, stream);
+        case 4: return launch_one<DT, D, 4>(a, head_first, head_count, stream);
+        case 8: return launch_one<DT, D, 8>(a, head_first, head_count, stream);
+        case 16: return launch_one<DT, D, 16>(a, head_first, head_count, stream);
         default: return cudaErrorNotSupported;
     }
 }
@@ -386,17 +386,15 @@ bool ok_dim(int d, int g) {
 template <int DT, int D>
 cudaError_t by_heads(const DecodeArgs& a, cudaStream_t stream) {
     const int gh = a.num_q_heads / a.num_kv_heads;
-    if (ok_group<DT, D>(a.num_queries * gh)) return by_group<DT, D>(a, a.num_queries * gh, stream);
+    if (ok_group<DT, D>(a.num_queries * gh)) return by_group<DT, D>(a, a.num_queries * gh, 0, 0, stream);
     if (a.num_queries != 1) return cudaErrorNotSupported;
     int most = kSimtMaxRows;
     while (!ok_group<DT, D>(most)) most /= 2;
     for (int h = 0; h < gh; h += most) {
-        DecodeArgs part = a;
-        part.head_first = h;
-        part.head_count = gh - h < most ? gh - h : most;
+        const int n = gh - h < most ? gh - h : most;
         int rows = 1;
-        while (rows < part.head_count) rows *= 2;
-        const cudaError_t e = by_group<DT, D>(part, rows, stream);
+        while (rows < n) rows *= 2;
+        const cudaError_t e = by_group<DT, D>(a, rows, h, n, stream);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

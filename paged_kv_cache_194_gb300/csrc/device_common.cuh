@@ -172,24 +172,6 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// Launch `kernel` to start as the kernel before it on the stream drains; the
-// kernel waits for that one's results itself (griddepcontrol.wait).
-template <typename... Params, typename... Args>
-inline cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
-                                    Args... args) {
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 // Length a decode kernel uses for sequence b: the device value clamped to
 // [0, max_len] (max_len <= max_blocks * block_size is checked on the host);
 // out-of-range values are flagged once (by the caller passing report = true).

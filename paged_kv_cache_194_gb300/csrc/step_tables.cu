@@ -28,6 +28,7 @@
 // one CTA.  Releases of a quarter of 256 requests: 4.9 us; of 4096 requests'
 // two hundred thousand blocks: 6.6 us.
 #include "device_common.cuh"
+#include "step_internal.h"
 
 namespace pkv {
 namespace {
