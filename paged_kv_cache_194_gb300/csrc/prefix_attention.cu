@@ -97,7 +97,7 @@ constexpr uint32_t kPCol = kTok, kPCols = kTok / 2;
 constexpr uint32_t kOCol = kPCol + kNS * kPCols;
 static_assert(kOCol + kDim == kTmemCols, "tensor memory");
 
-enum Bar { kQReady, kQFree, kOFree, kSRead, kDone, kSFull, kPFull = kSFull + kNS, kPvDone = kPFull + kNS, kKFull = kPvDone + kNS,
+enum Bar { kQReady, kQFree, kOFree, kDone, kSFull, kPFull = kSFull + kNS, kPvDone = kPFull + kNS, kKFull = kPvDone + kNS,
            kVFull = kKFull + kMaxStages,
            // FP8 pools: Q split into E4M3 terms, stages free (BF16 ones are by S done and PV done)
            kQOp = kVFull + kMaxStages, kKEmpty, kVEmpty = kKEmpty + kMaxStages, kNumBars = kVEmpty + kMaxStages };
@@ -199,6 +199,13 @@ __device__ __forceinline__ bool pair_any(int id, bool yes) {
         : "memory");
     return r != 0;
 }
+// "The scores are in registers": the softmax warps pass by (every one of them
+// for every tile, after an expired wait too, so that the meeting always ends),
+// the S warp waits.  At an mbarrier this took 300 to 600 cycles of the chain that
+// sets the pace of shared tiles, here a tenth.
+constexpr int kMeetId = 5, kMeetThreads = kSoftmax + 32;
+__device__ __forceinline__ void scores_read() { asm volatile("barrier.cta.arrive %0, %1;\n" ::"n"(kMeetId), "n"(kMeetThreads) : "memory"); }
+__device__ __forceinline__ void wait_scores_read() { asm volatile("barrier.cta.sync %0, %1;\n" ::"n"(kMeetId), "n"(kMeetThreads) : "memory"); }
 __device__ __forceinline__ void pair_sync(int id) { asm volatile("barrier.cta.sync %0, 64;\n" ::"r"(1 + id) : "memory"); }
 
 // ------------------------------------------------------------------- plan
@@ -584,7 +591,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
     // (kWarpK and behind); its barriers cover what they write.
     if (warp == kWarpS) {
         for (int i = lane; i < kNumBars; i += 32)
-            bar_init(B(i), ((i >= kPFull && i < kPFull + kNS) || i == kOFree || i == kSRead || i == kQOp) ? kSoftmaxWarps
+            bar_init(B(i), ((i >= kPFull && i < kPFull + kNS) || i == kOFree || i == kQOp) ? kSoftmaxWarps
                                                                                            : (i == kDone ? 2u : 1u));
         if (lane == 0) *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
@@ -675,51 +682,59 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                 if (!bar_wait(B(full0 + j % kSt), (j / kSt) & 1)) fail();
     } else if (warp == kWarpS) {
         // ----------------------------------------------------- S = Q K^T
-        if (lane == 0) {
-            bool ok = true;
-            const uint64_t dq = sdesc(sbase, 16);
-            const uint64_t dk0 = sdesc(sbase + kKVOff, 16);
-            constexpr int kSt = stages_of<kFp8>();
-            Seg sg;
-            int k = 0, seg = 0;
-            for (; ok && w.next(a, sg); ++seg) {
-                // This segment's Q rows, once the last S of the one before has read its own.
-                if (seg > 0 && !bar_wait(B(kQFree), (seg - 1) & 1)) {
-                    ok = false;
-                    break;
-                }
-                bar_expect_tx(B(kQReady), static_cast<uint32_t>((sg.own ? 1 : a.seqs_per_tile) * a.gh * kDim * 2));
-                for (int h2 = 0; h2 < 2; ++h2)
-                    tma_4d(sbase + h2 * kQHalf, sg.own ? &tmq_own : &tmq_group, 0, sg.head * a.gh, sg.seq0, h2, B(kQReady));
-                for (int t = 0; t < sg.n; ++t, ++k) {
-                    const int s = k % kNS, st = k % kSt;
-                    // Q (FP8: split), K k, and S k - 1 taken to registers
-                    if (*abort_flag || (t == 0 && !bar_wait(B(kFp8 ? kQOp : kQReady), seg & 1)) ||
-                        !bar_wait(B(kKFull + st), (k / kSt) & 1) ||
-                        (k > 0 && !bar_wait(B(kSRead), (k - 1) & 1))) {
-                        ok = false;
-                        break;
-                    }
-                    fence_after();
-                    const uint64_t dk = dk0 + static_cast<uint64_t>((st * (kFp8 ? 2 * kRawBytes : kStageBytes)) >> 4);
-                    const uint32_t sb = tmem;
-#pragma unroll
-                    for (int ks = 0; ks < 8; ++ks) {  // 16 columns a step; FP8: 32, first of Q's high terms, then of the low ones
-                        const uint32_t kin = (ks & 3) * 32;
-                        if constexpr (kFp8)
-                            mma_f8(sb, dq + (((ks >> 2) * kQHalf + kin) >> 4), dk + (kin >> 4), idesc_f8(kTok, 0), ks > 0 ? 1u : 0u);
-                        else mma_bf16(sb, dq + (((ks >> 2) * kQHalf + kin) >> 4), dk + (((ks >> 2) * kHalfBytes + kin) >> 4),
-                                 idesc(kTok, 0), ks > 0 ? 1u : 0u);
-                    }
-                    mma_commit(B(kSFull + s));
-                    if constexpr (kSt != kNS) mma_commit(B(kKEmpty + st));
-                    if (t == sg.n - 1) mma_commit(B(kQFree));
-                }
-            }
-            if (!ok) {
+        // Lane 0 waits, copies and issues; the warp meets the softmax warps.
+        bool ok = true;
+        const uint64_t dq = sdesc(sbase, 16);
+        const uint64_t dk0 = sdesc(sbase + kKVOff, 16);
+        constexpr int kSt = stages_of<kFp8>();
+        auto check = [&](bool fine) {
+            if (!fine) {
+                ok = false;
                 fail();
-                if (seg > 0) bar_wait(B(kQReady), (seg - 1) & 1);  // (no copy of Q may land after the CTA has gone)
             }
+        };
+        Seg sg;
+        int k = 0, seg = 0, copies = 0;
+        for (; w.next(a, sg); ++seg) {
+            if (lane == 0 && ok) {
+                // This segment's Q rows, once the last S of the one before has read its own.
+                if (seg > 0) check(bar_wait(B(kQFree), (seg - 1) & 1));
+                if (ok) {
+                    bar_expect_tx(B(kQReady), static_cast<uint32_t>((sg.own ? 1 : a.seqs_per_tile) * a.gh * kDim * 2));
+                    for (int h2 = 0; h2 < 2; ++h2)
+                        tma_4d(sbase + h2 * kQHalf, sg.own ? &tmq_own : &tmq_group, 0, sg.head * a.gh, sg.seq0, h2, B(kQReady));
+                    ++copies;
+                }
+            }
+            for (int t = 0; t < sg.n; ++t, ++k) {
+                const int s = k % kNS, st = k % kSt;
+                // Q (FP8: split), K k, and S k - 1 taken to registers
+                if (lane == 0 && ok)
+                    check(!*abort_flag && (t != 0 || bar_wait(B(kFp8 ? kQOp : kQReady), seg & 1)) &&
+                          bar_wait(B(kKFull + st), (k / kSt) & 1));
+                __syncwarp();
+                if (k > 0) wait_scores_read();
+                if (lane != 0 || !ok) continue;
+                fence_after();
+                const uint64_t dk = dk0 + static_cast<uint64_t>((st * (kFp8 ? 2 * kRawBytes : kStageBytes)) >> 4);
+                const uint32_t sb = tmem;
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks) {  // 16 columns a step; FP8: 32, first of Q's high terms, then of the low ones
+                    const uint32_t kin = (ks & 3) * 32;
+                    if constexpr (kFp8)
+                        mma_f8(sb, dq + (((ks >> 2) * kQHalf + kin) >> 4), dk + (kin >> 4), idesc_f8(kTok, 0), ks > 0 ? 1u : 0u);
+                    else mma_bf16(sb, dq + (((ks >> 2) * kQHalf + kin) >> 4), dk + (((ks >> 2) * kHalfBytes + kin) >> 4),
+                             idesc(kTok, 0), ks > 0 ? 1u : 0u);
+                }
+                mma_commit(B(kSFull + s));
+                if constexpr (kSt != kNS) mma_commit(B(kKEmpty + st));
+                if (t == sg.n - 1) mma_commit(B(kQFree));
+            }
+        }
+        __syncwarp();
+        if (k > 0) wait_scores_read();  // (of the last tile)
+        if (lane == 0) {
+            if (!ok && copies > 0) bar_wait(B(kQReady), (copies - 1) & 1);  // (no copy of Q may land after the CTA has gone)
             mma_commit(B(kDone));  // completes once every MMA this thread issued has finished
             if (!bar_wait(B(kDone), 0)) fail();
         }
@@ -853,8 +868,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                     uint32_t v[32];
                     tmem_ld32(sa + 32 * hf, v);
                     fence_before();
-                    __syncwarp();
-                    if (lane == 0) bar_arrive(B(kSRead));
+                    scores_read();
                     const int seen = visible - 32 * hf;  // of this thread's 32 tokens
                     float mx = -INFINITY;
                     if (qk > 0.f) {
@@ -938,8 +952,8 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                             tmem_st32(oa, o);
                         }
                     }
-                } else if (lane == 0) {
-                    bar_arrive(B(kSRead));
+                } else {
+                    scores_read();
                 }
                 if (visible < kTok) {  // V rows past the last token: zero (stale or unwritten rows could hold NaN)
                     constexpr int kSt = stages_of<kFp8>();
