@@ -50,13 +50,14 @@
 //   the same prefix alone                               46 us, floor 20 (products at the measured rate: 18)
 //   64 sequences, 2048 shared, 128 to 2048 own          61 us, floor 43.5
 //   64 sequences, 2048 own tokens, nothing shared       88 us, floor 79.5 (6.1 TB/s)
-//   55 in 8 groups, FP8, 1024 to 8192 shared            63 us, floor 20
+//   55 in 8 groups, FP8, 1024 to 8192 shared            56 us, floor 20
 //   4 sequences, 512 shared, up to 64 own               12 us
 // (paged_decode_attention: 622, 597, 79, 86, 104 and 21.6 us.)  What bounds a
-// shared tile is the chain S issued (750 cycles) - done (450) - taken to
-// registers (200) - seen by the S thread (300 to 600), about 1.1 us a tile and
-// CTA, two CTAs side by side (tensor pipe active 42 %).  A call adds 2.5 us of
-// plan, 2 until the first tiles land, and the merge's 3.
+// shared tile of a BF16 pool is the chain S issued (900 cycles of the S thread,
+// two CTAs side by side) - done (500) - taken to registers (270) - met (100):
+// 1870 cycles a tile and CTA, tensor pipe active 42 %; of an FP8 pool the softmax
+// (250 to load, 850 maxima and exponentials, 550 to split the weights) and its
+// wait.  A call adds 2.5 us of plan, 2 until the first tiles land, and the merge's 3.
 #include <cuda.h>
 
 #include <atomic>
@@ -214,9 +215,8 @@ __device__ __forceinline__ void pair_sync(int id) { asm volatile("barrier.cta.sy
 // cost, every unit being nt + unit_cost long; the last unit_cost places of it
 // hold no tile.  Two tiles' worth for BF16 (64 sequences over 32768 shared
 // tokens: 69, 64, 65 us with 1, 2, 3), five for FP8, where the tiles of
-// full row tiles also take longer than own ones (64 sequences, 2048 shared
-// tokens, own ones up to 2048: 77, 73, 69, 67.5, 68 us with 1 to 5; eight
-// groups over 1024 to 8192 tokens: 74, 67, 65, 64, 61.5).
+// full row tiles also take longer than own ones (the same batch: 80, 78, 77, 79
+// us with 3 to 6; eight groups over 1024 to 8192 tokens: 59, 59, 56, 56).
 int unit_cost_of(pkv_dtype kv) { return kv == PKV_FP8_E4M3 ? 5 : 2; }
 
 // A list of cost T is cut into n = min(T, ctas) ranges, none of them empty, the
@@ -791,7 +791,9 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
         // loop, without waiting or working, only to meet its partner.
         bool dead = false;
         auto wait = [&](int b, int phase) {
-            if (!dead && !bar_wait_warp(B(b), phase & 1)) {
+            // (one look first: passing a barrier that is complete takes a third of
+            // the time that way, and with FP8 pools S mostly is)
+            if (!dead && !__all_sync(0xFFFFFFFFu, bar_test(B(b), phase & 1)) && !bar_wait_warp(B(b), phase & 1)) {
                 dead = true;
                 if (lane == 0) fail();
             }
