@@ -518,6 +518,9 @@ pkv_status kv_bm_check(const pkv_block_manager* bm);
  * keep their bound.  After a call that reported PKV_ERRBIT_TIMEOUT, the
  * workspace's counters may be non-zero (clear them before reusing it), and
  * the output rows of the units the stopped CTAs took part in are unwritten.
+ * paged_prefix_decode_attention's sharing design takes it for a CTA's first wait
+ * for a K tile: the rows that a stopped CTA took part in become NaN, and the
+ * workspace needs no clearing.
  */
 void pkv_set_first_wait_limit_for_testing(int32_t polls, int32_t cta);
 

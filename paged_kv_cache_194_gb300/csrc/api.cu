@@ -730,6 +730,8 @@ pkv_status paged_prefix_decode_attention(const void* q, pkv_dtype q_dtype, const
     a.num_kv_heads = p->d.num_kv_heads;
     a.block_size = p->d.block_size;
     a.num_blocks = p->d.num_blocks;
+    a.test_polls = g_test_wait_polls;
+    a.test_cta = g_test_wait_cta;
     a.gh = num_q_heads / p->d.num_kv_heads;
     a.seqs_per_tile = kPrefixRows / a.gh;
     a.qk_scale_log2 = scale * p->d.k_scale * 1.4426950408889634f;

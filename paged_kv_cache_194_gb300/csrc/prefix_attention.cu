@@ -41,8 +41,9 @@
 // shared memory first, by the softmax warps or by four more, took 2.3 us a tile
 // where this takes 1: the extra 56 KB a tile through shared memory and the
 // waits between the steps.)
-// Every wait is bounded; a CTA whose wait expires sets PKV_ERRBIT_TIMEOUT,
-// waits for its copies and products in flight, frees its TMEM and leaves.
+// Every wait is bounded; a CTA whose wait expires sets PKV_ERRBIT_TIMEOUT, makes
+// its pieces NaN, waits for its copies and products in flight, frees its TMEM
+// and leaves.
 //
 // Measured (calls back to back in a graph; 32 query over 8 KV heads; "floor" is
 // bytes at the measured copy rate):
@@ -103,7 +104,7 @@ enum Bar { kQReady, kQFree, kOFree, kDone, kSFull, kPFull = kSFull + kNS, kPvDon
            // FP8 pools: Q split into E4M3 terms, stages free (BF16 ones are by S done and PV done)
            kQOp = kVFull + kMaxStages, kKEmpty, kVEmpty = kKEmpty + kMaxStages, kNumBars = kVEmpty + kMaxStages };
 constexpr int kBarOff = kKVOff + kNS * kStageBytes;
-constexpr int kExOff = kBarOff + (8 * kNumBars + 8 + 63) / 64 * 64;  // the two threads of a row meet here: maxima
+constexpr int kExOff = kBarOff + (8 * kNumBars + 12 + 63) / 64 * 64;  // the two threads of a row meet here: maxima
 constexpr int kSumOff = kExOff + 2 * kRows * 4;                        // and sums, [2][kRows] floats each
 // The units of this CTA's range, as far as they fit (else the workspace's copy).
 constexpr int kSeqCache = 1024, kGroupCache = 128;
@@ -200,10 +201,29 @@ __device__ __forceinline__ bool pair_any(int id, bool yes) {
         : "memory");
     return r != 0;
 }
-// "The scores are in registers": the softmax warps pass by (every one of them
-// for every tile, after an expired wait too, so that the meeting always ends),
-// the S warp waits.  At an mbarrier this took 300 to 600 cycles of the chain that
-// sets the pace of shared tiles, here a tenth.
+// A wait that also ends when another role of the CTA has given up (a poll lasts
+// about 1.5 us, so within 0.1 ms).
+__device__ __forceinline__ bool bar_wait_or(uint32_t b, uint32_t parity, const volatile int* abort_flag, uint32_t polls = kSpin) {
+    for (uint32_t i = 0; i < polls; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(ok)
+            : "r"(b), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        if ((i & 63u) == 63u && *abort_flag) break;
+    }
+    return false;
+}
+// "The scores are in registers": the softmax warps pass by, the S warp waits.  At
+// an mbarrier this took 300 to 600 cycles of the chain that sets the pace of
+// shared tiles, here a tenth.  A warp passes for tile k + 1 only once S k + 1 is
+// done, and the S warp has met all of them for tile k before it issues that, so
+// no one is counted twice.  This wait has no bound of its own: a warp that gave up
+// passes no more, the S warp comes to no other meeting once it sees the abort
+// flag, and where it is at one already, softmax warp 0 passes for the others
+// until it leaves (see the end of the softmax part).
 constexpr int kMeetId = 5, kMeetThreads = kSoftmax + 32;
 __device__ __forceinline__ void scores_read() { asm volatile("barrier.cta.arrive %0, %1;\n" ::"n"(kMeetId), "n"(kMeetThreads) : "memory"); }
 __device__ __forceinline__ void wait_scores_read() { asm volatile("barrier.cta.sync %0, %1;\n" ::"n"(kMeetId), "n"(kMeetThreads) : "memory"); }
@@ -584,6 +604,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
     auto B = [&](int i) { return bars + 8u * i; };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kBarOff + 8 * kNumBars);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kBarOff + 8 * kNumBars + 4);
+    volatile int* s_done = abort_flag + 1;  // the S warp comes to no other meeting
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     const Early early = fetch_early(a);  // (under way while the CTA sets itself up)
@@ -593,7 +614,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
         for (int i = lane; i < kNumBars; i += 32)
             bar_init(B(i), ((i >= kPFull && i < kPFull + kNS) || i == kOFree || i == kQOp) ? kSoftmaxWarps
                                                                                            : (i == kDone ? 2u : 1u));
-        if (lane == 0) *abort_flag = 0;
+        if (lane == 0) *abort_flag = *s_done = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
     if (warp >= kWarpK && lane == 0) {  // (the descriptors are fetched while the plan is made)
@@ -651,7 +672,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                     cache = idx < a.max_blocks ? __ldg(a.tables + static_cast<size_t>(sg.row) * a.max_blocks + idx) : 0;
                 }
                 if (__any_sync(0xFFFFFFFFu, *abort_flag != 0) ||
-                    (k >= kSt && !bar_wait_warp(B(empty0 + s), ((k / kSt) - 1) & 1))) {
+                    (k >= kSt && !__all_sync(0xFFFFFFFFu, bar_wait_or(B(empty0 + s), ((k / kSt) - 1) & 1, abort_flag)))) {
                     ok = false;
                     break;
                 }
@@ -683,22 +704,19 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
     } else if (warp == kWarpS) {
         // ----------------------------------------------------- S = Q K^T
         // Lane 0 waits, copies and issues; the warp meets the softmax warps.
-        bool ok = true;
+        bool ok = true;  // of the warp
         const uint64_t dq = sdesc(sbase, 16);
         const uint64_t dk0 = sdesc(sbase + kKVOff, 16);
         constexpr int kSt = stages_of<kFp8>();
-        auto check = [&](bool fine) {
-            if (!fine) {
-                ok = false;
-                fail();
-            }
-        };
+        // (test hook: this CTA's first wait for a tile may be cut short)
+        const uint32_t first_polls =
+            a.test_polls >= 0 && (a.test_cta < 0 || a.test_cta == static_cast<int>(blockIdx.x)) ? a.test_polls : kSpin;
         Seg sg;
         int k = 0, seg = 0, copies = 0;
-        for (; w.next(a, sg); ++seg) {
-            if (lane == 0 && ok) {
+        for (; ok && w.next(a, sg); ++seg) {
+            if (lane == 0) {
                 // This segment's Q rows, once the last S of the one before has read its own.
-                if (seg > 0) check(bar_wait(B(kQFree), (seg - 1) & 1));
+                ok = seg == 0 || bar_wait_or(B(kQFree), (seg - 1) & 1, abort_flag);
                 if (ok) {
                     bar_expect_tx(B(kQReady), static_cast<uint32_t>((sg.own ? 1 : a.seqs_per_tile) * a.gh * kDim * 2));
                     for (int h2 = 0; h2 < 2; ++h2)
@@ -709,12 +727,13 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
             for (int t = 0; t < sg.n; ++t, ++k) {
                 const int s = k % kNS, st = k % kSt;
                 // Q (FP8: split), K k, and S k - 1 taken to registers
-                if (lane == 0 && ok)
-                    check(!*abort_flag && (t != 0 || bar_wait(B(kFp8 ? kQOp : kQReady), seg & 1)) &&
-                          bar_wait(B(kKFull + st), (k / kSt) & 1));
-                __syncwarp();
+                if (lane == 0)
+                    ok = ok && !*abort_flag && (t != 0 || bar_wait_or(B(kFp8 ? kQOp : kQReady), seg & 1, abort_flag)) &&
+                         bar_wait_or(B(kKFull + st), (k / kSt) & 1, abort_flag, k == 0 ? first_polls : kSpin);
+                ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
+                if (!ok) break;
                 if (k > 0) wait_scores_read();
-                if (lane != 0 || !ok) continue;
+                if (lane != 0) continue;
                 fence_after();
                 const uint64_t dk = dk0 + static_cast<uint64_t>((st * (kFp8 ? 2 * kRawBytes : kStageBytes)) >> 4);
                 const uint32_t sb = tmem;
@@ -731,10 +750,14 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                 if (t == sg.n - 1) mma_commit(B(kQFree));
             }
         }
-        __syncwarp();
-        if (k > 0) wait_scores_read();  // (of the last tile)
+        ok = __shfl_sync(0xFFFFFFFFu, ok && !*abort_flag ? 1 : 0, 0) != 0;
+        if (ok && k > 0) wait_scores_read();  // (of the last tile)
         if (lane == 0) {
-            if (!ok && copies > 0) bar_wait(B(kQReady), (copies - 1) & 1);  // (no copy of Q may land after the CTA has gone)
+            *s_done = 1;
+            if (!ok) {
+                fail();
+                if (copies > 0) bar_wait(B(kQReady), (copies - 1) & 1);  // (no copy of Q may land after the CTA has gone)
+            }
             mma_commit(B(kDone));  // completes once every MMA this thread issued has finished
             if (!bar_wait(B(kDone), 0)) fail();
         }
@@ -751,9 +774,9 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                 for (int t = 0; t < sg.n; ++t, ++k) {
                     const int s = k % kNS, st = k % kSt;
                     // V k, P k, and for a new segment an O that has been read out
-                    if (*abort_flag || !bar_wait(B(kVFull + st), (k / kSt) & 1) ||
-                        !bar_wait(B(kPFull + s), (k / kNS) & 1) ||
-                        (t == 0 && seg > 0 && !bar_wait(B(kOFree), (seg - 1) & 1))) {
+                    if (*abort_flag || !bar_wait_or(B(kVFull + st), (k / kSt) & 1, abort_flag) ||
+                        !bar_wait_or(B(kPFull + s), (k / kNS) & 1, abort_flag) ||
+                        (t == 0 && seg > 0 && !bar_wait_or(B(kOFree), (seg - 1) & 1, abort_flag))) {
                         ok = false;
                         break;
                     }
@@ -793,10 +816,15 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
         auto wait = [&](int b, int phase) {
             // (one look first: passing a barrier that is complete takes a third of
             // the time that way, and with FP8 pools S mostly is)
-            if (!dead && !__all_sync(0xFFFFFFFFu, bar_test(B(b), phase & 1)) && !bar_wait_warp(B(b), phase & 1)) {
+            if (!dead && !__all_sync(0xFFFFFFFFu, bar_test(B(b), phase & 1)) &&
+                !__all_sync(0xFFFFFFFFu, bar_wait_or(B(b), phase & 1, abort_flag))) {
                 dead = true;
                 if (lane == 0) fail();
+                __syncwarp();
             }
+        };
+        auto pass = [&]() {
+            if (!dead) scores_read();
         };
 
         // FP8 pools: the tensor cores take K and V as stored, and one type for
@@ -870,7 +898,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                     uint32_t v[32];
                     tmem_ld32(sa + 32 * hf, v);
                     fence_before();
-                    scores_read();
+                    pass();
                     const int seen = visible - 32 * hf;  // of this thread's 32 tokens
                     float mx = -INFINITY;
                     if (qk > 0.f) {
@@ -955,7 +983,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                         }
                     }
                 } else {
-                    scores_read();
+                    pass();
                 }
                 if (visible < kTok) {  // V rows past the last token: zero (stale or unwritten rows could hold NaN)
                     constexpr int kSt = stages_of<kFp8>();
@@ -1015,7 +1043,11 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                         }
                     }
                 }
-                if (m < nv && hf == 0) (sg.own ? a.own_lse : a.pre_lse)[row0 + lane] = l > 0.f ? m_used - weight_shift_of<kFp8>() + log2f(l) : -INFINITY;
+                // (NaN from a CTA that gave up: its rows must not look like results)
+                if (m < nv && hf == 0)
+                    (sg.own ? a.own_lse : a.pre_lse)[row0 + lane] =
+                        dead || *abort_flag != 0 ? __uint_as_float(0x7FC00000u)
+                                                 : (l > 0.f ? m_used - weight_shift_of<kFp8>() + log2f(l) : -INFINITY);
             } else if (lane == 0) {
                 bar_arrive(B(kOFree));
             }
@@ -1023,6 +1055,15 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
             sg = nx;
             has = has_next;
         }
+        // Every tile is behind this warp.  In a CTA that gave up the S warp may
+        // be at a meeting that others no longer come to; it needs eight of these at
+        // most, and looks at the flag before the next.
+        if (warp == 0)
+            for (uint32_t i = 0; *s_done == 0 && i < kSpin; ++i) {
+                if (*abort_flag != 0) scores_read();
+                __nanosleep(500);
+                __syncwarp();
+            }
     }
     fence_before();
     __syncthreads();

@@ -43,6 +43,7 @@ struct PrefixArgs {
     int ctas;                      // CTAs of the attention kernel
     int unit_cost;                 // cost of a unit beside its tiles, in tiles (set by the launch)
     float qk_scale_log2, v_scale;
+    int test_polls, test_cta;      // test hook: polls of that CTA's (< 0: every CTA's) first wait for a tile; < 0: none
     // workspace: the plan ...
     int32_t* totals;               // cost of the whole list
     int2* seqs;                    // [B] {clamped length, tiles read with the group}

@@ -1,6 +1,7 @@
 """GPU parity of decode attention over shared prefixes against 64-bit softmax
 attention of every sequence on its own, and against paged_decode_attention."""
 import itertools
+import time
 
 import pytest
 import torch
@@ -381,3 +382,31 @@ def test_prefix_many_segments_of_many_tiles(kv):
     bt.prefix.zero_()  # nothing shared: own units only
     bt.check(bt.run(), "tc")
     assert bt.pool.errors() == 0
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("cta", [0, 7, 200, -1])
+def test_prefix_expired_waits(kv, cta):
+    """The failure path on demand: one CTA's first wait for a tile (or every
+    one's) gives up.  The call returns with the timeout bit set, rows that the
+    CTA took part in are NaN and all others right; the next call is right."""
+    # (long enough that every CTA of a full GPU has a tile: its range is longer than the cost of a unit's end)
+    bt = Batch((12000, 10500, 8192, 8400, 11600, 70, 0), [(0, 5, 8192)], 32, 8, bs=64, kv=kv, seed=9)
+    ws = pk.prefix_decode_workspace(bt.pool, len(bt.lens), 1, 32, bt.max_len)
+    good = bt.run(workspace=ws)
+    bt.check(good, "tc")
+    try:
+        pk.set_first_wait_limit_for_testing(0, cta)
+        t0 = time.perf_counter()
+        out = bt.run(workspace=ws)
+        torch.cuda.synchronize()
+        dt = time.perf_counter() - t0
+    finally:
+        pk.set_first_wait_limit_for_testing(-1)
+    assert dt < 5.0
+    assert bt.pool.errors() == pk.ERRBIT_TIMEOUT
+    lost = torch.isnan(out).any(2)
+    assert torch.isnan(out[lost]).all() and torch.equal(out[~lost], good[~lost])
+    assert lost.any() and (lost[:6].all() if cta < 0 else not lost.all()) and not lost[6].any()
+    bt.pool.clear_errors()
+    assert torch.equal(bt.run(workspace=ws), good) and bt.pool.errors() == 0
