@@ -220,10 +220,10 @@ __device__ __forceinline__ bool bar_wait_or(uint32_t b, uint32_t parity, const v
 // an mbarrier this took 300 to 600 cycles of the chain that sets the pace of
 // shared tiles, here a tenth.  A warp passes for tile k + 1 only once S k + 1 is
 // done, and the S warp has met all of them for tile k before it issues that, so
-// no one is counted twice.  This wait has no bound of its own: a warp that gave up
-// passes no more, the S warp comes to no other meeting once it sees the abort
-// flag, and where it is at one already, softmax warp 0 passes for the others
-// until it leaves (see the end of the softmax part).
+// no one is counted twice.  This wait has no bound of its own.  In a CTA that gave
+// up, softmax warps run ahead and count for others, so the S warp, which comes to
+// a meeting or two after the abort flag is up, could be left waiting at one:
+// softmax warp 0 then passes until it leaves (at the end of the softmax part).
 constexpr int kMeetId = 5, kMeetThreads = kSoftmax + 32;
 __device__ __forceinline__ void scores_read() { asm volatile("barrier.cta.arrive %0, %1;\n" ::"n"(kMeetId), "n"(kMeetThreads) : "memory"); }
 __device__ __forceinline__ void wait_scores_read() { asm volatile("barrier.cta.sync %0, %1;\n" ::"n"(kMeetId), "n"(kMeetThreads) : "memory"); }
@@ -730,24 +730,29 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                 if (lane == 0)
                     ok = ok && !*abort_flag && (t != 0 || bar_wait_or(B(kFp8 ? kQOp : kQReady), seg & 1, abort_flag)) &&
                          bar_wait_or(B(kKFull + st), (k / kSt) & 1, abort_flag, k == 0 ? first_polls : kSpin);
-                ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
-                if (!ok) break;
+                __syncwarp();
                 if (k > 0) wait_scores_read();
-                if (lane != 0) continue;
-                fence_after();
-                const uint64_t dk = dk0 + static_cast<uint64_t>((st * (kFp8 ? 2 * kRawBytes : kStageBytes)) >> 4);
-                const uint32_t sb = tmem;
+                if (lane == 0 && ok) {
+                    fence_after();
+                    const uint64_t dk = dk0 + static_cast<uint64_t>((st * (kFp8 ? 2 * kRawBytes : kStageBytes)) >> 4);
+                    const uint32_t sb = tmem;
 #pragma unroll
-                for (int ks = 0; ks < 8; ++ks) {  // 16 columns a step; FP8: 32, first of Q's high terms, then of the low ones
-                    const uint32_t kin = (ks & 3) * 32;
-                    if constexpr (kFp8)
-                        mma_f8(sb, dq + (((ks >> 2) * kQHalf + kin) >> 4), dk + (kin >> 4), idesc_f8(kTok, 0), ks > 0 ? 1u : 0u);
-                    else mma_bf16(sb, dq + (((ks >> 2) * kQHalf + kin) >> 4), dk + (((ks >> 2) * kHalfBytes + kin) >> 4),
-                             idesc(kTok, 0), ks > 0 ? 1u : 0u);
+                    for (int ks = 0; ks < 8; ++ks) {  // 16 columns a step; FP8: 32, first of Q's high terms, then of the low ones
+                        const uint32_t kin = (ks & 3) * 32;
+                        if constexpr (kFp8)
+                            mma_f8(sb, dq + (((ks >> 2) * kQHalf + kin) >> 4), dk + (kin >> 4), idesc_f8(kTok, 0), ks > 0 ? 1u : 0u);
+                        else mma_bf16(sb, dq + (((ks >> 2) * kQHalf + kin) >> 4), dk + (((ks >> 2) * kHalfBytes + kin) >> 4),
+                                 idesc(kTok, 0), ks > 0 ? 1u : 0u);
+                    }
+                    mma_commit(B(kSFull + s));
+                    if constexpr (kSt != kNS) mma_commit(B(kKEmpty + st));
+                    if (t == sg.n - 1) mma_commit(B(kQFree));
                 }
-                mma_commit(B(kSFull + s));
-                if constexpr (kSt != kNS) mma_commit(B(kKEmpty + st));
-                if (t == sg.n - 1) mma_commit(B(kQFree));
+                // (here, while S k runs: before the meeting a vote would cost 100 cycles a tile)
+                if (!__all_sync(0xFFFFFFFFu, ok)) {
+                    ok = false;
+                    break;
+                }
             }
         }
         ok = __shfl_sync(0xFFFFFFFFu, ok && !*abort_flag ? 1 : 0, 0) != 0;
@@ -823,9 +828,6 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                 __syncwarp();
             }
         };
-        auto pass = [&]() {
-            if (!dead) scores_read();
-        };
 
         // FP8 pools: the tensor cores take K and V as stored, and one type for
         // both operands.  A query row is scaled by the power of two that brings
@@ -898,7 +900,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                     uint32_t v[32];
                     tmem_ld32(sa + 32 * hf, v);
                     fence_before();
-                    pass();
+                    scores_read();
                     const int seen = visible - 32 * hf;  // of this thread's 32 tokens
                     float mx = -INFINITY;
                     if (qk > 0.f) {
@@ -983,7 +985,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                         }
                     }
                 } else {
-                    pass();
+                    scores_read();
                 }
                 if (visible < kTok) {  // V rows past the last token: zero (stale or unwritten rows could hold NaN)
                     constexpr int kSt = stages_of<kFp8>();
@@ -1055,9 +1057,8 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
             sg = nx;
             has = has_next;
         }
-        // Every tile is behind this warp.  In a CTA that gave up the S warp may
-        // be at a meeting that others no longer come to; it needs eight of these at
-        // most, and looks at the flag before the next.
+        // Every tile is behind this warp.  In a CTA that gave up the S warp may be
+        // at a meeting whose passes are all spent: nine of these end any.
         if (warp == 0)
             for (uint32_t i = 0; *s_done == 0 && i < kSpin; ++i) {
                 if (*abort_flag != 0) scores_read();
