@@ -47,11 +47,11 @@
 //
 // Measured (calls back to back in a graph; 32 query over 8 KV heads; "floor" is
 // bytes at the measured copy rate):
-//   64 sequences, 32768 shared tokens, up to 1024 own   64 us, floor 40 us
+//   64 sequences, 32768 shared tokens, up to 1024 own   65 us, floor 40 us
 //   the same prefix alone                               46 us, floor 20 (products at the measured rate: 18)
-//   64 sequences, 2048 shared, 128 to 2048 own          61 us, floor 43.5
+//   64 sequences, 2048 shared, 128 to 2048 own          62 us, floor 43.5
 //   64 sequences, 2048 own tokens, nothing shared       88 us, floor 79.5 (6.1 TB/s)
-//   55 in 8 groups, FP8, 1024 to 8192 shared            56 us, floor 20
+//   55 in 8 groups, FP8, 1024 to 8192 shared            53 us, floor 20
 //   4 sequences, 512 shared, up to 64 own               12 us
 // (paged_decode_attention: 622, 597, 79, 86, 104 and 21.6 us.)  What bounds a
 // shared tile of a BF16 pool is the chain S issued (900 cycles of the S thread,
@@ -221,9 +221,9 @@ __device__ __forceinline__ bool bar_wait_or(uint32_t b, uint32_t parity, const v
 // shared tiles, here a tenth.  A warp passes for tile k + 1 only once S k + 1 is
 // done, and the S warp has met all of them for tile k before it issues that, so
 // no one is counted twice.  This wait has no bound of its own.  In a CTA that gave
-// up, softmax warps run ahead and count for others, so the S warp, which comes to
-// a meeting or two after the abort flag is up, could be left waiting at one:
-// softmax warp 0 then passes until it leaves (at the end of the softmax part).
+// up, softmax warps run ahead and count for others, so the S warp could be left
+// waiting: softmax warp 0 then passes until it leaves (at the end of the softmax
+// part).
 constexpr int kMeetId = 5, kMeetThreads = kSoftmax + 32;
 __device__ __forceinline__ void scores_read() { asm volatile("barrier.cta.arrive %0, %1;\n" ::"n"(kMeetId), "n"(kMeetThreads) : "memory"); }
 __device__ __forceinline__ void wait_scores_read() { asm volatile("barrier.cta.sync %0, %1;\n" ::"n"(kMeetId), "n"(kMeetThreads) : "memory"); }
@@ -703,20 +703,28 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                 if (!bar_wait(B(full0 + j % kSt), (j / kSt) & 1)) fail();
     } else if (warp == kWarpS) {
         // ----------------------------------------------------- S = Q K^T
-        // Lane 0 waits, copies and issues; the warp meets the softmax warps.
-        bool ok = true;  // of the warp
+        // Lane 0 waits, copies and issues; the warp meets the softmax warps.  (After
+        // an expired wait it meets them to the end of the segment: a vote of the warp
+        // per tile, wherever it stood, cost 1 to 2 % of long shared prefixes.)
+        bool ok = true;
         const uint64_t dq = sdesc(sbase, 16);
         const uint64_t dk0 = sdesc(sbase + kKVOff, 16);
         constexpr int kSt = stages_of<kFp8>();
+        auto check = [&](bool fine) {
+            if (!fine) {
+                ok = false;
+                fail();
+            }
+        };
         // (test hook: this CTA's first wait for a tile may be cut short)
         const uint32_t first_polls =
             a.test_polls >= 0 && (a.test_cta < 0 || a.test_cta == static_cast<int>(blockIdx.x)) ? a.test_polls : kSpin;
         Seg sg;
         int k = 0, seg = 0, copies = 0;
-        for (; ok && w.next(a, sg); ++seg) {
+        for (; __all_sync(0xFFFFFFFFu, ok) && w.next(a, sg); ++seg) {
             if (lane == 0) {
                 // This segment's Q rows, once the last S of the one before has read its own.
-                ok = seg == 0 || bar_wait_or(B(kQFree), (seg - 1) & 1, abort_flag);
+                if (seg > 0) check(bar_wait_or(B(kQFree), (seg - 1) & 1, abort_flag));
                 if (ok) {
                     bar_expect_tx(B(kQReady), static_cast<uint32_t>((sg.own ? 1 : a.seqs_per_tile) * a.gh * kDim * 2));
                     for (int h2 = 0; h2 < 2; ++h2)
@@ -727,33 +735,28 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
             for (int t = 0; t < sg.n; ++t, ++k) {
                 const int s = k % kNS, st = k % kSt;
                 // Q (FP8: split), K k, and S k - 1 taken to registers
-                if (lane == 0)
-                    ok = ok && !*abort_flag && (t != 0 || bar_wait_or(B(kFp8 ? kQOp : kQReady), seg & 1, abort_flag)) &&
-                         bar_wait_or(B(kKFull + st), (k / kSt) & 1, abort_flag, k == 0 ? first_polls : kSpin);
+                if (lane == 0 && ok)
+                    check(!*abort_flag && (t != 0 || bar_wait_or(B(kFp8 ? kQOp : kQReady), seg & 1, abort_flag)) &&
+                          bar_wait_or(B(kKFull + st), (k / kSt) & 1, abort_flag, k == 0 ? first_polls : kSpin));
                 __syncwarp();
                 if (k > 0) wait_scores_read();
-                if (lane == 0 && ok) {
-                    fence_after();
-                    const uint64_t dk = dk0 + static_cast<uint64_t>((st * (kFp8 ? 2 * kRawBytes : kStageBytes)) >> 4);
-                    const uint32_t sb = tmem;
+                if (lane != 0 || !ok) continue;
+                fence_after();
+                const uint64_t dk = dk0 + static_cast<uint64_t>((st * (kFp8 ? 2 * kRawBytes : kStageBytes)) >> 4);
+                const uint32_t sb = tmem;
 #pragma unroll
-                    for (int ks = 0; ks < 8; ++ks) {  // 16 columns a step; FP8: 32, first of Q's high terms, then of the low ones
-                        const uint32_t kin = (ks & 3) * 32;
-                        if constexpr (kFp8)
-                            mma_f8(sb, dq + (((ks >> 2) * kQHalf + kin) >> 4), dk + (kin >> 4), idesc_f8(kTok, 0), ks > 0 ? 1u : 0u);
-                        else mma_bf16(sb, dq + (((ks >> 2) * kQHalf + kin) >> 4), dk + (((ks >> 2) * kHalfBytes + kin) >> 4),
-                                 idesc(kTok, 0), ks > 0 ? 1u : 0u);
-                    }
-                    mma_commit(B(kSFull + s));
-                    if constexpr (kSt != kNS) mma_commit(B(kKEmpty + st));
-                    if (t == sg.n - 1) mma_commit(B(kQFree));
+                for (int ks = 0; ks < 8; ++ks) {  // 16 columns a step; FP8: 32, first of Q's high terms, then of the low ones
+                    const uint32_t kin = (ks & 3) * 32;
+                    if constexpr (kFp8)
+                        mma_f8(sb, dq + (((ks >> 2) * kQHalf + kin) >> 4), dk + (kin >> 4), idesc_f8(kTok, 0), ks > 0 ? 1u : 0u);
+                    else mma_bf16(sb, dq + (((ks >> 2) * kQHalf + kin) >> 4), dk + (((ks >> 2) * kHalfBytes + kin) >> 4),
+                             idesc(kTok, 0), ks > 0 ? 1u : 0u);
                 }
-                // (here, while S k runs: before the meeting a vote would cost 100 cycles a tile)
-                if (!__all_sync(0xFFFFFFFFu, ok)) {
-                    ok = false;
-                    break;
-                }
+                mma_commit(B(kSFull + s));
+                if constexpr (kSt != kNS) mma_commit(B(kKEmpty + st));
+                if (t == sg.n - 1) mma_commit(B(kQFree));
             }
+            __syncwarp();
         }
         ok = __shfl_sync(0xFFFFFFFFu, ok && !*abort_flag ? 1 : 0, 0) != 0;
         if (ok && k > 0) wait_scores_read();  // (of the last tile)
@@ -1058,11 +1061,12 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
             has = has_next;
         }
         // Every tile is behind this warp.  In a CTA that gave up the S warp may be
-        // at a meeting whose passes are all spent: nine of these end any.
+        // at a meeting whose passes are all spent, with more of its segment to come:
+        // nine of these end any.
         if (warp == 0)
-            for (uint32_t i = 0; *s_done == 0 && i < kSpin; ++i) {
+            for (uint32_t i = 0; *s_done == 0 && i < 64 * kSpin; ++i) {
                 if (*abort_flag != 0) scores_read();
-                __nanosleep(500);
+                __nanosleep(100);
                 __syncwarp();
             }
     }
