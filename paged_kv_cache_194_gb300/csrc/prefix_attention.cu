@@ -1064,10 +1064,9 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
         // at a meeting whose passes are all spent, with more of its segment to come:
         // nine of these end any.
         if (warp == 0)
-            for (uint32_t i = 0; *s_done == 0 && i < 64 * kSpin; ++i) {
-                if (*abort_flag != 0) scores_read();
+            for (uint32_t i = 0; __any_sync(0xFFFFFFFFu, *s_done == 0) && i < 64 * kSpin; ++i) {
+                if (__any_sync(0xFFFFFFFFu, *abort_flag != 0)) scores_read();
                 __nanosleep(100);
-                __syncwarp();
             }
     }
     fence_before();
