@@ -34,13 +34,15 @@
 //    tensor memory as BF16 pairs (at most 2^-8 of each weight; the sum l is
 //    taken in fp32 before that rounding), the running maximum moved only when
 //    it grows by more than 8, so that O is seldom rescaled.
-// FP8 pools: the tensor cores multiply K and V as stored (kind f8f6f4, E4M3
-// operands), half the bytes in the ring; Q and P enter as the sum of two E4M3
-// terms, so S is two passes over K's 128 columns, 32 a step, and PV two over the
-// 64 tokens: as many instructions as for BF16.  (Tiles converted to FP16 in
-// shared memory first, by the softmax warps or by four more, took 2.3 us a tile
-// where this takes 1: the extra 56 KB a tile through shared memory and the
-// waits between the steps.)
+// FP8 pools: the tensor cores multiply K as stored (kind f8f6f4, E4M3
+// operands); Q enters as the sum of two E4M3 terms, so S is two passes over K's
+// 128 columns, 32 a step: as many instructions as for BF16.  The weights need
+// more range than E4M3 has: below 2^-15 of a row's largest a sum of two E4M3
+// terms is zero, and with one key 11 nats above 8192 others nine tenths of the
+// output were lost.  Hence P is FP16, and the softmax warps write each V tile as
+// FP16 (exactly) to shared memory for PV.  (That takes 4 us more than two E4M3
+// terms on prefixes or own tokens alone, 6 to 7 %, and 4 us less where both are
+// mixed.)
 // Every wait is bounded; a CTA whose wait expires sets PKV_ERRBIT_TIMEOUT, makes
 // its pieces NaN, waits for its copies and products in flight, frees its TMEM
 // and leaves.
@@ -51,14 +53,14 @@
 //   the same prefix alone                               46 us, floor 20 (products at the measured rate: 18)
 //   64 sequences, 2048 shared, 128 to 2048 own          62 us, floor 43.5
 //   64 sequences, 2048 own tokens, nothing shared       88 us, floor 79.5 (6.1 TB/s)
-//   55 in 8 groups, FP8, 1024 to 8192 shared            53 us, floor 20
+//   55 in 8 groups, FP8, 1024 to 8192 shared            50 us, floor 20
 //   4 sequences, 512 shared, up to 64 own               12 us
 // (paged_decode_attention: 622, 597, 79, 86, 104 and 21.6 us.)  What bounds a
 // shared tile of a BF16 pool is the chain S issued (900 cycles of the S thread,
 // two CTAs side by side) - done (500) - taken to registers (270) - met (100):
 // 1870 cycles a tile and CTA, tensor pipe active 42 %; of an FP8 pool the softmax
-// (250 to load, 850 maxima and exponentials, 550 to split the weights) and its
-// wait.  A call adds 2.5 us of plan, 2 until the first tiles land, and the merge's 3.
+// (250 to load, 850 maxima and exponentials, then the weights and the V tile).
+// A call adds 2.5 us of plan, 2 until the first tiles land, and the merge's 3.
 #include <cuda.h>
 
 #include <atomic>
@@ -78,16 +80,14 @@ constexpr int kThreads = kSoftmax + 128;
 constexpr int kRows = kPrefixRows;
 constexpr int kTok = 64;
 constexpr int kDim = 128;
-constexpr int kNS = 2;                        // P buffers, and stages of the BF16 rings
-constexpr int kMaxStages = 4;
-template <bool kFp8>
-constexpr int stages_of() { return kFp8 ? kMaxStages : kNS; }  // of the K ring, and of the V ring: 64 KB both ways
+constexpr int kNS = 2;                        // P buffers, stages of the K ring and of the V ring
 constexpr int kQHalf = kRows * 128;           // one 64-column half of the Q tile
 constexpr int kHalfBytes = kTok * 128;        // one 64-column half of a K or V tile
 constexpr int kKVOff = 2 * kQHalf;
 constexpr int kStageBytes = 4 * kHalfBytes;   // K + V
 constexpr int kRawBytes = kTok * kDim;        // FP8 pools: a K or V tile, [64 rows][128 bytes]
-static_assert(kNS * kStageBytes == kMaxStages * 2 * kRawBytes, "one ring size");
+constexpr int kWideOff = kKVOff + kNS * 2 * kRawBytes;  // and behind their rings V tiles in FP16, as BF16 ones lie
+static_assert(kNS * (2 * kRawBytes + 2 * kHalfBytes) == kNS * kStageBytes, "64 KB either way");
 constexpr int kAlignSlack = 1024;
 static_assert(12 * kPrefixMaxSeqs + 24 * kPrefixMaxGroups <= kNS * kStageBytes, "the plan fits into the ring");
 // Tensor memory: the scores of one tile, two P buffers, O.  The softmax takes the
@@ -100,9 +100,9 @@ constexpr uint32_t kOCol = kPCol + kNS * kPCols;
 static_assert(kOCol + kDim == kTmemCols, "tensor memory");
 
 enum Bar { kQReady, kQFree, kOFree, kDone, kSFull, kPFull = kSFull + kNS, kPvDone = kPFull + kNS, kKFull = kPvDone + kNS,
-           kVFull = kKFull + kMaxStages,
-           // FP8 pools: Q split into E4M3 terms, stages free (BF16 ones are by S done and PV done)
-           kQOp = kVFull + kMaxStages, kKEmpty, kVEmpty = kKEmpty + kMaxStages, kNumBars = kVEmpty + kMaxStages };
+           kVFull = kKFull + kNS,
+           // FP8 pools: Q split into E4M3 terms, V stages that the softmax warps have read
+           kQOp = kVFull + kNS, kVEmpty, kNumBars = kVEmpty + kNS };
 constexpr int kBarOff = kKVOff + kNS * kStageBytes;
 constexpr int kExOff = kBarOff + (8 * kNumBars + 12 + 63) / 64 * 64;  // the two threads of a row meet here: maxima
 constexpr int kSumOff = kExOff + 2 * kRows * 4;                        // and sums, [2][kRows] floats each
@@ -149,24 +149,14 @@ __device__ __forceinline__ void tmem_ld_16x64(uint32_t a, uint32_t (&v)[32]) {
         : "r"(a));
     asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
 }
-// Instruction descriptor: E4M3 x E4M3 -> F32, otherwise as idesc().
-constexpr uint32_t idesc_f8(int n, int b_mn) { return idesc(n, b_mn) & ~((1u << 7) | (1u << 10)); }
+// Instruction descriptor with operand formats 0, otherwise as idesc(): E4M3 x
+// E4M3 -> F32 for kind f8f6f4, F16 x F16 -> F32 for kind f16.
+constexpr uint32_t idesc0(int n, int b_mn) { return idesc(n, b_mn) & ~((1u << 7) | (1u << 10)); }
 __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
     asm volatile(
         "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
         "l"(a), "l"(b), "r"(id), "r"(acc)
         : "memory");
-}
-__device__ __forceinline__ void mma_f8_ta(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t id, uint32_t acc) {
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-        "r"(a_tmem), "l"(b), "r"(id), "r"(acc)
-        : "memory");
-}
-__device__ __forceinline__ void tmem_st8(uint32_t a, const uint32_t (&v)[8]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(a), "r"(v[0]), "r"(v[1]),
-                 "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
 }
 // Four values up to 448 as the sum of two E4M3 terms: hi = rn(x), lo = rn(x -
 // hi), x rounded to FP16 first.  Exact for 8-bit significands whose last bit is
@@ -183,12 +173,30 @@ __device__ __forceinline__ void split4(float x0, float x1, float x2, float x3, u
         : "=r"(hi), "=r"(lo)
         : "f"(x0), "f"(x1), "f"(x2), "f"(x3));
 }
-// Slack of the running maximum (log2), and the power of two that E4M3 weights
-// are scaled by: 2^(5 + 3) stays below 448.
+// Slack of the running maximum (log2), and the power of two that FP16 weights
+// are scaled by: 2^(7 + 8) stays below 65504, and weights are normal numbers
+// (half a step: 2^-11 of them) down to 2^-21 of the base, and not zero down to
+// 2^-32.  BF16 has FP32's range.
+constexpr float kSlack = 8.f;
 template <bool kFp8>
-constexpr float slack_of() { return kFp8 ? 3.f : 8.f; }
-template <bool kFp8>
-constexpr float weight_shift_of() { return kFp8 ? 5.f : 0.f; }
+constexpr float weight_shift_of() { return kFp8 ? 7.f : 0.f; }
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+// 16 E4M3 values as FP16, exactly: 0-7 to a, 8-15 to b.
+__device__ __forceinline__ void widen16(const uint4& x, uint4& a, uint4& b) {
+    auto four = [](uint32_t u, uint32_t& lo, uint32_t& hi) {
+        asm("{\n .reg .b16 c, d;\n mov.b32 {c, d}, %2;\n cvt.rn.f16x2.e4m3x2 %0, c;\n cvt.rn.f16x2.e4m3x2 %1, d;\n}\n"
+            : "=r"(lo), "=r"(hi)
+            : "r"(u));
+    };
+    four(x.x, a.x, a.y);
+    four(x.y, a.z, a.w);
+    four(x.z, b.x, b.y);
+    four(x.w, b.z, b.w);
+}
 
 // Rendezvous of the two warps that share 32 rows (named barrier 1 + id), and
 // with it: does any of their threads say yes?
@@ -234,9 +242,9 @@ __device__ __forceinline__ void pair_sync(int id) { asm volatile("barrier.cta.sy
 // split), its piece to write out, the pipeline to refill.  The list is cut by
 // cost, every unit being nt + unit_cost long; the last unit_cost places of it
 // hold no tile.  Two tiles' worth for BF16 (64 sequences over 32768 shared
-// tokens: 69, 64, 65 us with 1, 2, 3), five for FP8, where the tiles of
-// full row tiles also take longer than own ones (the same batch: 80, 78, 77, 79
-// us with 3 to 6; eight groups over 1024 to 8192 tokens: 59, 59, 56, 56).
+// tokens: 69, 64, 65 us with 1, 2, 3), five for FP8 (eight groups over
+// 1024 to 8192 tokens: 52, 52, 50, 51 us with 3 to 6; prefixes alone and own
+// tokens alone differ by less than 1 %).
 int unit_cost_of(pkv_dtype kv) { return kv == PKV_FP8_E4M3 ? 5 : 2; }
 
 // A list of cost T is cut into n = min(T, ctas) ranges, none of them empty, the
@@ -612,8 +620,9 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
     // (kWarpK and behind); its barriers cover what they write.
     if (warp == kWarpS) {
         for (int i = lane; i < kNumBars; i += 32)
-            bar_init(B(i), ((i >= kPFull && i < kPFull + kNS) || i == kOFree || i == kQOp) ? kSoftmaxWarps
-                                                                                           : (i == kDone ? 2u : 1u));
+            bar_init(B(i), (i >= kPFull && i < kPFull + kNS) || i == kOFree || i == kQOp || i >= kVEmpty
+                               ? kSoftmaxWarps
+                               : (i == kDone ? 2u : 1u));
         if (lane == 0) *abort_flag = *s_done = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
@@ -643,15 +652,13 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
 
     if (warp == kWarpK || warp == kWarpV) {
         // ------------------------------------------------ producers: K, V
-        // A stage is freed by the completion of the products that read it: S
-        // done for K, PV done for V, where there are as many stages as P buffers
-        // (a commit less for the MMA threads, who set the pace), else by a barrier
-        // of its own.
-        constexpr int kSt = stages_of<kFp8>();
+        // A stage is freed by the completion of the products that read it (no
+        // commit of its own for the MMA threads, who set the pace): S done for K, PV
+        // done for V; an FP8 V tile by the softmax warps that have read it.
         const bool is_v = warp == kWarpV;
         const CUtensorMap* map = is_v ? &tmv : &tmk;
         const int full0 = is_v ? kVFull : kKFull;
-        const int empty0 = kSt == kNS ? (is_v ? kPvDone : kSFull) : (is_v ? kVEmpty : kKEmpty);
+        const int empty0 = is_v ? (kFp8 ? kVEmpty : kPvDone) : kSFull;
         const int bs = a.block_size;
         const int64_t layer_blk0 = static_cast<int64_t>(a.layer) * a.num_blocks;
         int k = 0;
@@ -662,7 +669,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
             const bool has_next = w.next(a, nx);  // (early: its loads overlap this segment)
             int cache = 0, cache_base = INT_MIN / 2;  // 32 table entries, one per lane
             for (int t = 0; t < sg.n && ok; ++t, ++k) {
-                const int s = k % kSt;
+                const int s = k % kNS;
                 const int tt = t + sg.turn < sg.n ? t + sg.turn : t + sg.turn - sg.n;
                 const int tok0 = (sg.tile + tt) * kTok, n = min(kTok, sg.end - tok0), nblk = (n + bs - 1) / bs;
                 const int idx0 = tok0 / bs;
@@ -672,7 +679,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                     cache = idx < a.max_blocks ? __ldg(a.tables + static_cast<size_t>(sg.row) * a.max_blocks + idx) : 0;
                 }
                 if (__any_sync(0xFFFFFFFFu, *abort_flag != 0) ||
-                    (k >= kSt && !__all_sync(0xFFFFFFFFu, bar_wait_or(B(empty0 + s), ((k / kSt) - 1) & 1, abort_flag)))) {
+                    (k >= kNS && !__all_sync(0xFFFFFFFFu, bar_wait_or(B(empty0 + s), ((k / kNS) - 1) & 1, abort_flag)))) {
                     ok = false;
                     break;
                 }
@@ -699,8 +706,8 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
         if (!ok && lane == 0) fail();
         // drain: the copies in flight land before the CTA frees anything
         if (lane == 0)
-            for (int j = k - 1; j >= 0 && j >= k - kSt; --j)
-                if (!bar_wait(B(full0 + j % kSt), (j / kSt) & 1)) fail();
+            for (int j = k - 1; j >= 0 && j >= k - kNS; --j)
+                if (!bar_wait(B(full0 + j % kNS), (j / kNS) & 1)) fail();
     } else if (warp == kWarpS) {
         // ----------------------------------------------------- S = Q K^T
         // Lane 0 waits, copies and issues; the warp meets the softmax warps.  (After
@@ -709,7 +716,6 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
         bool ok = true;
         const uint64_t dq = sdesc(sbase, 16);
         const uint64_t dk0 = sdesc(sbase + kKVOff, 16);
-        constexpr int kSt = stages_of<kFp8>();
         auto check = [&](bool fine) {
             if (!fine) {
                 ok = false;
@@ -733,27 +739,26 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                 }
             }
             for (int t = 0; t < sg.n; ++t, ++k) {
-                const int s = k % kNS, st = k % kSt;
+                const int s = k % kNS;
                 // Q (FP8: split), K k, and S k - 1 taken to registers
                 if (lane == 0 && ok)
                     check(!*abort_flag && (t != 0 || bar_wait_or(B(kFp8 ? kQOp : kQReady), seg & 1, abort_flag)) &&
-                          bar_wait_or(B(kKFull + st), (k / kSt) & 1, abort_flag, k == 0 ? first_polls : kSpin));
+                          bar_wait_or(B(kKFull + s), (k / kNS) & 1, abort_flag, k == 0 ? first_polls : kSpin));
                 __syncwarp();
                 if (k > 0) wait_scores_read();
                 if (lane != 0 || !ok) continue;
                 fence_after();
-                const uint64_t dk = dk0 + static_cast<uint64_t>((st * (kFp8 ? 2 * kRawBytes : kStageBytes)) >> 4);
+                const uint64_t dk = dk0 + static_cast<uint64_t>((s * (kFp8 ? 2 * kRawBytes : kStageBytes)) >> 4);
                 const uint32_t sb = tmem;
 #pragma unroll
                 for (int ks = 0; ks < 8; ++ks) {  // 16 columns a step; FP8: 32, first of Q's high terms, then of the low ones
                     const uint32_t kin = (ks & 3) * 32;
                     if constexpr (kFp8)
-                        mma_f8(sb, dq + (((ks >> 2) * kQHalf + kin) >> 4), dk + (kin >> 4), idesc_f8(kTok, 0), ks > 0 ? 1u : 0u);
+                        mma_f8(sb, dq + (((ks >> 2) * kQHalf + kin) >> 4), dk + (kin >> 4), idesc0(kTok, 0), ks > 0 ? 1u : 0u);
                     else mma_bf16(sb, dq + (((ks >> 2) * kQHalf + kin) >> 4), dk + (((ks >> 2) * kHalfBytes + kin) >> 4),
                              idesc(kTok, 0), ks > 0 ? 1u : 0u);
                 }
                 mma_commit(B(kSFull + s));
-                if constexpr (kSt != kNS) mma_commit(B(kKEmpty + st));
                 if (t == sg.n - 1) mma_commit(B(kQFree));
             }
             __syncwarp();
@@ -774,31 +779,27 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
         // ------------------------------------------------------- O += P V
         if (lane == 0) {
             bool ok = true;
-            const uint64_t dv0 = sdesc(sbase + kKVOff + (kFp8 ? kRawBytes : 2 * kHalfBytes), kHalfBytes);
-            constexpr int kSt = stages_of<kFp8>();
+            const uint64_t dv0 = sdesc(sbase + (kFp8 ? kWideOff : kKVOff + 2 * kHalfBytes), kHalfBytes);
             Seg sg;
             int k = 0;
             for (int seg = 0; ok && w.next(a, sg); ++seg) {
                 for (int t = 0; t < sg.n; ++t, ++k) {
-                    const int s = k % kNS, st = k % kSt;
-                    // V k, P k, and for a new segment an O that has been read out
-                    if (*abort_flag || !bar_wait_or(B(kVFull + st), (k / kSt) & 1, abort_flag) ||
+                    const int s = k % kNS;
+                    // V k (FP8: with P k), P k, and for a new segment an O that has been read out
+                    if (*abort_flag || (!kFp8 && !bar_wait_or(B(kVFull + s), (k / kNS) & 1, abort_flag)) ||
                         !bar_wait_or(B(kPFull + s), (k / kNS) & 1, abort_flag) ||
                         (t == 0 && seg > 0 && !bar_wait_or(B(kOFree), (seg - 1) & 1, abort_flag))) {
                         ok = false;
                         break;
                     }
                     fence_after();
-                    const uint64_t dv = dv0 + static_cast<uint64_t>((st * (kFp8 ? 2 * kRawBytes : kStageBytes)) >> 4);
+                    const uint64_t dv = dv0 + static_cast<uint64_t>((s * (kFp8 ? 2 * kHalfBytes : kStageBytes)) >> 4);
                     const uint32_t pb = tmem + kPCol + static_cast<uint32_t>(s) * kPCols;
 #pragma unroll
-                    for (int ks = 0; ks < kTok / 16; ++ks) {  // 16 tokens a step; FP8: 32, of P's high, then of its low terms
-                        const uint32_t acc = t > 0 || ks > 0 ? 1u : 0u;
-                        if constexpr (kFp8) mma_f8_ta(tmem + kOCol, pb + 8 * ks, dv + (((ks & 1) * 32 * 128) >> 4), idesc_f8(kDim, 1), acc);
-                        else mma_bf16_ta(tmem + kOCol, pb + 8 * ks, dv + ((ks * 16 * 128) >> 4), idesc(kDim, 1), acc);
-                    }
+                    for (int ks = 0; ks < kTok / 16; ++ks)  // 16 tokens a step
+                        mma_bf16_ta(tmem + kOCol, pb + 8 * ks, dv + ((ks * 16 * 128) >> 4), kFp8 ? idesc0(kDim, 1) : idesc(kDim, 1),
+                                  t > 0 || ks > 0 ? 1u : 0u);
                     mma_commit(B(kPvDone + s));
-                    if constexpr (kSt != kNS) mma_commit(B(kVEmpty + st));
                 }
             }
             if (!ok) fail();
@@ -880,6 +881,41 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
             if (lane == 0) bar_arrive(B(kQOp));
         };
 
+        // FP8 pools: V k as FP16, the rows behind the last token as zeros, by the
+        // pairs that have no rows (else by all, behind their weights; 64 sequences
+        // with 2048 own tokens took 85 us with one FP16 tile, which waits for PV
+        // k - 1, and 74 with two, prefixes alone 60 and 56).  Eight threads read a
+        // row's 128 bytes and write its two 64-column halves, those of the second
+        // half their odd chunks first, so that the eight stores fall into different
+        // banks.  The FP16 tile is free: the warp has waited for PV k - 2.
+        auto widen_v = [&](int k, int visible, int rows) {
+            constexpr int kPairs = kSoftmaxWarps / 2;
+            const int s = k % kNS, with_rows = (rows + 31) / 32, skip = with_rows < kPairs ? with_rows : 0;
+            if (pair >= skip) {
+                wait(kVFull + s, k / kNS);
+                const uint8_t* raw = smem + kKVOff + (2 * s + 1) * kRawBytes;
+                const int c = lane & 7, half = c >> 2, ch = 2 * (c & 3) + half;
+                uint8_t* wide = smem + kWideOff + (2 * s + half) * kHalfBytes;
+                auto row = [&](int t) {
+                    uint4 x = *reinterpret_cast<const uint4*>(raw + tile_off(t, c, 0)), lo, hi;
+                    if (t >= visible) x = make_uint4(0u, 0u, 0u, 0u);
+                    widen16(x, lo, hi);
+                    *reinterpret_cast<uint4*>(wide + tile_off(t, ch, 0)) = half ? hi : lo;
+                    *reinterpret_cast<uint4*>(wide + tile_off(t, ch ^ 1, 0)) = half ? lo : hi;
+                };
+                if (skip == 0) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) row(4 * warp + (lane >> 3) + i * (kTok / 2));
+                } else {
+                    const int pairs = kPairs - skip;
+                    for (int t = 4 * (hf * pairs + pair - skip) + (lane >> 3); t < kTok; t += 8 * pairs) row(t);
+                }
+                fence_async_smem();
+                __syncwarp();
+            }
+            if (lane == 0) bar_arrive(B(kVEmpty + s));
+        };
+
         Seg sg, nx;
         bool has = w.next(a, sg);
         if (kFp8 && has) convert_q(0, sg);
@@ -925,11 +961,11 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                     // Lazy base: it moves (and O and l are rescaled) only when
                     // a row's maximum grew by more than the slack; only then do the two
                     // threads of a row exchange theirs.
-                    if (pair_any(pair, m < nv && (mx > m_used + slack_of<kFp8>() || m_used == -INFINITY))) {
+                    if (pair_any(pair, m < nv && (mx > m_used + kSlack || m_used == -INFINITY))) {
                         ex[hf * kRows + m] = mx;
                         pair_sync(pair);
                         const float m_new = fmaxf(m_used, fmaxf(mx, ex[(hf ^ 1) * kRows + m]));
-                        rescale = m < nv && m_used != -INFINITY && m_new > m_used + slack_of<kFp8>();
+                        rescale = m < nv && m_used != -INFINITY && m_new > m_used + kSlack;
                         alpha = rescale ? ex2(m_used - m_new) : 1.f;
                         if (rescale || m_used == -INFINITY) m_used = m_new;
                     }
@@ -944,8 +980,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                             fma2(x0, x1, __uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), qk, qk, -base, -base);
                             const float p0 = ex2(x0), p1 = ex2(x1);
                             add2(l0, l1, l0, l1, p0, p1);
-                            if constexpr (kFp8) v[2 * i] = __float_as_uint(p0), v[2 * i + 1] = __float_as_uint(p1);
-                            else pk[i] = bf16x2(p0, p1);
+                            pk[i] = kFp8 ? f16x2(p0, p1) : bf16x2(p0, p1);
                         }
                         lt = l0 + l1;
                     } else {
@@ -954,23 +989,11 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                             const float p0 = 2 * i < seen ? ex2(fmaf(__uint_as_float(v[2 * i]), qk, -base)) : 0.f;
                             const float p1 = 2 * i + 1 < seen ? ex2(fmaf(__uint_as_float(v[2 * i + 1]), qk, -base)) : 0.f;
                             lt += p0 + p1;
-                            if constexpr (kFp8) v[2 * i] = __float_as_uint(p0), v[2 * i + 1] = __float_as_uint(p1);
-                            else pk[i] = bf16x2(p0, p1);
+                            pk[i] = kFp8 ? f16x2(p0, p1) : bf16x2(p0, p1);
                         }
                     }
                     l = l * alpha + lt;
-                    if constexpr (kFp8) {  // columns 0-15 of the buffer: high terms of tokens 0-63; 16-31: low terms
-                        uint32_t hi[8], lo[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            split4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]), __uint_as_float(v[4 * i + 2]),
-                                   __uint_as_float(v[4 * i + 3]), hi[i], lo[i]);
-                        tmem_st8(pa + 8 * hf, hi);
-                        tmem_st8(pa + 16 + 8 * hf, lo);
-                        asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
-                    } else {
-                        tmem_st16(pa + 16 * hf, pk);
-                    }
+                    tmem_st16(pa + 16 * hf, pk);
                     // This warp has waited for PV k - 2 and k - 3, and PV k + 1 cannot
                     // finish before P k + 1 is signalled, so a parity wait for PV
                     // k - 1, or for PV k at the end, is unambiguous.
@@ -990,14 +1013,14 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                 } else {
                     scores_read();
                 }
-                if (visible < kTok) {  // V rows past the last token: zero (stale or unwritten rows could hold NaN)
-                    constexpr int kSt = stages_of<kFp8>();
-                    const int st = k % kSt;
-                    wait(kVFull + st, k / kSt);
-                    uint8_t* vs = smem + kKVOff + (kFp8 ? (2 * st + 1) * kRawBytes : st * kStageBytes + 2 * kHalfBytes);
-                    constexpr int kHalves = kFp8 ? 1 : 2;
+                // V rows past the last token: zero (stale or unwritten rows could hold NaN)
+                if constexpr (kFp8) {
+                    widen_v(k, visible, nv);
+                } else if (visible < kTok) {
+                    wait(kVFull + s, k / kNS);
+                    uint8_t* vs = smem + kKVOff + s * kStageBytes + 2 * kHalfBytes;
                     const int nz = kTok - visible;
-                    for (int e = threadIdx.x; e < kHalves * nz * 8; e += kSoftmax) {  // whole 128-byte rows: any swizzle
+                    for (int e = threadIdx.x; e < 2 * nz * 8; e += kSoftmax) {  // whole 128-byte rows: any swizzle
                         const int h2 = e / (nz * 8), rem = e % (nz * 8);
                         *reinterpret_cast<uint4*>(vs + h2 * kHalfBytes + (visible + rem / 8) * 128 + (rem % 8) * 16) =
                             make_uint4(0u, 0u, 0u, 0u);
