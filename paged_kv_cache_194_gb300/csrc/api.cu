@@ -109,6 +109,15 @@ EncodeTiledFn encode_fn() {
     return fn;
 }
 
+// cuTensorMapEncodeTiled, which wants a current context: a host thread has none
+// before its first call that binds its device's (a launch or a copy would).
+template <typename... Args>
+bool encode_tiled(EncodeTiledFn fn, Args... args) {
+    if (fn(args...) == CUDA_SUCCESS) return true;
+    int dev = 0;
+    return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && fn(args...) == CUDA_SUCCESS;
+}
+
 // TMA descriptors over the whole K and V pools, viewed as 2D tensors
 // [rows = layers*blocks*kv_heads*block_size][head_dim]; one box is one
 // (block, kv head) chunk of 64 BF16 or 128 E4M3 columns, 128-byte swizzled.
@@ -132,11 +141,11 @@ bool ensure_tmaps(pkv_pool* p) {
         const cuuint32_t estr3[3] = {1, 1, 1};
         bool ok3 = true;
         for (int i = 0; i < 2 && ok3; ++i) {
-            CUresult r = enc(i == 0 ? &p->tmap_k : &p->tmap_v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
-                             i == 0 ? d.k_base : d.v_base, dims3, strides3, box3, estr3,
-                             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-            ok3 = r == CUDA_SUCCESS;
+            const bool r = encode_tiled(enc, i == 0 ? &p->tmap_k : &p->tmap_v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                                        i == 0 ? d.k_base : d.v_base, dims3, strides3, box3, estr3,
+                                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+            ok3 = r;
         }
         if (ok3) {
             p->tmap_3d = 1;
@@ -146,11 +155,12 @@ bool ensure_tmaps(pkv_pool* p) {
             const cuuint32_t boxh[3] = {64, static_cast<cuuint32_t>(d.block_size), 1};
             bool okh = true;
             for (int i = 0; i < 2 && okh; ++i) {
-                CUresult r = enc(i == 0 ? &p->tmap_kh : &p->tmap_vh, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
-                                 i == 0 ? d.k_base : d.v_base, dims3, strides3, boxh, estr3,
-                                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-                okh = r == CUDA_SUCCESS;
+                const bool r = encode_tiled(enc, i == 0 ? &p->tmap_kh : &p->tmap_vh,
+                                            CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, i == 0 ? d.k_base : d.v_base, dims3,
+                                            strides3, boxh, estr3, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                okh = r;
             }
             p->tmap_half = okh ? 1 : 0;
             // Boxes of two adjacent KV heads of a block (the rows of head h+1
@@ -160,11 +170,12 @@ bool ensure_tmaps(pkv_pool* p) {
                 const cuuint32_t box2[3] = {64, static_cast<cuuint32_t>(2 * d.block_size), 2};
                 bool ok2 = true;
                 for (int i = 0; i < 2 && ok2; ++i) {
-                    CUresult r = enc(i == 0 ? &p->tmap_k2 : &p->tmap_v2, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
-                                     i == 0 ? d.k_base : d.v_base, dims3, strides3, box2, estr3,
-                                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-                    ok2 = r == CUDA_SUCCESS;
+                    const bool r = encode_tiled(enc, i == 0 ? &p->tmap_k2 : &p->tmap_v2,
+                                                CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, i == 0 ? d.k_base : d.v_base,
+                                                dims3, strides3, box2, estr3, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                    ok2 = r;
                 }
                 p->tmap_pair = ok2 ? 1 : 0;
             }
@@ -178,10 +189,10 @@ bool ensure_tmaps(pkv_pool* p) {
     const cuuint32_t estr[2] = {1, 1};
     const CUtensorMapDataType dt = bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8;
     for (int i = 0; i < 2; ++i) {
-        CUresult r = enc(i == 0 ? &p->tmap_k : &p->tmap_v, dt, 2, i == 0 ? d.k_base : d.v_base, dims, strides, box,
-                         estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-        if (r != CUDA_SUCCESS) return false;
+        const bool r = encode_tiled(enc, i == 0 ? &p->tmap_k : &p->tmap_v, dt, 2, i == 0 ? d.k_base : d.v_base, dims,
+                                    strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+        if (!r) return false;
     }
     p->tmap_state = 1;
     return true;
@@ -631,9 +642,9 @@ bool encode_q_map(CUtensorMap* map, const void* q, int num_seqs, int num_q_heads
     const cuuint64_t strides[3] = {256, 256ull * num_q_heads, 128};
     const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(gh), static_cast<cuuint32_t>(seqs), 1};
     const cuuint32_t estr[4] = {1, 1, 1, 1};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(q), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode_tiled(enc, map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(q), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 // PKV_ALGO_TC when the sharing design runs, else what decode attention runs.
