@@ -1,10 +1,12 @@
 // C ABI of libpkv.so: argument validation, split planning and launches.
 // Everything here runs on the host; it allocates no device memory and never
 // synchronises a stream.
+#include <atomic>
 #include <cmath>
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <mutex>
 
 #include "pkv_internal.h"
 #include "step_internal.h"
@@ -28,7 +30,7 @@ pkv_status cuda_status(cudaError_t e) {
     return PKV_ERR_CUDA;
 }
 
-int g_sms[64] = {0};
+std::atomic<int> g_sms[64];
 
 // Balanced persistent schedule: at most this many sequences (each CTA scans
 // the lengths once), at most kBalCtasPerSm CTAs per SM.
@@ -95,17 +97,14 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t
                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 EncodeTiledFn encode_fn() {
-    static EncodeTiledFn fn = nullptr;
-    static bool tried = false;
-    if (!tried) {
-        tried = true;
+    static const EncodeTiledFn fn = []() -> EncodeTiledFn {
         void* p = nullptr;
         cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-    }
+        const bool found =
+            cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess;
+        return found ? reinterpret_cast<EncodeTiledFn>(p) : nullptr;
+    }();
     return fn;
 }
 
@@ -121,9 +120,7 @@ bool encode_tiled(EncodeTiledFn fn, Args... args) {
 // TMA descriptors over the whole K and V pools, viewed as 2D tensors
 // [rows = layers*blocks*kv_heads*block_size][head_dim]; one box is one
 // (block, kv head) chunk of 64 BF16 or 128 E4M3 columns, 128-byte swizzled.
-bool ensure_tmaps(pkv_pool* p) {
-    if (p->tmap_state != 0) return p->tmap_state == 1;
-    p->tmap_state = -1;
+bool encode_tmaps(pkv_pool* p) {
     const pkv_pool_desc& d = p->d;
     if (d.kv_dtype != PKV_BF16 && d.kv_dtype != PKV_FP8_E4M3) return false;
     const uint64_t rows = static_cast<uint64_t>(d.num_layers) * d.num_blocks * d.num_kv_heads * d.block_size;
@@ -149,7 +146,6 @@ bool ensure_tmaps(pkv_pool* p) {
         }
         if (ok3) {
             p->tmap_3d = 1;
-            p->tmap_state = 1;
             // Boxes of one 64-column half of a block (the tcgen05 kernel keeps
             // the two halves of a tile apart).
             const cuuint32_t boxh[3] = {64, static_cast<cuuint32_t>(d.block_size), 1};
@@ -194,8 +190,23 @@ bool ensure_tmaps(pkv_pool* p) {
                                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
         if (!r) return false;
     }
-    p->tmap_state = 1;
     return true;
+}
+
+// Encodes them with the pool's first call that wants them.  First calls may come
+// from several threads at once: none looks at a pool that another is encoding.
+bool ensure_tmaps(pkv_pool* p) {
+    int state = __atomic_load_n(&p->tmap_state, __ATOMIC_ACQUIRE);
+    if (state == 0) {
+        static std::mutex encoding;
+        const std::lock_guard<std::mutex> lock(encoding);
+        state = p->tmap_state;
+        if (state == 0) {
+            state = encode_tmaps(p) ? 1 : -1;
+            __atomic_store_n(&p->tmap_state, state, __ATOMIC_RELEASE);
+        }
+    }
+    return state == 1;
 }
 }  // namespace
 

@@ -46,3 +46,25 @@ def test_first_call_of_a_host_thread(kv, used):
         in_new_thread(f)
     torch.cuda.synchronize()
     assert torch.equal(out, want) and torch.equal(dec, make().run(algo="mma"))
+
+
+def test_first_calls_of_a_pool_from_several_threads():
+    """A pool's first calls may come at once: each finds the pool's descriptors complete."""
+    n = 8
+    for _ in range(100):
+        pool = pk.KVPool(1, 4, 16, 2, 128, "bf16")
+        gate, got = threading.Barrier(n), []
+
+        def first(i):
+            gate.wait()
+            if i % 2:
+                got.append(pk.lib().paged_prefix_decode_algo(pool.handle, 4, 1, 8, 64, 3))
+            else:
+                got.append(pk.lib().paged_multi_query_algo(pool.handle, 64, 8, 0, 3))
+
+        threads = [threading.Thread(target=first, args=(i,)) for i in range(n)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        assert got == [3] * n
