@@ -77,3 +77,14 @@ def test_prefix_groups_take_the_sharing_design(q_heads, kv_heads, kv):
 def test_prefix_shapes_take_the_sharing_design(shape, kv):
     lens, groups = SHAPES[shape]
     assert Batch(lens, groups, kv=kv).design() == "tc"
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_prefix_without_groups(kv):
+    """Nothing to share: over FP8 pools the call is decode attention, bit for
+    bit; asked for by name, the sharing design still takes it."""
+    bt = Batch((900, 1, 0, 64, 2000), [], 8, 2, kv=kv, seed=6)
+    assert bt.design() == ("mma" if kv == "fp8" else "tc") and bt.design("tc") == "tc"
+    if kv == "fp8":
+        assert torch.equal(bt.run(), bt.run(algo="mma"))
+    _check(bt)
