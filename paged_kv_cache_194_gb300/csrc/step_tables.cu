@@ -18,14 +18,14 @@
 // A batch is at most some thousand lengths, so nothing here is bound by bytes:
 // a call costs its launch, a few dependent rounds to L2, and the instructions
 // that one SM issues.  Hence one CTA that scans 1024 requests a round (both
-// sums at once, in 32 bits that saturate, one barrier), writes tables and, for
-// up to kInlineTokens token rows, the slots too; a second kernel, launched to
-// start as the first ends, fills longer slot maps, one thread per token row.
+// sums at once, in 32 bits that saturate, one barrier), writes tables and, where
+// they are few, the slots too; a second kernel, launched to start as the first
+// ends, fills longer slot maps, one thread per token row.
 // (Block sizes are powers of two; with runtime divisions instead of shifts the
 // scan took four times as long.)  256 requests of one token each: 3.3 us, of
 // which an empty launch is 2; 1024 requests, 128 of them prompts of up to 2048
 // tokens, 8 thousand blocks and 131 thousand rows: 11.5 us, six of them in the
-// one CTA.  Releases of a quarter of 256 requests: 4.9 us; of 4096 requests'
+// one CTA.  Releases of a quarter of 256 requests: 4.6 us; of 4096 requests'
 // two hundred thousand blocks: 6.6 us.
 #include "device_common.cuh"
 #include "step_internal.h"
@@ -35,7 +35,6 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
-constexpr int kInlineTokens = 8192;  // token rows the scanning CTA fills itself
 constexpr int kDirect = 2;           // rows or blocks of a request that its own thread writes
 constexpr int kAhead = 8;            // blocks that a thread fetches at once
 constexpr int kFillThreads = 256;
@@ -294,8 +293,13 @@ __global__ void __launch_bounds__(kFillThreads) fill_kernel(const GrowArgs a) {
 }
 
 // ---------------------------------------------------------------- release
-constexpr int kReleasePerCta = kWarps;        // requests of one CTA of the large form: one per warp
-constexpr long long kSmallEntries = 1 << 18;  // table entries up to which one CTA does it all
+constexpr int kReleasePerCta = kWarps;  // requests of one CTA of the large form: one per warp
+// Requests up to which one CTA does it all (us, half of them finished, one CTA /
+// many: 16 requests 2.8 / 3.3, or 15.6 / 16.1 with 64 thousand table entries;
+// 128: 3.1 / 3.2 and 10.9 / 9.2; 256: 3.7 / 3.2 and 14.5 / 9.0 with 256
+// thousand; 1024: 5.9 / 3.5 and 37 / 9.7 with a million).
+constexpr int kSmallRelease = 128;
+static_assert(kSmallRelease <= kThreads, "a thread each");
 
 // Blocks request b gives back: entries [*first, *first + *count) of its row.
 // *len: its length; *gone: whether it is released (if the ring has room).
@@ -341,14 +345,14 @@ __device__ __forceinline__ void put_state(const ReleaseArgs& a, int head, int co
     if (!ok && a.err) atomicOr(a.err, PKV_ERRBIT_STEP);
 }
 
-// Up to kThreads requests in one CTA: a thread each, then the blocks of those
-// that have any by a warp each.  The outputs may be the inputs.
+// Up to kSmallRelease requests in one CTA: a thread each, then the blocks of
+// those that have any by a warp each.  The outputs may be the inputs.
 __global__ void __launch_bounds__(kThreads, 1) release_small_kernel(const ReleaseArgs a) {
     __shared__ int sums[1][kWarps];
     struct Run {
         int b, first, count, tail;
     };
-    __shared__ Run runs[kThreads];
+    __shared__ Run runs[kSmallRelease];
     __shared__ int num_runs;
     const int head = a.free_state[0], count = a.free_state[1], b = threadIdx.x;
     Given g{0, 0, 0, false};
@@ -428,9 +432,17 @@ __global__ void __launch_bounds__(kThreads, 1) release_commit_kernel(const Relea
 
 }  // namespace
 
+// The scanning CTA fills the token rows itself where they are few, or no more
+// than its threads write for their own requests (kDirect each); else the second
+// kernel does.  Us, scanning CTA / second kernel, requests x rows in all: 1 x
+// 256 3.9 / 4.0, 1 x 1024 4.9 / 4.5; 64 x 256 4.1 / 4.6, 64 x 512 5.2 / 4.6; 256
+// x 512 3.5 / 5.0, 256 x 1024 7.0 / 4.8; 1024 x 2048 5.2 / 6.8, 1024 x 4096 9.1 /
+// 6.6; 4096 x 4096 12.3 / 12.9, 4096 x 8192 16.6 / 13.3.  256 threads start sooner
+// than 1024 (64 requests: 4.6 / 5.2 us), which scan more at once (512: 6.4 / 6.1).
 cudaError_t launch_tables_grow(const GrowArgs& a, cudaStream_t stream) {
-    const bool inline_rows = a.max_tokens <= kInlineTokens;
-    const int threads = a.num_seqs <= 256 && a.max_tokens <= 1024 ? 256 : kThreads;
+    const int64_t direct = static_cast<int64_t>(kDirect) * a.num_seqs;
+    const bool inline_rows = a.max_tokens <= 256 || a.max_tokens <= (direct < 4096 ? direct : 4096);
+    const int threads = a.num_seqs <= 256 ? 256 : kThreads;
     grow_kernel<<<1, threads, 0, stream>>>(a, inline_rows ? 1 : 0);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || inline_rows) return e;
@@ -439,7 +451,7 @@ cudaError_t launch_tables_grow(const GrowArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_tables_release(const ReleaseArgs& a, cudaStream_t stream) {
-    if (a.num_seqs <= kThreads && static_cast<long long>(a.num_seqs) * a.max_blocks <= kSmallEntries) {
+    if (a.num_seqs <= kSmallRelease) {
         release_small_kernel<<<1, kThreads, 0, stream>>>(a);  // (all 32 warps: they share out the blocks)
         return cudaGetLastError();
     }
