@@ -732,8 +732,7 @@ pkv_status paged_prefix_decode_attention(const void* q, pkv_dtype q_dtype, const
     st = attention_call(q, q_dtype, p, layer, block_tables, max_blocks_per_seq, seq_lens, num_seqs, 1, num_q_heads,
                         max_seq_len, scale, 0, decode_algo, workspace, workspace_bytes, out, stream, nullptr, nullptr,
                         PKV_BF16, true);
-    // (which may lack a kernel for a number of query heads that sharing serves)
-    if (st != PKV_OK && !(design == PKV_ALGO_TC && st == PKV_ERR_UNSUPPORTED && q_dtype == PKV_BF16)) return st;
+    if (st != PKV_OK) return st;
     if (design < 0) return PKV_ERR_UNSUPPORTED;
     if (num_seqs == 0) return PKV_OK;
     if (!workspace || workspace_bytes < need || !aligned(workspace, 256)) return PKV_ERR_WORKSPACE;
