@@ -43,23 +43,25 @@
 // FP16 (exactly) to shared memory for PV.  (That takes 4 us more than two E4M3
 // terms on prefixes or own tokens alone, 6 to 7 %, and 4 us less where both are
 // mixed.)
-// Every wait is bounded; a CTA whose wait expires sets PKV_ERRBIT_TIMEOUT, makes
-// its pieces NaN, waits for its copies and products in flight, frees its TMEM
-// and leaves.
+// Every wait at an mbarrier is bounded; a CTA whose wait expires sets
+// PKV_ERRBIT_TIMEOUT, makes its pieces NaN, waits for its copies and products in
+// flight, frees its TMEM and leaves.  (Only the pairs' named barriers have no
+// bound of their own: see pair_any.)
 //
 // Measured (calls back to back in a graph; 32 query over 8 KV heads; "floor" is
 // bytes at the measured copy rate):
-//   64 sequences, 32768 shared tokens, up to 1024 own   65 us, floor 40 us
+//   64 sequences, 32768 shared tokens, up to 1024 own   64 us, floor 40 us
 //   the same prefix alone                               46 us, floor 20 (products at the measured rate: 18)
-//   64 sequences, 2048 shared, 128 to 2048 own          62 us, floor 43.5
+//   64 sequences, 2048 shared, 128 to 2048 own          61 us, floor 43.5
 //   64 sequences, 2048 own tokens, nothing shared       88 us, floor 79.5 (6.1 TB/s)
-//   55 in 8 groups, FP8, 1024 to 8192 shared            50 us, floor 20
+//   55 in 8 groups, FP8, 1024 to 8192 shared            49 us, floor 20
 //   4 sequences, 512 shared, up to 64 own               12 us
 // (paged_decode_attention: 622, 597, 79, 86, 104 and 21.6 us.)  What bounds a
 // shared tile of a BF16 pool is the chain S issued (900 cycles of the S thread,
-// two CTAs side by side) - done (500) - taken to registers (270) - met (100):
-// 1870 cycles a tile and CTA, tensor pipe active 42 %; of an FP8 pool the softmax
-// (250 to load, 850 maxima and exponentials, then the weights and the V tile).
+// two CTAs side by side) - done (500) - taken to registers (270) - told
+// (100): 1870 cycles a tile and CTA, tensor pipe active 42 %; of an FP8 pool the
+// softmax (250 to load, 850 maxima and exponentials, then the weights and the V
+// tile).
 // A call adds 2.5 us of plan, 2 until the first tiles land, and the merge's 3.
 #include <cuda.h>
 
@@ -99,12 +101,13 @@ constexpr uint32_t kPCol = kTok, kPCols = kTok / 2;
 constexpr uint32_t kOCol = kPCol + kNS * kPCols;
 static_assert(kOCol + kDim == kTmemCols, "tensor memory");
 
-enum Bar { kQReady, kQFree, kOFree, kDone, kSFull, kPFull = kSFull + kNS, kPvDone = kPFull + kNS, kKFull = kPvDone + kNS,
+enum Bar { kQReady, kQFree, kOFree, kDone, kSRead, kSFull, kPFull = kSFull + kNS, kPvDone = kPFull + kNS, kKFull = kPvDone + kNS,
            kVFull = kKFull + kNS,
+           // (kSRead: the scores are in registers, S may be written again)
            // FP8 pools: Q split into E4M3 terms, V stages that the softmax warps have read
            kQOp = kVFull + kNS, kVEmpty, kNumBars = kVEmpty + kNS };
 constexpr int kBarOff = kKVOff + kNS * kStageBytes;
-constexpr int kExOff = kBarOff + (8 * kNumBars + 12 + 63) / 64 * 64;  // the two threads of a row meet here: maxima
+constexpr int kExOff = kBarOff + (8 * kNumBars + 8 + 63) / 64 * 64;  // the two threads of a row meet here: maxima
 constexpr int kSumOff = kExOff + 2 * kRows * 4;                        // and sums, [2][kRows] floats each
 // The units of this CTA's range, as far as they fit (else the workspace's copy).
 constexpr int kSeqCache = 1024, kGroupCache = 128;
@@ -199,7 +202,10 @@ __device__ __forceinline__ void widen16(const uint4& x, uint4& a, uint4& b) {
 }
 
 // Rendezvous of the two warps that share 32 rows (named barrier 1 + id), and
-// with it: does any of their threads say yes?
+// with it: does any of their threads say yes?  Both warps come to the same ones
+// in the same order, in a CTA that gave up as well: which ones there are follows
+// from the segments, the pair's common votes and nothing else, and every wait in
+// between is bounded.
 __device__ __forceinline__ bool pair_any(int id, bool yes) {
     uint32_t r;
     asm volatile(
@@ -224,17 +230,6 @@ __device__ __forceinline__ bool bar_wait_or(uint32_t b, uint32_t parity, const v
     }
     return false;
 }
-// "The scores are in registers": the softmax warps pass by, the S warp waits.  At
-// an mbarrier this took 300 to 600 cycles of the chain that sets the pace of
-// shared tiles, here a tenth.  A warp passes for tile k + 1 only once S k + 1 is
-// done, and the S warp has met all of them for tile k before it issues that, so
-// no one is counted twice.  This wait has no bound of its own.  In a CTA that gave
-// up, softmax warps run ahead and count for others, so the S warp could be left
-// waiting: softmax warp 0 then passes until it leaves (at the end of the softmax
-// part).
-constexpr int kMeetId = 5, kMeetThreads = kSoftmax + 32;
-__device__ __forceinline__ void scores_read() { asm volatile("barrier.cta.arrive %0, %1;\n" ::"n"(kMeetId), "n"(kMeetThreads) : "memory"); }
-__device__ __forceinline__ void wait_scores_read() { asm volatile("barrier.cta.sync %0, %1;\n" ::"n"(kMeetId), "n"(kMeetThreads) : "memory"); }
 __device__ __forceinline__ void pair_sync(int id) { asm volatile("barrier.cta.sync %0, 64;\n" ::"r"(1 + id) : "memory"); }
 
 // ------------------------------------------------------------------- plan
@@ -612,7 +607,6 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
     auto B = [&](int i) { return bars + 8u * i; };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kBarOff + 8 * kNumBars);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kBarOff + 8 * kNumBars + 4);
-    volatile int* s_done = abort_flag + 1;  // the S warp comes to no other meeting
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     const Early early = fetch_early(a);  // (under way while the CTA sets itself up)
@@ -620,10 +614,10 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
     // (kWarpK and behind); its barriers cover what they write.
     if (warp == kWarpS) {
         for (int i = lane; i < kNumBars; i += 32)
-            bar_init(B(i), (i >= kPFull && i < kPFull + kNS) || i == kOFree || i == kQOp || i >= kVEmpty
+            bar_init(B(i), (i >= kPFull && i < kPFull + kNS) || i == kOFree || i == kSRead || i == kQOp || i >= kVEmpty
                                ? kSoftmaxWarps
                                : (i == kDone ? 2u : 1u));
-        if (lane == 0) *abort_flag = *s_done = 0;
+        if (lane == 0) *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
     if (warp >= kWarpK && lane == 0) {  // (the descriptors are fetched while the plan is made)
@@ -710,67 +704,55 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                 if (!bar_wait(B(full0 + j % kNS), (j / kNS) & 1)) fail();
     } else if (warp == kWarpS) {
         // ----------------------------------------------------- S = Q K^T
-        // Lane 0 waits, copies and issues; the warp meets the softmax warps.  (After
-        // an expired wait it meets them to the end of the segment: a vote of the warp
-        // per tile, wherever it stood, cost 1 to 2 % of long shared prefixes.)
-        bool ok = true;
-        const uint64_t dq = sdesc(sbase, 16);
-        const uint64_t dk0 = sdesc(sbase + kKVOff, 16);
-        auto check = [&](bool fine) {
-            if (!fine) {
-                ok = false;
-                fail();
-            }
-        };
-        // (test hook: this CTA's first wait for a tile may be cut short)
-        const uint32_t first_polls =
-            a.test_polls >= 0 && (a.test_cta < 0 || a.test_cta == static_cast<int>(blockIdx.x)) ? a.test_polls : kSpin;
-        Seg sg;
-        int k = 0, seg = 0, copies = 0;
-        for (; __all_sync(0xFFFFFFFFu, ok) && w.next(a, sg); ++seg) {
-            if (lane == 0) {
-                // This segment's Q rows, once the last S of the one before has read its own.
-                if (seg > 0) check(bar_wait_or(B(kQFree), (seg - 1) & 1, abort_flag));
-                if (ok) {
-                    bar_expect_tx(B(kQReady), static_cast<uint32_t>((sg.own ? 1 : a.seqs_per_tile) * a.gh * kDim * 2));
-                    for (int h2 = 0; h2 < 2; ++h2)
-                        tma_4d(sbase + h2 * kQHalf, sg.own ? &tmq_own : &tmq_group, 0, sg.head * a.gh, sg.seq0, h2, B(kQReady));
-                    ++copies;
-                }
-            }
-            for (int t = 0; t < sg.n; ++t, ++k) {
-                const int s = k % kNS;
-                // Q (FP8: split), K k, and S k - 1 taken to registers
-                if (lane == 0 && ok)
-                    check(!*abort_flag && (t != 0 || bar_wait_or(B(kFp8 ? kQOp : kQReady), seg & 1, abort_flag)) &&
-                          bar_wait_or(B(kKFull + s), (k / kNS) & 1, abort_flag, k == 0 ? first_polls : kSpin));
-                __syncwarp();
-                if (k > 0) wait_scores_read();
-                if (lane != 0 || !ok) continue;
-                fence_after();
-                const uint64_t dk = dk0 + static_cast<uint64_t>((s * (kFp8 ? 2 * kRawBytes : kStageBytes)) >> 4);
-                const uint32_t sb = tmem;
-#pragma unroll
-                for (int ks = 0; ks < 8; ++ks) {  // 16 columns a step; FP8: 32, first of Q's high terms, then of the low ones
-                    const uint32_t kin = (ks & 3) * 32;
-                    if constexpr (kFp8)
-                        mma_f8(sb, dq + (((ks >> 2) * kQHalf + kin) >> 4), dk + (kin >> 4), idesc0(kTok, 0), ks > 0 ? 1u : 0u);
-                    else mma_bf16(sb, dq + (((ks >> 2) * kQHalf + kin) >> 4), dk + (((ks >> 2) * kHalfBytes + kin) >> 4),
-                             idesc(kTok, 0), ks > 0 ? 1u : 0u);
-                }
-                mma_commit(B(kSFull + s));
-                if (t == sg.n - 1) mma_commit(B(kQFree));
-            }
-            __syncwarp();
-        }
-        ok = __shfl_sync(0xFFFFFFFFu, ok && !*abort_flag ? 1 : 0, 0) != 0;
-        if (ok && k > 0) wait_scores_read();  // (of the last tile)
+        // (The softmax warps tell at an mbarrier that they have read a tile's
+        // scores.  A named barrier in its place, which has no bound, took 1 to 2 %
+        // longer on every batch timed.)
         if (lane == 0) {
-            *s_done = 1;
-            if (!ok) {
-                fail();
-                if (copies > 0) bar_wait(B(kQReady), (copies - 1) & 1);  // (no copy of Q may land after the CTA has gone)
+            bool ok = true;
+            const uint64_t dq = sdesc(sbase, 16);
+            const uint64_t dk0 = sdesc(sbase + kKVOff, 16);
+            // (test hook: this CTA's first wait for a tile may be cut short)
+            const uint32_t first_polls =
+                a.test_polls >= 0 && (a.test_cta < 0 || a.test_cta == static_cast<int>(blockIdx.x)) ? a.test_polls : kSpin;
+            Seg sg;
+            int k = 0, copies = 0;
+            for (int seg = 0; ok && w.next(a, sg); ++seg) {
+                // This segment's Q rows, once the last S of the one before has read its own.
+                if (seg > 0 && !bar_wait_or(B(kQFree), (seg - 1) & 1, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                bar_expect_tx(B(kQReady), static_cast<uint32_t>((sg.own ? 1 : a.seqs_per_tile) * a.gh * kDim * 2));
+                for (int h2 = 0; h2 < 2; ++h2)
+                    tma_4d(sbase + h2 * kQHalf, sg.own ? &tmq_own : &tmq_group, 0, sg.head * a.gh, sg.seq0, h2, B(kQReady));
+                ++copies;
+                for (int t = 0; t < sg.n; ++t, ++k) {
+                    const int s = k % kNS;
+                    // Q (FP8: split), K k, and S k - 1 taken to registers
+                    if (*abort_flag || (t == 0 && !bar_wait_or(B(kFp8 ? kQOp : kQReady), seg & 1, abort_flag)) ||
+                        !bar_wait_or(B(kKFull + s), (k / kNS) & 1, abort_flag, k == 0 ? first_polls : kSpin) ||
+                        (k > 0 && !bar_wait_or(B(kSRead), (k - 1) & 1, abort_flag))) {
+                        ok = false;
+                        break;
+                    }
+                    fence_after();
+                    const uint64_t dk = dk0 + static_cast<uint64_t>((s * (kFp8 ? 2 * kRawBytes : kStageBytes)) >> 4);
+                    const uint32_t sb = tmem;
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks) {  // 16 columns a step; FP8: 32, first of Q's high terms, then of the low ones
+                        const uint32_t kin = (ks & 3) * 32;
+                        if constexpr (kFp8)
+                            mma_f8(sb, dq + (((ks >> 2) * kQHalf + kin) >> 4), dk + (kin >> 4), idesc0(kTok, 0), ks > 0 ? 1u : 0u);
+                        else mma_bf16(sb, dq + (((ks >> 2) * kQHalf + kin) >> 4), dk + (((ks >> 2) * kHalfBytes + kin) >> 4),
+                                 idesc(kTok, 0), ks > 0 ? 1u : 0u);
+                    }
+                    mma_commit(B(kSFull + s));
+                    if (t == sg.n - 1) mma_commit(B(kQFree));
+                }
             }
+            if (!ok) fail();
+            // (no copy of Q may land after the CTA has gone)
+            if (copies > 0 && !bar_wait(B(kQReady), (copies - 1) & 1)) fail();
             mma_commit(B(kDone));  // completes once every MMA this thread issued has finished
             if (!bar_wait(B(kDone), 0)) fail();
         }
@@ -939,7 +921,8 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                     uint32_t v[32];
                     tmem_ld32(sa + 32 * hf, v);
                     fence_before();
-                    scores_read();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(B(kSRead));
                     const int seen = visible - 32 * hf;  // of this thread's 32 tokens
                     float mx = -INFINITY;
                     if (qk > 0.f) {
@@ -1010,8 +993,8 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                             tmem_st32(oa, o);
                         }
                     }
-                } else {
-                    scores_read();
+                } else if (lane == 0) {
+                    bar_arrive(B(kSRead));
                 }
                 // V rows past the last token: zero (stale or unwritten rows could hold NaN)
                 if constexpr (kFp8) {
@@ -1083,14 +1066,6 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
             sg = nx;
             has = has_next;
         }
-        // Every tile is behind this warp.  In a CTA that gave up the S warp may be
-        // at a meeting whose passes are all spent, with more of its segment to come:
-        // nine of these end any.
-        if (warp == 0)
-            for (uint32_t i = 0; __any_sync(0xFFFFFFFFu, *s_done == 0) && i < 64 * kSpin; ++i) {
-                if (__any_sync(0xFFFFFFFFu, *abort_flag != 0)) scores_read();
-                __nanosleep(100);
-            }
     }
     fence_before();
     __syncthreads();

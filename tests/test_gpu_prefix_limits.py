@@ -1,6 +1,8 @@
 """Shared-prefix decode attention at the limits of its plan: more sequences and
 groups than the caches of a CTA hold, ranges that pass thousands of sequences
 with no tiles of their own; which design takes which batch."""
+import time
+
 import pytest
 import torch
 
@@ -88,3 +90,28 @@ def test_prefix_without_groups(kv):
     if kv == "fp8":
         assert torch.equal(bt.run(), bt.run(algo="mma"))
     _check(bt)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("cta", [0, 1, 151, 152, 303, -1])
+def test_prefix_expired_waits_in_many_segments(kv, cta):
+    """A CTA with several segments of several tiles gives up at its first tile:
+    all of its roles leave, whatever is still to come in its range."""
+    lens = tuple(600 + 37 * (i % 11) for i in range(56))
+    bt = Batch(lens, [(0, 30, 320), (30, 56, 448)], 16, 8, bs=64, seed=40, kv=kv)
+    ws = pk.prefix_decode_workspace(bt.pool, len(lens), 2, 16, bt.max_len)
+    good = bt.run(workspace=ws)
+    try:
+        pk.set_first_wait_limit_for_testing(0, cta)
+        t0 = time.perf_counter()
+        out = bt.run(workspace=ws)
+        torch.cuda.synchronize()
+        took = time.perf_counter() - t0
+    finally:
+        pk.set_first_wait_limit_for_testing(-1)
+    assert took < 5.0 and bt.pool.errors() == pk.ERRBIT_TIMEOUT
+    lost = torch.isnan(out).any(2)
+    assert torch.isnan(out[lost]).all() and torch.equal(out[~lost], good[~lost])
+    assert lost.all() if cta < 0 else lost.any() and not lost.all()
+    bt.pool.clear_errors()
+    assert torch.equal(bt.run(workspace=ws), good) and bt.pool.errors() == 0
