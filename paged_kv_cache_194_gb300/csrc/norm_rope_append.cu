@@ -28,9 +28,13 @@
 //    a token ahead); 24 warps per SM overlap one another's waits.  Fetching the
 //    rows a token ahead as well costs the registers of a third of the warps, and
 //    was slower (170 us where this takes 130).
-// 4096 tokens of 48 heads, BF16: 17.4 us, 5.9 TB/s (87 % of the measured copy
-// rate).  32771 tokens, three position axes, interleaved, FP8 pool: 130 us, 5.7
-// TB/s (84 %).  64 tokens: 3 us, an empty launch being 2.
+// 4096 tokens of 48 heads, BF16, 103 MB: 21.1 us, 4.9 TB/s (72 % of the measured
+// copy rate), over buffers that rotate through six times that much; 17.5 us on
+// the same ones again and again, which the L2 (129 MB) serves in part.  What
+// bounds it is the walk, not memory: a warp takes about seven tokens, and asks
+// for the rows of one only after it has stored those of the one before.  32771
+// tokens, three position axes, interleaved, FP8 pool: 132 us, 5.6 TB/s (83 %).  64
+// tokens: 3 us, an empty launch being 2.
 #include "device_common.cuh"
 #include "step_internal.h"
 
