@@ -322,8 +322,9 @@ int32_t paged_decode_algo(const pkv_pool* pool, int32_t group, pkv_algo requeste
  *   algo          PKV_ALGO_AUTO: the sharing design (tcgen05) where it serves
  *                 the pool, else paged_decode_attention's choice, which reads
  *                 every sequence's prefix (from L2, mostly) and looks at no
- *                 group; that also for FP8 pools when num_groups is 0, where it
- *                 is the faster one.  PKV_ALGO_TC: the sharing design or
+ *                 group; that also for FP8 pools when num_groups is 0 and a KV
+ *                 head has less than 8 query heads, where it is the faster one.
+ *                 PKV_ALGO_TC: the sharing design or
  *                 PKV_ERR_UNSUPPORTED.  PKV_ALGO_MMA, PKV_ALGO_SIMT: those.
  *                 The sharing design serves BF16 and FP8 pools of head_dim 128, up to
  *                 4096 sequences, 512 groups and 128 query heads per KV head.

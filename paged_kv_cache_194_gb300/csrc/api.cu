@@ -659,15 +659,17 @@ bool encode_q_map(CUtensorMap* map, const void* q, int num_seqs, int num_q_heads
 }
 
 // PKV_ALGO_TC when the sharing design runs, else what decode attention runs.
-// Without groups there is nothing to share, and over FP8 pools AUTO leaves the
-// call to decode attention (us here / there, 32 query over 8 KV heads: 74 / 59
-// for 64 x 2048 tokens, 70 / 59 for 8 x 16384, 40 / 28 for 256 x 64, 36 / 31 for
-// 64 of up to 1024; only few long sequences lose, 23 / 34 for 1 x 16384).  Over
-// BF16 pools the sharing design is as fast or faster (89 / 88, 87 / 92, 27 / 23,
-// 33 / 36, 20 / 67).
+// Without groups there is nothing to share, and over FP8 pools AUTO leaves calls
+// of less than 8 query heads per KV head to decode attention (us here / there, 32
+// query over 8 KV heads: 72 / 59 for 64 x 2048 tokens, 70 / 59 for 8 x 16384, 40 /
+// 28 for 256 x 64, 36 / 31 for 64 of up to 1024; only few long sequences lose, 23
+// / 34 for 1 x 16384).  From 8 heads on the sharing design, whose time hardly
+// depends on them, is as fast or faster (8: 74 / 64, 68 / 65 and 20 / 23 for 8 x
+// 2048; 16: 28 / 44, 28 / 70, 15 / 47), and over BF16 pools for any number (89 /
+// 88, 87 / 92, 27 / 23, 33 / 36, 20 / 67).
 int prefix_design(const pkv_pool* p, int num_seqs, int num_groups, int num_q_heads, int max_seq_len, pkv_algo algo) {
     const int gh = num_q_heads / p->d.num_kv_heads;
-    const bool left = num_groups == 0 && p->d.kv_dtype == PKV_FP8_E4M3;
+    const bool left = num_groups == 0 && p->d.kv_dtype == PKV_FP8_E4M3 && gh < 8;
     if ((algo == PKV_ALGO_AUTO && !left) || algo == PKV_ALGO_TC) {
         pkv_pool* mp = const_cast<pkv_pool*>(p);
         if (prefix_tc_fits(p, num_seqs, num_groups, gh, max_seq_len) && ensure_tmaps(mp) &&

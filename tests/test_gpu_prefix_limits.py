@@ -81,13 +81,16 @@ def test_prefix_shapes_take_the_sharing_design(shape, kv):
     assert Batch(lens, groups, kv=kv).design() == "tc"
 
 
+@pytest.mark.parametrize("q_heads", [2, 8, 14, 16, 40, 128])
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
-def test_prefix_without_groups(kv):
-    """Nothing to share: over FP8 pools the call is decode attention, bit for
-    bit; asked for by name, the sharing design still takes it."""
-    bt = Batch((900, 1, 0, 64, 2000), [], 8, 2, kv=kv, seed=6)
-    assert bt.design() == ("mma" if kv == "fp8" else "tc") and bt.design("tc") == "tc"
-    if kv == "fp8":
+def test_prefix_without_groups(kv, q_heads):
+    """Nothing to share: over FP8 pools calls of less than 8 query heads per KV
+    head are decode attention, bit for bit; asked for by name, and for more
+    heads, the sharing design takes them."""
+    bt = Batch((900, 1, 0, 64, 2000), [], q_heads, 2, kv=kv, seed=6)
+    left = kv == "fp8" and q_heads < 16
+    assert bt.design() == ("mma" if left else "tc") and bt.design("tc") == "tc"
+    if left:
         assert torch.equal(bt.run(), bt.run(algo="mma"))
     _check(bt)
 
