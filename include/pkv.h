@@ -62,6 +62,7 @@ typedef enum pkv_dtype { PKV_F32 = 0, PKV_BF16 = 1, PKV_FP8_E4M3 = 2 } pkv_dtype
 #define PKV_ERRBIT_POSITION 16 /* a position outside [0, max_pos) of the rotation table */
 #define PKV_ERRBIT_STEP 32     /* tables: new_tokens < 0 or past max_tokens, or a free list state that cannot be */
 #define PKV_ERRBIT_GROUP 64    /* shared prefixes: offsets not ascending within [0, num_seqs], or a length < 0 */
+#define PKV_ERRBIT_OFFSETS 128 /* packed rows: a sequence's offsets do not ascend, or leave the rows */
 
 /* Kernel design used by paged_decode_attention. */
 typedef enum pkv_algo {
@@ -445,6 +446,128 @@ pkv_status kv_tables_release(const pkv_pool* pool, const int32_t* block_tables, 
                              const int32_t* seq_lens, const int32_t* finished, const int32_t* keep_blocks,
                              int32_t num_seqs, int32_t* free_ring, int32_t ring_size, const int32_t* free_state,
                              int32_t* seq_lens_out, int32_t* free_state_out, void* stream);
+
+/*
+ * A cache that is quantised as it is written, with a scale and an offset for
+ * every row ("TensorRT-LLM, in depth", "Quantization": a smaller element in the
+ * KV cache is memory, and so requests, won back).  The pool is that of
+ * kv_pool_create but for its element: codes of 4 or 8 bits, laid out
+ * [num_layers][num_blocks][num_kv_heads][block_size][head_dim] (two 4-bit codes
+ * a byte, element 2 j in the low half), and next to them one pair of bfloat16,
+ * (scale, offset), per row: [num_layers][num_blocks][num_kv_heads][block_size][2].
+ * A row x of head_dim values, N = 2^bits - 1, in binary32:
+ *     offset = the largest bfloat16 <= min(x)
+ *     scale  = the smallest bfloat16 >= max((max(x) - offset) / N, |offset| 2^-16, 2^-100)
+ *     code_i = floor((x_i - offset) * ((1 / scale) (1 + 2^-21)) + 1/2)
+ * and code c stands for offset + scale c: no value is off by more than half a
+ * scale.  (Halves go up; 16-bit inputs give them often, and the reciprocal's
+ * excess keeps its rounding out of them.)  A row with an infinity or a NaN, or
+ * whose range is not finite in binary32, stores (NaN, NaN) and codes of 0: it
+ * reads as NaN.
+ */
+typedef struct kv_quant_pool_desc {
+    int32_t num_layers;
+    int32_t num_blocks;
+    int32_t block_size;   /* 16, 32 or 64 */
+    int32_t num_kv_heads;
+    int32_t head_dim;     /* 64 or 128 */
+    int32_t bits;         /* 4 or 8 */
+    void* k_codes;        /* device, 16-byte aligned */
+    void* v_codes;
+    void* k_params;       /* device, 16-byte aligned */
+    void* v_params;
+    int32_t* error_word;  /* device, optional */
+} kv_quant_pool_desc;
+typedef struct kv_quant_pool kv_quant_pool;  /* host handle, as pkv_pool */
+pkv_status kv_quant_pool_create(const kv_quant_pool_desc* desc, kv_quant_pool** out);
+void kv_quant_pool_destroy(kv_quant_pool* pool);
+/* Bytes of one code tensor (K or V) and of one params tensor (either may be NULL). */
+pkv_status kv_quant_pool_bytes(const kv_quant_pool_desc* desc, size_t* codes_out, size_t* params_out);
+
+/*
+ * Quantise new rows into the pool.
+ *   k, v          device; token t's heads are [num_kv_heads][head_dim], contiguous,
+ *                 at element t * k_stride (v_stride): rows of one fused projection,
+ *                 or tensors of their own.  Strides are multiples of 8 elements
+ *                 (16 bytes) of in_dtype (PKV_F32 or PKV_BF16), >= 0.
+ *   slot_mapping  as kv_append: -1 skips the token, others outside the pool are
+ *                 skipped and set PKV_ERRBIT_SLOT.
+ */
+pkv_status kv_quant_append(const kv_quant_pool* pool, int32_t layer, const void* k, const void* v, pkv_dtype in_dtype,
+                           int64_t k_stride, int64_t v_stride, const int64_t* slot_mapping, int32_t num_tokens,
+                           void* stream);
+
+/*
+ * Read a cache back: the rows of a batch of sequences, packed one sequence after
+ * the other, as the values that they stand for ("How does TensorRT-LLM work?",
+ * "The paged KV cache": a prompt that begins like an earlier one starts from its
+ * blocks; its attention reads them in front of its own rows, prompt_attention).
+ *   offsets       device int32 [num_seqs + 1]: rows offsets[b] .. offsets[b + 1] - 1
+ *                 are tokens 0 .. of sequence b.  Offsets that do not ascend within
+ *                 [0, num_rows] set PKV_ERRBIT_OFFSETS, and that sequence is not
+ *                 read; rows before the first and behind the last sequence are left
+ *                 as they were.
+ *   block_tables  device int32 [num_seqs][max_blocks_per_seq].  A row past its
+ *                 table (PKV_ERRBIT_SEQ_LEN), or whose entry is outside the pool
+ *                 (PKV_ERRBIT_BLOCK_ID), becomes zero.
+ *   k_out, v_out  device [num_rows][num_kv_heads][head_dim], F32 for an F32 pool,
+ *                 else BF16: code * scale (+ offset) in binary32, rounded to nearest.
+ */
+pkv_status kv_read(const pkv_pool* pool, int32_t layer, const int32_t* block_tables, int32_t max_blocks_per_seq,
+                   const int32_t* offsets, int32_t num_seqs, int32_t num_rows, void* k_out, void* v_out, void* stream);
+pkv_status kv_quant_read(const kv_quant_pool* pool, int32_t layer, const int32_t* block_tables,
+                         int32_t max_blocks_per_seq, const int32_t* offsets, int32_t num_seqs, int32_t num_rows,
+                         void* k_out, void* v_out, void* stream);
+
+/*
+ * paged_decode_attention over a quantised cache: same arguments and result, with
+ * K_t and V_t the values that the codes stand for.  q and out are BF16; any number
+ * of query heads per KV head.  A row that reads as NaN makes the queries that see
+ * it NaN; rows behind a sequence's end are not looked at.
+ *   workspace  at least paged_quant_decode_plan's bytes, 256-byte aligned, zeroed
+ *              before its first call; every call leaves its counters zero.  Calls
+ *              that share a workspace are stream-ordered.
+ */
+pkv_status paged_quant_decode_plan(const kv_quant_pool* pool, int32_t num_seqs, int32_t num_q_heads, int32_t max_seq_len,
+                                   size_t* workspace_bytes_out);
+pkv_status paged_quant_decode_attention(const void* q, pkv_dtype q_dtype, const kv_quant_pool* pool, int32_t layer,
+                                        const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                                        int32_t num_seqs, int32_t num_q_heads, int32_t max_seq_len, float scale,
+                                        void* workspace, size_t workspace_bytes, void* out, void* stream);
+
+/*
+ * Causal attention over whole prompts ("How does TensorRT-LLM work?", "The full
+ * journey of one request": the prompt's tokens are processed at once), packed one
+ * after the other, of any lengths, with grouped heads.  Sequence b's queries are
+ * rows q_offsets[b] .. q_offsets[b + 1] - 1 of q, its keys and values rows
+ * k_offsets[b] .. k_offsets[b + 1] - 1 of k and v.  Its n queries are the last n
+ * of its m positions: query i sees keys 0 .. m - n + i (m = n: a whole prompt; m >
+ * n: a chunk, with the rows of a cached prefix in front).  A query that sees no
+ * key gets a zero row.
+ *   q, k, v    device, dtype PKV_BF16 or PKV_F32; row t's heads are [heads][head_dim],
+ *              contiguous, at element t * stride: rows of one projection, or tensors
+ *              of their own.  Strides are multiples of 8 elements, >= heads * head_dim
+ *              (for one row: any).  head_dim 64 or 128.
+ *   out        device [q_rows][num_q_heads][head_dim] of dtype; may not overlap the
+ *              inputs.  Rows of no sequence are left as they were.
+ *   q_offsets, k_offsets   device int32 [num_seqs + 1], ascending in [0, q_rows] and
+ *              [0, k_rows]; may be the same array.  A sequence whose offsets are not
+ *              sets PKV_ERRBIT_OFFSETS and is left out.
+ *   error_word device int32, optional (PKV_ERRBIT_OFFSETS, PKV_ERRBIT_TIMEOUT)
+ *   workspace  prompt_attention_plan's bytes, 256-byte aligned, zeroed before its first
+ *              call (NULL where the plan needs none); stream-ordered calls may share it
+ * Offsets are read on the device: a captured call may be replayed with other ones.
+ * Softmax and accumulation are binary32; with BF16 the weights are rounded to BF16
+ * for their product with V.  A value of v that is not finite reaches the queries up
+ * to 127 positions before it, too; rows of other sequences never do.
+ */
+pkv_status prompt_attention_plan(int32_t num_seqs, int32_t q_rows, int32_t num_q_heads, int32_t num_kv_heads,
+                                 int32_t head_dim, pkv_dtype dtype, size_t* workspace_bytes_out);
+pkv_status prompt_attention(const void* q, const void* k, const void* v, pkv_dtype dtype, int64_t q_stride,
+                            int64_t k_stride, int64_t v_stride, const int32_t* q_offsets, const int32_t* k_offsets,
+                            int32_t num_seqs, int32_t q_rows, int32_t k_rows, int32_t num_q_heads, int32_t num_kv_heads,
+                            int32_t head_dim, float scale, void* workspace, size_t workspace_bytes, void* out,
+                            int32_t* error_word, void* stream);
 
 /*
  * Host-side block manager ("How does TensorRT-LLM work?", "The paged KV

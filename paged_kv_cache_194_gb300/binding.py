@@ -22,7 +22,7 @@ ALGOS = {"auto": 0, "simt": 1, "mma": 2, "tc": 3}
 STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported", 3: "workspace", 4: "cuda error",
           5: "device bounds", 6: "out of blocks", 7: "inconsistent"}
 ERRBIT_BLOCK_ID, ERRBIT_SLOT, ERRBIT_SEQ_LEN, ERRBIT_TIMEOUT = 1, 2, 4, 8
-ERRBIT_POSITION, ERRBIT_STEP, ERRBIT_GROUP = 16, 32, 64
+ERRBIT_POSITION, ERRBIT_STEP, ERRBIT_GROUP, ERRBIT_OFFSETS = 16, 32, 64, 128
 
 # Every symbol include/pkv.h declares.
 EXPORTS = ("kv_pool_create", "kv_pool_destroy", "kv_pool_tensor_bytes", "kv_bytes_per_token",
@@ -31,6 +31,9 @@ EXPORTS = ("kv_pool_create", "kv_pool_destroy", "kv_pool_tensor_bytes", "kv_byte
            "paged_decode_append_attention",
            "paged_prefix_decode_plan", "paged_prefix_decode_algo", "paged_prefix_decode_attention",
            "kv_append_norm_rope", "kv_tables_grow", "kv_tables_release",
+           "kv_quant_pool_create", "kv_quant_pool_destroy", "kv_quant_pool_bytes", "kv_quant_append", "kv_read",
+           "kv_quant_read", "paged_quant_decode_plan", "paged_quant_decode_attention", "prompt_attention_plan",
+           "prompt_attention",
            "paged_decode_attention_static_ws", "pkv_set_first_wait_limit_for_testing", "pkv_status_string",
            "pkv_last_cuda_error",
            "kv_block_manager_create", "kv_block_manager_destroy", "kv_bm_num_free", "kv_bm_add_sequence",
@@ -62,6 +65,13 @@ class NormRopeDesc(ctypes.Structure):
                 ("interleaved", ctypes.c_int32), ("num_axes", ctypes.c_int32), ("sections", ctypes.c_int32 * 3),
                 ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("weight_dtype", ctypes.c_int),
                 ("eps", ctypes.c_float)]
+
+
+class QuantPoolDesc(ctypes.Structure):
+    _fields_ = [("num_layers", ctypes.c_int32), ("num_blocks", ctypes.c_int32), ("block_size", ctypes.c_int32),
+                ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("bits", ctypes.c_int32),
+                ("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p), ("k_params", ctypes.c_void_p),
+                ("v_params", ctypes.c_void_p), ("error_word", ctypes.c_void_p)]
 
 
 _lib = None
@@ -126,6 +136,28 @@ def lib() -> ctypes.CDLL:
     L.kv_tables_grow.argtypes = [P, P, c.c_int32, P, P, c.c_int32, P, c.c_int32, P, c.c_int32, P, P, P, P, P, P, P, P]
     L.kv_tables_release.restype = c.c_int
     L.kv_tables_release.argtypes = [P, P, c.c_int32, P, P, P, c.c_int32, P, c.c_int32, P, P, P, P]
+    L.kv_quant_pool_create.restype = c.c_int
+    L.kv_quant_pool_create.argtypes = [c.POINTER(QuantPoolDesc), c.POINTER(P)]
+    L.kv_quant_pool_destroy.restype = None
+    L.kv_quant_pool_destroy.argtypes = [P]
+    L.kv_quant_pool_bytes.restype = c.c_int
+    L.kv_quant_pool_bytes.argtypes = [c.POINTER(QuantPoolDesc), c.POINTER(c.c_size_t), c.POINTER(c.c_size_t)]
+    L.kv_quant_append.restype = c.c_int
+    L.kv_quant_append.argtypes = [P, c.c_int32, P, P, c.c_int, c.c_int64, c.c_int64, P, c.c_int32, P]
+    for read in (L.kv_read, L.kv_quant_read):
+        read.restype = c.c_int
+        read.argtypes = [P, c.c_int32, P, c.c_int32, P, c.c_int32, c.c_int32, P, P, P]
+    L.paged_quant_decode_plan.restype = c.c_int
+    L.paged_quant_decode_plan.argtypes = [P, c.c_int32, c.c_int32, c.c_int32, c.POINTER(c.c_size_t)]
+    L.paged_quant_decode_attention.restype = c.c_int
+    L.paged_quant_decode_attention.argtypes = [P, c.c_int, P, c.c_int32, P, c.c_int32, P, c.c_int32, c.c_int32,
+                                               c.c_int32, c.c_float, P, c.c_size_t, P, P]
+    L.prompt_attention_plan.restype = c.c_int
+    L.prompt_attention_plan.argtypes = [c.c_int32, c.c_int32, c.c_int32, c.c_int32, c.c_int32, c.c_int,
+                                        c.POINTER(c.c_size_t)]
+    L.prompt_attention.restype = c.c_int
+    L.prompt_attention.argtypes = [P, P, P, c.c_int, c.c_int64, c.c_int64, c.c_int64, P, P, c.c_int32, c.c_int32,
+                                   c.c_int32, c.c_int32, c.c_int32, c.c_int32, c.c_float, P, c.c_size_t, P, P, P]
     L.pkv_set_first_wait_limit_for_testing.restype = None
     L.pkv_set_first_wait_limit_for_testing.argtypes = [c.c_int32, c.c_int32]
     L.pkv_status_string.restype = c.c_char_p
@@ -201,6 +233,7 @@ class KVPool:
         self.handle = h
         # for the native calls
         self.address = h.value
+        self.device = self.k.device
         self.device_index = self.k.device.index if self.k.is_cuda else -1
 
     @property
@@ -410,22 +443,26 @@ _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.curre
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
-def _here(pool: KVPool, stream) -> bool:
+def _here(pool, stream) -> bool:
     """Whether a call needs no other device or stream than the current ones."""
     return stream is None and (pool.device_index < 0 or pool.device_index == _current_device())
 
 
-def _on(pool: KVPool, stream):
+def _on(pool, stream):
     """Context in which the pool's device is current, and `stream` when given
     (so that allocations belong to it)."""
+    return _on_device(pool.device, stream, "the pool")
+
+
+def _on_device(device: torch.device, stream, whose: str):
     if stream is not None:
-        if stream.device != pool.k.device:
-            raise ValueError("stream must be on %s, the pool's device, not %s" % (pool.k.device, stream.device))
+        if stream.device != device:
+            raise ValueError("stream must be on %s, %s's device, not %s" % (device, whose, stream.device))
         return torch.cuda.stream(stream)
-    return torch.cuda.device(pool.k.device)
+    return torch.cuda.device(device)
 
 
-def _stream_handle(pool: KVPool) -> int:
+def _stream_handle(pool) -> int:
     return _raw_stream(pool.device_index) if pool.device_index >= 0 else 0
 
 
@@ -579,3 +616,160 @@ def kv_tables_release(pool: KVPool, block_tables: torch.Tensor, seq_lens: torch.
     if rc:
         raise PkvError(rc, "kv_tables_release")
     return seq_lens_out, free_state_out
+
+
+# ------------------------------------------------- a quantised cache, whole prompts
+class QuantKVPool:
+    """A paged KV cache of 4- or 8-bit codes: k_codes and v_codes [layers, blocks,
+    kv_heads, block_size, head_dim * bits / 8] (torch.uint8; 4 bits: element 2 j
+    in the low half of byte j) and k_params and v_params [layers, blocks,
+    kv_heads, block_size, 2] (bfloat16: scale and offset of each row).  A code c
+    stands for offset + scale * c."""
+
+    def __init__(self, num_layers: int, num_blocks: int, block_size: int, num_kv_heads: int, head_dim: int, bits: int,
+                 device: str = "cuda", fill: Optional[int] = None):
+        self.num_layers, self.num_blocks, self.block_size = num_layers, num_blocks, block_size
+        self.num_kv_heads, self.head_dim, self.bits = num_kv_heads, head_dim, bits
+        self.kv_dtype = "q%d" % bits
+        self.handle = self.address = None
+        self._desc = QuantPoolDesc(num_layers, num_blocks, block_size, num_kv_heads, head_dim, bits)
+        _check(lib().kv_quant_pool_bytes(ctypes.byref(self._desc), None, None), "kv_quant_pool_bytes")
+        rows = (num_layers, num_blocks, num_kv_heads, block_size)
+        self.k_codes, self.v_codes = (torch.empty(rows + (head_dim * bits // 8,), dtype=torch.uint8, device=device)
+                                      for _ in range(2))
+        self.k_params, self.v_params = (torch.empty(rows + (2,), dtype=torch.bfloat16, device=device) for _ in range(2))
+        if fill is not None:
+            for x in (self.k_codes, self.v_codes, self.k_params, self.v_params):
+                x.view(torch.uint8).fill_(fill)
+        self.error_word = torch.zeros(1, dtype=torch.int32, device=device)
+        for name in ("k_codes", "v_codes", "k_params", "v_params", "error_word"):
+            setattr(self._desc, name, getattr(self, name).data_ptr())
+        h = ctypes.c_void_p()
+        _check(lib().kv_quant_pool_create(ctypes.byref(self._desc), ctypes.byref(h)), "kv_quant_pool_create")
+        self.handle, self.address = h, h.value
+        self.device = self.k_codes.device
+        self.device_index = self.device.index if self.k_codes.is_cuda else -1
+
+    def errors(self) -> int:
+        """Read (synchronously) the error bits the kernels have set."""
+        return int(self.error_word.item())
+
+    def clear_errors(self):
+        self.error_word.zero_()
+
+    def close(self):
+        if getattr(self, "handle", None) is not None and self.handle.value:
+            lib().kv_quant_pool_destroy(self.handle)
+            self.handle = self.address = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def kv_quant_append(pool: QuantKVPool, layer: int, k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor,
+                    stream=None) -> None:
+    """Quantise k, v [T, Hkv, D] (float32 or bfloat16, possibly slices of one
+    projection's rows) into the pool at slot_mapping [T] (int64; -1: skipped),
+    each row with a scale and an offset of its own."""
+    if not _here(pool, stream):
+        with _on(pool, stream):
+            return kv_quant_append(pool, layer, k, v, slot_mapping)
+    rc = _step().quant_append(pool.address, pool.device_index, pool.num_kv_heads, pool.head_dim, layer, k, v, slot_mapping,
+                              _stream_handle(pool))
+    if rc:
+        raise PkvError(rc, "kv_quant_append")
+
+
+def kv_read(pool, layer: int, block_tables: torch.Tensor, offsets: torch.Tensor, num_rows: int,
+            k_out: Optional[torch.Tensor] = None, v_out: Optional[torch.Tensor] = None,
+            stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """The rows of a batch read back from a KVPool or a QuantKVPool, packed: rows
+    offsets[b] .. offsets[b + 1] - 1 (int32 [B + 1]) are the first tokens of
+    sequence b, gathered through block_tables [B, max_blocks] (int32).  Returns
+    k, v [num_rows, Hkv, D], float32 from a float32 pool, else bfloat16; rows of
+    no sequence keep what k_out and v_out held."""
+    if not _here(pool, stream):
+        with _on(pool, stream):
+            return kv_read(pool, layer, block_tables, offsets, num_rows, k_out, v_out)
+    shape, f32 = (num_rows, pool.num_kv_heads, pool.head_dim), pool.kv_dtype == "f32"
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=torch.float32 if f32 else torch.bfloat16, device=pool.device)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=torch.float32 if f32 else torch.bfloat16, device=pool.device)
+    rc = _step().read_rows(pool.address, isinstance(pool, QuantKVPool), pool.device_index, pool.num_kv_heads, pool.head_dim,
+                           f32, layer, block_tables, offsets, num_rows, k_out, v_out, _stream_handle(pool))
+    if rc:
+        raise PkvError(rc, "kv_read")
+    return k_out, v_out
+
+
+def quant_decode_workspace(pool: QuantKVPool, num_seqs: int, num_q_heads: int, max_seq_len: int) -> Optional[torch.Tensor]:
+    """A zeroed workspace for paged_quant_decode_attention calls of this size."""
+    if not _here(pool, None):
+        with _on(pool, None):
+            return quant_decode_workspace(pool, num_seqs, num_q_heads, max_seq_len)
+    ws = ctypes.c_size_t()
+    _check(lib().paged_quant_decode_plan(pool.handle, num_seqs, num_q_heads, max_seq_len, ctypes.byref(ws)),
+           "paged_quant_decode_plan")
+    return torch.zeros(ws.value, dtype=torch.uint8, device=pool.device) if ws.value else None
+
+
+def paged_quant_decode_attention(q: torch.Tensor, pool: QuantKVPool, layer: int, block_tables: torch.Tensor,
+                                 seq_lens: torch.Tensor, max_seq_len: int, scale: float,
+                                 out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                                 stream=None) -> torch.Tensor:
+    """paged_decode_attention over a quantised cache: q [B, Hq, D] bfloat16."""
+    if not _here(pool, stream):
+        with _on(pool, stream):
+            return paged_quant_decode_attention(q, pool, layer, block_tables, seq_lens, max_seq_len, scale, out, workspace)
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if workspace is None and q.dim() == 3:
+        workspace = quant_decode_workspace(pool, q.shape[0], q.shape[1], max_seq_len)
+    rc = _step().quant_attention(pool.address, pool.device_index, pool.head_dim, layer, q, block_tables, seq_lens,
+                                 max_seq_len, scale, workspace, out, _stream_handle(pool))
+    if rc:
+        raise PkvError(rc, "paged_quant_decode_attention")
+    return out
+
+
+def prompt_attention_workspace(q: torch.Tensor, num_seqs: int, num_kv_heads: int) -> Optional[torch.Tensor]:
+    """A zeroed workspace for prompt_attention calls of this size."""
+    index = q.device.index if q.is_cuda else -1
+    if index >= 0 and index != _current_device():
+        with torch.cuda.device(index):
+            return prompt_attention_workspace(q, num_seqs, num_kv_heads)
+    if q.dim() != 3 or q.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("q must be [rows, num_q_heads, head_dim], float32 or bfloat16")
+    ws = ctypes.c_size_t()
+    _check(lib().prompt_attention_plan(num_seqs, q.shape[0], q.shape[1], num_kv_heads, q.shape[2], _dtype_code(q.dtype),
+                                       ctypes.byref(ws)), "prompt_attention_plan")
+    return torch.zeros(ws.value, dtype=torch.uint8, device=q.device) if ws.value else None
+
+
+def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offsets: torch.Tensor, k_offsets: torch.Tensor,
+                     scale: float, out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                     error_word: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Causal attention over packed prompts: sequence b's queries are rows
+    q_offsets[b] .. q_offsets[b + 1] - 1 of q [Tq, Hq, D], its keys and values
+    rows k_offsets[b] .. k_offsets[b + 1] - 1 of k and v [Tk, Hkv, D] (bfloat16
+    or float32, possibly slices of one projection's rows); its queries are the
+    last of its positions.  Returns [Tq, Hq, D]; rows of no sequence keep what
+    `out` held.  error_word: int32 [1], gets ERRBIT_OFFSETS where offsets do not
+    ascend within the rows."""
+    index = q.device.index if q.is_cuda else -1
+    if stream is not None or (index >= 0 and index != _current_device()):
+        with _on_device(q.device, stream, "q"):
+            return prompt_attention(q, k, v, q_offsets, k_offsets, scale, out, workspace, error_word)
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if workspace is None and q.dim() == 3 and k.dim() == 3:
+        workspace = prompt_attention_workspace(q, max(0, q_offsets.numel() - 1), k.shape[1])
+    rc = _step().prompt_attention(index, q, k, v, q_offsets, k_offsets, scale, workspace, out, error_word,
+                                  _raw_stream(index) if index >= 0 else 0)
+    if rc:
+        raise PkvError(rc, "prompt_attention")
+    return out

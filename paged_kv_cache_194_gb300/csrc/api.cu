@@ -9,6 +9,7 @@
 #include <mutex>
 
 #include "pkv_internal.h"
+#include "quant_internal.h"
 #include "step_internal.h"
 
 namespace pkv {
@@ -209,6 +210,24 @@ bool ensure_tmaps(pkv_pool* p) {
     return state == 1;
 }
 }  // namespace
+
+bool encode_map(CUtensorMap* map, int elem_bytes, int rank, const void* base, const uint64_t* dims,
+                const uint64_t* strides, const uint32_t* box) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc || rank < 2 || rank > 5) return false;
+    cuuint64_t d[5], st[4];
+    cuuint32_t bx[5], es[5];
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        bx[i] = box[i];
+        es[i] = 1;
+        if (i > 0) st[i - 1] = strides[i - 1];
+    }
+    const CUtensorMapDataType type = elem_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    return encode_tiled(enc, map, type, static_cast<cuuint32_t>(rank), const_cast<void*>(base), d, st, bx, es,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
 
 void set_last_error(cudaError_t e) {
     std::snprintf(g_last_cuda_error, sizeof(g_last_cuda_error), "%s: %s", cudaGetErrorName(e),

@@ -330,12 +330,157 @@ PyObject* tables_release(PyObject*, PyObject* const* argv, Py_ssize_t n) {
     });
 }
 
+// (pool, device, kv_heads, head_dim, layer, k, v, slot_mapping, stream)
+PyObject* quant_append(PyObject*, PyObject* const* argv, Py_ssize_t n) {
+    return guarded([&]() -> long {
+        Args a(argv, n, 9);
+        const auto* pool = static_cast<const kv_quant_pool*>(a.address());
+        const Place at_{a.int32("device")};
+        const int64_t kv_heads = a.integer(), dim = a.integer();
+        const int32_t layer = a.int32("layer");
+        const at::Tensor& k = a.tensor("k");
+        const at::Tensor& v = a.tensor("v");
+        const at::Tensor& slots = a.tensor("slot_mapping");
+        if (k.dim() != 3) refuse("k", "must be [T, num_kv_heads, head_dim]");
+        const int64_t T = k.size(0);
+        if (v.scalar_type() != k.scalar_type()) refuse("v", "must have k's dtype");
+        const int64_t ks = head_rows(at_, "k", k, T, kv_heads, dim, k.scalar_type());
+        const int64_t vs = head_rows(at_, "v", v, T, kv_heads, dim, k.scalar_type());
+        const auto* ps = static_cast<const int64_t*>(at_.data("slot_mapping", slots, at::kLong, {T}));
+        void* stream = a.address();
+        const pkv_dtype type = code_of("k", k);
+        const int32_t tokens = count_of("k", T);
+        at_.runnable();
+        const void *pk = k.data_ptr(), *pv = v.data_ptr();
+        return released([&] { return kv_quant_append(pool, layer, pk, pv, type, ks, vs, ps, tokens, stream); });
+    });
+}
+
+// (pool, quantised, device, kv_heads, head_dim, f32, layer, block_tables, offsets, num_rows, k_out, v_out, stream)
+PyObject* read_rows(PyObject*, PyObject* const* argv, Py_ssize_t n) {
+    return guarded([&]() -> long {
+        Args a(argv, n, 13);
+        const void* pool = a.address();
+        const bool quantised = a.integer() != 0;
+        const Place at_{a.int32("device")};
+        const int64_t kv_heads = a.integer(), dim = a.integer();
+        const at::ScalarType type = a.integer() ? at::kFloat : at::kBFloat16;
+        const int32_t layer = a.int32("layer");
+        const at::Tensor& tables = a.tensor("block_tables");
+        const at::Tensor& offsets = a.tensor("offsets");
+        const int32_t rows = a.int32("num_rows");
+        if (offsets.dim() != 1 || offsets.size(0) < 1) refuse("offsets", "must be [num_seqs + 1]");
+        const int64_t B = offsets.size(0) - 1;
+        const int32_t width = table_width(tables, B), num_seqs = count_of("offsets", B);
+        const auto* pt = static_cast<const int32_t*>(at_.data("block_tables", tables, at::kInt));
+        const auto* po = static_cast<const int32_t*>(at_.data("offsets", offsets, at::kInt));
+        void* pk = at_.data("k_out", a.tensor("k_out"), type, {rows, kv_heads, dim});
+        void* pv = at_.data("v_out", a.tensor("v_out"), type, {rows, kv_heads, dim});
+        void* stream = a.address();
+        at_.runnable();
+        return released([&] {
+            return quantised ? kv_quant_read(static_cast<const kv_quant_pool*>(pool), layer, pt, width, po, num_seqs, rows,
+                                             pk, pv, stream)
+                             : kv_read(static_cast<const pkv_pool*>(pool), layer, pt, width, po, num_seqs, rows, pk, pv,
+                                       stream);
+        });
+    });
+}
+
+// (pool, device, head_dim, layer, q, block_tables, seq_lens, max_seq_len, scale, workspace | None, out, stream)
+PyObject* quant_attention(PyObject*, PyObject* const* argv, Py_ssize_t n) {
+    return guarded([&]() -> long {
+        Args a(argv, n, 12);
+        const auto* pool = static_cast<const kv_quant_pool*>(a.address());
+        const Place at_{a.int32("device")};
+        const int64_t dim = a.integer();
+        const int32_t layer = a.int32("layer");
+        const at::Tensor& q = a.tensor("q");
+        const at::Tensor& tables = a.tensor("block_tables");
+        const at::Tensor& lens = a.tensor("seq_lens");
+        const int32_t max_len = a.int32("max_seq_len");
+        const float scale = static_cast<float>(a.real());
+        if (q.dim() != 3 || q.size(2) != dim) refuse("q", "must be [num_seqs, num_q_heads, head_dim]");
+        const int64_t B = q.size(0);
+        const int32_t width = table_width(tables, B), num_seqs = count_of("q", B), heads = count_of("q", q.size(1));
+        const void* pq = at_.data("q", q, kAny);
+        const pkv_dtype type = code_of("q", q);
+        const auto* pt = static_cast<const int32_t*>(at_.data("block_tables", tables, at::kInt));
+        const auto* pl = static_cast<const int32_t*>(at_.data("seq_lens", lens, at::kInt, {B}));
+        void* ws = nullptr;
+        size_t ws_bytes = 0;
+        if (a.none()) {
+            a.skip();
+        } else {
+            const at::Tensor& w = a.tensor("workspace");
+            ws = at_.data("workspace", w, kAny);
+            ws_bytes = w.nbytes();
+        }
+        void* pout = at_.data("out", a.tensor("out"), q.scalar_type(), {B, q.size(1), dim});
+        void* stream = a.address();
+        at_.runnable();
+        return released([&] {
+            return paged_quant_decode_attention(pq, type, pool, layer, pt, width, pl, num_seqs, heads, max_len, scale, ws,
+                                                ws_bytes, pout, stream);
+        });
+    });
+}
+
+// (device, q, k, v, q_offsets, k_offsets, scale, workspace | None, out, error_word | None, stream)
+PyObject* prompt(PyObject*, PyObject* const* argv, Py_ssize_t n) {
+    return guarded([&]() -> long {
+        Args a(argv, n, 11);
+        const Place at_{a.int32("device")};
+        const at::Tensor& q = a.tensor("q");
+        const at::Tensor& k = a.tensor("k");
+        const at::Tensor& v = a.tensor("v");
+        const at::Tensor& qo = a.tensor("q_offsets");
+        const at::Tensor& ko = a.tensor("k_offsets");
+        const float scale = static_cast<float>(a.real());
+        if (q.dim() != 3) refuse("q", "must be [rows, num_q_heads, head_dim]");
+        if (k.dim() != 3) refuse("k", "must be [rows, num_kv_heads, head_dim]");
+        const int64_t T = q.size(0), Hq = q.size(1), D = q.size(2), Tk = k.size(0), Hk = k.size(1);
+        const int64_t qs = head_rows(at_, "q", q, T, Hq, D, q.scalar_type());
+        const int64_t ks = head_rows(at_, "k", k, Tk, Hk, D, q.scalar_type());
+        const int64_t vs = head_rows(at_, "v", v, Tk, Hk, D, q.scalar_type());
+        if (qo.dim() != 1 || qo.size(0) < 1) refuse("q_offsets", "must be [num_seqs + 1]");
+        const int64_t B = qo.size(0) - 1;
+        const auto* pqo = static_cast<const int32_t*>(at_.data("q_offsets", qo, at::kInt));
+        const auto* pko = static_cast<const int32_t*>(at_.data("k_offsets", ko, at::kInt, {B + 1}));
+        void* ws = nullptr;
+        size_t ws_bytes = 0;
+        if (a.none()) {
+            a.skip();
+        } else {
+            const at::Tensor& w = a.tensor("workspace");
+            ws = at_.data("workspace", w, kAny);
+            ws_bytes = w.nbytes();
+        }
+        void* pout = at_.data("out", a.tensor("out"), q.scalar_type(), {T, Hq, D});
+        int32_t* err = nullptr;
+        if (a.none()) a.skip();
+        else err = static_cast<int32_t*>(at_.data("error_word", a.tensor("error_word"), at::kInt, {1}));
+        void* stream = a.address();
+        const pkv_dtype type = code_of("q", q);
+        const int32_t num_seqs = count_of("q_offsets", B), rows = count_of("q", T), k_rows = count_of("k", Tk);
+        const int32_t q_heads = count_of("q", Hq), kv_heads = count_of("k", Hk), dim = count_of("q", D);
+        at_.runnable();
+        const void *pq = q.data_ptr(), *pk = k.data_ptr(), *pv = v.data_ptr();
+        return released([&] {
+            return prompt_attention(pq, pk, pv, type, qs, ks, vs, pqo, pko, num_seqs, rows, k_rows, q_heads, kv_heads, dim,
+                                    scale, ws, ws_bytes, pout, err, stream);
+        });
+    });
+}
+
 template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
 PyMethodDef method(const char* name) {
     return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(F)), METH_FASTCALL, nullptr};
 }
 PyMethodDef methods[] = {method<prefix_attention>("prefix_attention"), method<norm_rope>("norm_rope"),
                          method<tables_grow>("tables_grow"), method<tables_release>("tables_release"),
+                         method<quant_append>("quant_append"), method<read_rows>("read_rows"),
+                         method<quant_attention>("quant_attention"), method<prompt>("prompt_attention"),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_pkvstep", "Native argument checks of the serving-step calls.", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
