@@ -559,7 +559,7 @@ pkv_status paged_quant_decode_attention(const void* q, pkv_dtype q_dtype, const 
  * Offsets are read on the device: a captured call may be replayed with other ones.
  * Softmax and accumulation are binary32; with BF16 the weights are rounded to BF16
  * for their product with V.  A value of v that is not finite reaches the queries up
- * to 127 positions before it, too; rows of other sequences never do.
+ * to 255 positions before it, too; rows of other sequences never do.
  */
 pkv_status prompt_attention_plan(int32_t num_seqs, int32_t q_rows, int32_t num_q_heads, int32_t num_kv_heads,
                                  int32_t head_dim, pkv_dtype dtype, size_t* workspace_bytes_out);

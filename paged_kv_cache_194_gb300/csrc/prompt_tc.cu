@@ -1,0 +1,558 @@
+// Causal attention over packed prompts on the 5th-generation tensor cores
+// (tcgen05 with accumulators in tensor memory): BF16, head_dim 64 or 128.
+//
+// A row tile is 128 rows (query, head of the group) of one (sequence, KV head), so
+// a K or V row serves the whole group and a tile's causal edge spans few positions.
+// A unit is two row tiles, A and B, that walk over the same 128-key tiles together:
+// while the softmax of one runs, the tensor core multiplies for the other.  One
+// persistent CTA per SM takes units from a common counter, long sequences' first and
+// within a sequence the ones with the most keys first, so that what is left for the
+// end is short.  With fewer units than SMs a unit is one row tile.
+// 10 warps:
+//  * warp 8, producer: takes units, loads Q tiles, and K and V tiles into one ring
+//    (K 0, V 0, K 1, ...) by TMA;
+//  * warp 9, one thread issues every MMA: S = Q K^T into the tile's 128 score columns,
+//    then O += P V with P (BF16) read from tensor memory over those columns.  Its turns
+//    alternate: P V of A's tile j and S of A's tile j + 1, the same for B, ...  MMAs
+//    complete in order, so "S j + 1 done" says that P V j is done too;
+//  * warps 0-3 and 4-7, softmax of A and of B: thread m owns row m.  The running
+//    maximum moves only when a score passes it by 8 (log2 units), which rescales O in
+//    tensor memory; otherwise O is not touched until it is written out.
+// Tensor memory: 2 x 128 score columns, 2 x head_dim output columns.
+// Shared memory: Q 2 x 32 KB, four ring stages of 32 KB, the units' plan.
+// Every wait is bounded: an expired one sets PKV_ERRBIT_TIMEOUT and ends the CTA, whose
+// copies and products have landed by then, without its outputs.
+#include <cuda.h>
+
+#include <climits>
+
+#include "quant_internal.h"
+#include "tc_common.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int kThreads = 320;
+constexpr int kRows = 128, kKeys = 128;
+constexpr int kHalf = 128 * 128;     // 64 columns of 128 rows
+constexpr int kStages = 4;
+constexpr int kSlots = 2;            // units in the queue
+constexpr int kSortSeqs = 256;       // up to so many sequences are taken longest first
+
+enum Bar {
+    kQFull = 0, kQFree = 2, kFull = 4, kFree = kFull + kStages, kSFull = kFree + kStages, kPFull = kSFull + 2,
+    kOFull = kPFull + 2, kOFree = kOFull + 2, kUFull = kOFree + 2, kUFree = kUFull + kSlots, kDone = kUFree + kSlots, kBars
+};
+
+struct Unit {
+    int q0;        // first query row (packed)
+    int n;         // queries from there to the end of the sequence
+    int k0, m;     // first key row, keys of the sequence
+    int head;      // KV head
+    int seen;      // keys that query q0 sees (may be negative)
+    int more;      // 0: no unit, the list is at its end
+    int pad;
+};
+
+template <int kDim>
+struct Layout {
+    static constexpr int kHalves = kDim / 64;
+    static constexpr int kTile = kHalves * kHalf;  // bytes of a Q, K or V tile
+    static constexpr int kQ = 0, kRing = 2 * kTile, kBar = kRing + kStages * kTile;
+    static constexpr int kQueue = kBar + 8 * kBars + 16, kMisc = kQueue + kSlots * static_cast<int>(sizeof(Unit));
+    static constexpr int kPlan = (kMisc + 64 + 127) / 128 * 128;
+    static constexpr int kSmem = kPlan + (kPromptMaxSeqs + 1) * 4 + kPromptMaxSeqs * 2 + 1024;
+    static_assert(kSmem <= 232448, "shared memory per CTA");
+};
+
+struct Span {
+    int q0, n, k0, m;
+};
+__device__ __forceinline__ Span span_of(const PromptArgs& a, int b, bool report) {
+    Span s{a.q_offsets[b], a.q_offsets[b + 1], a.k_offsets[b], a.k_offsets[b + 1]};
+    const bool ok = s.q0 >= 0 && s.n >= s.q0 && s.n <= a.q_rows && s.k0 >= 0 && s.m >= s.k0 && s.m <= a.k_rows;
+    if (!ok && report && a.err) atomicOr(a.err, PKV_ERRBIT_OFFSETS);
+    s.n = ok ? s.n - s.q0 : 0;
+    s.m = ok ? s.m - s.k0 : 0;
+    return s;
+}
+
+__device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* map, int half, int head, int row, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];\n" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(half), "r"(head), "r"(row), "r"(bar)
+        : "memory");
+}
+
+// What the roles agree on about a unit.
+struct Shape {
+    int tiles[2];  // key tiles of row tile A and of B
+    int nt;        // of the unit
+    __device__ Shape(const Unit& u, int qpt, int per_unit) {
+        for (int x = 0; x < 2; ++x) {
+            const int first = x * qpt;  // first query of the row tile
+            const int last = min(u.n, first + qpt) - 1;
+            const bool there = x < per_unit && first < u.n;
+            tiles[x] = there ? max(0, (u.seen + last + kKeys - 1) / kKeys) : 0;
+        }
+        nt = max(tiles[0], tiles[1]);
+    }
+};
+
+template <int kDim>
+__global__ void __launch_bounds__(kThreads, 1)
+prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                 const __grid_constant__ CUtensorMap mv, const PromptArgs a) {
+    using Lt = Layout<kDim>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = su32(smem);
+    auto B = [&](int i) { return sbase + Lt::kBar + 8u * i; };
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Lt::kBar + 8 * kBars);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lt::kBar + 8 * kBars + 4);
+    volatile Unit* queue = reinterpret_cast<volatile Unit*>(smem + Lt::kQueue);
+    int* misc = reinterpret_cast<int*>(smem + Lt::kMisc);  // {row tiles per unit}
+    int* cum = reinterpret_cast<int*>(smem + Lt::kPlan);   // [B + 1] units of one KV head before each sequence in order
+    uint16_t* order = reinterpret_cast<uint16_t*>(smem + Lt::kPlan + (kPromptMaxSeqs + 1) * 4);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int gh = a.num_q_heads / a.num_kv_heads, qpt = kRows / gh;  // queries of a row tile
+
+    if (tid == 0) {
+        for (int i = 0; i < kBars; ++i)
+            bar_init(B(i), (i >= kPFull && i < kPFull + 2) || (i >= kOFree && i < kOFree + 2) ? 4u
+                           : i >= kUFree && i < kDone ? 9u : 1u);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    }
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(su32(tmem_slot)), "r"(512)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
+    }
+    // the plan: sequences in order, and the row tiles before each
+    int* keys = cum + 1;  // (first the keys, for the order)
+    for (int b = tid; b < a.num_seqs; b += kThreads) keys[b] = span_of(a, b, blockIdx.x == 0).m;
+    __syncthreads();
+    for (int b = tid; b < a.num_seqs; b += kThreads) {
+        int rank = b;
+        if (a.num_seqs <= kSortSeqs) {
+            rank = 0;
+            for (int o = 0; o < a.num_seqs; ++o) rank += keys[o] > keys[b] || (keys[o] == keys[b] && o < b);
+        }
+        order[rank] = static_cast<uint16_t>(b);
+    }
+    __syncthreads();
+    if (warp == 0) {
+        for (int per = 2;; per = 1) {  // two row tiles a unit, unless that leaves SMs without one
+            int at = 0;
+            for (int r0 = 0; r0 < a.num_seqs; r0 += 32) {
+                int n = 0;
+                if (r0 + lane < a.num_seqs) n = (span_of(a, order[r0 + lane], false).n + per * qpt - 1) / (per * qpt);
+                int incl = n;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int x = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+                    if (lane >= d) incl += x;
+                }
+                if (r0 + lane < a.num_seqs) cum[r0 + lane + 1] = at + incl;
+                at += __shfl_sync(0xFFFFFFFFu, incl, 31);
+            }
+            if (lane == 0) cum[0] = 0, misc[0] = per;
+            if (per == 1 || static_cast<int64_t>(at) * a.num_kv_heads >= gridDim.x) break;
+        }
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int per_unit = misc[0];
+    auto fail = [&]() {
+        *abort_flag = 1;
+        if (a.err) atomicOr(a.err, PKV_ERRBIT_TIMEOUT);
+    };
+    // a bounded wait that ends early when another role has given up
+    auto wait = [&](int i, int parity) -> bool {
+        for (uint32_t k = 0; k < kSpin; ++k) {
+            uint32_t ok;
+            asm volatile(
+                "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+                : "=r"(ok)
+                : "r"(B(i)), "r"(parity)
+                : "memory");
+            if (ok) return true;
+            if ((k & 255) == 255 && *abort_flag) return false;
+        }
+        return false;
+    };
+    auto take = [&](int i) -> Unit {  // the i-th unit of this CTA, once it is in the queue
+        const volatile Unit& s = queue[i % kSlots];
+        return Unit{s.q0, s.n, s.k0, s.m, s.head, s.seen, s.more, 0};
+    };
+
+    if (warp == 8) {
+        // ------------------------------------------------------------ producer
+        bool ok = true;
+        int stage = 0, q_count[2] = {0, 0};  // tiles put into the ring, Q tiles loaded
+        const int total = cum[a.num_seqs] * a.num_kv_heads;
+        int next = lane == 0 ? atomicAdd(a.counters, 1) : 0;
+        for (int i = 0; ok; ++i) {
+            const int id = __shfl_sync(0xFFFFFFFFu, next, 0);
+            if (lane == 0 && id < total) next = atomicAdd(a.counters, 1);  // the one after, while this one runs
+            Unit u{};
+            if (id < total) {
+                int lo = 0, hi = a.num_seqs;  // the last place whose first unit is at or before id
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (static_cast<int64_t>(cum[mid]) * a.num_kv_heads <= id) lo = mid;
+                    else hi = mid;
+                }
+                const Span s = span_of(a, order[lo], false);
+                const int j = id - cum[lo] * a.num_kv_heads;
+                const int first = (cum[lo + 1] - cum[lo] - 1 - j / a.num_kv_heads) * per_unit * qpt;
+                u = Unit{s.q0 + first, s.n - first, s.k0, s.m, j % a.num_kv_heads, s.m - s.n + first + 1, 1, 0};
+            }
+            if (i >= kSlots) ok = wait(kUFree + i % kSlots, (i / kSlots - 1) & 1);
+            if (!ok) break;
+            if (lane == 0) {
+                volatile Unit& s = queue[i % kSlots];
+                s.q0 = u.q0, s.n = u.n, s.k0 = u.k0, s.m = u.m, s.head = u.head, s.seen = u.seen, s.more = u.more;
+                bar_arrive(B(kUFull + i % kSlots));
+            }
+            __syncwarp();
+            if (!u.more) break;
+            const Shape sh(u, qpt, per_unit);
+            auto load_q = [&](int x) {
+                if (sh.tiles[x] == 0) return;
+                if (q_count[x] > 0 && !wait(kQFree + x, (q_count[x] - 1) & 1)) {
+                    ok = false;
+                    return;
+                }
+                if (lane == 0) bar_expect_tx(B(kQFull + x), Lt::kHalves * qpt * gh * 128);
+                __syncwarp();
+                if (lane < Lt::kHalves)
+                    tma_4d(sbase + Lt::kQ + x * Lt::kTile + lane * kHalf, &mq, lane, u.head * gh, u.q0 + x * qpt, B(kQFull + x));
+                ++q_count[x];
+            };
+            auto load_kv = [&](const CUtensorMap* map, int j) {
+                const int s = stage % kStages;
+                if (stage >= kStages && !wait(kFree + s, (stage / kStages - 1) & 1)) {
+                    ok = false;
+                    return;
+                }
+                if (lane == 0) bar_expect_tx(B(kFull + s), Lt::kTile);
+                __syncwarp();
+                if (lane < Lt::kHalves)
+                    tma_4d(sbase + Lt::kRing + s * Lt::kTile + lane * kHalf, map, lane, u.head, u.k0 + j * kKeys, B(kFull + s));
+                ++stage;
+            };
+            if (sh.nt > 0) load_q(0);
+            for (int j = 0; j < sh.nt && ok; ++j) {
+                load_kv(&mk, j);
+                if (j == 0 && ok) load_q(1);
+                if (ok) load_kv(&mv, j);
+            }
+        }
+        if (!ok && lane == 0) fail();
+        // the copies under way land before the CTA ends
+        for (int k = stage - 1; k >= 0 && k >= stage - kStages; --k) bar_wait(B(kFull + k % kStages), (k / kStages) & 1);
+        for (int x = 0; x < 2; ++x)
+            if (q_count[x] > 0) bar_wait(B(kQFull + x), (q_count[x] - 1) & 1);
+        // the last CTA to finish leaves the counters at zero
+        if (lane == 0) {
+            __threadfence();
+            if (atomicAdd(a.counters + 1, 1) == static_cast<int>(gridDim.x) - 1) {
+                a.counters[0] = 0;
+                a.counters[1] = 0;
+            }
+        }
+    } else if (warp == 9) {
+        // ---------------------------------------------------------- MMA issuer
+        if (lane == 0) {
+            bool ok = true;
+            const uint64_t dq = sdesc(sbase + Lt::kQ, 16), dk = sdesc(sbase + Lt::kRing, 16);
+            const uint64_t dv = sdesc(sbase + Lt::kRing, kHalf);
+            int q_count[2] = {0, 0}, s_count[2] = {0, 0}, o_count[2] = {0, 0};  // units, tiles and outputs of A and B
+            int base = 0, base_next = 0;  // ring place of the unit's first tile, and of the next unit's
+            auto unit = [&](int i, Unit& u) -> bool {
+                if (!wait(kUFull + i % kSlots, (i / kSlots) & 1)) return false;
+                u = take(i);
+                bar_arrive(B(kUFree + i % kSlots));
+                return true;
+            };
+            auto scores = [&](int x, int j, const Shape& sh, int at) -> bool {  // S of row tile x, key tile j
+                if (j == 0 && !wait(kQFull + x, q_count[x]++ & 1)) return false;
+                const int place = at + 2 * j, s = place % kStages;
+                if (!wait(kFull + s, (place / kStages) & 1)) return false;
+                fence_after();
+                const uint64_t q = dq + static_cast<uint64_t>((x * Lt::kTile) >> 4);
+                const uint64_t k = dk + static_cast<uint64_t>((s * Lt::kTile) >> 4);
+#pragma unroll
+                for (int ks = 0; ks < kDim / 16; ++ks) {
+                    const uint32_t off = ((ks >> 2) * kHalf + (ks & 3) * 32) >> 4;
+                    mma_bf16(tmem + x * kKeys, q + off, k + off, idesc(kKeys, 0), ks > 0 ? 1u : 0u);
+                }
+                mma_commit(B(kSFull + x));
+                if (j == sh.tiles[x] - 1) mma_commit(B(kQFree + x));
+                if (x == 1 || sh.tiles[1] <= j) mma_commit(B(kFree + s));  // its last reader
+                return true;
+            };
+            auto values = [&](int x, int j, const Shape& sh, int at) -> bool {  // P V
+                if (!wait(kPFull + x, s_count[x]++ & 1)) return false;
+                const int place = at + 2 * j + 1, s = place % kStages;
+                if (!wait(kFull + s, (place / kStages) & 1)) return false;
+                if (j == 0 && o_count[x] > 0 && !wait(kOFree + x, (o_count[x] - 1) & 1)) return false;
+                fence_after();
+                const uint64_t v = dv + static_cast<uint64_t>((s * Lt::kTile) >> 4);
+#pragma unroll
+                for (int ks = 0; ks < kKeys / 16; ++ks)
+                    mma_bf16_ta(tmem + 2 * kKeys + x * kDim, tmem + x * kKeys + 8 * ks, v + ((ks * 16 * 128) >> 4),
+                                idesc(kDim, 1), (j > 0 || ks > 0) ? 1u : 0u);
+                if (j == sh.tiles[x] - 1) {
+                    mma_commit(B(kOFull + x));
+                    ++o_count[x];
+                }
+                if (x == 1 || sh.tiles[1] <= j) mma_commit(B(kFree + s));
+                return true;
+            };
+            int i = 0;
+            Unit u{}, un{};
+            auto next_unit = [&]() -> bool {  // the next one that has tiles
+                do {
+                    if (!unit(i, un)) return false;
+                    ++i;
+                } while (un.more && Shape(un, qpt, per_unit).nt == 0);
+                return true;
+            };
+            ok = next_unit();
+            if (ok && un.more) {
+                const Shape sh(un, qpt, per_unit);
+                for (int x = 0; x < 2 && ok; ++x)
+                    if (sh.tiles[x] > 0) ok = scores(x, 0, sh, 0);
+                base_next = 2 * sh.nt;
+            }
+            while (ok && un.more) {
+                u = un;
+                const Shape sh(u, qpt, per_unit);
+                const int at = base;
+                base = base_next;
+                for (int j = 0; j < sh.nt && ok; ++j) {
+                    const bool end = j == sh.nt - 1;
+                    if (end && !(ok = next_unit())) break;
+                    const Shape shn(un, qpt, per_unit);
+                    for (int x = 0; x < 2 && ok; ++x) {
+                        if (j < sh.tiles[x]) ok = values(x, j, sh, at);
+                        if (ok && j + 1 < sh.tiles[x]) ok = scores(x, j + 1, sh, at);
+                        if (ok && end && un.more && shn.tiles[x] > 0) ok = scores(x, 0, shn, base);
+                    }
+                    if (end) base_next = base + 2 * shn.nt;
+                }
+            }
+            if (!ok) fail();
+            mma_commit(B(kDone));  // every product, and every signal of one, has landed before the CTA ends
+            if (!bar_wait(B(kDone), 0)) fail();
+        }
+        __syncwarp();
+    } else {
+        // -------------------------------------------------- softmax and output
+        const int x = warp >> 2, m = tid & 127;  // row tile, row
+        const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+        const uint32_t ts = tmem + lane_off + x * kKeys, to = tmem + lane_off + 2 * kKeys + x * kDim;
+        const float qk = a.scale_log2;
+        const int qi = m / gh, hi = m % gh;  // query of the tile, head of the group
+        int s_count = 0, o_count = 0, base = 0;
+        bool ok = true;
+        for (int i = 0; ok; ++i) {
+            if (!__all_sync(0xFFFFFFFFu, wait(kUFull + i % kSlots, (i / kSlots) & 1))) {
+                ok = false;
+                break;
+            }
+            const Unit u = take(i);
+            __syncwarp();
+            if (lane == 0) bar_arrive(B(kUFree + i % kSlots));
+            if (!u.more) break;
+            const Shape sh(u, qpt, per_unit);
+            const int place0 = base;
+            base += 2 * sh.nt;
+            const int query = x * qpt + qi;
+            const bool valid = x < per_unit && qi < qpt && query < u.n;
+            const bool busy = __any_sync(0xFFFFFFFFu, valid);
+            const int lim = valid ? u.seen + query : INT_MAX;  // keys that the row sees
+            const int tiles = sh.tiles[x];
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
+                                 (static_cast<int64_t>(u.q0 + query) * a.num_q_heads + u.head * gh + hi) * kDim;
+            float m_used = -INFINITY, l = 0.f;
+            for (int j = 0; j < tiles; ++j) {
+                if (!__all_sync(0xFFFFFFFFu, wait(kSFull + x, s_count & 1))) {
+                    ok = false;
+                    break;
+                }
+                ++s_count;
+                fence_after();
+                const int key0 = j * kKeys;
+                if (busy) {
+                    const bool full = __all_sync(0xFFFFFFFFu, key0 + kKeys <= lim);
+                    uint32_t v[kKeys];
+#pragma unroll
+                    for (int c = 0; c < kKeys / 32; ++c) tmem_ld32_nowait(ts + 32 * c, v + 32 * c);
+                    asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
+                    float mx = -INFINITY;
+                    if (full && qk > 0.f) {
+                        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                        for (int k = 0; k < kKeys; k += 2)
+                            m4[(k >> 1) & 3] = max3(m4[(k >> 1) & 3], __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+                        mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * qk;
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < kKeys; ++k)
+                            if (key0 + k < lim) mx = fmaxf(mx, __uint_as_float(v[k]) * qk);
+                    }
+                    const float m_new = fmaxf(m_used, mx);
+                    const bool rescale = m_used != -INFINITY && m_new > m_used + 8.f;
+                    const float alpha = rescale ? ex2(m_used - m_new) : 1.f;
+                    if (m_used == -INFINITY || rescale) m_used = m_new;
+                    const float base2 = m_used == -INFINITY ? 0.f : m_used;
+                    if (__any_sync(0xFFFFFFFFu, rescale)) {  // ("S j done": P V j - 1 is, too)
+#pragma unroll 1
+                        for (int c = 0; c < kDim / 32; ++c) {
+                            uint32_t o[32];
+                            tmem_ld32(to + 32 * c, o);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                            tmem_st32(to + 32 * c, o);
+                        }
+                        l *= alpha;
+                    }
+                    float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        uint32_t p[32];
+                        if (full) {
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) {
+                                float x0, x1;
+                                fma2(x0, x1, __uint_as_float(v[64 * hf + 2 * k]), __uint_as_float(v[64 * hf + 2 * k + 1]), qk,
+                                     qk, -base2, -base2);
+                                const float p0 = ex2(x0), p1 = ex2(x1);
+                                add2(l0, l1, l0, l1, p0, p1);
+                                p[k] = bf16x2(p0, p1);
+                            }
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) {
+                                const int t = key0 + 64 * hf + 2 * k;
+                                const float p0 = t < lim ? ex2(fmaf(__uint_as_float(v[64 * hf + 2 * k]), qk, -base2)) : 0.f;
+                                const float p1 =
+                                    t + 1 < lim ? ex2(fmaf(__uint_as_float(v[64 * hf + 2 * k + 1]), qk, -base2)) : 0.f;
+                                l0 += p0;
+                                l1 += p1;
+                                p[k] = bf16x2(p0, p1);
+                            }
+                        }
+                        tmem_st32(ts + 32 * hf, p);
+                    }
+                    l += l0 + l1;
+                }
+                // V rows behind the sequence: zero (they are another's, or unwritten, and may hold NaN).  The
+                // first row tile that multiplies this key tile sees to it, before its P is ready
+                const int there = u.m - key0;
+                if (there < kKeys && (x == 0 || sh.tiles[0] <= j)) {
+                    const int place = place0 + 2 * j + 1, s = place % kStages;
+                    if (!__all_sync(0xFFFFFFFFu, wait(kFull + s, (place / kStages) & 1))) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t* vs = smem + Lt::kRing + s * Lt::kTile;
+                    const int gone = kKeys - there;  // whole 128-byte rows: the swizzle does not matter
+                    for (int e = m; e < Lt::kHalves * gone * 8; e += 128) {
+                        const int h = e / (gone * 8), r = there + e % (gone * 8) / 8;
+                        *reinterpret_cast<uint4*>(vs + h * kHalf + r * 128 + e % 8 * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    fence_async_smem();
+                }
+                fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(B(kPFull + x));
+            }
+            if (!ok) break;
+            if (tiles == 0) {  // no key is seen
+                if (valid)
+                    for (int k = 0; k < kDim / 8; ++k) reinterpret_cast<uint4*>(out)[k] = make_uint4(0u, 0u, 0u, 0u);
+                continue;
+            }
+            if (!__all_sync(0xFFFFFFFFu, wait(kOFull + x, o_count & 1))) {
+                ok = false;
+                break;
+            }
+            ++o_count;
+            fence_after();
+            uint32_t o[kDim];
+#pragma unroll
+            for (int c = 0; c < kDim / 32; ++c) tmem_ld32_nowait(to + 32 * c, o + 32 * c);
+            asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
+            fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(B(kOFree + x));  // the next unit's first P V may overwrite it
+            if (valid) {
+                const float inv = 1.f / l;
+#pragma unroll
+                for (int k = 0; k < kDim / 8; ++k) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        w[e] = lim > 0 ? bf16x2(__uint_as_float(o[8 * k + 2 * e]) * inv, __uint_as_float(o[8 * k + 2 * e + 1]) * inv)
+                                       : 0u;
+                    reinterpret_cast<uint4*>(out)[k] = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+        }
+        if (!ok && lane == 0) fail();
+    }
+    fence_before();  // every role has left its waits
+    __syncthreads();
+    fence_after();
+    if (warp == 0)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(512) : "memory");
+}
+
+// Descriptor of packed rows [rows][heads][kDim] as {64 columns, column halves, heads, rows}.
+bool encode_rows(CUtensorMap* map, const void* base, int dim, int64_t rows, int heads, int64_t stride, int box_heads,
+                 int box_rows) {
+    const uint64_t dims[4] = {64, static_cast<uint64_t>(dim / 64), static_cast<uint64_t>(heads), static_cast<uint64_t>(rows)};
+    const uint64_t row = rows > 1 ? static_cast<uint64_t>(stride) : static_cast<uint64_t>(heads) * dim;
+    const uint64_t strides[3] = {128, static_cast<uint64_t>(dim) * 2, row * 2};
+    const uint32_t box[4] = {64, 1, static_cast<uint32_t>(box_heads), static_cast<uint32_t>(box_rows)};
+    return encode_map(map, 2, 4, base, dims, strides, box);
+}
+
+template <int kDim>
+cudaError_t launch(const PromptArgs& a, cudaStream_t stream) {
+    const int gh = a.num_q_heads / a.num_kv_heads, qpt = kRows / gh;
+    CUtensorMap mq, mk, mv;
+    if (!encode_rows(&mq, a.q, kDim, a.q_rows, a.num_q_heads, a.q_stride, gh, qpt) ||
+        !encode_rows(&mk, a.k, kDim, a.k_rows, a.num_kv_heads, a.k_stride, 1, kKeys) ||
+        !encode_rows(&mv, a.v, kDim, a.k_rows, a.num_kv_heads, a.v_stride, 1, kKeys))
+        return cudaErrorNotSupported;
+    const cudaError_t e = cudaFuncSetAttribute(prompt_tc_kernel<kDim>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               Layout<kDim>::kSmem);
+    if (e != cudaSuccess) return e;
+    const int64_t most = (static_cast<int64_t>(a.q_rows) / qpt + a.num_seqs) * a.num_kv_heads;  // row tiles
+    const int sms = num_sms() > 0 ? num_sms() : 148;
+    prompt_tc_kernel<kDim><<<static_cast<unsigned>(most < sms ? most : sms), kThreads, Layout<kDim>::kSmem, stream>>>(mq, mk, mv, a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+bool prompt_tc_fits(pkv_dtype t, int num_seqs, int q_rows, int num_q_heads, int num_kv_heads) {
+    const int gh = num_q_heads / num_kv_heads;
+    // (units are counted in 32 bits)
+    return t == PKV_BF16 && gh <= kRows && num_seqs <= kPromptMaxSeqs &&
+           (static_cast<int64_t>(q_rows) + num_seqs) * num_kv_heads <= INT32_MAX / 2;
+}
+
+cudaError_t launch_prompt_tc(int head_dim, const PromptArgs& a, cudaStream_t stream) {
+    return head_dim == 64 ? launch<64>(a, stream) : launch<128>(a, stream);
+}
+
+}  // namespace pkv

@@ -115,19 +115,19 @@ def test_rows_of_no_sequence(inp):
 
 @pytest.mark.parametrize("inp", ["bf16", "f32"])
 def test_values_that_are_not_finite_stay_with_their_sequence(inp):
-    """A key that is not finite is seen only behind its place; a value reaches at most 127 positions more."""
+    """A key that is not finite is seen only behind its place; a value reaches at most 255 positions more."""
     lens = (300, 300, 300)
     cpu, gpu = case(lens, lens, 4, 2, 128, inp, fused=False, seed=6)
     o = dev(offsets(lens))
     want = pk.prompt_attention(*gpu, o, o, 0.1)
     gpu[1][300 + 200, 0, 5] = float("nan")
-    gpu[2][300 + 250, 1, 7] = float("inf")
+    gpu[2][300 + 290, 1, 7] = float("inf")
     got = pk.prompt_attention(*gpu, o, o, 0.1)
     assert torch.equal(got[:300], want[:300]) and torch.equal(got[600:], want[600:])
     assert torch.equal(got[300:500, :2], want[300:500, :2])      # before the key, its heads
     assert got[500:600, :2].isnan().all()
-    assert torch.equal(got[300:300 + 250 - 127, 2:], want[300:300 + 250 - 127, 2:])
-    assert not got[550:600, 2:, 7].isfinite().any()
+    assert torch.equal(got[300:300 + 290 - 255, 2:], want[300:300 + 290 - 255, 2:])
+    assert not got[590:600, 2:, 7].isfinite().any()
 
 
 @pytest.mark.parametrize("inp", ["bf16", "f32"])
