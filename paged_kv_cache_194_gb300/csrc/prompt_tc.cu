@@ -11,10 +11,11 @@
 // 10 warps:
 //  * warp 8, producer: takes units, loads Q tiles, and K and V tiles into one ring
 //    (K 0, V 0, K 1, ...) by TMA;
-//  * warp 9, one thread issues every MMA: S = Q K^T into the tile's 128 score columns,
-//    then O += P V with P (BF16) read from tensor memory over those columns.  Its turns
-//    alternate: P V of A's tile j and S of A's tile j + 1, the same for B, ...  MMAs
-//    complete in order, so "S j + 1 done" says that P V j is done too;
+//  * warps 9 and 10, one thread each issues the MMAs of A and of B: S = Q K^T into the
+//    row tile's 128 score columns, then O += P V with P (BF16) read from tensor memory
+//    over those columns, then S of the next key tile.  One thread's MMAs complete in
+//    order, so "S j + 1 done" says that P V j is done too.  (One issuer for both spent
+//    4200 of 4500 cycles per pair of tiles on its own instructions);
 //  * warps 0-3 and 4-7, softmax of A and of B: thread m owns row m.  The running
 //    maximum moves only when a score passes it by 8 (log2 units), which rescales O in
 //    tensor memory; otherwise O is not touched until it is written out.
@@ -32,7 +33,7 @@
 namespace pkv {
 namespace {
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;
 constexpr int kRows = 128, kKeys = 128;
 constexpr int kHalf = 128 * 128;     // 64 columns of 128 rows
 constexpr int kStages = 4;
@@ -41,7 +42,8 @@ constexpr int kSortSeqs = 256;       // up to so many sequences are taken longes
 
 enum Bar {
     kQFull = 0, kQFree = 2, kFull = 4, kFree = kFull + kStages, kSFull = kFree + kStages, kPFull = kSFull + 2,
-    kOFull = kPFull + 2, kOFree = kOFull + 2, kUFull = kOFree + 2, kUFree = kUFull + kSlots, kDone = kUFree + kSlots, kBars
+    kOFull = kPFull + 4, kOFree = kOFull + 2, kUFull = kOFree + 2, kUFree = kUFull + kSlots, kDone = kUFree + kSlots,
+    kBars = kDone + 2
 };
 
 struct Unit {
@@ -119,8 +121,9 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
 
     if (tid == 0) {
         for (int i = 0; i < kBars; ++i)
-            bar_init(B(i), (i >= kPFull && i < kPFull + 2) || (i >= kOFree && i < kOFree + 2) ? 4u
-                           : i >= kUFree && i < kDone ? 9u : 1u);
+            bar_init(B(i), (i >= kPFull && i < kPFull + 4) || (i >= kOFree && i < kOFree + 2) ? 4u
+                           : i >= kUFree && i < kDone ? 10u
+                           : i >= kFree && i < kFree + kStages ? 2u : 1u);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
@@ -265,94 +268,92 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                 a.counters[1] = 0;
             }
         }
-    } else if (warp == 9) {
-        // ---------------------------------------------------------- MMA issuer
+    } else if (warp == 9 || warp == 10) {
+        // ------------------------------------------- MMA issuers: A's and B's
         if (lane == 0) {
+            const int x = warp - 9;
+            const uint32_t ts = tmem + x * kKeys, to = tmem + 2 * kKeys + x * kDim;
+            const uint64_t dq = sdesc(sbase + Lt::kQ + x * Lt::kTile, 16), dk = sdesc(sbase + Lt::kRing, 16);
+            const uint64_t dv = sdesc(sbase + Lt::kRing + Lt::kTile, kHalf);
+            constexpr uint64_t kPair = (2 * Lt::kTile) >> 4;  // from a K (V) stage to the next
+            int units = 0, q_count = 0, p_count = 0, o_count = 0;
+            int c = 0, j = 0, tiles = 0, nt = 0;  // key tile of all, of the unit; the row tile's, the unit's
             bool ok = true;
-            const uint64_t dq = sdesc(sbase + Lt::kQ, 16), dk = sdesc(sbase + Lt::kRing, 16);
-            const uint64_t dv = sdesc(sbase + Lt::kRing, kHalf);
-            int q_count[2] = {0, 0}, s_count[2] = {0, 0}, o_count[2] = {0, 0};  // units, tiles and outputs of A and B
-            int base = 0, base_next = 0;  // ring place of the unit's first tile, and of the next unit's
-            auto unit = [&](int i, Unit& u) -> bool {
-                if (!wait(kUFull + i % kSlots, (i / kSlots) & 1)) return false;
-                u = take(i);
-                bar_arrive(B(kUFree + i % kSlots));
-                return true;
+            // the next key tile of this row tile: 1, 0 at the list's end, -1 on failure
+            auto advance = [&]() -> int {
+                for (;;) {
+                    if (++j < tiles) {
+                        ++c;
+                        return 1;
+                    }
+                    for (; j < nt; ++j) {  // tiles that only the other row tile multiplies
+                        ++c;
+                        const int st = 2 * (c & 1), ph = (c >> 1) & 1;
+                        for (int v = 0; v < 2; ++v) {
+                            if (!wait(kFull + st + v, ph)) return -1;
+                            bar_arrive(B(kFree + st + v));
+                        }
+                    }
+                    if (!wait(kUFull + units % kSlots, (units / kSlots) & 1)) return -1;
+                    const Unit u = take(units);
+                    bar_arrive(B(kUFree + units % kSlots));
+                    ++units;
+                    if (!u.more) return 0;
+                    const Shape sh(u, qpt, per_unit);
+                    tiles = sh.tiles[x], nt = sh.nt, j = -1;
+                }
             };
-            auto scores = [&](int x, int j, const Shape& sh, int at) -> bool {  // S of row tile x, key tile j
-                if (j == 0 && !wait(kQFull + x, q_count[x]++ & 1)) return false;
-                const int place = at + 2 * j, s = place % kStages;
-                if (!wait(kFull + s, (place / kStages) & 1)) return false;
+            auto scores = [&]() -> bool {
+                const int st = 2 * (c & 1);
+                if (j == 0 && !wait(kQFull + x, q_count++ & 1)) return false;
+                if (!wait(kFull + st, (c >> 1) & 1)) return false;
                 fence_after();
-                const uint64_t q = dq + static_cast<uint64_t>((x * Lt::kTile) >> 4);
-                const uint64_t k = dk + static_cast<uint64_t>((s * Lt::kTile) >> 4);
+                const uint64_t k = dk + (c & 1) * kPair;
 #pragma unroll
                 for (int ks = 0; ks < kDim / 16; ++ks) {
                     const uint32_t off = ((ks >> 2) * kHalf + (ks & 3) * 32) >> 4;
-                    mma_bf16(tmem + x * kKeys, q + off, k + off, idesc(kKeys, 0), ks > 0 ? 1u : 0u);
+                    mma_bf16(ts, dq + off, k + off, idesc(kKeys, 0), ks > 0 ? 1u : 0u);
                 }
                 mma_commit(B(kSFull + x));
-                if (j == sh.tiles[x] - 1) mma_commit(B(kQFree + x));
-                if (x == 1 || sh.tiles[1] <= j) mma_commit(B(kFree + s));  // its last reader
+                mma_commit(B(kFree + st));
+                if (j == tiles - 1) mma_commit(B(kQFree + x));
                 return true;
             };
-            auto values = [&](int x, int j, const Shape& sh, int at) -> bool {  // P V
-                if (!wait(kPFull + x, s_count[x]++ & 1)) return false;
-                const int place = at + 2 * j + 1, s = place % kStages;
-                if (!wait(kFull + s, (place / kStages) & 1)) return false;
-                if (j == 0 && o_count[x] > 0 && !wait(kOFree + x, (o_count[x] - 1) & 1)) return false;
-                fence_after();
-                const uint64_t v = dv + static_cast<uint64_t>((s * Lt::kTile) >> 4);
+            auto values = [&]() -> bool {  // P V, the first 64 keys while P of the others is computed
+                const int st = 2 * (c & 1) + 1;
+                const uint64_t v = dv + (c & 1) * kPair;
+                if (!wait(kFull + st, (c >> 1) & 1)) return false;
+                if (j == 0 && o_count > 0 && !wait(kOFree + x, (o_count - 1) & 1)) return false;
 #pragma unroll
-                for (int ks = 0; ks < kKeys / 16; ++ks)
-                    mma_bf16_ta(tmem + 2 * kKeys + x * kDim, tmem + x * kKeys + 8 * ks, v + ((ks * 16 * 128) >> 4),
-                                idesc(kDim, 1), (j > 0 || ks > 0) ? 1u : 0u);
-                if (j == sh.tiles[x] - 1) {
+                for (int hf = 0; hf < 2; ++hf) {
+                    if (!wait(kPFull + 2 * x + hf, p_count & 1)) return false;
+                    fence_after();
+#pragma unroll
+                    for (int ks = 4 * hf; ks < 4 * hf + 4; ++ks)
+                        mma_bf16_ta(to, ts + 8 * ks, v + ((ks * 16 * 128) >> 4), idesc(kDim, 1), (j > 0 || ks > 0) ? 1u : 0u);
+                }
+                ++p_count;
+                if (j == tiles - 1) {
                     mma_commit(B(kOFull + x));
-                    ++o_count[x];
+                    ++o_count;
                 }
-                if (x == 1 || sh.tiles[1] <= j) mma_commit(B(kFree + s));
+                mma_commit(B(kFree + st));
                 return true;
             };
-            int i = 0;
-            Unit u{}, un{};
-            auto next_unit = [&]() -> bool {  // the next one that has tiles
-                do {
-                    if (!unit(i, un)) return false;
-                    ++i;
-                } while (un.more && Shape(un, qpt, per_unit).nt == 0);
-                return true;
-            };
-            ok = next_unit();
-            if (ok && un.more) {
-                const Shape sh(un, qpt, per_unit);
-                for (int x = 0; x < 2 && ok; ++x)
-                    if (sh.tiles[x] > 0) ok = scores(x, 0, sh, 0);
-                base_next = 2 * sh.nt;
+            c = -1, j = -1;
+            int more = advance();
+            if (more > 0) ok = scores();
+            while (ok && more > 0) {
+                ok = values();
+                if (ok) more = advance();
+                if (ok && more > 0) ok = scores();
             }
-            while (ok && un.more) {
-                u = un;
-                const Shape sh(u, qpt, per_unit);
-                const int at = base;
-                base = base_next;
-                for (int j = 0; j < sh.nt && ok; ++j) {
-                    const bool end = j == sh.nt - 1;
-                    if (end && !(ok = next_unit())) break;
-                    const Shape shn(un, qpt, per_unit);
-                    for (int x = 0; x < 2 && ok; ++x) {
-                        if (j < sh.tiles[x]) ok = values(x, j, sh, at);
-                        if (ok && j + 1 < sh.tiles[x]) ok = scores(x, j + 1, sh, at);
-                        if (ok && end && un.more && shn.tiles[x] > 0) ok = scores(x, 0, shn, base);
-                    }
-                    if (end) base_next = base + 2 * shn.nt;
-                }
-            }
-            if (!ok) fail();
-            mma_commit(B(kDone));  // every product, and every signal of one, has landed before the CTA ends
-            if (!bar_wait(B(kDone), 0)) fail();
+            if (!ok || more < 0) fail();
+            mma_commit(B(kDone + x));  // every product, and every signal of one, has landed before the CTA ends
+            if (!bar_wait(B(kDone + x), 0)) fail();
         }
         __syncwarp();
-    } else {
+    } else if (warp < 8) {
         // -------------------------------------------------- softmax and output
         const int x = warp >> 2, m = tid & 127;  // row tile, row
         const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
@@ -371,8 +372,8 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             if (lane == 0) bar_arrive(B(kUFree + i % kSlots));
             if (!u.more) break;
             const Shape sh(u, qpt, per_unit);
-            const int place0 = base;
-            base += 2 * sh.nt;
+            const int place0 = base;  // key tiles of the units before
+            base += sh.nt;
             const int query = x * qpt + qi;
             const bool valid = x < per_unit && qi < qpt && query < u.n;
             const bool busy = __any_sync(0xFFFFFFFFu, valid);
@@ -389,6 +390,28 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                 ++s_count;
                 fence_after();
                 const int key0 = j * kKeys;
+                // V rows behind the sequence: zero (they are another's, or unwritten, and may hold NaN), before
+                // any P of this tile is ready; A and B both see to it
+                const int there = u.m - key0;
+                if (there < kKeys) {
+                    const int c = place0 + j, s = 2 * (c & 1) + 1;
+                    if (!__all_sync(0xFFFFFFFFu, wait(kFull + s, (c >> 1) & 1))) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t* vs = smem + Lt::kRing + s * Lt::kTile;
+                    const int gone = kKeys - there;  // whole 128-byte rows: the swizzle does not matter
+                    for (int e = m; e < Lt::kHalves * gone * 8; e += 128) {
+                        const int h = e / (gone * 8), r = there + e % (gone * 8) / 8;
+                        *reinterpret_cast<uint4*>(vs + h * kHalf + r * 128 + e % 8 * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    fence_async_smem();
+                }
+                auto ready = [&](int hf) {  // P of 64 keys is in tensor memory
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(B(kPFull + 2 * x + hf));
+                };
                 if (busy) {
                     const bool full = __all_sync(0xFFFFFFFFu, key0 + kKeys <= lim);
                     uint32_t v[kKeys];
@@ -450,29 +473,13 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                             }
                         }
                         tmem_st32(ts + 32 * hf, p);
+                        ready(hf);
                     }
                     l += l0 + l1;
+                } else {
+                    ready(0);
+                    ready(1);
                 }
-                // V rows behind the sequence: zero (they are another's, or unwritten, and may hold NaN).  The
-                // first row tile that multiplies this key tile sees to it, before its P is ready
-                const int there = u.m - key0;
-                if (there < kKeys && (x == 0 || sh.tiles[0] <= j)) {
-                    const int place = place0 + 2 * j + 1, s = place % kStages;
-                    if (!__all_sync(0xFFFFFFFFu, wait(kFull + s, (place / kStages) & 1))) {
-                        ok = false;
-                        break;
-                    }
-                    uint8_t* vs = smem + Lt::kRing + s * Lt::kTile;
-                    const int gone = kKeys - there;  // whole 128-byte rows: the swizzle does not matter
-                    for (int e = m; e < Lt::kHalves * gone * 8; e += 128) {
-                        const int h = e / (gone * 8), r = there + e % (gone * 8) / 8;
-                        *reinterpret_cast<uint4*>(vs + h * kHalf + r * 128 + e % 8 * 16) = make_uint4(0u, 0u, 0u, 0u);
-                    }
-                    fence_async_smem();
-                }
-                fence_before();
-                __syncwarp();
-                if (lane == 0) bar_arrive(B(kPFull + x));
             }
             if (!ok) break;
             if (tiles == 0) {  // no key is seen
