@@ -8,15 +8,16 @@
 // persistent CTA per SM takes units from a common counter, long sequences' first and
 // within a sequence the ones with the most keys first, so that what is left for the
 // end is short.  With fewer units than SMs a unit is one row tile.
-// 10 warps:
-//  * warp 8, producer: takes units, loads Q tiles, and K and V tiles into one ring
+// 20 warps (the last one idle):
+//  * warp 16, producer: takes units, loads Q tiles, and K and V tiles into one ring
 //    (K 0, V 0, K 1, ...) by TMA;
-//  * warps 9 and 10, one thread each issues the MMAs of A and of B: S = Q K^T into the
+//  * warps 17 and 18, one thread each issues the MMAs of A and of B: S = Q K^T into the
 //    row tile's 128 score columns, then O += P V with P (BF16) read from tensor memory
 //    over those columns, then S of the next key tile.  One thread's MMAs complete in
 //    order, so "S j + 1 done" says that P V j is done too.  (One issuer for both spent
 //    4200 of 4500 cycles per pair of tiles on its own instructions);
-//  * warps 0-3 and 4-7, softmax of A and of B: thread m owns row m.  The running
+//  * warps 0-7 and 8-15, softmax of A and of B: two threads own a row, one its first 64
+//    keys of a tile and half of its output columns, the other the rest.  The running
 //    maximum moves only when a score passes it by 8 (log2 units), which rescales O in
 //    tensor memory; otherwise O is not touched until it is written out.
 // Tensor memory: 2 x 128 score columns, 2 x head_dim output columns.
@@ -33,7 +34,9 @@
 namespace pkv {
 namespace {
 
-constexpr int kThreads = 384;
+constexpr int kSoftmaxWarps = 16;     // eight for each row tile, two threads a row
+constexpr int kProducer = 16, kIssuer = 17;  // warps (two issuers)
+constexpr int kThreads = 640;
 constexpr int kRows = 128, kKeys = 128;
 constexpr int kHalf = 128 * 128;     // 64 columns of 128 rows
 constexpr int kStages = 4;
@@ -42,7 +45,7 @@ constexpr int kSortSeqs = 256;       // up to so many sequences are taken longes
 
 enum Bar {
     kQFull = 0, kQFree = 2, kFull = 4, kFree = kFull + kStages, kSFull = kFree + kStages, kPFull = kSFull + 2,
-    kOFull = kPFull + 4, kOFree = kOFull + 2, kUFull = kOFree + 2, kUFree = kUFull + kSlots, kDone = kUFree + kSlots,
+    kOFull = kPFull + 2, kOFree = kOFull + 2, kUFull = kOFree + 2, kUFree = kUFull + kSlots, kDone = kUFree + kSlots,
     kBars = kDone + 2
 };
 
@@ -62,7 +65,8 @@ struct Layout {
     static constexpr int kTile = kHalves * kHalf;  // bytes of a Q, K or V tile
     static constexpr int kQ = 0, kRing = 2 * kTile, kBar = kRing + kStages * kTile;
     static constexpr int kQueue = kBar + 8 * kBars + 16, kMisc = kQueue + kSlots * static_cast<int>(sizeof(Unit));
-    static constexpr int kPlan = (kMisc + 64 + 127) / 128 * 128;
+    static constexpr int kSay = (kMisc + 64 + 127) / 128 * 128;  // what a row's two threads tell each other
+    static constexpr int kPlan = kSay + 2 * 4 * kRows * 8;
     static constexpr int kSmem = kPlan + (kPromptMaxSeqs + 1) * 4 + kPromptMaxSeqs * 2 + 1024;
     static_assert(kSmem <= 232448, "shared memory per CTA");
 };
@@ -83,6 +87,28 @@ __device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* map, int
     asm volatile(
         "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];\n" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(half), "r"(head), "r"(row), "r"(bar)
+        : "memory");
+}
+
+// Eight columns of this thread's lane times f.  (Few registers: a row's scores are live around it.)
+__device__ __forceinline__ void tmem_scale8(uint32_t at, float f) {
+    uint32_t v[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "r"(at));
+    asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * f);
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(at), "r"(v[0]), "r"(v[1]),
+                 "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+// 16 columns of this thread's lane.
+__device__ __forceinline__ void tmem_st16_nowait(uint32_t at, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(at),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
 }
 
@@ -112,6 +138,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     auto B = [&](int i) { return sbase + Lt::kBar + 8u * i; };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Lt::kBar + 8 * kBars);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lt::kBar + 8 * kBars + 4);
+    int* turn = reinterpret_cast<int*>(smem + Lt::kBar + 8 * kBars + 8);  // 1 while an issuer has the tensor core
     volatile Unit* queue = reinterpret_cast<volatile Unit*>(smem + Lt::kQueue);
     int* misc = reinterpret_cast<int*>(smem + Lt::kMisc);  // {row tiles per unit}
     int* cum = reinterpret_cast<int*>(smem + Lt::kPlan);   // [B + 1] units of one KV head before each sequence in order
@@ -121,10 +148,11 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
 
     if (tid == 0) {
         for (int i = 0; i < kBars; ++i)
-            bar_init(B(i), (i >= kPFull && i < kPFull + 4) || (i >= kOFree && i < kOFree + 2) ? 4u
-                           : i >= kUFree && i < kDone ? 10u
+            bar_init(B(i), (i >= kPFull && i < kPFull + 2) || (i >= kOFree && i < kOFree + 2) ? 8u
+                           : i >= kUFree && i < kDone ? kSoftmaxWarps + 2u
                            : i >= kFree && i < kFree + kStages ? 2u : 1u);
         *abort_flag = 0;
+        *turn = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
     if (warp == 0) {
@@ -132,6 +160,8 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
     }
+    for (int i = tid; i < 2 * 4 * kRows; i += kThreads)  // (tellings are numbered from 1)
+        reinterpret_cast<uint2*>(smem + Lt::kSay)[i] = make_uint2(0u, 0u);
     // the plan: sequences in order, and the row tiles before each
     int* keys = cum + 1;  // (first the keys, for the order)
     for (int b = tid; b < a.num_seqs; b += kThreads) keys[b] = span_of(a, b, blockIdx.x == 0).m;
@@ -192,7 +222,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
         return Unit{s.q0, s.n, s.k0, s.m, s.head, s.seen, s.more, 0};
     };
 
-    if (warp == 8) {
+    if (warp == kProducer) {
         // ------------------------------------------------------------ producer
         bool ok = true;
         int stage = 0, q_count[2] = {0, 0};  // tiles put into the ring, Q tiles loaded
@@ -268,100 +298,166 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                 a.counters[1] = 0;
             }
         }
-    } else if (warp == 9 || warp == 10) {
+    } else if (warp == kIssuer || warp == kIssuer + 1) {
         // ------------------------------------------- MMA issuers: A's and B's
-        if (lane == 0) {
-            const int x = warp - 9;
-            const uint32_t ts = tmem + x * kKeys, to = tmem + 2 * kKeys + x * kDim;
-            const uint64_t dq = sdesc(sbase + Lt::kQ + x * Lt::kTile, 16), dk = sdesc(sbase + Lt::kRing, 16);
-            const uint64_t dv = sdesc(sbase + Lt::kRing + Lt::kTile, kHalf);
-            constexpr uint64_t kPair = (2 * Lt::kTile) >> 4;  // from a K (V) stage to the next
-            int units = 0, q_count = 0, p_count = 0, o_count = 0;
-            int c = 0, j = 0, tiles = 0, nt = 0;  // key tile of all, of the unit; the row tile's, the unit's
-            bool ok = true;
-            // the next key tile of this row tile: 1, 0 at the list's end, -1 on failure
-            auto advance = [&]() -> int {
-                for (;;) {
-                    if (++j < tiles) {
-                        ++c;
-                        return 1;
+        // The whole warp walks through the list, so that descriptors and addresses are uniform values;
+        // one lane issues.  (A single lane's walk issued an MMA every 85 cycles, of the 64 that one takes.)
+        const int x = __shfl_sync(0xFFFFFFFFu, warp - kIssuer, 0);
+        uint32_t leader_;
+        asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(leader_));
+        const bool leader = leader_ != 0;
+        const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+        const uint32_t ts = tm + x * kKeys, to = tm + 2 * kKeys + x * kDim;
+        const uint64_t dq = sdesc(sbase + Lt::kQ + x * Lt::kTile, 16), dk = sdesc(sbase + Lt::kRing, 16);
+        const uint64_t dv = sdesc(sbase + Lt::kRing + Lt::kTile, kHalf);
+        constexpr uint64_t kPair = (2 * Lt::kTile) >> 4;  // from a K (V) stage to the next
+        int units = 0, q_count = 0, p_count = 0, o_count = 0;
+        int c = -1, j = -1, tiles = 0, nt = 0;  // key tile of all, of the unit; the row tile's, the unit's
+        auto await = [&](int i, int parity) -> bool { return __all_sync(0xFFFFFFFFu, wait(i, parity)); };
+        auto arrive = [&](int i) {
+            if (leader) bar_arrive(B(i));
+        };
+        // the next key tile of this row tile, in another unit: 1, 0 at the list's end, -1 on failure
+        auto next_unit = [&]() -> int {
+            for (;;) {
+                for (++j; j < nt; ++j) {  // tiles that only the other row tile multiplies
+                    ++c;
+                    const int st = 2 * (c & 1), ph = (c >> 1) & 1;
+                    for (int v = 0; v < 2; ++v) {
+                        if (!await(kFull + st + v, ph)) return -1;
+                        arrive(kFree + st + v);
                     }
-                    for (; j < nt; ++j) {  // tiles that only the other row tile multiplies
-                        ++c;
-                        const int st = 2 * (c & 1), ph = (c >> 1) & 1;
-                        for (int v = 0; v < 2; ++v) {
-                            if (!wait(kFull + st + v, ph)) return -1;
-                            bar_arrive(B(kFree + st + v));
-                        }
-                    }
-                    if (!wait(kUFull + units % kSlots, (units / kSlots) & 1)) return -1;
-                    const Unit u = take(units);
-                    bar_arrive(B(kUFree + units % kSlots));
-                    ++units;
-                    if (!u.more) return 0;
-                    const Shape sh(u, qpt, per_unit);
-                    tiles = sh.tiles[x], nt = sh.nt, j = -1;
                 }
-            };
-            auto scores = [&]() -> bool {
-                const int st = 2 * (c & 1);
-                if (j == 0 && !wait(kQFull + x, q_count++ & 1)) return false;
-                if (!wait(kFull + st, (c >> 1) & 1)) return false;
-                fence_after();
-                const uint64_t k = dk + (c & 1) * kPair;
+                if (!await(kUFull + units % kSlots, (units / kSlots) & 1)) return -1;
+                const Unit u = take(units);
+                __syncwarp();
+                arrive(kUFree + units % kSlots);
+                ++units;
+                const Shape sh(u, qpt, per_unit);
+                const int more = __shfl_sync(0xFFFFFFFFu, u.more, 0);
+                if (!more) return 0;
+                tiles = __shfl_sync(0xFFFFFFFFu, sh.tiles[x], 0), nt = __shfl_sync(0xFFFFFFFFu, sh.nt, 0), j = -1;
+                if (tiles > 0) {
+                    j = 0;
+                    ++c;
+                    return 1;
+                }
+            }
+        };
+        // One issuer's products at a time, so that a row tile's come as fast as they can while the other
+        // tile's softmax runs (side by side both tiles would wait for both, and the tensor core for them)
+        auto begin = [&]() -> bool {
+            for (uint32_t k = 0; k < kSpin; ++k) {
+                int got = 0;
+                if (leader) got = atomicCAS(turn, 0, 1) == 0;
+                if (__any_sync(0xFFFFFFFFu, got)) return true;
+                if ((k & 255) == 255 && __any_sync(0xFFFFFFFFu, *abort_flag)) return false;
+            }
+            return false;
+        };
+        auto end = [&]() {
+            if (leader) atomicExch(turn, 0);
+        };
+        auto scores = [&](int t) {  // S of key tile t
+            const uint64_t k = dk + (t & 1) * kPair;
+            if (leader) {
 #pragma unroll
                 for (int ks = 0; ks < kDim / 16; ++ks) {
                     const uint32_t off = ((ks >> 2) * kHalf + (ks & 3) * 32) >> 4;
                     mma_bf16(ts, dq + off, k + off, idesc(kKeys, 0), ks > 0 ? 1u : 0u);
                 }
-                mma_commit(B(kSFull + x));
-                mma_commit(B(kFree + st));
-                if (j == tiles - 1) mma_commit(B(kQFree + x));
-                return true;
-            };
-            auto values = [&]() -> bool {  // P V, the first 64 keys while P of the others is computed
-                const int st = 2 * (c & 1) + 1;
-                const uint64_t v = dv + (c & 1) * kPair;
-                if (!wait(kFull + st, (c >> 1) & 1)) return false;
-                if (j == 0 && o_count > 0 && !wait(kOFree + x, (o_count - 1) & 1)) return false;
-#pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    if (!wait(kPFull + 2 * x + hf, p_count & 1)) return false;
-                    fence_after();
-#pragma unroll
-                    for (int ks = 4 * hf; ks < 4 * hf + 4; ++ks)
-                        mma_bf16_ta(to, ts + 8 * ks, v + ((ks * 16 * 128) >> 4), idesc(kDim, 1), (j > 0 || ks > 0) ? 1u : 0u);
-                }
-                ++p_count;
-                if (j == tiles - 1) {
-                    mma_commit(B(kOFull + x));
-                    ++o_count;
-                }
-                mma_commit(B(kFree + st));
-                return true;
-            };
-            c = -1, j = -1;
-            int more = advance();
-            if (more > 0) ok = scores();
-            while (ok && more > 0) {
-                ok = values();
-                if (ok) more = advance();
-                if (ok && more > 0) ok = scores();
             }
-            if (!ok || more < 0) fail();
+        };
+        bool ok = true;
+        int more = next_unit();
+        bool fresh = true;  // S of the current tile is not issued yet
+        while (more > 0) {
+            if (fresh) {
+                ok = await(kQFull + x, q_count++ & 1) && await(kFull + 2 * (c & 1), (c >> 1) & 1) && begin();
+                if (!ok) break;
+                fence_after();
+                scores(c);
+                end();
+                if (leader) {
+                    mma_commit(B(kSFull + x));
+                    mma_commit(B(kFree + 2 * (c & 1)));
+                    if (tiles == 1) mma_commit(B(kQFree + x));
+                }
+                __syncwarp();
+                fresh = false;
+            }
+            // P V of this tile, then S of the unit's next
+            const int st = 2 * (c & 1) + 1;
+            const uint64_t v = dv + (c & 1) * kPair;
+            const bool last = j == tiles - 1;
+            ok = await(kFull + st, (c >> 1) & 1) && (j > 0 || o_count == 0 || await(kOFree + x, (o_count - 1) & 1)) &&
+                 (last || await(kFull + 2 * ((c + 1) & 1), ((c + 1) >> 1) & 1)) && await(kPFull + x, p_count & 1) && begin();
+            if (!ok) break;
+            ++p_count;
+            fence_after();
+            if (leader) {
+#pragma unroll
+                for (int ks = 0; ks < kKeys / 16; ++ks)
+                    mma_bf16_ta(to, ts + 8 * ks, v + ((ks * 16 * 128) >> 4), idesc(kDim, 1), (j > 0 || ks > 0) ? 1u : 0u);
+            }
+            if (!last) scores(c + 1);
+            end();
+            if (leader) {
+                if (last) {
+                    mma_commit(B(kOFull + x));
+                } else {
+                    mma_commit(B(kSFull + x));
+                    mma_commit(B(kFree + 2 * ((c + 1) & 1)));
+                    if (j == tiles - 2) mma_commit(B(kQFree + x));
+                }
+                mma_commit(B(kFree + st));
+            }
+            __syncwarp();
+            if (last) {
+                ++o_count;
+                more = next_unit();
+                fresh = true;
+            } else {
+                ++c;
+                ++j;
+            }
+        }
+        if (lane == 0 && (!ok || more < 0)) fail();
+        if (leader) {
             mma_commit(B(kDone + x));  // every product, and every signal of one, has landed before the CTA ends
             if (!bar_wait(B(kDone + x), 0)) fail();
         }
         __syncwarp();
-    } else if (warp < 8) {
+    } else if (warp < kSoftmaxWarps) {
         // -------------------------------------------------- softmax and output
-        const int x = warp >> 2, m = tid & 127;  // row tile, row
+        const int x = warp >> 3, hf = (warp >> 2) & 1, m = 32 * (warp & 3) + lane;  // row tile, half of the keys, row
+        constexpr int kMine = kKeys / 2, kCols = kDim / 2;                          // this thread's keys, and columns of O
         const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-        const uint32_t ts = tmem + lane_off + x * kKeys, to = tmem + lane_off + 2 * kKeys + x * kDim;
+        const uint32_t ts = tmem + lane_off + x * kKeys, to = tmem + lane_off + 2 * kKeys + x * kDim + hf * kCols;
         const float qk = a.scale_log2;
         const int qi = m / gh, hi = m % gh;  // query of the tile, head of the group
         int s_count = 0, o_count = 0, base = 0;
         bool ok = true;
+        // A row's two threads tell each other a value: {value, number of the telling}.  (No named barrier: a
+        // wait for it would have no end if the other warp had given up.)
+        volatile uint2* say = reinterpret_cast<volatile uint2*>(smem + Lt::kSay) + (x * 2 + hf) * kRows + m;
+        volatile uint2* hear = reinterpret_cast<volatile uint2*>(smem + Lt::kSay) + (x * 2 + 1 - hf) * kRows + m;
+        auto exchange = [&](int slot, float mine, int number, float& other) -> bool {
+            const uint32_t to_ = su32(const_cast<uint2*>(say + slot * 4 * kRows));
+            const uint32_t from = su32(const_cast<uint2*>(hear + slot * 4 * kRows));
+            asm volatile("st.volatile.shared.v2.b32 [%0], {%1, %2};\n" ::"r"(to_), "r"(__float_as_uint(mine)), "r"(number)
+                         : "memory");
+            for (uint32_t k = 0; k < kSpin; ++k) {
+                uint32_t bits, n;
+                asm volatile("ld.volatile.shared.v2.b32 {%0, %1}, [%2];\n" : "=r"(bits), "=r"(n) : "r"(from) : "memory");
+                if (__all_sync(0xFFFFFFFFu, n == static_cast<uint32_t>(number))) {
+                    other = __uint_as_float(bits);
+                    return true;
+                }
+                if ((k & 255) == 255 && __any_sync(0xFFFFFFFFu, *abort_flag)) return false;
+            }
+            return false;
+        };
         for (int i = 0; ok; ++i) {
             if (!__all_sync(0xFFFFFFFFu, wait(kUFull + i % kSlots, (i / kSlots) & 1))) {
                 ok = false;
@@ -380,7 +476,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             const int lim = valid ? u.seen + query : INT_MAX;  // keys that the row sees
             const int tiles = sh.tiles[x];
             __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
-                                 (static_cast<int64_t>(u.q0 + query) * a.num_q_heads + u.head * gh + hi) * kDim;
+                                 (static_cast<int64_t>(u.q0 + query) * a.num_q_heads + u.head * gh + hi) * kDim + hf * kCols;
             float m_used = -INFINITY, l = 0.f;
             for (int j = 0; j < tiles; ++j) {
                 if (!__all_sync(0xFFFFFFFFu, wait(kSFull + x, s_count & 1))) {
@@ -389,10 +485,76 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                 }
                 ++s_count;
                 fence_after();
-                const int key0 = j * kKeys;
+                const int key0 = j * kKeys + hf * kMine;  // this thread's first key
+                if (busy) {
+                    uint32_t v[kMine];
+#pragma unroll
+                    for (int c = 0; c < kMine / 32; ++c) tmem_ld32_nowait(ts + hf * kMine + 32 * c, v + 32 * c);
+                    asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
+                    const bool full = __all_sync(0xFFFFFFFFu, key0 + kMine <= lim);
+                    float mx = -INFINITY;
+                    if (full && qk > 0.f) {
+                        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                        for (int k = 0; k < kMine; k += 2)
+                            m4[(k >> 1) & 3] = max3(m4[(k >> 1) & 3], __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+                        mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * qk;
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < kMine; ++k)
+                            if (key0 + k < lim) mx = fmaxf(mx, __uint_as_float(v[k]) * qk);
+                    }
+                    float other;
+                    if (!exchange(0, mx, s_count, other)) {
+                        ok = false;
+                        break;
+                    }
+                    const float m_new = fmaxf(m_used, fmaxf(mx, other));
+                    const bool rescale = m_used != -INFINITY && m_new > m_used + 8.f;
+                    const float alpha = rescale ? ex2(m_used - m_new) : 1.f;
+                    if (m_used == -INFINITY || rescale) m_used = m_new;
+                    const float base2 = m_used == -INFINITY ? 0.f : m_used;
+                    if (__any_sync(0xFFFFFFFFu, rescale)) {  // ("S j done": P V j - 1 is, too)
+#pragma unroll 1
+                        for (int c = 0; c < kCols; c += 8) tmem_scale8(to + c, alpha);
+                        asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
+                        l *= alpha;
+                    }
+                    float l0 = 0.f, l1 = 0.f;
+                    // P as BF16 pairs, 16 columns at a time, in the registers of the scores that it replaces.
+                    // (The other thread has read its scores: it told their maximum.)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        if (full) {
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) {
+                                uint32_t* y = v + 32 * c;
+                                float x0, x1;
+                                fma2(x0, x1, __uint_as_float(y[2 * k]), __uint_as_float(y[2 * k + 1]), qk, qk, -base2, -base2);
+                                const float p0 = ex2(x0), p1 = ex2(x1);
+                                add2(l0, l1, l0, l1, p0, p1);
+                                y[k] = bf16x2(p0, p1);
+                            }
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) {
+                                uint32_t* y = v + 32 * c;
+                                const int t = key0 + 32 * c + 2 * k;
+                                const float p0 = t < lim ? ex2(fmaf(__uint_as_float(y[2 * k]), qk, -base2)) : 0.f;
+                                const float p1 = t + 1 < lim ? ex2(fmaf(__uint_as_float(y[2 * k + 1]), qk, -base2)) : 0.f;
+                                l0 += p0;
+                                l1 += p1;
+                                y[k] = bf16x2(p0, p1);
+                            }
+                        }
+                        tmem_st16_nowait(ts + hf * (kMine / 2) + 16 * c, v + 32 * c);
+                    }
+                    asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
+                    l += l0 + l1;
+                }
                 // V rows behind the sequence: zero (they are another's, or unwritten, and may hold NaN), before
-                // any P of this tile is ready; A and B both see to it
-                const int there = u.m - key0;
+                // P is ready; A and B both see to it
+                const int there = u.m - j * kKeys;
                 if (there < kKeys) {
                     const int c = place0 + j, s = 2 * (c & 1) + 1;
                     if (!__all_sync(0xFFFFFFFFu, wait(kFull + s, (c >> 1) & 1))) {
@@ -401,109 +563,40 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                     }
                     uint8_t* vs = smem + Lt::kRing + s * Lt::kTile;
                     const int gone = kKeys - there;  // whole 128-byte rows: the swizzle does not matter
-                    for (int e = m; e < Lt::kHalves * gone * 8; e += 128) {
+                    for (int e = (tid & 255); e < Lt::kHalves * gone * 8; e += 256) {
                         const int h = e / (gone * 8), r = there + e % (gone * 8) / 8;
                         *reinterpret_cast<uint4*>(vs + h * kHalf + r * 128 + e % 8 * 16) = make_uint4(0u, 0u, 0u, 0u);
                     }
                     fence_async_smem();
                 }
-                auto ready = [&](int hf) {  // P of 64 keys is in tensor memory
-                    fence_before();
-                    __syncwarp();
-                    if (lane == 0) bar_arrive(B(kPFull + 2 * x + hf));
-                };
-                if (busy) {
-                    const bool full = __all_sync(0xFFFFFFFFu, key0 + kKeys <= lim);
-                    uint32_t v[kKeys];
-#pragma unroll
-                    for (int c = 0; c < kKeys / 32; ++c) tmem_ld32_nowait(ts + 32 * c, v + 32 * c);
-                    asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
-                    float mx = -INFINITY;
-                    if (full && qk > 0.f) {
-                        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                        for (int k = 0; k < kKeys; k += 2)
-                            m4[(k >> 1) & 3] = max3(m4[(k >> 1) & 3], __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
-                        mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * qk;
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < kKeys; ++k)
-                            if (key0 + k < lim) mx = fmaxf(mx, __uint_as_float(v[k]) * qk);
-                    }
-                    const float m_new = fmaxf(m_used, mx);
-                    const bool rescale = m_used != -INFINITY && m_new > m_used + 8.f;
-                    const float alpha = rescale ? ex2(m_used - m_new) : 1.f;
-                    if (m_used == -INFINITY || rescale) m_used = m_new;
-                    const float base2 = m_used == -INFINITY ? 0.f : m_used;
-                    if (__any_sync(0xFFFFFFFFu, rescale)) {  // ("S j done": P V j - 1 is, too)
-#pragma unroll 1
-                        for (int c = 0; c < kDim / 32; ++c) {
-                            uint32_t o[32];
-                            tmem_ld32(to + 32 * c, o);
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-                            tmem_st32(to + 32 * c, o);
-                        }
-                        l *= alpha;
-                    }
-                    float l0 = 0.f, l1 = 0.f;
-#pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        uint32_t p[32];
-                        if (full) {
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) {
-                                float x0, x1;
-                                fma2(x0, x1, __uint_as_float(v[64 * hf + 2 * k]), __uint_as_float(v[64 * hf + 2 * k + 1]), qk,
-                                     qk, -base2, -base2);
-                                const float p0 = ex2(x0), p1 = ex2(x1);
-                                add2(l0, l1, l0, l1, p0, p1);
-                                p[k] = bf16x2(p0, p1);
-                            }
-                        } else {
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) {
-                                const int t = key0 + 64 * hf + 2 * k;
-                                const float p0 = t < lim ? ex2(fmaf(__uint_as_float(v[64 * hf + 2 * k]), qk, -base2)) : 0.f;
-                                const float p1 =
-                                    t + 1 < lim ? ex2(fmaf(__uint_as_float(v[64 * hf + 2 * k + 1]), qk, -base2)) : 0.f;
-                                l0 += p0;
-                                l1 += p1;
-                                p[k] = bf16x2(p0, p1);
-                            }
-                        }
-                        tmem_st32(ts + 32 * hf, p);
-                        ready(hf);
-                    }
-                    l += l0 + l1;
-                } else {
-                    ready(0);
-                    ready(1);
-                }
+                fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(B(kPFull + x));
             }
             if (!ok) break;
             if (tiles == 0) {  // no key is seen
                 if (valid)
-                    for (int k = 0; k < kDim / 8; ++k) reinterpret_cast<uint4*>(out)[k] = make_uint4(0u, 0u, 0u, 0u);
+                    for (int k = 0; k < kCols / 8; ++k) reinterpret_cast<uint4*>(out)[k] = make_uint4(0u, 0u, 0u, 0u);
                 continue;
             }
-            if (!__all_sync(0xFFFFFFFFu, wait(kOFull + x, o_count & 1))) {
+            float l_other;
+            if (!exchange(1, l, s_count, l_other) || !__all_sync(0xFFFFFFFFu, wait(kOFull + x, o_count & 1))) {
                 ok = false;
                 break;
             }
             ++o_count;
             fence_after();
-            uint32_t o[kDim];
+            uint32_t o[kCols];
 #pragma unroll
-            for (int c = 0; c < kDim / 32; ++c) tmem_ld32_nowait(to + 32 * c, o + 32 * c);
+            for (int c = 0; c < kCols / 32; ++c) tmem_ld32_nowait(to + 32 * c, o + 32 * c);
             asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
             fence_before();
             __syncwarp();
             if (lane == 0) bar_arrive(B(kOFree + x));  // the next unit's first P V may overwrite it
             if (valid) {
-                const float inv = 1.f / l;
+                const float inv = 1.f / (l + l_other);
 #pragma unroll
-                for (int k = 0; k < kDim / 8; ++k) {
+                for (int k = 0; k < kCols / 8; ++k) {
                     uint32_t w[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
