@@ -17,9 +17,9 @@
 //    order, so "S j + 1 done" says that P V j is done too.  (One issuer for both spent
 //    4200 of 4500 cycles per pair of tiles on its own instructions);
 //  * warps 0-7 and 8-15, softmax of A and of B: two threads own a row, one its first 64
-//    keys of a tile and half of its output columns, the other the rest.  The running
-//    maximum moves only when a score passes it by 8 (log2 units), which rescales O in
-//    tensor memory; otherwise O is not touched until it is written out.
+//    keys of a tile and half of its output columns, the other the rest.  The base of a
+//    row's weights is a past maximum: it moves only when a score passes it by 8 (log2
+//    units), which rescales O in tensor memory before the next tile's products.
 // Tensor memory: 2 x 128 score columns, 2 x head_dim output columns.
 // Shared memory: Q 2 x 32 KB, four ring stages of 32 KB, the units' plan.
 // Every wait is bounded: an expired one sets PKV_ERRBIT_TIMEOUT and ends the CTA, whose
@@ -41,6 +41,7 @@ constexpr int kRows = 128, kKeys = 128;
 constexpr int kHalf = 128 * 128;     // 64 columns of 128 rows
 constexpr int kStages = 4;
 constexpr int kSlots = 2;            // units in the queue
+constexpr float kFar = 60.f;         // weights stay below 2^60
 constexpr int kSortSeqs = 256;       // up to so many sequences are taken longest first
 
 enum Bar {
@@ -66,7 +67,7 @@ struct Layout {
     static constexpr int kQ = 0, kRing = 2 * kTile, kBar = kRing + kStages * kTile;
     static constexpr int kQueue = kBar + 8 * kBars + 16, kMisc = kQueue + kSlots * static_cast<int>(sizeof(Unit));
     static constexpr int kSay = (kMisc + 64 + 127) / 128 * 128;  // what a row's two threads tell each other
-    static constexpr int kPlan = kSay + 2 * 4 * kRows * 8;
+    static constexpr int kPlan = kSay + 3 * 4 * kRows * 8;
     static constexpr int kSmem = kPlan + (kPromptMaxSeqs + 1) * 4 + kPromptMaxSeqs * 2 + 1024;
     static_assert(kSmem <= 232448, "shared memory per CTA");
 };
@@ -103,6 +104,19 @@ __device__ __forceinline__ void tmem_scale8(uint32_t at, float f) {
                  "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                  : "memory");
 }
+// The same for BF16 pairs.
+__device__ __forceinline__ void tmem_scale8_bf16(uint32_t at, float f) {
+    uint32_t v[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "r"(at));
+    asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = bf16x2(bf16_lo(v[k]) * f, bf16_hi(v[k]) * f);
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(at), "r"(v[0]), "r"(v[1]),
+                 "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
 // 16 columns of this thread's lane.
 __device__ __forceinline__ void tmem_st16_nowait(uint32_t at, const uint32_t* v) {
     asm volatile(
@@ -110,6 +124,11 @@ __device__ __forceinline__ void tmem_st16_nowait(uint32_t at, const uint32_t* v)
         "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
         "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
+}
+
+// The next base: whole steps above the last one, so that a change of base is exact.
+__device__ __forceinline__ float above(float base, float top) {
+    return base == -INFINITY ? top : base + ceilf(top - base);
 }
 
 // What the roles agree on about a unit.
@@ -160,7 +179,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
     }
-    for (int i = tid; i < 2 * 4 * kRows; i += kThreads)  // (tellings are numbered from 1)
+    for (int i = tid; i < 3 * 4 * kRows; i += kThreads)  // (tellings are numbered from 1)
         reinterpret_cast<uint2*>(smem + Lt::kSay)[i] = make_uint2(0u, 0u);
     // the plan: sequences in order, and the row tiles before each
     int* keys = cum + 1;  // (first the keys, for the order)
@@ -398,7 +417,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             if (leader) {
 #pragma unroll
                 for (int ks = 0; ks < kKeys / 16; ++ks)
-                    mma_bf16_ta(to, ts + 8 * ks, v + ((ks * 16 * 128) >> 4), idesc(kDim, 1), (j > 0 || ks > 0) ? 1u : 0u);
+                    mma_bf16_ta(to, ts + (ks & 4) * (kKeys / 8) + (ks & 3) * 8, v + ((ks * 16 * 128) >> 4), idesc(kDim, 1), (j > 0 || ks > 0) ? 1u : 0u);
             }
             if (!last) scores(c + 1);
             end();
@@ -440,16 +459,17 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
         bool ok = true;
         // A row's two threads tell each other a value: {value, number of the telling}.  (No named barrier: a
         // wait for it would have no end if the other warp had given up.)
-        volatile uint2* say = reinterpret_cast<volatile uint2*>(smem + Lt::kSay) + (x * 2 + hf) * kRows + m;
-        volatile uint2* hear = reinterpret_cast<volatile uint2*>(smem + Lt::kSay) + (x * 2 + 1 - hf) * kRows + m;
-        auto exchange = [&](int slot, float mine, int number, float& other) -> bool {
-            const uint32_t to_ = su32(const_cast<uint2*>(say + slot * 4 * kRows));
-            const uint32_t from = su32(const_cast<uint2*>(hear + slot * 4 * kRows));
-            asm volatile("st.volatile.shared.v2.b32 [%0], {%1, %2};\n" ::"r"(to_), "r"(__float_as_uint(mine)), "r"(number)
+        const uint32_t say = sbase + Lt::kSay + ((x * 2 + hf) * kRows + m) * 8;
+        const uint32_t its_say = sbase + Lt::kSay + ((x * 2 + 1 - hf) * kRows + m) * 8;
+        auto tell = [&](int slot, float mine, int number) {
+            asm volatile("st.volatile.shared.v2.b32 [%0], {%1, %2};\n" ::"r"(say + slot * 4 * kRows * 8),
+                         "r"(__float_as_uint(mine)), "r"(number)
                          : "memory");
+        };
+        auto hear = [&](int slot, int number, float& other) -> bool {
             for (uint32_t k = 0; k < kSpin; ++k) {
                 uint32_t bits, n;
-                asm volatile("ld.volatile.shared.v2.b32 {%0, %1}, [%2];\n" : "=r"(bits), "=r"(n) : "r"(from) : "memory");
+                asm volatile("ld.volatile.shared.v2.b32 {%0, %1}, [%2];\n" : "=r"(bits), "=r"(n) : "r"(its_say + slot * 4 * kRows * 8) : "memory");
                 if (__all_sync(0xFFFFFFFFu, n == static_cast<uint32_t>(number))) {
                     other = __uint_as_float(bits);
                     return true;
@@ -463,21 +483,23 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                 ok = false;
                 break;
             }
-            const Unit u = take(i);
-            __syncwarp();
-            if (lane == 0) bar_arrive(B(kUFree + i % kSlots));
-            if (!u.more) break;
-            const Shape sh(u, qpt, per_unit);
-            const int place0 = base;  // key tiles of the units before
-            base += sh.nt;
-            const int query = x * qpt + qi;
-            const bool valid = x < per_unit && qi < qpt && query < u.n;
-            const bool busy = __any_sync(0xFFFFFFFFu, valid);
-            const int lim = valid ? u.seen + query : INT_MAX;  // keys that the row sees
-            const int tiles = sh.tiles[x];
-            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
-                                 (static_cast<int64_t>(u.q0 + query) * a.num_q_heads + u.head * gh + hi) * kDim + hf * kCols;
-            float m_used = -INFINITY, l = 0.f;
+            // (a unit's place in the queue is kept while it is worked on: what is needed once is read when it is)
+            const volatile Unit& slot = queue[i % kSlots];
+            if (!slot.more) break;
+            int lim, tiles, place0;  // keys that the row sees, key tiles of the row tile, and of the units before
+            bool busy;
+            {
+                const Unit u = take(i);
+                const Shape sh(u, qpt, per_unit);
+                place0 = base;
+                base += sh.nt;
+                const int query = x * qpt + qi;
+                const bool valid = x < per_unit && qi < qpt && query < u.n;
+                busy = __any_sync(0xFFFFFFFFu, valid);
+                lim = valid ? u.seen + query : INT_MAX;
+                tiles = sh.tiles[x];
+            }
+            float m_used = -INFINITY, m_next = -INFINITY, l = 0.f;  // base of this tile's weights, of the next one's
             for (int j = 0; j < tiles; ++j) {
                 if (!__all_sync(0xFFFFFFFFu, wait(kSFull + x, s_count & 1))) {
                     ok = false;
@@ -486,49 +508,58 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                 ++s_count;
                 fence_after();
                 const int key0 = j * kKeys + hf * kMine;  // this thread's first key
+                float mx = -INFINITY, its = -INFINITY, m_own = 0.f, l0 = 0.f;
                 if (busy) {
-                    uint32_t v[kMine];
-#pragma unroll
-                    for (int c = 0; c < kMine / 32; ++c) tmem_ld32_nowait(ts + hf * kMine + 32 * c, v + 32 * c);
-                    asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
                     const bool full = __all_sync(0xFFFFFFFFu, key0 + kMine <= lim);
-                    float mx = -INFINITY;
-                    if (full && qk > 0.f) {
-                        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    {  // the maximum first, from a load of its own: the weights' loop then keeps few registers
+                        uint32_t v[kMine];
 #pragma unroll
-                        for (int k = 0; k < kMine; k += 2)
-                            m4[(k >> 1) & 3] = max3(m4[(k >> 1) & 3], __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
-                        mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * qk;
-                    } else {
+                        for (int c = 0; c < kMine / 32; ++c) tmem_ld32_nowait(ts + hf * kMine + 32 * c, v + 32 * c);
+                        asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
+                        if (full && qk > 0.f) {
+                            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                        for (int k = 0; k < kMine; ++k)
-                            if (key0 + k < lim) mx = fmaxf(mx, __uint_as_float(v[k]) * qk);
+                            for (int k = 0; k < kMine; k += 2)
+                                m4[(k >> 1) & 3] = max3(m4[(k >> 1) & 3], __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+                            mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * qk;
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < kMine; ++k)
+                                if (key0 + k < lim) mx = fmaxf(mx, __uint_as_float(v[k]) * qk);
+                        }
                     }
-                    float other;
-                    if (!exchange(0, mx, s_count, other)) {
-                        ok = false;
-                        break;
-                    }
-                    const float m_new = fmaxf(m_used, fmaxf(mx, other));
-                    const bool rescale = m_used != -INFINITY && m_new > m_used + 8.f;
-                    const float alpha = rescale ? ex2(m_used - m_new) : 1.f;
-                    if (m_used == -INFINITY || rescale) m_used = m_new;
-                    const float base2 = m_used == -INFINITY ? 0.f : m_used;
-                    if (__any_sync(0xFFFFFFFFu, rescale)) {  // ("S j done": P V j - 1 is, too)
+                    // The base of this tile's weights 2^(score - base) was agreed on after the tile before, so that no
+                    // thread waits here for the other's maximum (which cost 340 of 3400 cycles); they hear it when
+                    // their weights are written.  The unit's first tile has no tile before.
+                    tell(0, mx, s_count);
+                    if (j == 0) {
+                        if (!hear(0, s_count, its)) {
+                            ok = false;
+                            break;
+                        }
+                        m_used = fmaxf(mx, its);
+                    } else if (__any_sync(0xFFFFFFFFu, m_next != m_used)) {  // ("S j done": P V j - 1 is, too)
+                        const float alpha = m_used == -INFINITY ? 0.f : ex2(m_used - m_next);
 #pragma unroll 1
                         for (int c = 0; c < kCols; c += 8) tmem_scale8(to + c, alpha);
                         asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
                         l *= alpha;
+                        m_used = m_next;
                     }
-                    float l0 = 0.f, l1 = 0.f;
-                    // P as BF16 pairs, 16 columns at a time, in the registers of the scores that it replaces.
-                    // (The other thread has read its scores: it told their maximum.)
+                    // far above the base: a base of this thread's own, until both know better
+                    m_own = mx > m_used + kFar ? above(m_used, mx) : m_used;
+                    const float base2 = m_own == -INFINITY ? 0.f : m_own;
+                    float l1 = 0.f;
+                    // P as BF16 pairs, 16 columns at a time over this thread's own scores, which it has read by then
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
+                        uint32_t v[32];
+                        tmem_ld32_nowait(ts + hf * kMine + 32 * c, v);
+                        asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
                         if (full) {
 #pragma unroll
                             for (int k = 0; k < 16; ++k) {
-                                uint32_t* y = v + 32 * c;
+                                uint32_t* y = v;
                                 float x0, x1;
                                 fma2(x0, x1, __uint_as_float(y[2 * k]), __uint_as_float(y[2 * k + 1]), qk, qk, -base2, -base2);
                                 const float p0 = ex2(x0), p1 = ex2(x1);
@@ -538,7 +569,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                         } else {
 #pragma unroll
                             for (int k = 0; k < 16; ++k) {
-                                uint32_t* y = v + 32 * c;
+                                uint32_t* y = v;
                                 const int t = key0 + 32 * c + 2 * k;
                                 const float p0 = t < lim ? ex2(fmaf(__uint_as_float(y[2 * k]), qk, -base2)) : 0.f;
                                 const float p1 = t + 1 < lim ? ex2(fmaf(__uint_as_float(y[2 * k + 1]), qk, -base2)) : 0.f;
@@ -547,14 +578,42 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                                 y[k] = bf16x2(p0, p1);
                             }
                         }
-                        tmem_st16_nowait(ts + hf * (kMine / 2) + 16 * c, v + 32 * c);
+                        tmem_st16_nowait(ts + hf * kMine + 16 * c, v);
                     }
                     asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
-                    l += l0 + l1;
+                    l0 += l1;
+                    if (j > 0) {
+                        fence_before();
+                        tell(2, 0.f, s_count);  // (its weights are written)
+                        if (__any_sync(0xFFFFFFFFu, mx > m_used + kFar)) {
+                            // One warp of the two brings the rows' weights, and O, to a common base; the first if it
+                            // has such a row
+                            float none;
+                            if (!hear(0, s_count, its) || !hear(2, s_count, none)) {
+                                ok = false;
+                                break;
+                            }
+                            fence_after();
+                            const float top = fmaxf(mx, its);
+                            if (hf == 0 || !__any_sync(0xFFFFFFFFu, its > m_used + kFar)) {
+                                const float m_new = top > m_used + kFar ? above(m_used, top) : m_used;
+                                const float m_its = its > m_used + kFar ? above(m_used, its) : m_used;
+                                auto f = [&](float from) { return from == m_new ? 1.f : from == -INFINITY ? 0.f : ex2(from - m_new); };
+#pragma unroll 1
+                                for (int c = 0; c < kMine / 2; c += 8) {
+                                    tmem_scale8_bf16(ts + hf * kMine + c, f(m_own));
+                                    tmem_scale8_bf16(ts + (1 - hf) * kMine + c, f(m_its));
+                                }
+#pragma unroll 1
+                                for (int c = 0; c < kDim; c += 8) tmem_scale8(to - hf * kCols + c, f(m_used));
+                                asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
+                            }
+                        }
+                    }
                 }
                 // V rows behind the sequence: zero (they are another's, or unwritten, and may hold NaN), before
                 // P is ready; A and B both see to it
-                const int there = u.m - j * kKeys;
+                const int there = slot.m - j * kKeys;
                 if (there < kKeys) {
                     const int c = place0 + j, s = 2 * (c & 1) + 1;
                     if (!__all_sync(0xFFFFFFFFu, wait(kFull + s, (c >> 1) & 1))) {
@@ -572,15 +631,37 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                 fence_before();
                 __syncwarp();
                 if (lane == 0) bar_arrive(B(kPFull + x));
+                if (busy) {  // the next tile's base, while the products run
+                    if (j > 0 && !hear(0, s_count, its)) {
+                        ok = false;
+                        break;
+                    }
+                    const float top = fmaxf(mx, its);
+                    if (__any_sync(0xFFFFFFFFu, top > m_used + kFar)) {
+                        const float m_new = top > m_used + kFar ? above(m_used, top) : m_used;
+                        l = m_used == m_new ? l : m_used == -INFINITY ? 0.f : l * ex2(m_used - m_new);
+                        l0 = m_own == m_new ? l0 : l0 * ex2(m_own - m_new);
+                        m_used = m_new;
+                    }
+                    m_next = top > m_used + 8.f ? above(m_used, top) : m_used;
+                    l += l0;
+                }
             }
             if (!ok) break;
+            const bool valid = lim != INT_MAX;
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
+                                 (static_cast<int64_t>(slot.q0 + x * qpt + qi) * a.num_q_heads + slot.head * gh + hi) * kDim + hf * kCols;
+            __syncwarp();
+            if (lane == 0) bar_arrive(B(kUFree + i % kSlots));
             if (tiles == 0) {  // no key is seen
                 if (valid)
                     for (int k = 0; k < kCols / 8; ++k) reinterpret_cast<uint4*>(out)[k] = make_uint4(0u, 0u, 0u, 0u);
                 continue;
             }
-            float l_other;
-            if (!exchange(1, l, s_count, l_other) || !__all_sync(0xFFFFFFFFu, wait(kOFull + x, o_count & 1))) {
+            // (a base that was to change stays: both threads' l and O are in this one)
+            float l_other = 0.f;
+            tell(1, l, s_count);
+            if (!hear(1, s_count, l_other) || !__all_sync(0xFFFFFFFFu, wait(kOFull + x, o_count & 1))) {
                 ok = false;
                 break;
             }

@@ -76,7 +76,7 @@ struct PromptArgs {
     float scale_log2;
     int32_t* counters;                         // [2], zero between calls (tensor-core design)
 };
-constexpr int kPromptMaxSeqs = 4096;           // sequences that the tensor-core design plans in shared memory
+constexpr int kPromptMaxSeqs = 2048;           // sequences that the tensor-core design plans in shared memory
 bool prompt_tc_fits(pkv_dtype t, int num_seqs, int q_rows, int num_q_heads, int num_kv_heads);
 cudaError_t launch_prompt_tc(int head_dim, const PromptArgs& a, cudaStream_t stream);
 cudaError_t launch_prompt_simt(pkv_dtype t, int head_dim, const PromptArgs& a, cudaStream_t stream);
