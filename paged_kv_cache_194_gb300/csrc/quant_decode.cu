@@ -24,11 +24,15 @@
 //    sum 2^t_j z'_j have a running maximum of their own and stay in binary32.
 //
 // Schedule: the 64-token tiles of all (sequence, KV head, part of the group) units
-// form one list, cut into equal ranges, one per resident CTA.  In a tile each of a
-// CTA's four warps has 16 tokens of one block, and loads its next steps' rows while
-// it multiplies; the warps meet at the end of a unit.  A unit cut by ranges leaves
-// pieces in the workspace, and the CTA that leaves the last of them joins them, in
-// order (the result does not depend on who that is).
+// form one list, in which a unit weighs kUnitCost tiles beside its own; it is cut into
+// equal ranges, one per resident CTA.  In a tile each of a CTA's four warps has 16
+// tokens of one block; the rows of its next few steps, of the next unit's first ones at
+// a unit's end, are on their way into a ring of its own in shared memory while it
+// multiplies.  The warps meet at the end of a unit.
+// A unit cut by ranges leaves pieces in the workspace, and the CTA that leaves the last
+// of them joins them, in order (the result does not depend on who that is).
+#include <type_traits>
+
 #include "device_common.cuh"
 #include "quant_internal.h"
 
@@ -37,8 +41,19 @@ namespace {
 
 constexpr int kThreads = 128, kWarps = 4;
 constexpr int kTile = 64, kStep = 16;
-constexpr int kCtasPerSm = 4;
+constexpr int kUnitCost = 2;
 constexpr int kMaxCtas = 1024;
+// CTAs per SM, and steps whose rows are under way in a warp (pair: taken two at a time).  HBM answers after 2.5 to 3 us
+// under load, so an SM wants 130 to 150 KB on their way.
+constexpr int ctas_per_sm(int bits, int dim, int nt, bool pair) {
+    if (dim == 64) return nt == 1 ? 4 : 3;
+    return nt == 2 ? 2 : pair ? (bits == 4 ? 3 : 2) : (bits == 4 ? 4 : 3);
+}
+constexpr int depth_of(int bits, int dim, int nt, bool pair) {
+    if (dim == 64) return bits == 4 ? 8 : (nt == 1 ? 4 : 6);
+    return nt == 2 ? (bits == 4 ? 8 : 4) : pair ? 6 : (bits == 4 ? 4 : 3);
+}
+constexpr float kNone = -1e30f;  // a maximum of nothing
 constexpr unsigned kAll = 0xFFFFFFFFu;
 
 __device__ __forceinline__ float ex2f(float x) {
@@ -71,13 +86,13 @@ __device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
 template <int kWords>
 __device__ __forceinline__ void load_words(uint32_t* w, const uint8_t* p) {
     if constexpr (kWords == 1) {
-        asm volatile("ld.global.L1::no_allocate.b32 %0, [%1];\n" : "=r"(w[0]) : "l"(p));
+        w[0] = *reinterpret_cast<const uint32_t*>(p);
     } else if constexpr (kWords == 2) {
-        asm volatile("ld.global.L1::no_allocate.v2.b32 {%0,%1}, [%2];\n" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
+        const uint2 v = *reinterpret_cast<const uint2*>(p);
+        w[0] = v.x, w[1] = v.y;
     } else {
-        asm volatile("ld.global.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];\n"
-                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                     : "l"(p));
+        const uint4 v = *reinterpret_cast<const uint4*>(p);
+        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
     }
 }
 __device__ __forceinline__ int count_up(int* p) {
@@ -101,22 +116,43 @@ struct Share {
     }
 };
 
+// A warp's 16 rows in shared memory: K, V, then the pairs of both.  Rows and their 16-byte chunks are placed so that
+// the lanes of a load below meet no bank twice (head_dim 128): K row r at place r, its chunks of an odd 128-byte
+// row exchanged by halves; V's even rows first, chunks exchanged by row.
 template <int kBits, int kDim>
-struct Loaded {  // one step's rows of a lane: K rows g, g + 8; V rows 2t, 2t + 1, 2t + 8, 2t + 9; pairs of g, g + 8
-    uint32_t k[2][Share<kBits, kDim>::kKW];
-    uint32_t v[4][Share<kBits, kDim>::kVW];
-    uint32_t kp[2], vp[2];
+struct Stage {
+    static constexpr int kRow = kDim * kBits / 8, kChunks = kRow / 16;
+    static constexpr int kV = 16 * kRow, kPairs = 32 * kRow, kBytes = kPairs + 128;
+    __device__ static int k_at(int row, int chunk) { return row * kRow + ((kChunks == 8 ? chunk ^ ((row & 1) << 2) : chunk) << 4); }
+    __device__ static int v_at(int row, int chunk) {
+        if constexpr (kChunks == 8) return kV + row * kRow + ((chunk ^ (row & 6)) << 4);
+        const int place = (row >> 1) | ((row & 1) << 3);
+        if constexpr (kChunks == 4) return kV + place * kRow + ((chunk ^ (place & 2)) << 4);
+        return kV + place * kRow + (chunk << 4);
+    }
 };
 
-template <int kBits, int kDim, int kNT>
-__global__ void __launch_bounds__(kThreads, kNT == 1 ? kCtasPerSm : 3) quant_decode_kernel(const QuantDecodeArgs a) {
+// A segment: tiles [first, end) of a unit, tokens [token0, token1) of its sequence.
+struct Seg {
+    int b, nt, unit, first, end, token0, token1;
+    long long at;  // list place of the unit, whose tiles lie behind its own cost
+};
+
+template <int kBits, int kDim, int kNT, bool kPair>
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(kBits, kDim, kNT, kPair)) quant_decode_kernel(const QuantDecodeArgs a) {
     using S = Share<kBits, kDim>;
-    constexpr int kCols = 8 * kNT, kPitch = kDim + 4;
-    __shared__ float so[kWarps][kCols][kPitch];
+    static_assert(!kPair || kNT == 1);
+    constexpr int kCols = 8 * kNT, kSumCols = kPair ? 4 : kCols, kPitch = kDim + 4;
+    constexpr int kDepth = depth_of(kBits, kDim, kNT, kPair), kNS = kPair ? 2 : 1;  // (steps at a time)
+    using St = Stage<kBits, kDim>;
+    extern __shared__ __align__(16) uint8_t dynamic[];
+    auto so = reinterpret_cast<float (*)[kSumCols][kPitch]>(dynamic);  // [kWarps]
+    uint8_t* ring = dynamic + sizeof(float) * kWarps * kSumCols * kPitch + (threadIdx.x >> 5) * (kDepth * St::kBytes);
     __shared__ float sm[kWarps][kCols], sl[kWarps][kCols], sz[kWarps][kCols];
     __shared__ long long scan[kThreads];
-    __shared__ int last_flag, found[2];
+    __shared__ int last_flag[2], found;
     __shared__ long long found_at;
+    __shared__ Seg split[2];  // this CTA's pieces of units that others share: at its range's start, and at its end
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int gh = a.num_q_heads / a.num_kv_heads, parts = (gh + kCols - 1) / kCols;
     const int per_seq = a.num_kv_heads * parts, bs_mask = (1 << a.block_shift) - 1;
@@ -127,7 +163,10 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? kCtasPerSm : 3) quant_dec
         const int L = a.lens[b];
         return L < 0 ? 0 : (L > a.max_len ? a.max_len : L);
     };
-    auto tiles_of = [&](int b) { return static_cast<long long>((len_of(b) + kTile - 1) / kTile) * per_seq; };
+    auto cost_of = [&](int b) {  // of a sequence's units in the list
+        const int L = len_of(b);
+        return L > 0 ? static_cast<long long>((L + kTile - 1) / kTile + kUnitCost) * per_seq : 0;
+    };
     // empty sequences' rows, and lengths that cannot be
     for (int b = blockIdx.x; b < a.num_seqs; b += gridDim.x) {
         const int L = a.lens[b];
@@ -141,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? kCtasPerSm : 3) quant_dec
     const int run = (a.num_seqs + kThreads - 1) / kThreads;  // sequences per thread
     long long mine = 0;
     for (int i = 0; i < run; ++i)
-        if (tid * run + i < a.num_seqs) mine += tiles_of(tid * run + i);
+        if (tid * run + i < a.num_seqs) mine += cost_of(tid * run + i);
     scan[tid] = mine;
     __syncthreads();
     for (int d = 1; d < kThreads; d <<= 1) {
@@ -159,43 +198,143 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? kCtasPerSm : 3) quant_dec
         long long at = scan[tid] - mine;
         int b = tid * run;
         for (;; ++b) {
-            const long long n = tiles_of(b);
+            const long long n = cost_of(b);
             if (g0 < at + n) break;
             at += n;
         }
-        found[0] = b;
+        found = b;
         found_at = at;
     }
     __syncthreads();
-    int b = found[0], L = len_of(b), nt = (L + kTile - 1) / kTile;
-    long long seq_at = found_at;  // list place of the sequence's first tile
 
-    for (long long at = g0; at < g1;) {
-        // the segment: tiles [first, end) of unit `unit` of sequence b
-        const int unit = static_cast<int>((at - seq_at) / nt), first = static_cast<int>((at - seq_at) % nt);
-        const long long unit_at = seq_at + static_cast<long long>(unit) * nt;
-        const int end = static_cast<int>(g1 - unit_at < nt ? g1 - unit_at : nt);
-        const int h = unit / parts, q0 = (unit % parts) * kCols, rows = min(kCols, gh - q0);
-        const int token0 = first * kTile, token1 = min(L, end * kTile);
+    // (whether [first, end) is a piece of the CTA's range, which ends at g1)
+    auto clip = [&](Seg& s, int L) -> bool {
+        const long long left = g1 - s.at - kUnitCost;
+        s.end = static_cast<int>(left < s.nt ? left : s.nt);
+        s.token0 = s.first * kTile;
+        s.token1 = min(L, s.end * kTile);
+        return s.end > s.first;
+    };
+    auto next = [&](Seg& s) -> bool {  // the unit behind s
+        s.at += s.nt + kUnitCost;
+        if (s.at + kUnitCost >= g1) return false;
+        int L = 0;
+        if (++s.unit == per_seq) {
+            s.unit = 0;
+            do L = len_of(++s.b);
+            while (L == 0);
+            s.nt = (L + kTile - 1) / kTile;
+        } else {
+            L = len_of(s.b);
+        }
+        s.first = 0;
+        return clip(s, L);
+    };
+    auto head_of = [&](const Seg& s) { return s.unit / parts; };
+    auto q0_of = [&](const Seg& s) { return (s.unit % parts) * kCols; };
+    auto steps_of = [&](const Seg& s) {  // step i of this warp: 16 tokens from token0 + 16 (warp + 4 i)
+        return s.token0 + kStep * warp < s.token1 ? (s.token1 - s.token0 - kStep * warp + kTile - 1) / kTile : 0;
+    };
+    // table entries of the 32 steps from i0 on, one a lane
+    auto entries = [&](const Seg& s, int i0) {
+        const int i = i0 + lane;
+        int blk = 0;
+        if (i < steps_of(s)) {
+            blk = a.tables[static_cast<size_t>(s.b) * a.max_blocks + ((s.token0 + kStep * (warp + kWarps * i)) >> a.block_shift)];
+            if (static_cast<unsigned>(blk) >= static_cast<unsigned>(a.num_blocks)) {
+                if (a.err) atomicOr(a.err, PKV_ERRBIT_BLOCK_ID);
+                blk = 0;  // (the flag marks the output as wrong)
+            }
+        }
+        return blk;
+    };
+    int win = 0, win_next = 0;
+    // asks for the rows of step i (one group of copies, an empty one behind the last step)
+    auto ask = [&](const Seg& s, int steps, int i) {
+        if (i < steps) {
+            if ((i & 31) == 0 && i > 0) win = win_next;
+            if ((i & 31) == 16) win_next = entries(s, (i & ~31) + 32);
+            const int blk = __shfl_sync(kAll, win, i & 31);
+            const int tok = s.token0 + kStep * (warp + kWarps * i);
+            const size_t row = ((static_cast<size_t>(blk) * a.num_kv_heads + head_of(s)) << a.block_shift) + (tok & bs_mask);
+            const uint8_t* k = a.k_codes + row * S::kRow;
+            const uint8_t* v = a.v_codes + row * S::kRow;
+            uint8_t* dst = ring + i % kDepth * St::kBytes;
+            constexpr int kAll16 = 16 * St::kChunks;  // 16-byte chunks of K
+#pragma unroll
+            for (int c0 = 0; c0 < kAll16; c0 += 32) {
+                const int c = c0 + lane;
+                cp_async16(dst + St::k_at(c / St::kChunks, c % St::kChunks), k + 16 * c, 16);
+                cp_async16(dst + St::v_at(c / St::kChunks, c % St::kChunks), v + 16 * c, 16);
+            }
+            if (lane < 8)
+                cp_async16(dst + St::kPairs + 16 * lane,
+                           reinterpret_cast<const uint8_t*>(lane < 4 ? a.k_params + row : a.v_params + row) + 16 * (lane & 3), 16);
+        }
+        cp_async_commit();
+    };
+    // parts of step i's rows to this lane's registers
+    auto take_k = [&](uint32_t (&k)[2][S::kKW], int i) {
+        const uint8_t* src = ring + i % kDepth * St::kBytes;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            if constexpr (S::kKW == 8) {
+                load_words<4>(k[r], src + St::k_at(g + 8 * r, t));
+                load_words<4>(k[r] + 4, src + St::k_at(g + 8 * r, 4 + t));
+            } else {
+                load_words<S::kKW>(k[r], src + St::k_at(g + 8 * r, 4 * S::kKW * t / 16) + 4 * S::kKW * t % 16);
+            }
+        }
+    };
+    auto take_v = [&](uint32_t (&v)[4][S::kVW], int i) {
+        const uint8_t* src = ring + i % kDepth * St::kBytes;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            load_words<S::kVW>(v[r], src + St::v_at(2 * t + (r & 1) + 8 * (r >> 1), 4 * S::kVW * g / 16) + 4 * S::kVW * g % 16);
+    };
+    auto q_row = [&](const Seg& s, int n) {  // of column 8 n + g (the first one's where there is no such head)
+        const int q0 = q0_of(s), r = 8 * n + g;
+        return a.q + (static_cast<size_t>(s.b) * a.num_q_heads + head_of(s) * gh + q0 + (r < min(kCols, gh - q0) ? r : 0)) * kDim;
+    };
 
+    Seg seg;
+    seg.b = found;
+    {
+        const int L = len_of(seg.b);
+        seg.nt = (L + kTile - 1) / kTile;
+        seg.unit = static_cast<int>((g0 - found_at) / (seg.nt + kUnitCost));
+        seg.at = found_at + static_cast<long long>(seg.unit) * (seg.nt + kUnitCost);
+        seg.first = static_cast<int>(g0 - seg.at > kUnitCost ? g0 - seg.at - kUnitCost : 0);
+        if (!clip(seg, L)) return;  // (nothing but a unit's own cost)
+    }
+    auto fetch_q = [&]() {  // the unit's query rows, on their way while the first rows of the cache are asked for
+#pragma unroll
+        for (int n = 0; n < kNT; ++n)
+            asm volatile("prefetch.global.L1 [%0];\n" ::"l"(q_row(seg, n) + S::k_dim(t, 0)));
+    };
+    fetch_q();
+    win = entries(seg, 0);
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) ask(seg, steps_of(seg), d);
+    bool has[2] = {false, false};
+    for (bool more = true; more;) {
         // ------------------------------------------------- queries -> operands
         uint32_t qf[kNT][S::kKSteps][2];
-        float fs[kNT][2], fz[kNT][2];  // of columns 2t, 2t + 1: factors of s (q . n) and of z
+        float fs[kNT][2], fz[kNT][2];  // of this lane's columns in the softmax: factors of s (q . n) and of z
 #pragma unroll
         for (int n = 0; n < kNT; ++n) {
             float x[S::kKW][32 / kBits];
             float top = 0.f, sum = 0.f;
-            const bool real = 8 * n + g < rows;
-            const __nv_bfloat16* qr =
-                a.q + (static_cast<size_t>(b) * a.num_q_heads + h * gh + q0 + (real ? 8 * n + g : 0)) * kDim;
+            const __nv_bfloat16* qr = q_row(seg, n);
+            const bool real = 8 * n + g < min(kCols, gh - q0_of(seg));
 #pragma unroll
             for (int w = 0; w < S::kKW; ++w) {
-                const uint32_t* src = reinterpret_cast<const uint32_t*>(qr + S::k_dim(t, w));
+                uint32_t qw[16 / kBits];
+                load_words<16 / kBits>(qw, reinterpret_cast<const uint8_t*>(qr + S::k_dim(t, w)));
 #pragma unroll
                 for (int j = 0; j < 32 / kBits; j += 2) {
-                    const uint32_t two = real ? src[j / 2] : 0u;
-                    x[w][j] = bf16_lo(two);
-                    x[w][j + 1] = bf16_hi(two);
+                    x[w][j] = real ? bf16_lo(qw[j / 2]) : 0.f;
+                    x[w][j + 1] = real ? bf16_hi(qw[j / 2]) : 0.f;
                     top = fmaxf(top, fmaxf(fabsf(x[w][j]), fabsf(x[w][j + 1])));
                 }
             }
@@ -232,59 +371,15 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? kCtasPerSm : 3) quant_dec
             const float f = a.scale_log2 * down * down2;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const float fj = __shfl_sync(kAll, f, (2 * t + j) * 4);
+                const int col = 2 * (kPair ? t & 1 : t) + j;
+                const float fj = __shfl_sync(kAll, f, col * 4);
                 fs[n][j] = fj * 16777216.f;
-                fz[n][j] = fj * __shfl_sync(kAll, sum, (2 * t + j) * 4);
+                fz[n][j] = fj * __shfl_sync(kAll, sum, col * 4);
             }
         }
 
         // ---------------------------------------------------------- the tokens
-        // step i of this warp: 16 tokens from token0 + 16 (warp + 4 i)
-        const int steps = token0 + kStep * warp < token1 ? (token1 - token0 - kStep * warp + kTile - 1) / kTile : 0;
-        const int32_t* table = a.tables + static_cast<size_t>(b) * a.max_blocks;
-        // table entries of 32 steps, one a lane, and of the next 32
-        auto entries = [&](int i0) {
-            const int i = i0 + lane;
-            int blk = 0;
-            if (i < steps) {
-                blk = table[(token0 + kStep * (warp + kWarps * i)) >> a.block_shift];
-                if (static_cast<unsigned>(blk) >= static_cast<unsigned>(a.num_blocks)) {
-                    if (a.err) atomicOr(a.err, PKV_ERRBIT_BLOCK_ID);
-                    blk = 0;  // (the flag marks the output as wrong)
-                }
-            }
-            return blk;
-        };
-        int win = entries(0), win_next = 0;
-        auto load = [&](Loaded<kBits, kDim>& x, int i) {
-            if (i >= steps) return;
-            if ((i & 31) == 0 && i > 0) win = win_next;
-            if ((i & 31) == 16) win_next = entries((i & ~31) + 32);
-            const int blk = __shfl_sync(kAll, win, i & 31);
-            const int tok = token0 + kStep * (warp + kWarps * i);
-            const size_t row = ((static_cast<size_t>(blk) * a.num_kv_heads + h) << a.block_shift) + (tok & bs_mask);
-            const uint8_t* k = a.k_codes + row * S::kRow;
-            const uint8_t* v = a.v_codes + row * S::kRow;
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const uint8_t* p = k + (g + 8 * r) * S::kRow;
-                if constexpr (S::kKW == 8) {
-                    load_words<4>(x.k[r], p + 16 * t);
-                    load_words<4>(x.k[r] + 4, p + 64 + 16 * t);
-                } else {
-                    load_words<S::kKW>(x.k[r], p + 4 * S::kKW * t);
-                }
-            }
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                load_words<S::kVW>(x.v[r], v + (2 * t + (r & 1) + 8 * (r >> 1)) * S::kRow + 4 * S::kVW * g);
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                load_words<1>(&x.kp[r], reinterpret_cast<const uint8_t*>(a.k_params + row + g + 8 * r));
-                load_words<1>(&x.vp[r], reinterpret_cast<const uint8_t*>(a.v_params + row + g + 8 * r));
-            }
-        };
-
+        const int steps = steps_of(seg);
         float o[kNT][S::kKSteps][4];
         float mw[kNT][2], m[kNT][2], l[kNT][2], zs[kNT][2];  // bases of O, and of l and zs
 #pragma unroll
@@ -294,65 +389,79 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? kCtasPerSm : 3) quant_dec
 #pragma unroll
                 for (int j = 0; j < 4; ++j) o[n][i][j] = 0.f;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) mw[n][j] = m[n][j] = -INFINITY, l[n][j] = zs[n][j] = 0.f;
+            for (int j = 0; j < 2; ++j) mw[n][j] = m[n][j] = kNone, l[n][j] = zs[n][j] = 0.f;
         }
 
-        auto use = [&](const Loaded<kBits, kDim>& x, int i) {
-            const int left = token1 - (token0 + kStep * (warp + kWarps * i));  // tokens of the step that are there
-            // S^T
-            float sc[kNT][2][4] = {};
+        // Steps i .. i + kNS - 1.  With at most four heads two steps share the softmax: columns 4 to 7 of the products
+        // are nobody's, so lanes with t >= 2 take the second step's scores of the first four.
+        auto use = [&](int i, auto whole_steps) {
+            constexpr bool kWhole = decltype(whole_steps)::value;  // every token is there
+            float sc[kNS][kNT][2][4] = {};
 #pragma unroll
-            for (int ks = 0; ks < S::kKSteps; ++ks) {
-                uint32_t a0, a1, a2, a3;
-                if constexpr (kBits == 4) {
-                    const uint32_t w0 = x.k[0][ks / 2] >> (8 * (ks & 1)), w1 = x.k[1][ks / 2] >> (8 * (ks & 1));
-                    a0 = w0 & 0x000F000Fu, a2 = w0 & 0x00F000F0u;
-                    a1 = w1 & 0x000F000Fu, a3 = w1 & 0x00F000F0u;
-                } else {
-                    a0 = x.k[0][ks] & 0x00FF00FFu, a2 = (x.k[0][ks] >> 8) & 0x00FF00FFu;
-                    a1 = x.k[1][ks] & 0x00FF00FFu, a3 = (x.k[1][ks] >> 8) & 0x00FF00FFu;
+            for (int e = 0; e < kNS; ++e) {
+                uint32_t xk[2][S::kKW];
+                take_k(xk, i + e);
+#pragma unroll
+                for (int ks = 0; ks < S::kKSteps; ++ks) {
+                    uint32_t a0, a1, a2, a3;
+                    if constexpr (kBits == 4) {
+                        const uint32_t w0 = xk[0][ks / 2] >> (8 * (ks & 1)), w1 = xk[1][ks / 2] >> (8 * (ks & 1));
+                        a0 = w0 & 0x000F000Fu, a2 = w0 & 0x00F000F0u;
+                        a1 = w1 & 0x000F000Fu, a3 = w1 & 0x00F000F0u;
+                    } else {
+                        a0 = xk[0][ks] & 0x00FF00FFu, a2 = (xk[0][ks] >> 8) & 0x00FF00FFu;
+                        a1 = xk[1][ks] & 0x00FF00FFu, a3 = (xk[1][ks] >> 8) & 0x00FF00FFu;
+                    }
+#pragma unroll
+                    for (int n = 0; n < kNT; ++n) mma16(sc[e][n][ks & 1], a0, a1, a2, a3, qf[n][ks][0], qf[n][ks][1]);
                 }
-#pragma unroll
-                for (int n = 0; n < kNT; ++n) mma16(sc[n][ks & 1], a0, a1, a2, a3, qf[n][ks][0], qf[n][ks][1]);
             }
-            // exponents of the weights: rows g (r = 0) and g + 8 (r = 1)
+            // exponents of the weights: rows g (r = 0) and g + 8 (r = 1) of this lane's step
+            const int my = i + (kPair ? t >> 1 : 0);
+            const int left = kWhole ? kStep : seg.token1 - (seg.token0 + kStep * (warp + kWarps * my));  // tokens that are there
+            const uint32_t* pairs = reinterpret_cast<const uint32_t*>(ring + my % kDepth * St::kBytes + St::kPairs);
             float ks_[2], kz[2], lg[2], vz[2];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 const bool there = g + 8 * r < left;
-                ks_[r] = bf16_lo(x.kp[r]), kz[r] = bf16_hi(x.kp[r]);
-                lg[r] = there ? lg2f(bf16_lo(x.vp[r])) : 0.f;
-                vz[r] = there ? bf16_hi(x.vp[r]) : 0.f;
+                const uint32_t kp = pairs[g + 8 * r], vp = pairs[16 + g + 8 * r];
+                ks_[r] = bf16_lo(kp), kz[r] = bf16_hi(kp);
+                lg[r] = there ? lg2f(bf16_lo(vp)) : 0.f;
+                vz[r] = there ? bf16_hi(vp) : 0.f;
             }
-            uint32_t pb[kNT][2];
+            uint32_t pb[kNS][kNT][2];
 #pragma unroll
             for (int n = 0; n < kNT; ++n) {
                 float y[2][2], e[2][2];
                 bool grown = false;
 #pragma unroll
-                for (int r = 0; r < 2; ++r)
+                for (int j = 0; j < 2; ++j) {
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const float dot = sc[n][0][2 * r + j] + sc[n][1][2 * r + j];
+                    for (int r = 0; r < 2; ++r) {
+                        float dot = sc[0][n][0][2 * r + j] + sc[0][n][1][2 * r + j];
+                        if constexpr (kPair) {
+                            const float other = __shfl_xor_sync(kAll, sc[1][n][0][2 * r + j] + sc[1][n][1][2 * r + j], 2);
+                            dot = t < 2 ? dot : other;
+                        }
                         const float x_ = fmaf(ks_[r], dot * fs[n][j], kz[r] * fz[n][j]);
                         y[r][j] = g + 8 * r < left ? x_ : -INFINITY;
                         e[r][j] = y[r][j] + lg[r];
-                        grown |= y[r][j] > m[n][j] + 8.f || e[r][j] > mw[n][j] + 8.f;
                     }
+                    grown |= fmaxf(y[0][j], y[1][j]) > m[n][j] + 8.f || fmaxf(e[0][j], e[1][j]) > mw[n][j] + 8.f;
+                }
                 // the maxima move only when an exponent passes one by 8 (weights stay below 2^8)
                 if (__any_sync(kAll, grown)) {
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         float top = fmaxf(y[0][j], y[1][j]), topw = fmaxf(e[0][j], e[1][j]);
 #pragma unroll
-                        for (int d = 4; d < 32; d <<= 1) {
+                        for (int d = kPair ? 2 : 4; d < 32; d <<= 1) {
                             top = fmaxf(top, __shfl_xor_sync(kAll, top, d));
                             topw = fmaxf(topw, __shfl_xor_sync(kAll, topw, d));
                         }
                         top = fmaxf(top, m[n][j]);
                         topw = fmaxf(topw, mw[n][j]);
-                        const float f = m[n][j] == -INFINITY ? 0.f : ex2f(m[n][j] - top);
-                        const float fw = mw[n][j] == -INFINITY ? 0.f : ex2f(mw[n][j] - topw);
+                        const float f = ex2f(m[n][j] - top), fw = ex2f(mw[n][j] - topw);
                         m[n][j] = top;
                         mw[n][j] = topw;
                         l[n][j] *= f;
@@ -367,67 +476,68 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? kCtasPerSm : 3) quant_dec
                 float w[2][2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const float base = m[n][j] == -INFINITY ? 0.f : m[n][j], basew = mw[n][j] == -INFINITY ? 0.f : mw[n][j];
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
-                        w[r][j] = ex2f(e[r][j] - basew);
-                        const float p = ex2f(y[r][j] - base);
+                        w[r][j] = ex2f(e[r][j] - mw[n][j]);
+                        const float p = ex2f(y[r][j] - m[n][j]);
                         l[n][j] += p;
                         zs[n][j] = fmaf(p, vz[r], zs[n][j]);
                     }
                 }
 #pragma unroll
-                for (int r = 0; r < 2; ++r) pb[n][r] = turn(half2_of(w[r][0], w[r][1]));
+                for (int r = 0; r < 2; ++r) {
+                    pb[0][n][r] = turn(half2_of(w[r][0], w[r][1]));
+                    if constexpr (kPair) pb[1][n][r] = __shfl_xor_sync(kAll, pb[0][n][r], 16);  // (rows 4 to 7 come to 0 to 3)
+                }
             }
             // O^T
 #pragma unroll
-            for (int wi = 0; wi < S::kVW; ++wi) {
+            for (int e = 0; e < kNS; ++e) {
+                if (e > 0 && !kWhole && i + e >= steps) break;
+                uint32_t xv[4][S::kVW];
+                take_v(xv, i + e);
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    const uint32_t sel = hf ? 0x7632u : 0x5410u;
-                    const uint32_t x0 = __byte_perm(x.v[0][wi], x.v[1][wi], sel), x1 = __byte_perm(x.v[2][wi], x.v[3][wi], sel);
-                    if constexpr (kBits == 4) {
+                for (int wi = 0; wi < S::kVW; ++wi) {
 #pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            const uint32_t y0 = x0 >> (8 * u), y1 = x1 >> (8 * u);
+                    for (int hf = 0; hf < 2; ++hf) {
+                        const uint32_t sel = hf ? 0x7632u : 0x5410u;
+                        const uint32_t x0 = __byte_perm(xv[0][wi], xv[1][wi], sel), x1 = __byte_perm(xv[2][wi], xv[3][wi], sel);
+                        if constexpr (kBits == 4) {
+#pragma unroll
+                            for (int u = 0; u < 2; ++u) {
+                                const uint32_t y0 = x0 >> (8 * u), y1 = x1 >> (8 * u);
+#pragma unroll
+                                for (int n = 0; n < kNT; ++n)
+                                    mma16(o[n][4 * wi + 2 * hf + u], y0 & 0x000F000Fu, y0 & 0x00F000F0u, y1 & 0x000F000Fu,
+                                          y1 & 0x00F000F0u, pb[e][n][0], pb[e][n][1]);
+                            }
+                        } else {
 #pragma unroll
                             for (int n = 0; n < kNT; ++n)
-                                mma16(o[n][4 * wi + 2 * hf + u], y0 & 0x000F000Fu, y0 & 0x00F000F0u, y1 & 0x000F000Fu,
-                                      y1 & 0x00F000F0u, pb[n][0], pb[n][1]);
+                                mma16(o[n][2 * wi + hf], x0 & 0x00FF00FFu, (x0 >> 8) & 0x00FF00FFu, x1 & 0x00FF00FFu,
+                                      (x1 >> 8) & 0x00FF00FFu, pb[e][n][0], pb[e][n][1]);
                         }
-                    } else {
-#pragma unroll
-                        for (int n = 0; n < kNT; ++n)
-                            mma16(o[n][2 * wi + hf], x0 & 0x00FF00FFu, (x0 >> 8) & 0x00FF00FFu, x1 & 0x00FF00FFu,
-                                  (x1 >> 8) & 0x00FF00FFu, pb[n][0], pb[n][1]);
                     }
                 }
             }
         };
 
-        if constexpr (kBits == 4) {  // two steps under way
-            Loaded<kBits, kDim> s0, s1;
-            load(s0, 0);
-            load(s1, 1);
-            for (int i = 0; i < steps; i += 2) {
-                use(s0, i);
-                load(s0, i + 2);
-                if (i + 1 < steps) {
-                    use(s1, i + 1);
-                    load(s1, i + 3);
-                }
-            }
-        } else {
-            Loaded<kBits, kDim> s0, s1;
-            load(s0, 0);
-            for (int i = 0; i < steps; i += 2) {
-                load(s1, i + 1);
-                use(s0, i);
-                if (i + 1 < steps) {
-                    load(s0, i + 2);
-                    use(s1, i + 1);
-                }
-            }
+        for (int i = 0; i < steps; i += kNS) {
+            cp_async_wait<kDepth - kNS>();
+            __syncwarp();
+            // (only a sequence's last tokens lie in steps that are not whole, or have no second one)
+            if (i + kNS < steps) use(i, std::true_type{});
+            else use(i, std::false_type{});
+            __syncwarp();  // (the rows may be written over)
+#pragma unroll
+            for (int e = 0; e < kNS; ++e) ask(seg, steps, i + e + kDepth);
+        }
+        // the next unit's first rows are under way from here on
+        const Seg done = seg;
+        more = next(seg);
+        if (more) {
+            fetch_q();
+            win = entries(seg, 0);
         }
 
         // ------------------------------------------------ the warps' sums meet
@@ -436,13 +546,14 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? kCtasPerSm : 3) quant_dec
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
 #pragma unroll
-                for (int d = 4; d < 32; d <<= 1) {
+                for (int d = kPair ? 2 : 4; d < 32; d <<= 1) {
                     l[n][j] += __shfl_xor_sync(kAll, l[n][j], d);
                     zs[n][j] += __shfl_xor_sync(kAll, zs[n][j], d);
                 }
                 const int col = 8 * n + 2 * t + j;
+                if (kPair && t >= 2) continue;
                 // O in the base of l, the codes' 2^24 (and the upper nibbles' 2^-4) taken out
-                const float up = 16777216.f * (mw[n][j] == -INFINITY ? 0.f : ex2f(mw[n][j] - m[n][j]));
+                const float up = 16777216.f * ex2f(mw[n][j] - m[n][j]);
                 if (g == 0) {
                     sm[warp][col] = m[n][j];
                     sl[warp][col] = l[n][j];
@@ -455,94 +566,112 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? kCtasPerSm : 3) quant_dec
                     so[warp][col][(2 * i + 1) * 8 + g] = o[n][i][2 + j] * (kBits == 4 ? 0.0625f * up : up);
                 }
             }
+        if (more) {
+#pragma unroll
+            for (int d = 0; d < kDepth; ++d) ask(seg, steps_of(seg), d);
+        }
         __syncthreads();
-        const bool whole = first == 0 && end == nt;
-        const int slot = 2 * static_cast<int>(c) + (at == g0 ? 0 : 1);
-        const size_t out0 = static_cast<size_t>(b) * a.num_q_heads + h * gh + q0;
-        for (int i = tid; i < rows * kDim; i += kThreads) {
-            const int r = i / kDim, d = i % kDim, at_ = (d % (kDim / 8)) * 8 + d / (kDim / 8);
-            float M = sm[0][r];
+        const bool whole = done.first == 0 && done.end == done.nt;
+        const int place = g0 >= done.at + kUnitCost ? 0 : 1, rows = min(kCols, gh - q0_of(done));
+        const size_t slot = 2 * static_cast<size_t>(c) + place;
+        const size_t out0 = static_cast<size_t>(done.b) * a.num_q_heads + head_of(done) * gh + q0_of(done);
+        // lane (w, r): what the sums of warp w weigh in column r, by shuffles over the warps' lanes
+        constexpr int kPerPass = kThreads / kDim;  // rows that the CTA's threads write at once
+        const int d = tid % kDim, at_ = (d % (kDim / 8)) * 8 + d / (kDim / 8);
 #pragma unroll
-            for (int w = 1; w < kWarps; ++w) M = fmaxf(M, sm[w][r]);
-            float lw = 0.f, ow = 0.f;
+        for (int n = 0; n < kNT; ++n) {
+            const int w = lane >> 3, r8 = 8 * n + (lane & 7);
+            const float mr = sm[w][r8], lr = sl[w][r8];
+            float M = fmaxf(mr, __shfl_xor_sync(kAll, mr, 8));
+            M = fmaxf(M, __shfl_xor_sync(kAll, M, 16));
+            const float f = ex2f(mr - M);
+            float lw = f * lr, zw = f * sz[w][r8];
+            lw += __shfl_xor_sync(kAll, lw, 8);
+            lw += __shfl_xor_sync(kAll, lw, 16);
+            zw += __shfl_xor_sync(kAll, zw, 8);
+            zw += __shfl_xor_sync(kAll, zw, 16);
+            const float inv = 1.f / lw;
+            if (!whole && tid < 8 && r8 < rows)
+                reinterpret_cast<float2*>(a.part_ml)[slot * kCols + r8] = make_float2(M, lw);
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float f = sm[w][r] == -INFINITY && sl[w][r] == 0.f ? 0.f : ex2f(sm[w][r] - (M == -INFINITY ? 0.f : M));
-                lw += f * sl[w][r];
-                ow += f * (so[w][r][at_] + sz[w][r]);
-            }
-            if (whole) {
-                a.out[(out0 + r) * kDim + d] = __float2bfloat16_rn(__fdiv_rn(ow, lw));
-            } else {
-                a.part_o[(static_cast<size_t>(slot) * kCols + r) * kDim + d] = ow;
-                if (d == 0) {
-                    a.part_ml[2 * (static_cast<size_t>(slot) * kCols + r)] = M;
-                    a.part_ml[2 * (static_cast<size_t>(slot) * kCols + r) + 1] = lw;
+            for (int k = 0; k < (kPair ? 4 : 8); k += kPerPass) {
+                const int r = k + tid / kDim;  // (the same in a warp)
+                float y = __shfl_sync(kAll, zw, r);
+#pragma unroll
+                for (int v = 0; v < kWarps; ++v) y = fmaf(__shfl_sync(kAll, f, 8 * v + r), so[v][8 * n + r][at_], y);
+                const float i = __shfl_sync(kAll, inv, r);
+                if (8 * n + r < rows) {
+                    if (whole) a.out[(out0 + 8 * n + r) * kDim + d] = __float2bfloat16_rn(y * i);
+                    else a.part_o[(slot * kCols + 8 * n + r) * kDim + d] = y;
                 }
             }
         }
+        __syncthreads();  // (the shared sums are read, the piece is written)
         if (!whole) {
-            // the unit's pieces: CTAs c0 .. c1, each one piece
-            const long long c0 = ((unit_at + 1) * P - 1) / total, c1 = ((unit_at + nt) * P - 1) / total;
-            int* counter = a.counters + static_cast<size_t>(b) * per_seq + unit;
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) {
-                const int pieces = static_cast<int>(c1 - c0 + 1);
-                last_flag = count_up(counter) == pieces - 1;
-                if (last_flag) *counter = 0;
-            }
-            __syncthreads();
-            if (last_flag) {
+            has[place] = true;
+            if (tid == 0) {  // count the piece; who counts the last one joins them, when its own range is done
+                split[place] = done;
                 __threadfence();
-                const int extra = unit_at > c0 * total / P ? 1 : 0;  // the first piece does not begin its CTA's range
-                const int n = static_cast<int>(c1 - c0 + 1);
-                auto slot_of = [&](int i) { return static_cast<size_t>(2 * (c0 + i) + (i == 0 ? extra : 0)); };
-                for (int r = warp; r < rows; r += kWarps) {
-                    float M = -INFINITY;
-                    for (int i = lane; i < n; i += 32) M = fmaxf(M, __ldcg(a.part_ml + 2 * (slot_of(i) * kCols + r)));
-                    M = warp_max(M);
-                    const float base = M == -INFINITY ? 0.f : M;
-                    constexpr int kPer = kDim / 32;
-                    float acc[kPer] = {}, lw = 0.f;
-                    for (int i0 = 0; i0 < n; i0 += 32) {
-                        float f = 0.f, lf = 0.f;
-                        if (i0 + lane < n) {
-                            const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + slot_of(i0 + lane) * kCols + r);
-                            f = ex2f(ml.x - base);
-                            lf = f * ml.y;
-                        }
-                        lw += warp_sum(lf);
-                        const int k1 = min(32, n - i0);
-#pragma unroll 8
-                        for (int k = 0; k < k1; ++k) {
-                            const float fk = __shfl_sync(kAll, f, k);
-                            const float* src = a.part_o + (slot_of(i0 + k) * kCols + r) * kDim + kPer * lane;
-                            if constexpr (kPer == 4) {
-                                const float4 y = __ldcg(reinterpret_cast<const float4*>(src));
-                                acc[0] += fk * y.x, acc[1] += fk * y.y, acc[2] += fk * y.z, acc[3] += fk * y.w;
-                            } else {
-                                const float2 y = __ldcg(reinterpret_cast<const float2*>(src));
-                                acc[0] += fk * y.x, acc[1] += fk * y.y;
-                            }
+                const long long c0 = ((done.at + kUnitCost + 1) * P - 1) / total, c1 = ((done.at + kUnitCost + done.nt) * P - 1) / total;
+                int* counter = a.counters + static_cast<size_t>(done.b) * per_seq + done.unit;
+                last_flag[place] = count_up(counter) == static_cast<int>(c1 - c0);
+                if (last_flag[place]) *counter = 0;
+            }
+        }
+    }
+    if (!has[0] && !has[1]) return;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        if (!has[k] || !last_flag[k]) continue;
+        __threadfence();
+        const Seg u = split[k];
+        // the unit's pieces: CTAs c0 .. c0 + n - 1, each one piece, the first one's at its range's start or end
+        const long long c0 = ((u.at + kUnitCost + 1) * P - 1) / total, c1 = ((u.at + kUnitCost + u.nt) * P - 1) / total;
+        const int n = static_cast<int>(c1 - c0 + 1), extra = c0 * total / P >= u.at + kUnitCost ? 0 : 1;
+        const int rows = min(kCols, gh - q0_of(u));
+        const size_t out0 = static_cast<size_t>(u.b) * a.num_q_heads + head_of(u) * gh + q0_of(u);
+        auto slot_of = [&](int i) { return static_cast<size_t>(2 * (c0 + i) + (i == 0 ? extra : 0)); };
+        for (int r = warp; r < rows; r += kWarps) {
+            float M = kNone;
+            for (int i = lane; i < n; i += 32) M = fmaxf(M, __ldcg(a.part_ml + 2 * (slot_of(i) * kCols + r)));
+            M = warp_max(M);
+            constexpr int kPer = kDim / 32;
+            float acc[kPer] = {}, lw = 0.f;
+            for (int i0 = 0; i0 < n; i0 += 32) {
+                float f = 0.f, lf = 0.f;
+                if (i0 + lane < n) {
+                    const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + slot_of(i0 + lane) * kCols + r);
+                    f = ex2f(ml.x - M);
+                    lf = f * ml.y;
+                }
+                lw += warp_sum(lf);
+                const int k1 = min(32, n - i0);
+                for (int j0 = 0; j0 < k1; j0 += 16) {  // 16 pieces' rows in one round trip
+                    float y[16][kPer];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const float* src = a.part_o + (slot_of(i0 + min(j0 + j, k1 - 1)) * kCols + r) * kDim + kPer * lane;
+                        if constexpr (kPer == 4) {
+                            const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
+                            y[j][0] = v.x, y[j][1] = v.y, y[j][2] = v.z, y[j][3] = v.w;
+                        } else {
+                            const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
+                            y[j][0] = v.x, y[j][1] = v.y;
                         }
                     }
-                    uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + (out0 + r) * kDim + kPer * lane);
 #pragma unroll
-                    for (int k = 0; k < kPer; k += 2)
-                        dst[k / 2] = pack_bf16x2_rn(__fdiv_rn(acc[k], lw), __fdiv_rn(acc[k + 1], lw));
+                    for (int j = 0; j < 16; ++j) {
+                        const float fj = __shfl_sync(kAll, f, (j0 + j) & 31);
+#pragma unroll
+                        for (int k = 0; k < kPer; ++k)
+                            if (j0 + j < k1) acc[k] = fmaf(fj, y[j][k], acc[k]);
+                    }
                 }
             }
-        }
-        __syncthreads();  // (the shared sums are read)
-        at = unit_at + end;
-        if (at < g1 && unit == per_seq - 1) {  // the next sequence that has tokens
-            seq_at += static_cast<long long>(nt) * per_seq;
-            do {
-                ++b;
-                L = len_of(b);
-            } while (L == 0);
-            nt = (L + kTile - 1) / kTile;
+            uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + (out0 + r) * kDim + kPer * lane);
+#pragma unroll
+            for (int j = 0; j < kPer; j += 2) dst[j / 2] = pack_bf16x2_rn(__fdiv_rn(acc[j], lw), __fdiv_rn(acc[j + 1], lw));
         }
     }
 }
@@ -565,19 +694,31 @@ size_t quant_decode_workspace(int num_seqs, int num_q_heads, int num_kv_heads, i
     return counters + ml + static_cast<size_t>(kMaxCtas) * 2 * cols * head_dim * sizeof(float);
 }
 
+template <int kBits, int kDim, int kNT, bool kPair>
+static cudaError_t launch(const QuantDecodeArgs& a, cudaStream_t stream) {
+    constexpr int kSumCols = kPair ? 4 : 8 * kNT;
+    constexpr int smem = static_cast<int>(sizeof(float)) * kWarps * kSumCols * (kDim + 4) +
+                         kWarps * depth_of(kBits, kDim, kNT, kPair) * Stage<kBits, kDim>::kBytes;
+    static_assert(ctas_per_sm(kBits, kDim, kNT, kPair) * (smem + 3072) <= 228 * 1024, "shared memory per SM");
+    const auto kernel = quant_decode_kernel<kBits, kDim, kNT, kPair>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess)  // (all of an SM's CTAs have to fit)
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    if (e != cudaSuccess) return e;
+    const int sms = num_sms() > 0 ? num_sms() : 148, ctas = sms * ctas_per_sm(kBits, kDim, kNT, kPair);
+    return launch_dependent(kernel, dim3(ctas < kMaxCtas ? ctas : kMaxCtas), dim3(kThreads), smem, stream, a);
+}
+
 cudaError_t launch_quant_decode(int bits, int head_dim, const QuantDecodeArgs& a, cudaStream_t stream) {
-    const int cols = columns(a.num_q_heads / a.num_kv_heads);
-    const int sms = num_sms() > 0 ? num_sms() : 148;
-    const int ctas = min(kMaxCtas, sms * (cols == 8 ? kCtasPerSm : 3));
-    auto run = [&](auto kernel) {
-        return launch_dependent(kernel, dim3(ctas), dim3(kThreads), 0, stream, a);
+    const int gh = a.num_q_heads / a.num_kv_heads;
+    auto pick = [&](auto four, auto eight, auto sixteen) {
+        return gh <= 4 ? four(a, stream) : columns(gh) == 8 ? eight(a, stream) : sixteen(a, stream);
     };
-    auto pick = [&](auto narrow, auto wide) { return cols == 8 ? run(narrow) : run(wide); };
     if (bits == 4)
-        return head_dim == 64 ? pick(quant_decode_kernel<4, 64, 1>, quant_decode_kernel<4, 64, 2>)
-                              : pick(quant_decode_kernel<4, 128, 1>, quant_decode_kernel<4, 128, 2>);
-    return head_dim == 64 ? pick(quant_decode_kernel<8, 64, 1>, quant_decode_kernel<8, 64, 2>)
-                          : pick(quant_decode_kernel<8, 128, 1>, quant_decode_kernel<8, 128, 2>);
+        return head_dim == 64 ? pick(launch<4, 64, 1, true>, launch<4, 64, 1, false>, launch<4, 64, 2, false>)
+                              : pick(launch<4, 128, 1, true>, launch<4, 128, 1, false>, launch<4, 128, 2, false>);
+    return head_dim == 64 ? pick(launch<8, 64, 1, true>, launch<8, 64, 1, false>, launch<8, 64, 2, false>)
+                          : pick(launch<8, 128, 1, true>, launch<8, 128, 1, false>, launch<8, 128, 2, false>);
 }
 
 }  // namespace pkv
