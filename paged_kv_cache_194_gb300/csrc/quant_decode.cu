@@ -41,17 +41,19 @@ namespace {
 
 constexpr int kThreads = 128, kWarps = 4;
 constexpr int kTile = 64, kStep = 16;
-constexpr int kUnitCost = 2;
+constexpr int kUnitCost = 4;
 constexpr int kMaxCtas = 1024;
 // CTAs per SM, and steps whose rows are under way in a warp (pair: taken two at a time).  HBM answers after 2.5 to 3 us
 // under load, so an SM wants 130 to 150 KB on their way.
 constexpr int ctas_per_sm(int bits, int dim, int nt, bool pair) {
+    (void)bits, (void)pair;
     if (dim == 64) return nt == 1 ? 4 : 3;
-    return nt == 2 ? 2 : pair ? (bits == 4 ? 3 : 2) : (bits == 4 ? 4 : 3);
+    return nt == 2 ? 2 : bits == 4 ? 3 : 2;
 }
 constexpr int depth_of(int bits, int dim, int nt, bool pair) {
-    if (dim == 64) return bits == 4 ? 8 : (nt == 1 ? 4 : 6);
-    return nt == 2 ? (bits == 4 ? 8 : 4) : pair ? 6 : (bits == 4 ? 4 : 3);
+    (void)pair;
+    if (dim == 64) return bits == 4 ? 10 : 6;
+    return nt == 2 ? (bits == 4 ? 12 : 6) : bits == 4 ? 6 : 6;
 }
 constexpr float kNone = -1e30f;  // a maximum of nothing
 constexpr unsigned kAll = 0xFFFFFFFFu;
@@ -93,6 +95,14 @@ __device__ __forceinline__ void load_words(uint32_t* w, const uint8_t* p) {
     } else {
         const uint4 v = *reinterpret_cast<const uint4*>(p);
         w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    }
+}
+template <int kWords>
+__device__ __forceinline__ void load_global(uint32_t* w, const void* p) {
+    if constexpr (kWords == 2) {
+        asm volatile("ld.global.v2.b32 {%0,%1}, [%2];\n" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
+    } else {
+        asm volatile("ld.global.v4.b32 {%0,%1,%2,%3}, [%4];\n" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(p));
     }
 }
 __device__ __forceinline__ int count_up(int* p) {
@@ -146,10 +156,15 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kBits, kDim, kNT, kPair)
     constexpr int kDepth = depth_of(kBits, kDim, kNT, kPair), kNS = kPair ? 2 : 1;  // (steps at a time)
     using St = Stage<kBits, kDim>;
     extern __shared__ __align__(16) uint8_t dynamic[];
-    auto so = reinterpret_cast<float (*)[kSumCols][kPitch]>(dynamic);  // [kWarps]
-    uint8_t* ring = dynamic + sizeof(float) * kWarps * kSumCols * kPitch + (threadIdx.x >> 5) * (kDepth * St::kBytes);
+    constexpr int kRing = kDepth * St::kBytes;
+    // a warp's sums for the others, over the last places of its ring: so(w)[column][kPitch]
+    constexpr int kSumBytes = static_cast<int>(sizeof(float)) * kSumCols * kPitch;
+    constexpr int kSumPlaces = (kSumBytes + St::kBytes - 1) / St::kBytes, kEarly = kDepth - kSumPlaces;
+    static_assert(kEarly >= kNS);
+    uint8_t* ring = dynamic + (threadIdx.x >> 5) * kRing;
+    auto so = [&](int w) { return reinterpret_cast<float (*)[kPitch]>(dynamic + w * kRing + kEarly * St::kBytes); };
     __shared__ float sm[kWarps][kCols], sl[kWarps][kCols], sz[kWarps][kCols];
-    __shared__ long long scan[kThreads];
+    __shared__ long long scan[kWarps];
     __shared__ int last_flag[2], found;
     __shared__ long long found_at;
     __shared__ Seg split[2];  // this CTA's pieces of units that others share: at its range's start, and at its end
@@ -181,21 +196,26 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kBits, kDim, kNT, kPair)
     long long mine = 0;
     for (int i = 0; i < run; ++i)
         if (tid * run + i < a.num_seqs) mine += cost_of(tid * run + i);
-    scan[tid] = mine;
-    __syncthreads();
-    for (int d = 1; d < kThreads; d <<= 1) {
-        const long long x = tid >= d ? scan[tid - d] : 0;
-        __syncthreads();
-        scan[tid] += x;
-        __syncthreads();
+    long long incl = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long x = __shfl_up_sync(kAll, incl, d);
+        if (lane >= d) incl += x;
     }
-    const long long total = scan[kThreads - 1];
+    if (lane == 31) scan[warp] = incl;
+    __syncthreads();
+    long long total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) incl += scan[w];
+        total += scan[w];
+    }
     const long long P = total < static_cast<long long>(gridDim.x) ? total : static_cast<long long>(gridDim.x);
     const long long c = blockIdx.x;
     if (c >= P) return;
     const long long g0 = c * total / P, g1 = (c + 1) * total / P;
-    if (g0 >= scan[tid] - mine && g0 < scan[tid]) {
-        long long at = scan[tid] - mine;
+    if (g0 >= incl - mine && g0 < incl) {
+        long long at = incl - mine;
         int b = tid * run;
         for (;; ++b) {
             const long long n = cost_of(b);
@@ -307,12 +327,18 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kBits, kDim, kNT, kPair)
         seg.first = static_cast<int>(g0 - seg.at > kUnitCost ? g0 - seg.at - kUnitCost : 0);
         if (!clip(seg, L)) return;  // (nothing but a unit's own cost)
     }
-    auto fetch_q = [&]() {  // the unit's query rows, on their way while the first rows of the cache are asked for
+    // this lane's share of the unit's query rows, BF16 pairs: asked for before the cache's rows, behind whose flood they
+    // would come 3 us later
+    uint32_t qw[kNT][S::kKW][16 / kBits];
+    auto load_q = [&]() {
 #pragma unroll
-        for (int n = 0; n < kNT; ++n)
-            asm volatile("prefetch.global.L1 [%0];\n" ::"l"(q_row(seg, n) + S::k_dim(t, 0)));
+        for (int n = 0; n < kNT; ++n) {
+            const __nv_bfloat16* qr = q_row(seg, n);
+#pragma unroll
+            for (int w = 0; w < S::kKW; ++w) load_global<16 / kBits>(qw[n][w], qr + S::k_dim(t, w));
+        }
     };
-    fetch_q();
+    load_q();
     win = entries(seg, 0);
 #pragma unroll
     for (int d = 0; d < kDepth; ++d) ask(seg, steps_of(seg), d);
@@ -325,16 +351,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kBits, kDim, kNT, kPair)
         for (int n = 0; n < kNT; ++n) {
             float x[S::kKW][32 / kBits];
             float top = 0.f, sum = 0.f;
-            const __nv_bfloat16* qr = q_row(seg, n);
             const bool real = 8 * n + g < min(kCols, gh - q0_of(seg));
 #pragma unroll
             for (int w = 0; w < S::kKW; ++w) {
-                uint32_t qw[16 / kBits];
-                load_words<16 / kBits>(qw, reinterpret_cast<const uint8_t*>(qr + S::k_dim(t, w)));
 #pragma unroll
                 for (int j = 0; j < 32 / kBits; j += 2) {
-                    x[w][j] = real ? bf16_lo(qw[j / 2]) : 0.f;
-                    x[w][j + 1] = real ? bf16_hi(qw[j / 2]) : 0.f;
+                    x[w][j] = real ? bf16_lo(qw[n][w][j / 2]) : 0.f;
+                    x[w][j + 1] = real ? bf16_hi(qw[n][w][j / 2]) : 0.f;
                     top = fmaxf(top, fmaxf(fabsf(x[w][j]), fabsf(x[w][j + 1])));
                 }
             }
@@ -536,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kBits, kDim, kNT, kPair)
         const Seg done = seg;
         more = next(seg);
         if (more) {
-            fetch_q();
+            load_q();
             win = entries(seg, 0);
         }
 
@@ -562,15 +585,15 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kBits, kDim, kNT, kPair)
                 // element (dimension g (kDim / 8) + x) of column col at [x][g]: all lanes in different banks
 #pragma unroll
                 for (int i = 0; i < S::kKSteps; ++i) {
-                    so[warp][col][(2 * i) * 8 + g] = o[n][i][j] * up;
-                    so[warp][col][(2 * i + 1) * 8 + g] = o[n][i][2 + j] * (kBits == 4 ? 0.0625f * up : up);
+                    so(warp)[col][(2 * i) * 8 + g] = o[n][i][j] * up;
+                    so(warp)[col][(2 * i + 1) * 8 + g] = o[n][i][2 + j] * (kBits == 4 ? 0.0625f * up : up);
                 }
             }
+        __syncthreads();
         if (more) {
 #pragma unroll
-            for (int d = 0; d < kDepth; ++d) ask(seg, steps_of(seg), d);
+            for (int d = 0; d < kEarly; ++d) ask(seg, steps_of(seg), d);
         }
-        __syncthreads();
         const bool whole = done.first == 0 && done.end == done.nt;
         const int place = g0 >= done.at + kUnitCost ? 0 : 1, rows = min(kCols, gh - q0_of(done));
         const size_t slot = 2 * static_cast<size_t>(c) + place;
@@ -598,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kBits, kDim, kNT, kPair)
                 const int r = k + tid / kDim;  // (the same in a warp)
                 float y = __shfl_sync(kAll, zw, r);
 #pragma unroll
-                for (int v = 0; v < kWarps; ++v) y = fmaf(__shfl_sync(kAll, f, 8 * v + r), so[v][8 * n + r][at_], y);
+                for (int v = 0; v < kWarps; ++v) y = fmaf(__shfl_sync(kAll, f, 8 * v + r), so(v)[8 * n + r][at_], y);
                 const float i = __shfl_sync(kAll, inv, r);
                 if (8 * n + r < rows) {
                     if (whole) a.out[(out0 + 8 * n + r) * kDim + d] = __float2bfloat16_rn(y * i);
@@ -607,6 +630,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kBits, kDim, kNT, kPair)
             }
         }
         __syncthreads();  // (the shared sums are read, the piece is written)
+        if (more) {
+#pragma unroll
+            for (int d = kEarly; d < kDepth; ++d) ask(seg, steps_of(seg), d);
+        }
         if (!whole) {
             has[place] = true;
             if (tid == 0) {  // count the piece; who counts the last one joins them, when its own range is done
@@ -696,9 +723,7 @@ size_t quant_decode_workspace(int num_seqs, int num_q_heads, int num_kv_heads, i
 
 template <int kBits, int kDim, int kNT, bool kPair>
 static cudaError_t launch(const QuantDecodeArgs& a, cudaStream_t stream) {
-    constexpr int kSumCols = kPair ? 4 : 8 * kNT;
-    constexpr int smem = static_cast<int>(sizeof(float)) * kWarps * kSumCols * (kDim + 4) +
-                         kWarps * depth_of(kBits, kDim, kNT, kPair) * Stage<kBits, kDim>::kBytes;
+    constexpr int smem = kWarps * depth_of(kBits, kDim, kNT, kPair) * Stage<kBits, kDim>::kBytes;
     static_assert(ctas_per_sm(kBits, kDim, kNT, kPair) * (smem + 3072) <= 228 * 1024, "shared memory per SM");
     const auto kernel = quant_decode_kernel<kBits, kDim, kNT, kPair>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
