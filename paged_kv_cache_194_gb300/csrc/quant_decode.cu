@@ -269,23 +269,23 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kBits, kDim, kNT, kPair)
         return blk;
     };
     int win = 0, win_next = 0;
-    // asks for the rows of step i (one group of copies, an empty one behind the last step)
-    auto ask = [&](const Seg& s, int steps, int i) {
+    // asks for the rows of step i, into this place of the ring (one group of copies, an empty one behind the last step)
+    const uint64_t block_rows = static_cast<uint64_t>(a.num_kv_heads) << a.block_shift;
+    uint64_t head_row = 0;  // first row of the segment's head in a block
+    auto ask = [&](const Seg& s, int steps, int i, uint8_t* dst) {
         if (i < steps) {
             if ((i & 31) == 0 && i > 0) win = win_next;
             if ((i & 31) == 16) win_next = entries(s, (i & ~31) + 32);
-            const int blk = __shfl_sync(kAll, win, i & 31);
-            const int tok = s.token0 + kStep * (warp + kWarps * i);
-            const size_t row = ((static_cast<size_t>(blk) * a.num_kv_heads + head_of(s)) << a.block_shift) + (tok & bs_mask);
-            const uint8_t* k = a.k_codes + row * S::kRow;
-            const uint8_t* v = a.v_codes + row * S::kRow;
-            uint8_t* dst = ring + i % kDepth * St::kBytes;
+            const uint32_t blk = __shfl_sync(kAll, win, i & 31);
+            const uint64_t row = blk * block_rows + head_row + ((s.token0 + kStep * (warp + kWarps * i)) & bs_mask);
+            const uint8_t* k = a.k_codes + row * S::kRow + 16 * lane;
+            const uint8_t* v = a.v_codes + row * S::kRow + 16 * lane;
             constexpr int kAll16 = 16 * St::kChunks;  // 16-byte chunks of K
 #pragma unroll
             for (int c0 = 0; c0 < kAll16; c0 += 32) {
                 const int c = c0 + lane;
-                cp_async16(dst + St::k_at(c / St::kChunks, c % St::kChunks), k + 16 * c, 16);
-                cp_async16(dst + St::v_at(c / St::kChunks, c % St::kChunks), v + 16 * c, 16);
+                cp_async16(dst + St::k_at(c / St::kChunks, c % St::kChunks), k + 16 * c0, 16);
+                cp_async16(dst + St::v_at(c / St::kChunks, c % St::kChunks), v + 16 * c0, 16);
             }
             if (lane < 8)
                 cp_async16(dst + St::kPairs + 16 * lane,
@@ -293,9 +293,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kBits, kDim, kNT, kPair)
         }
         cp_async_commit();
     };
-    // parts of step i's rows to this lane's registers
-    auto take_k = [&](uint32_t (&k)[2][S::kKW], int i) {
-        const uint8_t* src = ring + i % kDepth * St::kBytes;
+    // parts of a step's rows to this lane's registers
+    auto take_k = [&](uint32_t (&k)[2][S::kKW], const uint8_t* src) {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             if constexpr (S::kKW == 8) {
@@ -306,8 +305,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kBits, kDim, kNT, kPair)
             }
         }
     };
-    auto take_v = [&](uint32_t (&v)[4][S::kVW], int i) {
-        const uint8_t* src = ring + i % kDepth * St::kBytes;
+    auto take_v = [&](uint32_t (&v)[4][S::kVW], const uint8_t* src) {
 #pragma unroll
         for (int r = 0; r < 4; ++r)
             load_words<S::kVW>(v[r], src + St::v_at(2 * t + (r & 1) + 8 * (r >> 1), 4 * S::kVW * g / 16) + 4 * S::kVW * g % 16);
@@ -340,8 +338,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kBits, kDim, kNT, kPair)
     };
     load_q();
     win = entries(seg, 0);
+    head_row = static_cast<uint64_t>(head_of(seg)) << a.block_shift;
 #pragma unroll
-    for (int d = 0; d < kDepth; ++d) ask(seg, steps_of(seg), d);
+    for (int d = 0; d < kDepth; ++d) ask(seg, steps_of(seg), d, ring + d * St::kBytes);
     bool has[2] = {false, false};
     for (bool more = true; more;) {
         // ------------------------------------------------- queries -> operands
@@ -417,13 +416,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kBits, kDim, kNT, kPair)
 
         // Steps i .. i + kNS - 1.  With at most four heads two steps share the softmax: columns 4 to 7 of the products
         // are nobody's, so lanes with t >= 2 take the second step's scores of the first four.
-        auto use = [&](int i, auto whole_steps) {
+        auto use = [&](int i, const uint8_t* at_ring, auto whole_steps) {
             constexpr bool kWhole = decltype(whole_steps)::value;  // every token is there
             float sc[kNS][kNT][2][4] = {};
 #pragma unroll
             for (int e = 0; e < kNS; ++e) {
                 uint32_t xk[2][S::kKW];
-                take_k(xk, i + e);
+                take_k(xk, at_ring + e * St::kBytes);
 #pragma unroll
                 for (int ks = 0; ks < S::kKSteps; ++ks) {
                     uint32_t a0, a1, a2, a3;
@@ -442,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kBits, kDim, kNT, kPair)
             // exponents of the weights: rows g (r = 0) and g + 8 (r = 1) of this lane's step
             const int my = i + (kPair ? t >> 1 : 0);
             const int left = kWhole ? kStep : seg.token1 - (seg.token0 + kStep * (warp + kWarps * my));  // tokens that are there
-            const uint32_t* pairs = reinterpret_cast<const uint32_t*>(ring + my % kDepth * St::kBytes + St::kPairs);
+            const uint32_t* pairs = reinterpret_cast<const uint32_t*>(at_ring + (my - i) * St::kBytes + St::kPairs);
             float ks_[2], kz[2], lg[2], vz[2];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
@@ -518,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kBits, kDim, kNT, kPair)
             for (int e = 0; e < kNS; ++e) {
                 if (e > 0 && !kWhole && i + e >= steps) break;
                 uint32_t xv[4][S::kVW];
-                take_v(xv, i + e);
+                take_v(xv, at_ring + e * St::kBytes);
 #pragma unroll
                 for (int wi = 0; wi < S::kVW; ++wi) {
 #pragma unroll
@@ -545,15 +544,18 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kBits, kDim, kNT, kPair)
             }
         };
 
+        static_assert(kDepth % kNS == 0);
+        uint8_t* place = ring;  // of step i
         for (int i = 0; i < steps; i += kNS) {
             cp_async_wait<kDepth - kNS>();
             __syncwarp();
             // (only a sequence's last tokens lie in steps that are not whole, or have no second one)
-            if (i + kNS < steps) use(i, std::true_type{});
-            else use(i, std::false_type{});
+            if (i + kNS < steps) use(i, place, std::true_type{});
+            else use(i, place, std::false_type{});
             __syncwarp();  // (the rows may be written over)
 #pragma unroll
-            for (int e = 0; e < kNS; ++e) ask(seg, steps, i + e + kDepth);
+            for (int e = 0; e < kNS; ++e) ask(seg, steps, i + e + kDepth, place + e * St::kBytes);
+            place = place + kNS * St::kBytes == ring + kRing ? ring : place + kNS * St::kBytes;
         }
         // the next unit's first rows are under way from here on
         const Seg done = seg;
@@ -561,6 +563,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kBits, kDim, kNT, kPair)
         if (more) {
             load_q();
             win = entries(seg, 0);
+            head_row = static_cast<uint64_t>(head_of(seg)) << a.block_shift;
         }
 
         // ------------------------------------------------ the warps' sums meet
@@ -592,11 +595,11 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kBits, kDim, kNT, kPair)
         __syncthreads();
         if (more) {
 #pragma unroll
-            for (int d = 0; d < kEarly; ++d) ask(seg, steps_of(seg), d);
+            for (int d = 0; d < kEarly; ++d) ask(seg, steps_of(seg), d, ring + d * St::kBytes);
         }
         const bool whole = done.first == 0 && done.end == done.nt;
-        const int place = g0 >= done.at + kUnitCost ? 0 : 1, rows = min(kCols, gh - q0_of(done));
-        const size_t slot = 2 * static_cast<size_t>(c) + place;
+        const int side = g0 >= done.at + kUnitCost ? 0 : 1, rows = min(kCols, gh - q0_of(done));
+        const size_t slot = 2 * static_cast<size_t>(c) + side;
         const size_t out0 = static_cast<size_t>(done.b) * a.num_q_heads + head_of(done) * gh + q0_of(done);
         // lane (w, r): what the sums of warp w weigh in column r, by shuffles over the warps' lanes
         constexpr int kPerPass = kThreads / kDim;  // rows that the CTA's threads write at once
@@ -632,17 +635,17 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kBits, kDim, kNT, kPair)
         __syncthreads();  // (the shared sums are read, the piece is written)
         if (more) {
 #pragma unroll
-            for (int d = kEarly; d < kDepth; ++d) ask(seg, steps_of(seg), d);
+            for (int d = kEarly; d < kDepth; ++d) ask(seg, steps_of(seg), d, ring + d * St::kBytes);
         }
         if (!whole) {
-            has[place] = true;
+            has[side] = true;
             if (tid == 0) {  // count the piece; who counts the last one joins them, when its own range is done
-                split[place] = done;
+                split[side] = done;
                 __threadfence();
                 const long long c0 = ((done.at + kUnitCost + 1) * P - 1) / total, c1 = ((done.at + kUnitCost + done.nt) * P - 1) / total;
                 int* counter = a.counters + static_cast<size_t>(done.b) * per_seq + done.unit;
-                last_flag[place] = count_up(counter) == static_cast<int>(c1 - c0);
-                if (last_flag[place]) *counter = 0;
+                last_flag[side] = count_up(counter) == static_cast<int>(c1 - c0);
+                if (last_flag[side]) *counter = 0;
             }
         }
     }
