@@ -45,15 +45,13 @@ constexpr int kUnitCost = 4;
 constexpr int kMaxCtas = 1024;
 // CTAs per SM, and steps whose rows are under way in a warp (pair: taken two at a time).  HBM answers after 2.5 to 3 us
 // under load, so an SM wants 130 to 150 KB on their way.
-constexpr int ctas_per_sm(int bits, int dim, int nt, bool pair) {
-    (void)bits, (void)pair;
+constexpr int ctas_per_sm(int bits, int dim, int nt) {
     if (dim == 64) return nt == 1 ? 4 : 3;
-    return nt == 2 ? 2 : bits == 4 ? 3 : 2;
+    return nt == 1 && bits == 4 ? 3 : 2;
 }
-constexpr int depth_of(int bits, int dim, int nt, bool pair) {
-    (void)pair;
+constexpr int depth_of(int bits, int dim, int nt) {
     if (dim == 64) return bits == 4 ? 10 : 6;
-    return nt == 2 ? (bits == 4 ? 12 : 6) : bits == 4 ? 6 : 6;
+    return nt == 2 && bits == 4 ? 12 : 6;
 }
 constexpr float kNone = -1e30f;  // a maximum of nothing
 constexpr unsigned kAll = 0xFFFFFFFFu;
@@ -149,11 +147,11 @@ struct Seg {
 };
 
 template <int kBits, int kDim, int kNT, bool kPair>
-__global__ void __launch_bounds__(kThreads, ctas_per_sm(kBits, kDim, kNT, kPair)) quant_decode_kernel(const QuantDecodeArgs a) {
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(kBits, kDim, kNT)) quant_decode_kernel(const QuantDecodeArgs a) {
     using S = Share<kBits, kDim>;
     static_assert(!kPair || kNT == 1);
     constexpr int kCols = 8 * kNT, kSumCols = kPair ? 4 : kCols, kPitch = kDim + 4;
-    constexpr int kDepth = depth_of(kBits, kDim, kNT, kPair), kNS = kPair ? 2 : 1;  // (steps at a time)
+    constexpr int kDepth = depth_of(kBits, kDim, kNT), kNS = kPair ? 2 : 1;  // (steps at a time)
     using St = Stage<kBits, kDim>;
     extern __shared__ __align__(16) uint8_t dynamic[];
     constexpr int kRing = kDepth * St::kBytes;
@@ -178,10 +176,6 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kBits, kDim, kNT, kPair)
         const int L = a.lens[b];
         return L < 0 ? 0 : (L > a.max_len ? a.max_len : L);
     };
-    auto cost_of = [&](int b) {  // of a sequence's units in the list
-        const int L = len_of(b);
-        return L > 0 ? static_cast<long long>((L + kTile - 1) / kTile + kUnitCost) * per_seq : 0;
-    };
     // empty sequences' rows, and lengths that cannot be
     for (int b = blockIdx.x; b < a.num_seqs; b += gridDim.x) {
         const int L = a.lens[b];
@@ -191,12 +185,21 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kBits, kDim, kNT, kPair)
         for (int i = tid; i < a.num_q_heads * kDim / 2; i += kThreads) o[i] = 0u;
     }
 
-    // this CTA's range [g0, g1) of the list, and the sequence that tile g0 lies in
+    // this CTA's range [g0, g1) of the list, and the sequence that it begins in
     const int run = (a.num_seqs + kThreads - 1) / kThreads;  // sequences per thread
-    long long mine = 0;
+    long long mine = 0;   // cost of this thread's
+    int some = 0, most = 0;  // how many have tokens, and the most tiles of one
     for (int i = 0; i < run; ++i)
-        if (tid * run + i < a.num_seqs) mine += cost_of(tid * run + i);
-    long long incl = mine;
+        if (tid * run + i < a.num_seqs) {
+            const int nt = (len_of(tid * run + i) + kTile - 1) / kTile;
+            if (nt > 0) mine += nt + kUnitCost, ++some;
+            most = max(most, nt);
+        }
+    // With no more units than CTAs, and none long, every unit is a CTA's of its own: joining its pieces would take longer
+    // than they save.  (us whole / cut, 32 heads: 8.2 / 10.2 for one sequence of 512 tokens, 11.6 / 10.5 for one of 1024;
+    // 12.3 / 20.6 and 17.9 / 24.9 for fifty.)
+    const bool long8 = __syncthreads_or(most > 8), long16 = __syncthreads_or(most > 16);
+    long long incl = mine | static_cast<long long>(some) << 40;  // (both sums at once: costs stay below 2^40)
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
         const long long x = __shfl_up_sync(kAll, incl, d);
@@ -204,21 +207,27 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kBits, kDim, kNT, kPair)
     }
     if (lane == 31) scan[warp] = incl;
     __syncthreads();
-    long long total = 0;
+    long long sum = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
         if (w < warp) incl += scan[w];
-        total += scan[w];
+        sum += scan[w];
     }
+    const long long units = (sum >> 40) * per_seq;
+    const bool apart = units <= gridDim.x && !(4 * units >= gridDim.x ? long16 : long8);
+    auto cost = [&](int nt) { return apart ? 1 : nt + kUnitCost; };
+    auto pick = [&](long long x) { return (apart ? x >> 40 : x & ((1ll << 40) - 1)) * per_seq; };
+    const long long total = pick(sum), before = pick(incl) - (apart ? some : mine) * per_seq;
     const long long P = total < static_cast<long long>(gridDim.x) ? total : static_cast<long long>(gridDim.x);
     const long long c = blockIdx.x;
     if (c >= P) return;
     const long long g0 = c * total / P, g1 = (c + 1) * total / P;
-    if (g0 >= incl - mine && g0 < incl) {
-        long long at = incl - mine;
+    if (g0 >= before && g0 < pick(incl)) {
+        long long at = before;
         int b = tid * run;
         for (;; ++b) {
-            const long long n = cost_of(b);
+            const int nt = (len_of(b) + kTile - 1) / kTile;
+            const long long n = nt > 0 ? static_cast<long long>(cost(nt)) * per_seq : 0;
             if (g0 < at + n) break;
             at += n;
         }
@@ -230,14 +239,14 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kBits, kDim, kNT, kPair)
     // (whether [first, end) is a piece of the CTA's range, which ends at g1)
     auto clip = [&](Seg& s, int L) -> bool {
         const long long left = g1 - s.at - kUnitCost;
-        s.end = static_cast<int>(left < s.nt ? left : s.nt);
+        s.end = apart || left > s.nt ? s.nt : static_cast<int>(left);
         s.token0 = s.first * kTile;
         s.token1 = min(L, s.end * kTile);
         return s.end > s.first;
     };
     auto next = [&](Seg& s) -> bool {  // the unit behind s
-        s.at += s.nt + kUnitCost;
-        if (s.at + kUnitCost >= g1) return false;
+        s.at += cost(s.nt);
+        if (s.at + (apart ? 0 : kUnitCost) >= g1) return false;
         int L = 0;
         if (++s.unit == per_seq) {
             s.unit = 0;
@@ -320,9 +329,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kBits, kDim, kNT, kPair)
     {
         const int L = len_of(seg.b);
         seg.nt = (L + kTile - 1) / kTile;
-        seg.unit = static_cast<int>((g0 - found_at) / (seg.nt + kUnitCost));
-        seg.at = found_at + static_cast<long long>(seg.unit) * (seg.nt + kUnitCost);
-        seg.first = static_cast<int>(g0 - seg.at > kUnitCost ? g0 - seg.at - kUnitCost : 0);
+        seg.unit = static_cast<int>((g0 - found_at) / cost(seg.nt));
+        seg.at = found_at + static_cast<long long>(seg.unit) * cost(seg.nt);
+        seg.first = static_cast<int>(!apart && g0 - seg.at > kUnitCost ? g0 - seg.at - kUnitCost : 0);
         if (!clip(seg, L)) return;  // (nothing but a unit's own cost)
     }
     // this lane's share of the unit's query rows, BF16 pairs: asked for before the cache's rows, behind whose flood they
@@ -726,14 +735,14 @@ size_t quant_decode_workspace(int num_seqs, int num_q_heads, int num_kv_heads, i
 
 template <int kBits, int kDim, int kNT, bool kPair>
 static cudaError_t launch(const QuantDecodeArgs& a, cudaStream_t stream) {
-    constexpr int smem = kWarps * depth_of(kBits, kDim, kNT, kPair) * Stage<kBits, kDim>::kBytes;
-    static_assert(ctas_per_sm(kBits, kDim, kNT, kPair) * (smem + 3072) <= 228 * 1024, "shared memory per SM");
+    constexpr int smem = kWarps * depth_of(kBits, kDim, kNT) * Stage<kBits, kDim>::kBytes;
+    static_assert(ctas_per_sm(kBits, kDim, kNT) * (smem + 3072) <= 228 * 1024, "shared memory per SM");
     const auto kernel = quant_decode_kernel<kBits, kDim, kNT, kPair>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess)  // (all of an SM's CTAs have to fit)
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
     if (e != cudaSuccess) return e;
-    const int sms = num_sms() > 0 ? num_sms() : 148, ctas = sms * ctas_per_sm(kBits, kDim, kNT, kPair);
+    const int sms = num_sms() > 0 ? num_sms() : 148, ctas = sms * ctas_per_sm(kBits, kDim, kNT);
     return launch_dependent(kernel, dim3(ctas < kMaxCtas ? ctas : kMaxCtas), dim3(kThreads), smem, stream, a);
 }
 
