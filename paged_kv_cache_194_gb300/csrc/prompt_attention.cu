@@ -5,6 +5,9 @@
 // A CTA of 256 threads keeps their O in registers (4 rows x head_dim / 16 columns
 // each) and walks over the keys, 64 at a time: S = Q K^T (4 x 4 each), softmax
 // statistics by the 16 threads of a row, P through shared memory, O += P V.
+//
+// For F32 rows, and for BF16 ones that the tensor-core design does not take (more than
+// 128 query heads per KV head, more sequences than it plans for, no key at all).
 #include "device_common.cuh"
 #include "quant_internal.h"
 
@@ -27,14 +30,19 @@ __device__ __forceinline__ Span span_of(const PromptArgs& a, int b, bool report)
     return s;
 }
 
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+    const uint2 w = *reinterpret_cast<const uint2*>(p);
+    return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
+}
+
 template <typename T, int kDim>
-__global__ void __launch_bounds__(kThreads) prompt_simt_kernel(const PromptArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) prompt_simt_kernel(const PromptArgs a) {
     constexpr int kPitch = kDim + 4, kCols = kDim / 16;
     extern __shared__ float smem[];
     float* sq = smem;                       // [kRows][kPitch]
-    float* sk = sq + kRows * kPitch;        // [kKeys][kPitch]
-    float* sv = sk + kKeys * kPitch;        // [kKeys][kDim]
-    float* sp = sv + kKeys * kDim;          // [kRows][kKeys + 4]
+    float* skv = sq + kRows * kPitch;       // [kKeys][kPitch] K, then V
+    float* sp = skv + kKeys * kPitch;       // [kRows][kKeys + 4]
     const int tid = threadIdx.x, gh = a.num_q_heads / a.num_kv_heads, h = blockIdx.y;
     // unit blockIdx.x: the sequences' row tiles, one sequence after the other
     int tile = blockIdx.x, b = 0;
@@ -52,10 +60,12 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(const PromptArgs 
     const T* q = static_cast<const T*>(a.q);
     const T* k = static_cast<const T*>(a.k) + s.k0 * a.k_stride + static_cast<int64_t>(h) * kDim;
     const T* v = static_cast<const T*>(a.v) + s.k0 * a.v_stride + static_cast<int64_t>(h) * kDim;
-    for (int i = tid; i < kRows * kDim; i += kThreads) {
-        const int64_t r = row0 + i / kDim;
-        sq[i / kDim * kPitch + i % kDim] =
-            r < rows ? load_q<T>(q + (s.q0 + r / gh) * a.q_stride + (h * gh + r % gh) * kDim + i % kDim) : 0.f;
+    constexpr int kQuads = kDim / 4;  // four elements at a time
+    for (int i = tid; i < kRows * kQuads; i += kThreads) {
+        const int64_t r = row0 + i / kQuads;
+        const int d = i % kQuads * 4;
+        *reinterpret_cast<float4*>(sq + i / kQuads * kPitch + d) =
+            r < rows ? load4(q + (s.q0 + r / gh) * a.q_stride + (h * gh + r % gh) * kDim + d) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
     const int ty = tid / 16, tx = tid % 16;  // rows 4 ty .. + 3, keys tx + 16 j, columns tx * 4 + 64 j
     int seen[4];                             // keys that each row sees
@@ -68,11 +78,16 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(const PromptArgs 
     float o[4][kCols] = {}, mx[4], l[4] = {};
     for (int i = 0; i < 4; ++i) mx[i] = -INFINITY;
     for (int t0 = 0; t0 < keys; t0 += kKeys) {
+        // V's rows are on their way, in registers, while K's are multiplied
+        constexpr int kMine = kKeys * kQuads / kThreads;
+        float4 vr[kMine];
         __syncthreads();
-        for (int i = tid; i < kKeys * kDim; i += kThreads) {
-            const int t = t0 + i / kDim;
-            sk[i / kDim * kPitch + i % kDim] = t < keys ? load_q<T>(k + t * a.k_stride + i % kDim) : 0.f;
-            sv[i] = t < keys ? load_q<T>(v + t * a.v_stride + i % kDim) : 0.f;
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+            const int e = tid + i * kThreads, t = t0 + e / kQuads, d = e % kQuads * 4;
+            *reinterpret_cast<float4*>(skv + e / kQuads * kPitch + d) =
+                t < keys ? load4(k + t * a.k_stride + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+            vr[i] = t < keys ? load4(v + t * a.v_stride + d) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
         __syncthreads();
         float x[4][4] = {};
@@ -82,7 +97,7 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(const PromptArgs 
 #pragma unroll
             for (int i = 0; i < 4; ++i) qa[i] = *reinterpret_cast<const float4*>(sq + (4 * ty + i) * kPitch + d);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) kb[j] = *reinterpret_cast<const float4*>(sk + (tx + 16 * j) * kPitch + d);
+            for (int j = 0; j < 4; ++j) kb[j] = *reinterpret_cast<const float4*>(skv + (tx + 16 * j) * kPitch + d);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -115,21 +130,31 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(const PromptArgs 
 #pragma unroll
             for (int c = 0; c < kCols; ++c) o[i][c] *= alpha;
         }
-        __syncwarp();  // (a row's 16 threads are of one warp)
-#pragma unroll 4
-        for (int t = 0; t < kKeys; ++t) {
-            float p[4];
+        __syncthreads();
 #pragma unroll
-            for (int i = 0; i < 4; ++i) p[i] = sp[(4 * ty + i) * (kKeys + 4) + t];
+        for (int i = 0; i < kMine; ++i) {
+            const int e = tid + i * kThreads;
+            *reinterpret_cast<float4*>(skv + e / kQuads * kPitch + e % kQuads * 4) = vr[i];
+        }
+        __syncthreads();
+#pragma unroll 2
+        for (int t = 0; t < kKeys; t += 4) {
+            float4 p[4];
 #pragma unroll
-            for (int c = 0; c < kCols; c += 4) {
-                const float4 w = *reinterpret_cast<const float4*>(sv + t * kDim + 16 * c + 4 * tx);
+            for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4*>(sp + (4 * ty + i) * (kKeys + 4) + t);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    o[i][c] = fmaf(p[i], w.x, o[i][c]);
-                    o[i][c + 1] = fmaf(p[i], w.y, o[i][c + 1]);
-                    o[i][c + 2] = fmaf(p[i], w.z, o[i][c + 2]);
-                    o[i][c + 3] = fmaf(p[i], w.w, o[i][c + 3]);
+            for (int u = 0; u < 4; ++u) {
+#pragma unroll
+                for (int c = 0; c < kCols; c += 4) {
+                    const float4 w = *reinterpret_cast<const float4*>(skv + (t + u) * kPitch + 16 * c + 4 * tx);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float pu = u == 0 ? p[i].x : u == 1 ? p[i].y : u == 2 ? p[i].z : p[i].w;
+                        o[i][c] = fmaf(pu, w.x, o[i][c]);
+                        o[i][c + 1] = fmaf(pu, w.y, o[i][c + 1]);
+                        o[i][c + 2] = fmaf(pu, w.z, o[i][c + 2]);
+                        o[i][c + 3] = fmaf(pu, w.w, o[i][c + 3]);
+                    }
                 }
             }
         }
@@ -147,7 +172,7 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(const PromptArgs 
 
 template <typename T, int kDim>
 cudaError_t launch_simt(const PromptArgs& a, cudaStream_t stream) {
-    constexpr int smem = (kRows * (kDim + 4) + kKeys * (kDim + 4) + kKeys * kDim + kRows * (kKeys + 4)) * 4;
+    constexpr int smem = (kRows * (kDim + 4) + kKeys * (kDim + 4) + kRows * (kKeys + 4)) * 4;  // (two CTAs an SM)
     const int64_t tiles = static_cast<int64_t>(a.q_rows) * (a.num_q_heads / a.num_kv_heads) / kRows + a.num_seqs;
     if (tiles > INT32_MAX || a.num_kv_heads > 65535) return cudaErrorNotSupported;
     const cudaError_t e = cudaFuncSetAttribute(prompt_simt_kernel<T, kDim>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
