@@ -26,7 +26,7 @@
 // copies and products have landed by then, without its outputs.
 #include <cuda.h>
 
-#include <climits>
+#include <type_traits>
 
 #include "quant_internal.h"
 #include "tc_common.cuh"
@@ -461,6 +461,8 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
         // wait for it would have no end if the other warp had given up.)
         const uint32_t say = sbase + Lt::kSay + ((x * 2 + hf) * kRows + m) * 8;
         const uint32_t its_say = sbase + Lt::kSay + ((x * 2 + 1 - hf) * kRows + m) * 8;
+        // Tiles' maxima take two places in turn: a thread may be a tile ahead of the other, but not two, as products wait
+        // for both.
         auto tell = [&](int slot, float mine, int number) {
             asm volatile("st.volatile.shared.v2.b32 [%0], {%1, %2};\n" ::"r"(say + slot * 4 * kRows * 8),
                          "r"(__float_as_uint(mine)), "r"(number)
@@ -486,17 +488,18 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             // (a unit's place in the queue is kept while it is worked on: what is needed once is read when it is)
             const volatile Unit& slot = queue[i % kSlots];
             if (!slot.more) break;
-            int lim, tiles, place0;  // keys that the row sees, key tiles of the row tile, and of the units before
-            bool busy;
+            int lim, tiles, place0, m_keys;  // keys that the row sees, key tiles of the row tile and of the units before, keys
+            bool busy, valid;
             {
                 const Unit u = take(i);
                 const Shape sh(u, qpt, per_unit);
                 place0 = base;
+                m_keys = u.m;
                 base += sh.nt;
                 const int query = x * qpt + qi;
-                const bool valid = x < per_unit && qi < qpt && query < u.n;
+                valid = x < per_unit && qi < qpt && query < u.n;
                 busy = __any_sync(0xFFFFFFFFu, valid);
-                lim = valid ? u.seen + query : INT_MAX;
+                lim = u.seen + min(query, u.n - 1);  // (no row: as another)
                 tiles = sh.tiles[x];
             }
             float m_used = -INFINITY, m_next = -INFINITY, l = 0.f;  // base of this tile's weights, of the next one's
@@ -510,35 +513,13 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                 const int key0 = j * kKeys + hf * kMine;  // this thread's first key
                 float mx = -INFINITY, its = -INFINITY, m_own = 0.f, l0 = 0.f;
                 if (busy) {
-                    const bool full = __all_sync(0xFFFFFFFFu, key0 + kMine <= lim);
-                    {  // the maximum first, from a load of its own: the weights' loop then keeps few registers
-                        uint32_t v[kMine];
-#pragma unroll
-                        for (int c = 0; c < kMine / 32; ++c) tmem_ld32_nowait(ts + hf * kMine + 32 * c, v + 32 * c);
-                        asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
-                        if (full && qk > 0.f) {
-                            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                            for (int k = 0; k < kMine; k += 2)
-                                m4[(k >> 1) & 3] = max3(m4[(k >> 1) & 3], __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
-                            mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * qk;
-                        } else {
-#pragma unroll
-                            for (int k = 0; k < kMine; ++k)
-                                if (key0 + k < lim) mx = fmaxf(mx, __uint_as_float(v[k]) * qk);
-                        }
-                    }
+                    // a row sees its first `mine` keys; all rows of the warp see the first `all`, none one from `any` on
+                    const int mine = min(max(lim - key0, 0), kMine);
+                    const int all = __reduce_min_sync(0xFFFFFFFFu, mine), any = __reduce_max_sync(0xFFFFFFFFu, mine);
+                    const bool full = all == kMine;
                     // The base of this tile's weights 2^(score - base) was agreed on after the tile before, so that no
-                    // thread waits here for the other's maximum (which cost 340 of 3400 cycles); they hear it when
-                    // their weights are written.  The unit's first tile has no tile before.
-                    tell(0, mx, s_count);
-                    if (j == 0) {
-                        if (!hear(0, s_count, its)) {
-                            ok = false;
-                            break;
-                        }
-                        m_used = fmaxf(mx, its);
-                    } else if (__any_sync(0xFFFFFFFFu, m_next != m_used)) {  // ("S j done": P V j - 1 is, too)
+                    // thread waits here for its row's maximum: they tell each other theirs when the weights are made.
+                    if (j > 0 && __any_sync(0xFFFFFFFFu, m_next != m_used)) {  // ("S j done": P V j - 1 is, too)
                         const float alpha = m_used == -INFINITY ? 0.f : ex2(m_used - m_next);
 #pragma unroll 1
                         for (int c = 0; c < kCols; c += 8) tmem_scale8(to + c, alpha);
@@ -546,50 +527,111 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                         l *= alpha;
                         m_used = m_next;
                     }
-                    // far above the base: a base of this thread's own, until both know better
-                    m_own = mx > m_used + kFar ? above(m_used, mx) : m_used;
-                    const float base2 = m_own == -INFINITY ? 0.f : m_own;
                     float l1 = 0.f;
-                    // P as BF16 pairs, 16 columns at a time over this thread's own scores, which it has read by then
+                    bool made = false;
+                    if (j > 0 && full && qk > 0.f) {
+                        // one pass: the maximum beside the weights, which are written unless one was far above the base
+                        uint32_t v[kMine];
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        uint32_t v[32];
-                        tmem_ld32_nowait(ts + hf * kMine + 32 * c, v);
+                        for (int c = 0; c < kMine / 32; ++c) tmem_ld32_nowait(ts + hf * kMine + 32 * c, v + 32 * c);
                         asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
-                        if (full) {
+                        const float base2 = m_used == -INFINITY ? 0.f : m_used;
+                        float m2[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                            for (int k = 0; k < 16; ++k) {
-                                uint32_t* y = v;
-                                float x0, x1;
-                                fma2(x0, x1, __uint_as_float(y[2 * k]), __uint_as_float(y[2 * k + 1]), qk, qk, -base2, -base2);
-                                const float p0 = ex2(x0), p1 = ex2(x1);
-                                add2(l0, l1, l0, l1, p0, p1);
-                                y[k] = bf16x2(p0, p1);
-                            }
+                        for (int k = 0; k < kMine / 2; ++k) {
+                            const float y0 = __uint_as_float(v[2 * k]), y1 = __uint_as_float(v[2 * k + 1]);
+                            m2[k & 1] = max3(m2[k & 1], y0, y1);
+                            float x0, x1;
+                            fma2(x0, x1, y0, y1, qk, qk, -base2, -base2);
+                            const float p0 = ex2(x0), p1 = ex2(x1);
+                            add2(l0, l1, l0, l1, p0, p1);
+                            v[k] = bf16x2(p0, p1);
+                        }
+                        mx = fmaxf(m2[0], m2[1]) * qk;
+                        made = !__any_sync(0xFFFFFFFFu, mx > m_used + kFar);
+                        if (made) {
+                            m_own = m_used;
+                            tmem_st16_nowait(ts + hf * kMine, v);
+                            tmem_st16_nowait(ts + hf * kMine + 16, v + 16);
                         } else {
+                            mx = -INFINITY, l0 = l1 = 0.f;
+                        }
+                    }
+                    if (!made) {
+                        {  // the maximum first, from a load of its own: the weights' loop then keeps few registers
+                            uint32_t v[kMine];
 #pragma unroll
-                            for (int k = 0; k < 16; ++k) {
-                                uint32_t* y = v;
-                                const int t = key0 + 32 * c + 2 * k;
-                                const float p0 = t < lim ? ex2(fmaf(__uint_as_float(y[2 * k]), qk, -base2)) : 0.f;
-                                const float p1 = t + 1 < lim ? ex2(fmaf(__uint_as_float(y[2 * k + 1]), qk, -base2)) : 0.f;
-                                l0 += p0;
-                                l1 += p1;
-                                y[k] = bf16x2(p0, p1);
+                            for (int c = 0; c < kMine / 32; ++c) tmem_ld32_nowait(ts + hf * kMine + 32 * c, v + 32 * c);
+                            asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
+                            if (full && qk > 0.f) {
+                                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                                for (int k = 0; k < kMine; k += 2)
+                                    m4[(k >> 1) & 3] = max3(m4[(k >> 1) & 3], __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+                                mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * qk;
+                            } else {
+#pragma unroll
+                                for (int c = 0; c < kMine; c += 16) {
+                                    if (c >= any) continue;
+                                    float m2[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                                    for (int k = c; k < c + 16; ++k)
+                                        m2[k & 1] = fmaxf(m2[k & 1], k < mine ? __uint_as_float(v[k]) * qk : -INFINITY);
+                                    mx = max3(mx, m2[0], m2[1]);
+                                }
                             }
                         }
-                        tmem_st16_nowait(ts + hf * kMine + 16 * c, v);
+                        if (j == 0) {  // (the unit's first tile has no tile before)
+                            tell(2 * (s_count & 1), mx, s_count);
+                            if (!hear(2 * (s_count & 1), s_count, its)) {
+                                ok = false;
+                                break;
+                            }
+                            m_used = fmaxf(mx, its);
+                        }
+                        // far above the base: a base of this thread's own, until both know better
+                        m_own = mx > m_used + kFar ? above(m_used, mx) : m_used;
+                        const float base2 = m_own == -INFINITY ? 0.f : m_own;
+                        // P as BF16 pairs, 16 columns at a time over this thread's own scores, which it has read by then
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            uint32_t v[32];
+                            if (32 * c >= any) {  // nobody's keys
+#pragma unroll
+                                for (int k = 0; k < 16; ++k) v[k] = 0u;
+                            } else {
+                                tmem_ld32_nowait(ts + hf * kMine + 32 * c, v);
+                                asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
+                                auto weights = [&](auto hide) {
+#pragma unroll
+                                    for (int k = 0; k < 16; ++k) {
+                                        float x0, x1;
+                                        fma2(x0, x1, __uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]), qk, qk, -base2, -base2);
+                                        if (hide()) {  // a weight of 0 for what the row does not see
+                                            x0 = 32 * c + 2 * k < mine ? x0 : -INFINITY;
+                                            x1 = 32 * c + 2 * k + 1 < mine ? x1 : -INFINITY;
+                                        }
+                                        const float p0 = ex2(x0), p1 = ex2(x1);
+                                        add2(l0, l1, l0, l1, p0, p1);
+                                        v[k] = bf16x2(p0, p1);
+                                    }
+                                };
+                                if (32 * c + 32 <= all) weights(std::false_type());
+                                else weights(std::true_type());
+                            }
+                            tmem_st16_nowait(ts + hf * kMine + 16 * c, v);
+                        }
                     }
-                    asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
                     l0 += l1;
+                    const bool far = j > 0 && !made && __any_sync(0xFFFFFFFFu, mx > m_used + kFar);
+                    asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
                     if (j > 0) {
                         fence_before();
-                        tell(2, 0.f, s_count);  // (its weights are written)
-                        if (__any_sync(0xFFFFFFFFu, mx > m_used + kFar)) {
+                        tell(2 * (s_count & 1), mx, s_count);  // (told: its weights are written)
+                        if (far) {
                             // One warp of the two brings the rows' weights, and O, to a common base; the first if it
                             // has such a row
-                            float none;
-                            if (!hear(0, s_count, its) || !hear(2, s_count, none)) {
+                            if (!hear(2 * (s_count & 1), s_count, its)) {
                                 ok = false;
                                 break;
                             }
@@ -613,7 +655,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                 }
                 // V rows behind the sequence: zero (they are another's, or unwritten, and may hold NaN), before
                 // P is ready; A and B both see to it
-                const int there = slot.m - j * kKeys;
+                const int there = m_keys - j * kKeys;
                 if (there < kKeys) {
                     const int c = place0 + j, s = 2 * (c & 1) + 1;
                     if (!__all_sync(0xFFFFFFFFu, wait(kFull + s, (c >> 1) & 1))) {
@@ -632,7 +674,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                 __syncwarp();
                 if (lane == 0) bar_arrive(B(kPFull + x));
                 if (busy) {  // the next tile's base, while the products run
-                    if (j > 0 && !hear(0, s_count, its)) {
+                    if (j > 0 && !hear(2 * (s_count & 1), s_count, its)) {
                         ok = false;
                         break;
                     }
@@ -648,20 +690,31 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                 }
             }
             if (!ok) break;
-            const bool valid = lim != INT_MAX;
-            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
-                                 (static_cast<int64_t>(slot.q0 + x * qpt + qi) * a.num_q_heads + slot.head * gh + hi) * kDim + hf * kCols;
+            // the row's place in the output, counted in heads; -1: no row
+            const int64_t row = valid ? static_cast<int64_t>(slot.q0 + x * qpt + qi) * a.num_q_heads + slot.head * gh + hi : -1;
+            // Chunks of 16 bytes are stored with kChunks lanes on a row: lane g kChunks + c has chunk c of the
+            // rows of the group's lanes.  (A row to a lane took 4000 cycles of a unit: a line for each lane of a store.)
+            constexpr int kChunks = kCols / 8;
+            auto store = [&](const uint4* w) {
+                const int own = lane % kChunks;
+                __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + hf * kCols + own * 8;
+#pragma unroll
+                for (int k = 0; k < kChunks; ++k) {
+                    const int64_t r = __shfl_sync(0xFFFFFFFFu, row, lane - own + k);
+                    if (r >= 0) *reinterpret_cast<uint4*>(out + r * kDim) = w[k];
+                }
+            };
             __syncwarp();
             if (lane == 0) bar_arrive(B(kUFree + i % kSlots));
             if (tiles == 0) {  // no key is seen
-                if (valid)
-                    for (int k = 0; k < kCols / 8; ++k) reinterpret_cast<uint4*>(out)[k] = make_uint4(0u, 0u, 0u, 0u);
+                uint4 w[kChunks] = {};
+                store(w);
                 continue;
             }
             // (a base that was to change stays: both threads' l and O are in this one)
             float l_other = 0.f;
-            tell(1, l, s_count);
-            if (!hear(1, s_count, l_other) || !__all_sync(0xFFFFFFFFu, wait(kOFull + x, o_count & 1))) {
+            if (busy) tell(1, l, s_count);
+            if ((busy && !hear(1, s_count, l_other)) || !__all_sync(0xFFFFFFFFu, wait(kOFull + x, o_count & 1))) {
                 ok = false;
                 break;
             }
@@ -674,18 +727,35 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             fence_before();
             __syncwarp();
             if (lane == 0) bar_arrive(B(kOFree + x));  // the next unit's first P V may overwrite it
-            if (valid) {
-                const float inv = 1.f / (l + l_other);
+            const float inv = 1.f / (l + l_other);
+            uint4 w[kChunks];
 #pragma unroll
-                for (int k = 0; k < kCols / 8; ++k) {
-                    uint32_t w[4];
+            for (int k = 0; k < kChunks; ++k) {
+                uint32_t y[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        w[e] = lim > 0 ? bf16x2(__uint_as_float(o[8 * k + 2 * e]) * inv, __uint_as_float(o[8 * k + 2 * e + 1]) * inv)
-                                       : 0u;
-                    reinterpret_cast<uint4*>(out)[k] = make_uint4(w[0], w[1], w[2], w[3]);
+                for (int e = 0; e < 4; ++e)
+                    y[e] = lim > 0 ? bf16x2(__uint_as_float(o[8 * k + 2 * e]) * inv, __uint_as_float(o[8 * k + 2 * e + 1]) * inv) : 0u;
+                w[k] = make_uint4(y[0], y[1], y[2], y[3]);
+            }
+            // chunk c of lane r to lane c, place r, of the group: a transposition by halves
+#pragma unroll
+            for (int d = kChunks / 2; d > 0; d >>= 1) {
+                const bool up = lane & d;
+#pragma unroll
+                for (int k = 0; k < kChunks; ++k) {
+                    if (k & d) continue;
+                    auto swap = [&](uint32_t& lo, uint32_t& hi2) {
+                        const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, up ? lo : hi2, d);
+                        if (up) lo = got;
+                        else hi2 = got;
+                    };
+                    swap(w[k].x, w[k + d].x);
+                    swap(w[k].y, w[k + d].y);
+                    swap(w[k].z, w[k + d].z);
+                    swap(w[k].w, w[k + d].w);
                 }
             }
+            store(w);
         }
         if (!ok && lane == 0) fail();
     }
