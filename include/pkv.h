@@ -491,7 +491,8 @@ pkv_status kv_quant_pool_bytes(const kv_quant_pool_desc* desc, size_t* codes_out
  *                 or tensors of their own.  Strides are multiples of 8 elements
  *                 (16 bytes) of in_dtype (PKV_F32 or PKV_BF16), >= 0.
  *   slot_mapping  as kv_append: -1 skips the token, others outside the pool are
- *                 skipped and set PKV_ERRBIT_SLOT.
+ *                 skipped and set PKV_ERRBIT_SLOT; tokens that name the same slot
+ *                 race (what lands there may be a mix of them).
  */
 pkv_status kv_quant_append(const kv_quant_pool* pool, int32_t layer, const void* k, const void* v, pkv_dtype in_dtype,
                            int64_t k_stride, int64_t v_stride, const int64_t* slot_mapping, int32_t num_tokens,
@@ -525,8 +526,9 @@ pkv_status kv_quant_read(const kv_quant_pool* pool, int32_t layer, const int32_t
  * of query heads per KV head.  A row that reads as NaN makes the queries that see
  * it NaN; rows behind a sequence's end are not looked at.
  *   workspace  at least paged_quant_decode_plan's bytes, 256-byte aligned, zeroed
- *              before its first call; every call leaves its counters zero.  Calls
- *              that share a workspace are stream-ordered.
+ *              before its first call; every call leaves its counters zero, for calls
+ *              of any size that it is large enough for.  Calls that share a workspace
+ *              are stream-ordered.
  */
 pkv_status paged_quant_decode_plan(const kv_quant_pool* pool, int32_t num_seqs, int32_t num_q_heads, int32_t max_seq_len,
                                    size_t* workspace_bytes_out);

@@ -165,7 +165,7 @@ pkv_status paged_quant_decode_plan(const kv_quant_pool* p, int32_t num_seqs, int
     if (!p || num_seqs < 0 || num_q_heads < 1 || max_seq_len < 0) return PKV_ERR_INVALID_ARG;
     if (num_q_heads % p->d.num_kv_heads != 0) return PKV_ERR_INVALID_ARG;
     if (num_seqs > 65535 || num_q_heads > 65535) return PKV_ERR_UNSUPPORTED;
-    if (ws_out) *ws_out = quant_decode_workspace(num_seqs, num_q_heads, p->d.num_kv_heads, p->d.head_dim, nullptr, nullptr);
+    if (ws_out) *ws_out = quant_decode_workspace(num_q_heads, p->d.num_kv_heads, p->d.head_dim, nullptr, nullptr);
     return PKV_OK;
 }
 
@@ -186,7 +186,7 @@ pkv_status paged_quant_decode_attention(const void* q, pkv_dtype q_dtype, const 
     if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256))) return PKV_ERR_WORKSPACE;
     const size_t first = p->layer_rows * layer;
     QuantDecodeArgs a{};
-    quant_decode_workspace(num_seqs, num_q_heads, p->d.num_kv_heads, p->d.head_dim, static_cast<uint8_t*>(workspace), &a);
+    quant_decode_workspace(num_q_heads, p->d.num_kv_heads, p->d.head_dim, static_cast<uint8_t*>(workspace), &a);
     a.q = static_cast<const __nv_bfloat16*>(q);
     a.out = static_cast<__nv_bfloat16*>(out);
     a.k_codes = static_cast<const uint8_t*>(p->d.k_codes) + first * p->row_bytes;

@@ -652,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kBits, kDim, kNT)) quant
                 split[side] = done;
                 __threadfence();
                 const long long c0 = ((done.at + kUnitCost + 1) * P - 1) / total, c1 = ((done.at + kUnitCost + done.nt) * P - 1) / total;
-                int* counter = a.counters + static_cast<size_t>(done.b) * per_seq + done.unit;
+                int* counter = a.counters + c0;  // (no other unit's first piece is this CTA's)
                 last_flag[side] = count_up(counter) == static_cast<int>(c1 - c0);
                 if (last_flag[side]) *counter = 0;
             }
@@ -719,11 +719,11 @@ int columns(int gh) { return gh <= 8 ? 8 : 16; }
 
 }  // namespace
 
-size_t quant_decode_workspace(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, uint8_t* base,
-                              QuantDecodeArgs* a) {
+size_t quant_decode_workspace(int num_q_heads, int num_kv_heads, int head_dim, uint8_t* base, QuantDecodeArgs* a) {
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-    const int gh = num_q_heads / num_kv_heads, cols = columns(gh), parts = (gh + cols - 1) / cols;
-    const size_t counters = up(static_cast<size_t>(num_seqs) * num_kv_heads * parts * sizeof(int32_t));
+    const int cols = columns(num_q_heads / num_kv_heads);
+    // (counters at one place for calls of all sizes: they are what a call leaves for the next)
+    const size_t counters = up(kMaxCtas * sizeof(int32_t));
     const size_t ml = up(static_cast<size_t>(kMaxCtas) * 2 * cols * 2 * sizeof(float));
     if (a) {
         a->counters = reinterpret_cast<int32_t*>(base);

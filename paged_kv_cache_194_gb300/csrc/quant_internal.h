@@ -61,8 +61,7 @@ struct QuantDecodeArgs {
     int32_t* counters;
     float *part_o, *part_ml;
 };
-size_t quant_decode_workspace(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, uint8_t* base,
-                              QuantDecodeArgs* a);
+size_t quant_decode_workspace(int num_q_heads, int num_kv_heads, int head_dim, uint8_t* base, QuantDecodeArgs* a);
 cudaError_t launch_quant_decode(int bits, int head_dim, const QuantDecodeArgs& a, cudaStream_t stream);
 
 // ---------------------------------------------------------- prompt attention

@@ -367,3 +367,92 @@ def test_attention_captured_with_other_lengths_and_on_a_stream():
     call(stream=side)
     side.synchronize()
     b.check(out)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("lens", [(512,), (513,), (1024,), (1025,), (1024, 700) * 60, (1025, 700) * 60, (64,) * 152,
+                                  (2048, 1, 1), (1, 30) * 500], ids=lambda x: "%dx%d" % (len(x), max(x)))
+def test_attention_short_units_and_many(bits, lens):
+    """Units that are a CTA's own, and ones that are cut: both sides of the rule."""
+    b = Quantised(lens, bits=bits, bs=32, seed=11)
+    b.check()
+    assert b.pool.errors() == 0
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+def test_attention_workspace_serves_calls_of_all_sizes(bits):
+    """One workspace, the largest call's, for calls of other batches and heads: each leaves it as the next needs it."""
+    calls = [Quantised(lens, Hq, Hk, D, 16, bits, seed=12) for lens, Hq, Hk, D in
+             [((9000, 5000), 8, 2, 128), ((3000, 0, 1, 64, 2500, 700) * 8, 8, 2, 128), ((20000,), 16, 1, 128),
+              ((4000,) * 30, 8, 4, 64), ((7000, 1), 40, 1, 64), ((2000,) * 70, 8, 2, 128)]]
+    sizes = [pk.quant_decode_workspace(b.pool, len(b.lens), b.q.shape[1], b.max_len).numel() for b in calls]
+    ws = torch.zeros(max(sizes), dtype=torch.uint8, device="cuda")
+    first = [b.check(b.run(workspace=ws)) for b in calls]
+    for i in (5, 0, 3, 1, 4, 2, 1, 5):
+        assert torch.equal(calls[i].run(workspace=ws), first[i]), i
+
+
+def test_attention_two_graphs_share_a_workspace():
+    a, b = Quantised((6000, 40), bits=4, seed=13), Quantised((900,) * 20, bits=4, seed=14)
+    ws = max((pk.quant_decode_workspace(x.pool, len(x.lens), 8, x.max_len) for x in (a, b)), key=lambda w: w.numel())
+    graphs = []
+    for x in (a, b):
+        args = (x.q.cuda(), x.pool, 1, x.tables.cuda(), dev(x.lens), x.max_len, x.scale)
+        out = torch.empty_like(args[0])
+        pk.paged_quant_decode_attention(*args, out=out, workspace=ws)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            pk.paged_quant_decode_attention(*args, out=out, workspace=ws)
+        graphs.append((graph, out, x, args))
+    for _ in range(3):
+        for graph, out, x, _ in graphs:
+            out.fill_(9.0)
+            graph.replay()
+        torch.cuda.synchronize()
+        for _, out, x, _ in graphs:
+            x.check(out)
+
+
+def test_attention_on_two_streams_at_once():
+    a, b = Quantised((6000, 40), bits=4, seed=15), Quantised((900,) * 20, bits=8, seed=16)
+    want = [a.check(), b.check()]
+    side = [torch.cuda.Stream(), torch.cuda.Stream()]
+    args = [(x.q.cuda(), x.pool, 1, x.tables.cuda(), dev(x.lens), x.max_len, x.scale) for x in (a, b)]
+    ws = [pk.quant_decode_workspace(x.pool, len(x.lens), 8, x.max_len) for x in (a, b)]
+    outs = [torch.empty_like(x[0]) for x in args]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i in range(2):
+            pk.paged_quant_decode_attention(*args[i], out=outs[i], workspace=ws[i], stream=side[i])
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
+
+
+@pytest.mark.parametrize("kind", ["q4", "q8", "bf16"])
+def test_read_back_of_many_sequences(kind):
+    """More sequences than a CTA keeps offsets of, most of them empty or one row long."""
+    g = torch.Generator().manual_seed(21)
+    lens = torch.randint(0, 4, (3000,), generator=g).tolist()
+    lens[7], lens[2999] = 50, 33
+    tables, nb = tables_of(lens, 16, g)
+    pool, values = fill_pool(kind, nb, 16, 2, 128, g)
+    off = np.concatenate([[0], np.cumsum(lens)])
+    k, v = pk.kv_read(pool, 1, tables.cuda(), dev(off), int(off[-1]))
+    check_rows(k, expect_rows(values[0][1], tables, lens, 16))
+    check_rows(v, expect_rows(values[1][1], tables, lens, 16))
+    assert pool.errors() == 0
+
+
+@pytest.mark.parametrize("bits,inp", list(itertools.product([4, 8], ["bf16", "f32"])))
+def test_append_one_row_to_many_slots(bits, inp):
+    """A token stride of zero: one row, stored at every slot."""
+    dt = BF if inp == "bf16" else torch.float32
+    x = torch.randn(2, 1, 3, 64, generator=torch.Generator().manual_seed(22)).to(dt)
+    pool = pk.QuantKVPool(1, 3, 16, 3, 64, bits, fill=0xFF)
+    slots = torch.tensor([0, 17, 33, -1, 47])
+    pk.kv_quant_append(pool, 0, x[0].cuda().expand(5, 3, 64), x[1].cuda().expand(5, 3, 64), slots.cuda())
+    want = raw(pk.QuantKVPool(1, 3, 16, 3, 64, bits, fill=0xFF))
+    expect_append(want, 0, x[0].expand(5, 3, 64), x[1].expand(5, 3, 64), slots, 16, bits)
+    for got, w in zip(raw(pool), want):
+        assert torch.equal(got, w)
