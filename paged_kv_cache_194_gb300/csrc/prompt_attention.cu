@@ -44,19 +44,37 @@ __global__ void __launch_bounds__(kThreads, 2) prompt_simt_kernel(const PromptAr
     float* skv = sq + kRows * kPitch;       // [kKeys][kPitch] K, then V
     float* sp = skv + kKeys * kPitch;       // [kRows][kKeys + 4]
     const int tid = threadIdx.x, gh = a.num_q_heads / a.num_kv_heads, h = blockIdx.y;
-    // unit blockIdx.x: the sequences' row tiles, one sequence after the other
-    int tile = blockIdx.x, b = 0;
-    Span s{};
-    for (;; ++b) {
-        if (b >= a.num_seqs) return;
-        s = span_of(a, b, blockIdx.x == 0 && h == 0 && tid == 0);
-        const int tiles = static_cast<int>((static_cast<int64_t>(s.n) * gh + kRows - 1) / kRows);
-        if (tile < tiles) break;
-        tile -= tiles;
+    // unit blockIdx.x: the sequences' row tiles, one sequence after the other (256 sequences at a time)
+    __shared__ long long sums[kThreads / 32];
+    __shared__ Span mine_;
+    __shared__ long long tile_;
+    const bool reports = blockIdx.x == 0 && h == 0;
+    long long before = 0;
+    bool found = false;
+    for (int b0 = 0; b0 < a.num_seqs && (reports || !found); b0 += kThreads) {
+        const Span at = b0 + tid < a.num_seqs ? span_of(a, b0 + tid, reports) : Span{};
+        const long long tiles = (static_cast<long long>(at.n) * gh + kRows - 1) / kRows;
+        long long incl = tiles;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const long long x = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+            if (tid % 32 >= d) incl += x;
+        }
+        if (tid % 32 == 31) sums[tid / 32] = incl;
+        __syncthreads();
+        incl += before;
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < tid / 32) incl += sums[w];
+            before += sums[w];
+        }
+        const bool here = blockIdx.x >= incl - tiles && blockIdx.x < incl;
+        if (here) mine_ = at, tile_ = blockIdx.x - (incl - tiles);
+        found |= __syncthreads_or(here) != 0;
     }
-    if (blockIdx.x == 0 && h == 0 && tid == 0)
-        for (int c = b + 1; c < a.num_seqs; ++c) span_of(a, c, true);
-    const int64_t row0 = static_cast<int64_t>(tile) * kRows, rows = static_cast<int64_t>(s.n) * gh;
+    if (!found) return;
+    const Span s = mine_;
+    const long long tile = tile_;
+    const int64_t row0 = tile * kRows, rows = static_cast<int64_t>(s.n) * gh;
     const T* q = static_cast<const T*>(a.q);
     const T* k = static_cast<const T*>(a.k) + s.k0 * a.k_stride + static_cast<int64_t>(h) * kDim;
     const T* v = static_cast<const T*>(a.v) + s.k0 * a.v_stride + static_cast<int64_t>(h) * kDim;

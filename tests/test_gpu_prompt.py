@@ -275,3 +275,76 @@ def test_prompts_then_decode_then_a_chunk_on_the_cached_rows(bits):
             assert (err <= (2.0 ** -8 + 2.0 ** -23) * want.abs()).all()
             at += n
     assert pool.errors() == 0 and plain.errors() == 0
+
+
+@pytest.mark.parametrize("inp", ["bf16", "f32"])
+@pytest.mark.parametrize("Hq,Hk", [(130, 1), (128, 1), (3, 3)])
+def test_many_sequences_and_many_heads(inp, Hq, Hk):
+    """Past what the tensor-core design plans for: more than 128 query heads to a KV head, more than 2048 sequences."""
+    g = torch.Generator().manual_seed(Hq)
+    lens = torch.randint(0, 4, (2100,), generator=g).tolist() if Hq == 3 else [5, 0, 70, 129]
+    lens[1], lens[-1] = 0, 131
+    cpu, gpu = case(lens, lens, Hq, Hk, 64, inp, fused=True, seed=30)
+    o = dev(offsets(lens))
+    err = torch.zeros(1, dtype=I32, device="cuda")
+    check(pk.prompt_attention(*gpu, o, o, 0.125, error_word=err), cpu, lens, lens, 0.125)
+    assert int(err) == 0
+    o[-2:] += 1  # (the last sequence now ends behind the rows)
+    pk.prompt_attention(*gpu, o, o, 0.125, error_word=err)
+    assert int(err) == pk.ERRBIT_OFFSETS
+
+
+@pytest.mark.parametrize("lens", [(20,) * 250, (20,) * 300, (1,) * 2048], ids=lambda x: "%dx%d" % (len(x), max(x)))
+def test_as_many_sequences_as_are_planned(lens):
+    cpu, gpu = case(lens, lens, 8, 4, 128, "bf16", fused=False, seed=31)
+    o = dev(offsets(lens))
+    check(pk.prompt_attention(*gpu, o, o, 0.1), cpu, lens, lens, 0.1)
+
+
+def test_two_graphs_share_a_workspace_and_two_streams_do_not():
+    g = []
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    for seed, lens in ((32, (700, 3)), (33, (64, 200, 1000))):
+        cpu, gpu = case(lens, lens, 8, 2, 128, "bf16", fused=True, seed=seed)
+        o = dev(offsets(lens))
+        out = pk.prompt_attention(*gpu, o, o, 0.1, workspace=ws)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            pk.prompt_attention(*gpu, o, o, 0.1, out=out, workspace=ws)
+        g.append((graph, out, cpu, gpu, o, lens))
+    for _ in range(3):
+        for graph, out, *_ in g:
+            out.fill_(9.0)
+            graph.replay()
+        torch.cuda.synchronize()
+        for _, out, cpu, _, _, lens in g:
+            check(out, cpu, lens, lens, 0.1)
+    assert (ws == 0).all()
+    side = [torch.cuda.Stream(), torch.cuda.Stream()]
+    own = [pk.prompt_attention_workspace(x[3][0], len(x[5]), 2) for x in g]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i, (_, out, _, gpu, o, _) in enumerate(g):
+            pk.prompt_attention(*gpu, o, o, 0.1, out=out, workspace=own[i], stream=side[i])
+    torch.cuda.synchronize()
+    for _, out, cpu, _, _, lens in g:
+        check(out, cpu, lens, lens, 0.1)
+
+
+def test_scores_that_rise_tile_by_tile():
+    """Each tile's scores are far above (and below) the tile's before: the base of the weights moves at every tile, by
+    more than the weights' range, in some rows of a warp and in one half of a tile's keys."""
+    lens, D = (900,), 128
+    cpu, _ = case(lens, lens, 4, 1, D, "bf16", fused=False, seed=34)
+    q, k, v = cpu
+    q[..., 0] = 8.0
+    steps = torch.arange(900) // 64
+    for up in (steps.float() * 20, (14 - steps).float() * 20, (steps % 3).float() * 30, (steps == 9).float() * 400):
+        k[:, 0, 0] = up.to(BF)
+        for rows in (slice(None), slice(0, 900, 2)):
+            qq = q.clone()
+            qq[rows, :, 0] = -8.0 if rows != slice(None) else 8.0
+            gpu = [x.cuda() for x in (qq, k, v)]
+            o = dev(offsets(lens))
+            check(pk.prompt_attention(*gpu, o, o, 1.0), (qq, k, v), lens, lens, 1.0)
