@@ -7,7 +7,12 @@
 // while the softmax of one runs, the tensor core multiplies for the other.  One
 // persistent CTA per SM takes units from a common counter, long sequences' first and
 // within a sequence the ones with the most keys first, so that what is left for the
-// end is short.  With fewer units than SMs a unit is one row tile.
+// end is short.  With fewer units than SMs the keys of units are cut into pieces, whose
+// sums a second kernel joins (us, 32 query heads on 8: 300 queries behind 8000 keys
+// 158 -> 57, 512 behind 32256 596 -> 233; pieces of fewer than eight tiles do not pay: 100
+// queries on 600 keys 18.3, in pieces of four 23.9), or, where none is longer than such a
+// piece, a unit is one row tile.  That kernel's launch costs 1 to 3 us, so calls whose rows
+// alone make a unit for every SM take an instance without it.
 // 20 warps (the last one idle):
 //  * warp 16, producer: takes units, loads Q tiles, and K and V tiles into one ring
 //    (K 0, V 0, K 1, ...) by TMA;
@@ -43,6 +48,8 @@ constexpr int kStages = 4;
 constexpr int kSlots = 2;            // units in the queue
 constexpr float kFar = 60.f;         // weights stay below 2^60
 constexpr int kSortSeqs = 256;       // up to so many sequences are taken longest first
+constexpr int kLeastPiece = 8;       // key tiles of a unit's piece, at least
+constexpr int kJoinThreads = 1024;
 
 enum Bar {
     kQFull = 0, kQFree = 2, kFull = 4, kFree = kFull + kStages, kSFull = kFree + kStages, kPFull = kSFull + 2,
@@ -57,7 +64,10 @@ struct Unit {
     int head;      // KV head
     int seen;      // keys that query q0 sees (may be negative)
     int more;      // 0: no unit, the list is at its end
-    int pad;
+    // Of a unit whose keys are cut into pieces (k0, m and seen count from the piece's first key):
+    int first;     // key tiles before the piece
+    int len;       // key tiles of a piece; INT_MAX: not cut
+    int slot;      // place of the unit's first piece in the workspace
 };
 
 template <int kDim>
@@ -82,6 +92,11 @@ __device__ __forceinline__ Span span_of(const PromptArgs& a, int b, bool report)
     s.n = ok ? s.n - s.q0 : 0;
     s.m = ok ? s.m - s.k0 : 0;
     return s;
+}
+
+// Pieces that a sequence's units are cut into (part: tiles of a piece, 0: not cut).
+__device__ __forceinline__ int pieces_of(int m, int part) {
+    return part > 0 && m > 0 ? ((m - 1) / kKeys + part) / part : 1;
 }
 
 __device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* map, int half, int head, int row, uint32_t bar) {
@@ -132,6 +147,7 @@ __device__ __forceinline__ float above(float base, float top) {
 }
 
 // What the roles agree on about a unit.
+template <bool kCut>
 struct Shape {
     int tiles[2];  // key tiles of row tile A and of B
     int nt;        // of the unit
@@ -141,12 +157,14 @@ struct Shape {
             const int last = min(u.n, first + qpt) - 1;
             const bool there = x < per_unit && first < u.n;
             tiles[x] = there ? max(0, (u.seen + last + kKeys - 1) / kKeys) : 0;
+            if (kCut) tiles[x] = min(tiles[x], u.len);
         }
         nt = max(tiles[0], tiles[1]);
     }
 };
 
-template <int kDim>
+// kCut: the keys of units may be cut into pieces.
+template <int kDim, bool kCut>
 __global__ void __launch_bounds__(kThreads, 1)
 prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                  const __grid_constant__ CUtensorMap mv, const PromptArgs a) {
@@ -159,8 +177,8 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lt::kBar + 8 * kBars + 4);
     int* turn = reinterpret_cast<int*>(smem + Lt::kBar + 8 * kBars + 8);  // 1 while an issuer has the tensor core
     volatile Unit* queue = reinterpret_cast<volatile Unit*>(smem + Lt::kQueue);
-    int* misc = reinterpret_cast<int*>(smem + Lt::kMisc);  // {row tiles per unit}
-    int* cum = reinterpret_cast<int*>(smem + Lt::kPlan);   // [B + 1] units of one KV head before each sequence in order
+    int* misc = reinterpret_cast<int*>(smem + Lt::kMisc);  // {row tiles per unit, key tiles of a piece}
+    int* cum = reinterpret_cast<int*>(smem + Lt::kPlan);   // [B + 1] units (pieces) of one KV head before each sequence in order
     uint16_t* order = reinterpret_cast<uint16_t*>(smem + Lt::kPlan + (kPromptMaxSeqs + 1) * 4);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int gh = a.num_q_heads / a.num_kv_heads, qpt = kRows / gh;  // queries of a row tile
@@ -174,6 +192,8 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
         *turn = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
+    if (warp == kProducer && lane < 3)
+        asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(lane == 0 ? &mq : lane == 1 ? &mk : &mv)) : "memory");
     if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(su32(tmem_slot)), "r"(512)
                      : "memory");
@@ -195,29 +215,63 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     }
     __syncthreads();
     if (warp == 0) {
-        for (int per = 2;; per = 1) {  // two row tiles a unit, unless that leaves SMs without one
-            int at = 0;
-            for (int r0 = 0; r0 < a.num_seqs; r0 += 32) {
-                int n = 0;
-                if (r0 + lane < a.num_seqs) n = (span_of(a, order[r0 + lane], false).n + per * qpt - 1) / (per * qpt);
-                int incl = n;
-#pragma unroll
-                for (int d = 1; d < 32; d <<= 1) {
-                    const int x = __shfl_up_sync(0xFFFFFFFFu, incl, d);
-                    if (lane >= d) incl += x;
-                }
-                if (r0 + lane < a.num_seqs) cum[r0 + lane + 1] = at + incl;
-                at += __shfl_sync(0xFFFFFFFFu, incl, 31);
-            }
-            if (lane == 0) cum[0] = 0, misc[0] = per;
-            if (per == 1 || static_cast<int64_t>(at) * a.num_kv_heads >= gridDim.x) break;
+        // Two row tiles a unit.  If that leaves SMs without one, the units' keys are cut into pieces of equal length, one
+        // for each SM; where no unit is longer than such a piece, a unit is one row tile.
+        int64_t units = 0, tiles = 0;
+        int most = 0;
+        for (int b = lane; b < a.num_seqs; b += 32) {
+            const Span s = span_of(a, b, false);
+            const int nt = s.m / kKeys + (s.m % kKeys > 0), n = s.n / (2 * qpt) + (s.n % (2 * qpt) > 0);
+            units += n;
+            tiles += static_cast<int64_t>(n) * nt;
+            if (n > 0) most = max(most, nt);
         }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) {
+            units += __shfl_xor_sync(0xFFFFFFFFu, units, d);
+            tiles += __shfl_xor_sync(0xFFFFFFFFu, tiles, d);
+        }
+        most = __reduce_max_sync(0xFFFFFFFFu, most);
+        int per = 2, part = 0;
+        if (units * a.num_kv_heads < gridDim.x) {
+            int64_t all = 0;
+            if constexpr (kCut) part = static_cast<int>(max(static_cast<int64_t>(kLeastPiece), tiles * a.num_kv_heads / gridDim.x));
+            for (; part > 0 && part < most; part += 1 + part / 16) {  // no more pieces than SMs
+                all = 0;
+                for (int b = lane; b < a.num_seqs; b += 32) {
+                    const Span s = span_of(a, b, false);
+                    all += static_cast<int64_t>((s.n + 2 * qpt - 1) / (2 * qpt)) * pieces_of(s.m, part);
+                }
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, d);
+                if (all * a.num_kv_heads <= gridDim.x) break;
+            }
+            if (part >= most) part = 0;
+            if (part == 0) per = 1;
+        }
+        int at = 0;
+        for (int r0 = 0; r0 < a.num_seqs; r0 += 32) {
+            int n = 0;
+            if (r0 + lane < a.num_seqs) {
+                const Span s = span_of(a, order[r0 + lane], false);
+                n = (s.n + per * qpt - 1) / (per * qpt) * pieces_of(s.m, part);
+            }
+            int incl = n;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int x = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+                if (lane >= d) incl += x;
+            }
+            if (r0 + lane < a.num_seqs) cum[r0 + lane + 1] = at + incl;
+            at += __shfl_sync(0xFFFFFFFFu, incl, 31);
+        }
+        if (lane == 0) cum[0] = 0, misc[0] = per, misc[1] = part;
     }
     fence_before();
     __syncthreads();
     fence_after();
     const uint32_t tmem = *tmem_slot;
-    const int per_unit = misc[0];
+    const int per_unit = misc[0], part = kCut ? misc[1] : 0;
     auto fail = [&]() {
         *abort_flag = 1;
         if (a.err) atomicOr(a.err, PKV_ERRBIT_TIMEOUT);
@@ -238,7 +292,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     };
     auto take = [&](int i) -> Unit {  // the i-th unit of this CTA, once it is in the queue
         const volatile Unit& s = queue[i % kSlots];
-        return Unit{s.q0, s.n, s.k0, s.m, s.head, s.seen, s.more, 0};
+        return Unit{s.q0, s.n, s.k0, s.m, s.head, s.seen, s.more, 0, kCut ? s.len : 0, 0};
     };
 
     if (warp == kProducer) {
@@ -246,10 +300,11 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
         bool ok = true;
         int stage = 0, q_count[2] = {0, 0};  // tiles put into the ring, Q tiles loaded
         const int total = cum[a.num_seqs] * a.num_kv_heads;
-        int next = lane == 0 ? atomicAdd(a.counters, 1) : 0;
+        // (the first unit is the CTA's own number's; the others come from the counter)
+        int next = blockIdx.x;
         for (int i = 0; ok; ++i) {
             const int id = __shfl_sync(0xFFFFFFFFu, next, 0);
-            if (lane == 0 && id < total) next = atomicAdd(a.counters, 1);  // the one after, while this one runs
+            if (lane == 0 && id < total) next = gridDim.x + atomicAdd(a.counters, 1);  // the one after, while this one runs
             Unit u{};
             if (id < total) {
                 int lo = 0, hi = a.num_seqs;  // the last place whose first unit is at or before id
@@ -259,20 +314,28 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                     else hi = mid;
                 }
                 const Span s = span_of(a, order[lo], false);
-                const int j = id - cum[lo] * a.num_kv_heads;
-                const int first = (cum[lo + 1] - cum[lo] - 1 - j / a.num_kv_heads) * per_unit * qpt;
-                u = Unit{s.q0 + first, s.n - first, s.k0, s.m, j % a.num_kv_heads, s.m - s.n + first + 1, 1, 0};
+                const int j = id - cum[lo] * a.num_kv_heads, head = j % a.num_kv_heads;
+                const int pieces = pieces_of(s.m, part), unit = j / a.num_kv_heads / pieces;
+                const int piece = j / a.num_kv_heads - unit * pieces, skip = piece * part * kKeys;
+                const int first = ((cum[lo + 1] - cum[lo]) / pieces - 1 - unit) * per_unit * qpt;
+                u = Unit{s.q0 + first, s.n - first, s.k0 + skip, s.m - skip, head, s.m - s.n + first + 1 - skip, 1,
+                         piece * part, pieces > 1 ? part : INT_MAX, id - piece * a.num_kv_heads};
+                if (kCut && piece > 0 && Shape<kCut>(u, qpt, per_unit).nt == 0) {  // (no query sees this piece)
+                    --i;
+                    continue;
+                }
             }
             if (i >= kSlots) ok = wait(kUFree + i % kSlots, (i / kSlots - 1) & 1);
             if (!ok) break;
             if (lane == 0) {
                 volatile Unit& s = queue[i % kSlots];
                 s.q0 = u.q0, s.n = u.n, s.k0 = u.k0, s.m = u.m, s.head = u.head, s.seen = u.seen, s.more = u.more;
+                if constexpr (kCut) s.first = u.first, s.len = u.len, s.slot = u.slot;
                 bar_arrive(B(kUFull + i % kSlots));
             }
             __syncwarp();
             if (!u.more) break;
-            const Shape sh(u, qpt, per_unit);
+            const Shape<kCut> sh(u, qpt, per_unit);
             auto load_q = [&](int x) {
                 if (sh.tiles[x] == 0) return;
                 if (q_count[x] > 0 && !wait(kQFree + x, (q_count[x] - 1) & 1)) {
@@ -352,7 +415,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                 __syncwarp();
                 arrive(kUFree + units % kSlots);
                 ++units;
-                const Shape sh(u, qpt, per_unit);
+                const Shape<kCut> sh(u, qpt, per_unit);
                 const int more = __shfl_sync(0xFFFFFFFFu, u.more, 0);
                 if (!more) return 0;
                 tiles = __shfl_sync(0xFFFFFFFFu, sh.tiles[x], 0), nt = __shfl_sync(0xFFFFFFFFu, sh.nt, 0), j = -1;
@@ -492,7 +555,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             bool busy, valid;
             {
                 const Unit u = take(i);
-                const Shape sh(u, qpt, per_unit);
+                const Shape<kCut> sh(u, qpt, per_unit);
                 place0 = base;
                 m_keys = u.m;
                 base += sh.nt;
@@ -692,6 +755,15 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             if (!ok) break;
             // the row's place in the output, counted in heads; -1: no row
             const int64_t row = valid ? static_cast<int64_t>(slot.q0 + x * qpt + qi) * a.num_q_heads + slot.head * gh + hi : -1;
+            // the row tile's pieces, and this one's place among them
+            int pieces = 1, before = 0, len = INT_MAX, slot0 = 0;
+            if constexpr (kCut) before = slot.first, len = slot.len, slot0 = slot.slot;
+            if (len != INT_MAX) {
+                const int n = min(slot.n - x * qpt, qpt), sees = slot.seen + x * qpt;
+                if (n > 0) pieces = (max(0, (sees + n - 1 + kKeys - 1) / kKeys) + before + len - 1) / len;
+                if (tid % 256 == 0 && before == 0 && pieces > 1)
+                    a.tiles[2 * slot0 + x] = make_int4(pieces, slot.q0 + x * qpt, n | slot.head << 8, sees);
+            }
             // Chunks of 16 bytes are stored with kChunks lanes on a row: lane g kChunks + c has chunk c of the
             // rows of the group's lanes.  (A row to a lane took 4000 cycles of a unit: a line for each lane of a store.)
             constexpr int kChunks = kCols / 8;
@@ -708,7 +780,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             if (lane == 0) bar_arrive(B(kUFree + i % kSlots));
             if (tiles == 0) {  // no key is seen
                 uint4 w[kChunks] = {};
-                store(w);
+                if (before == 0) store(w);
                 continue;
             }
             // (a base that was to change stays: both threads' l and O are in this one)
@@ -727,7 +799,18 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             fence_before();
             __syncwarp();
             if (lane == 0) bar_arrive(B(kOFree + x));  // the next unit's first P V may overwrite it
-            const float inv = 1.f / (l + l_other);
+            l += l_other;
+            if (pieces > 1) {  // a part of each row's sums: the pieces are joined by the next kernel
+                const int64_t part_ = (static_cast<int64_t>(slot0) + before / len * a.num_kv_heads) * kSoftmaxWarps + warp;
+                float4* po = a.part_o + part_ * (kCols / 4) * 32 + lane;
+#pragma unroll
+                for (int k = 0; k < kCols / 4; ++k)
+                    po[32 * k] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]), __uint_as_float(o[4 * k + 2]),
+                                             __uint_as_float(o[4 * k + 3]));
+                a.part_ml[part_ * 32 + lane] = make_float2(m_used, l);
+                continue;
+            }
+            const float inv = 1.f / l;
             uint4 w[kChunks];
 #pragma unroll
             for (int k = 0; k < kChunks; ++k) {
@@ -766,6 +849,65 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(512) : "memory");
 }
 
+// The pieces of row tiles, joined in their order.  A CTA has one row tile (or none: the place's units were not cut), a
+// thread one row and a quarter of half of its columns: as the pieces lie, so that a warp's loads are whole lines.
+template <int kDim>
+__global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const PromptArgs a) {
+    constexpr int kQuads = kDim / 8, kMine = kQuads / 4, kAtOnce = 8 / kMine;  // of a half row, of a thread; pieces under way
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    const int4 tile = a.tiles[blockIdx.x];
+    const int pieces = tile.x;
+    if (pieces == 0) return;
+    __syncthreads();
+    if (threadIdx.x == 0) a.tiles[blockIdx.x].x = 0;  // (for the next call)
+    const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 7, quarter = threadIdx.x >> 8;
+    const int gh = a.num_q_heads / a.num_kv_heads, row = 32 * (w & 3) + lane, qi = row / gh;
+    if (qi >= (tile.z & 255)) return;
+    const int64_t part = static_cast<int64_t>(blockIdx.x / 2) * kSoftmaxWarps + blockIdx.x % 2 * 8 + w;
+    const int64_t step = static_cast<int64_t>(a.num_kv_heads) * kSoftmaxWarps;  // from a piece to the next
+    const float2* ml = a.part_ml + part * 32 + lane;
+    const float4* po = a.part_o + (part * kQuads + quarter * kMine) * 32 + lane;
+    float top = -INFINITY;
+#pragma unroll 8
+    for (int p = 0; p < pieces; ++p) top = fmaxf(top, ml[p * step * 32].x);
+    if (top == -INFINITY) top = 0.f;
+    float l = 0.f, o[kMine][4] = {};
+    for (int p0 = 0; p0 < pieces; p0 += kAtOnce) {
+        float2 s[kAtOnce];
+        float4 y[kAtOnce][kMine];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            const int64_t p = min(p0 + i, pieces - 1);
+            s[i] = ml[p * step * 32];
+            if (p0 + i >= pieces) s[i].x = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < kMine; ++k) y[i][k] = po[(p * step * kQuads + k) * 32];
+        }
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            const float f = ex2(s[i].x - top);
+            if (f == 0.f) continue;  // (a piece that weighs nothing, or of which the row sees nothing)
+            l = fmaf(f, s[i].y, l);
+#pragma unroll
+            for (int k = 0; k < kMine; ++k) {
+                o[k][0] = fmaf(f, y[i][k].x, o[k][0]);
+                o[k][1] = fmaf(f, y[i][k].y, o[k][1]);
+                o[k][2] = fmaf(f, y[i][k].z, o[k][2]);
+                o[k][3] = fmaf(f, y[i][k].w, o[k][3]);
+            }
+        }
+    }
+    const float inv = 1.f / l;
+    const bool sees = tile.w + qi > 0;
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
+                         ((static_cast<int64_t>(tile.y) + qi) * a.num_q_heads + (tile.z >> 8) * gh + row % gh) * kDim +
+                         (w >> 2) * (kDim / 2) + quarter * kMine * 4;
+#pragma unroll
+    for (int k = 0; k < kMine; ++k)
+        reinterpret_cast<uint2*>(out)[k] =
+            sees ? make_uint2(bf16x2(o[k][0] * inv, o[k][1] * inv), bf16x2(o[k][2] * inv, o[k][3] * inv)) : make_uint2(0u, 0u);
+}
+
 // Descriptor of packed rows [rows][heads][kDim] as {64 columns, column halves, heads, rows}.
 bool encode_rows(CUtensorMap* map, const void* base, int dim, int64_t rows, int heads, int64_t stride, int box_heads,
                  int box_rows) {
@@ -776,6 +918,8 @@ bool encode_rows(CUtensorMap* map, const void* base, int dim, int64_t rows, int 
     return encode_map(map, 2, 4, base, dims, strides, box);
 }
 
+int grid_size() { return num_sms() > 0 ? num_sms() : 148; }
+
 template <int kDim>
 cudaError_t launch(const PromptArgs& a, cudaStream_t stream) {
     const int gh = a.num_q_heads / a.num_kv_heads, qpt = kRows / gh;
@@ -784,13 +928,18 @@ cudaError_t launch(const PromptArgs& a, cudaStream_t stream) {
         !encode_rows(&mk, a.k, kDim, a.k_rows, a.num_kv_heads, a.k_stride, 1, kKeys) ||
         !encode_rows(&mv, a.v, kDim, a.k_rows, a.num_kv_heads, a.v_stride, 1, kKeys))
         return cudaErrorNotSupported;
-    const cudaError_t e = cudaFuncSetAttribute(prompt_tc_kernel<kDim>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               Layout<kDim>::kSmem);
+    // Keys may be cut where the units of all rows are fewer than SMs, and one may be longer than a piece
+    const bool cut = static_cast<int64_t>(a.q_rows) / (2 * qpt) * a.num_kv_heads < grid_size() && a.k_rows > kLeastPiece * kKeys;
+    const auto kernel = cut ? prompt_tc_kernel<kDim, true> : prompt_tc_kernel<kDim, false>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<kDim>::kSmem);
     if (e != cudaSuccess) return e;
-    const int64_t most = (static_cast<int64_t>(a.q_rows) / qpt + a.num_seqs) * a.num_kv_heads;  // row tiles
-    const int sms = num_sms() > 0 ? num_sms() : 148;
-    prompt_tc_kernel<kDim><<<static_cast<unsigned>(most < sms ? most : sms), kThreads, Layout<kDim>::kSmem, stream>>>(mq, mk, mv, a);
-    return cudaGetLastError();
+    // row tiles, times the key tiles that one may have
+    const int64_t most = (static_cast<int64_t>(a.q_rows) / qpt + a.num_seqs) * a.num_kv_heads * (a.k_rows / kKeys + 1);
+    const int sms = grid_size();
+    kernel<<<static_cast<unsigned>(most < sms ? most : sms), kThreads, Layout<kDim>::kSmem, stream>>>(mq, mk, mv, a);
+    const cudaError_t r = cudaGetLastError();
+    if (r != cudaSuccess || !cut) return r;
+    return launch_dependent(prompt_join_kernel<kDim>, dim3(2 * sms), dim3(kJoinThreads), 0, stream, a);
 }
 
 }  // namespace
@@ -800,6 +949,20 @@ bool prompt_tc_fits(pkv_dtype t, int num_seqs, int q_rows, int num_q_heads, int 
     // (units are counted in 32 bits)
     return t == PKV_BF16 && gh <= kRows && num_seqs <= kPromptMaxSeqs &&
            (static_cast<int64_t>(q_rows) + num_seqs) * num_kv_heads <= INT32_MAX / 2;
+}
+
+// {counter of units, of CTAs}, for each row tile that is cut what the joining kernel needs, and its pieces' (maximum, sum)
+// and O.  There are no more pieces than SMs.
+size_t prompt_tc_workspace(int head_dim, uint8_t* base, PromptArgs* a) {
+    const size_t pieces = static_cast<size_t>(grid_size()), parts = pieces * kSoftmaxWarps;
+    const size_t tiles = 256, ml = tiles + (pieces * 2 * sizeof(int4) + 255) / 256 * 256, o = ml + parts * 32 * sizeof(float2);
+    if (a) {
+        a->counters = reinterpret_cast<int32_t*>(base);
+        a->tiles = reinterpret_cast<int4*>(base + tiles);
+        a->part_ml = reinterpret_cast<float2*>(base + ml);
+        a->part_o = reinterpret_cast<float4*>(base + o);
+    }
+    return o + parts * 32 * (head_dim / 2) * sizeof(float);
 }
 
 cudaError_t launch_prompt_tc(int head_dim, const PromptArgs& a, cudaStream_t stream) {

@@ -214,7 +214,8 @@ pkv_status prompt_attention_plan(int32_t num_seqs, int32_t q_rows, int32_t num_q
     if (dtype != PKV_F32 && dtype != PKV_BF16) return PKV_ERR_INVALID_ARG;
     if (head_dim != 64 && head_dim != 128) return PKV_ERR_UNSUPPORTED;
     if (num_q_heads > 65535) return PKV_ERR_UNSUPPORTED;
-    if (ws_out) *ws_out = prompt_tc_fits(dtype, num_seqs, q_rows, num_q_heads, num_kv_heads) ? 256 : 0;
+    if (ws_out)
+        *ws_out = prompt_tc_fits(dtype, num_seqs, q_rows, num_q_heads, num_kv_heads) ? prompt_tc_workspace(head_dim, nullptr, nullptr) : 0;
     return PKV_OK;
 }
 
@@ -260,7 +261,7 @@ pkv_status prompt_attention(const void* q, const void* k, const void* v, pkv_dty
     a.num_q_heads = num_q_heads;
     a.num_kv_heads = num_kv_heads;
     a.scale_log2 = scale * 1.4426950408889634f;
-    a.counters = static_cast<int32_t*>(workspace);
+    prompt_tc_workspace(head_dim, static_cast<uint8_t*>(workspace), &a);
     // without a key the other design writes the zero rows (a descriptor has no empty dimension)
     if (k_rows > 0 && prompt_tc_fits(dtype, num_seqs, q_rows, num_q_heads, num_kv_heads)) {
         const cudaError_t r = launch_prompt_tc(head_dim, a, static_cast<cudaStream_t>(stream));

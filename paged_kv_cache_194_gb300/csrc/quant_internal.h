@@ -73,8 +73,13 @@ struct PromptArgs {
     int32_t* err;
     int num_seqs, q_rows, k_rows, num_q_heads, num_kv_heads;
     float scale_log2;
-    int32_t* counters;                         // [2], zero between calls (tensor-core design)
+    // tensor-core design: {units, CTAs} and row tiles that are cut, zero between calls, and the pieces' sums
+    int32_t* counters;
+    int4* tiles;
+    float2* part_ml;
+    float4* part_o;
 };
+size_t prompt_tc_workspace(int head_dim, uint8_t* base, PromptArgs* a);
 constexpr int kPromptMaxSeqs = 2048;           // sequences that the tensor-core design plans in shared memory
 bool prompt_tc_fits(pkv_dtype t, int num_seqs, int q_rows, int num_q_heads, int num_kv_heads);
 cudaError_t launch_prompt_tc(int head_dim, const PromptArgs& a, cudaStream_t stream);

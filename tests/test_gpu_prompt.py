@@ -303,7 +303,7 @@ def test_as_many_sequences_as_are_planned(lens):
 
 def test_two_graphs_share_a_workspace_and_two_streams_do_not():
     g = []
-    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    ws = pk.prompt_attention_workspace(torch.zeros(1264, 8, 128, dtype=BF, device="cuda"), 3, 2)
     for seed, lens in ((32, (700, 3)), (33, (64, 200, 1000))):
         cpu, gpu = case(lens, lens, 8, 2, 128, "bf16", fused=True, seed=seed)
         o = dev(offsets(lens))
@@ -320,7 +320,7 @@ def test_two_graphs_share_a_workspace_and_two_streams_do_not():
         torch.cuda.synchronize()
         for _, out, cpu, _, _, lens in g:
             check(out, cpu, lens, lens, 0.1)
-    assert (ws == 0).all()
+    assert (ws[:256] == 0).all()
     side = [torch.cuda.Stream(), torch.cuda.Stream()]
     own = [pk.prompt_attention_workspace(x[3][0], len(x[5]), 2) for x in g]
     torch.cuda.synchronize()
@@ -348,3 +348,60 @@ def test_scores_that_rise_tile_by_tile():
             gpu = [x.cuda() for x in (qq, k, v)]
             o = dev(offsets(lens))
             check(pk.prompt_attention(*gpu, o, o, 1.0), (qq, k, v), lens, lens, 1.0)
+
+
+PIECES = [((1,), (5000,)), ((300,), (8300,)), ((40, 7), (3000, 9001)), ((130, 0, 1, 64), (1500, 700, 2049, 64)),
+          ((200, 3), (150, 4000)), ((1,), (512,)), ((1,), (513,)), ((2000,), (2000,))]
+
+
+@pytest.mark.parametrize("Hq,Hk,D", [(8, 2, 128), (5, 1, 128), (16, 1, 64), (128, 1, 128)])
+@pytest.mark.parametrize("q_lens,k_lens", PIECES, ids=str)
+def test_few_queries_behind_long_prefixes(Hq, Hk, D, q_lens, k_lens):
+    """Fewer units than SMs: their keys are cut into pieces, which are joined in one order."""
+    cpu, gpu = case(q_lens, k_lens, Hq, Hk, D, "bf16", fused=False, seed=40)
+    qo, ko = dev(offsets(q_lens)), dev(offsets(k_lens))
+    ws = pk.prompt_attention_workspace(gpu[0], len(q_lens), Hk)
+    out = pk.prompt_attention(*gpu, qo, ko, D ** -0.5, workspace=ws)
+    check(out, cpu, q_lens, k_lens, D ** -0.5)
+    for _ in range(3):
+        assert torch.equal(pk.prompt_attention(*gpu, qo, ko, D ** -0.5, workspace=ws), out)
+
+
+def test_pieces_whose_scores_are_far_apart():
+    """Pieces that weigh nothing next to others, keys and values that are not finite behind what a query sees."""
+    q_lens, k_lens = (70,), (6000,)
+    (q, k, v), _ = case(q_lens, k_lens, 8, 2, 128, "bf16", fused=False, seed=41)
+    q[..., 0] = 8.0
+    o = [dev(offsets(x)) for x in (q_lens, k_lens)]
+    for at in (0, 700, 3100, 5900):
+        k[:, :, 0] = 0
+        k[at:at + 50, :, 0] = 60.0
+        check(pk.prompt_attention(*[x.cuda() for x in (q, k, v)], *o, 1.0), (q, k, v), q_lens, k_lens, 1.0)
+    want = pk.prompt_attention(*[x.cuda() for x in (q, k, v)], *o, 1.0)
+    k[5999, 1] = float("nan")
+    got = pk.prompt_attention(*[x.cuda() for x in (q, k, v)], *o, 1.0)
+    assert torch.equal(got[:69], want[:69]) and got[69, 4:].isnan().all() and torch.equal(got[69, :4], want[69, :4])
+
+
+def test_captured_from_whole_units_to_pieces_and_back():
+    Tq, Tk = 3000, 9000
+    cpu, gpu = case((Tq,), (Tk,), 8, 2, 128, "bf16", fused=False, seed=42)
+    qo, ko = dev([0, 1000, 2000, 3000]), dev([0, 3000, 6000, 9000])
+    out = torch.empty(Tq, 8, 128, dtype=BF, device="cuda")
+    ws = pk.prompt_attention_workspace(gpu[0], 3, 2)
+    call = lambda: pk.prompt_attention(*gpu, qo, ko, 0.1, out=out, workspace=ws)
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for q_cuts, k_cuts in (([0, 1000, 2000, 3000], [0, 3000, 6000, 9000]), ([0, 20, 20, 21], [0, 8000, 8000, 9000]),
+                           ([0, 0, 3000, 3000], [0, 0, 3000, 3000]), ([0, 3, 6, 9], [0, 3000, 3001, 9000])):
+        qo.copy_(dev(q_cuts))
+        ko.copy_(dev(k_cuts))
+        out.fill_(9.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        n, m = np.diff(q_cuts).tolist(), np.diff(k_cuts).tolist()
+        check(out[:q_cuts[-1]], [x[:t] for x, t in zip(cpu, (q_cuts[-1], k_cuts[-1], k_cuts[-1]))], n, m, 0.1)
+        assert (out[q_cuts[-1]:] == 9).all()
