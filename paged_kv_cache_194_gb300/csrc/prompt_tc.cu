@@ -201,6 +201,9 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     }
     for (int i = tid; i < 3 * 4 * kRows; i += kThreads)  // (tellings are numbered from 1)
         reinterpret_cast<uint2*>(smem + Lt::kSay)[i] = make_uint2(0u, 0u);
+    // (nothing before reads or writes what the kernel before this one may)
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
     // the plan: sequences in order, and the row tiles before each
     int* keys = cum + 1;  // (first the keys, for the order)
     for (int b = tid; b < a.num_seqs; b += kThreads) keys[b] = span_of(a, b, blockIdx.x == 0).m;
@@ -936,8 +939,8 @@ cudaError_t launch(const PromptArgs& a, cudaStream_t stream) {
     // row tiles, times the key tiles that one may have
     const int64_t most = (static_cast<int64_t>(a.q_rows) / qpt + a.num_seqs) * a.num_kv_heads * (a.k_rows / kKeys + 1);
     const int sms = grid_size();
-    kernel<<<static_cast<unsigned>(most < sms ? most : sms), kThreads, Layout<kDim>::kSmem, stream>>>(mq, mk, mv, a);
-    const cudaError_t r = cudaGetLastError();
+    const cudaError_t r = launch_dependent(kernel, dim3(static_cast<unsigned>(most < sms ? most : sms)), dim3(kThreads),
+                                           Layout<kDim>::kSmem, stream, mq, mk, mv, a);
     if (r != cudaSuccess || !cut) return r;
     return launch_dependent(prompt_join_kernel<kDim>, dim3(2 * sms), dim3(kJoinThreads), 0, stream, a);
 }
