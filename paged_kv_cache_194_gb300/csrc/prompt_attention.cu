@@ -6,6 +6,10 @@
 // each) and walks over the keys, 64 at a time: S = Q K^T (4 x 4 each), softmax
 // statistics by the 16 threads of a row, P through shared memory, O += P V.
 //
+// Bound by its reads of shared memory beside the FMAs (a 4 x 4 square takes eight 16-byte
+// reads for 64 FMAs): 4 prompts of 2000 tokens, 32 query heads on 8 of 128, FP32, take 2.4 ms,
+// 31 TFLOP/s of what is seen; 47 of 285 to 571 tokens of 8 heads 770 us, 24 TFLOP/s.
+//
 // For F32 rows, and for BF16 ones that the tensor-core design does not take (more than
 // 128 query heads per KV head, more sequences than it plans for, no key at all).
 #include "device_common.cuh"

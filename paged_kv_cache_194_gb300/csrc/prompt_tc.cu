@@ -9,22 +9,39 @@
 // within a sequence the ones with the most keys first, so that what is left for the
 // end is short.  With fewer units than SMs the keys of units are cut into pieces, whose
 // sums a second kernel joins (us, 32 query heads on 8: 300 queries behind 8000 keys
-// 158 -> 57, 512 behind 32256 596 -> 233; pieces of fewer than eight tiles do not pay: 100
-// queries on 600 keys 18.3, in pieces of four 23.9), or, where none is longer than such a
-// piece, a unit is one row tile.  That kernel's launch costs 1 to 3 us, so calls whose rows
-// alone make a unit for every SM take an instance without it.
-// 20 warps (the last one idle):
+// 158 -> 57, 512 behind 32256 596 -> 233, 20 behind 1980 24 -> 20), or, where that would not
+// shorten a unit by three tiles, a unit is one row tile (3 x 100 queries on 600 keys: 18.6,
+// cut 23.9).  The second kernel's launch costs 2 to 3 us (8 prompts of 130: 15.3, with it
+// 17.8), so calls whose rows alone make a unit for every SM, or have few keys a sequence,
+// take an instance without it.
+//
+// What bounds it: the chain of a row tile, 3300 cycles for each key tile (clock stamps): S seen
+// and loaded 320, weights 850, written and signalled 400, taken by the issuer 330, P V and the
+// next S 1030, S seen 350.  The other row tile fills it, so the tensor core works 2060 of 3300
+// cycles.  Scores in two places would break the chain, but two row tiles' scores and outputs
+// take all of tensor memory; halves of 64 keys in turn made the score products slower (48.5
+// cycles for 64 keys, 64 for 128: their operands' way out of shared memory) and the whole too
+// (1.66 ms for the case below).  A unit costs about two more key tiles than it has.
+// Measured, 32 query heads on 8 of 128: one prompt of 16384 tokens 1.49 ms, 1.48 PFLOP/s of
+// what is seen; 16 prompts of 128 to 4096 630 us; 8 chunks of 256 to 512 behind up to 8192 194
+// us; 33 prompts of 1 to 127 20.5 us, of which a call of one row takes 7.6.
+//
+// 20 warps (the last one idle; a row's scores live in registers, 96 for each of 640 threads):
 //  * warp 16, producer: takes units, loads Q tiles, and K and V tiles into one ring
 //    (K 0, V 0, K 1, ...) by TMA;
 //  * warps 17 and 18, one thread each issues the MMAs of A and of B: S = Q K^T into the
 //    row tile's 128 score columns, then O += P V with P (BF16) read from tensor memory
-//    over those columns, then S of the next key tile.  One thread's MMAs complete in
+//    over those columns (each thread's 64 keys in the first half of its own 64 columns),
+//    then S of the next key tile.  One thread's MMAs complete in
 //    order, so "S j + 1 done" says that P V j is done too.  (One issuer for both spent
 //    4200 of 4500 cycles per pair of tiles on its own instructions);
 //  * warps 0-7 and 8-15, softmax of A and of B: two threads own a row, one its first 64
 //    keys of a tile and half of its output columns, the other the rest.  The base of a
-//    row's weights is a past maximum: it moves only when a score passes it by 8 (log2
-//    units), which rescales O in tensor memory before the next tile's products.
+//    row's weights is a past maximum, agreed on while the tile's products run: it moves
+//    only when a score passes it by 8 (log2 units), which rescales O in tensor memory
+//    before the next tile's products, or by 60 at once, before this tile's.  Statistics
+//    and sums are FP32; a weight is rounded to BF16 for its product with V, the type that
+//    the tensor core takes beside V's.
 // Tensor memory: 2 x 128 score columns, 2 x head_dim output columns.
 // Shared memory: Q 2 x 32 KB, four ring stages of 32 KB, the units' plan.
 // Every wait is bounded: an expired one sets PKV_ERRBIT_TIMEOUT and ends the CTA, whose
@@ -48,7 +65,8 @@ constexpr int kStages = 4;
 constexpr int kSlots = 2;            // units in the queue
 constexpr float kFar = 60.f;         // weights stay below 2^60
 constexpr int kSortSeqs = 256;       // up to so many sequences are taken longest first
-constexpr int kLeastPiece = 8;       // key tiles of a unit's piece, at least
+constexpr int kLeastPiece = 4;       // key tiles of a unit's piece, at least
+constexpr int kWorth = 3;            // what cutting costs, in key tiles
 constexpr int kJoinThreads = 1024;
 
 enum Bar {
@@ -249,7 +267,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                 for (int d = 16; d > 0; d >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, d);
                 if (all * a.num_kv_heads <= gridDim.x) break;
             }
-            if (part >= most) part = 0;
+            if (part + kWorth > most) part = 0;
             if (part == 0) per = 1;
         }
         int at = 0;
@@ -931,8 +949,9 @@ cudaError_t launch(const PromptArgs& a, cudaStream_t stream) {
         !encode_rows(&mk, a.k, kDim, a.k_rows, a.num_kv_heads, a.k_stride, 1, kKeys) ||
         !encode_rows(&mv, a.v, kDim, a.k_rows, a.num_kv_heads, a.v_stride, 1, kKeys))
         return cudaErrorNotSupported;
-    // Keys may be cut where the units of all rows are fewer than SMs, and one may be longer than a piece
-    const bool cut = static_cast<int64_t>(a.q_rows) / (2 * qpt) * a.num_kv_heads < grid_size() && a.k_rows > kLeastPiece * kKeys;
+    // Keys may be cut where the units of all rows are fewer than SMs, and sequences are long enough on the whole
+    const bool cut = static_cast<int64_t>(a.q_rows) / (2 * qpt) * a.num_kv_heads < grid_size() && 
+                     a.k_rows >= (kLeastPiece + kWorth) * kKeys && a.k_rows / a.num_seqs >= (kLeastPiece + kWorth) * kKeys / 2;
     const auto kernel = cut ? prompt_tc_kernel<kDim, true> : prompt_tc_kernel<kDim, false>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<kDim>::kSmem);
     if (e != cudaSuccess) return e;
