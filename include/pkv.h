@@ -557,8 +557,8 @@ pkv_status paged_quant_decode_attention(const void* q, pkv_dtype q_dtype, const 
  *              sets PKV_ERRBIT_OFFSETS and is left out.
  *   error_word device int32, optional (PKV_ERRBIT_OFFSETS, PKV_ERRBIT_TIMEOUT)
  *   workspace  prompt_attention_plan's bytes, 256-byte aligned, zeroed before its first
- *              call and after one that set PKV_ERRBIT_TIMEOUT (NULL where the plan needs
- *              none).  Stream-ordered calls of one head_dim, of any sizes, may share it.
+ *              call (NULL where the plan needs none); every call leaves its counters zero.
+ *              Stream-ordered calls of any sizes that it is large enough for may share it.
  * Offsets are read on the device: a captured call may be replayed with other ones.
  * Softmax and accumulation are binary32; with BF16 the weights are rounded to BF16
  * for their product with V.  A value of v that is not finite reaches the queries up
