@@ -7,11 +7,13 @@
 // while the softmax of one runs, the tensor core multiplies for the other.  One
 // persistent CTA per SM takes units from a common counter, long sequences' first and
 // within a sequence the ones with the most keys first, so that what is left for the
-// end is short.  With fewer units than SMs the keys of units are cut into pieces, whose
-// sums a second kernel joins (us, 32 query heads on 8: 300 queries behind 8000 keys
-// 158 -> 57, 512 behind 32256 596 -> 233, 20 behind 1980 24 -> 20), or, where that would not
-// shorten a unit by three tiles, a unit is one row tile (3 x 100 queries on 600 keys: 18.6,
-// cut 23.9).  The second kernel's launch costs 2 to 3 us (8 prompts of 130: 15.3, with it
+// end is short.  Of the units behind the last round that fills all SMs (all, where they are
+// fewer than SMs) the keys are cut into pieces, whose sums a second kernel joins (us, 32
+// query heads on 8: 300 queries behind 8000 keys 158 -> 58, 512 behind 32256 596 -> 235, 20
+// behind 1980 24 -> 20, 4 x 300 behind 7700, 160 units, 216 -> 143), unless that would not
+// shorten a unit by three tiles (3 x 100 queries on 600 keys: 18.6, cut 23.9; units are then
+// single row tiles if they are fewer than SMs), or those units fill more than half of the
+// SMs (2048 queries behind 8192, 256 units: 247, as they are).  The second kernel's launch costs 2 to 3 us (8 prompts of 130: 15.3, with it
 // 17.8), so calls whose rows alone make a unit for every SM, or have few keys a sequence,
 // take an instance without it.
 //
@@ -48,6 +50,7 @@
 // copies and products have landed by then, without its outputs.
 #include <cuda.h>
 
+#include <climits>
 #include <type_traits>
 
 #include "quant_internal.h"
@@ -67,6 +70,7 @@ constexpr float kFar = 60.f;         // weights stay below 2^60
 constexpr int kSortSeqs = 256;       // up to so many sequences are taken longest first
 constexpr int kLeastPiece = 4;       // key tiles of a unit's piece, at least
 constexpr int kWorth = 3;            // what cutting costs, in key tiles
+constexpr int kPieces = 2;           // pieces for each SM, at most
 constexpr int kJoinThreads = 1024;
 
 enum Bar {
@@ -115,6 +119,12 @@ __device__ __forceinline__ Span span_of(const PromptArgs& a, int b, bool report)
 // Pieces that a sequence's units are cut into (part: tiles of a piece, 0: not cut).
 __device__ __forceinline__ int pieces_of(int m, int part) {
     return part > 0 && m > 0 ? ((m - 1) / kKeys + part) / part : 1;
+}
+
+// Keys that a sequence's units behind its first `whole` see at most (units of `queries`, the ones that see the most first).
+__device__ __forceinline__ int keys_behind(const Span& s, int queries, int whole) {
+    const int units = (s.n + queries - 1) / queries;
+    return max(0, min(s.m, s.m - s.n + (units - whole) * queries));
 }
 
 __device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* map, int half, int head, int row, uint32_t bar) {
@@ -195,7 +205,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lt::kBar + 8 * kBars + 4);
     int* turn = reinterpret_cast<int*>(smem + Lt::kBar + 8 * kBars + 8);  // 1 while an issuer has the tensor core
     volatile Unit* queue = reinterpret_cast<volatile Unit*>(smem + Lt::kQueue);
-    int* misc = reinterpret_cast<int*>(smem + Lt::kMisc);  // {row tiles per unit, key tiles of a piece}
+    int* misc = reinterpret_cast<int*>(smem + Lt::kMisc);  // {row tiles per unit; key tiles of a piece, places of whole units, whole ones of the next}
     int* cum = reinterpret_cast<int*>(smem + Lt::kPlan);   // [B + 1] units (pieces) of one KV head before each sequence in order
     uint16_t* order = reinterpret_cast<uint16_t*>(smem + Lt::kPlan + (kPromptMaxSeqs + 1) * 4);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -236,63 +246,83 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     }
     __syncthreads();
     if (warp == 0) {
-        // Two row tiles a unit.  If that leaves SMs without one, the units' keys are cut into pieces of equal length, one
-        // for each SM; where no unit is longer than such a piece, a unit is one row tile.
-        int64_t units = 0, tiles = 0;
-        int most = 0;
-        for (int b = lane; b < a.num_seqs; b += 32) {
-            const Span s = span_of(a, b, false);
-            const int nt = s.m / kKeys + (s.m % kKeys > 0), n = s.n / (2 * qpt) + (s.n % (2 * qpt) > 0);
-            units += n;
-            tiles += static_cast<int64_t>(n) * nt;
-            if (n > 0) most = max(most, nt);
-        }
+        // Two row tiles a unit.  The units behind the last round that fills all SMs have their keys cut into pieces of
+        // equal length, if they are few enough; with fewer units than SMs and none cut, a unit is one row tile.
+        int per = 2, part = 0, whole = a.num_seqs, ahead = 0;  // places whose units are whole, whole ones of the next
+        auto count = [&](int n) { return (n + per * qpt - 1) / (per * qpt); };
+        auto items = [&](const Span& s, int r) {  // of place r
+            const int n = count(s.n), first = r < whole ? n : r == whole ? min(ahead, n) : 0;
+            return n == first ? n : first + (n - first) * pieces_of(keys_behind(s, per * qpt, first), part);
+        };
+        auto fill = [&]() {
+            int at = 0;
+            for (int r0 = 0; r0 < a.num_seqs; r0 += 32) {
+                const int n = r0 + lane < a.num_seqs ? items(span_of(a, order[r0 + lane], false), r0 + lane) : 0;
+                int incl = n;
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) {
-            units += __shfl_xor_sync(0xFFFFFFFFu, units, d);
-            tiles += __shfl_xor_sync(0xFFFFFFFFu, tiles, d);
-        }
-        most = __reduce_max_sync(0xFFFFFFFFu, most);
-        int per = 2, part = 0;
-        if (units * a.num_kv_heads < gridDim.x) {
-            int64_t all = 0;
-            if constexpr (kCut) part = static_cast<int>(max(static_cast<int64_t>(kLeastPiece), tiles * a.num_kv_heads / gridDim.x));
-            for (; part > 0 && part < most; part += 1 + part / 16) {  // no more pieces than SMs
-                all = 0;
-                for (int b = lane; b < a.num_seqs; b += 32) {
-                    const Span s = span_of(a, b, false);
-                    all += static_cast<int64_t>((s.n + 2 * qpt - 1) / (2 * qpt)) * pieces_of(s.m, part);
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int x = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+                    if (lane >= d) incl += x;
                 }
+                if (r0 + lane < a.num_seqs) cum[r0 + lane + 1] = at + incl;
+                at += __shfl_sync(0xFFFFFFFFu, incl, 31);
+            }
+            if (lane == 0) cum[0] = 0;
+            __syncwarp();
+            return at;
+        };
+        const int64_t units = static_cast<int64_t>(fill()) * a.num_kv_heads;
+        const int grid = gridDim.x;
+        if constexpr (kCut) {
+            const int64_t rounds = units / grid;
+            const int in_full = static_cast<int>(rounds * grid / a.num_kv_heads);  // units of a head in full rounds
+            const int64_t room = rounds == 0 ? grid : kPieces * grid;              // pieces that fit
+            if (2 * (units - rounds * grid) <= grid || rounds == 0) {
+                int lo = 0, hi = a.num_seqs;  // the place of unit in_full
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (cum[mid] <= in_full) lo = mid;
+                    else hi = mid;
+                }
+                whole = lo, ahead = in_full - cum[lo];
+                int most = 0;  // key tiles of the longest unit behind
+                int64_t tiles = 0;
+                for (int r = whole + lane; r < a.num_seqs; r += 32) {
+                    const Span s = span_of(a, order[r], false);
+                    const int first = r == whole ? ahead : 0, n = count(s.n) - first;
+                    const int nt = (keys_behind(s, per * qpt, first) + kKeys - 1) / kKeys;
+                    if (n > 0) most = max(most, nt), tiles += static_cast<int64_t>(n) * nt;
+                }
+                most = __reduce_max_sync(0xFFFFFFFFu, most);
 #pragma unroll
-                for (int d = 16; d > 0; d >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, d);
-                if (all * a.num_kv_heads <= gridDim.x) break;
-            }
-            if (part + kWorth > most) part = 0;
-            if (part == 0) per = 1;
-        }
-        int at = 0;
-        for (int r0 = 0; r0 < a.num_seqs; r0 += 32) {
-            int n = 0;
-            if (r0 + lane < a.num_seqs) {
-                const Span s = span_of(a, order[r0 + lane], false);
-                n = (s.n + per * qpt - 1) / (per * qpt) * pieces_of(s.m, part);
-            }
-            int incl = n;
+                for (int d = 16; d > 0; d >>= 1) tiles += __shfl_xor_sync(0xFFFFFFFFu, tiles, d);
+                part = static_cast<int>(max(static_cast<int64_t>(kLeastPiece), tiles * a.num_kv_heads / room));
+                for (; part < most; part += 1 + part / 16) {
+                    int64_t all = 0;
+                    for (int r = whole + lane; r < a.num_seqs; r += 32) {
+                        const Span s = span_of(a, order[r], false);
+                        all += items(s, r) - (r == whole ? ahead : 0);
+                    }
 #pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int x = __shfl_up_sync(0xFFFFFFFFu, incl, d);
-                if (lane >= d) incl += x;
+                    for (int d = 16; d > 0; d >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, d);
+                    if (all * a.num_kv_heads <= room) break;
+                }
+                if (part + kWorth > most) part = 0;
+                if (part == 0) whole = a.num_seqs, ahead = 0;
+                else fill();
             }
-            if (r0 + lane < a.num_seqs) cum[r0 + lane + 1] = at + incl;
-            at += __shfl_sync(0xFFFFFFFFu, incl, 31);
         }
-        if (lane == 0) cum[0] = 0, misc[0] = per, misc[1] = part;
+        if (part == 0 && units < grid) {
+            per = 1;
+            fill();
+        }
+        if (lane == 0) misc[0] = per, misc[1] = part, misc[2] = whole, misc[3] = ahead;
     }
     fence_before();
     __syncthreads();
     fence_after();
     const uint32_t tmem = *tmem_slot;
-    const int per_unit = misc[0], part = kCut ? misc[1] : 0;
+    const int per_unit = misc[0];
     auto fail = [&]() {
         *abort_flag = 1;
         if (a.err) atomicOr(a.err, PKV_ERRBIT_TIMEOUT);
@@ -336,11 +366,21 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                 }
                 const Span s = span_of(a, order[lo], false);
                 const int j = id - cum[lo] * a.num_kv_heads, head = j % a.num_kv_heads;
-                const int pieces = pieces_of(s.m, part), unit = j / a.num_kv_heads / pieces;
-                const int piece = j / a.num_kv_heads - unit * pieces, skip = piece * part * kKeys;
-                const int first = ((cum[lo + 1] - cum[lo]) / pieces - 1 - unit) * per_unit * qpt;
+                int unit = j / a.num_kv_heads, pieces = 1, piece = 0, part = 0, slot = 0;
+                if constexpr (kCut) {
+                    part = misc[1];
+                    const int ahead = lo < misc[2] ? INT_MAX : lo == misc[2] ? misc[3] : 0;  // whole units
+                    if (unit >= ahead) {
+                        pieces = pieces_of(keys_behind(s, per_unit * qpt, ahead), part);
+                        piece = (unit - ahead) % pieces;
+                        unit = ahead + (unit - ahead) / pieces;
+                        slot = id - (piece + cum[misc[2]] + misc[3]) * a.num_kv_heads;  // (counted from the first that is cut)
+                    }
+                }
+                const int skip = piece * part * kKeys;
+                const int first = ((s.n + per_unit * qpt - 1) / (per_unit * qpt) - 1 - unit) * per_unit * qpt;
                 u = Unit{s.q0 + first, s.n - first, s.k0 + skip, s.m - skip, head, s.m - s.n + first + 1 - skip, 1,
-                         piece * part, pieces > 1 ? part : INT_MAX, id - piece * a.num_kv_heads};
+                         piece * part, pieces > 1 ? part : INT_MAX, slot};
                 if (kCut && piece > 0 && Shape<kCut>(u, qpt, per_unit).nt == 0) {  // (no query sees this piece)
                     --i;
                     continue;
@@ -876,15 +916,16 @@ template <int kDim>
 __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const PromptArgs a) {
     constexpr int kQuads = kDim / 8, kMine = kQuads / 4, kAtOnce = 8 / kMine;  // of a half row, of a thread; pieces under way
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
-    const int4 tile = a.tiles[blockIdx.x];
+    const int place = blockIdx.x;
+    const int4 tile = a.tiles[place];
     const int pieces = tile.x;
     if (pieces == 0) return;
     __syncthreads();
-    if (threadIdx.x == 0) a.tiles[blockIdx.x].x = 0;  // (for the next call)
+    if (threadIdx.x == 0) a.tiles[place].x = 0;  // (for the next call)
     const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 7, quarter = threadIdx.x >> 8;
     const int gh = a.num_q_heads / a.num_kv_heads, row = 32 * (w & 3) + lane, qi = row / gh;
     if (qi >= (tile.z & 255)) return;
-    const int64_t part = static_cast<int64_t>(blockIdx.x / 2) * kSoftmaxWarps + blockIdx.x % 2 * 8 + w;
+    const int64_t part = static_cast<int64_t>(place / 2) * kSoftmaxWarps + place % 2 * 8 + w;
     const int64_t step = static_cast<int64_t>(a.num_kv_heads) * kSoftmaxWarps;  // from a piece to the next
     const float2* ml = a.part_ml + part * 32 + lane;
     const float4* po = a.part_o + (part * kQuads + quarter * kMine) * 32 + lane;
@@ -949,19 +990,21 @@ cudaError_t launch(const PromptArgs& a, cudaStream_t stream) {
         !encode_rows(&mk, a.k, kDim, a.k_rows, a.num_kv_heads, a.k_stride, 1, kKeys) ||
         !encode_rows(&mv, a.v, kDim, a.k_rows, a.num_kv_heads, a.v_stride, 1, kKeys))
         return cudaErrorNotSupported;
-    // Keys may be cut where the units of all rows are fewer than SMs, and sequences are long enough on the whole
-    const bool cut = static_cast<int64_t>(a.q_rows) / (2 * qpt) * a.num_kv_heads < grid_size() && 
-                     a.k_rows >= (kLeastPiece + kWorth) * kKeys && a.k_rows / a.num_seqs >= (kLeastPiece + kWorth) * kKeys / 2;
+    const int sms = grid_size();
+    // Keys may be cut where sequences are long enough on the whole, and the units of all rows are fewer than SMs, or a few
+    // more than fill them a few times, with prefixes long enough for units to be of like length.
+    const int64_t units = static_cast<int64_t>(a.q_rows) / (2 * qpt) * a.num_kv_heads;
+    const bool cut = a.k_rows >= (kLeastPiece + kWorth) * kKeys && a.k_rows / a.num_seqs >= (kLeastPiece + kWorth) * kKeys / 2 &&
+                     (units < sms || (units < 4 * sms && 2 * (units % sms) <= sms && a.k_rows / 3 >= a.q_rows));
     const auto kernel = cut ? prompt_tc_kernel<kDim, true> : prompt_tc_kernel<kDim, false>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<kDim>::kSmem);
     if (e != cudaSuccess) return e;
     // row tiles, times the key tiles that one may have
     const int64_t most = (static_cast<int64_t>(a.q_rows) / qpt + a.num_seqs) * a.num_kv_heads * (a.k_rows / kKeys + 1);
-    const int sms = grid_size();
     const cudaError_t r = launch_dependent(kernel, dim3(static_cast<unsigned>(most < sms ? most : sms)), dim3(kThreads),
                                            Layout<kDim>::kSmem, stream, mq, mk, mv, a);
     if (r != cudaSuccess || !cut) return r;
-    return launch_dependent(prompt_join_kernel<kDim>, dim3(2 * sms), dim3(kJoinThreads), 0, stream, a);
+    return launch_dependent(prompt_join_kernel<kDim>, dim3(2 * kPieces * sms), dim3(kJoinThreads), 0, stream, a);
 }
 
 }  // namespace
@@ -974,9 +1017,9 @@ bool prompt_tc_fits(pkv_dtype t, int num_seqs, int q_rows, int num_q_heads, int 
 }
 
 // {counter of units, of CTAs}, for each row tile that is cut what the joining kernel needs, and its pieces' (maximum, sum)
-// and O.  There are no more pieces than SMs.
+// and O.
 size_t prompt_tc_workspace(int head_dim, uint8_t* base, PromptArgs* a) {
-    const size_t pieces = static_cast<size_t>(grid_size()), parts = pieces * kSoftmaxWarps;
+    const size_t pieces = static_cast<size_t>(kPieces * grid_size()), parts = pieces * kSoftmaxWarps;
     const size_t tiles = 256, ml = tiles + (pieces * 2 * sizeof(int4) + 255) / 256 * 256, o = ml + parts * 32 * sizeof(float2);
     if (a) {
         a->counters = reinterpret_cast<int32_t*>(base);

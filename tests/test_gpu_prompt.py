@@ -405,3 +405,17 @@ def test_captured_from_whole_units_to_pieces_and_back():
         n, m = np.diff(q_cuts).tolist(), np.diff(k_cuts).tolist()
         check(out[:q_cuts[-1]], [x[:t] for x, t in zip(cpu, (q_cuts[-1], k_cuts[-1], k_cuts[-1]))], n, m, 0.1)
         assert (out[q_cuts[-1]:] == 9).all()
+
+
+@pytest.mark.parametrize("Hq,Hk,D,q_lens,k_lens", [
+    (32, 8, 64, (300,) * 4, (2300, 2300, 2301, 2150)),     # 160 units on 152 SMs: a round, and eight in pieces
+    (32, 8, 128, (1290,), (5100,)),                        # the units of one sequence: some whole, some not
+    (16, 16, 64, (130,) * 10 + (70,) * 3, (1500,) * 12 + (1000,)),
+    (32, 8, 64, (2600,), (8000,)), (5, 1, 64, (4100, 3), (12500, 1200))], ids=str)
+def test_units_behind_the_last_full_round(Hq, Hk, D, q_lens, k_lens):
+    cpu, gpu = case(q_lens, k_lens, Hq, Hk, D, "bf16", fused=False, seed=43)
+    qo, ko = dev(offsets(q_lens)), dev(offsets(k_lens))
+    ws = pk.prompt_attention_workspace(gpu[0], len(q_lens), Hk)
+    out = pk.prompt_attention(*gpu, qo, ko, D ** -0.5, workspace=ws)
+    check(out, cpu, q_lens, k_lens, D ** -0.5)
+    assert torch.equal(pk.prompt_attention(*gpu, qo, ko, D ** -0.5, workspace=ws), out)
