@@ -6,9 +6,10 @@
 // each) and walks over the keys, 64 at a time: S = Q K^T (4 x 4 each), softmax
 // statistics by the 16 threads of a row, P through shared memory, O += P V.
 //
-// Bound by its reads of shared memory beside the FMAs (a 4 x 4 square takes eight 16-byte
-// reads for 64 FMAs): 4 prompts of 2000 tokens, 32 query heads on 8 of 128, FP32, take 2.4 ms,
-// 31 TFLOP/s of what is seen; 47 of 285 to 571 tokens of 8 heads 770 us, 24 TFLOP/s.
+// Bound by its reads of shared memory (a 4 x 4 square takes eight 16-byte reads, 32 cycles of
+// the SM's port, for 64 FMAs a lane, 16 of its cycles): 4 prompts of 2000 tokens, 32 query
+// heads on 8 of 128, FP32, take 3.8 ms, 34.6 TFLOP/s of what is seen; 47 of 400 tokens of 8 heads
+// 0.69 ms, 22.4 TFLOP/s.  Eight rows a thread: 3.4 and 0.83 ms, so not taken.
 //
 // For F32 rows, and for BF16 ones that the tensor-core design does not take (more than
 // 128 query heads per KV head, more sequences than it plans for, no key at all).
@@ -72,7 +73,7 @@ __global__ void __launch_bounds__(kThreads, 2) prompt_simt_kernel(const PromptAr
             before += sums[w];
         }
         const bool here = blockIdx.x >= incl - tiles && blockIdx.x < incl;
-        if (here) mine_ = at, tile_ = blockIdx.x - (incl - tiles);
+        if (here) mine_ = at, tile_ = incl - 1 - blockIdx.x;  // (the longest first)
         found |= __syncthreads_or(here) != 0;
     }
     if (!found) return;
