@@ -706,15 +706,23 @@ def kv_read(pool, layer: int, block_tables: torch.Tensor, offsets: torch.Tensor,
     return k_out, v_out
 
 
+def _counters_zeroed(size: int, device) -> Optional[torch.Tensor]:
+    if not size:
+        return None
+    ws = torch.empty(size, dtype=torch.uint8, device=device)
+    ws[:65536].zero_()
+    return ws
+
+
 def quant_decode_workspace(pool: QuantKVPool, num_seqs: int, num_q_heads: int, max_seq_len: int) -> Optional[torch.Tensor]:
-    """A zeroed workspace for paged_quant_decode_attention calls of this size."""
+    """A workspace (its counters zeroed) for paged_quant_decode_attention calls of this size."""
     if not _here(pool, None):
         with _on(pool, None):
             return quant_decode_workspace(pool, num_seqs, num_q_heads, max_seq_len)
     ws = ctypes.c_size_t()
     _check(lib().paged_quant_decode_plan(pool.handle, num_seqs, num_q_heads, max_seq_len, ctypes.byref(ws)),
            "paged_quant_decode_plan")
-    return torch.zeros(ws.value, dtype=torch.uint8, device=pool.device) if ws.value else None
+    return _counters_zeroed(ws.value, pool.device)
 
 
 def paged_quant_decode_attention(q: torch.Tensor, pool: QuantKVPool, layer: int, block_tables: torch.Tensor,
@@ -737,7 +745,7 @@ def paged_quant_decode_attention(q: torch.Tensor, pool: QuantKVPool, layer: int,
 
 
 def prompt_attention_workspace(q: torch.Tensor, num_seqs: int, num_kv_heads: int) -> Optional[torch.Tensor]:
-    """A zeroed workspace for prompt_attention calls of this size."""
+    """A workspace (its counters zeroed) for prompt_attention calls of this size."""
     index = q.device.index if q.is_cuda else -1
     if index >= 0 and index != _current_device():
         with torch.cuda.device(index):
@@ -747,7 +755,7 @@ def prompt_attention_workspace(q: torch.Tensor, num_seqs: int, num_kv_heads: int
     ws = ctypes.c_size_t()
     _check(lib().prompt_attention_plan(num_seqs, q.shape[0], q.shape[1], num_kv_heads, q.shape[2], _dtype_code(q.dtype),
                                        ctypes.byref(ws)), "prompt_attention_plan")
-    return torch.zeros(ws.value, dtype=torch.uint8, device=q.device) if ws.value else None
+    return _counters_zeroed(ws.value, q.device)
 
 
 def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offsets: torch.Tensor, k_offsets: torch.Tensor,

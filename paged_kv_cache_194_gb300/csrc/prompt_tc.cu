@@ -1018,6 +1018,7 @@ bool prompt_tc_fits(pkv_dtype t, int num_seqs, int q_rows, int num_q_heads, int 
 
 // {counter of units, of CTAs}, for each row tile that is cut what the joining kernel needs, and its pieces' (maximum, sum)
 // and O.
+// (The counters and what the joining kernel needs, 64 bytes an SM, are the part that calls leave zero: the first 64 KB.)
 size_t prompt_tc_workspace(int head_dim, uint8_t* base, PromptArgs* a) {
     const size_t pieces = static_cast<size_t>(kPieces * grid_size()), parts = pieces * kSoftmaxWarps;
     const size_t tiles = 256, ml = tiles + (pieces * 2 * sizeof(int4) + 255) / 256 * 256, o = ml + parts * 32 * sizeof(float2);
