@@ -164,7 +164,7 @@ pkv_status paged_quant_decode_plan(const kv_quant_pool* p, int32_t num_seqs, int
                                    size_t* ws_out) {
     if (!p || num_seqs < 0 || num_q_heads < 1 || max_seq_len < 0) return PKV_ERR_INVALID_ARG;
     if (num_q_heads % p->d.num_kv_heads != 0) return PKV_ERR_INVALID_ARG;
-    if (num_seqs > 65535 || num_q_heads > 65535) return PKV_ERR_UNSUPPORTED;
+    if (num_seqs > 65535 || num_q_heads > 65535 || max_seq_len > INT32_MAX - 63) return PKV_ERR_UNSUPPORTED;  // (tiles of 64)
     if (ws_out) *ws_out = quant_decode_workspace(num_q_heads, p->d.num_kv_heads, p->d.head_dim, nullptr, nullptr);
     return PKV_OK;
 }

@@ -214,3 +214,29 @@ def test_binding_checks_shapes_types_and_devices():
             if name in k:
                 with pytest.raises((TypeError, ValueError, AttributeError, RuntimeError, ctypes.ArgumentError)):
                     f(**{**k, name: bad})
+
+
+def test_lengths_past_32_bits_of_tiles_are_refused(pool):
+    ws = ctypes.c_size_t()
+    h = pool()
+    assert pk.lib().paged_quant_decode_plan(h, 1, 8, 2 ** 31 - 64, ctypes.byref(ws)) == 0
+    for n in (2 ** 31 - 63, 2 ** 31 - 1):
+        assert pk.lib().paged_quant_decode_plan(h, 1, 8, n, ctypes.byref(ws)) == 2
+
+
+def test_workspaces_grow_with_what_they_serve(pool):
+    """A workspace of a larger call serves the smaller ones: sizes depend on neither the batch nor the lengths."""
+    ws, h = ctypes.c_size_t(), pool()
+    sizes = set()
+    for B, n in ((1, 1), (4, 100), (65535, 2 ** 31 - 64)):
+        assert pk.lib().paged_quant_decode_plan(h, B, 8, n, ctypes.byref(ws)) == 0
+        sizes.add(ws.value)
+    assert len(sizes) == 1 and sizes.pop() > 65536
+    prompts = set()
+    for B, T in ((1, 1), (2048, 2048), (7, 100000)):
+        assert pk.lib().prompt_attention_plan(B, T, 8, 2, 128, 1, ctypes.byref(ws)) == 0
+        prompts.add(ws.value)
+    assert len(prompts) == 1 and prompts.pop() > 65536
+    for B, T, Hq, Hk, dt in ((2049, 5000, 8, 2, 1), (2, 9, 258, 2, 1), (2, 9, 8, 2, 0)):  # the CUDA cores' design needs none
+        assert pk.lib().prompt_attention_plan(B, T, Hq, Hk, 128, dt, ctypes.byref(ws)) == 0
+        assert ws.value == 0
