@@ -34,8 +34,8 @@
 // units are a CTA's own each.
 //
 // Measured with 32 query heads on 8 of 128, rows read from HBM at up to 6.79 TB/s: 55
-// sequences of 8192 tokens of 8 bits 172 us (5.5 TB/s); two of 130 thousand of 4 bits 65 us
-// (4.4 TB/s); 64 of 128 to 4096 of 4 bits 44.5 us (3.3 TB/s); four of up to 512 8.4 us.  Of 4-bit
+// sequences of 8192 tokens of 8 bits 162 us (5.9 TB/s); two of 130 thousand of 4 bits 59.5 us
+// (4.8 TB/s); 64 of 128 to 4096 of 4 bits 42.4 us (3.5 TB/s); four of up to 512 8.0 us.  Of 4-bit
 // rows the work on codes bounds it as much as memory does (250 instructions for 16 tokens of
 // a warp, issued in 48 % of the cycles by the three warps of a scheduler that registers leave
 // room for); a call's start, until rows flow, takes 3 to 4 us, and writing and joining pieces
@@ -172,6 +172,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kBits, kDim, kNT)) quant
     auto so = [&](int w) { return reinterpret_cast<float (*)[kPitch]>(dynamic + w * kRing + kEarly * St::kBytes); };
     __shared__ float sm[kWarps][kCols], sl[kWarps][kCols], sz[kWarps][kCols];
     __shared__ long long scan[kWarps];
+    __shared__ int lengths[kWarps];  // 1: a sequence of more than 8 tiles, 2: of more than 16
     __shared__ int last_flag[2], found;
     __shared__ long long found_at;
     __shared__ Seg split[2];  // this CTA's pieces of units that others share: at its range's start, and at its end
@@ -207,30 +208,37 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kBits, kDim, kNT)) quant
     // With no more units than CTAs, and none long, every unit is a CTA's of its own: joining its pieces would take longer
     // than they save.  (us whole / cut, 32 heads: 8.2 / 10.2 for one sequence of 512 tokens, 11.6 / 10.5 for one of 1024;
     // 12.3 / 20.6 and 17.9 / 24.9 for fifty.)
-    const bool long8 = __syncthreads_or(most > 8), long16 = __syncthreads_or(most > 16);
+    const bool warp8 = __any_sync(kAll, most > 8), warp16 = __any_sync(kAll, most > 16);
     long long incl = mine | static_cast<long long>(some) << 40;  // (both sums at once: costs stay below 2^40)
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
         const long long x = __shfl_up_sync(kAll, incl, d);
         if (lane >= d) incl += x;
     }
-    if (lane == 31) scan[warp] = incl;
+    if (lane == 31) scan[warp] = incl, lengths[warp] = warp8 + 2 * warp16;
     __syncthreads();
     long long sum = 0;
+    int longer = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
         if (w < warp) incl += scan[w];
         sum += scan[w];
+        longer |= lengths[w];
     }
     const long long units = (sum >> 40) * per_seq;
-    const bool apart = units <= gridDim.x && !(4 * units >= gridDim.x ? long16 : long8);
+    const bool apart = units <= gridDim.x && !(4 * units >= gridDim.x ? longer & 2 : longer & 1);
     auto cost = [&](int nt) { return apart ? 1 : nt + kUnitCost; };
     auto pick = [&](long long x) { return (apart ? x >> 40 : x & ((1ll << 40) - 1)) * per_seq; };
     const long long total = pick(sum), before = pick(incl) - (apart ? some : mine) * per_seq;
     const long long P = total < static_cast<long long>(gridDim.x) ? total : static_cast<long long>(gridDim.x);
     const long long c = blockIdx.x;
     if (c >= P) return;
-    const long long g0 = c * total / P, g1 = (c + 1) * total / P;
+    // (products in 32 bits where they will do: a 64-bit division is a call, around which the compiler keeps its registers
+    // otherwise: 65.8 us instead of 59.5 for two sequences of 130 thousand tokens, with two barriers fewer before it)
+    auto share = [&](long long i) {
+        return total <= (1 << 21) ? static_cast<long long>(static_cast<uint32_t>(i * total) / static_cast<uint32_t>(P)) : i * total / P;
+    };
+    const long long g0 = share(c), g1 = share(c + 1);
     if (g0 >= before && g0 < pick(incl)) {
         long long at = before;
         int b = tid * run;
