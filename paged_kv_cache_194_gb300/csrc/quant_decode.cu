@@ -35,7 +35,7 @@
 //
 // Measured with 32 query heads on 8 of 128, rows read from HBM at up to 6.79 TB/s: 55
 // sequences of 8192 tokens of 8 bits 162 us (5.9 TB/s); two of 130 thousand of 4 bits 59.5 us
-// (4.8 TB/s); 64 of 128 to 4096 of 4 bits 42.4 us (3.5 TB/s); four of up to 512 8.0 us.  Of 4-bit
+// (4.8 TB/s); 64 of 128 to 4096 of 4 bits 41.7 us (3.5 TB/s); four of up to 512 8.0 us.  Of 4-bit
 // rows the work on codes bounds it as much as memory does (250 instructions for 16 tokens of
 // a warp, issued in 48 % of the cycles by the three warps of a scheduler that registers leave
 // room for); a call's start, until rows flow, takes 3 to 4 us, and writing and joining pieces
@@ -50,7 +50,7 @@ namespace {
 
 constexpr int kThreads = 128, kWarps = 4;
 constexpr int kTile = 64, kStep = 16;
-constexpr int kUnitCost = 4;
+constexpr int kUnitCost = 6;  // (us for 64 sequences of 128 to 4096 tokens with 4, 6, 10: 42.5, 41.6, 42.5; 256 of 256 to 512: 45.2, 44.9, 44.4)
 constexpr int kMaxCtas = 1024;
 // CTAs per SM, and steps whose rows are under way in a warp (pair: taken two at a time).  HBM answers after 2.5 to 3 us
 // under load, so an SM wants 130 to 150 KB on their way.
