@@ -456,3 +456,16 @@ def test_append_one_row_to_many_slots(bits, inp):
     expect_append(want, 0, x[0].expand(5, 3, 64), x[1].expand(5, 3, 64), slots, 16, bits)
     for got, w in zip(raw(pool), want):
         assert torch.equal(got, w)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("Hq,Hk,D", [(8, 2, 128), (16, 2, 64), (32, 2, 128), (5, 1, 64), (40, 2, 128)])
+def test_attention_many_short_sequences(bits, Hq, Hk, D):
+    """Units that are a warp's own: empty sequences between, one token, whole and cut steps and tiles, one longer unit."""
+    g = torch.Generator().manual_seed(23)
+    lens = torch.randint(0, 100, (1200 // Hk,), generator=g).tolist()
+    lens[:12] = [0, 1, 15, 16, 17, 31, 32, 33, 63, 64, 65, 130]
+    lens[-3:] = [0, 97, 0]
+    b = Quantised(lens, Hq, Hk, D, 16, bits, seed=24)
+    first = b.check()
+    assert b.pool.errors() == 0 and torch.equal(b.run(), first)
