@@ -35,7 +35,7 @@
 //
 // Measured with 32 query heads on 8 of 128, rows read from HBM at up to 6.79 TB/s: 55
 // sequences of 8192 tokens of 8 bits 162 us (5.9 TB/s); two of 130 thousand of 4 bits 59.5 us
-// (4.8 TB/s); 64 of 128 to 4096 of 4 bits 42.9 us (3.4 TB/s); four of up to 512 8.0 us.  Of 4-bit
+// (4.8 TB/s); 64 of 128 to 4096 of 4 bits 41.8 us (3.5 TB/s); four of up to 512 8.0 us.  Of 4-bit
 // rows the work on codes bounds it as much as memory does (250 instructions for 16 tokens of
 // a warp, issued in 48 % of the cycles by the three warps of a scheduler that registers leave
 // room for); a call's start, until rows flow, takes 3 to 4 us, and writing and joining pieces
@@ -804,8 +804,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kBits, kDim, kNT)) quant
             }
         }
     };
-    if (alone) work(std::true_type{});
-    else work(std::false_type{});
+    if (!alone) work(std::false_type{});
+    else work(std::true_type{});
 }
 
 int columns(int gh) { return gh <= 8 ? 8 : 16; }
