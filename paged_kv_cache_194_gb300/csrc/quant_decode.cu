@@ -34,10 +34,10 @@
 // units are a CTA's own each, many short ones a warp's.
 //
 // Measured with 32 query heads on 8 of 128, rows read from HBM at up to 6.79 TB/s: 55
-// sequences of 8192 tokens of 8 bits 162 us (5.9 TB/s); two of 130 thousand of 4 bits 59.5 us
+// sequences of 8192 tokens of 8 bits 162 us (5.9 TB/s); two of 130 thousand of 4 bits 59 us
 // (4.8 TB/s); 64 of 128 to 4096 of 4 bits 41.8 us (3.5 TB/s); four of up to 512 8.0 us.  Of 4-bit
 // rows the work on codes bounds it as much as memory does (250 instructions for 16 tokens of
-// a warp, issued in 48 % of the cycles by the three warps of a scheduler that registers leave
+// a warp, issued in 51 % of the cycles by the three warps of a scheduler that registers leave
 // room for); a call's start, until rows flow, takes 3 to 4 us, and writing and joining pieces
 // at its end 4 to 5.
 #include <type_traits>
