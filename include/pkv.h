@@ -526,9 +526,10 @@ pkv_status kv_quant_read(const kv_quant_pool* pool, int32_t layer, const int32_t
  * of query heads per KV head.  A row that reads as NaN makes the queries that see
  * it NaN; rows behind a sequence's end are not looked at.
  *   workspace  at least paged_quant_decode_plan's bytes, 256-byte aligned, the first
- *              64 KB (or all) zeroed before its first call; every call leaves its
- *              counters, which lie there, zero, for calls of any size that it is large
- *              enough for.  Calls that share a workspace are stream-ordered.
+ *              64 KB (or all) zeroed before its first call; every call leaves them zero,
+ *              and writes what it likes behind them.  Stream-ordered calls of any
+ *              size that it is large enough for may share it, prompt_attention's among
+ *              them; those of other entry points may not.
  */
 pkv_status paged_quant_decode_plan(const kv_quant_pool* pool, int32_t num_seqs, int32_t num_q_heads, int32_t max_seq_len,
                                    size_t* workspace_bytes_out);
@@ -558,8 +559,10 @@ pkv_status paged_quant_decode_attention(const void* q, pkv_dtype q_dtype, const 
  *   error_word device int32, optional (PKV_ERRBIT_OFFSETS, PKV_ERRBIT_TIMEOUT)
  *   workspace  prompt_attention_plan's bytes, 256-byte aligned, the first 64 KB (or all)
  *              zeroed before its first call (NULL where the plan needs none); every call
- *              leaves its counters, which lie there, zero.  Stream-ordered calls of any
- *              sizes that it is large enough for may share it.
+ *              leaves them zero, and writes what it likes behind them.  Stream-ordered
+ *              calls of any sizes that it is large enough for may share it,
+ *              paged_quant_decode_attention's among them; those of other entry points
+ *              may not.
  * Offsets are read on the device: a captured call may be replayed with other ones.
  * Softmax and accumulation are binary32; with BF16 the weights are rounded to BF16
  * for their product with V.  A value of v that is not finite reaches the queries up

@@ -715,7 +715,8 @@ def _counters_zeroed(size: int, device) -> Optional[torch.Tensor]:
 
 
 def quant_decode_workspace(pool: QuantKVPool, num_seqs: int, num_q_heads: int, max_seq_len: int) -> Optional[torch.Tensor]:
-    """A workspace (its counters zeroed) for paged_quant_decode_attention calls of this size."""
+    """A workspace (its counters zeroed) for paged_quant_decode_attention calls of this size; stream-ordered calls of it
+    and of prompt_attention may share one that is large enough for each."""
     if not _here(pool, None):
         with _on(pool, None):
             return quant_decode_workspace(pool, num_seqs, num_q_heads, max_seq_len)
@@ -745,7 +746,8 @@ def paged_quant_decode_attention(q: torch.Tensor, pool: QuantKVPool, layer: int,
 
 
 def prompt_attention_workspace(q: torch.Tensor, num_seqs: int, num_kv_heads: int) -> Optional[torch.Tensor]:
-    """A workspace (its counters zeroed) for prompt_attention calls of this size."""
+    """A workspace (its counters zeroed) for prompt_attention calls of this size; stream-ordered calls of it and of
+    paged_quant_decode_attention may share one that is large enough for each."""
     index = q.device.index if q.is_cuda else -1
     if index >= 0 and index != _current_device():
         with torch.cuda.device(index):

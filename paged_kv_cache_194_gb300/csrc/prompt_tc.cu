@@ -921,7 +921,7 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const PromptA
     const int pieces = tile.x;
     if (pieces == 0) return;
     __syncthreads();
-    if (threadIdx.x == 0) a.tiles[place].x = 0;  // (for the next call)
+    if (threadIdx.x == 0) a.tiles[place] = make_int4(0, 0, 0, 0);  // (for the next call, of either operator)
     const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 7, quarter = threadIdx.x >> 8;
     const int gh = a.num_q_heads / a.num_kv_heads, row = 32 * (w & 3) + lane, qi = row / gh;
     if (qi >= (tile.z & 255)) return;
@@ -980,7 +980,12 @@ bool encode_rows(CUtensorMap* map, const void* base, int dim, int64_t rows, int 
     return encode_map(map, 2, 4, base, dims, strides, box);
 }
 
-int grid_size() { return num_sms() > 0 ? num_sms() : 148; }
+constexpr int kMostSms = 1000;  // whose row tiles' list has room among the workspace's zeros
+static_assert(256 + kPieces * kMostSms * 2 * sizeof(int4) <= kWorkspaceZeros);
+int grid_size() {
+    const int n = num_sms();
+    return n < 1 ? 148 : n < kMostSms ? n : kMostSms;
+}
 
 template <int kDim>
 cudaError_t launch(const PromptArgs& a, cudaStream_t stream) {
@@ -1018,10 +1023,10 @@ bool prompt_tc_fits(pkv_dtype t, int num_seqs, int q_rows, int num_q_heads, int 
 
 // {counter of units, of CTAs}, for each row tile that is cut what the joining kernel needs, and its pieces' (maximum, sum)
 // and O.
-// (The counters and what the joining kernel needs, 64 bytes an SM, are the part that calls leave zero: the first 64 KB.)
+// (The counters and what the joining kernel needs, 64 bytes an SM, are the part that calls leave zero.)
 size_t prompt_tc_workspace(int head_dim, uint8_t* base, PromptArgs* a) {
     const size_t pieces = static_cast<size_t>(kPieces * grid_size()), parts = pieces * kSoftmaxWarps;
-    const size_t tiles = 256, ml = tiles + (pieces * 2 * sizeof(int4) + 255) / 256 * 256, o = ml + parts * 32 * sizeof(float2);
+    const size_t tiles = 256, ml = kWorkspaceZeros, o = ml + parts * 32 * sizeof(float2);
     if (a) {
         a->counters = reinterpret_cast<int32_t*>(base);
         a->tiles = reinterpret_cast<int4*>(base + tiles);

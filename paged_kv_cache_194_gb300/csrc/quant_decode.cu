@@ -816,7 +816,8 @@ size_t quant_decode_workspace(int num_q_heads, int num_kv_heads, int head_dim, u
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     const int cols = columns(num_q_heads / num_kv_heads);
     // (counters at one place for calls of all sizes: they are what a call leaves for the next)
-    const size_t counters = up(kMaxCtas * sizeof(int32_t));
+    constexpr size_t counters = kWorkspaceZeros;
+    static_assert(kMaxCtas * sizeof(int32_t) <= counters);
     const size_t ml = up(static_cast<size_t>(kMaxCtas) * 2 * cols * 2 * sizeof(float));
     if (a) {
         a->counters = reinterpret_cast<int32_t*>(base);

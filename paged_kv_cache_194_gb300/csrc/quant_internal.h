@@ -16,6 +16,10 @@ struct kv_quant_pool {
 
 namespace pkv {
 
+// What the operators here leave zero for the next call on a workspace lies in its first bytes, and nothing else does, so
+// that calls of all of them may share one.
+constexpr size_t kWorkspaceZeros = 65536;
+
 // A TMA descriptor (128-byte swizzle, no fill) of a tensor of `bytes`-byte
 // elements; false where the driver has none.  strides: of dimensions 1 .. rank - 1.
 bool encode_map(CUtensorMap* map, int elem_bytes, int rank, const void* base, const uint64_t* dims,
