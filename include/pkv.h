@@ -555,7 +555,8 @@ pkv_status paged_quant_decode_attention(const void* q, pkv_dtype q_dtype, const 
  *              inputs.  Rows of no sequence are left as they were.
  *   q_offsets, k_offsets   device int32 [num_seqs + 1], ascending in [0, q_rows] and
  *              [0, k_rows]; may be the same array.  A sequence whose offsets are not
- *              sets PKV_ERRBIT_OFFSETS and is left out.
+ *              sets PKV_ERRBIT_OFFSETS and is left out.  Where the others overlap, and
+ *              have more than q_rows queries together, they may be left out, too.
  *   error_word device int32, optional (PKV_ERRBIT_OFFSETS, PKV_ERRBIT_TIMEOUT)
  *   workspace  prompt_attention_plan's bytes, 256-byte aligned, the first 64 KB (or all)
  *              zeroed before its first call (NULL where the plan needs none); every call

@@ -249,9 +249,10 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
         // Two row tiles a unit.  The units behind the last round that fills all SMs have their keys cut into pieces of
         // equal length, if they are few enough; with fewer units than SMs and none cut, a unit is one row tile.
         int per = 2, part = 0, whole = a.num_seqs, ahead = 0;  // places whose units are whole, whole ones of the next
+        bool sound = true;  // no more queries than there are rows: units are counted in 32 bits
         auto count = [&](int n) { return (n + per * qpt - 1) / (per * qpt); };
         auto items = [&](const Span& s, int r) {  // of place r
-            const int n = count(s.n), first = r < whole ? n : r == whole ? min(ahead, n) : 0;
+            const int n = sound ? count(s.n) : 0, first = r < whole ? n : r == whole ? min(ahead, n) : 0;
             return n == first ? n : first + (n - first) * pieces_of(keys_behind(s, per * qpt, first), part);
         };
         auto fill = [&]() {
@@ -271,6 +272,12 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             __syncwarp();
             return at;
         };
+        // Sequences of offsets that descend may overlap, so that their queries are more than the rows: none is taken then.
+        int64_t queries = 0;
+        for (int r = lane; r < a.num_seqs; r += 32) queries += span_of(a, r, false).n;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) queries += __shfl_xor_sync(0xFFFFFFFFu, queries, d);
+        sound = queries <= a.q_rows;
         const int64_t units = static_cast<int64_t>(fill()) * a.num_kv_heads;
         const int grid = gridDim.x;
         if constexpr (kCut) {

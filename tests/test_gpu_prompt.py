@@ -419,3 +419,21 @@ def test_units_behind_the_last_full_round(Hq, Hk, D, q_lens, k_lens):
     out = pk.prompt_attention(*gpu, qo, ko, D ** -0.5, workspace=ws)
     check(out, cpu, q_lens, k_lens, D ** -0.5)
     assert torch.equal(pk.prompt_attention(*gpu, qo, ko, D ** -0.5, workspace=ws), out)
+
+
+def test_sequences_that_overlap_are_not_counted_past_their_rows():
+    """Offsets that go back and forth: half of the sequences ascend and are the same rows, more queries together than
+    there are rows.  Their units would not be countable in 32 bits in a large call: none is taken."""
+    T, B = 64, 300
+    cpu, gpu = case((T,), (T,), 128, 1, 64, "bf16", fused=False, seed=44)
+    o = dev([0, T] * (B // 2) + [0])
+    err = torch.zeros(1, dtype=I32, device="cuda")
+    out = torch.full_like(gpu[0], 77.0)
+    ws = pk.prompt_attention_workspace(gpu[0], B, 1)
+    pk.prompt_attention(*gpu, o, o, 0.1, out=out, error_word=err, workspace=ws)
+    assert int(err) == pk.ERRBIT_OFFSETS and (out == 77).all() and not ws[:65536].any()
+    o = dev([0, T] + [T] * (B - 1))  # and right offsets again
+    err.zero_()
+    pk.prompt_attention(*gpu, o, o, 0.1, out=out, error_word=err, workspace=ws)
+    check(out, cpu, (T,), (T,), 0.1)
+    assert int(err) == 0
