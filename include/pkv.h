@@ -557,7 +557,8 @@ pkv_status paged_quant_decode_attention(const void* q, pkv_dtype q_dtype, const 
  *              [0, k_rows]; may be the same array.  A sequence whose offsets are not
  *              sets PKV_ERRBIT_OFFSETS and is left out.  Where the others overlap, and
  *              have more than q_rows queries together, they may be left out, too.
- *   error_word device int32, optional (PKV_ERRBIT_OFFSETS, PKV_ERRBIT_TIMEOUT)
+ *   error_word device int32, optional (PKV_ERRBIT_OFFSETS, PKV_ERRBIT_TIMEOUT; rows that
+ *              an expired wait costs are NaN, with or without it)
  *   workspace  prompt_attention_plan's bytes, 256-byte aligned, the first 64 KB (or all)
  *              zeroed before its first call (NULL where the plan needs none); every call
  *              leaves them zero, and writes what it likes behind them.  Stream-ordered
@@ -653,7 +654,9 @@ pkv_status kv_bm_check(const pkv_block_manager* bm);
  * the output rows of the units the stopped CTAs took part in are unwritten.
  * paged_prefix_decode_attention's sharing design takes it for a CTA's first wait
  * for a K tile: the rows that a stopped CTA took part in become NaN, and the
- * workspace needs no clearing.
+ * workspace needs no clearing.  So does prompt_attention's tcgen05 design, with
+ * the rows of the units that a stopped CTA had in hand (and of all that are left
+ * when every CTA has stopped).
  */
 void pkv_set_first_wait_limit_for_testing(int32_t polls, int32_t cta);
 

@@ -366,7 +366,7 @@ def paged_decode_attention_static_ws(q: torch.Tensor, pool: KVPool, layer: int, 
 
 
 def set_first_wait_limit_for_testing(polls: int, cta: int = -1) -> None:
-    """Make the tensor-core decode design's first stage wait give up after
+    """Make the first stage wait of the tensor-core designs (decode, shared prefixes, prompts) give up after
     `polls` polls in CTA `cta` (every CTA when negative) for later calls from
     this thread; polls < 0 restores the normal bound (test hook)."""
     lib().pkv_set_first_wait_limit_for_testing(int(polls), int(cta))
@@ -769,7 +769,7 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offset
     or float32, possibly slices of one projection's rows); its queries are the
     last of its positions.  Returns [Tq, Hq, D]; rows of no sequence keep what
     `out` held.  error_word: int32 [1], gets ERRBIT_OFFSETS where offsets do not
-    ascend within the rows."""
+    ascend within the rows, ERRBIT_TIMEOUT where a wait expired (whose rows are NaN)."""
     index = q.device.index if q.is_cuda else -1
     if stream is not None or (index >= 0 and index != _current_device()):
         with _on_device(q.device, stream, "q"):

@@ -243,6 +243,11 @@ int dtype_bytes(pkv_dtype t) {
     return 0;
 }
 
+void first_wait_limit(int32_t* polls, int32_t* cta) {
+    *polls = g_test_wait_polls;
+    *cta = g_test_wait_cta;
+}
+
 size_t workspace_counter_bytes(int num_seqs, int num_kv_heads) { return counters_bytes(num_seqs, num_kv_heads); }
 
 int num_sms() {

@@ -35,6 +35,8 @@ constexpr int kTileTokens = 64;  // tokens one decode CTA stages per pipeline st
 int dtype_bytes(pkv_dtype t);
 int num_sms();  // SM count of the current device (cached)
 void set_last_error(cudaError_t e);
+// What the calling thread set by pkv_set_first_wait_limit_for_testing: polls (< 0: off) and the CTA (< 0: every one).
+void first_wait_limit(int32_t* polls, int32_t* cta);
 // Bytes at the front of a decode workspace that hold the per-(sequence, KV
 // head) piece counters (int32 [num_seqs][num_kv_heads], rounded up to 256).
 size_t workspace_counter_bytes(int num_seqs, int num_kv_heads);

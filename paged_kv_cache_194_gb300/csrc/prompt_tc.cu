@@ -47,7 +47,7 @@
 // Tensor memory: 2 x 128 score columns, 2 x head_dim output columns.
 // Shared memory: Q 2 x 32 KB, four ring stages of 32 KB, the units' plan.
 // Every wait is bounded: an expired one sets PKV_ERRBIT_TIMEOUT and ends the CTA, whose
-// copies and products have landed by then, without its outputs.
+// copies and products have landed by then; the rows of the units that it had are NaN.
 #include <cuda.h>
 
 #include <climits>
@@ -72,6 +72,19 @@ constexpr int kLeastPiece = 4;       // key tiles of a unit's piece, at least
 constexpr int kWorth = 3;            // what cutting costs, in key tiles
 constexpr int kPieces = 2;           // pieces for each SM, at most
 constexpr int kJoinThreads = 1024;
+
+// Words of the plan and, for a CTA that gives up, of what it had in hand.
+enum Misc {
+    kPerUnit = 0,       // row tiles of a unit
+    kPart = 1,          // key tiles of a piece (0: nothing is cut)
+    kWhole = 2,         // places of the list whose units are whole
+    kAhead = 3,         // whole units of the next place
+    kUntaken = 4,       // the first unit that no CTA took (for the last CTA to finish)
+    kTaken = 5,         // units that this CTA took
+    kHeld = 6,          // the last eight of them
+    kStopped = kHeld + 8,  // for each softmax warp, which of the CTA's units it gave up at
+    kMiscWords = kStopped + kSoftmaxWarps
+};
 
 enum Bar {
     kQFull = 0, kQFree = 2, kFull = 4, kFree = kFull + kStages, kSFull = kFree + kStages, kPFull = kSFull + 2,
@@ -98,7 +111,7 @@ struct Layout {
     static constexpr int kTile = kHalves * kHalf;  // bytes of a Q, K or V tile
     static constexpr int kQ = 0, kRing = 2 * kTile, kBar = kRing + kStages * kTile;
     static constexpr int kQueue = kBar + 8 * kBars + 16, kMisc = kQueue + kSlots * static_cast<int>(sizeof(Unit));
-    static constexpr int kSay = (kMisc + 64 + 127) / 128 * 128;  // what a row's two threads tell each other
+    static constexpr int kSay = (kMisc + 4 * kMiscWords + 127) / 128 * 128;  // what a row's two threads tell each other
     static constexpr int kPlan = kSay + 3 * 4 * kRows * 8;
     static constexpr int kSmem = kPlan + (kPromptMaxSeqs + 1) * 4 + kPromptMaxSeqs * 2 + 1024;
     static_assert(kSmem <= 232448, "shared memory per CTA");
@@ -205,7 +218,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lt::kBar + 8 * kBars + 4);
     int* turn = reinterpret_cast<int*>(smem + Lt::kBar + 8 * kBars + 8);  // 1 while an issuer has the tensor core
     volatile Unit* queue = reinterpret_cast<volatile Unit*>(smem + Lt::kQueue);
-    int* misc = reinterpret_cast<int*>(smem + Lt::kMisc);  // {row tiles per unit; key tiles of a piece, places of whole units, whole ones of the next}
+    int* misc = reinterpret_cast<int*>(smem + Lt::kMisc);
     int* cum = reinterpret_cast<int*>(smem + Lt::kPlan);   // [B + 1] units (pieces) of one KV head before each sequence in order
     uint16_t* order = reinterpret_cast<uint16_t*>(smem + Lt::kPlan + (kPromptMaxSeqs + 1) * 4);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -323,20 +336,20 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             per = 1;
             fill();
         }
-        if (lane == 0) misc[0] = per, misc[1] = part, misc[2] = whole, misc[3] = ahead;
+        if (lane == 0) misc[kPerUnit] = per, misc[kPart] = part, misc[kWhole] = whole, misc[kAhead] = ahead, misc[kUntaken] = INT_MAX;
     }
     fence_before();
     __syncthreads();
     fence_after();
     const uint32_t tmem = *tmem_slot;
-    const int per_unit = misc[0];
+    const int per_unit = misc[kPerUnit];
     auto fail = [&]() {
         *abort_flag = 1;
         if (a.err) atomicOr(a.err, PKV_ERRBIT_TIMEOUT);
     };
     // a bounded wait that ends early when another role has given up
-    auto wait = [&](int i, int parity) -> bool {
-        for (uint32_t k = 0; k < kSpin; ++k) {
+    auto wait = [&](int i, int parity, uint32_t polls = kSpin) -> bool {
+        for (uint32_t k = 0; k < polls; ++k) {
             uint32_t ok;
             asm volatile(
                 "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
@@ -352,43 +365,48 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
         const volatile Unit& s = queue[i % kSlots];
         return Unit{s.q0, s.n, s.k0, s.m, s.head, s.seen, s.more, 0, kCut ? s.len : 0, 0};
     };
+    const int total = cum[a.num_seqs] * a.num_kv_heads;
+    auto unit_of = [&](int id) -> Unit {  // unit `id` of the list
+        int lo = 0, hi = a.num_seqs;  // the last place whose first unit is at or before id
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (static_cast<int64_t>(cum[mid]) * a.num_kv_heads <= id) lo = mid;
+            else hi = mid;
+        }
+        const Span s = span_of(a, order[lo], false);
+        const int j = id - cum[lo] * a.num_kv_heads, head = j % a.num_kv_heads;
+        int unit = j / a.num_kv_heads, pieces = 1, piece = 0, part = 0, slot = 0;
+        if constexpr (kCut) {
+            part = misc[kPart];
+            const int ahead = lo < misc[kWhole] ? INT_MAX : lo == misc[kWhole] ? misc[kAhead] : 0;  // whole units
+            if (unit >= ahead) {
+                pieces = pieces_of(keys_behind(s, per_unit * qpt, ahead), part);
+                piece = (unit - ahead) % pieces;
+                unit = ahead + (unit - ahead) / pieces;
+                slot = id - (piece + cum[misc[kWhole]] + misc[kAhead]) * a.num_kv_heads;  // (counted from the first that is cut)
+            }
+        }
+        const int skip = piece * part * kKeys;
+        const int first = ((s.n + per_unit * qpt - 1) / (per_unit * qpt) - 1 - unit) * per_unit * qpt;
+        return Unit{s.q0 + first, s.n - first, s.k0 + skip, s.m - skip, head, s.m - s.n + first + 1 - skip, 1,
+                    piece * part, pieces > 1 ? part : INT_MAX, slot};
+    };
 
     if (warp == kProducer) {
         // ------------------------------------------------------------ producer
         bool ok = true;
         int stage = 0, q_count[2] = {0, 0};  // tiles put into the ring, Q tiles loaded
-        const int total = cum[a.num_seqs] * a.num_kv_heads;
         // (the first unit is the CTA's own number's; the others come from the counter)
-        int next = blockIdx.x;
+        int next = blockIdx.x, taken = 0;
         for (int i = 0; ok; ++i) {
             const int id = __shfl_sync(0xFFFFFFFFu, next, 0);
             if (lane == 0 && id < total) next = gridDim.x + atomicAdd(a.counters, 1);  // the one after, while this one runs
+            taken = i + 1;
+            if (lane == 0) misc[kHeld + i % 8] = id;
             Unit u{};
             if (id < total) {
-                int lo = 0, hi = a.num_seqs;  // the last place whose first unit is at or before id
-                while (hi - lo > 1) {
-                    const int mid = (lo + hi) >> 1;
-                    if (static_cast<int64_t>(cum[mid]) * a.num_kv_heads <= id) lo = mid;
-                    else hi = mid;
-                }
-                const Span s = span_of(a, order[lo], false);
-                const int j = id - cum[lo] * a.num_kv_heads, head = j % a.num_kv_heads;
-                int unit = j / a.num_kv_heads, pieces = 1, piece = 0, part = 0, slot = 0;
-                if constexpr (kCut) {
-                    part = misc[1];
-                    const int ahead = lo < misc[2] ? INT_MAX : lo == misc[2] ? misc[3] : 0;  // whole units
-                    if (unit >= ahead) {
-                        pieces = pieces_of(keys_behind(s, per_unit * qpt, ahead), part);
-                        piece = (unit - ahead) % pieces;
-                        unit = ahead + (unit - ahead) / pieces;
-                        slot = id - (piece + cum[misc[2]] + misc[3]) * a.num_kv_heads;  // (counted from the first that is cut)
-                    }
-                }
-                const int skip = piece * part * kKeys;
-                const int first = ((s.n + per_unit * qpt - 1) / (per_unit * qpt) - 1 - unit) * per_unit * qpt;
-                u = Unit{s.q0 + first, s.n - first, s.k0 + skip, s.m - skip, head, s.m - s.n + first + 1 - skip, 1,
-                         piece * part, pieces > 1 ? part : INT_MAX, slot};
-                if (kCut && piece > 0 && Shape<kCut>(u, qpt, per_unit).nt == 0) {  // (no query sees this piece)
+                u = unit_of(id);
+                if (kCut && u.first > 0 && Shape<kCut>(u, qpt, per_unit).nt == 0) {  // (no query sees this piece)
                     --i;
                     continue;
                 }
@@ -436,6 +454,10 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             }
         }
         if (!ok && lane == 0) fail();
+        if (lane == 0) {  // (the one after is this CTA's, too)
+            misc[kHeld + taken % 8] = next;
+            misc[kTaken] = taken + 1;
+        }
         // the copies under way land before the CTA ends
         for (int k = stage - 1; k >= 0 && k >= stage - kStages; --k) bar_wait(B(kFull + k % kStages), (k / kStages) & 1);
         for (int x = 0; x < 2; ++x)
@@ -444,7 +466,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
         if (lane == 0) {
             __threadfence();
             if (atomicAdd(a.counters + 1, 1) == static_cast<int>(gridDim.x) - 1) {
-                a.counters[0] = 0;
+                misc[kUntaken] = gridDim.x + atomicExch(a.counters, 0);
                 a.counters[1] = 0;
             }
         }
@@ -463,7 +485,9 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
         constexpr uint64_t kPair = (2 * Lt::kTile) >> 4;  // from a K (V) stage to the next
         int units = 0, q_count = 0, p_count = 0, o_count = 0;
         int c = -1, j = -1, tiles = 0, nt = 0;  // key tile of all, of the unit; the row tile's, the unit's
-        auto await = [&](int i, int parity) -> bool { return __all_sync(0xFFFFFFFFu, wait(i, parity)); };
+        auto await = [&](int i, int parity, uint32_t polls = kSpin) -> bool { return __all_sync(0xFFFFFFFFu, wait(i, parity, polls)); };
+        const bool limited = a.test_wait_polls >= 0 && x == 0 && (a.test_wait_cta < 0 || a.test_wait_cta == static_cast<int>(blockIdx.x));
+        uint32_t polls = limited ? static_cast<uint32_t>(a.test_wait_polls) : kSpin;  // of the first wait for a key tile
         auto arrive = [&](int i) {
             if (leader) bar_arrive(B(i));
         };
@@ -523,8 +547,9 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
         bool fresh = true;  // S of the current tile is not issued yet
         while (more > 0) {
             if (fresh) {
-                ok = await(kQFull + x, q_count++ & 1) && await(kFull + 2 * (c & 1), (c >> 1) & 1) && begin();
+                ok = await(kQFull + x, q_count++ & 1) && await(kFull + 2 * (c & 1), (c >> 1) & 1, polls) && begin();
                 if (!ok) break;
+                polls = kSpin;
                 fence_after();
                 scores(c);
                 end();
@@ -611,7 +636,8 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             }
             return false;
         };
-        for (int i = 0; ok; ++i) {
+        int i = 0;
+        for (; ok; ++i) {
             if (!__all_sync(0xFFFFFFFFu, wait(kUFull + i % kSlots, (i / kSlots) & 1))) {
                 ok = false;
                 break;
@@ -908,6 +934,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             }
             store(w);
         }
+        if (lane == 0) misc[kStopped + warp] = ok ? INT_MAX : i;
         if (!ok && lane == 0) fail();
     }
     fence_before();  // every role has left its waits
@@ -915,6 +942,38 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     fence_after();
     if (warp == 0)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(512) : "memory");
+
+    // Rows that are lost become NaN: of the units that this CTA had in hand when it gave up, and, where every CTA did, of
+    // those that none took.  A piece says so by its statistics, and has the joining kernel told of its row tile.
+    if (*abort_flag == 0 && misc[kUntaken] >= total) return;
+    auto lose = [&](int id) {
+        const Unit u = unit_of(id);
+        const Shape<kCut> sh(u, qpt, per_unit);
+        const float nan = __uint_as_float(0x7FC00000u);
+        for (int x = 0; x < per_unit; ++x) {
+            const int n = min(u.n - x * qpt, qpt), sees = u.seen + u.first * kKeys + x * qpt;
+            if (n <= 0) continue;
+            const int pieces = u.len == INT_MAX ? 1 : (max(0, (sees + n - 1 + kKeys - 1) / kKeys) + u.len - 1) / u.len;
+            if (pieces > 1) {
+                if (sh.tiles[x] == 0) continue;  // (no query sees this piece)
+                const int64_t part_ = (static_cast<int64_t>(u.slot) + u.first / u.len * a.num_kv_heads) * kSoftmaxWarps + 8 * x;
+                if (tid < 8 * 32) a.part_ml[part_ * 32 + tid] = make_float2(nan, nan);
+                if (tid == 0) a.tiles[2 * u.slot + x] = make_int4(pieces, u.q0 + x * qpt, n | u.head << 8, sees);
+            } else if (u.first == 0) {
+                uint4* out = reinterpret_cast<uint4*>(a.out);
+                for (int e = tid; e < n * gh * (kDim / 8); e += kThreads) {
+                    const int r = e / (kDim / 8), h = u.head * gh + r % gh;
+                    out[(static_cast<int64_t>(u.q0 + x * qpt + r / gh) * a.num_q_heads + h) * (kDim / 8) + e % (kDim / 8)] =
+                        make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u);
+                }
+            }
+        }
+    };
+    int first = INT_MAX;
+    for (int w = 0; w < kSoftmaxWarps; ++w) first = min(first, misc[kStopped + w]);
+    for (int i = first; i < misc[kTaken]; ++i)
+        if (misc[kHeld + i % 8] < total) lose(misc[kHeld + i % 8]);
+    for (int id = misc[kUntaken]; id < total; ++id) lose(id);
 }
 
 // The pieces of row tiles, joined in their order.  A CTA has one row tile (or none: the place's units were not cut), a

@@ -261,6 +261,7 @@ pkv_status prompt_attention(const void* q, const void* k, const void* v, pkv_dty
     a.num_q_heads = num_q_heads;
     a.num_kv_heads = num_kv_heads;
     a.scale_log2 = scale * 1.4426950408889634f;
+    first_wait_limit(&a.test_wait_polls, &a.test_wait_cta);
     prompt_tc_workspace(head_dim, static_cast<uint8_t*>(workspace), &a);
     // without a key the other design writes the zero rows (a descriptor has no empty dimension)
     if (k_rows > 0 && prompt_tc_fits(dtype, num_seqs, q_rows, num_q_heads, num_kv_heads)) {

@@ -77,6 +77,7 @@ struct PromptArgs {
     int32_t* err;
     int num_seqs, q_rows, k_rows, num_q_heads, num_kv_heads;
     float scale_log2;
+    int32_t test_wait_polls, test_wait_cta;    // as first_wait_limit gives them
     // tensor-core design: {units, CTAs} and row tiles that are cut, zero between calls, and the pieces' sums
     int32_t* counters;
     int4* tiles;
