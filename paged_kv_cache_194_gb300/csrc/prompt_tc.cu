@@ -204,11 +204,74 @@ struct Shape {
     }
 };
 
+// The plan in shared memory.
+struct Plan {
+    const int *misc, *cum;
+    const uint16_t* order;
+};
+// Unit `id` of the list.
+template <bool kCut>
+__device__ __forceinline__ Unit unit_at(const PromptArgs& a, const Plan& p, int id, int per_unit) {
+    const int *misc = p.misc, *cum = p.cum, qpt = kRows / (a.num_q_heads / a.num_kv_heads);
+    const uint16_t* order = p.order;
+    int lo = 0, hi = a.num_seqs;  // the last place whose first unit is at or before id
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (static_cast<int64_t>(cum[mid]) * a.num_kv_heads <= id) lo = mid;
+        else hi = mid;
+    }
+    const Span s = span_of(a, order[lo], false);
+    const int j = id - cum[lo] * a.num_kv_heads, head = j % a.num_kv_heads;
+    int unit = j / a.num_kv_heads, pieces = 1, piece = 0, part = 0, slot = 0;
+    if constexpr (kCut) {
+        part = misc[kPart];
+        const int ahead = lo < misc[kWhole] ? INT_MAX : lo == misc[kWhole] ? misc[kAhead] : 0;  // whole units
+        if (unit >= ahead) {
+            pieces = pieces_of(keys_behind(s, per_unit * qpt, ahead), part);
+            piece = (unit - ahead) % pieces;
+            unit = ahead + (unit - ahead) / pieces;
+            slot = id - (piece + cum[misc[kWhole]] + misc[kAhead]) * a.num_kv_heads;  // (counted from the first that is cut)
+        }
+    }
+    const int skip = piece * part * kKeys;
+    const int first = ((s.n + per_unit * qpt - 1) / (per_unit * qpt) - 1 - unit) * per_unit * qpt;
+    return Unit{s.q0 + first, s.n - first, s.k0 + skip, s.m - skip, head, s.m - s.n + first + 1 - skip, 1,
+                piece * part, pieces > 1 ? part : INT_MAX, slot};
+}
+
+// NaN for what unit `id` was to write: its rows, or a piece's statistics, with the joining kernel told of its row tile.
+// (A call of its own: inlined, it cost the kernel's loops 1 %.)
+template <int kDim, bool kCut>
+__device__ __noinline__ void lose_unit(const PromptArgs& a, const Plan plan, int id, int per_unit) {
+    const Unit u = unit_at<kCut>(a, plan, id, per_unit);
+    const int gh = a.num_q_heads / a.num_kv_heads, qpt = kRows / gh, tid = threadIdx.x;
+    const Shape<kCut> sh(u, qpt, per_unit);
+    const float nan = __uint_as_float(0x7FC00000u);
+    for (int x = 0; x < per_unit; ++x) {
+        const int n = min(u.n - x * qpt, qpt), sees = u.seen + u.first * kKeys + x * qpt;
+        if (n <= 0) continue;
+        const int pieces = u.len == INT_MAX ? 1 : (max(0, (sees + n - 1 + kKeys - 1) / kKeys) + u.len - 1) / u.len;
+        if (pieces > 1) {
+            if (sh.tiles[x] == 0) continue;  // (no query sees this piece)
+            const int64_t part_ = (static_cast<int64_t>(u.slot) + u.first / u.len * a.num_kv_heads) * kSoftmaxWarps + 8 * x;
+            if (tid < 8 * 32) a.part_ml[part_ * 32 + tid] = make_float2(nan, nan);
+            if (tid == 0) a.tiles[2 * u.slot + x] = make_int4(pieces, u.q0 + x * qpt, n | u.head << 8, sees);
+        } else if (u.first == 0) {
+            uint4* out = reinterpret_cast<uint4*>(a.out);
+            for (int e = tid; e < n * gh * (kDim / 8); e += kThreads) {
+                const int r = e / (kDim / 8), h = u.head * gh + r % gh;
+                out[(static_cast<int64_t>(u.q0 + x * qpt + r / gh) * a.num_q_heads + h) * (kDim / 8) + e % (kDim / 8)] =
+                    make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u);
+            }
+        }
+    }
+}
+
 // kCut: the keys of units may be cut into pieces.
 template <int kDim, bool kCut>
 __global__ void __launch_bounds__(kThreads, 1)
 prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                 const __grid_constant__ CUtensorMap mv, const PromptArgs a) {
+                 const __grid_constant__ CUtensorMap mv, const __grid_constant__ PromptArgs a) {
     using Lt = Layout<kDim>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -365,37 +428,14 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
         const volatile Unit& s = queue[i % kSlots];
         return Unit{s.q0, s.n, s.k0, s.m, s.head, s.seen, s.more, 0, kCut ? s.len : 0, 0};
     };
-    const int total = cum[a.num_seqs] * a.num_kv_heads;
-    auto unit_of = [&](int id) -> Unit {  // unit `id` of the list
-        int lo = 0, hi = a.num_seqs;  // the last place whose first unit is at or before id
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (static_cast<int64_t>(cum[mid]) * a.num_kv_heads <= id) lo = mid;
-            else hi = mid;
-        }
-        const Span s = span_of(a, order[lo], false);
-        const int j = id - cum[lo] * a.num_kv_heads, head = j % a.num_kv_heads;
-        int unit = j / a.num_kv_heads, pieces = 1, piece = 0, part = 0, slot = 0;
-        if constexpr (kCut) {
-            part = misc[kPart];
-            const int ahead = lo < misc[kWhole] ? INT_MAX : lo == misc[kWhole] ? misc[kAhead] : 0;  // whole units
-            if (unit >= ahead) {
-                pieces = pieces_of(keys_behind(s, per_unit * qpt, ahead), part);
-                piece = (unit - ahead) % pieces;
-                unit = ahead + (unit - ahead) / pieces;
-                slot = id - (piece + cum[misc[kWhole]] + misc[kAhead]) * a.num_kv_heads;  // (counted from the first that is cut)
-            }
-        }
-        const int skip = piece * part * kKeys;
-        const int first = ((s.n + per_unit * qpt - 1) / (per_unit * qpt) - 1 - unit) * per_unit * qpt;
-        return Unit{s.q0 + first, s.n - first, s.k0 + skip, s.m - skip, head, s.m - s.n + first + 1 - skip, 1,
-                    piece * part, pieces > 1 ? part : INT_MAX, slot};
-    };
+    const Plan plan{misc, cum, order};
+    auto unit_of = [&](int id) -> Unit { return unit_at<kCut>(a, plan, id, per_unit); };
 
     if (warp == kProducer) {
         // ------------------------------------------------------------ producer
         bool ok = true;
         int stage = 0, q_count[2] = {0, 0};  // tiles put into the ring, Q tiles loaded
+        const int total = cum[a.num_seqs] * a.num_kv_heads;
         // (the first unit is the CTA's own number's; the others come from the counter)
         int next = blockIdx.x, taken = 0;
         for (int i = 0; ok; ++i) {
@@ -466,7 +506,8 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
         if (lane == 0) {
             __threadfence();
             if (atomicAdd(a.counters + 1, 1) == static_cast<int>(gridDim.x) - 1) {
-                misc[kUntaken] = gridDim.x + atomicExch(a.counters, 0);
+                if (ok) a.counters[0] = 0;  // (this CTA saw the list's end)
+                else misc[kUntaken] = gridDim.x + atomicExch(a.counters, 0);
                 a.counters[1] = 0;
             }
         }
@@ -485,9 +526,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
         constexpr uint64_t kPair = (2 * Lt::kTile) >> 4;  // from a K (V) stage to the next
         int units = 0, q_count = 0, p_count = 0, o_count = 0;
         int c = -1, j = -1, tiles = 0, nt = 0;  // key tile of all, of the unit; the row tile's, the unit's
-        auto await = [&](int i, int parity, uint32_t polls = kSpin) -> bool { return __all_sync(0xFFFFFFFFu, wait(i, parity, polls)); };
-        const bool limited = a.test_wait_polls >= 0 && x == 0 && (a.test_wait_cta < 0 || a.test_wait_cta == static_cast<int>(blockIdx.x));
-        uint32_t polls = limited ? static_cast<uint32_t>(a.test_wait_polls) : kSpin;  // of the first wait for a key tile
+        auto await = [&](int i, int parity) -> bool { return __all_sync(0xFFFFFFFFu, wait(i, parity)); };
         auto arrive = [&](int i) {
             if (leader) bar_arrive(B(i));
         };
@@ -544,12 +583,14 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
         };
         bool ok = true;
         int more = next_unit();
+        if (x == 0 && more > 0 && a.test_wait_polls >= 0 && (a.test_wait_cta < 0 || a.test_wait_cta == static_cast<int>(blockIdx.x)) &&
+            !__all_sync(0xFFFFFFFFu, wait(kFull + 2 * (c & 1), (c >> 1) & 1, a.test_wait_polls)))
+            more = -1;  // (under test: the first wait for a key tile)
         bool fresh = true;  // S of the current tile is not issued yet
         while (more > 0) {
             if (fresh) {
-                ok = await(kQFull + x, q_count++ & 1) && await(kFull + 2 * (c & 1), (c >> 1) & 1, polls) && begin();
+                ok = await(kQFull + x, q_count++ & 1) && await(kFull + 2 * (c & 1), (c >> 1) & 1) && begin();
                 if (!ok) break;
-                polls = kSpin;
                 fence_after();
                 scores(c);
                 end();
@@ -944,36 +985,14 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(512) : "memory");
 
     // Rows that are lost become NaN: of the units that this CTA had in hand when it gave up, and, where every CTA did, of
-    // those that none took.  A piece says so by its statistics, and has the joining kernel told of its row tile.
+    // those that none took.
+    const int total = cum[a.num_seqs] * a.num_kv_heads;
     if (*abort_flag == 0 && misc[kUntaken] >= total) return;
-    auto lose = [&](int id) {
-        const Unit u = unit_of(id);
-        const Shape<kCut> sh(u, qpt, per_unit);
-        const float nan = __uint_as_float(0x7FC00000u);
-        for (int x = 0; x < per_unit; ++x) {
-            const int n = min(u.n - x * qpt, qpt), sees = u.seen + u.first * kKeys + x * qpt;
-            if (n <= 0) continue;
-            const int pieces = u.len == INT_MAX ? 1 : (max(0, (sees + n - 1 + kKeys - 1) / kKeys) + u.len - 1) / u.len;
-            if (pieces > 1) {
-                if (sh.tiles[x] == 0) continue;  // (no query sees this piece)
-                const int64_t part_ = (static_cast<int64_t>(u.slot) + u.first / u.len * a.num_kv_heads) * kSoftmaxWarps + 8 * x;
-                if (tid < 8 * 32) a.part_ml[part_ * 32 + tid] = make_float2(nan, nan);
-                if (tid == 0) a.tiles[2 * u.slot + x] = make_int4(pieces, u.q0 + x * qpt, n | u.head << 8, sees);
-            } else if (u.first == 0) {
-                uint4* out = reinterpret_cast<uint4*>(a.out);
-                for (int e = tid; e < n * gh * (kDim / 8); e += kThreads) {
-                    const int r = e / (kDim / 8), h = u.head * gh + r % gh;
-                    out[(static_cast<int64_t>(u.q0 + x * qpt + r / gh) * a.num_q_heads + h) * (kDim / 8) + e % (kDim / 8)] =
-                        make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u);
-                }
-            }
-        }
-    };
     int first = INT_MAX;
     for (int w = 0; w < kSoftmaxWarps; ++w) first = min(first, misc[kStopped + w]);
     for (int i = first; i < misc[kTaken]; ++i)
-        if (misc[kHeld + i % 8] < total) lose(misc[kHeld + i % 8]);
-    for (int id = misc[kUntaken]; id < total; ++id) lose(id);
+        if (misc[kHeld + i % 8] < total) lose_unit<kDim, kCut>(a, plan, misc[kHeld + i % 8], per_unit);
+    for (int id = misc[kUntaken]; id < total; ++id) lose_unit<kDim, kCut>(a, plan, id, per_unit);
 }
 
 // The pieces of row tiles, joined in their order.  A CTA has one row tile (or none: the place's units were not cut), a
