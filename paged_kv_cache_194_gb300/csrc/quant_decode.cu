@@ -651,12 +651,15 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kBits, kDim, kNT)) quant
                         }
                         const int col = 8 * n + 2 * t + j;
                         if ((kPair && t >= 2) || col >= rows) continue;
-                        const float up = 16777216.f * ex2f(mw[n][j] - m[n][j]), up2 = kBits == 4 ? 0.0625f * up : up, inv = 1.f / l[n][j];
+                        // O in the base of l, the codes' 2^24 (and the upper nibbles' 2^-4) taken out.  The bases differ by V's
+                        // scale, up to 2^132 with the maxima's lag: in two halves.
+                        const float half = ex2f(0.5f * (mw[n][j] - m[n][j])), inv = 1.f / l[n][j];
+                        const float up = 16777216.f * inv * half, up2 = kBits == 4 ? 0.0625f * up : up, z = zs[n][j] * inv;
                         // this lane's dimensions of the head: kDim / 8 from g (kDim / 8) on
                         uint32_t y[S::kKSteps];
 #pragma unroll
                         for (int i = 0; i < S::kKSteps; ++i)
-                            y[i] = pack_bf16x2_rn(fmaf(o[n][i][j], up, zs[n][j]) * inv, fmaf(o[n][i][2 + j], up2, zs[n][j]) * inv);
+                            y[i] = pack_bf16x2_rn(fmaf(o[n][i][j] * up, half, z), fmaf(o[n][i][2 + j] * up2, half, z));
                         uint4* dst = reinterpret_cast<uint4*>(a.out + (out0 + col) * kDim + g * (kDim / 8));
 #pragma unroll
                         for (int i = 0; i < S::kKSteps; i += 4) dst[i / 4] = make_uint4(y[i], y[i + 1], y[i + 2], y[i + 3]);
@@ -674,8 +677,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kBits, kDim, kNT)) quant
                         }
                         const int col = 8 * n + 2 * t + j;
                         if (kPair && t >= 2) continue;
-                        // O in the base of l, the codes' 2^24 (and the upper nibbles' 2^-4) taken out
-                        const float up = 16777216.f * ex2f(mw[n][j] - m[n][j]);
+                        const float half = ex2f(0.5f * (mw[n][j] - m[n][j])), up = 16777216.f * half;  // (as above)
+                        const float up2 = kBits == 4 ? 0.0625f * up : up;
                         if (g == 0) {
                             sm[warp][col] = m[n][j];
                             sl[warp][col] = l[n][j];
@@ -684,8 +687,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kBits, kDim, kNT)) quant
                         // element (dimension g (kDim / 8) + x) of column col at [x][g]: all lanes in different banks
 #pragma unroll
                         for (int i = 0; i < S::kKSteps; ++i) {
-                            so(warp)[col][(2 * i) * 8 + g] = o[n][i][j] * up;
-                            so(warp)[col][(2 * i + 1) * 8 + g] = o[n][i][2 + j] * (kBits == 4 ? 0.0625f * up : up);
+                            so(warp)[col][(2 * i) * 8 + g] = o[n][i][j] * up * half;
+                            so(warp)[col][(2 * i + 1) * 8 + g] = o[n][i][2 + j] * up2 * half;
                         }
                     }
                 __syncthreads();

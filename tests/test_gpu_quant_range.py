@@ -1,0 +1,49 @@
+"""GPU tests of decode attention over codes where magnitudes are far from one: values near the largest numbers, scores
+far from zero, weights far below the largest one."""
+import pytest
+import torch
+
+import quant_reference as ref
+import quant_tight as tight
+from paged_kv_cache_194_gb300 import binding as pk
+from test_gpu_quant_cache import BF, Quantised
+from test_gpu_quant_tight import put
+
+pytestmark = pytest.mark.gpu
+
+# a CTA a unit, cut units, a warp a unit; two steps at a time and one
+SHAPES = [((300, 5), 8, 2, 128), ((6000, 40), 8, 2, 128), ((60,) * 200, 8, 2, 128), ((300, 5), 16, 2, 64),
+          ((6000, 40), 16, 1, 128)]
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("lens,Hq,Hk,D", SHAPES, ids=str)
+def test_value_rows_of_large_scales(bits, lens, Hq, Hk, D):
+    """Scales above 2^104, which times the codes' 2^24 are past 32 bits, beside rows of small ones."""
+    b = Quantised(lens, Hq, Hk, D, 16, bits, seed=80)
+    g = torch.Generator().manual_seed(81)
+    T = sum(lens)
+    k = torch.randn(T, Hk, D, generator=g).to(BF)
+    v = (torch.rand(T, Hk, D, generator=g) * 2 - 1) * 3e33
+    v[torch.rand(T, generator=g) < 0.1] *= 1e-30
+    v[torch.rand(T, generator=g) < 0.1] = 2e33  # (rows of one value: codes of zero)
+    v[..., ::7] = 0
+    put(b, k, v.to(BF))
+    out = b.run()
+    assert out.isfinite().all()
+    tight.check(out, *tight.codes(b.q, b.pools(), b.tables, b.lens, b.scale, bits))
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+def test_one_token_of_the_largest_values(bits):
+    """A weight of one: the row itself, with a scale of up to 2^124."""
+    b = Quantised((1, 1, 1), bits=bits, seed=82)
+    g = torch.Generator().manual_seed(83)
+    v = ((torch.rand(3, 2, 128, generator=g) - 0.5) * 3.3e38).to(BF)
+    v[1] = 3e38
+    put(b, v * 1e-38, v)
+    p, c = b.pools()[3], b.pools()[2]
+    blk = b.tables[:, 0].long()
+    want = ref.values(c[blk, :, 0], p[blk, :, 0], bits).repeat_interleave(4, 1)
+    err = (b.run().cpu().double() - want).abs()
+    assert (err <= (2.0 ** -8 + 2.0 ** -10) * want.abs() + 2.0 ** -11 * 3.3e38).all()
