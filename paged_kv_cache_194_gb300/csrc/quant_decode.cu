@@ -18,10 +18,10 @@
 //    movmatrix.
 //  * Queries enter in FP16 after a power of two that brings the row's largest to
 //    [2^14, 2^15): exact for every element within 2^-29 of it.
-//  * V's scale goes into the weight's exponent: w_j = 2^(t_j + log2 s'_j - m) with m
-//    the running maximum of those exponents, so FP16 weights neither overflow nor
-//    lose what matters whatever the scales.  The sum of 2^t_j and the offsets' part
-//    sum 2^t_j z'_j have a running maximum of their own and stay in binary32.
+//  * V's scale goes into the weight's exponent: w_j = 2^((t_j - m) + log2 s'_j - lift)
+//    with m the running maximum of the t_j, m + lift that of t_j + log2 s'_j, so FP16
+//    weights neither overflow nor lose what matters whatever the scales.  The sum of
+//    2^(t_j - m) and the offsets' part sum 2^(t_j - m) z'_j stay in binary32.
 //
 // Schedule: the 64-token tiles of all (sequence, KV head, part of the group) units
 // form one list, in which a unit weighs kUnitCost tiles beside its own; it is cut into
@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kBits, kDim, kNT)) quant
             // ---------------------------------------------------------- the tokens
             const int steps = steps_of(seg);
             float o[kNT][S::kKSteps][4];
-            float mw[kNT][2], m[kNT][2], l[kNT][2], zs[kNT][2];  // bases of O, and of l and zs
+            float m[kNT][2], lift[kNT][2], l[kNT][2], zs[kNT][2];  // the base of l and zs, and how far O's lies above it
 #pragma unroll
             for (int n = 0; n < kNT; ++n) {
 #pragma unroll
@@ -478,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kBits, kDim, kNT)) quant
 #pragma unroll
                     for (int j = 0; j < 4; ++j) o[n][i][j] = 0.f;
 #pragma unroll
-                for (int j = 0; j < 2; ++j) mw[n][j] = m[n][j] = kNone, l[n][j] = zs[n][j] = 0.f;
+                for (int j = 0; j < 2; ++j) m[n][j] = kNone, lift[n][j] = l[n][j] = zs[n][j] = 0.f;
             }
 
             // Steps i .. i + kNS - 1.  With at most four heads two steps share the softmax: columns 4 to 7 of the products
@@ -521,7 +521,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kBits, kDim, kNT)) quant
                 uint32_t pb[kNS][kNT][2];
 #pragma unroll
                 for (int n = 0; n < kNT; ++n) {
-                    float y[2][2], e[2][2];
+                    // Exponents of the weights: u of l's, e of O's, above l's base both.  (V's scale is added to the
+                    // difference: the scores themselves may be too large to hold it.)
+                    float y[2][2], u[2][2], e[2][2];
                     bool grown = false;
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
@@ -534,25 +536,32 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kBits, kDim, kNT)) quant
                             }
                             const float x_ = fmaf(ks_[r], dot * fs[n][j], kz[r] * fz[n][j]);
                             y[r][j] = g + 8 * r < left ? x_ : -INFINITY;
-                            e[r][j] = y[r][j] + lg[r];
+                            u[r][j] = y[r][j] - m[n][j];
+                            e[r][j] = u[r][j] + lg[r];
                         }
-                        grown |= fmaxf(y[0][j], y[1][j]) > m[n][j] + 8.f || fmaxf(e[0][j], e[1][j]) > mw[n][j] + 8.f;
+                        grown |= fmaxf(u[0][j], u[1][j]) > 8.f || fmaxf(e[0][j], e[1][j]) > lift[n][j] + 8.f;
                     }
                     // the maxima move only when an exponent passes one by 8 (weights stay below 2^8)
                     if (__any_sync(kAll, grown)) {
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
-                            float top = fmaxf(y[0][j], y[1][j]), topw = fmaxf(e[0][j], e[1][j]);
+                            float top = fmaxf(y[0][j], y[1][j]);
 #pragma unroll
-                            for (int d = kPair ? 2 : 4; d < 32; d <<= 1) {
-                                top = fmaxf(top, __shfl_xor_sync(kAll, top, d));
-                                topw = fmaxf(topw, __shfl_xor_sync(kAll, topw, d));
-                            }
+                            for (int x = kPair ? 2 : 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, x));
                             top = fmaxf(top, m[n][j]);
-                            topw = fmaxf(topw, mw[n][j]);
-                            const float f = ex2f(m[n][j] - top), fw = ex2f(mw[n][j] - topw);
+#pragma unroll
+                            for (int r = 0; r < 2; ++r) {
+                                u[r][j] = y[r][j] - top;
+                                e[r][j] = u[r][j] + lg[r];
+                            }
+                            float topw = fmaxf(e[0][j], e[1][j]);
+#pragma unroll
+                            for (int x = kPair ? 2 : 4; x < 32; x <<= 1) topw = fmaxf(topw, __shfl_xor_sync(kAll, topw, x));
+                            const float down = m[n][j] - top;
+                            topw = fmaxf(topw, lift[n][j] + down);
+                            const float f = ex2f(down), fw = ex2f(lift[n][j] - topw + down);
                             m[n][j] = top;
-                            mw[n][j] = topw;
+                            lift[n][j] = topw;
                             l[n][j] *= f;
                             zs[n][j] *= f;
 #pragma unroll
@@ -567,8 +576,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kBits, kDim, kNT)) quant
                     for (int j = 0; j < 2; ++j) {
 #pragma unroll
                         for (int r = 0; r < 2; ++r) {
-                            w[r][j] = ex2f(e[r][j] - mw[n][j]);
-                            const float p = ex2f(y[r][j] - m[n][j]);
+                            w[r][j] = ex2f(e[r][j] - lift[n][j]);
+                            const float p = ex2f(u[r][j]);
                             l[n][j] += p;
                             zs[n][j] = fmaf(p, vz[r], zs[n][j]);
                         }
@@ -653,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kBits, kDim, kNT)) quant
                         if ((kPair && t >= 2) || col >= rows) continue;
                         // O in the base of l, the codes' 2^24 (and the upper nibbles' 2^-4) taken out.  The bases differ by V's
                         // scale, up to 2^132 with the maxima's lag: in two halves.
-                        const float half = ex2f(0.5f * (mw[n][j] - m[n][j])), inv = 1.f / l[n][j];
+                        const float half = ex2f(0.5f * lift[n][j]), inv = 1.f / l[n][j];
                         const float up = 16777216.f * inv * half, up2 = kBits == 4 ? 0.0625f * up : up, z = zs[n][j] * inv;
                         // this lane's dimensions of the head: kDim / 8 from g (kDim / 8) on
                         uint32_t y[S::kKSteps];
@@ -677,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kBits, kDim, kNT)) quant
                         }
                         const int col = 8 * n + 2 * t + j;
                         if (kPair && t >= 2) continue;
-                        const float half = ex2f(0.5f * (mw[n][j] - m[n][j])), up = 16777216.f * half;  // (as above)
+                        const float half = ex2f(0.5f * lift[n][j]), up = 16777216.f * half;  // (as above)
                         const float up2 = kBits == 4 ? 0.0625f * up : up;
                         if (g == 0) {
                             sm[warp][col] = m[n][j];

@@ -47,3 +47,18 @@ def test_one_token_of_the_largest_values(bits):
     want = ref.values(c[blk, :, 0], p[blk, :, 0], bits).repeat_interleave(4, 1)
     err = (b.run().cpu().double() - want).abs()
     assert (err <= (2.0 ** -8 + 2.0 ** -10) * want.abs() + 2.0 ** -11 * 3.3e38).all()
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("wide", [-1e3, 1e5, -1e7, 1e9])
+@pytest.mark.parametrize("lens,Hq,Hk,D", SHAPES, ids=str)
+def test_scores_far_from_zero(bits, wide, lens, Hq, Hk, D):
+    """Keys that are all alike, so that all weights are, with scores of up to 10^12 that leave no room for the
+    logarithms of the values' scales: the mean of the values."""
+    b = Quantised(lens, Hq, Hk, D, 16, bits, seed=84)
+    g = torch.Generator().manual_seed(85)
+    T = sum(lens)
+    v = torch.randn(T, Hk, D, generator=g) * 10.0 ** torch.randint(-2, 3, (T, 1, 1), generator=g)
+    put(b, (torch.randn(1, Hk, D, generator=g) + 1).expand(T, Hk, D).to(BF).contiguous(), v.to(BF))
+    b.q = (torch.rand(b.q.shape, generator=g) * wide).to(BF)
+    tight.check(b.run(), *tight.codes(b.q, b.pools(), b.tables, b.lens, 0.0, bits))
