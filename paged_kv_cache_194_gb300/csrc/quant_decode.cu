@@ -62,7 +62,7 @@ constexpr int depth_of(int bits, int dim, int nt) {
     if (dim == 64) return bits == 4 ? 10 : 6;
     return nt == 2 && bits == 4 ? 12 : 6;
 }
-constexpr float kNone = -1e30f;  // a maximum of nothing
+constexpr float kNone = -3.402823466e38f;  // a maximum of nothing: finite, so that nothing minus nothing is 0
 constexpr unsigned kAll = 0xFFFFFFFFu;
 
 __device__ __forceinline__ float ex2f(float x) {

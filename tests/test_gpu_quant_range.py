@@ -62,3 +62,16 @@ def test_scores_far_from_zero(bits, wide, lens, Hq, Hk, D):
     put(b, (torch.randn(1, Hk, D, generator=g) + 1).expand(T, Hk, D).to(BF).contiguous(), v.to(BF))
     b.q = (torch.rand(b.q.shape, generator=g) * wide).to(BF)
     tight.check(b.run(), *tight.codes(b.q, b.pools(), b.tables, b.lens, 0.0, bits))
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("sign", [-1, 1])
+@pytest.mark.parametrize("lens,Hq,Hk,D", SHAPES, ids=str)
+def test_scores_of_the_largest_magnitude(bits, sign, lens, Hq, Hk, D):
+    """All scores at -10^36 (10^36): far below any that stands for no key."""
+    b = Quantised(lens, Hq, Hk, D, 16, bits, seed=86)
+    T = sum(lens)
+    v = torch.randn(T, Hk, D, generator=torch.Generator().manual_seed(87)).to(BF)
+    put(b, torch.full((T, Hk, D), 1e17).to(BF), v)
+    b.q = torch.full(b.q.shape, sign * 1e18).to(BF)
+    tight.check(b.run(), *tight.codes(b.q, b.pools(), b.tables, b.lens, 0.0, bits))
