@@ -19,9 +19,11 @@
 //  * Queries enter in FP16 after a power of two that brings the row's largest to
 //    [2^14, 2^15): exact for every element within 2^-29 of it.
 //  * V's scale goes into the weight's exponent: w_j = 2^((t_j - m) + log2 s'_j - lift)
-//    with m the running maximum of the t_j, m + lift that of t_j + log2 s'_j, so FP16
-//    weights neither overflow nor lose what matters whatever the scales.  The sum of
-//    2^(t_j - m) and the offsets' part sum 2^(t_j - m) z'_j stay in binary32.
+//    with m the running maximum of the t_j, m + lift + 7 that of t_j + log2 s'_j: FP16
+//    weights (the type that codes are multiplied with) of up to 2^7, 2^15 while the
+//    maxima lag by 8, which are rounded by 2^-11 and, below 2^-21 of the largest, by
+//    2^-32 of it.  The sum of 2^(t_j - m) and the offsets' part sum 2^(t_j - m) z'_j
+//    stay in binary32.
 //
 // Schedule: the 64-token tiles of all (sequence, KV head, part of the group) units
 // form one list, in which a unit weighs kUnitCost tiles beside its own; it is cut into
@@ -63,6 +65,8 @@ constexpr int depth_of(int bits, int dim, int nt) {
     return nt == 2 && bits == 4 ? 12 : 6;
 }
 constexpr float kNone = -3.402823466e38f;  // a maximum of nothing: finite, so that nothing minus nothing is 0
+constexpr float kHigh = 7.f;  // log2 of the largest weight: FP16's small numbers then reach far below it
+constexpr float kLag = 8.f;   // that the maxima may be behind
 constexpr unsigned kAll = 0xFFFFFFFFu;
 
 __device__ __forceinline__ float ex2f(float x) {
@@ -539,9 +543,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kBits, kDim, kNT)) quant
                             u[r][j] = y[r][j] - m[n][j];
                             e[r][j] = u[r][j] + lg[r];
                         }
-                        grown |= fmaxf(u[0][j], u[1][j]) > 8.f || fmaxf(e[0][j], e[1][j]) > lift[n][j] + 8.f;
+                        grown |= fmaxf(u[0][j], u[1][j]) > kLag || fmaxf(e[0][j], e[1][j]) > lift[n][j] + (kHigh + kLag);
                     }
-                    // the maxima move only when an exponent passes one by 8 (weights stay below 2^8)
+                    // the maxima move only when an exponent passes one by 8 (weights stay below 2^8, FP16 ones below 2^15)
                     if (__any_sync(kAll, grown)) {
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
@@ -558,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kBits, kDim, kNT)) quant
 #pragma unroll
                             for (int x = kPair ? 2 : 4; x < 32; x <<= 1) topw = fmaxf(topw, __shfl_xor_sync(kAll, topw, x));
                             const float down = m[n][j] - top;
-                            topw = fmaxf(topw, lift[n][j] + down);
+                            topw = fmaxf(topw - kHigh, lift[n][j] + down);
                             const float f = ex2f(down), fw = ex2f(lift[n][j] - topw + down);
                             m[n][j] = top;
                             lift[n][j] = topw;

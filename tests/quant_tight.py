@@ -22,7 +22,7 @@ from quant_reference import HALF, unpack
 STEPS = 24
 FP16 = 2.0 ** -11       # half a step
 SMALLEST = 2.0 ** -25   # half of FP16's smallest number, as a part of ...
-SHIFT = 0               # ... the largest weight times 2^-SHIFT
+SHIFT = 7               # ... the largest weight times 2^-SHIFT
 
 
 def _weights(x):

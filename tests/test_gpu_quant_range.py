@@ -75,3 +75,23 @@ def test_scores_of_the_largest_magnitude(bits, sign, lens, Hq, Hk, D):
     put(b, torch.full((T, Hk, D), 1e17).to(BF), v)
     b.q = torch.full(b.q.shape, sign * 1e18).to(BF)
     tight.check(b.run(), *tight.codes(b.q, b.pools(), b.tables, b.lens, 0.0, bits))
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("nats", [12.0, 17.7, 19.0])
+def test_many_keys_far_below_one(bits, nats):
+    """In each warp's part of a long unit one key outweighs each of the others by up to 2^27; together they matter all the
+    same: values of 0 at the one (but for one element, which gives its row a scale), of 1 to 2 at the others."""
+    L, B, Hk = 131072, 60, 8
+    b = Quantised((L,), 4 * Hk, Hk, 128, 64, bits, seed=88)
+    g = torch.Generator().manual_seed(89)
+    k = (torch.randn(L, Hk, 128, generator=g) * 0.05).to(BF)
+    v = (1 + torch.rand(L, Hk, 128, generator=g)).to(BF)
+    v[..., 0] = 0  # (an offset of 0: the values are all in the codes)
+    for t in range(L // 3, L // 3 + 64, 16):  # (four warps take 16 tokens each in turns)
+        k[t], v[t], v[t, :, 0] = nats / 128 ** 0.5, 0, 2
+    put(b, k, v)
+    b.q = torch.ones_like(b.q)
+    want, bound = tight.codes(b.q, b.pools(), b.tables, b.lens, b.scale, bits)
+    b.q, b.tables, b.lens = (x.repeat_interleave(B, 0) for x in (b.q, b.tables, torch.tensor(b.lens)))  # (the same blocks)
+    tight.check(b.run(), want.expand(B, -1, -1), bound.expand(B, -1, -1))
