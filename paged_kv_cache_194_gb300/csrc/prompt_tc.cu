@@ -41,7 +41,7 @@
 //    keys of a tile and half of its output columns, the other the rest.  The base of a
 //    row's weights is a past maximum, agreed on while the tile's products run: it moves
 //    only when a score passes it by 8 (log2 units), which rescales O in tensor memory
-//    before the next tile's products, or by 60 at once, before this tile's.  Statistics
+//    before the next tile's products, or by 16 at once, before this tile's.  Statistics
 //    and sums are FP32; a weight is rounded to BF16 for its product with V, the type that
 //    the tensor core takes beside V's.
 // Tensor memory: 2 x 128 score columns, 2 x head_dim output columns.
@@ -66,7 +66,7 @@ constexpr int kRows = 128, kKeys = 128;
 constexpr int kHalf = 128 * 128;     // 64 columns of 128 rows
 constexpr int kStages = 4;
 constexpr int kSlots = 2;            // units in the queue
-constexpr float kFar = 60.f;         // weights stay below 2^60
+constexpr float kFar = 16.f;         // weights stay below 2^16, and sums of 2^96 times the values' 2^16 keys in 32 bits
 constexpr int kSortSeqs = 256;       // up to so many sequences are taken longest first
 constexpr int kLeastPiece = 4;       // key tiles of a unit's piece, at least
 constexpr int kWorth = 3;            // what cutting costs, in key tiles

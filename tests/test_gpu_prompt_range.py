@@ -1,0 +1,27 @@
+"""GPU tests of prompt attention where magnitudes are far from one: large values under rising scores, large scores, keys
+that are not finite among pieces that weigh nothing."""
+import pytest
+import torch
+
+import quant_tight as tight
+from paged_kv_cache_194_gb300 import binding as pk
+from test_gpu_prompt import case, offsets
+from test_gpu_quant_cache import dev
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("inp", ["bf16", "f32"])
+@pytest.mark.parametrize("q_lens,k_lens", [((900,), (900,)), ((200,), (5000,))], ids=str)
+@pytest.mark.parametrize("rise", [12.0, 30.0, 55.0])
+def test_large_values_under_rising_scores(inp, q_lens, k_lens, rise):
+    """Scores that rise by 2^rise from one tile of keys to the next, so that the weights' base lags behind them, and
+    values of 2^96: sums of weights and values stay within 32 bits."""
+    (q, k, v), _ = case(q_lens, k_lens, 4, 2, 128, inp, fused=False, seed=90)
+    q = q * 0.01
+    q[..., 0] = 1.0
+    k[..., 0] = (torch.arange(k.shape[0]) // 128 * rise * 0.6931)[:, None].to(k.dtype)
+    v = v * 2.0 ** 96
+    out = pk.prompt_attention(*[x.cuda() for x in (q, k, v)], dev(offsets(q_lens)), dev(offsets(k_lens)), 1.0)
+    assert out.isfinite().all()
+    tight.check(out, *tight.prompts(q, k, v, q_lens, k_lens, 1.0))
