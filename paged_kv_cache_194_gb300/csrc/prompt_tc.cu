@@ -879,7 +879,8 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                     const float top = fmaxf(mx, its);
                     if (__any_sync(0xFFFFFFFFu, top > m_used + kFar)) {
                         const float m_new = top > m_used + kFar ? above(m_used, top) : m_used;
-                        l = m_used == m_new ? l : m_used == -INFINITY ? 0.f : l * ex2(m_used - m_new);
+                        // (from no base: l is 0, or NaN where the row has seen a key that is)
+                        l = m_used == m_new || m_used == -INFINITY ? l : l * ex2(m_used - m_new);
                         l0 = m_own == m_new ? l0 : l0 * ex2(m_own - m_new);
                         m_used = m_new;
                     }
@@ -1033,7 +1034,8 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const PromptA
 #pragma unroll
         for (int i = 0; i < kAtOnce; ++i) {
             const float f = ex2(s[i].x - top);
-            if (f == 0.f) continue;  // (a piece that weighs nothing, or of which the row sees nothing)
+            // (a piece that weighs nothing, or of which the row sees nothing; a sum of NaN tells of a key that is)
+            if (f == 0.f && s[i].y == s[i].y) continue;
             l = fmaf(f, s[i].y, l);
 #pragma unroll
             for (int k = 0; k < kMine; ++k) {

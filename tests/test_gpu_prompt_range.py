@@ -25,3 +25,20 @@ def test_large_values_under_rising_scores(inp, q_lens, k_lens, rise):
     out = pk.prompt_attention(*[x.cuda() for x in (q, k, v)], dev(offsets(q_lens)), dev(offsets(k_lens)), 1.0)
     assert out.isfinite().all()
     tight.check(out, *tight.prompts(q, k, v, q_lens, k_lens, 1.0))
+
+
+@pytest.mark.parametrize("inp", ["bf16", "f32"])
+@pytest.mark.parametrize("bad", [slice(100, 101), slice(128, 256), slice(0, 640)], ids=str)
+@pytest.mark.parametrize("heavy", [3100, 5900])
+def test_keys_that_are_nan_where_nothing_weighs(inp, bad, heavy):
+    """A query that sees a key of NaN is NaN, whatever the other keys of its tile or piece weigh beside the rest."""
+    (q, k, v), _ = case((70,), (6000,), 8, 2, 128, inp, fused=False, seed=91)
+    q[..., 0] = 8.0
+    k[:, :, 0] = 0
+    k[heavy:heavy + 50, :, 0] = 60.0
+    o = [dev(offsets(x)) for x in ((70,), (6000,))]
+    want = pk.prompt_attention(*[x.cuda() for x in (q, k, v)], *o, 1.0)
+    tight.check(want, *tight.prompts(q, k, v, (70,), (6000,), 1.0))
+    k[bad, 1] = float("nan")
+    got = pk.prompt_attention(*[x.cuda() for x in (q, k, v)], *o, 1.0)
+    assert got[:, 4:].isnan().all() and torch.equal(got[:, :4], want[:, :4])
