@@ -47,10 +47,9 @@ __device__ __forceinline__ uint64_t add2_down(uint64_t a, uint64_t b) {
     asm("add.rm.f32x2 %0, %1, %2;\n" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(d) : "l"(a), "l"(b));
-    return d;
+// (a product of pairs would be fused with a sum that follows, which the format rounds by itself)
+__device__ __forceinline__ uint64_t mul_each(uint64_t a, float b) {
+    return pair(__fmul_rn(__uint_as_float(static_cast<uint32_t>(a)), b), __fmul_rn(__uint_as_float(static_cast<uint32_t>(a >> 32)), b));
 }
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     uint64_t d;
@@ -149,12 +148,12 @@ __global__ void __launch_bounds__(kThreads) quant_append_kernel(const QuantAppen
         const float s0 = fmaxf(fmaxf(__fdiv_rn(range, N), fabsf(z) * 0x1p-16f), 0x1p-100f);
         const uint32_t sb = (__float_as_uint(s0) + 0xFFFFu) & 0xFFFF0000u;
         const float inv = __fmul_rn(__frcp_rn(__uint_as_float(sb)), 1.f + 0x1p-21f);
-        const uint64_t z2 = pair(-z, -z), inv2 = pair(inv, inv), half2 = pair(0.5f, 0.5f), int2 = pair(8388608.f, 8388608.f);
+        const uint64_t z2 = pair(-z, -z), half2 = pair(0.5f, 0.5f), int2 = pair(8388608.f, 8388608.f);
         // floor((x - z) inv + 1/2): in the low bits of 2^23 + it
         uint32_t n[16];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            const uint64_t y = add2_down(add2(mul2(add2(x[k], z2), inv2), half2), int2);
+            const uint64_t y = add2_down(add2(mul_each(add2(x[k], z2), inv), half2), int2);
             n[2 * k] = static_cast<uint32_t>(y), n[2 * k + 1] = static_cast<uint32_t>(y >> 32);
         }
         const int in = static_cast<int>(slot[i]) & ((1 << a.block_shift) - 1);
