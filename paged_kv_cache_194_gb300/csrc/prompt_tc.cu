@@ -67,6 +67,7 @@ constexpr int kHalf = 128 * 128;     // 64 columns of 128 rows
 constexpr int kStages = 4;
 constexpr int kSlots = 2;            // units in the queue
 constexpr float kFar = 16.f;         // weights stay below 2^16, and sums of 2^96 times the values' 2^16 keys in 32 bits
+constexpr float kLarge = 0x1p29f;    // from here on kFar does not show beside a base, whose steps are wider than 2 kFar
 constexpr int kSortSeqs = 256;       // up to so many sequences are taken longest first
 constexpr int kLeastPiece = 4;       // key tiles of a unit's piece, at least
 constexpr int kWorth = 3;            // what cutting costs, in key tiles
@@ -120,10 +121,11 @@ struct Layout {
 struct Span {
     int q0, n, k0, m;
 };
-__device__ __forceinline__ Span span_of(const PromptArgs& a, int b, bool report) {
+__device__ __forceinline__ Span span_of(const PromptArgs& a, int b, bool report, bool* bad = nullptr) {
     Span s{a.q_offsets[b], a.q_offsets[b + 1], a.k_offsets[b], a.k_offsets[b + 1]};
     const bool ok = s.q0 >= 0 && s.n >= s.q0 && s.n <= a.q_rows && s.k0 >= 0 && s.m >= s.k0 && s.m <= a.k_rows;
     if (!ok && report && a.err) atomicOr(a.err, PKV_ERRBIT_OFFSETS);
+    if (bad) *bad |= !ok;
     s.n = ok ? s.n - s.q0 : 0;
     s.m = ok ? s.m - s.k0 : 0;
     return s;
@@ -182,9 +184,10 @@ __device__ __forceinline__ void tmem_st16_nowait(uint32_t at, const uint32_t* v)
         : "memory");
 }
 
-// The next base: whole steps above the last one, so that a change of base is exact.
+// The next base: whole steps above the last one, so that a change of base is exact.  (Far enough above, nothing is left of
+// the weights before, and the sum might miss `top` by more than weights may be above the base.)
 __device__ __forceinline__ float above(float base, float top) {
-    return base == -INFINITY ? top : base + ceilf(top - base);
+    return top - base > 4096.f ? top : base + ceilf(top - base);
 }
 
 // What the roles agree on about a unit.
@@ -303,6 +306,13 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
     }
+    if (qpt * gh < kRows) {  // rows of Q tiles that no query has
+        const int gone = kRows - qpt * gh;
+        for (int e = tid; e < 2 * Lt::kHalves * gone * 8; e += kThreads)
+            *reinterpret_cast<uint4*>(smem + Lt::kQ + e / (gone * 8) * kHalf + (qpt * gh + e % (gone * 8) / 8) * 128 + e % 8 * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+        fence_async_smem();
+    }
     for (int i = tid; i < 3 * 4 * kRows; i += kThreads)  // (tellings are numbered from 1)
         reinterpret_cast<uint2*>(smem + Lt::kSay)[i] = make_uint2(0u, 0u);
     // (nothing before reads or writes what the kernel before this one may)
@@ -310,8 +320,9 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     // the plan: sequences in order, and the row tiles before each
     int* keys = cum + 1;  // (first the keys, for the order)
-    for (int b = tid; b < a.num_seqs; b += kThreads) keys[b] = span_of(a, b, blockIdx.x == 0).m;
-    __syncthreads();
+    bool bad = false;
+    for (int b = tid; b < a.num_seqs; b += kThreads) keys[b] = span_of(a, b, blockIdx.x == 0, &bad).m;
+    bad = __syncthreads_or(bad);
     for (int b = tid; b < a.num_seqs; b += kThreads) {
         int rank = b;
         if (a.num_seqs <= kSortSeqs) {
@@ -349,11 +360,13 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             return at;
         };
         // Sequences of offsets that descend may overlap, so that their queries are more than the rows: none is taken then.
-        int64_t queries = 0;
-        for (int r = lane; r < a.num_seqs; r += 32) queries += span_of(a, r, false).n;
+        if (bad) {
+            int64_t queries = 0;
+            for (int r = lane; r < a.num_seqs; r += 32) queries += span_of(a, r, false).n;
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) queries += __shfl_xor_sync(0xFFFFFFFFu, queries, d);
-        sound = queries <= a.q_rows;
+            for (int d = 16; d > 0; d >>= 1) queries += __shfl_xor_sync(0xFFFFFFFFu, queries, d);
+            sound = queries <= a.q_rows;
+        }
         const int64_t units = static_cast<int64_t>(fill()) * a.num_kv_heads;
         const int grid = gridDim.x;
         if constexpr (kCut) {
@@ -746,7 +759,8 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                             v[k] = bf16x2(p0, p1);
                         }
                         mx = fmaxf(m2[0], m2[1]) * qk;
-                        made = !__any_sync(0xFFFFFFFFu, mx > m_used + kFar);
+                        // (equal: a base from kLarge on; scores below such a one are so by a step, and weigh nothing)
+                        made = !__any_sync(0xFFFFFFFFu, mx >= m_used + kFar);
                         if (made) {
                             m_own = m_used;
                             tmem_st16_nowait(ts + hf * kMine, v);
@@ -800,11 +814,18 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                             } else {
                                 tmem_ld32_nowait(ts + hf * kMine + 32 * c, v);
                                 asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
+                                float q_ = qk;
+                                if (__any_sync(0xFFFFFFFFu, fabsf(base2) >= kLarge)) {
+                                    // as the largest score was rounded, before the base is taken away
+                                    q_ = 1.f;
+#pragma unroll
+                                    for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__fmul_rn(__uint_as_float(v[k]), qk));
+                                }
                                 auto weights = [&](auto hide) {
 #pragma unroll
                                     for (int k = 0; k < 16; ++k) {
                                         float x0, x1;
-                                        fma2(x0, x1, __uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]), qk, qk, -base2, -base2);
+                                        fma2(x0, x1, __uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]), q_, q_, -base2, -base2);
                                         if (hide()) {  // a weight of 0 for what the row does not see
                                             x0 = 32 * c + 2 * k < mine ? x0 : -INFINITY;
                                             x1 = 32 * c + 2 * k + 1 < mine ? x1 : -INFINITY;
@@ -987,8 +1008,8 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
 
     // Rows that are lost become NaN: of the units that this CTA had in hand when it gave up, and, where every CTA did, of
     // those that none took.
+    if (*abort_flag == 0 && misc[kUntaken] == INT_MAX) return;
     const int total = cum[a.num_seqs] * a.num_kv_heads;
-    if (*abort_flag == 0 && misc[kUntaken] >= total) return;
     int first = INT_MAX;
     for (int w = 0; w < kSoftmaxWarps; ++w) first = min(first, misc[kStopped + w]);
     for (int i = first; i < misc[kTaken]; ++i)

@@ -7,6 +7,7 @@ import quant_tight as tight
 from paged_kv_cache_194_gb300 import binding as pk
 from test_gpu_prompt import case, offsets
 from test_gpu_quant_cache import dev
+from test_gpu_quant_tight import PROMPTS, check_picks, ids, picks
 
 pytestmark = pytest.mark.gpu
 
@@ -42,3 +43,14 @@ def test_keys_that_are_nan_where_nothing_weighs(inp, bad, heavy):
     k[bad, 1] = float("nan")
     got = pk.prompt_attention(*[x.cuda() for x in (q, k, v)], *o, 1.0)
     assert got[:, 4:].isnan().all() and torch.equal(got[:, :4], want[:, :4])
+
+
+@pytest.mark.parametrize("inp", ["bf16", "f32"])
+@pytest.mark.parametrize("wide", [-2.0 ** 12, 2.0 ** 20, 2.0 ** 30, 2.0 ** 50])
+@pytest.mark.parametrize("q_lens,k_lens,Hq,Hk,D", [PROMPTS[0], PROMPTS[2], PROMPTS[4], PROMPTS[7]], ids=ids)
+def test_large_scores(inp, wide, q_lens, k_lens, Hq, Hk, D):
+    """Scores of up to 10^19: 32 bits have steps of many units there, and the largest still outweighs the others."""
+    q, k, v, want = picks(inp, q_lens, k_lens, Hq, Hk, D, abs(wide))
+    sign = -1.0 if wide < 0 else 1.0  # (a negative scale: every score turned around, twice)
+    out = pk.prompt_attention(*[x.cuda() for x in (q * sign, k, v)], dev(offsets(q_lens)), dev(offsets(k_lens)), 0.25 * sign)
+    check_picks(inp, out, want)

@@ -141,11 +141,9 @@ def test_every_key_counts_once(inp, step, q_lens, k_lens, Hq, Hk, D):
     assert (err <= (half + 2.0 ** -22) * want).all(), float(err.max())
 
 
-@pytest.mark.parametrize("inp", ["bf16", "f32"])
-@pytest.mark.parametrize("q_lens,k_lens,Hq,Hk,D", PROMPTS, ids=ids)
-def test_every_query_picks_a_key(inp, q_lens, k_lens, Hq, Hk, D):
-    """Keys of signs, a query in the direction of one key that it sees, first, last and tiles' borders among them: the
-    output is that key's value."""
+def picks(inp, q_lens, k_lens, Hq, Hk, D, wide=1.0):
+    """Keys of signs, each query in the direction of one key that it sees, first, last and tiles' borders among them: q, k,
+    v, and the output, which is that key's value."""
     g = torch.Generator().manual_seed(77)
     (q, k, v), _ = case(q_lens, k_lens, Hq, Hk, D, inp, fused=False, seed=78)
     k = (torch.randint(0, 2, k.shape, generator=g) * 2 - 1).to(k.dtype) * 2
@@ -162,13 +160,24 @@ def test_every_query_picks_a_key(inp, q_lens, k_lens, Hq, Hk, D):
             pick[i % Hq] = border
             j = ik + pick
             h = torch.arange(Hq) // (Hq // Hk)
-            q[iq + i], want[iq + i] = k[j, h] * 8, v[j, h].double()
+            q[iq + i], want[iq + i] = k[j, h] * (8 * wide), v[j, h].double()
         iq, ik = iq + n, ik + m
-    # a key's own score is 32 D, another's 32 times a sum of D signs: at most 0.7 D of 10^4 keys and as many queries
-    # (beyond ten standard deviations), so that others weigh less than 2^-100 with a scale of 1/4
-    out = pk.prompt_attention(*[x.cuda() for x in (q, k, v)], dev(offsets(q_lens)), dev(offsets(k_lens)), 0.25)
+    return q, k, v, want
+
+
+def check_picks(inp, out, want):
     # The key's weight is 2^x with x within 8 of 0 (the base of weights need not be their maximum): BF16 rounds it for its
     # product with V by up to half a step, 2^-8, and the sum that the output is divided by is of weights that are not
     # rounded.  The output is rounded by as much again: (1 + 2^-8)^2 = 1 + 2^-7 + 2^-16, and the quotient's 2^-22.
     err = 2.0 ** -7 + 2.0 ** -16 + 2.0 ** -22 if inp == "bf16" else 2.0 ** -22
     assert ((out.cpu().double() - want).abs() <= err * want.abs()).all()
+
+
+@pytest.mark.parametrize("inp", ["bf16", "f32"])
+@pytest.mark.parametrize("q_lens,k_lens,Hq,Hk,D", PROMPTS, ids=ids)
+def test_every_query_picks_a_key(inp, q_lens, k_lens, Hq, Hk, D):
+    # a key's own score is 32 D, another's 32 times a sum of D signs: at most 0.7 D of 10^4 keys and as many queries
+    # (beyond ten standard deviations), so that others weigh less than 2^-100 with a scale of 1/4
+    q, k, v, want = picks(inp, q_lens, k_lens, Hq, Hk, D)
+    out = pk.prompt_attention(*[x.cuda() for x in (q, k, v)], dev(offsets(q_lens)), dev(offsets(k_lens)), 0.25)
+    check_picks(inp, out, want)
