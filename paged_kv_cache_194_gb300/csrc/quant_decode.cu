@@ -17,7 +17,8 @@
 //    free, so each lane takes one contiguous run of its rows' bytes; P turns around by
 //    movmatrix.
 //  * Queries enter in FP16 after a power of two that brings the row's largest to
-//    [2^14, 2^15): exact for every element within 2^-29 of it.
+//    [2^14, 2^15): exact for every element within 2^-31 of it (2^-27 for those that
+//    meet upper nibbles, as 1/16 of themselves); what is less is rounded by 2^-25.
 //  * V's scale goes into the weight's exponent: w_j = 2^((t_j - m) + log2 s'_j - lift)
 //    with m the running maximum of the t_j, m + lift + 7 that of t_j + log2 s'_j: FP16
 //    weights (the type that codes are multiplied with) of up to 2^7, 2^15 while the

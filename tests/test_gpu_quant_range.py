@@ -95,3 +95,20 @@ def test_many_keys_far_below_one(bits, nats):
     want, bound = tight.codes(b.q, b.pools(), b.tables, b.lens, b.scale, bits)
     b.q, b.tables, b.lens = (x.repeat_interleave(B, 0) for x in (b.q, b.tables, torch.tensor(b.lens)))  # (the same blocks)
     tight.check(b.run(), want.expand(B, -1, -1), bound.expand(B, -1, -1))
+
+
+@pytest.mark.parametrize("bits,ratio", [(4, 27), (8, 31)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_small_elements_of_a_query_row_count(bits, ratio, D):
+    """Scores that depend on elements 2^-ratio of their row's largest alone, which meets codes of zero."""
+    N = 2 ** bits - 1
+    lens = (200, 3000)
+    b = Quantised(lens, 4, 1, D, 16, bits, seed=92)
+    g = torch.Generator().manual_seed(93)
+    k = torch.randint(0, N + 1, (sum(lens), 1, D), generator=g).to(BF)
+    k[..., 0], k[..., 1] = 0, N  # (an offset of 0, a scale of 1)
+    put(b, k, torch.randn(k.shape, generator=g).to(BF))
+    q = (1 + torch.rand(b.q.shape, generator=g)) * (torch.randint(0, 2, b.q.shape, generator=g) * 2 - 1) * 2.0 ** -ratio
+    q[..., 0] = 1.0
+    b.q, b.scale = q.to(BF), 2.0 ** ratio / (N * D ** 0.5)
+    tight.check(b.run(), *tight.codes(b.q, b.pools(), b.tables, b.lens, b.scale, bits))
