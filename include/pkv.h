@@ -507,7 +507,10 @@ pkv_status kv_quant_append(const kv_quant_pool* pool, int32_t layer, const void*
  *                 are tokens 0 .. of sequence b.  Offsets that do not ascend within
  *                 [0, num_rows] set PKV_ERRBIT_OFFSETS, and that sequence is not
  *                 read; rows before the first and behind the last sequence are left
- *                 as they were.
+ *                 as they were.  There is no room between sequences: a chunk whose
+ *                 attention reads cached rows in front of its own is appended first
+ *                 and read back with them (as the values it is kept as), or each
+ *                 sequence is read by a call of its own.
  *   block_tables  device int32 [num_seqs][max_blocks_per_seq].  A row past its
  *                 table (PKV_ERRBIT_SEQ_LEN), or whose entry is outside the pool
  *                 (PKV_ERRBIT_BLOCK_ID), becomes zero.
@@ -522,9 +525,15 @@ pkv_status kv_quant_read(const kv_quant_pool* pool, int32_t layer, const int32_t
 
 /*
  * paged_decode_attention over a quantised cache: same arguments and result, with
- * K_t and V_t the values that the codes stand for.  q and out are BF16; any number
- * of query heads per KV head.  A row that reads as NaN makes the queries that see
- * it NaN; rows behind a sequence's end are not looked at.
+ * K_t and V_t the values that the codes stand for.  q and out are BF16 (F32 queries
+ * are refused); any number of query heads per KV head, each 16 of which read the
+ * cache for themselves.  A row that reads as NaN makes the queries that see it NaN;
+ * rows behind a sequence's end are not looked at.
+ * Softmax, sums and the offsets' part are binary32; the codes' part multiplies FP16
+ * weights, rounded by 2^-11 of themselves and, below 2^-21 of the largest, by 2^-32
+ * of it.  Results are finite while |scale| times the largest |q| stays below 2^100,
+ * scores and 2^8 times the sum of |v| over a sequence's tokens below 2^127.  Pools
+ * that something else has written hold scales >= 0.
  *   workspace  at least paged_quant_decode_plan's bytes, 256-byte aligned, the first
  *              64 KB (or all) zeroed before its first call; every call leaves them zero,
  *              and writes what it likes behind them.  Stream-ordered calls of any
@@ -567,8 +576,13 @@ pkv_status paged_quant_decode_attention(const void* q, pkv_dtype q_dtype, const 
  *              may not.
  * Offsets are read on the device: a captured call may be replayed with other ones.
  * Softmax and accumulation are binary32; with BF16 the weights are rounded to BF16
- * for their product with V.  A value of v that is not finite reaches the queries up
- * to 255 positions before it, too; rows of other sequences never do.
+ * (by 2^-8) for their product with V, and may be up to 2^16: results are finite while
+ * scores, and 2^16 times the sum of |v| over the keys that a query sees, stay below
+ * 2^127 (with F32 the sum itself).  A value of v that is not finite reaches the
+ * queries up to 255 positions before it, too; rows of other sequences never do.
+ * BF16 calls of up to 2048 sequences and 128 query heads per KV head run on the
+ * tensor cores, all others on the CUDA cores, which take long BF16 rows about 30 times
+ * as long.
  */
 pkv_status prompt_attention_plan(int32_t num_seqs, int32_t q_rows, int32_t num_q_heads, int32_t num_kv_heads,
                                  int32_t head_dim, pkv_dtype dtype, size_t* workspace_bytes_out);
