@@ -188,7 +188,8 @@ cudaError_t launch_append(const QuantAppendArgs& a, cudaStream_t stream) {
         return launch_dependent(kernel, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, stream, a);
     };
     // Several rows under way in a warp once there are enough for all SMs.
-    if (rows >= 152 * kWarps * kRows * 4) return run(quant_append_kernel<kBits, kDim, T, 2>, 2);
+    const int64_t sms = num_sms() > 0 ? num_sms() : 148;
+    if (rows >= sms * kWarps * kRows * 4) return run(quant_append_kernel<kBits, kDim, T, 2>, 2);
     return run(quant_append_kernel<kBits, kDim, T, 1>, 1);
 }
 
@@ -378,8 +379,9 @@ template <int kKind>
 cudaError_t launch_kind(int head_dim, const ReadArgs& a, cudaStream_t stream) {
     const int sms = num_sms() > 0 ? num_sms() : 148;
     const int64_t want = (static_cast<int64_t>(a.num_rows) + kWarps - 1) / kWarps;
-    // A warp's next row is looked up while one is under way, which pays for codes (us, 8 CTAs an SM / 64: 4 bits 31.9 / 33.3
-    // for 36 thousand rows); E4M3 rows come faster from many warps of few rows (43.6 / 40.8 for 41 thousand).
+    // A warp's next row is looked up while one is under way, which pays for codes (us for 41 thousand rows, 8 CTAs an SM / 64:
+    // 4 bits 37.3 / 38.3, with head_dim 64 25.3 / 27.8; 8 bits 43.4 / 41.8, 27.8 / 29.0); wider rows come faster from many
+    // warps of few rows (E4M3 43.3 / 40.7, head_dim 64 26.5 / 27.5; BF16 54.8 / 51.6; 20 thousand of FP32 58.1 / 53.9).
     const int most = (kKind == kReadQ4 || kKind == kReadQ8 ? 8 : 64) * sms;
     const int blocks = static_cast<int>(want < most ? want : most);
     if (head_dim == 64) return launch_dependent(read_kernel<kKind, 64>, dim3(blocks), dim3(kThreads), 0, stream, a);
