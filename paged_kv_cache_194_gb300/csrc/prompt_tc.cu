@@ -24,9 +24,10 @@
 // take all of tensor memory; halves of 64 keys in turn made the score products slower (48.5
 // cycles for 64 keys, 64 for 128: their operands' way out of shared memory) and the whole too
 // (1.66 ms for the case below).  A unit costs about two more key tiles than it has.
-// Measured, 32 query heads on 8 of 128: one prompt of 16384 tokens 1.49 ms, 1.48 PFLOP/s of
-// what is seen; 16 prompts of 128 to 4096 630 us; 8 chunks of 256 to 512 behind up to 8192 194
-// us; 33 prompts of 1 to 127 20.5 us, of which a call of one row takes 7.6.
+// Measured over rotating inputs, 32 query heads on 8 of 128: one prompt of 16384 tokens 1.54 ms,
+// 1.43 PFLOP/s of what is seen (1.49 ms back to back on the same ones); 16 prompts of 128 to 4096
+// 591 to 668 us; 8 chunks of 256 to 512 behind up to 8192 185 to 204 us; 33 prompts of 1 to 127
+// 21.3 us, of which a call of one row takes 7.6.
 //
 // 20 warps (the last one idle; a row's scores live in registers, 96 for each of 640 threads):
 //  * warp 16, producer: takes units, loads Q tiles, and K and V tiles into one ring

@@ -38,11 +38,12 @@
 //
 // Measured with 32 query heads on 8 of 128, rows read from HBM at up to 6.79 TB/s: 55
 // sequences of 8192 tokens of 8 bits 162 us (5.9 TB/s); two of 130 thousand of 4 bits 59 us
-// (4.8 TB/s); 64 of 128 to 4096 of 4 bits 41.8 us (3.5 TB/s); four of up to 512 8.0 us.  Of 4-bit
-// rows the work on codes bounds it as much as memory does (250 instructions for 16 tokens of
-// a warp, issued in 51 % of the cycles by the three warps of a scheduler that registers leave
-// room for); a call's start, until rows flow, takes 3 to 4 us, and writing and joining pieces
-// at its end 4 to 5.
+// (4.8 TB/s); 64 of 128 to 4096 of 4 bits 42 us (3.5 TB/s); four of up to 512 8.4 us.  Of 4-bit
+// rows neither memory nor the issue slots are full: 250 instructions for 16 tokens of a warp are
+// issued in 51 % of the cycles (two long ones; 47 % of the mixed batch's) by the three warps of a
+// scheduler that registers leave room for, each of which waits for its own results, and at a
+// unit's end for the next one's rows; a call's start, until rows flow, takes 3 to 4 us, and
+// writing and joining pieces at its end 4 to 5.
 #include <type_traits>
 
 #include "device_common.cuh"
@@ -53,7 +54,9 @@ namespace {
 
 constexpr int kThreads = 128, kWarps = 4;
 constexpr int kTile = 64, kStep = 16;
-constexpr int kUnitCost = 6;  // (us for 64 sequences of 128 to 4096 tokens with 4, 6, 10: 42.5, 41.6, 42.5; 256 of 256 to 512: 45.2, 44.9, 44.4)
+// (us for 64 sequences of 128 to 4096 tokens with 4, 6, 10: 42.5, 41.6, 42.5; of 8 bits 61.4, 61.0, 61.3; head_dim 64 32.0,
+// 32.1, 32.0; 16 heads per KV head 33.9, 32.6, 33.6; 256 of 256 to 512, cut: 45.2, 44.9, 44.4)
+constexpr int kUnitCost = 6;
 constexpr int kMaxCtas = 1024;
 // CTAs per SM, and steps whose rows are under way in a warp (pair: taken two at a time).  HBM answers after 2.5 to 3 us
 // under load, so an SM wants 130 to 150 KB on their way.
@@ -212,7 +215,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kBits, kDim, kNT)) quant
         }
     // With no more units than CTAs, and none long, every unit is a CTA's of its own: joining its pieces would take longer
     // than they save.  (us whole / cut, 32 heads: 8.2 / 10.2 for one sequence of 512 tokens, 11.6 / 10.5 for one of 1024;
-    // 12.3 / 20.6 and 17.9 / 24.9 for fifty.)
+    // 12.3 / 20.6 and 17.9 / 24.9 for fifty; thirty of 512 11.0 / 14.4, of 8 bits 10.8 / 19.2, head_dim 64 10.3 / 12.7; eight
+    // of 900 15.1 / 12.4, 13.7 / 12.7, 13.4 / 11.0.  16 heads per KV head, four times the sequences: 14.0 / 33.3, and 18.4 /
+    // 20.7 for 900, where the rule cuts.)
     most = __reduce_max_sync(kAll, most);
     long long incl = mine | static_cast<long long>(some) << 40;  // (both sums at once: costs stay below 2^40)
 #pragma unroll
@@ -234,7 +239,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kBits, kDim, kNT)) quant
     // Many short units are a warp's own each: nothing to meet for.  The rule goes by tiles of one warp: the longest unit or
     // an equal share, and half of the other, against a share of a CTA's tiles and the ends of its units.  (us with warps'
     // own units / cut, 32 heads on 8, 4 bits: 256 sequences of 64 to 128 tokens 15.9 / 26.2, of 256 to 512 36.9 / 44.9,
-    // 128 of 512 26.5 / 30.5; 100 of 300 to 600 27.2 / 25.0, 300 of up to 2000 93.8 / 83.7: cut.)
+    // 128 of 512 26.5 / 30.5; 100 of 300 to 600 27.2 / 25.0, 300 of up to 2000 93.8 / 83.7: cut.  The first, the second
+    // and the fourth of them: 8 bits 18.4 / 32.9, 47.5 / 57.1, 26.0 / 31.8; head_dim 64 11.0 / 20.8, 25.1 / 32.9, 22.8 / 20.4: cut; 16 heads
+    // per KV head, four times the sequences, 24.4 / 61.2, 57.6 / 87.9, 33.0 / 47.0.)
     const long long mask = (1ll << 40) - 1, tiles = ((sum & mask) - kUnitCost * (sum >> 40)) * per_seq;
     bool alone = false;
     if (!apart && units >= gridDim.x && tiles + 2 * units <= 1 << 18) {
