@@ -516,6 +516,7 @@ pkv_status kv_quant_append(const kv_quant_pool* pool, int32_t layer, const void*
  *                 (PKV_ERRBIT_BLOCK_ID), becomes zero.
  *   k_out, v_out  device [num_rows][num_kv_heads][head_dim], F32 for an F32 pool,
  *                 else BF16: code * scale (+ offset) in binary32, rounded to nearest.
+ *                 They may not overlap.
  */
 pkv_status kv_read(const pkv_pool* pool, int32_t layer, const int32_t* block_tables, int32_t max_blocks_per_seq,
                    const int32_t* offsets, int32_t num_seqs, int32_t num_rows, void* k_out, void* v_out, void* stream);

@@ -42,14 +42,15 @@ size_t rows_of_layer(const kv_quant_pool_desc* d) {
     return static_cast<size_t>(d->num_blocks) * d->num_kv_heads * d->block_size;
 }
 
-// The checks and arguments that reading back any pool shares.
+// The checks and arguments that reading back any pool shares (row: bytes of a packed row).
 pkv_status read_call(const int32_t* tables, int32_t max_blocks, const int32_t* offsets, int32_t num_seqs,
-                     int32_t num_rows, void* k_out, void* v_out, ReadArgs* a) {
+                     int32_t num_rows, size_t row, void* k_out, void* v_out, ReadArgs* a) {
     if (max_blocks < 1 || num_seqs < 0 || num_rows < 0) return PKV_ERR_INVALID_ARG;
     if (num_seqs == 0 || num_rows == 0) return PKV_OK;
     if (!tables || !offsets || !k_out || !v_out) return PKV_ERR_INVALID_ARG;
     if (!aligned(tables, 4) || !aligned(offsets, 4) || !aligned(k_out, 16) || !aligned(v_out, 16))
         return PKV_ERR_INVALID_ARG;
+    if (overlap(k_out, num_rows * row, v_out, num_rows * row)) return PKV_ERR_INVALID_ARG;
     a->tables = tables;
     a->offsets = offsets;
     a->k_out = k_out;
@@ -127,7 +128,8 @@ pkv_status kv_read(const pkv_pool* p, int32_t layer, const int32_t* tables, int3
                    int32_t num_seqs, int32_t num_rows, void* k_out, void* v_out, void* stream) {
     if (!p || layer < 0 || layer >= p->d.num_layers) return PKV_ERR_INVALID_ARG;
     ReadArgs a{};
-    const pkv_status st = read_call(tables, max_blocks, offsets, num_seqs, num_rows, k_out, v_out, &a);
+    const size_t row = static_cast<size_t>(p->d.num_kv_heads) * p->d.head_dim * (p->d.kv_dtype == PKV_F32 ? 4 : 2);
+    const pkv_status st = read_call(tables, max_blocks, offsets, num_seqs, num_rows, row, k_out, v_out, &a);
     if (st != PKV_OK || !a.tables) return st;
     a.k = static_cast<const uint8_t*>(p->d.k_base) + static_cast<size_t>(layer) * p->layer_bytes;
     a.v = static_cast<const uint8_t*>(p->d.v_base) + static_cast<size_t>(layer) * p->layer_bytes;
@@ -146,7 +148,8 @@ pkv_status kv_quant_read(const kv_quant_pool* p, int32_t layer, const int32_t* t
                          void* stream) {
     if (!p || layer < 0 || layer >= p->d.num_layers) return PKV_ERR_INVALID_ARG;
     ReadArgs a{};
-    const pkv_status st = read_call(tables, max_blocks, offsets, num_seqs, num_rows, k_out, v_out, &a);
+    const size_t row = static_cast<size_t>(p->d.num_kv_heads) * p->d.head_dim * 2;
+    const pkv_status st = read_call(tables, max_blocks, offsets, num_seqs, num_rows, row, k_out, v_out, &a);
     if (st != PKV_OK || !a.tables) return st;
     const size_t first = p->layer_rows * layer;
     a.k = static_cast<const uint8_t*>(p->d.k_codes) + first * p->row_bytes;
