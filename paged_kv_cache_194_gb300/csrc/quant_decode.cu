@@ -240,8 +240,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kBits, kDim, kNT)) quant
     // an equal share, and half of the other, against a share of a CTA's tiles and the ends of its units.  (us with warps'
     // own units / cut, 32 heads on 8, 4 bits: 256 sequences of 64 to 128 tokens 15.9 / 26.2, of 256 to 512 36.9 / 44.9,
     // 128 of 512 26.5 / 30.5; 100 of 300 to 600 27.2 / 25.0, 300 of up to 2000 93.8 / 83.7: cut.  The first, the second
-    // and the fourth of them: 8 bits 18.4 / 32.9, 47.5 / 57.1, 26.0 / 31.8; head_dim 64 11.0 / 20.8, 25.1 / 32.9, 22.8 / 20.4: cut; 16 heads
-    // per KV head, four times the sequences, 24.4 / 61.2, 57.6 / 87.9, 33.0 / 47.0.)
+    // and the fourth of them: 8 bits 18.4 / 32.9, 47.5 / 57.1, 26.0 / 31.8; head_dim 64 11.0 / 20.8, 25.1 / 32.9, and
+    // 22.8 / 20.4: cut; 16 heads per KV head, four times the sequences, 24.4 / 61.2, 57.6 / 87.9, 33.0 / 47.0.)
     const long long mask = (1ll << 40) - 1, tiles = ((sum & mask) - kUnitCost * (sum >> 40)) * per_seq;
     bool alone = false;
     if (!apart && units >= gridDim.x && tiles + 2 * units <= 1 << 18) {
