@@ -579,8 +579,9 @@ pkv_status paged_quant_decode_attention(const void* q, pkv_dtype q_dtype, const 
  * Softmax and accumulation are binary32; with BF16 the weights are rounded to BF16
  * (by 2^-8) for their product with V, and may be up to 2^16 (2^32 with scores past
  * 2^24): results are finite while scores, and that times the sum of |v| over the keys
- * that a query sees, stay below 2^127 (with F32 the sum itself).  A value of v that is not finite reaches the
- * queries up to 255 positions before it, too; rows of other sequences never do.
+ * that a query sees, stay below 2^127 (with F32 the sum itself).  A value of v that
+ * is not finite reaches the queries up to 255 positions before it, too; rows of other
+ * sequences never do.
  * BF16 calls of up to 2048 sequences and 128 query heads per KV head run on the
  * tensor cores, all others on the CUDA cores, which take long BF16 rows about 30 times
  * as long.
